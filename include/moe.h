@@ -12,6 +12,12 @@
  *   moe_quantize_act_q8, moe_grouped_gemm_q, moe_grouped_gemm_gateup_silu_q,
  *   moe_grouped_gemm_down_q            keep-quant expert GEMMs (Q8_0 / Q4_K weights)
  *   moe_dequantize_q_bf16              keep-quant weights expanded to bf16
+ *   moe_quantize_act_fp8, moe_grouped_gemm_gateup_silu_fp8, moe_grouped_gemm_fp8
+ *                                      expert products with FP8 activations and weights
+ *   moe_silu_mul_backward_fp8, moe_transpose_fp8w
+ *                                      their data gradient (weights frozen)
+ *   moe_combine_backward, moe_route_backward, moe_route_logits_backward
+ *                                      gradients of the combine and of the router
  *
  * Sources (vllm.cpp pages):
  *   [I3094]  issue #3094 "Row: BACKEND-ROCM-BF16-MOE": names the two grouped
@@ -399,6 +405,92 @@ int moe_grouped_gemm_down_fp8w(const void* act_bf16, const uint8_t* w2_e4m3,
                                int I, int H, int G, void* out_bf16, void* workspace,
                                size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * FP8 expert products -- activations AND weights in 8-bit floating point, for
+ * the weight format of the *_fp8w calls above: E4M3 codes ("fn" variant) with
+ * one f32 scale per 128 x 128 block of each group's weight matrix; an
+ * activation row carries one f32 scale per 128 of its columns (the last block
+ * of a row may be short).  For row r of group g, output n and blocks b of the
+ * contraction:
+ *   y[r,n] = sum_b (sa[r,b] * sw[g,n/128,b]) * sum_{k in b} a[r,k] * w[g,n,k]
+ * The block sums run on E4M3 products accumulated in f32 and are joined in f32
+ * in block order.  A NaN or an infinity in an activation row makes that row's
+ * results NaN.
+ *
+ * moe_quantize_act_fp8 -- the activation quantiser.  For pair p = t*K + j, with
+ * f = pair_weight ? f32(pair_weight[p] * routed_scale) : routed_scale and
+ * destination row r = pair_to_row ? pair_to_row[p] : p, per block of 128 columns:
+ *   v = f32(x[t,c]) * f,  amax = max |v| (NaN skipped),
+ *   d = max(amax / 448, 2^-126),  code = E4M3(v * (1 / d)),  scales[r,b] = d
+ * each a single binary32 operation, the codes rounded to nearest even and
+ * saturated (NaN stays NaN).  Bit-exact.  Forward: pair_weight NULL and
+ * routed_scale 1 give the routed rows of x in expert order (no x_perm needed);
+ * backward: x is the output's gradient and f the combine's factor of the row.
+ *   x           bf16 [T, H], 16-byte aligned; H a multiple of 16; 1 <= K <= 64
+ *   pair_to_row int32 [T*K] or NULL (pair order); a row outside [0, T*K) is skipped
+ *   pair_weight f32 [T*K] or NULL
+ *   codes       uint8 [T*K, H] out, 16-byte aligned
+ *   scales      f32 [T*K, ceil(H/128)] out
+ *
+ * moe_grouped_gemm_fp8 -- the plain product and the down projection:
+ *   out[dst, n] = bf16( y[r,n] * pair_weight[dst] ),  dst = row_to_pair ? row_to_pair[r] : r
+ * (one f32 multiply and one rounding; no multiply without pair_weight).
+ *   a_codes, a_scales  [P, K], [P, ceil(K/128)], rows in group order
+ *   w_e4m3, w_scale    uint8 [G, N, K], f32 [G, ceil(N/128), ceil(K/128)]
+ *   group_offsets      int32 [G+1], read on the device, clamped to [0, P]; may
+ *                      be NULL when G == 1
+ *   row_to_pair        int32 [P] or NULL; a dst outside [0, P) is skipped
+ *   out                bf16 [P, N]; rows outside every group are not written
+ *   P >= 0; K a multiple of 16, N of 8; 1 <= G <= 1024
+ *
+ * moe_grouped_gemm_gateup_silu_fp8 -- gate/up with SiLU-mul, the result
+ * quantised for the down projection in the same launch: gate and up are
+ * narrowed to bf16 (as in moe_grouped_gemm_gateup_silu_bf16), then
+ *   v = silu(gate) * up  in f32,  quantised per 128 columns as above.
+ *   w13_e4m3, w13_scale  uint8 [G, 2I, H] (gate rows first), f32 [G, ceil(2I/128), ceil(H/128)]
+ *   gate_up     bf16 [P, 2I] out or NULL: the narrowed gate and up rows (what
+ *               moe_silu_mul_backward_fp8 reads)
+ *   act_codes   uint8 [P, I] out;  act_scales f32 [P, ceil(I/128)] out
+ *   H and I multiples of 16
+ *
+ * Data gradient, weights frozen: quantise dout with the combine's factors,
+ * multiply by the transposed w2 (moe_grouped_gemm_fp8, [G, I, H]), pass the
+ * SiLU-mul, multiply by the transposed w13 ([G, H, 2I]) with row_to_pair, sum a
+ * token's pairs with moe_combine.
+ *
+ * moe_silu_mul_backward_fp8 -- with g, u the halves of gate_up, s = sigmoid(g):
+ *   dg = dact * u * s * (1 + g * (1 - s)),   du = dact * g * s    (f32)
+ * and the row [dg, du] of 2I columns quantised per 128 of its columns.
+ *   gate_up bf16 [P, 2I], dact bf16 [P, I]; codes uint8 [P, 2I], scales
+ *   f32 [P, ceil(2I/128)] out; I a multiple of 16.  The exponential is the fast
+ *   one (a few binary32 ulps).
+ *
+ * moe_transpose_fp8w -- [G, R, C] codes and their block scales as [G, C, R]
+ * (exact: a block's scale moves with it); R and C multiples of 16.
+ *
+ * Errors of the five: MOE_ERR_ARG (sizes, NULL operands, NULL group_offsets
+ * with G > 1), MOE_ERR_ALIGN (codes, x and bf16 buffers 16-byte, scales and
+ * indices 4-byte aligned; the multiples above), MOE_ERR_CUDA.  P = 0 (T = 0) is
+ * a no-op.  No workspace.  A device-side wait that runs past its limit sets
+ * MOE_STATUS_TIMEOUT (moe_set_wait_limit_ns).
+ * ---------------------------------------------------------------------- */
+int moe_quantize_act_fp8(const void* x_bf16, int T, int H, int K, const int32_t* pair_to_row,
+                         const float* pair_weight, float routed_scale, uint8_t* codes,
+                         float* scales, void* stream);
+int moe_grouped_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_e4m3,
+                         const float* w_scale, const int32_t* group_offsets,
+                         const float* pair_weight, const int32_t* row_to_pair, int P, int K, int N,
+                         int G, void* out_bf16, void* stream);
+int moe_grouped_gemm_gateup_silu_fp8(const uint8_t* a_codes, const float* a_scales,
+                                     const uint8_t* w13_e4m3, const float* w13_scale,
+                                     const int32_t* group_offsets, int P, int H, int I, int G,
+                                     void* gate_up_bf16, uint8_t* act_codes, float* act_scales,
+                                     void* stream);
+int moe_silu_mul_backward_fp8(const void* gate_up_bf16, const void* dact_bf16, int P, int I,
+                              uint8_t* codes, float* scales, void* stream);
+int moe_transpose_fp8w(const uint8_t* w_e4m3, const float* w_scale, int G, int R, int C,
+                       uint8_t* out_e4m3, float* out_scale, void* stream);
+
 /* moe_set_gemm_pairing -- tiling of moe_grouped_gemm_gateup_silu_bf16 (also
  * with gathered or staged rows) and moe_grouped_gemm_down_bf16:
  *   MOE_GEMM_AUTO (default): CTA-pair tiles when P >= 1024, the groups average
@@ -600,6 +692,81 @@ int shared_expert_gate(const void* sd, int sd_dtype, const float* gl, int T, int
 size_t moe_gate_workspace_size(int T); /* for moe_combine_gate and shared_expert_gate */
 
 /* ------------------------------------------------------------------------
+ * moe_combine_backward -- the gradient of moe_combine's routed sum
+ * out[t,:] = routed_scale * sum_k w[t,k] * eo[t,k,:] (w = 1 when NULL):
+ *   dw[t,k]   = routed_scale * sum_c f32(eo[t,k,c]) * f32(dout[t,c])   f32
+ *   deo[t,k,c] = f32(dout[t,c]) * f32(w[t,k] * routed_scale), rounded once
+ * (the shared term's gradient is dout itself).  eo holds the rows as moe_combine
+ * read them: with weights applied here, not in the down projection.  Sums are
+ * f32 in a fixed order: the same call gives the same bits.
+ *   expert_out   [T,K,H] f32 or bf16; may be NULL when dw is NULL
+ *   dout         [T,H] f32 or bf16
+ *   dw           f32 [T,K] out or NULL
+ *   d_expert_out [T,K,H] f32 or bf16 out or NULL (not both NULL)
+ *   T >= 0, 1 <= K <= 64, H > 0 multiple of 8
+ * Errors: as moe_combine; MOE_ERR_ARG when neither output is given.
+ * ---------------------------------------------------------------------- */
+int moe_combine_backward(const void* expert_out, int eo_dtype, const float* w, const void* dout,
+                         int do_dtype, float routed_scale, int T, int K, int H, float* dw,
+                         void* d_expert_out, int deo_dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_backward -- the gradient of the router's weights with respect to
+ * its logits (the choice of experts, and so select_bias and the groups, have
+ * none), plus two auxiliary losses.  With g = grad_w, j over a token's K chosen
+ * experts, p = softmax(l) over all experts, s = sigmoid(l):
+ *   softmax, renormalize 1: dl_j  = w_j (g_j - sum_i g_i w_i), w the chosen
+ *                           experts' own softmax; 0 elsewhere
+ *   softmax, renormalize 0: dl_e  = p_e ([e chosen] g_e - sum_i g_i p_i)
+ *   sigmoid, renormalize 1: dl_j  = s_j (1 - s_j) (g_j - sum_i g_i s_i / S) / S,
+ *                           S = sum_i s_i
+ *   sigmoid, renormalize 0: dl_j  = g_j s_j (1 - s_j)
+ *   balance loss: balance_coef * sum_e f_e mean_t P[t,e], f_e = E * count_e / (K T)
+ *                 from expert_offsets (no gradient through f), P = p (softmax) or
+ *                 s / sum s (sigmoid)
+ *   z-loss:       z_coef * mean_t (logsumexp_e l[t,e])^2
+ * All f32.  An expert at -inf has weight and gradient 0, and a token whose every
+ * logit is -inf adds nothing to either loss; other infinities and NaN give NaN in
+ * their own row.
+ *   logits         f32 [T,E] (with the bias, as moe_route_topk's logits_out)
+ *   topk_ids       int32 [T,K], distinct per token; an id outside [0,E) is
+ *                  skipped and raises MOE_STATUS_BAD_ID
+ *   grad_w         f32 [T,K] or NULL (zero: the auxiliary losses alone)
+ *   expert_offsets int32 [E+1] from moe_permute; may be NULL when balance_coef is 0
+ *   grad_logits    f32 [T,E] out
+ *   losses         f32 [2] out or NULL: balance and z-loss, coefficients included
+ *   workspace      >= moe_route_backward_workspace_size(T, E) bytes, 16-byte
+ *                  aligned; may be NULL when losses is NULL
+ *   T >= 0 (T = 0: losses are 0), 1 <= E <= 1024, 1 <= K <= min(E, 32)
+ * Errors: MOE_ERR_UNSUPPORTED (scoring not 0 or 1), MOE_ERR_ARG, MOE_ERR_ALIGN
+ * (4 bytes), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.
+ *
+ * moe_route_logits_backward -- through the logits product l = x W^T + bias:
+ *   grad_x[t,:]        = bf16( sum_e dl[t,e] * w_router[e,:] )
+ *   grad_w_router[e,:] = sum_t dl[t,e] * x[t,:]       f32
+ *   grad_bias[e]       = sum_t dl[t,e]                f32
+ * dl enters at 24-bit (grad_w_router) or at least 16-bit (grad_x) precision, sums
+ * are f32 in a fixed order: the same call gives the same bits.
+ *   grad_logits f32 [T,E];  x bf16 [T,H];  w_router bf16 [E,H]
+ *   each output may be NULL (not all three); x may be NULL without
+ *   grad_w_router, w_router without grad_x
+ *   workspace   >= moe_route_logits_backward_workspace_size(T, H, E) bytes, 16-byte aligned
+ *   T >= 0 (T = 0: the sums are 0), H > 0 multiple of 8, 1 <= E <= 1024
+ * Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (x, w_router, grad_x and grad_w_router 16
+ * bytes, the others 4), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+int moe_route_backward(const float* logits, const int32_t* topk_ids, const float* grad_w,
+                       const int32_t* expert_offsets, int T, int E, int K, int renormalize,
+                       int scoring, float balance_coef, float z_coef, float* grad_logits,
+                       float* losses, void* workspace, size_t ws_bytes, void* stream);
+size_t moe_route_backward_workspace_size(int T, int E);
+int moe_route_logits_backward(const float* grad_logits, const void* x_bf16,
+                              const void* w_router_bf16, int T, int H, int E, void* grad_x_bf16,
+                              float* grad_w_router, float* grad_bias, void* workspace,
+                              size_t ws_bytes, void* stream);
+size_t moe_route_logits_backward_workspace_size(int T, int H, int E);
+
+/* ------------------------------------------------------------------------
  * Introspection (not on the hot path; these synchronise the device).
  *
  * moe_device_status: reads and optionally clears the library's device status
@@ -631,7 +798,18 @@ enum {
   MOE_KID_GEMM_Q_DOWN = 16,   /* moe_grouped_gemm_down_q */
   MOE_KID_DEQUANT_Q = 17,     /* moe_dequantize_q_bf16 */
   MOE_KID_EXP_SIGMOID = 18,   /* moe_exp_sigmoid_f32 */
-  MOE_KID_COUNT = 20
+  MOE_KID_QUANT_FP8 = 19,        /* moe_quantize_act_fp8 */
+  MOE_KID_GEMM_FP8 = 20,         /* moe_grouped_gemm_fp8 */
+  MOE_KID_GEMM_FP8_GATEUP = 21,  /* moe_grouped_gemm_gateup_silu_fp8 */
+  MOE_KID_SILU_BACKWARD = 22,    /* moe_silu_mul_backward_fp8 */
+  MOE_KID_TRANSPOSE_FP8 = 23,    /* moe_transpose_fp8w */
+  MOE_KID_COMBINE_BACKWARD = 24, /* moe_combine_backward */
+  MOE_KID_ROUTE_BACKWARD = 25,   /* moe_route_backward */
+  MOE_KID_ROUTE_LOSSES = 26,     /* moe_route_backward: the losses' last sum */
+  MOE_KID_ROUTE_DX = 27,         /* moe_route_logits_backward: grad_x */
+  MOE_KID_ROUTE_DW = 28,         /* moe_route_logits_backward: grad_w_router */
+  MOE_KID_ROUTE_DBIAS = 29,      /* moe_route_logits_backward: grad_bias */
+  MOE_KID_COUNT = 32
 };
 int moe_device_status(int* status_out, int clear);
 int moe_launch_counts(unsigned long long* counts, int n);

@@ -26,9 +26,11 @@ KID = {
     "permute_place": 4, "permute_gather": 5, "gemm_gateup": 6, "gemm_down": 7, "combine": 8,
     "combine_gate": 9, "shared_gate": 10, "gate_sigmoid": 11, "permute_small": 12,
     "quant_act": 13, "gemm_q": 14, "gemm_q_gateup": 15, "gemm_q_down": 16, "dequant_q": 17,
-    "exp_sigmoid": 18,
+    "exp_sigmoid": 18, "quant_fp8": 19, "gemm_fp8": 20, "gemm_fp8_gateup": 21,
+    "silu_backward": 22, "transpose_fp8": 23, "combine_backward": 24, "route_backward": 25,
+    "route_losses": 26, "route_dx": 27, "route_dw": 28, "route_dbias": 29,
 }
-KID_COUNT = 20
+KID_COUNT = 32
 QFMT_Q8_0, QFMT_Q4_K = 1, 2
 
 EXPORTS = (
@@ -43,6 +45,10 @@ EXPORTS = (
     "moe_quantize_act_q8", "moe_grouped_gemm_q", "moe_grouped_gemm_gateup_silu_q",
     "moe_grouped_gemm_down_q", "moe_dequantize_q_bf16", "moe_exp_sigmoid_f32",
     "moe_grouped_gemm_gateup_silu_bf16_staged", "moe_gateup_staged_workspace_size",
+    "moe_quantize_act_fp8", "moe_grouped_gemm_fp8", "moe_grouped_gemm_gateup_silu_fp8",
+    "moe_silu_mul_backward_fp8", "moe_transpose_fp8w", "moe_combine_backward",
+    "moe_route_backward", "moe_route_backward_workspace_size", "moe_route_logits_backward",
+    "moe_route_logits_backward_workspace_size",
 )
 
 
@@ -99,6 +105,17 @@ _SIGS = {
     "moe_gate_workspace_size": ([_I], _SZ),
     "moe_device_status": ([ctypes.POINTER(_I), _I], _I),
     "moe_exp_sigmoid_f32": ([ctypes.c_uint32, ctypes.c_longlong, _P, _P, _P], _I),
+    "moe_quantize_act_fp8": ([_P, _I, _I, _I, _P, _P, _F, _P, _P, _P], _I),
+    "moe_grouped_gemm_fp8": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P], _I),
+    "moe_grouped_gemm_gateup_silu_fp8": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P],
+                                         _I),
+    "moe_silu_mul_backward_fp8": ([_P, _P, _I, _I, _P, _P, _P], _I),
+    "moe_transpose_fp8w": ([_P, _P, _I, _I, _I, _P, _P, _P], _I),
+    "moe_combine_backward": ([_P, _I, _P, _P, _I, _F, _I, _I, _I, _P, _P, _I, _P], _I),
+    "moe_route_backward": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P, _P, _P, _SZ, _P], _I),
+    "moe_route_backward_workspace_size": ([_I, _I], _SZ),
+    "moe_route_logits_backward": ([_P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P], _I),
+    "moe_route_logits_backward_workspace_size": ([_I, _I, _I], _SZ),
     "moe_launch_counts": ([ctypes.POINTER(ctypes.c_ulonglong), _I], _I),
 }
 
@@ -318,6 +335,50 @@ def moe_dequantize_q_bf16(w, qfmt, rows, K, out, stream=None, check=True):
     return _check(rc) if check else rc
 
 
+def moe_quantize_act_fp8(x, T, H, K, pair_to_row, pair_weight, routed_scale, codes, scales,
+                         stream=None, check=True):
+    """bf16 rows as E4M3 codes with a scale per 128 columns, in expert order (see moe.h)."""
+    rc = lib().moe_quantize_act_fp8(_ptr(x), T, H, K, _ptr(pair_to_row), _ptr(pair_weight),
+                                    float(routed_scale), _ptr(codes), _ptr(scales),
+                                    _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_grouped_gemm_fp8(a_codes, a_scales, w_e4m3, w_scale, group_offsets, pair_weight,
+                         row_to_pair, P, K, N, G, out, stream=None, check=True):
+    """Grouped product of FP8 activations and FP8 weights, bf16 out; with pair_weight and
+    row_to_pair the down projection (see moe.h)."""
+    rc = lib().moe_grouped_gemm_fp8(_ptr(a_codes), _ptr(a_scales), _ptr(w_e4m3), _ptr(w_scale),
+                                    _ptr(group_offsets), _ptr(pair_weight), _ptr(row_to_pair), P,
+                                    K, N, G, _ptr(out), _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_grouped_gemm_gateup_silu_fp8(a_codes, a_scales, w13_e4m3, w13_scale, group_offsets, P, H,
+                                     I, G, gate_up, act_codes, act_scales, stream=None,
+                                     check=True):
+    """FP8 gate/up product + SiLU-mul, quantised for the down projection (see moe.h)."""
+    rc = lib().moe_grouped_gemm_gateup_silu_fp8(_ptr(a_codes), _ptr(a_scales), _ptr(w13_e4m3),
+                                                _ptr(w13_scale), _ptr(group_offsets), P, H, I, G,
+                                                _ptr(gate_up), _ptr(act_codes), _ptr(act_scales),
+                                                _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_silu_mul_backward_fp8(gate_up, dact, P, I, codes, scales, stream=None, check=True):
+    """Gradient of the SiLU-mul, quantised as rows of 2I columns (see moe.h)."""
+    rc = lib().moe_silu_mul_backward_fp8(_ptr(gate_up), _ptr(dact), P, I, _ptr(codes),
+                                         _ptr(scales), _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_transpose_fp8w(w_e4m3, w_scale, G, R, C, out_e4m3, out_scale, stream=None, check=True):
+    """Block-scaled FP8 weights [G, R, C] as [G, C, R] (see moe.h)."""
+    rc = lib().moe_transpose_fp8w(_ptr(w_e4m3), _ptr(w_scale), G, R, C, _ptr(out_e4m3),
+                                  _ptr(out_scale), _stream(stream))
+    return _check(rc) if check else rc
+
+
 def moe_grouped_gemm_workspace_size(P, H, I, G) -> int:
     return lib().moe_grouped_gemm_workspace_size(P, H, I, G)
 
@@ -362,6 +423,44 @@ def shared_expert_gate(sd, sd_dtype, gl, T, H, out, out_dtype, workspace=None, w
     rc = lib().shared_expert_gate(_ptr(sd), sd_dtype, _ptr(gl), T, H, _ptr(out), out_dtype,
                                   _ptr(workspace), ws_bytes, _stream(stream))
     return _check(rc) if check else rc
+
+
+def moe_combine_backward(expert_out, eo_dtype, w, dout, do_dtype, routed_scale, T, K, H, dw,
+                         d_expert_out, deo_dtype, stream=None, check=True):
+    """Gradient of the combine's routed sum: routing weights and expert rows (see moe.h)."""
+    rc = lib().moe_combine_backward(_ptr(expert_out), eo_dtype, _ptr(w), _ptr(dout), do_dtype,
+                                    float(routed_scale), T, K, H, _ptr(dw), _ptr(d_expert_out),
+                                    deo_dtype, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_route_backward(logits, topk_ids, grad_w, expert_offsets, T, E, K, renormalize, scoring,
+                       balance_coef, z_coef, grad_logits, losses, workspace, ws_bytes,
+                       stream=None, check=True):
+    """Gradient of the routing weights, the balance loss and the z-loss with respect to the
+    logits (see moe.h)."""
+    rc = lib().moe_route_backward(_ptr(logits), _ptr(topk_ids), _ptr(grad_w),
+                                  _ptr(expert_offsets), T, E, K, renormalize, scoring,
+                                  float(balance_coef), float(z_coef), _ptr(grad_logits),
+                                  _ptr(losses), _ptr(workspace), ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_route_backward_workspace_size(T, E) -> int:
+    return lib().moe_route_backward_workspace_size(T, E)
+
+
+def moe_route_logits_backward(grad_logits, x, w_router, T, H, E, grad_x, grad_w_router, grad_bias,
+                              workspace, ws_bytes, stream=None, check=True):
+    """Gradient of the router's logits product: tokens, router weight, bias (see moe.h)."""
+    rc = lib().moe_route_logits_backward(_ptr(grad_logits), _ptr(x), _ptr(w_router), T, H, E,
+                                         _ptr(grad_x), _ptr(grad_w_router), _ptr(grad_bias),
+                                         _ptr(workspace), ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_route_logits_backward_workspace_size(T, H, E) -> int:
+    return lib().moe_route_logits_backward_workspace_size(T, H, E)
 
 
 def moe_gate_workspace_size(T) -> int:

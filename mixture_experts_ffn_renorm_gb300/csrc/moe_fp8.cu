@@ -1,0 +1,518 @@
+// moe_fp8.cu -- the expert products in 8-bit floating point: activations and
+// weights are E4M3 codes with one f32 scale per 128 columns of an activation
+// row and per 128 x 128 block of a weight matrix (the block-scaled format that
+// the FP8-weight calls of moe.h describe), and the data gradient of those
+// products through frozen weights.
+//
+// For row r of group g and output column n, with K cut into blocks b of 128:
+//   y[r,n] = sum_b  sa[r,b] * sw[g,n/128,b] * ( sum_{k in b} a[r,k] * w[g,n,k] )
+// The inner sums run on E4M3 values; the scaled joins of the blocks are f32.
+#include <cuda_fp8.h>
+
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace fp8 {
+namespace {
+
+constexpr int kBlk = 128;   // columns per activation scale, rows and columns per weight scale
+
+__host__ __device__ constexpr int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
+
+// d and 1 / d of a block whose largest magnitude is amax: every step one binary32
+// operation, so codes and scales are the same bits everywhere.  The floor keeps
+// 1 / d finite for blocks of zeros and of the smallest subnormals.
+__device__ __forceinline__ void block_scale(float amax, float& d, float& id) {
+  d = fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-126f);
+  id = __frcp_rn(d);
+}
+
+// four values as E4M3 codes (nearest even, saturating; NaN stays NaN), lowest first
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
+  return __half2float(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3));
+}
+
+// 16 bf16 values of two 16-byte vectors
+__device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&v)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 codes16(const float (&v)[16], float id) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = codes4(__fmul_rn(v[4 * i], id), __fmul_rn(v[4 * i + 1], id), __fmul_rn(v[4 * i + 2], id),
+                  __fmul_rn(v[4 * i + 3], id));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------------ quantiser
+// A lane owns 16 consecutive columns of one token, 8 lanes a scale block, so a
+// warp covers 512 columns: one 32-byte read per lane, then one 16-byte store per
+// lane for each of the token's K destination rows.  A row factor f scales every
+// value, and rounding is monotone, so the block's largest magnitude is
+// f32(amax(|x|) * |f|): it is reduced over the lanes once, not once per row.
+__global__ void __launch_bounds__(256)
+quant_rows_kernel(const uint16_t* __restrict__ x, int T, int H, int K,
+                  const int32_t* __restrict__ pair_to_row, const float* __restrict__ pair_weight,
+                  float routed_scale, uint8_t* __restrict__ codes, float* __restrict__ scales,
+                  unsigned long long* launches) {
+  count_launch(launches, MOE_KID_QUANT_FP8);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int chunks = (H + 511) / 512;
+  const long long item = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  if (item >= static_cast<long long>(T) * chunks) return;
+  const int t = static_cast<int>(item / chunks);
+  const int col = static_cast<int>(item % chunks) * 512 + lane * 16;
+  const bool live = col < H;   // H % 16 == 0
+  float v[16];
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  if (live) {
+    const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(t) * H + col);
+    a = __ldg(src);
+    b = __ldg(src + 1);
+  }
+  widen16(a, b, v);
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));   // fmaxf skips NaN
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (!live) return;
+  const int P = T * K;
+  const int nb = blocks_of(H);
+  for (int j = 0; j < K; ++j) {
+    const int p = t * K + j;
+    const int row = pair_to_row ? __ldg(pair_to_row + p) : p;
+    if (row < 0 || row >= P) continue;
+    const float f = pair_weight ? __fmul_rn(__ldg(pair_weight + p), routed_scale) : routed_scale;
+    float w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __fmul_rn(v[i], f);
+    float d, id;
+    block_scale(__fmul_rn(amax, fabsf(f)), d, id);
+    *reinterpret_cast<uint4*>(codes + static_cast<size_t>(row) * H + col) = codes16(w, id);
+    if ((lane & 7) == 0) scales[static_cast<size_t>(row) * nb + col / kBlk] = d;
+  }
+}
+
+// ------------------------------------------------------------------ SiLU-mul backward
+// a = silu(g) u with s = sigmoid(g):  dg = da u s (1 + g (1 - s)),  du = da g s.
+// The gradient row (dg, then du: 2I columns) is quantised in blocks of 128 of its
+// own columns straight from binary32.  Lanes own 16 columns as in the quantiser.
+__global__ void __launch_bounds__(256)
+silu_mul_backward_kernel(const uint16_t* __restrict__ gu, const uint16_t* __restrict__ dact, int P,
+                         int I, uint8_t* __restrict__ codes, float* __restrict__ scales,
+                         unsigned long long* launches) {
+  count_launch(launches, MOE_KID_SILU_BACKWARD);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int W = 2 * I;
+  const int chunks = (W + 511) / 512;
+  const long long item = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  if (item >= static_cast<long long>(P) * chunks) return;
+  const size_t r = static_cast<size_t>(item / chunks);
+  const int col = static_cast<int>(item % chunks) * 512 + lane * 16;
+  const bool live = col < W;
+  float v[16];
+  float amax = 0.0f;
+  if (live) {
+    const bool is_up = col >= I;             // I % 16 == 0: a lane's columns are all gate or all up
+    const int c = is_up ? col - I : col;
+    float g[16], u[16], da[16];
+    const uint4* pg = reinterpret_cast<const uint4*>(gu + r * W + c);
+    const uint4* pu = reinterpret_cast<const uint4*>(gu + r * W + I + c);
+    const uint4* pd = reinterpret_cast<const uint4*>(dact + r * I + c);
+    widen16(__ldg(pg), __ldg(pg + 1), g);
+    widen16(__ldg(pu), __ldg(pu + 1), u);
+    widen16(__ldg(pd), __ldg(pd + 1), da);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float s = __fdividef(1.0f, 1.0f + __expf(-g[i]));
+      v[i] = is_up ? da[i] * g[i] * s : da[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+      amax = fmaxf(amax, fabsf(v[i]));
+    }
+  }
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (!live) return;
+  float d, id;
+  block_scale(amax, d, id);
+  *reinterpret_cast<uint4*>(codes + r * W + col) = codes16(v, id);
+  if ((lane & 7) == 0) scales[r * blocks_of(W) + col / kBlk] = d;
+}
+
+// ------------------------------------------------------------------ weight transpose
+// 64 x 64 codes per block through shared memory (rows padded to 68 bytes)
+__global__ void __launch_bounds__(256)
+transpose_codes_kernel(const uint8_t* __restrict__ w, const float* __restrict__ scale, int R, int C,
+                       uint8_t* __restrict__ out, float* __restrict__ out_scale,
+                       unsigned long long* launches) {
+  __shared__ uint8_t tile[64][68];
+  count_launch(launches, MOE_KID_TRANSPOSE_FP8);
+  grid_dep_wait();
+  grid_dep_launch();
+  const size_t g = blockIdx.z;
+  const int c0 = blockIdx.x * 64, r0 = blockIdx.y * 64;
+  const int q = threadIdx.x & 15, y = threadIdx.x >> 4;
+  for (int i = y; i < 64; i += 16) {
+    const int r = r0 + i, c = c0 + 4 * q;
+    if (r < R && c < C)   // C % 16 == 0
+      *reinterpret_cast<uint32_t*>(&tile[i][4 * q]) =
+          __ldg(reinterpret_cast<const uint32_t*>(w + (g * R + r) * C + c));
+  }
+  __syncthreads();
+  for (int i = y; i < 64; i += 16) {
+    const int c = c0 + i, r = r0 + 4 * q;
+    if (c < C && r < R) {
+      const uint32_t v = tile[4 * q][i] | (tile[4 * q + 1][i] << 8) | (tile[4 * q + 2][i] << 16) |
+                         (static_cast<uint32_t>(tile[4 * q + 3][i]) << 24);
+      *reinterpret_cast<uint32_t*>(out + (g * C + c) * R + r) = v;
+    }
+  }
+  // the scale of a 128 x 128 block, by the block of threads at its first corner
+  if (threadIdx.x == 0 && c0 % kBlk == 0 && r0 % kBlk == 0) {
+    const int rb = blocks_of(R), cb = blocks_of(C);
+    out_scale[(g * cb + c0 / kBlk) * rb + r0 / kBlk] =
+        __ldg(scale + (g * rb + r0 / kBlk) * cb + c0 / kBlk);
+  }
+}
+
+// ------------------------------------------------------------------ grouped product
+struct GemmParams {
+  const uint8_t* a;
+  const float* sa;               // [P, blocks(K)]
+  const uint8_t* w;              // [G, rows, K]
+  const float* sw;               // [G, blocks(rows), blocks(K)]
+  const int32_t* group_offsets;  // [G + 1], or null: one group of P rows
+  int P, K, N, G;                // N: output columns (I for gate/up)
+  const float* pair_weight;
+  const int32_t* row_to_pair;
+  uint16_t* out;                 // bf16 [P, N]; gate/up: bf16 [P, 2N] or null
+  uint8_t* act;                  // gate/up: codes [P, N]
+  float* act_scale;              // gate/up: [P, blocks(N)]
+  unsigned long long* launches;
+  int kid;
+};
+
+// One block of 256 threads computes 32 rows x 256 weight rows on the CUDA cores:
+// 256 output columns, or 128 gate and the matching 128 up columns.  Warp y holds
+// rows 4y .. 4y + 3, lane x the weight rows x + 32 j: a scale block of an act row
+// is then one warp's.
+template <bool kGU>
+__global__ void __launch_bounds__(256)
+simple_gemm_kernel(const GemmParams p) {
+  __shared__ float as[32][33];
+  __shared__ float bs[256][33];
+  __shared__ int s_tile[3];
+  count_launch(p.launches, p.kid);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = threadIdx.x, x = tid & 31, y = tid >> 5;
+  if (tid == 0) {   // the group and rows of this block
+    int left = blockIdx.y;
+    s_tile[0] = -1;
+    for (int g = 0; g < p.G; ++g) {
+      const int lo = p.group_offsets ? max(0, min(p.P, p.group_offsets[g])) : 0;
+      const int hi = p.group_offsets ? max(lo, min(p.P, p.group_offsets[g + 1])) : p.P;
+      const int n = (hi - lo + 31) / 32;
+      if (left < n) {
+        s_tile[0] = g;
+        s_tile[1] = lo + 32 * left;
+        s_tile[2] = hi;
+        break;
+      }
+      left -= n;
+    }
+  }
+  __syncthreads();
+  const int g = s_tile[0];
+  if (g < 0) return;
+  const int r0 = s_tile[1], hi = s_tile[2];
+  const int rows = kGU ? 2 * p.N : p.N;               // weight rows of a group
+  const int n0 = blockIdx.x * (kGU ? 128 : 256);
+  const int nb = blocks_of(p.K), rb = blocks_of(rows);
+  // weight row of column slot j: gate rows then up rows for gate/up
+  auto wrow = [&](int slot) {
+    const int c = kGU ? n0 + (slot & 127) : n0 + slot;
+    return c < p.N ? (kGU && slot >= 128 ? p.N + c : c) : -1;
+  };
+  float acc[4][8], part[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = part[i][j] = 0.0f;
+  for (int k0 = 0; k0 < p.K; k0 += 32) {
+    for (int i = tid; i < 32 * 32; i += 256) {
+      const int r = r0 + (i >> 5), k = k0 + (i & 31);
+      as[i >> 5][i & 31] = r < hi && k < p.K ? e4m3_to_f32(p.a[static_cast<size_t>(r) * p.K + k]) : 0.0f;
+    }
+    for (int i = tid; i < 256 * 32; i += 256) {
+      const int wr = wrow(i >> 5), k = k0 + (i & 31);
+      bs[i >> 5][i & 31] = wr >= 0 && k < p.K
+          ? e4m3_to_f32(p.w[(static_cast<size_t>(g) * rows + wr) * p.K + k]) : 0.0f;
+    }
+    __syncthreads();
+    for (int k = 0; k < 32; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float b = bs[x + 32 * j][k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[i][j] = fmaf(as[4 * y + i][k], b, part[i][j]);
+      }
+    }
+    __syncthreads();
+    if ((k0 + 32) % kBlk == 0 || k0 + 32 >= p.K) {   // the end of a scale block
+      const int kb = k0 / kBlk;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int wr = wrow(x + 32 * j);
+        const float sw =
+            wr >= 0 ? __ldg(p.sw + (static_cast<size_t>(g) * rb + wr / kBlk) * nb + kb) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 4 * y + i;
+          const float sa = r < hi ? __ldg(p.sa + static_cast<size_t>(r) * nb + kb) : 0.0f;
+          acc[i][j] = fmaf(part[i][j], sa * sw, acc[i][j]);
+          part[i][j] = 0.0f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * y + i;
+    if (r >= hi) continue;   // the same for the whole warp
+    if (!kGU) {
+      const int dst = p.row_to_pair ? __ldg(p.row_to_pair + r) : r;
+      if (dst < 0 || dst >= p.P) continue;
+      const float w = p.pair_weight ? __ldg(p.pair_weight + dst) : 1.0f;
+      for (int j = 0; j < 8; ++j) {
+        const int c = n0 + x + 32 * j;
+        if (c < p.N) p.out[static_cast<size_t>(dst) * p.N + c] = f32_to_bf16_bits(__fmul_rn(acc[i][j], w));
+      }
+    } else {
+      float a[4], amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = n0 + x + 32 * j;
+        const uint16_t gb = f32_to_bf16_bits(acc[i][j]), ub = f32_to_bf16_bits(acc[i][j + 4]);
+        if (c < p.N && p.out) {
+          p.out[static_cast<size_t>(r) * 2 * p.N + c] = gb;
+          p.out[static_cast<size_t>(r) * 2 * p.N + p.N + c] = ub;
+        }
+        const float gv = bf16_bits_to_f32(gb);
+        a[j] = c < p.N ? __fdividef(gv, 1.0f + __expf(-gv)) * bf16_bits_to_f32(ub) : 0.0f;
+        amax = fmaxf(amax, fabsf(a[j]));
+      }
+      for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      float d, id;
+      block_scale(amax, d, id);
+      for (int j = 0; j < 4; ++j) {
+        const int c = n0 + x + 32 * j;
+        if (c < p.N)
+          p.act[static_cast<size_t>(r) * p.N + c] =
+              __nv_cvt_float_to_fp8(__fmul_rn(a[j], id), __NV_SATFINITE, __NV_E4M3);
+      }
+      if (x == 0) p.act_scale[static_cast<size_t>(r) * blocks_of(p.N) + n0 / kBlk] = d;
+    }
+  }
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// the checks the two products share; K is the contraction length
+int check_product(const char* op, const void* a, const void* sa, const void* w, const void* sw,
+                  const void* group_offsets, int P, int K, int N, int G) {
+  if (P < 0) return set_error(MOE_ERR_ARG, "%s: P=%d < 0", op, P);
+  if (K <= 0 || N <= 0) return set_error(MOE_ERR_ARG, "%s: dimensions must be positive", op);
+  if (G < 1 || G > gemm::kMaxGroups)
+    return set_error(MOE_ERR_ARG, "%s: G=%d outside [1, %d]", op, G, gemm::kMaxGroups);
+  if (P == 0) return MOE_OK;
+  if (!a || !sa || !w || !sw) return set_error(MOE_ERR_ARG, "%s: NULL operand or scales", op);
+  if (!group_offsets && G > 1)
+    return set_error(MOE_ERR_ARG, "%s: group_offsets is NULL with G=%d", op, G);
+  if (!aligned16(a) || !aligned16(w))
+    return set_error(MOE_ERR_ALIGN, "%s: codes must be 16-byte aligned", op);
+  if (!aligned4(sa) || !aligned4(sw) || !aligned4(group_offsets))
+    return set_error(MOE_ERR_ALIGN, "%s: scales and group_offsets must be 4-byte aligned", op);
+  return MOE_OK;
+}
+
+template <bool kGU>
+int launch_product(const char* op, GemmParams p, cudaStream_t stream) {
+  const long long row_tiles = (p.P + 31) / 32 + (p.G < p.P ? p.G : p.P);
+  if (row_tiles > 65535) return set_error(MOE_ERR_ARG, "%s: P=%d is too large", op, p.P);
+  p.launches = device_diag().launches;
+  const int cols = kGU ? 128 : 256;
+  return launch_status(launch_kernel(simple_gemm_kernel<kGU>,
+                                     dim3(static_cast<unsigned>((p.N + cols - 1) / cols),
+                                          static_cast<unsigned>(row_tiles)),
+                                     dim3(256), 0, stream, nullptr, 0, p),
+                       op);
+}
+
+}  // namespace
+}  // namespace fp8
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::fp8;
+
+extern "C" {
+
+int moe_quantize_act_fp8(const void* x_bf16, int T, int H, int K, const int32_t* pair_to_row,
+                         const float* pair_weight, float routed_scale, uint8_t* codes,
+                         float* scales, void* stream) {
+  clear_error();
+  const char* op = "moe_quantize_act_fp8";
+  if (T < 0 || H <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d", op, T, H);
+  if (K < 1 || K > 64) return set_error(MOE_ERR_ARG, "%s: K=%d outside [1, 64]", op, K);
+  if (static_cast<long long>(T) * K > 0x7FFFFFFFLL)
+    return set_error(MOE_ERR_ARG, "%s: T*K is too large", op);
+  if (H % 16 != 0) return set_error(MOE_ERR_ALIGN, "%s: H=%d is not a multiple of 16", op, H);
+  if (T == 0) return MOE_OK;
+  if (!x_bf16 || !codes || !scales) return set_error(MOE_ERR_ARG, "%s: NULL operand", op);
+  if (!aligned16(x_bf16) || !aligned16(codes))
+    return set_error(MOE_ERR_ALIGN, "%s: x and codes must be 16-byte aligned", op);
+  if (!aligned4(scales) || !aligned4(pair_to_row) || !aligned4(pair_weight))
+    return set_error(MOE_ERR_ALIGN, "%s: scales, pair_to_row and pair_weight must be 4-byte aligned",
+                     op);
+  const long long warps = static_cast<long long>(T) * ((H + 511) / 512);
+  const long long blocks = (warps + 7) / 8;
+  if (blocks > 0x7FFFFFFFLL) return set_error(MOE_ERR_ARG, "%s: T*H is too large", op);
+  return launch_status(
+      launch_kernel(quant_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                    static_cast<cudaStream_t>(stream), nullptr, 0,
+                    static_cast<const uint16_t*>(x_bf16), T, H, K, pair_to_row, pair_weight,
+                    routed_scale, codes, scales, device_diag().launches),
+      op);
+}
+
+int moe_grouped_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const uint8_t* w_e4m3,
+                         const float* w_scale, const int32_t* group_offsets,
+                         const float* pair_weight, const int32_t* row_to_pair, int P, int K, int N,
+                         int G, void* out_bf16, void* stream) {
+  clear_error();
+  const char* op = "moe_grouped_gemm_fp8";
+  int rc = check_product(op, a_codes, a_scales, w_e4m3, w_scale, group_offsets, P, K, N, G);
+  if (rc != MOE_OK) return rc;
+  if (K % 16 != 0 || N % 8 != 0)
+    return set_error(MOE_ERR_ALIGN, "%s: K=%d must be a multiple of 16 and N=%d of 8", op, K, N);
+  if (P == 0) return MOE_OK;
+  if (!out_bf16) return set_error(MOE_ERR_ARG, "%s: NULL out", op);
+  if (!aligned16(out_bf16)) return set_error(MOE_ERR_ALIGN, "%s: out must be 16-byte aligned", op);
+  if (!aligned4(pair_weight) || !aligned4(row_to_pair))
+    return set_error(MOE_ERR_ALIGN, "%s: pair_weight and row_to_pair must be 4-byte aligned", op);
+  GemmParams p{};
+  p.a = a_codes;
+  p.sa = a_scales;
+  p.w = w_e4m3;
+  p.sw = w_scale;
+  p.group_offsets = group_offsets;
+  p.P = P;
+  p.K = K;
+  p.N = N;
+  p.G = G;
+  p.pair_weight = pair_weight;
+  p.row_to_pair = row_to_pair;
+  p.out = static_cast<uint16_t*>(out_bf16);
+  p.kid = MOE_KID_GEMM_FP8;
+  return launch_product<false>(op, p, static_cast<cudaStream_t>(stream));
+}
+
+int moe_grouped_gemm_gateup_silu_fp8(const uint8_t* a_codes, const float* a_scales,
+                                     const uint8_t* w13_e4m3, const float* w13_scale,
+                                     const int32_t* group_offsets, int P, int H, int I, int G,
+                                     void* gate_up_bf16, uint8_t* act_codes, float* act_scales,
+                                     void* stream) {
+  clear_error();
+  const char* op = "moe_grouped_gemm_gateup_silu_fp8";
+  int rc = check_product(op, a_codes, a_scales, w13_e4m3, w13_scale, group_offsets, P, H, I, G);
+  if (rc != MOE_OK) return rc;
+  if (H % 16 != 0 || I % 16 != 0)
+    return set_error(MOE_ERR_ALIGN, "%s: H=%d and I=%d must be multiples of 16", op, H, I);
+  if (P == 0) return MOE_OK;
+  if (!act_codes || !act_scales) return set_error(MOE_ERR_ARG, "%s: NULL act_codes or act_scales", op);
+  if (!aligned16(act_codes) || !aligned16(gate_up_bf16) || !aligned4(act_scales))
+    return set_error(MOE_ERR_ALIGN,
+                     "%s: act_codes and gate_up must be 16-byte aligned, act_scales 4-byte", op);
+  GemmParams p{};
+  p.a = a_codes;
+  p.sa = a_scales;
+  p.w = w13_e4m3;
+  p.sw = w13_scale;
+  p.group_offsets = group_offsets;
+  p.P = P;
+  p.K = H;
+  p.N = I;
+  p.G = G;
+  p.out = static_cast<uint16_t*>(gate_up_bf16);
+  p.act = act_codes;
+  p.act_scale = act_scales;
+  p.kid = MOE_KID_GEMM_FP8_GATEUP;
+  return launch_product<true>(op, p, static_cast<cudaStream_t>(stream));
+}
+
+int moe_silu_mul_backward_fp8(const void* gate_up_bf16, const void* dact_bf16, int P, int I,
+                              uint8_t* codes, float* scales, void* stream) {
+  clear_error();
+  const char* op = "moe_silu_mul_backward_fp8";
+  if (P < 0 || I <= 0 || I > 0x3FFFFFFF) return set_error(MOE_ERR_ARG, "%s: bad sizes P=%d I=%d", op, P, I);
+  if (I % 16 != 0) return set_error(MOE_ERR_ALIGN, "%s: I=%d is not a multiple of 16", op, I);
+  if (P == 0) return MOE_OK;
+  if (!gate_up_bf16 || !dact_bf16 || !codes || !scales)
+    return set_error(MOE_ERR_ARG, "%s: NULL operand", op);
+  if (!aligned16(gate_up_bf16) || !aligned16(dact_bf16) || !aligned16(codes) || !aligned4(scales))
+    return set_error(MOE_ERR_ALIGN,
+                     "%s: gate_up, dact and codes must be 16-byte aligned, scales 4-byte", op);
+  const long long warps = static_cast<long long>(P) * ((2 * I + 511) / 512);
+  const long long blocks = (warps + 7) / 8;
+  if (blocks > 0x7FFFFFFFLL) return set_error(MOE_ERR_ARG, "%s: P*I is too large", op);
+  return launch_status(
+      launch_kernel(silu_mul_backward_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                    static_cast<cudaStream_t>(stream), nullptr, 0,
+                    static_cast<const uint16_t*>(gate_up_bf16),
+                    static_cast<const uint16_t*>(dact_bf16), P, I, codes, scales,
+                    device_diag().launches),
+      op);
+}
+
+int moe_transpose_fp8w(const uint8_t* w_e4m3, const float* w_scale, int G, int R, int C,
+                       uint8_t* out_e4m3, float* out_scale, void* stream) {
+  clear_error();
+  const char* op = "moe_transpose_fp8w";
+  if (G < 1 || G > gemm::kMaxGroups)
+    return set_error(MOE_ERR_ARG, "%s: G=%d outside [1, %d]", op, G, gemm::kMaxGroups);
+  if (R <= 0 || C <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes R=%d C=%d", op, R, C);
+  if (R % 16 != 0 || C % 16 != 0)
+    return set_error(MOE_ERR_ALIGN, "%s: R=%d and C=%d must be multiples of 16", op, R, C);
+  if ((R + 63) / 64 > 65535) return set_error(MOE_ERR_ARG, "%s: R=%d is too large", op, R);
+  if (!w_e4m3 || !w_scale || !out_e4m3 || !out_scale)
+    return set_error(MOE_ERR_ARG, "%s: NULL operand", op);
+  if (!aligned16(w_e4m3) || !aligned16(out_e4m3) || !aligned4(w_scale) || !aligned4(out_scale))
+    return set_error(MOE_ERR_ALIGN, "%s: codes must be 16-byte aligned, scales 4-byte", op);
+  return launch_status(
+      launch_kernel(transpose_codes_kernel,
+                    dim3(static_cast<unsigned>((C + 63) / 64), static_cast<unsigned>((R + 63) / 64),
+                         static_cast<unsigned>(G)),
+                    dim3(256), 0, static_cast<cudaStream_t>(stream), nullptr, 0, w_e4m3, w_scale, R,
+                    C, out_e4m3, out_scale, device_diag().launches),
+      op);
+}
+
+}  // extern "C"
