@@ -1,0 +1,74 @@
+// fp8_common.cuh -- block-scaled E4M3 rows: the scale and code arithmetic that
+// the quantiser and the products share, and the products' arguments.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace fp8 {
+
+constexpr int kBlk = 128;   // columns per activation scale, rows and columns per weight scale
+
+__host__ __device__ constexpr int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
+
+// d and 1 / d of a block whose largest magnitude is amax: every step one binary32
+// operation, so codes and scales are the same bits everywhere.  The floor keeps
+// 1 / d finite for blocks of zeros and of the smallest subnormals.
+__device__ __forceinline__ void block_scale(float amax, float& d, float& id) {
+  d = fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-126f);
+  id = __frcp_rn(d);
+}
+
+// four values as E4M3 codes (nearest even, saturating; NaN stays NaN), lowest first
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
+  return __half2float(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3));
+}
+
+// 16 bf16 values of two 16-byte vectors
+__device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&v)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 codes16(const float (&v)[16], float id) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = codes4(__fmul_rn(v[4 * i], id), __fmul_rn(v[4 * i + 1], id), __fmul_rn(v[4 * i + 2], id),
+                  __fmul_rn(v[4 * i + 3], id));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct GemmParams {
+  const uint8_t* a;
+  const float* sa;               // [P, blocks(K)]
+  const uint8_t* w;              // [G, rows, K]
+  const float* sw;               // [G, blocks(rows), blocks(K)]
+  const int32_t* group_offsets;  // [G + 1], or null: one group of P rows
+  int P, K, N, G;                // N: output columns (I for gate/up)
+  const float* pair_weight;
+  const int32_t* row_to_pair;
+  uint16_t* out;                 // bf16 [P, N]; gate/up: bf16 [P, 2N] or null
+  uint8_t* act;                  // gate/up: codes [P, N]
+  float* act_scale;              // gate/up: [P, blocks(N)]
+  int kid;
+};
+
+// the products on the tensor cores (moe_fp8_gemm.cu); gateup: SiLU-mul and
+// quantised activations.  Arguments already checked.
+int launch_product(const char* op, const GemmParams& p, bool gateup, cudaStream_t stream);
+
+}  // namespace fp8
+}  // namespace moe

@@ -7,55 +7,11 @@
 // For row r of group g and output column n, with K cut into blocks b of 128:
 //   y[r,n] = sum_b  sa[r,b] * sw[g,n/128,b] * ( sum_{k in b} a[r,k] * w[g,n,k] )
 // The inner sums run on E4M3 values; the scaled joins of the blocks are f32.
-#include <cuda_fp8.h>
-
-#include "gemm_common.cuh"
+#include "fp8_common.cuh"
 
 namespace moe {
 namespace fp8 {
 namespace {
-
-constexpr int kBlk = 128;   // columns per activation scale, rows and columns per weight scale
-
-__host__ __device__ constexpr int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
-
-// d and 1 / d of a block whose largest magnitude is amax: every step one binary32
-// operation, so codes and scales are the same bits everywhere.  The floor keeps
-// 1 / d finite for blocks of zeros and of the smallest subnormals.
-__device__ __forceinline__ void block_scale(float amax, float& d, float& id) {
-  d = fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-126f);
-  id = __frcp_rn(d);
-}
-
-// four values as E4M3 codes (nearest even, saturating; NaN stays NaN), lowest first
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
-}
-
-__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
-  return __half2float(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3));
-}
-
-// 16 bf16 values of two 16-byte vectors
-__device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&v)[16]) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 codes16(const float (&v)[16], float id) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = codes4(__fmul_rn(v[4 * i], id), __fmul_rn(v[4 * i + 1], id), __fmul_rn(v[4 * i + 2], id),
-                  __fmul_rn(v[4 * i + 3], id));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // ------------------------------------------------------------------ quantiser
 // A lane owns 16 consecutive columns of one token, 8 lanes a scale block, so a
@@ -192,147 +148,6 @@ transpose_codes_kernel(const uint8_t* __restrict__ w, const float* __restrict__ 
   }
 }
 
-// ------------------------------------------------------------------ grouped product
-struct GemmParams {
-  const uint8_t* a;
-  const float* sa;               // [P, blocks(K)]
-  const uint8_t* w;              // [G, rows, K]
-  const float* sw;               // [G, blocks(rows), blocks(K)]
-  const int32_t* group_offsets;  // [G + 1], or null: one group of P rows
-  int P, K, N, G;                // N: output columns (I for gate/up)
-  const float* pair_weight;
-  const int32_t* row_to_pair;
-  uint16_t* out;                 // bf16 [P, N]; gate/up: bf16 [P, 2N] or null
-  uint8_t* act;                  // gate/up: codes [P, N]
-  float* act_scale;              // gate/up: [P, blocks(N)]
-  unsigned long long* launches;
-  int kid;
-};
-
-// One block of 256 threads computes 32 rows x 256 weight rows on the CUDA cores:
-// 256 output columns, or 128 gate and the matching 128 up columns.  Warp y holds
-// rows 4y .. 4y + 3, lane x the weight rows x + 32 j: a scale block of an act row
-// is then one warp's.
-template <bool kGU>
-__global__ void __launch_bounds__(256)
-simple_gemm_kernel(const GemmParams p) {
-  __shared__ float as[32][33];
-  __shared__ float bs[256][33];
-  __shared__ int s_tile[3];
-  count_launch(p.launches, p.kid);
-  grid_dep_wait();
-  grid_dep_launch();
-  const int tid = threadIdx.x, x = tid & 31, y = tid >> 5;
-  if (tid == 0) {   // the group and rows of this block
-    int left = blockIdx.y;
-    s_tile[0] = -1;
-    for (int g = 0; g < p.G; ++g) {
-      const int lo = p.group_offsets ? max(0, min(p.P, p.group_offsets[g])) : 0;
-      const int hi = p.group_offsets ? max(lo, min(p.P, p.group_offsets[g + 1])) : p.P;
-      const int n = (hi - lo + 31) / 32;
-      if (left < n) {
-        s_tile[0] = g;
-        s_tile[1] = lo + 32 * left;
-        s_tile[2] = hi;
-        break;
-      }
-      left -= n;
-    }
-  }
-  __syncthreads();
-  const int g = s_tile[0];
-  if (g < 0) return;
-  const int r0 = s_tile[1], hi = s_tile[2];
-  const int rows = kGU ? 2 * p.N : p.N;               // weight rows of a group
-  const int n0 = blockIdx.x * (kGU ? 128 : 256);
-  const int nb = blocks_of(p.K), rb = blocks_of(rows);
-  // weight row of column slot j: gate rows then up rows for gate/up
-  auto wrow = [&](int slot) {
-    const int c = kGU ? n0 + (slot & 127) : n0 + slot;
-    return c < p.N ? (kGU && slot >= 128 ? p.N + c : c) : -1;
-  };
-  float acc[4][8], part[4][8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = part[i][j] = 0.0f;
-  for (int k0 = 0; k0 < p.K; k0 += 32) {
-    for (int i = tid; i < 32 * 32; i += 256) {
-      const int r = r0 + (i >> 5), k = k0 + (i & 31);
-      as[i >> 5][i & 31] = r < hi && k < p.K ? e4m3_to_f32(p.a[static_cast<size_t>(r) * p.K + k]) : 0.0f;
-    }
-    for (int i = tid; i < 256 * 32; i += 256) {
-      const int wr = wrow(i >> 5), k = k0 + (i & 31);
-      bs[i >> 5][i & 31] = wr >= 0 && k < p.K
-          ? e4m3_to_f32(p.w[(static_cast<size_t>(g) * rows + wr) * p.K + k]) : 0.0f;
-    }
-    __syncthreads();
-    for (int k = 0; k < 32; ++k) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float b = bs[x + 32 * j][k];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[i][j] = fmaf(as[4 * y + i][k], b, part[i][j]);
-      }
-    }
-    __syncthreads();
-    if ((k0 + 32) % kBlk == 0 || k0 + 32 >= p.K) {   // the end of a scale block
-      const int kb = k0 / kBlk;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int wr = wrow(x + 32 * j);
-        const float sw =
-            wr >= 0 ? __ldg(p.sw + (static_cast<size_t>(g) * rb + wr / kBlk) * nb + kb) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + 4 * y + i;
-          const float sa = r < hi ? __ldg(p.sa + static_cast<size_t>(r) * nb + kb) : 0.0f;
-          acc[i][j] = fmaf(part[i][j], sa * sw, acc[i][j]);
-          part[i][j] = 0.0f;
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 4 * y + i;
-    if (r >= hi) continue;   // the same for the whole warp
-    if (!kGU) {
-      const int dst = p.row_to_pair ? __ldg(p.row_to_pair + r) : r;
-      if (dst < 0 || dst >= p.P) continue;
-      const float w = p.pair_weight ? __ldg(p.pair_weight + dst) : 1.0f;
-      for (int j = 0; j < 8; ++j) {
-        const int c = n0 + x + 32 * j;
-        if (c < p.N) p.out[static_cast<size_t>(dst) * p.N + c] = f32_to_bf16_bits(__fmul_rn(acc[i][j], w));
-      }
-    } else {
-      float a[4], amax = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = n0 + x + 32 * j;
-        const uint16_t gb = f32_to_bf16_bits(acc[i][j]), ub = f32_to_bf16_bits(acc[i][j + 4]);
-        if (c < p.N && p.out) {
-          p.out[static_cast<size_t>(r) * 2 * p.N + c] = gb;
-          p.out[static_cast<size_t>(r) * 2 * p.N + p.N + c] = ub;
-        }
-        const float gv = bf16_bits_to_f32(gb);
-        a[j] = c < p.N ? __fdividef(gv, 1.0f + __expf(-gv)) * bf16_bits_to_f32(ub) : 0.0f;
-        amax = fmaxf(amax, fabsf(a[j]));
-      }
-      for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      float d, id;
-      block_scale(amax, d, id);
-      for (int j = 0; j < 4; ++j) {
-        const int c = n0 + x + 32 * j;
-        if (c < p.N)
-          p.act[static_cast<size_t>(r) * p.N + c] =
-              __nv_cvt_float_to_fp8(__fmul_rn(a[j], id), __NV_SATFINITE, __NV_E4M3);
-      }
-      if (x == 0) p.act_scale[static_cast<size_t>(r) * blocks_of(p.N) + n0 / kBlk] = d;
-    }
-  }
-}
-
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // the checks the two products share; K is the contraction length
@@ -351,19 +166,6 @@ int check_product(const char* op, const void* a, const void* sa, const void* w, 
   if (!aligned4(sa) || !aligned4(sw) || !aligned4(group_offsets))
     return set_error(MOE_ERR_ALIGN, "%s: scales and group_offsets must be 4-byte aligned", op);
   return MOE_OK;
-}
-
-template <bool kGU>
-int launch_product(const char* op, GemmParams p, cudaStream_t stream) {
-  const long long row_tiles = (p.P + 31) / 32 + (p.G < p.P ? p.G : p.P);
-  if (row_tiles > 65535) return set_error(MOE_ERR_ARG, "%s: P=%d is too large", op, p.P);
-  p.launches = device_diag().launches;
-  const int cols = kGU ? 128 : 256;
-  return launch_status(launch_kernel(simple_gemm_kernel<kGU>,
-                                     dim3(static_cast<unsigned>((p.N + cols - 1) / cols),
-                                          static_cast<unsigned>(row_tiles)),
-                                     dim3(256), 0, stream, nullptr, 0, p),
-                       op);
 }
 
 }  // namespace
@@ -432,7 +234,7 @@ int moe_grouped_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const ui
   p.row_to_pair = row_to_pair;
   p.out = static_cast<uint16_t*>(out_bf16);
   p.kid = MOE_KID_GEMM_FP8;
-  return launch_product<false>(op, p, static_cast<cudaStream_t>(stream));
+  return launch_product(op, p, false, static_cast<cudaStream_t>(stream));
 }
 
 int moe_grouped_gemm_gateup_silu_fp8(const uint8_t* a_codes, const float* a_scales,
@@ -465,7 +267,7 @@ int moe_grouped_gemm_gateup_silu_fp8(const uint8_t* a_codes, const float* a_scal
   p.act = act_codes;
   p.act_scale = act_scales;
   p.kid = MOE_KID_GEMM_FP8_GATEUP;
-  return launch_product<true>(op, p, static_cast<cudaStream_t>(stream));
+  return launch_product(op, p, true, static_cast<cudaStream_t>(stream));
 }
 
 int moe_silu_mul_backward_fp8(const void* gate_up_bf16, const void* dact_bf16, int P, int I,
