@@ -32,6 +32,16 @@ __device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
   return __half2float(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3));
 }
 
+// 8 bf16 values of a 16-byte vector
+__device__ __forceinline__ void widen8(const uint4& a, float (&v)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
 // 16 bf16 values of two 16-byte vectors
 __device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&v)[16]) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};

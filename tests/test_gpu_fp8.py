@@ -138,6 +138,9 @@ SHAPES = [
     ([64, 64, 64, 64], 384, 256),
     ([1500, 700], 256, 520),
     ([2] * 40, 528, 128),
+    # several tiles per SM pair, tiles of one and of two parts in turn, 6 and 3 scale blocks
+    ([300, 90] * 20, 768, 1032),
+    ([129, 500, 30] * 12, 384, 1544),
 ]
 
 
@@ -213,7 +216,8 @@ def test_product_keeps_a_bad_row_to_itself():
 
 
 @pytest.mark.parametrize("sizes,H,I", [([1], 2048, 16), ([5, 0, 40], 144, 208), ([17, 130, 5], 272, 400),
-                                       ([300, 33], 1040, 128), ([2] * 20, 528, 48), ([700], 256, 1024)])
+                                       ([300, 33], 1040, 128), ([2] * 20, 528, 48), ([700], 256, 1024),
+                                       ([300, 90] * 12, 768, 1040), ([129, 500, 30] * 8, 384, 912)])
 @pytest.mark.parametrize("keep", [True, False])
 def test_gateup(sizes, H, I, keep):
     G, P = len(sizes), sum(sizes) + 2
