@@ -4,38 +4,39 @@
 // y[r,n] = sum_b (sa[r,b] sw[n,b]) p_b[r,n], p_b the product over the 128
 // columns of scale block b.  The scales change with every block of the
 // contraction, so the tensor core sums one block at a time: each block's MMAs
-// start a fresh accumulator in tensor memory, and eight epilogue warps per CTA
+// start a fresh accumulator in tensor memory, and sixteen epilogue warps per CTA
 // join the blocks in registers, acc += p_b * s_b, while the tensor core fills the
-// next accumulators.
+// next accumulators.  The round trip MMA -> join -> MMA crosses the pair and takes
+// about as long as two blocks' MMAs, so the accumulators are a ring of four (or
+// eight half as wide in launches without larger groups).
 //
-// As in moe_gemm_pair.cu a tile has weight rows on the MMA's M side (256: 128
-// per SM, one tcgen05.mma.cta_group::2) and up to 256 rows of one group on its
-// N side, so a group pads to 16 rows and the same tile serves single tokens.
-// The round trip MMA -> join -> MMA crosses the pair and takes about as long as
-// two blocks' MMAs, so the accumulators are a ring: the tile's rows go in parts
-// of 128, each with an MMA sequence and one of four accumulators of its own (parts
-// of 64 and eight accumulators when no group has more than 64 rows).
+// Every MMA is a tcgen05.mma.cta_group::2 over the two SMs of a cluster, M = 256
+// (128 per SM); a stage of the operand ring holds, per CTA, 128 weight rows and at
+// most 128 token rows of one scale block (128 bytes a row).  Two kinds of tile:
+//   rows tiles     (blocks of more than 128 rows of a group): 256 token rows on M,
+//                  256 weight rows on N in two parts of 128.  A thread owns one
+//                  token row and 64 columns of one part, so the factor s_b is one
+//                  register: one fused multiply-add per product and block.
+//   weights tiles  (blocks of up to 128 rows): 256 weight rows on M, the rows on N,
+//                  padded to 16.  A thread owns one weight row and 32 of the token
+//                  rows, whose scales its warp keeps in shared memory.
+// Rows tiles need no transpose and no scale loads per product, and pad to 256 rows;
+// weights tiles pad to 16 rows, which is what ragged and decode-sized groups need.
 //
-// A thread of the epilogue owns one weight row and half of every part's rows: 128
-// sums.  The factors s_b[r] = sa[r,b] * sw[b] are the same for every weight row of
-// a scale block, so two warps form them once per CTA and block in shared memory,
-// and the epilogue reads four per 16-byte broadcast load.  They arrive on the same
-// barrier as the part's MMAs, so the epilogue waits once per part.  (tcgen05.ld
-// in the 16x256b shape would need a fourth of those loads and feed stmatrix, but
-// moves 1024 words in 64 cycles; the 32x32b shape used here takes 18.)
-//
-//   warp 0      TMA producer: the CTA's weight rows and its half of each part's
-//               token rows, 128 bytes (one scale block) of each per stage
+//   warp 0      TMA producer: the CTA's weight rows and token rows of each stage
 //   warp 1      tensor memory; in the even CTA the one thread that issues MMAs
-//   warps 2-3   the factors s_b
-//   warps 4-11  block joins and the epilogue
+//   warps 4-19  block joins and the epilogue
 //
 // gate/up: a CTA's 128 weight rows are 64 up rows, then the 64 gate rows of the
-// same features.  Both are narrowed to bf16 into a token-major staging buffer;
-// four threads per row then form silu(gate) * up of 16 features each in f32.  The
-// largest magnitude of a row's 128 features spans both CTAs of the pair: each
-// writes its own to both through distributed shared memory, and after one
-// cluster-scope barrier per tile both quantise with the same scale.
+// same features.  Gate and up are narrowed to bf16, silu(gate) * up is formed in
+// f32 and a row's 128 features are quantised with one scale.
+//   rows tiles: part 0 is the up half and part 1 the gate half of the same 128
+//     features, so two threads of a CTA hold a row's up and gate of 64 features;
+//     each takes 32 of them, through shared memory.  The row's largest magnitude
+//     is that of four threads.
+//   weights tiles: the bf16 results are transposed through shared memory; a row's
+//     128 features span both CTAs, which exchange their maxima through distributed
+//     shared memory and one cluster-scope barrier per tile.
 //
 // The tile schedule, the bounded waits and the exit of a CTA that gives up are
 // those of moe_gemm_pair.cu.
@@ -69,46 +70,38 @@ __device__ __forceinline__ void wait_lean(uint32_t bar, uint32_t parity, volatil
   __syncwarp();
 }
 
-// The accumulator of part r of block kb of a tile of np parts: every tile begins with
-// accumulator 0, and blocks of one parity, whose factors share a slot, share
-// accumulators.
-__device__ __forceinline__ int acc_of(int kb, int r, int np, bool small) {
-  return small ? kb & 7 : 2 * (kb & 1) + (np == 2 ? r : (kb >> 1) & 1);
-}
-
-constexpr int kThreads = 384;
-constexpr int kAuxRegs = 72, kEpiRegs = 216;
-// the split draws on the registers the block was launched with (168 a thread)
-static_assert(128 * kAuxRegs + 256 * kEpiRegs <= 384 * 168, "register split");
-constexpr int kTokBlock = 256;              // rows per tile at most (MMA N)
-constexpr int kPart = 128;                  // rows per accumulator
-constexpr int kSmallPart = 64;              // the same in launches without larger groups
-constexpr int kMaxAcc = 512 / kSmallPart;
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of other roles (two of its warps idle)
+constexpr int kAuxRegs = 64, kEpiRegs = 104;
+// the split draws on the registers the block was launched with (96 a thread)
+static_assert(128 * kAuxRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 96, "register split");
+constexpr int kTokBlock = 256;              // rows per rows tile
+constexpr int kTail = 128;                  // rows of a weights tile at most
 constexpr int kStages = 6;
 constexpr int kStageBytes = 128 * 128;      // one operand's stage per CTA, at most
+constexpr int kMaxAcc = 8;
 constexpr int kMaxGroupsLaunch = 512;       // groups of one launch (schedule in shared memory)
 constexpr int kMmaK = 32;                   // K per tcgen05.mma of 8-bit types
 constexpr unsigned long long kCopyGraceNs = 100000ull;  // see moe_gemm_pair.cu
 
-template <bool kGU>
 struct Smem {
-  static constexpr int kVecs = kGU ? 3 : 1;   // factor vectors per block: rows, or gate, up, up of the next block
-  static constexpr int kSlots = 2;            // blocks the factors run ahead: at most the ring's, see below
-  static constexpr int kSlotBytes = kVecs * kTokBlock * 4;
   static constexpr int W = 0;
   static constexpr int T = W + kStages * kStageBytes;
-  static constexpr int EPI = T + kStages * kStageBytes;         // two of [32 rows][128 features] bf16
-  static constexpr int FAC = EPI + 2 * 8192;                    // factor ring
-  static constexpr int META = FAC + kSlots * kSlotBytes;        // dst and weight, or row maxima
-  static constexpr int BARS = META + 4096;
-  // full, empty [kStages], tfull, tempty [kMaxAcc], sempty [kSlots], drain, maxima [2]
-  static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + kSlots + 3;
+  static constexpr int EPI = T + kStages * kStageBytes;         // 16 KB of staging
+  static constexpr int FAC = EPI + 16384;                       // weights tiles: a warp's row scales [2][32]
+  static constexpr int META = FAC + kEpiWarps * 256;            // weights tiles: dst and weight, or row maxima
+  static constexpr int RMAX = META + 2048;                      // rows tiles: row maxima (the peer may already
+                                                                // write those of a later weights tile)
+  static constexpr int BARS = RMAX + 2048;
+  // full, empty [kStages], tfull, tempty [kMaxAcc], drain, maxima [4]
+  static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + 5;
   static constexpr int MISC = BARS + NBARS * 8;                 // tmem slot, abort flag, scan
-  static constexpr int TILE_START = MISC + 96;
-  static constexpr int GOFF = TILE_START + (kMaxGroupsLaunch + 1) * 4;
+  static constexpr int ROWS_START = (MISC + 8 + 8 * (kThreads / 32) + 15) & ~15;
+  static constexpr int TAIL_START = ROWS_START + (kMaxGroupsLaunch + 1) * 4;
+  static constexpr int GOFF = TAIL_START + (kMaxGroupsLaunch + 1) * 4;
   static constexpr int ALLOC = GOFF + (kMaxGroupsLaunch + 1) * 4 + 1024;
-  static_assert(ALLOC <= 227 * 1024, "shared memory");
 };
+static_assert(Smem::ALLOC <= 227 * 1024, "shared memory");
 
 struct KernelParams {
   GemmParams g;
@@ -119,28 +112,43 @@ struct KernelParams {
 };
 
 struct Tile {
-  int g, r0, n_tok, n0;
+  int g, r0, n_tok, n0;          // n_tok > kTail: a rows tile
 };
 
-__device__ __forceinline__ Tile tile_at(int tile, const int* tile_start, const int* goff, int G,
-                                        int n_fb, int fb_cols) {
-  int lo = 0, hi = G;  // tile_start[lo] <= tile < tile_start[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tile_start[mid] <= tile) lo = mid; else hi = mid;
+// rows tiles first, then weights tiles; each kind by group, block of rows, columns
+struct Schedule {
+  const int* rows_start;         // [G + 1] first rows tile of a group
+  const int* tail_start;         // [G + 1] first weights tile of a group, counted from n_rows
+  const int* goff;
+  int G, n_fb, n_rows, total;
+  int fb_cols;
+  __device__ __forceinline__ Tile at(int tile) const {
+    const bool tail = tile >= n_rows;
+    const int* start = tail ? tail_start : rows_start;
+    if (tail) tile -= n_rows;
+    int lo = 0, hi = G;  // start[lo] <= tile < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= tile) lo = mid; else hi = mid;
+    }
+    const int local = tile - start[lo];
+    const int rows = goff[lo + 1] - goff[lo];
+    const int m = tail ? (rows - 1) / kTokBlock : local / n_fb;
+    Tile t;
+    t.g = lo;
+    t.r0 = goff[lo] + m * kTokBlock;
+    t.n_tok = min(goff[lo + 1], t.r0 + kTokBlock) - t.r0;
+    t.n0 = (tail ? local : local - m * n_fb) * fb_cols;
+    return t;
   }
-  const int local = tile - tile_start[lo];
-  const int m = local / n_fb;
-  Tile t;
-  t.g = lo;
-  t.r0 = goff[lo] + m * kTokBlock;
-  t.n_tok = min(goff[lo + 1], t.r0 + kTokBlock) - t.r0;
-  t.n0 = (local - m * n_fb) * fb_cols;
-  return t;
-}
+};
 
-__device__ __forceinline__ int group_tiles(int rows, int n_fb) {
-  return rows > 0 ? (rows + kTokBlock - 1) / kTokBlock * n_fb : 0;
+// blocks of a group that take rows tiles, and whether its last one takes weights tiles
+__device__ __forceinline__ int rows_blocks(int rows) {
+  return rows > 0 ? rows / kTokBlock + (rows % kTokBlock > kTail ? 1 : 0) : 0;
+}
+__device__ __forceinline__ int tail_blocks(int rows) {
+  return rows > 0 && rows % kTokBlock != 0 && rows % kTokBlock <= kTail ? 1 : 0;
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
@@ -149,12 +157,17 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
   return v;
 }
 
+// silu(g) u; tolerance-checked: the fast exponential and division serve
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
 template <bool kGU>
 __global__ void __launch_bounds__(kThreads, 1)
-fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant__ CUtensorMap tmT32,
-                const __grid_constant__ CUtensorMap tmT64, const __grid_constant__ CUtensorMap tmW,
-                const KernelParams kp) {
-  using S = Smem<kGU>;
+fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant__ CUtensorMap tmT32,
+                const __grid_constant__ CUtensorMap tmT64, const __grid_constant__ CUtensorMap tmT128,
+                const __grid_constant__ CUtensorMap tmW, const KernelParams kp) {
+  using S = Smem;
   const GemmParams& p = kp.g;
   constexpr int kFbCols = kGU ? 128 : 256;   // output features per tile (both CTAs)
   constexpr int kWBox = kGU ? 64 : 128;      // weight rows per TMA box
@@ -164,8 +177,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   const uint32_t sbase = ptx::smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::MISC + 4);
-  int* scan_tmp = reinterpret_cast<int*>(smem + S::MISC + 8);   // one int per warp
-  int* tile_start = reinterpret_cast<int*>(smem + S::TILE_START);
+  int2* scan_tmp = reinterpret_cast<int2*>(smem + S::MISC + 8);   // one pair per warp
+  int* rows_start = reinterpret_cast<int*>(smem + S::ROWS_START);
+  int* tail_start = reinterpret_cast<int*>(smem + S::TAIL_START);
   int* goff = reinterpret_cast<int*>(smem + S::GOFF);
 
   // opaque, so that the inner loops hold them in registers instead of reading them anew
@@ -180,9 +194,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   auto bar_empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto bar_tfull = [&](int a) { return bars + 8u * (2 * kStages + a); };
   auto bar_tempty = [&](int a) { return bars + 8u * (2 * kStages + kMaxAcc + a); };
-  auto bar_sempty = [&](int s) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + s); };
-  const uint32_t bar_drain = bars + 8u * (S::NBARS - 3);
-  auto bar_max = [&](int h) { return bars + 8u * (S::NBARS - 2 + h); };
+  const uint32_t bar_drain = bars + 8u * (2 * kStages + 2 * kMaxAcc);
+  auto bar_max = [&](int c) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + 1 + c); };
 
   count_launch(kp.launches, p.kid);
 
@@ -192,13 +205,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       ptx::mbar_init(bar_empty(s), 1);   // the pair's MMA commit
     }
     for (int a = 0; a < kMaxAcc; ++a) {
-      ptx::mbar_init(bar_tfull(a), 3);    // the pair's MMA commit and the CTA's factor warps
-      ptx::mbar_init(bar_tempty(a), 16);  // one arrive per epilogue warp of both CTAs
+      ptx::mbar_init(bar_tfull(a), 1);    // the pair's MMA commit
+      ptx::mbar_init(bar_tempty(a), 32);  // sixteen from the warps of either CTA that read it
     }
-    for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(bar_sempty(s), 8);   // the epilogue warps
-      ptx::mbar_init(bar_max(s), 8);      // a group's four warps in both CTAs
-    }
+    for (int c = 0; c < 4; ++c) ptx::mbar_init(bar_max(c), 8);  // a group's four warps in both CTAs
     ptx::mbar_init(bar_drain, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -207,6 +217,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     ptx::tma_prefetch_desc(&tmT16);
     ptx::tma_prefetch_desc(&tmT32);
     ptx::tma_prefetch_desc(&tmT64);
+    ptx::tma_prefetch_desc(&tmT128);
     ptx::tma_prefetch_desc(&tmW);
   }
   if (warp == 1) {
@@ -226,68 +237,79 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   const int chunk = (G + kThreads - 1) / kThreads;
   const int g_lo = min(G, static_cast<int>(threadIdx.x) * chunk);
   const int g_hi = min(G, g_lo + chunk);
-  int local = 0, rows_max = 0;
+  int n_big = 0, n_tail = 0, rows_max = 0;
   for (int g = g_lo; g < g_hi; ++g) {
     const int rows = goff[g + 1] - goff[g];
-    local += group_tiles(rows, n_fb);
+    n_big += rows_blocks(rows) * n_fb;
+    n_tail += tail_blocks(rows) * n_fb;
     rows_max = max(rows_max, rows);
   }
-  int incl = local;
+  int incl_b = n_big, incl_t = n_tail;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int b = __shfl_up_sync(0xffffffffu, incl_b, o), t = __shfl_up_sync(0xffffffffu, incl_t, o);
+    if (lane >= o) {
+      incl_b += b;
+      incl_t += t;
+    }
   }
-  if (lane == 31) scan_tmp[warp] = incl;
-  const bool small = __syncthreads_or(rows_max > kSmallPart) == 0;
-  int warp_base = 0, total = 0;
+  if (lane == 31) scan_tmp[warp] = make_int2(incl_b, incl_t);
+  const bool small = __syncthreads_or(rows_max > 64) == 0;   // eight accumulators of 64 columns
+  int run_b = incl_b - n_big, run_t = incl_t - n_tail;
+  Schedule sch{rows_start, tail_start, goff, G, n_fb, 0, 0, kFbCols};
   for (int w = 0; w < kThreads / 32; ++w) {
-    const int v = scan_tmp[w];
-    if (w < warp) warp_base += v;
-    total += v;
+    const int2 v = scan_tmp[w];
+    if (w < warp) {
+      run_b += v.x;
+      run_t += v.y;
+    }
+    sch.n_rows += v.x;
+    sch.total += v.x + v.y;
   }
-  int run = warp_base + incl - local;
   for (int g = g_lo; g < g_hi; ++g) {
-    tile_start[g] = run;
-    run += group_tiles(goff[g + 1] - goff[g], n_fb);
+    const int rows = goff[g + 1] - goff[g];
+    rows_start[g] = run_b;
+    tail_start[g] = run_t;
+    run_b += rows_blocks(rows) * n_fb;
+    run_t += tail_blocks(rows) * n_fb;
   }
-  if (threadIdx.x == 0) tile_start[G] = total;
+  if (threadIdx.x == 0) {
+    rows_start[G] = sch.n_rows;
+    tail_start[G] = sch.total - sch.n_rows;
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // the peer's barriers exist before any remote arrive or copy
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int nk = blocks_of(p.K);
-  const int part = small ? kSmallPart : kPart;
-  auto tile_of = [&](int tile) { return tile_at(tile, tile_start, goff, G, n_fb, kFbCols); };
+  const int acc_shift = small ? 3 : 2;             // log2 of the accumulators in the ring
+  const uint32_t acc_mask = (1u << acc_shift) - 1u;
+  const uint32_t acc_cols = 512u >> acc_shift;
 
   bool mma_any = false;
 
   if (warp < 4) {
     ptx::setmaxnreg_dec<kAuxRegs>();
     if (warp == 0) {
-      // ---------------------------------------------------------- TMA producer
-      // lane 0 the first weight box (up rows, or all), lane 1 the gate rows, lanes 2
-      // and 3 the CTA's half of the tokens of the tile's one or two parts
+      // ------------------------------------------------------------ TMA producer
+      // lane 0 the first weight box (up rows, or all), lane 1 the gate rows, lane 2 the
+      // CTA's token rows: its half of the 256 of a rows tile, or of a weights tile's padded rows
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = unit; ok && tile < total; tile += n_units) {
-        const Tile t = tile_of(tile);
-        const int np = t.n_tok > kPart ? 2 : 1;
-        auto half_of = [&](int s) { return ((min(kPart, t.n_tok - kPart * s) + 15) & ~15) >> 1; };
-        auto box_of = [&](int half) { return half <= 16 ? 16 : (half <= 32 ? 32 : 64); };
-        const int box0 = box_of(half_of(0)), box1 = np == 2 ? box_of(half_of(1)) : 0;
-        const uint32_t bytes = kStageBytes + (box0 + box1) * 128;
+      for (int tile = unit; ok && tile < sch.total; tile += n_units) {
+        const Tile t = sch.at(tile);
+        const int half = t.n_tok > kTail ? 128 : ((t.n_tok + 15) & ~15) >> 1;
+        const int tbox = half <= 16 ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
+        const uint32_t bytes = kStageBytes + tbox * 128;
         const int wrow = t.g * kp.rows_per_group + t.n0 + static_cast<int>(rank) * (kFbCols / 2);
-        const int s = lane == 3 ? 1 : 0;
-        const int tbox = s ? box1 : box0;
-        const bool issues = lane == 0 || lane == 2 || (kGU && lane == 1) || (np == 2 && lane == 3);
+        const bool issues = lane == 0 || lane == 2 || (kGU && lane == 1);
         const CUtensorMap* mbox =
-            lane < 2 ? &tmW : (tbox == 16 ? &tmT16 : (tbox == 32 ? &tmT32 : &tmT64));
-        const int ybox = lane >= 2 ? t.r0 + kPart * s + static_cast<int>(rank) * half_of(s)
+            lane < 2 ? &tmW : (tbox == 16 ? &tmT16 : (tbox == 32 ? &tmT32 : (tbox == 64 ? &tmT64 : &tmT128)));
+        const int ybox = lane == 2 ? t.r0 + static_cast<int>(rank) * half
                                    : (kGU && lane == 0 ? wrow + p.N : wrow);
-        const uint32_t dbox = lane >= 2 ? S::T + s * (kStageBytes / 2) : S::W + (lane == 1 ? kWBox * 128 : 0);
+        const uint32_t dbox = lane == 2 ? S::T : S::W + (lane == 1 ? kWBox * 128 : 0);
         for (int kb = 0; kb < nk; ++kb) {
           bool got = true;
           if (lane == 0) {
@@ -307,31 +329,32 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         }
       }
     } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer (even CTA)
+      // ------------------------------------------------------------ MMA issuer (even CTA)
       if (leader && ptx::elect_one()) {
         int stage = 0;
-        uint32_t phase = 0, free_mask = 0;   // a bit per accumulator: parity of its next release
+        uint32_t phase = 0, parts = 0;     // parts: accumulators taken from the ring so far
         bool ok = true;
-        for (int tile = unit; ok && tile < total; tile += n_units) {
-          const Tile t = tile_of(tile);
-          const int np = t.n_tok > kPart ? 2 : 1;
+        for (int tile = unit; ok && tile < sch.total; tile += n_units) {
+          const Tile t = sch.at(tile);
+          const bool big = t.n_tok > kTail;
+          const uint32_t idesc = ptx::idesc_e4m3_f32(256, big ? 128 : (t.n_tok + 15) & ~15);
           for (int kb = 0; ok && kb < nk; ++kb) {
             ok = wait_bar(bar_full(stage), phase, abort_flag, kp.status, kp.wait_ns);
-            for (int r = 0; ok && r < np; ++r) {
-              const int acc = acc_of(kb, r, np, small);
-              ok = wait_bar<true>(bar_tempty(acc), ((free_mask >> acc) & 1u) ^ 1u, abort_flag,
+            const uint64_t dw = ptx::desc_kmajor_sw128(sbase + S::W + stage * kStageBytes);
+            const uint64_t dt = ptx::desc_kmajor_sw128(sbase + S::T + stage * kStageBytes);
+            for (int r = 0; ok && r < (big ? 2 : 1); ++r, ++parts) {
+              const uint32_t acc = parts & acc_mask;
+              ok = wait_bar<true>(bar_tempty(acc), ((parts >> acc_shift) & 1u) ^ 1u, abort_flag,
                                   kp.status, kp.wait_ns);
               if (!ok) break;
-              free_mask ^= 1u << acc;
               ptx::tc_fence_after();
-              const uint32_t idesc = ptx::idesc_e4m3_f32(256, (min(kPart, t.n_tok - kPart * r) + 15) & ~15);
-              const uint64_t dw = ptx::desc_kmajor_sw128(sbase + S::W + stage * kStageBytes);
-              const uint64_t dt =
-                  ptx::desc_kmajor_sw128(sbase + S::T + stage * kStageBytes + r * (kStageBytes / 2));
-              const uint32_t d = tmem_base + static_cast<uint32_t>(acc * part);
-#pragma unroll
+              const uint32_t d = tmem_base + acc * acc_cols;
+              // rows tiles: tokens on M, 64 weight rows of each CTA on N
+              const uint64_t da = big ? dt : dw;
+              const uint64_t db = big ? dw + static_cast<uint64_t>(r * (64 * 128 / 16)) : dt;
+  #pragma unroll
               for (int k = 0; k < kBlk / kMmaK; ++k)   // a fresh sum per scale block
-                ptx::mma_e4m3_pair(d, dw + 2ull * k, dt + 2ull * k, idesc, k != 0 ? 1u : 0u);
+                ptx::mma_e4m3_pair(d, da + 2ull * k, db + 2ull * k, idesc, k != 0 ? 1u : 0u);
               mma_any = true;
               ptx::mma_commit_pair(bar_tfull(acc), 3);     // the part's sums are ready in both
             }
@@ -341,178 +364,240 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           }
         }
       }
-    } else {
-      // ---------------------------------------------------------- factors
-      // 64 threads, rows st, st + 64, ... of the tile; the scales are loaded two
-      // blocks ahead.  A slot is written again once the epilogue has passed its last
-      // block; the accumulators of a slot's blocks are its own, so they are then in
-      // their next turn and an arrive on a part's barrier never meets the turn before.
-      const int st = static_cast<int>(threadIdx.x) - 64;
-      const int rb = blocks_of(kp.rows_per_group);
-      uint32_t free_mask = 0;   // a bit per slot: parity of its next release
-      for (int tile = unit; !*abort_flag && tile < total; tile += n_units) {
-        const Tile t = tile_of(tile);
-        const int np = t.n_tok > kPart ? 2 : 1;
-        const int first = t.n0 + static_cast<int>(rank) * (kFbCols / 2);
-        const float* sw = p.sw + static_cast<size_t>(t.g) * rb * nk;
-        int w_at[S::kVecs];
-        w_at[0] = min(first / kBlk, rb - 1) * nk;
-        if (kGU) {
-          w_at[S::kVecs > 1 ? 1 : 0] = min((p.N + first) / kBlk, rb - 1) * nk;
-          w_at[S::kVecs > 2 ? 2 : 0] = min((p.N + first) / kBlk + 1, rb - 1) * nk;
-        }
-        const float* sa = p.sa + static_cast<size_t>(t.r0) * nk;
-        int a_at[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a_at[i] = min(st + 64 * i, t.n_tok - 1) * nk;
-        auto load = [&](int kb, float (&a)[4], float (&w)[S::kVecs]) {
-          const int k = min(kb, nk - 1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (64 * i < t.n_tok) a[i] = __ldg(sa + a_at[i] + k);
-#pragma unroll
-          for (int v = 0; v < S::kVecs; ++v) w[v] = __ldg(sw + w_at[v] + k);
-        };
-        float a0[4] = {}, w0[S::kVecs], a1[4] = {}, w1[S::kVecs];
-        load(0, a0, w0);
-        load(1, a1, w1);
-        for (int kb = 0; kb < nk; ++kb) {
-          float ca[4], cw[S::kVecs];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) { ca[i] = a0[i]; a0[i] = a1[i]; }
-#pragma unroll
-          for (int v = 0; v < S::kVecs; ++v) { cw[v] = w0[v]; w0[v] = w1[v]; }
-          load(kb + 2, a1, w1);
-          const int slot = kb & 1;
-          wait_lean(bar_sempty(slot), ((free_mask >> slot) & 1u) ^ 1u, abort_flag, kp.status, kp.wait_ns);
-          free_mask ^= 1u << slot;
-          const uint32_t at = sbase + S::FAC + slot * S::kSlotBytes + st * 4;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (64 * i < t.n_tok)
-#pragma unroll
-              for (int v = 0; v < S::kVecs; ++v)
-                ptx::st_shared_f32(at + v * (kTokBlock * 4) + i * 256, __fmul_rn(ca[i], cw[v]));
-          __syncwarp();
-          if (lane < np) ptx::mbar_arrive(bar_tfull(acc_of(kb, lane, np, small)));
-        }
-      }
     }
   } else {
     // ------------------------------------------------------------ joins and epilogue
-    // Two groups of four warps: group h takes columns 64 h .. + 63 of every part
-    // (32 h .. + 31 of parts of 64).
     ptx::setmaxnreg_inc<kEpiRegs>();
-    const int h = (warp - 4) >> 2;
-    const int et = (static_cast<int>(threadIdx.x) - 128) & 127;  // thread of its group
-    const int ea = static_cast<int>(threadIdx.x) - 128;          // 0..255 over both
-    const int q = warp & 3;                                      // TMEM lane quarter
-    const int f = q * 32 + lane;                                 // weight row within the CTA
-    const int width = part >> 1;                                 // the group's columns of a part
-    const uint32_t tmem_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * width;
-    const uint32_t ost = sbase + S::EPI + h * 8192;              // [32 rows][128 features] bf16
-    // this thread's 16-bit place in staging row j: 16-byte pieces XOR-swizzled by the row
-    const uint32_t place = ost + ((f >> 3) << 4) + (f & 7) * 2;
+    const int e = warp - 4;                          // 0..15
+    const int grp = e >> 2;                          // four warps that cover the 128 TMEM lanes
+    const int h = grp & 1, set = grp >> 1;           // rows tiles: columns 64 h .. of part `set`
+    const int q = warp & 3;                          // TMEM lane quarter
+    const int f = q * 32 + lane;                     // TMEM lane
+    const int et = e * 32 + lane;                    // 0..511
+    const int gt = et & 127;                         // thread of its group
+    const uint32_t tmem_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t tempty_leader = ptx::mapa_shared(bar_tempty(0), 0);
-    uint32_t full_mask = 0, tphase = 0;   // full_mask: a bit per accumulator, parity of its next sums
-    int parity = 0;                       // of the tile: META's half
-    auto dst_of = [&](const Tile& nt) {
-      const int r = nt.r0 + ea;
-      return ea < nt.n_tok ? (p.row_to_pair ? __ldg(p.row_to_pair + r) : r) : -1;
-    };
-    int nd = -1;
-    if (!kGU && unit < total) nd = dst_of(tile_of(unit));
-    for (int tile = unit; tile < total; tile += n_units, parity ^= 1) {
-      const Tile t = tile_of(tile);
-      const int first = t.n0 + static_cast<int>(rank) * (kFbCols / 2);   // the CTA's first column
-      int* dst_t = reinterpret_cast<int*>(smem + S::META) + parity * kTokBlock;            // plain
-      float* w_t = reinterpret_cast<float*>(smem + S::META + 2048) + parity * kTokBlock;
-      if (!kGU) {
-        // destination rows and weights of this tile, the next tile's rows a tile ahead; the last
-        // readers of this half (two tiles ago) passed the previous tile's vote
-        const int d = nd >= 0 && nd < p.P ? nd : -1;
-        dst_t[ea] = d;
-        w_t[ea] = p.pair_weight && d >= 0 ? __ldg(p.pair_weight + d) : 1.0f;
-        if (tile + n_units < total) nd = dst_of(tile_of(tile + n_units));
-      }
-      // the factor vector of this thread's weight row
-      int vec = 0;
-      if (kGU && f < 64) vec = (p.N + first + f) / kBlk == (p.N + first) / kBlk ? 1 : 2;
-      const uint32_t fac0 = sbase + S::FAC + vec * (kTokBlock * 4) + h * width * 4;
-      // sum[r][i]: row 128 r + 64 h + i of the tile (32 h + i in small launches)
-      float sum[2][64];
+    const int rb = blocks_of(kp.rows_per_group);
+    uint32_t parts = 0, tphase = 0;
+    int parity = 0;                                  // of the tile: META's half
+    for (int tile = unit; tile < sch.total; tile += n_units, parity ^= 1) {
+      const Tile t = sch.at(tile);
+      const float* sw = p.sw + static_cast<size_t>(t.g) * rb * nk;
+      if (t.n_tok > kTail) {
+        // ---------------------------------------------------------- rows tile
+        const int j = static_cast<int>(rank) * 128 + f;        // this thread's row of the tile
+        const bool live = j < t.n_tok;
+        const float* sa = p.sa + static_cast<size_t>(t.r0 + (live ? j : 0)) * nk;
+        // the weight rows behind this thread's 64 columns: one scale block, or (up rows of
+        // I not a multiple of 128) two that meet at a multiple of 16
+        const int wr = kGU ? t.n0 + 64 * h + (set == 0 ? p.N : 0) : t.n0 + 128 * h + 64 * set;
+        const int wb = min(wr / kBlk, rb - 1);
+        const float* sw0 = sw + static_cast<size_t>(wb) * nk;
+        const int split = kGU && set == 0 ? (wb + 1) * kBlk - wr : 64;     // columns of the first block
+        const size_t to_sw1 = kGU && split < 64 && wb + 1 < rb ? nk : 0;
+        float sum[64];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) sum[0][i] = sum[1][i] = 0.0f;
-
-      // one part of one block: its sums times their factors
-      auto join = [&](float (&to)[64], int acc, uint32_t fac, uint32_t parity_bit) {
-        wait_lean(bar_tfull(acc), parity_bit, abort_flag, kp.status, kp.wait_ns);
-        ptx::tc_fence_after();
-        const uint32_t taddr = tmem_lane + acc * part;
+        for (int i = 0; i < 64; ++i) sum[i] = 0.0f;
+        float a0 = __ldg(sa), w0 = __ldg(sw0), x0 = kGU ? __ldg(sw0 + to_sw1) : 0.0f;
+        for (int kb = 0; kb < nk; ++kb) {
+          const float s0 = __fmul_rn(a0, w0), s1 = kGU ? __fmul_rn(a0, x0) : 0.0f;
+          const int next = min(kb + 1, nk - 1);      // the next block's scales, on their way
+          a0 = __ldg(sa + next);
+          w0 = __ldg(sw0 + next);
+          if (kGU) x0 = __ldg(sw0 + to_sw1 + next);
+          const uint32_t at = parts + set, acc = at & 3u;
+          wait_lean(bar_tfull(acc), (at >> 2) & 1u, abort_flag, kp.status, kp.wait_ns);
+          ptx::tc_fence_after();
+          const uint32_t taddr = tmem_lane + acc * 128 + 64 * h;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c == 0 || !small) {
-            uint32_t v[32];
-            ptx::tmem_ld_32x32b_x32(taddr + 32 * c, v);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(taddr + 16 * c, v);
             ptx::tmem_ld_wait();
-            if (c == 1 || small) {     // the last of the accumulator: free it
+            if (c == 3) {                            // the warp has read all of it
               ptx::tc_fence_before();
-              if (lane == 0) ptx::mbar_arrive_remote_relaxed(tempty_leader + 8u * acc);
+              if (lane == 0) ptx::mbar_arrive_remote_relaxed_n(tempty_leader + 8u * acc, 2);
             }
+            const float sc = !kGU || 16 * c < split ? s0 : s1;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 s4 = ptx::ld_shared_v4(fac + c * 128 + i * 16);
-              float* s = to + 32 * c + 4 * i;
-              s[0] = fmaf(__uint_as_float(v[4 * i]), __uint_as_float(s4.x), s[0]);
-              s[1] = fmaf(__uint_as_float(v[4 * i + 1]), __uint_as_float(s4.y), s[1]);
-              s[2] = fmaf(__uint_as_float(v[4 * i + 2]), __uint_as_float(s4.z), s[2]);
-              s[3] = fmaf(__uint_as_float(v[4 * i + 3]), __uint_as_float(s4.w), s[3]);
+            for (int i = 0; i < 16; ++i) sum[16 * c + i] = fmaf(__uint_as_float(v[i]), sc, sum[16 * c + i]);
+          }
+          parts += 2;
+        }
+        // one decision for the sixteen warps
+        if (!ptx::bar_and(5, 32 * kEpiWarps, *abort_flag == 0)) break;
+        uint32_t pk[32];                             // the 64 results in bf16
+        int d = -1;
+        if (!kGU) {
+          float w = 1.0f;
+          if (live) {
+            d = p.row_to_pair ? __ldg(p.row_to_pair + t.r0 + j) : t.r0 + j;
+            if (d >= p.P) d = -1;
+            if (p.pair_weight && d >= 0) w = __ldg(p.pair_weight + d);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i)               // one f32 multiply, then the one bf16 rounding
+            pk[i] = gemm::pack_bf16x2(__fmul_rn(sum[2 * i], w), __fmul_rn(sum[2 * i + 1], w));
+        } else {
+          d = live ? t.r0 + j : -1;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) pk[i] = gemm::pack_bf16x2(sum[2 * i], sum[2 * i + 1]);
+        }
+        if (!kGU || p.out) {
+          // 16 columns of the warp's 32 rows at a time through its own 1 KB: two lanes store
+          // one row's 32 bytes
+          const uint32_t st = sbase + S::EPI + e * 1024;
+          const int cols = kGU ? 2 * p.N : p.N;
+          const int lim = kGU ? t.n0 + 64 * h : wr;  // the first column within its half
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t sx = (lane >> 2) & 1;
+            ptx::st_shared_v4(st + lane * 32 + (sx << 4), pk[8 * c], pk[8 * c + 1], pk[8 * c + 2], pk[8 * c + 3]);
+            ptx::st_shared_v4(st + lane * 32 + ((sx ^ 1u) << 4), pk[8 * c + 4], pk[8 * c + 5], pk[8 * c + 6], pk[8 * c + 7]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = 16 * i + (lane >> 1), k = lane & 1;
+              const uint4 val = ptx::ld_shared_v4(st + row * 32 + ((k ^ ((row >> 2) & 1)) << 4));
+              const int dr = __shfl_sync(0xffffffffu, d, row);
+              const int cc = lim + 16 * c + 8 * k;
+              if (dr >= 0 && cc < p.N)
+                *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(dr) * cols + (kGU && set == 0 ? p.N : 0) + cc) = val;
             }
+            __syncwarp();
           }
         }
-      };
-      auto pass_slot = [&](int slot) {
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar_sempty(slot));
-      };
-      if (t.n_tok > kPart) {
-        for (int kb = 0; kb < nk; kb += 2) {
-          join(sum[0], 0, fac0, full_mask & 1u);
-          join(sum[1], 1, fac0 + 512, (full_mask >> 1) & 1u);
-          pass_slot(0);
-          full_mask ^= 3u;
-          if (kb + 1 < nk) {
-            join(sum[0], 2, fac0 + S::kSlotBytes, (full_mask >> 2) & 1u);
-            join(sum[1], 3, fac0 + S::kSlotBytes + 512, (full_mask >> 3) & 1u);
-            pass_slot(1);
-            full_mask ^= 12u;
+        if (kGU) {
+          // Set 0 holds up, set 1 gate, of the same row and 64 features: set 0 goes on with the
+          // first 32 features and set 1 with the others, 16 at a time through shared memory.
+          float act[32], m = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            ptx::bar_sync(6, 32 * kEpiWarps);
+            const uint32_t mine = sbase + S::EPI + et * 16, theirs = sbase + S::EPI + (et ^ 256) * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t g4[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) g4[k] = set == 0 ? pk[16 + 8 * c + 4 * i + k] : pk[8 * c + 4 * i + k];
+              ptx::st_shared_v4(mine + i * 8192, g4[0], g4[1], g4[2], g4[3]);
+            }
+            ptx::bar_sync(6, 32 * kEpiWarps);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 o4 = ptx::ld_shared_v4(theirs + i * 8192);
+              const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t own = set == 0 ? pk[8 * c + 4 * i + k] : pk[16 + 8 * c + 4 * i + k];
+                const uint32_t gw = set == 0 ? o[k] : own, uw = set == 0 ? own : o[k];
+                const int n = 16 * c + 8 * i + 2 * k;
+                act[n] = silu_mul(__uint_as_float(gw << 16), __uint_as_float(uw << 16));
+                act[n + 1] = silu_mul(__uint_as_float(gw & 0xFFFF0000u), __uint_as_float(uw & 0xFFFF0000u));
+              }
+            }
           }
+          const int col = t.n0 + 64 * h + 32 * set;  // the first of this thread's 32 features
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (col + (i & 16) < p.N) m = fmaxf(m, fabsf(act[i]));        // N % 16 == 0
+          const uint32_t s_max = sbase + S::RMAX;    // [4 groups][128 rows]
+          ptx::st_shared_f32(s_max + (grp * 128 + f) * 4, m);
+          ptx::bar_sync(6, 32 * kEpiWarps);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = fmaxf(m, ptx::ld_shared_f32(s_max + (i * 128 + f) * 4));
+          if (live) {
+            float dd, id;
+            block_scale(m, dd, id);
+            const size_t r = static_cast<size_t>(t.r0 + j);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[k] = act[16 * i + k];
+              if (col + 16 * i < p.N) *reinterpret_cast<uint4*>(p.act + r * p.N + col + 16 * i) = codes16(x, id);
+            }
+            if (grp == 0) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = dd;
+          }
+        }
+        continue;
+      }
+      // ------------------------------------------------------------ weights tile
+      const int first = t.n0 + static_cast<int>(rank) * (kFbCols / 2);   // the CTA's first column
+      int* dst_t = reinterpret_cast<int*>(smem + S::META) + parity * kTail;               // plain
+      float* w_t = reinterpret_cast<float*>(smem + S::META + 1024) + parity * kTail;
+      if (!kGU && et < kTail) {
+        // destination rows and weights; the last readers of this half (two tiles ago) passed the
+        // previous tile's vote
+        int d = et < t.n_tok ? (p.row_to_pair ? __ldg(p.row_to_pair + t.r0 + et) : t.r0 + et) : -1;
+        if (d >= p.P) d = -1;
+        dst_t[et] = d;
+        w_t[et] = p.pair_weight && d >= 0 ? __ldg(p.pair_weight + d) : 1.0f;
+      }
+      // group grp joins the rows 32 grp .. of the tile; those without rows leave their arrivals
+      // on the accumulators' barriers to the others
+      const int n_grp = (t.n_tok + 31) >> 5;
+      float sum[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[i] = 0.0f;
+      if (grp < n_grp) {
+        const uint32_t n_arrive = n_grp == 3 ? (grp == 0 ? 2 : 1) : 4 / n_grp;
+        const int wr = kGU ? first + (f < 64 ? p.N + f : f - 64) : first + f;   // this thread's weight row
+        const float* sw_p = sw + static_cast<size_t>(min(wr / kBlk, rb - 1)) * nk;
+        const float* sa_p = p.sa + static_cast<size_t>(t.r0 + min(32 * grp + lane, t.n_tok - 1)) * nk;
+        const uint32_t fac = sbase + S::FAC + e * 256;
+        const bool wide = t.n_tok > 32 * grp + 16;
+        float a0 = __ldg(sa_p), w0 = __ldg(sw_p);
+        for (int kb = 0; kb < nk; ++kb) {
+          const float s = w0;
+          const uint32_t fk = fac + (kb & 1) * 128;
+          ptx::st_shared_f32(fk + lane * 4, a0);
+          const int next = min(kb + 1, nk - 1);      // the next block's scales, on their way
+          a0 = __ldg(sa_p + next);
+          w0 = __ldg(sw_p + next);
+          const uint32_t acc = parts & acc_mask;
+          wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, abort_flag, kp.status, kp.wait_ns);
+          ptx::tc_fence_after();
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(tmem_lane + acc * acc_cols + 32 * grp, v);
+          ptx::tmem_ld_wait();
+          ptx::tc_fence_before();
+          if (lane == 0) ptx::mbar_arrive_remote_relaxed_n(tempty_leader + 8u * acc, n_arrive);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i < 4 || wide) {
+              const uint4 a4 = ptx::ld_shared_v4(fk + 16 * i);
+              sum[4 * i] = fmaf(__uint_as_float(v[4 * i]), __fmul_rn(__uint_as_float(a4.x), s), sum[4 * i]);
+              sum[4 * i + 1] = fmaf(__uint_as_float(v[4 * i + 1]), __fmul_rn(__uint_as_float(a4.y), s), sum[4 * i + 1]);
+              sum[4 * i + 2] = fmaf(__uint_as_float(v[4 * i + 2]), __fmul_rn(__uint_as_float(a4.z), s), sum[4 * i + 2]);
+              sum[4 * i + 3] = fmaf(__uint_as_float(v[4 * i + 3]), __fmul_rn(__uint_as_float(a4.w), s), sum[4 * i + 3]);
+            }
+          }
+          ++parts;
         }
       } else {
-        for (int kb = 0; kb < nk; ++kb) {
-          const int acc = acc_of(kb, 0, 1, small);
-          join(sum[0], acc, fac0 + (kb & 1) * S::kSlotBytes, (full_mask >> acc) & 1u);
-          full_mask ^= 1u << acc;
-          pass_slot(kb & 1);
-        }
+        parts += nk;
       }
-      // one decision for the eight warps; the barrier also publishes dst_t / w_t
-      if (!ptx::bar_and(3, 256, *abort_flag == 0)) break;
-      // 32 rows of the group at a time through its staging buffer
-      const int tok = et >> 2, quad = et & 3;    // gate/up: row of the 32, 16 features of it
-      const int col = first + 16 * quad;
+      // one decision for the sixteen warps; the barrier also publishes dst_t / w_t
+      if (!ptx::bar_and(5, 32 * kEpiWarps, *abort_flag == 0)) break;
+      // 16 rows of the group at a time through its 4 KB of staging: [16 rows][128 features] bf16,
+      // 16-byte pieces XOR-swizzled by the row
+      const uint32_t ost = sbase + S::EPI + grp * 4096;
+      const uint32_t place = ost + ((f >> 3) << 4) + (f & 7) * 2;
+      const int tok = gt >> 3, oct = gt & 7;     // gate/up: row of the 16, 8 features of it
+      const int col = first + 8 * oct;
       const bool in = col < p.N;                 // N % 16 == 0
-      const uint32_t s_max = sbase + S::META + (parity * 2 + h) * 1024 + tok * 4;   // [2][2 groups][2 CTAs][128]
-      float act[4][16];
+      const uint32_t s_max = sbase + S::META + (parity * 4 + grp) * 256 + tok * 4;   // [2][4 groups][2 CTAs][32]
+      float act[2][8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int j0 = (c >> 1) * kPart + h * width + (c & 1) * 32;
-        if (j0 >= t.n_tok || (small && c > 0)) continue;   // the same for the whole group
+      for (int c = 0; c < 2; ++c) {
+        const int j0 = 32 * grp + 16 * c;
+        if (j0 >= t.n_tok) continue;             // the same for the whole group
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           float x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = sum[c >> 1][32 * (c & 1) + 4 * i + k];
+          for (int k = 0; k < 4; ++k) x[k] = sum[16 * c + 4 * i + k];
           if (!kGU && p.pair_weight) {           // one f32 multiply, then the one bf16 rounding
             const uint4 w4 = ptx::ld_shared_v4(ptx::smem_u32(w_t) + 4 * j0 + 16 * i);
             x[0] = __fmul_rn(x[0], __uint_as_float(w4.x));
@@ -523,79 +608,78 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
 #pragma unroll
           for (int k = 0; k < 2; ++k) {          // gate/up: narrowed before the activation
             const uint32_t pk = gemm::pack_bf16x2(x[2 * k], x[2 * k + 1]);
-            const int j = 4 * i + 2 * k;
-            ptx::st_shared_u16((place ^ ((j & 15) << 4)) + j * 256, static_cast<uint16_t>(pk));
-            ptx::st_shared_u16((place ^ (((j + 1) & 15) << 4)) + (j + 1) * 256,
-                               static_cast<uint16_t>(pk >> 16));
+            const int jj = 4 * i + 2 * k;
+            ptx::st_shared_u16((place ^ (jj << 4)) + jj * 256, static_cast<uint16_t>(pk));
+            ptx::st_shared_u16((place ^ ((jj + 1) << 4)) + (jj + 1) * 256, static_cast<uint16_t>(pk >> 16));
           }
         }
-        ptx::bar_sync(1 + h, 128);
+        ptx::bar_sync(1 + grp, 128);
         if (!kGU) {
           // sixteen threads store one row's 256 bytes
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int idx = et + 128 * i;
-            const int j = idx >> 4, k = idx & 15;
+          for (int i = 0; i < 2; ++i) {
+            const int idx = gt + 128 * i;
+            const int jj = idx >> 4, k = idx & 15;
             const int cc = first + 8 * k;
-            if (j0 + j < t.n_tok && cc < p.N) {
-              const int d = dst_t[j0 + j];
-              const uint4 val = ptx::ld_shared_v4(ost + j * 256 + ((k ^ (j & 15)) << 4));
+            if (j0 + jj < t.n_tok && cc < p.N) {
+              const int d = dst_t[j0 + jj];
+              const uint4 val = ptx::ld_shared_v4(ost + jj * 256 + ((k ^ jj) << 4));
               if (d >= 0) *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(d) * p.N + cc) = val;
             }
           }
         } else {
           const uint32_t row = ost + tok * 256;
-          const uint4 u0 = ptx::ld_shared_v4(row + (((2 * quad) ^ (tok & 15)) << 4));
-          const uint4 u1 = ptx::ld_shared_v4(row + (((2 * quad + 1) ^ (tok & 15)) << 4));
-          const uint4 g0 = ptx::ld_shared_v4(row + (((2 * quad + 8) ^ (tok & 15)) << 4));
-          const uint4 g1 = ptx::ld_shared_v4(row + (((2 * quad + 9) ^ (tok & 15)) << 4));
+          const uint4 u4 = ptx::ld_shared_v4(row + ((oct ^ tok) << 4));
+          const uint4 g4 = ptx::ld_shared_v4(row + (((oct + 8) ^ tok) << 4));
           if (p.out && in && j0 + tok < t.n_tok) {
             uint16_t* o = p.out + static_cast<size_t>(t.r0 + j0 + tok) * 2 * p.N + col;
-            reinterpret_cast<uint4*>(o)[0] = g0;
-            reinterpret_cast<uint4*>(o)[1] = g1;
-            reinterpret_cast<uint4*>(o + p.N)[0] = u0;
-            reinterpret_cast<uint4*>(o + p.N)[1] = u1;
+            *reinterpret_cast<uint4*>(o) = g4;
+            *reinterpret_cast<uint4*>(o + p.N) = u4;
           }
-          float g[16], u[16], m = 0.0f;
-          widen16(g0, g1, g);
-          widen16(u0, u1, u);
+          float g[8], u[8], m = 0.0f;
+          widen8(g4, g);
+          widen8(u4, u);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            // SiLU is tolerance-checked: the fast exponential and division serve
-            act[c][i] = __fdividef(g[i], 1.0f + __expf(-g[i])) * u[i];
+          for (int i = 0; i < 8; ++i) {
+            act[c][i] = silu_mul(g[i], u[i]);
             m = fmaxf(m, fabsf(act[c][i]));
           }
           if (!in) m = 0.0f;
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          if (quad == 0) {
-            const uint32_t at = s_max + rank * 512 + c * 128;
-            ptx::st_shared_f32(at, m);
-            ptx::st_cluster_f32(ptx::mapa_shared(at, rank ^ 1u), m);
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (oct == 0) {
+            const uint32_t mx = s_max + rank * 128 + c * 64;
+            ptx::st_shared_f32(mx, m);
+            ptx::st_cluster_f32(ptx::mapa_shared(mx, rank ^ 1u), m);
           }
         }
-        ptx::bar_sync(1 + h, 128);
+        ptx::bar_sync(1 + grp, 128);
       }
       if (kGU) {
         __syncwarp();
         if (lane == 0) {
-          ptx::mbar_arrive_remote(ptx::mapa_shared(bar_max(h), rank));
-          ptx::mbar_arrive_remote(ptx::mapa_shared(bar_max(h), rank ^ 1u));
+          ptx::mbar_arrive_remote(ptx::mapa_shared(bar_max(grp), rank));
+          ptx::mbar_arrive_remote(ptx::mapa_shared(bar_max(grp), rank ^ 1u));
         }
         // a warp that gives up here stops at the next tile's vote: the named barriers stay matched
-        const bool ok = wait_bar<true>(bar_max(h), tphase, abort_flag, kp.status, kp.wait_ns);
+        const bool ok = wait_bar<true>(bar_max(grp), tphase, abort_flag, kp.status, kp.wait_ns);
         tphase ^= 1u;
         if (ok) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int j = (c >> 1) * kPart + h * width + (c & 1) * 32 + tok;
-            if (j >= t.n_tok || (small && c > 0)) continue;
-            const float m = fmaxf(ptx::ld_shared_f32(s_max + c * 128), ptx::ld_shared_f32(s_max + 512 + c * 128));
+          for (int c = 0; c < 2; ++c) {
+            const int jj = 32 * grp + 16 * c + tok;
+            if (jj >= t.n_tok) continue;
+            const float m = fmaxf(ptx::ld_shared_f32(s_max + c * 64), ptx::ld_shared_f32(s_max + 128 + c * 64));
             float d, id;
             block_scale(m, d, id);
-            const size_t r = static_cast<size_t>(t.r0 + j);
-            if (in) *reinterpret_cast<uint4*>(p.act + r * p.N + col) = codes16(act[c], id);
-            if (quad == 0 && leader) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = d;
+            const size_t r = static_cast<size_t>(t.r0 + jj);
+            if (in)
+              *reinterpret_cast<uint2*>(p.act + r * p.N + col) = make_uint2(
+                  codes4(__fmul_rn(act[c][0], id), __fmul_rn(act[c][1], id), __fmul_rn(act[c][2], id),
+                         __fmul_rn(act[c][3], id)),
+                  codes4(__fmul_rn(act[c][4], id), __fmul_rn(act[c][5], id), __fmul_rn(act[c][6], id),
+                         __fmul_rn(act[c][7], id)));
+            if (oct == 0 && leader) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = d;
           }
         }
       }
@@ -609,7 +693,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       *abort_flag != 0 ||
       ld_cluster_u32(ptx::mapa_shared(sbase + S::MISC + 4, rank ^ 1u)) != 0;
   if (gave_up) {
-    if (warp == 1 && lane == 0 && leader && mma_any) {
+    if (warp == 1 && leader && mma_any) {   // the issuing thread
       ptx::mma_commit_pair(bar_drain, 1);
       gemm::spin_bounded(bar_drain, 0);
     }
@@ -628,10 +712,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
 }
 
 template <bool kGU>
-int launch_range(const char* op, const CUtensorMap (&tt)[3], const CUtensorMap& tw, KernelParams kp,
+int launch_range(const char* op, const CUtensorMap (&tt)[4], const CUtensorMap& tw, KernelParams kp,
                  cudaStream_t stream) {
-  auto kern = fp8_pair_kernel<kGU>;
-  const int smem = Smem<kGU>::ALLOC;
+  auto kern = fp8_gemm_kernel<kGU>;
+  const int smem = Smem::ALLOC;
   static std::atomic<int> pairs_dev[64] = {};   // resident clusters, once the kernel is configured
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -671,7 +755,7 @@ int launch_range(const char* op, const CUtensorMap (&tt)[3], const CUtensorMap& 
   if (pairs > max_pairs) pairs = max_pairs;
   return launch_status(launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1),
                                      dim3(kThreads, 1, 1), smem, stream, attr, 1, tt[0], tt[1],
-                                     tt[2], tw, kp),
+                                     tt[2], tt[3], tw, kp),
                        op);
 }
 
@@ -680,11 +764,11 @@ int launch_range(const char* op, const CUtensorMap (&tt)[3], const CUtensorMap& 
 int launch_product(const char* op, const GemmParams& p0, bool gateup, cudaStream_t stream) {
   GemmParams p = p0;
   const int rows = gateup ? 2 * p.N : p.N;
-  CUtensorMap tt[3], tw;
+  CUtensorMap tt[4], tw;
   int rc;
   // pairs of codes as 2-byte elements (K is a multiple of 16): the same bytes and the same
   // 128-byte swizzle as a bf16 operand's box
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < 4; ++i)
     if ((rc = gemm::make_tmap(&tt[i], p.a, p.P, p.K / 2, 16 << i, op, "a_codes")) != MOE_OK) return rc;
   if ((rc = gemm::make_tmap(&tw, p.w, static_cast<long long>(p.G) * rows, p.K / 2, gateup ? 64 : 128,
                             op, "weights")) != MOE_OK)

@@ -172,6 +172,12 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr
                : "memory");
 }
 
+// the same, counting for n arrivals
+__device__ __forceinline__ void mbar_arrive_remote_relaxed_n(uint32_t cluster_addr, uint32_t n) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(n)
+               : "memory");
+}
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
