@@ -51,19 +51,25 @@ namespace {
 using gemm::wait_bar;
 using gemm::wait_bar_spin;
 
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // Bounded wait (see gemm::wait_bar) for the loops that run once per scale block and
 // warp, where every instruction counts: the probe without a time hint (the one with a
 // hint is a software loop around it), and no result.  A wait that gives up raises the
 // status and the CTA's abort flag; its warp goes on with what is there, its later waits
 // end at once, and it stops at the tile's vote.
-__device__ __forceinline__ void wait_lean(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+__device__ __forceinline__ void wait_lean(uint32_t bar, uint32_t parity, uint32_t abort_flag,
                                           unsigned int* status, unsigned long long limit_ns) {
   if (!ptx::mbar_try_wait(bar, parity)) {
     const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(bar, parity) && !*abort_flag) {
+    while (!ptx::mbar_try_wait(bar, parity) && ld_shared_u32(abort_flag) == 0) {
       if (ptx::globaltimer_ns() - t0 > limit_ns) {
         if (status) atomicOr(status, static_cast<unsigned int>(MOE_STATUS_TIMEOUT));
-        *abort_flag = 1;
+        asm volatile("st.shared.u32 [%0], 1;" ::"r"(abort_flag) : "memory");
       }
     }
   }
@@ -117,27 +123,33 @@ struct Tile {
 
 // rows tiles first, then weights tiles; each kind by group, block of rows, columns
 struct Schedule {
-  const int* rows_start;         // [G + 1] first rows tile of a group
-  const int* tail_start;         // [G + 1] first weights tile of a group, counted from n_rows
-  const int* goff;
-  int G, n_fb, n_rows, total;
-  int fb_cols;
+  // [G + 1] words each in shared memory: first rows tile of a group; first weights tile,
+  // counted from the number of rows tiles; group offsets.  32-bit addresses: the epilogue
+  // warps have no registers to spare.
+  uint32_t base;
+  int G, N, fb_cols;
+  __device__ __forceinline__ int word(uint32_t at, int i) const { return ld_shared_u32(base + at + 4 * i); }
+  __device__ __forceinline__ int total() const { return word(Smem::ROWS_START, G) + word(Smem::TAIL_START, G); }
   __device__ __forceinline__ Tile at(int tile) const {
+    // opaque: what it works out for a tile is not kept in registers across the tile's loop
+    asm volatile("" : "+r"(tile));
+    const int n_fb = (N + fb_cols - 1) / fb_cols;
+    const int n_rows = word(Smem::ROWS_START, G);
     const bool tail = tile >= n_rows;
-    const int* start = tail ? tail_start : rows_start;
+    const uint32_t start = tail ? Smem::TAIL_START : Smem::ROWS_START;
     if (tail) tile -= n_rows;
     int lo = 0, hi = G;  // start[lo] <= tile < start[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (start[mid] <= tile) lo = mid; else hi = mid;
+      if (word(start, mid) <= tile) lo = mid; else hi = mid;
     }
-    const int local = tile - start[lo];
-    const int rows = goff[lo + 1] - goff[lo];
-    const int m = tail ? (rows - 1) / kTokBlock : local / n_fb;
+    const int local = tile - word(start, lo);
+    const int r0 = word(Smem::GOFF, lo), r1 = word(Smem::GOFF, lo + 1);
+    const int m = tail ? (r1 - r0 - 1) / kTokBlock : local / n_fb;
     Tile t;
     t.g = lo;
-    t.r0 = goff[lo] + m * kTokBlock;
-    t.n_tok = min(goff[lo + 1], t.r0 + kTokBlock) - t.r0;
+    t.r0 = r0 + m * kTokBlock;
+    t.n_tok = min(r1, t.r0 + kTokBlock) - t.r0;
     t.n0 = (tail ? local : local - m * n_fb) * fb_cols;
     return t;
   }
@@ -256,15 +268,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   if (lane == 31) scan_tmp[warp] = make_int2(incl_b, incl_t);
   const bool small = __syncthreads_or(rows_max > 64) == 0;   // eight accumulators of 64 columns
   int run_b = incl_b - n_big, run_t = incl_t - n_tail;
-  Schedule sch{rows_start, tail_start, goff, G, n_fb, 0, 0, kFbCols};
+  int all_b = 0, all_t = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     const int2 v = scan_tmp[w];
     if (w < warp) {
       run_b += v.x;
       run_t += v.y;
     }
-    sch.n_rows += v.x;
-    sch.total += v.x + v.y;
+    all_b += v.x;
+    all_t += v.y;
   }
   for (int g = g_lo; g < g_hi; ++g) {
     const int rows = goff[g + 1] - goff[g];
@@ -274,15 +286,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     run_t += tail_blocks(rows) * n_fb;
   }
   if (threadIdx.x == 0) {
-    rows_start[G] = sch.n_rows;
-    tail_start[G] = sch.total - sch.n_rows;
+    rows_start[G] = all_b;
+    tail_start[G] = all_t;
   }
+  const Schedule sch{sbase, G, p.N, kFbCols};
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // the peer's barriers exist before any remote arrive or copy
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int nk = blocks_of(p.K);
+  const int total = sch.total();
   const int acc_shift = small ? 3 : 2;             // log2 of the accumulators in the ring
   const uint32_t acc_mask = (1u << acc_shift) - 1u;
   const uint32_t acc_cols = 512u >> acc_shift;
@@ -298,7 +312,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = unit; ok && tile < sch.total; tile += n_units) {
+      for (int tile = unit; ok && tile < total; tile += n_units) {
         const Tile t = sch.at(tile);
         const int half = t.n_tok > kTail ? 128 : ((t.n_tok + 15) & ~15) >> 1;
         const int tbox = half <= 16 ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
@@ -334,7 +348,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         int stage = 0;
         uint32_t phase = 0, parts = 0;     // parts: accumulators taken from the ring so far
         bool ok = true;
-        for (int tile = unit; ok && tile < sch.total; tile += n_units) {
+        for (int tile = unit; ok && tile < total; tile += n_units) {
           const Tile t = sch.at(tile);
           const bool big = t.n_tok > kTail;
           const uint32_t idesc = ptx::idesc_e4m3_f32(256, big ? 128 : (t.n_tok + 15) & ~15);
@@ -378,26 +392,29 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     const uint32_t tmem_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t tempty_leader = ptx::mapa_shared(bar_tempty(0), 0);
     const int rb = blocks_of(kp.rows_per_group);
-    uint32_t parts = 0, tphase = 0;
-    int parity = 0;                                  // of the tile: META's half
-    for (int tile = unit; tile < sch.total; tile += n_units, parity ^= 1) {
-      const Tile t = sch.at(tile);
-      const float* sw = p.sw + static_cast<size_t>(t.g) * rb * nk;
-      if (t.n_tok > kTail) {
+    uint32_t parts = 0;        // accumulators passed so far
+    uint32_t n_tails = 0;      // weights tiles so far: META's half, the maxima's phase
+    for (int tile = unit; tile < total; tile += n_units) {
+      if (tile < sch.word(S::ROWS_START, G)) {
         // ---------------------------------------------------------- rows tile
-        const int j = static_cast<int>(rank) * 128 + f;        // this thread's row of the tile
-        const bool live = j < t.n_tok;
-        const float* sa = p.sa + static_cast<size_t>(t.r0 + (live ? j : 0)) * nk;
-        // the weight rows behind this thread's 64 columns: one scale block, or (up rows of
-        // I not a multiple of 128) two that meet at a multiple of 16
-        const int wr = kGU ? t.n0 + 64 * h + (set == 0 ? p.N : 0) : t.n0 + 128 * h + 64 * set;
-        const int wb = min(wr / kBlk, rb - 1);
-        const float* sw0 = sw + static_cast<size_t>(wb) * nk;
-        const int split = kGU && set == 0 ? (wb + 1) * kBlk - wr : 64;     // columns of the first block
-        const size_t to_sw1 = kGU && split < 64 && wb + 1 < rb ? nk : 0;
         float sum[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) sum[i] = 0.0f;
+        const float *sa, *sw0;
+        int split;
+        uint32_t to_sw1;
+        {
+          const Tile t = sch.at(tile);
+          const int j = static_cast<int>(rank) * 128 + f;      // this thread's row of the tile
+          sa = p.sa + static_cast<size_t>(t.r0 + (j < t.n_tok ? j : 0)) * nk;
+          // the weight rows behind this thread's 64 columns: one scale block, or (up rows of
+          // I not a multiple of 128) two that meet at a multiple of 16
+          const int wr = kGU ? t.n0 + 64 * h + (set == 0 ? p.N : 0) : t.n0 + 128 * h + 64 * set;
+          const int wb = min(wr / kBlk, rb - 1);
+          sw0 = p.sw + (static_cast<size_t>(t.g) * rb + wb) * nk;
+          split = kGU && set == 0 ? (wb + 1) * kBlk - wr : 64;           // columns of the first block
+          to_sw1 = kGU && split < 64 && wb + 1 < rb ? nk : 0;
+        }
         float a0 = __ldg(sa), w0 = __ldg(sw0), x0 = kGU ? __ldg(sw0 + to_sw1) : 0.0f;
         for (int kb = 0; kb < nk; ++kb) {
           const float s0 = __fmul_rn(a0, w0), s1 = kGU ? __fmul_rn(a0, x0) : 0.0f;
@@ -406,7 +423,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           w0 = __ldg(sw0 + next);
           if (kGU) x0 = __ldg(sw0 + to_sw1 + next);
           const uint32_t at = parts + set, acc = at & 3u;
-          wait_lean(bar_tfull(acc), (at >> 2) & 1u, abort_flag, kp.status, kp.wait_ns);
+          wait_lean(bar_tfull(acc), (at >> 2) & 1u, sbase + S::MISC + 4, kp.status, kp.wait_ns);
           ptx::tc_fence_after();
           const uint32_t taddr = tmem_lane + acc * 128 + 64 * h;
 #pragma unroll
@@ -425,7 +442,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           parts += 2;
         }
         // one decision for the sixteen warps
-        if (!ptx::bar_and(5, 32 * kEpiWarps, *abort_flag == 0)) break;
+        if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + 4) == 0)) break;
+        const Tile t = sch.at(tile);                 // anew
+        const int j = static_cast<int>(rank) * 128 + f;
+        const bool live = j < t.n_tok;
         uint32_t pk[32];                             // the 64 results in bf16
         int d = -1;
         if (!kGU) {
@@ -448,7 +468,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           // one row's 32 bytes
           const uint32_t st = sbase + S::EPI + e * 1024;
           const int cols = kGU ? 2 * p.N : p.N;
-          const int lim = kGU ? t.n0 + 64 * h : wr;  // the first column within its half
+          const int lim = kGU ? t.n0 + 64 * h : t.n0 + 128 * h + 64 * set;   // the first column within its half
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t sx = (lane >> 2) & 1;
@@ -523,6 +543,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         continue;
       }
       // ------------------------------------------------------------ weights tile
+      const Tile t = sch.at(tile);
+      const int parity = n_tails++ & 1;
+      const float* sw = p.sw + static_cast<size_t>(t.g) * rb * nk;
       const int first = t.n0 + static_cast<int>(rank) * (kFbCols / 2);   // the CTA's first column
       int* dst_t = reinterpret_cast<int*>(smem + S::META) + parity * kTail;               // plain
       float* w_t = reinterpret_cast<float*>(smem + S::META + 1024) + parity * kTail;
@@ -556,7 +579,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           a0 = __ldg(sa_p + next);
           w0 = __ldg(sw_p + next);
           const uint32_t acc = parts & acc_mask;
-          wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, abort_flag, kp.status, kp.wait_ns);
+          wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, sbase + S::MISC + 4, kp.status, kp.wait_ns);
           ptx::tc_fence_after();
           uint32_t v[32];
           ptx::tmem_ld_32x32b_x32(tmem_lane + acc * acc_cols + 32 * grp, v);
@@ -579,7 +602,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         parts += nk;
       }
       // one decision for the sixteen warps; the barrier also publishes dst_t / w_t
-      if (!ptx::bar_and(5, 32 * kEpiWarps, *abort_flag == 0)) break;
+      if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + 4) == 0)) break;
       // 16 rows of the group at a time through its 4 KB of staging: [16 rows][128 features] bf16,
       // 16-byte pieces XOR-swizzled by the row
       const uint32_t ost = sbase + S::EPI + grp * 4096;
@@ -662,8 +685,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           ptx::mbar_arrive_remote(ptx::mapa_shared(bar_max(grp), rank ^ 1u));
         }
         // a warp that gives up here stops at the next tile's vote: the named barriers stay matched
-        const bool ok = wait_bar<true>(bar_max(grp), tphase, abort_flag, kp.status, kp.wait_ns);
-        tphase ^= 1u;
+        const bool ok = wait_bar<true>(bar_max(grp), parity, abort_flag, kp.status, kp.wait_ns);
         if (ok) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
