@@ -24,7 +24,7 @@
 // weights tiles pad to 16 rows, which is what ragged and decode-sized groups need.
 //
 //   warp 0      TMA producer: the CTA's weight rows and token rows of each stage
-//   warp 1      tensor memory; in the even CTA the one thread that issues MMAs
+//   warps 1-2   tensor memory (1); in the even CTA the two threads that issue MMAs
 //   warps 4-19  block joins and the epilogue
 //
 // gate/up: a CTA's 128 weight rows are 64 up rows, then the 64 gate rows of the
@@ -77,7 +77,7 @@ __device__ __forceinline__ void wait_lean(uint32_t bar, uint32_t parity, uint32_
 }
 
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of other roles (two of its warps idle)
+constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of other roles (one of its warps idle)
 constexpr int kAuxRegs = 64, kEpiRegs = 104;
 // the split draws on the registers the block was launched with (96 a thread)
 static_assert(128 * kAuxRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 96, "register split");
@@ -99,8 +99,8 @@ struct Smem {
   static constexpr int RMAX = META + 2048;                      // rows tiles: row maxima (the peer may already
                                                                 // write those of a later weights tile)
   static constexpr int BARS = RMAX + 2048;
-  // full, empty [kStages], tfull, tempty [kMaxAcc], drain, maxima [4]
-  static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + 5;
+  // full, empty [kStages], tfull, tempty [kMaxAcc], drain [2], maxima [4]
+  static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + 6;
   static constexpr int MISC = BARS + NBARS * 8;                 // tmem slot, abort flag, scan
   static constexpr int ROWS_START = (MISC + 8 + 8 * (kThreads / 32) + 15) & ~15;
   static constexpr int TAIL_START = ROWS_START + (kMaxGroupsLaunch + 1) * 4;
@@ -206,22 +206,22 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   auto bar_empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto bar_tfull = [&](int a) { return bars + 8u * (2 * kStages + a); };
   auto bar_tempty = [&](int a) { return bars + 8u * (2 * kStages + kMaxAcc + a); };
-  const uint32_t bar_drain = bars + 8u * (2 * kStages + 2 * kMaxAcc);
-  auto bar_max = [&](int c) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + 1 + c); };
+  auto bar_drain = [&](int i) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + i); };
+  auto bar_max = [&](int c) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + 2 + c); };
 
   count_launch(kp.launches, p.kid);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(bar_full(s), 1);    // the even CTA's expect-tx arrive
-      ptx::mbar_init(bar_empty(s), 1);   // the pair's MMA commit
+      ptx::mbar_init(bar_empty(s), 2);   // two commits of the pair's MMA issuers
     }
     for (int a = 0; a < kMaxAcc; ++a) {
       ptx::mbar_init(bar_tfull(a), 1);    // the pair's MMA commit
       ptx::mbar_init(bar_tempty(a), 32);  // sixteen from the warps of either CTA that read it
     }
     for (int c = 0; c < 4; ++c) ptx::mbar_init(bar_max(c), 8);  // a group's four warps in both CTAs
-    ptx::mbar_init(bar_drain, 1);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(bar_drain(i), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -342,9 +342,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer (even CTA)
+    } else if (warp < 3) {
+      // ------------------------------------------------------------ MMA issuers (even CTA)
+      // One thread takes about 400 cycles a part for its waits, MMAs and commits, which is
+      // more than the MMAs run, so two take turns: the two parts of a rows tile's block,
+      // or the even and the odd blocks of a weights tile.
       if (leader && ptx::elect_one()) {
+        const int me = warp - 1;
         int stage = 0;
         uint32_t phase = 0, parts = 0;     // parts: accumulators taken from the ring so far
         bool ok = true;
@@ -353,27 +357,29 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           const bool big = t.n_tok > kTail;
           const uint32_t idesc = ptx::idesc_e4m3_f32(256, big ? 128 : (t.n_tok + 15) & ~15);
           for (int kb = 0; ok && kb < nk; ++kb) {
-            ok = wait_bar(bar_full(stage), phase, abort_flag, kp.status, kp.wait_ns);
-            const uint64_t dw = ptx::desc_kmajor_sw128(sbase + S::W + stage * kStageBytes);
-            const uint64_t dt = ptx::desc_kmajor_sw128(sbase + S::T + stage * kStageBytes);
-            for (int r = 0; ok && r < (big ? 2 : 1); ++r, ++parts) {
-              const uint32_t acc = parts & acc_mask;
-              ok = wait_bar<true>(bar_tempty(acc), ((parts >> acc_shift) & 1u) ^ 1u, abort_flag,
-                                  kp.status, kp.wait_ns);
+            if (big || (kb & 1) == me) {
+              const uint32_t at = big ? parts + me : parts, acc = at & acc_mask;
+              // the accumulator's release orders tensor memory only (see the arrives)
+              ok = wait_bar(bar_tempty(acc), ((at >> acc_shift) & 1u) ^ 1u, abort_flag, kp.status,
+                            kp.wait_ns) &&
+                   wait_bar(bar_full(stage), phase, abort_flag, kp.status, kp.wait_ns);
               if (!ok) break;
               ptx::tc_fence_after();
+              const uint64_t dw = ptx::desc_kmajor_sw128(sbase + S::W + stage * kStageBytes);
+              const uint64_t dt = ptx::desc_kmajor_sw128(sbase + S::T + stage * kStageBytes);
               const uint32_t d = tmem_base + acc * acc_cols;
               // rows tiles: tokens on M, 64 weight rows of each CTA on N
               const uint64_t da = big ? dt : dw;
-              const uint64_t db = big ? dw + static_cast<uint64_t>(r * (64 * 128 / 16)) : dt;
-  #pragma unroll
+              const uint64_t db = big ? dw + static_cast<uint64_t>(me * (64 * 128 / 16)) : dt;
+#pragma unroll
               for (int k = 0; k < kBlk / kMmaK; ++k)   // a fresh sum per scale block
                 ptx::mma_e4m3_pair(d, da + 2ull * k, db + 2ull * k, idesc, k != 0 ? 1u : 0u);
               mma_any = true;
               ptx::mma_commit_pair(bar_tfull(acc), 3);     // the part's sums are ready in both
+              ptx::mma_commit_pair(bar_empty(stage), 3);   // frees the stage in both CTAs (with
+              if (!big) ptx::mma_commit_pair(bar_empty(stage), 3);   // the other part's, or alone)
             }
-            if (!ok) break;
-            ptx::mma_commit_pair(bar_empty(stage), 3);     // frees the stage in both CTAs
+            parts += big ? 2 : 1;
             if (++stage == kStages) { stage = 0; phase ^= 1u; }
           }
         }
@@ -715,9 +721,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       *abort_flag != 0 ||
       ld_cluster_u32(ptx::mapa_shared(sbase + S::MISC + 4, rank ^ 1u)) != 0;
   if (gave_up) {
-    if (warp == 1 && leader && mma_any) {   // the issuing thread
-      ptx::mma_commit_pair(bar_drain, 1);
-      gemm::spin_bounded(bar_drain, 0);
+    if (mma_any) {   // the issuing threads
+      ptx::mma_commit_pair(bar_drain(warp - 1), 1);
+      gemm::spin_bounded(bar_drain(warp - 1), 0);
     }
     if (warp == 0 && lane == 0) {
       const uint64_t t0 = ptx::globaltimer_ns();
