@@ -1,45 +1,46 @@
 // moe_fp8_gemm.cu -- the grouped products of E4M3 activations and E4M3 weights
-// (moe_grouped_gemm_fp8, moe_grouped_gemm_gateup_silu_fp8) on CTA pairs.
+// (moe_grouped_gemm_fp8, moe_grouped_gemm_gateup_silu_fp8).
 //
 // y[r,n] = sum_b (sa[r,b] sw[n,b]) p_b[r,n], p_b the product over the 128
 // columns of scale block b.  The scales change with every block of the
 // contraction, so the tensor core sums one block at a time: each block's MMAs
-// start a fresh accumulator in tensor memory, and sixteen epilogue warps per CTA
-// join the blocks in registers, acc += p_b * s_b, while the tensor core fills the
-// next accumulators.  The round trip MMA -> join -> MMA crosses the pair and takes
-// about as long as two blocks' MMAs, so the accumulators are a ring of four (or
-// eight half as wide in launches without larger groups).
+// start a fresh accumulator in tensor memory, and sixteen epilogue warps join the
+// blocks in registers, acc += p_b * s_b, while the tensor core fills the next
+// accumulators.
 //
-// Every MMA is a tcgen05.mma.cta_group::2 over the two SMs of a cluster, M = 256
-// (128 per SM); a stage of the operand ring holds, per CTA, 128 weight rows and at
-// most 128 token rows of one scale block (128 bytes a row).  Two kinds of tile:
-//   rows tiles     (blocks of more than 128 rows of a group): 256 token rows on M,
-//                  256 weight rows on N in two parts of 128.  A thread owns one
-//                  token row and 64 columns of one part, so the factor s_b is one
+// A tile has 256 weight rows (256 output columns, or 128 features' up and gate
+// rows) in two parts of 128, each with its MMAs, its issuing thread and its half of
+// the epilogue warps.  Two kinds of tile:
+//   rows tiles     (blocks of more than 64 rows of a group): 128 token rows on the
+//                  MMA's M side, a part's 128 weight rows on N.  A thread owns one
+//                  token row and 64 of the columns, so the factor s_b is one
 //                  register: one fused multiply-add per product and block.
-//   weights tiles  (blocks of up to 128 rows): 256 weight rows on M, the rows on N,
-//                  padded to 16.  A thread owns one weight row and 32 of the token
-//                  rows, whose scales its warp keeps in shared memory.
-// Rows tiles need no transpose and no scale loads per product, and pad to 256 rows;
+//   weights tiles  (blocks of up to 64 rows): a part's 128 weight rows on M, the
+//                  token rows on N, padded to 16.  A thread owns one weight row and
+//                  32 of the token rows, whose scales its warp keeps in shared memory.
+// Rows tiles need no transpose and no scale loads per product, and pad to 128 rows;
 // weights tiles pad to 16 rows, which is what ragged and decode-sized groups need.
+// Every block makes the round trip MMA -> join -> MMA, so its latency counts more
+// than the bytes that a CTA pair would save: on pairs (256 x 256 tiles, 32 instead
+// of 48 KB a stage and SM) the barriers of the trip cross the SMs, it takes about
+// 1700 cycles against 512 of MMA work, and an 8192 x 4096 x 2048 product 75 us.
 //
-//   warp 0      TMA producer: the CTA's weight rows and token rows of each stage
-//   warps 1-2   tensor memory (1); in the even CTA the two threads that issue MMAs
-//   warps 4-19  block joins and the epilogue
+//   warp 0      TMA producer: 256 weight rows and up to 128 token rows of one scale
+//               block (128 bytes a row) per stage
+//   warps 1-2   tensor memory (1); the two threads that issue MMAs, one per part
+//   warps 4-19  block joins and the epilogue; part 0 the first eight, part 1 the others
 //
-// gate/up: a CTA's 128 weight rows are 64 up rows, then the 64 gate rows of the
-// same features.  Gate and up are narrowed to bf16, silu(gate) * up is formed in
-// f32 and a row's 128 features are quantised with one scale.
-//   rows tiles: part 0 is the up half and part 1 the gate half of the same 128
-//     features, so two threads of a CTA hold a row's up and gate of 64 features;
-//     each takes 32 of them, through shared memory.  The row's largest magnitude
-//     is that of four threads.
-//   weights tiles: the bf16 results are transposed through shared memory; a row's
-//     128 features span both CTAs, which exchange their maxima through distributed
-//     shared memory and one cluster-scope barrier per tile.
+// gate/up: part 0 holds the up rows and part 1 the gate rows of the same 128
+// features.  Gate and up are narrowed to bf16, silu(gate) * up is formed in f32 and
+// a row's 128 features are quantised with one scale.
+//   rows tiles: two threads hold a row's up and gate of 64 features; each takes 32
+//     of them, through shared memory.  The row's largest magnitude is that of four
+//     threads.
+//   weights tiles: the bf16 results are transposed through shared memory, and
+//     sixteen threads form a row's 128 activations.
 //
-// The tile schedule, the bounded waits and the exit of a CTA that gives up are
-// those of moe_gemm_pair.cu.
+// The tile schedule and the bounded waits are those of moe_gemm.cu; a CTA that gives
+// up drains its MMAs and copies before it frees tensor memory.
 #include <atomic>
 
 #include "fp8_common.cuh"
@@ -81,26 +82,24 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of other roles (
 constexpr int kAuxRegs = 64, kEpiRegs = 104;
 // the split draws on the registers the block was launched with (96 a thread)
 static_assert(128 * kAuxRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 96, "register split");
-constexpr int kTokBlock = 256;              // rows per rows tile
-constexpr int kTail = 128;                  // rows of a weights tile at most
-constexpr int kStages = 6;
-constexpr int kStageBytes = 128 * 128;      // one operand's stage per CTA, at most
+constexpr int kTokBlock = 128;              // rows per rows tile
+constexpr int kTail = 64;                   // rows of a weights tile at most
+constexpr int kStages = 4;
+constexpr int kWBytes = 256 * 128;          // a stage's weight rows
+constexpr int kTBytes = 128 * 128;          // a stage's token rows, at most
 constexpr int kMaxAcc = 8;
 constexpr int kMaxGroupsLaunch = 512;       // groups of one launch (schedule in shared memory)
 constexpr int kMmaK = 32;                   // K per tcgen05.mma of 8-bit types
-constexpr unsigned long long kCopyGraceNs = 100000ull;  // see moe_gemm_pair.cu
 
 struct Smem {
   static constexpr int W = 0;
-  static constexpr int T = W + kStages * kStageBytes;
-  static constexpr int EPI = T + kStages * kStageBytes;         // 16 KB of staging
+  static constexpr int T = W + kStages * kWBytes;
+  static constexpr int EPI = T + kStages * kTBytes;             // 16 KB of staging
   static constexpr int FAC = EPI + 16384;                       // weights tiles: a warp's row scales [2][32]
-  static constexpr int META = FAC + kEpiWarps * 256;            // weights tiles: dst and weight, or row maxima
-  static constexpr int RMAX = META + 2048;                      // rows tiles: row maxima (the peer may already
-                                                                // write those of a later weights tile)
-  static constexpr int BARS = RMAX + 2048;
-  // full, empty [kStages], tfull, tempty [kMaxAcc], drain [2], maxima [4]
-  static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + 6;
+  static constexpr int META = FAC + kEpiWarps * 256;            // dst and weight of weights tiles, or row maxima
+  static constexpr int BARS = META + 2048;
+  // full, empty [kStages], tfull, tempty [kMaxAcc], drain [2]
+  static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + 2;
   static constexpr int MISC = BARS + NBARS * 8;                 // tmem slot, abort flag, scan
   static constexpr int ROWS_START = (MISC + 8 + 8 * (kThreads / 32) + 15) & ~15;
   static constexpr int TAIL_START = ROWS_START + (kMaxGroupsLaunch + 1) * 4;
@@ -163,12 +162,6 @@ __device__ __forceinline__ int tail_blocks(int rows) {
   return rows > 0 && rows % kTokBlock != 0 && rows % kTokBlock <= kTail ? 1 : 0;
 }
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
-  return v;
-}
-
 // silu(g) u; tolerance-checked: the fast exponential and division serve
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
@@ -181,8 +174,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
                 const __grid_constant__ CUtensorMap tmW, const KernelParams kp) {
   using S = Smem;
   const GemmParams& p = kp.g;
-  constexpr int kFbCols = kGU ? 128 : 256;   // output features per tile (both CTAs)
-  constexpr int kWBox = kGU ? 64 : 128;      // weight rows per TMA box
+  constexpr int kFbCols = kGU ? 128 : 256;   // output features per tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -197,30 +189,26 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   // opaque, so that the inner loops hold them in registers instead of reading them anew
   int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("" : "+r"(warp), "+r"(lane));
-  const uint32_t rank = ptx::cluster_ctarank();
-  const bool leader = rank == 0;
-  const int unit = static_cast<int>(blockIdx.x >> 1);
-  const int n_units = static_cast<int>(gridDim.x >> 1);
+  const int unit = static_cast<int>(blockIdx.x);
+  const int n_units = static_cast<int>(gridDim.x);
   const uint32_t bars = sbase + S::BARS;
   auto bar_full = [&](int s) { return bars + 8u * s; };
   auto bar_empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto bar_tfull = [&](int a) { return bars + 8u * (2 * kStages + a); };
   auto bar_tempty = [&](int a) { return bars + 8u * (2 * kStages + kMaxAcc + a); };
   auto bar_drain = [&](int i) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + i); };
-  auto bar_max = [&](int c) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + 2 + c); };
 
   count_launch(kp.launches, p.kid);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar_full(s), 1);    // the even CTA's expect-tx arrive
-      ptx::mbar_init(bar_empty(s), 2);   // two commits of the pair's MMA issuers
+      ptx::mbar_init(bar_full(s), 1);    // the producer's expect-tx arrive
+      ptx::mbar_init(bar_empty(s), 2);   // the two issuers' MMA commits
     }
     for (int a = 0; a < kMaxAcc; ++a) {
-      ptx::mbar_init(bar_tfull(a), 1);    // the pair's MMA commit
-      ptx::mbar_init(bar_tempty(a), 32);  // sixteen from the warps of either CTA that read it
+      ptx::mbar_init(bar_tfull(a), 1);    // the issuer's MMA commit
+      ptx::mbar_init(bar_tempty(a), 8);   // the epilogue warps of its part
     }
-    for (int c = 0; c < 4; ++c) ptx::mbar_init(bar_max(c), 8);  // a group's four warps in both CTAs
     for (int i = 0; i < 2; ++i) ptx::mbar_init(bar_drain(i), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
@@ -233,8 +221,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     ptx::tma_prefetch_desc(&tmW);
   }
   if (warp == 1) {
-    ptx::tmem_alloc2(ptx::smem_u32(tmem_slot), 512);
-    ptx::tmem_relinquish2();
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
   }
 
   grid_dep_wait();
@@ -292,7 +280,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   const Schedule sch{sbase, G, p.N, kFbCols};
   ptx::tc_fence_before();
   __syncthreads();
-  ptx::cluster_sync();  // the peer's barriers exist before any remote arrive or copy
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int nk = blocks_of(p.K);
@@ -302,84 +289,73 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   const uint32_t acc_cols = 512u >> acc_shift;
 
   bool mma_any = false;
+  uint32_t loads = 0;   // stages the producer has filled
 
   if (warp < 4) {
     ptx::setmaxnreg_dec<kAuxRegs>();
     if (warp == 0) {
-      // ------------------------------------------------------------ TMA producer
-      // lane 0 the first weight box (up rows, or all), lane 1 the gate rows, lane 2 the
-      // CTA's token rows: its half of the 256 of a rows tile, or of a weights tile's padded rows
+      // ---------------------------------------------------------- TMA producer
+      // lanes 0 and 1 the boxes of the two parts' weight rows, lane 2 the token rows
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int tile = unit; ok && tile < total; tile += n_units) {
         const Tile t = sch.at(tile);
-        const int half = t.n_tok > kTail ? 128 : ((t.n_tok + 15) & ~15) >> 1;
-        const int tbox = half <= 16 ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
-        const uint32_t bytes = kStageBytes + tbox * 128;
-        const int wrow = t.g * kp.rows_per_group + t.n0 + static_cast<int>(rank) * (kFbCols / 2);
-        const bool issues = lane == 0 || lane == 2 || (kGU && lane == 1);
+        const int tbox = t.n_tok > 64 ? 128 : (t.n_tok > 32 ? 64 : (t.n_tok > 16 ? 32 : 16));
+        const uint32_t bytes = kWBytes + tbox * 128;
+        const int wrow = t.g * kp.rows_per_group + t.n0;
         const CUtensorMap* mbox =
             lane < 2 ? &tmW : (tbox == 16 ? &tmT16 : (tbox == 32 ? &tmT32 : (tbox == 64 ? &tmT64 : &tmT128)));
-        const int ybox = lane == 2 ? t.r0 + static_cast<int>(rank) * half
-                                   : (kGU && lane == 0 ? wrow + p.N : wrow);
-        const uint32_t dbox = lane == 2 ? S::T : S::W + (lane == 1 ? kWBox * 128 : 0);
+        const int ybox = lane == 2 ? t.r0 : (kGU ? (lane == 0 ? wrow + p.N : wrow) : wrow + 128 * lane);
+        const uint32_t dbox = lane == 2 ? S::T : S::W + lane * (kWBytes / 2);
+        const uint32_t dstep = lane == 2 ? kTBytes : kWBytes;
         for (int kb = 0; kb < nk; ++kb) {
           bool got = true;
           if (lane == 0) {
             // spinning: the producer's reaction time is part of the ring's round trip
             got = wait_bar_spin(bar_empty(stage), phase ^ 1u, abort_flag, kp.status, kp.wait_ns);
-            if (got && leader) ptx::mbar_arrive_expect_tx(bar_full(stage), 2 * bytes);
+            if (got) ptx::mbar_arrive_expect_tx(bar_full(stage), bytes);
           }
           if (!__shfl_sync(0xffffffffu, got ? 1 : 0, 0)) {
             ok = false;
             break;
           }
+          ++loads;
           // the maps see pairs of codes as 2-byte elements: 64 of them per scale block
-          if (issues)
-            ptx::tma_load_2d_pair(sbase + dbox + stage * kStageBytes, mbox, kb * 64, ybox,
-                                  ptx::mapa_shared(bar_full(stage), 0));
+          if (lane < 3) ptx::tma_load_2d(sbase + dbox + stage * dstep, mbox, kb * 64, ybox, bar_full(stage));
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
       }
     } else if (warp < 3) {
-      // ------------------------------------------------------------ MMA issuers (even CTA)
-      // One thread takes about 400 cycles a part for its waits, MMAs and commits, which is
-      // more than the MMAs run, so two take turns: the two parts of a rows tile's block,
-      // or the even and the odd blocks of a weights tile.
-      if (leader && ptx::elect_one()) {
-        const int me = warp - 1;
+      // ---------------------------------------------------------- MMA issuers
+      // One thread takes about 400 cycles a part for its waits, MMAs and commits, more than
+      // the MMAs run, so there is one for each part.
+      if (ptx::elect_one()) {
+        const uint32_t me = warp - 1;
         int stage = 0;
-        uint32_t phase = 0, parts = 0;     // parts: accumulators taken from the ring so far
+        uint32_t phase = 0, parts = me;    // the part's place among the accumulators taken so far
         bool ok = true;
         for (int tile = unit; ok && tile < total; tile += n_units) {
           const Tile t = sch.at(tile);
           const bool big = t.n_tok > kTail;
-          const uint32_t idesc = ptx::idesc_e4m3_f32(256, big ? 128 : (t.n_tok + 15) & ~15);
-          for (int kb = 0; ok && kb < nk; ++kb) {
-            if (big || (kb & 1) == me) {
-              const uint32_t at = big ? parts + me : parts, acc = at & acc_mask;
-              // the accumulator's release orders tensor memory only (see the arrives)
-              ok = wait_bar(bar_tempty(acc), ((at >> acc_shift) & 1u) ^ 1u, abort_flag, kp.status,
-                            kp.wait_ns) &&
-                   wait_bar(bar_full(stage), phase, abort_flag, kp.status, kp.wait_ns);
-              if (!ok) break;
-              ptx::tc_fence_after();
-              const uint64_t dw = ptx::desc_kmajor_sw128(sbase + S::W + stage * kStageBytes);
-              const uint64_t dt = ptx::desc_kmajor_sw128(sbase + S::T + stage * kStageBytes);
-              const uint32_t d = tmem_base + acc * acc_cols;
-              // rows tiles: tokens on M, 64 weight rows of each CTA on N
-              const uint64_t da = big ? dt : dw;
-              const uint64_t db = big ? dw + static_cast<uint64_t>(me * (64 * 128 / 16)) : dt;
+          const uint32_t idesc = ptx::idesc_e4m3_f32(128, big ? 128 : (t.n_tok + 15) & ~15);
+          for (int kb = 0; kb < nk; ++kb, parts += 2) {
+            const uint32_t acc = parts & acc_mask;
+            ok = wait_bar(bar_tempty(acc), ((parts >> acc_shift) & 1u) ^ 1u, abort_flag, kp.status,
+                          kp.wait_ns) &&
+                 wait_bar(bar_full(stage), phase, abort_flag, kp.status, kp.wait_ns);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint64_t dw = ptx::desc_kmajor_sw128(sbase + S::W + stage * kWBytes + me * (kWBytes / 2));
+            const uint64_t dt = ptx::desc_kmajor_sw128(sbase + S::T + stage * kTBytes);
+            const uint32_t d = tmem_base + acc * acc_cols;
+            const uint64_t da = big ? dt : dw, db = big ? dw : dt;   // rows tiles: tokens on M
 #pragma unroll
-              for (int k = 0; k < kBlk / kMmaK; ++k)   // a fresh sum per scale block
-                ptx::mma_e4m3_pair(d, da + 2ull * k, db + 2ull * k, idesc, k != 0 ? 1u : 0u);
-              mma_any = true;
-              ptx::mma_commit_pair(bar_tfull(acc), 3);     // the part's sums are ready in both
-              ptx::mma_commit_pair(bar_empty(stage), 3);   // frees the stage in both CTAs (with
-              if (!big) ptx::mma_commit_pair(bar_empty(stage), 3);   // the other part's, or alone)
-            }
-            parts += big ? 2 : 1;
+            for (int k = 0; k < kBlk / kMmaK; ++k)   // a fresh sum per scale block
+              ptx::mma_e4m3(d, da + 2ull * k, db + 2ull * k, idesc, k != 0 ? 1u : 0u);
+            mma_any = true;
+            ptx::mma_commit(bar_tfull(acc));         // the part's sums are ready
+            ptx::mma_commit(bar_empty(stage));       // frees the stage, with the other part's
             if (++stage == kStages) { stage = 0; phase ^= 1u; }
           }
         }
@@ -390,16 +366,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     ptx::setmaxnreg_inc<kEpiRegs>();
     const int e = warp - 4;                          // 0..15
     const int grp = e >> 2;                          // four warps that cover the 128 TMEM lanes
-    const int h = grp & 1, set = grp >> 1;           // rows tiles: columns 64 h .. of part `set`
+    const int h = grp & 1, set = grp >> 1;           // half of the columns of part `set`
     const int q = warp & 3;                          // TMEM lane quarter
     const int f = q * 32 + lane;                     // TMEM lane
     const int et = e * 32 + lane;                    // 0..511
-    const int gt = et & 127;                         // thread of its group
+    const int ht = (set << 7) | f;                   // thread among those of its half of the columns
     const uint32_t tmem_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    const uint32_t tempty_leader = ptx::mapa_shared(bar_tempty(0), 0);
     const int rb = blocks_of(kp.rows_per_group);
-    uint32_t parts = 0;        // accumulators passed so far
-    uint32_t n_tails = 0;      // weights tiles so far: META's half, the maxima's phase
+    uint32_t parts = set;      // the part's place among the accumulators passed so far
+    uint32_t n_tails = 0;      // weights tiles so far: META's half
     for (int tile = unit; tile < total; tile += n_units) {
       if (tile < sch.word(S::ROWS_START, G)) {
         // ---------------------------------------------------------- rows tile
@@ -411,11 +386,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         uint32_t to_sw1;
         {
           const Tile t = sch.at(tile);
-          const int j = static_cast<int>(rank) * 128 + f;      // this thread's row of the tile
+          const int j = f;                     // this thread's row of the tile
           sa = p.sa + static_cast<size_t>(t.r0 + (j < t.n_tok ? j : 0)) * nk;
           // the weight rows behind this thread's 64 columns: one scale block, or (up rows of
           // I not a multiple of 128) two that meet at a multiple of 16
-          const int wr = kGU ? t.n0 + 64 * h + (set == 0 ? p.N : 0) : t.n0 + 128 * h + 64 * set;
+          const int wr = kGU ? t.n0 + 64 * h + (set == 0 ? p.N : 0) : t.n0 + 128 * set + 64 * h;
           const int wb = min(wr / kBlk, rb - 1);
           sw0 = p.sw + (static_cast<size_t>(t.g) * rb + wb) * nk;
           split = kGU && set == 0 ? (wb + 1) * kBlk - wr : 64;           // columns of the first block
@@ -428,8 +403,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           a0 = __ldg(sa + next);
           w0 = __ldg(sw0 + next);
           if (kGU) x0 = __ldg(sw0 + to_sw1 + next);
-          const uint32_t at = parts + set, acc = at & 3u;
-          wait_lean(bar_tfull(acc), (at >> 2) & 1u, sbase + S::MISC + 4, kp.status, kp.wait_ns);
+          const uint32_t acc = parts & 3u;
+          wait_lean(bar_tfull(acc), (parts >> 2) & 1u, sbase + S::MISC + 4, kp.status, kp.wait_ns);
           ptx::tc_fence_after();
           const uint32_t taddr = tmem_lane + acc * 128 + 64 * h;
 #pragma unroll
@@ -439,7 +414,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
             ptx::tmem_ld_wait();
             if (c == 3) {                            // the warp has read all of it
               ptx::tc_fence_before();
-              if (lane == 0) ptx::mbar_arrive_remote_relaxed_n(tempty_leader + 8u * acc, 2);
+              if (lane == 0) ptx::mbar_arrive(bar_tempty(acc));
             }
             const float sc = !kGU || 16 * c < split ? s0 : s1;
 #pragma unroll
@@ -450,7 +425,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         // one decision for the sixteen warps
         if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + 4) == 0)) break;
         const Tile t = sch.at(tile);                 // anew
-        const int j = static_cast<int>(rank) * 128 + f;
+        const int j = f;
         const bool live = j < t.n_tok;
         uint32_t pk[32];                             // the 64 results in bf16
         int d = -1;
@@ -474,7 +449,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           // one row's 32 bytes
           const uint32_t st = sbase + S::EPI + e * 1024;
           const int cols = kGU ? 2 * p.N : p.N;
-          const int lim = kGU ? t.n0 + 64 * h : t.n0 + 128 * h + 64 * set;   // the first column within its half
+          const int lim = kGU ? t.n0 + 64 * h : t.n0 + 128 * set + 64 * h;   // the first column within its half
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t sx = (lane >> 2) & 1;
@@ -527,7 +502,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (col + (i & 16) < p.N) m = fmaxf(m, fabsf(act[i]));        // N % 16 == 0
-          const uint32_t s_max = sbase + S::RMAX;    // [4 groups][128 rows]
+          const uint32_t s_max = sbase + S::META;    // [4 groups][128 rows]
           ptx::st_shared_f32(s_max + (grp * 128 + f) * 4, m);
           ptx::bar_sync(6, 32 * kEpiWarps);
 #pragma unroll
@@ -551,10 +526,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       // ------------------------------------------------------------ weights tile
       const Tile t = sch.at(tile);
       const int parity = n_tails++ & 1;
-      const float* sw = p.sw + static_cast<size_t>(t.g) * rb * nk;
-      const int first = t.n0 + static_cast<int>(rank) * (kFbCols / 2);   // the CTA's first column
       int* dst_t = reinterpret_cast<int*>(smem + S::META) + parity * kTail;               // plain
-      float* w_t = reinterpret_cast<float*>(smem + S::META + 1024) + parity * kTail;
+      float* w_t = reinterpret_cast<float*>(smem + S::META + 512) + parity * kTail;
       if (!kGU && et < kTail) {
         // destination rows and weights; the last readers of this half (two tiles ago) passed the
         // previous tile's vote
@@ -563,19 +536,18 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         dst_t[et] = d;
         w_t[et] = p.pair_weight && d >= 0 ? __ldg(p.pair_weight + d) : 1.0f;
       }
-      // group grp joins the rows 32 grp .. of the tile; those without rows leave their arrivals
-      // on the accumulators' barriers to the others
-      const int n_grp = (t.n_tok + 31) >> 5;
+      // half h joins the rows 32 h .. of the tile; where the second half has none, the first
+      // one's warps arrive on the accumulators' barriers for both
       float sum[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) sum[i] = 0.0f;
-      if (grp < n_grp) {
-        const uint32_t n_arrive = n_grp == 3 ? (grp == 0 ? 2 : 1) : 4 / n_grp;
-        const int wr = kGU ? first + (f < 64 ? p.N + f : f - 64) : first + f;   // this thread's weight row
-        const float* sw_p = sw + static_cast<size_t>(min(wr / kBlk, rb - 1)) * nk;
-        const float* sa_p = p.sa + static_cast<size_t>(t.r0 + min(32 * grp + lane, t.n_tok - 1)) * nk;
+      if (32 * h < t.n_tok) {
+        const uint32_t n_arrive = t.n_tok > 32 ? 1 : 2;
+        const int wr = kGU ? t.n0 + f + (set == 0 ? p.N : 0) : t.n0 + 128 * set + f;   // this thread's weight row
+        const float* sw_p = p.sw + (static_cast<size_t>(t.g) * rb + min(wr / kBlk, rb - 1)) * nk;
+        const float* sa_p = p.sa + static_cast<size_t>(t.r0 + min(32 * h + lane, t.n_tok - 1)) * nk;
         const uint32_t fac = sbase + S::FAC + e * 256;
-        const bool wide = t.n_tok > 32 * grp + 16;
+        const bool wide = t.n_tok > 32 * h + 16;
         float a0 = __ldg(sa_p), w0 = __ldg(sw_p);
         for (int kb = 0; kb < nk; ++kb) {
           const float s = w0;
@@ -588,10 +560,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, sbase + S::MISC + 4, kp.status, kp.wait_ns);
           ptx::tc_fence_after();
           uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(tmem_lane + acc * acc_cols + 32 * grp, v);
+          ptx::tmem_ld_32x32b_x32(tmem_lane + acc * acc_cols + 32 * h, v);
           ptx::tmem_ld_wait();
           ptx::tc_fence_before();
-          if (lane == 0) ptx::mbar_arrive_remote_relaxed_n(tempty_leader + 8u * acc, n_arrive);
+          if (lane == 0) ptx::mbar_arrive_n(bar_tempty(acc), n_arrive);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (i < 4 || wide) {
@@ -602,26 +574,24 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
               sum[4 * i + 3] = fmaf(__uint_as_float(v[4 * i + 3]), __fmul_rn(__uint_as_float(a4.w), s), sum[4 * i + 3]);
             }
           }
-          ++parts;
+          parts += 2;
         }
       } else {
-        parts += nk;
+        parts += 2 * nk;
       }
-      // one decision for the sixteen warps; the barrier also publishes dst_t / w_t
+      // one decision for the sixteen warps (and those without rows wait for the others);
+      // the barrier also publishes dst_t / w_t
       if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + 4) == 0)) break;
-      // 16 rows of the group at a time through its 4 KB of staging: [16 rows][128 features] bf16,
+      // 16 rows of the half at a time through its 8 KB of staging: [16 rows][256 weight rows] bf16,
       // 16-byte pieces XOR-swizzled by the row
-      const uint32_t ost = sbase + S::EPI + grp * 4096;
-      const uint32_t place = ost + ((f >> 3) << 4) + (f & 7) * 2;
-      const int tok = gt >> 3, oct = gt & 7;     // gate/up: row of the 16, 8 features of it
-      const int col = first + 8 * oct;
-      const bool in = col < p.N;                 // N % 16 == 0
-      const uint32_t s_max = sbase + S::META + (parity * 4 + grp) * 256 + tok * 4;   // [2][4 groups][2 CTAs][32]
-      float act[2][8];
+      const uint32_t ost = sbase + S::EPI + h * 8192;
+      const uint32_t place = ost + ((ht >> 3) << 4) + (ht & 7) * 2;
+      const int tok = ht >> 4, oct = ht & 15;    // gate/up: row of the 16, 8 features of it
+      const int col = t.n0 + 8 * oct;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int j0 = 32 * grp + 16 * c;
-        if (j0 >= t.n_tok) continue;             // the same for the whole group
+        const int j0 = 32 * h + 16 * c;
+        if (j0 >= t.n_tok) continue;             // the same for the whole half
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x[4];
@@ -638,104 +608,76 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           for (int k = 0; k < 2; ++k) {          // gate/up: narrowed before the activation
             const uint32_t pk = gemm::pack_bf16x2(x[2 * k], x[2 * k + 1]);
             const int jj = 4 * i + 2 * k;
-            ptx::st_shared_u16((place ^ (jj << 4)) + jj * 256, static_cast<uint16_t>(pk));
-            ptx::st_shared_u16((place ^ ((jj + 1) << 4)) + (jj + 1) * 256, static_cast<uint16_t>(pk >> 16));
+            ptx::st_shared_u16((place ^ (jj << 4)) + jj * 512, static_cast<uint16_t>(pk));
+            ptx::st_shared_u16((place ^ ((jj + 1) << 4)) + (jj + 1) * 512, static_cast<uint16_t>(pk >> 16));
           }
         }
-        ptx::bar_sync(1 + grp, 128);
+        ptx::bar_sync(1 + h, 256);
         if (!kGU) {
-          // sixteen threads store one row's 256 bytes
+          // a warp stores one row's 512 bytes
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int idx = gt + 128 * i;
-            const int jj = idx >> 4, k = idx & 15;
-            const int cc = first + 8 * k;
+            const int jj = (ht >> 5) + 8 * i;
+            const int cc = t.n0 + 8 * lane;
             if (j0 + jj < t.n_tok && cc < p.N) {
               const int d = dst_t[j0 + jj];
-              const uint4 val = ptx::ld_shared_v4(ost + jj * 256 + ((k ^ jj) << 4));
+              const uint4 val = ptx::ld_shared_v4(ost + jj * 512 + ((lane ^ jj) << 4));
               if (d >= 0) *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(d) * p.N + cc) = val;
             }
           }
         } else {
-          const uint32_t row = ost + tok * 256;
+          // sixteen threads hold a row: up pieces first, then gate
+          const uint32_t row = ost + tok * 512;
           const uint4 u4 = ptx::ld_shared_v4(row + ((oct ^ tok) << 4));
-          const uint4 g4 = ptx::ld_shared_v4(row + (((oct + 8) ^ tok) << 4));
-          if (p.out && in && j0 + tok < t.n_tok) {
-            uint16_t* o = p.out + static_cast<size_t>(t.r0 + j0 + tok) * 2 * p.N + col;
+          const uint4 g4 = ptx::ld_shared_v4(row + (((oct + 16) ^ tok) << 4));
+          const bool in = col < p.N;             // N % 16 == 0
+          const bool live = j0 + tok < t.n_tok;
+          const size_t r = static_cast<size_t>(t.r0 + j0 + tok);
+          if (p.out && in && live) {
+            uint16_t* o = p.out + r * 2 * p.N + col;
             *reinterpret_cast<uint4*>(o) = g4;
             *reinterpret_cast<uint4*>(o + p.N) = u4;
           }
-          float g[8], u[8], m = 0.0f;
+          float g[8], u[8], act[8], m = 0.0f;
           widen8(g4, g);
           widen8(u4, u);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            act[c][i] = silu_mul(g[i], u[i]);
-            m = fmaxf(m, fabsf(act[c][i]));
+            act[i] = silu_mul(g[i], u[i]);
+            m = fmaxf(m, fabsf(act[i]));
           }
           if (!in) m = 0.0f;
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (oct == 0) {
-            const uint32_t mx = s_max + rank * 128 + c * 64;
-            ptx::st_shared_f32(mx, m);
-            ptx::st_cluster_f32(ptx::mapa_shared(mx, rank ^ 1u), m);
-          }
+          for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          float d, id;
+          block_scale(m, d, id);
+          if (in && live)
+            *reinterpret_cast<uint2*>(p.act + r * p.N + col) = make_uint2(
+                codes4(__fmul_rn(act[0], id), __fmul_rn(act[1], id), __fmul_rn(act[2], id), __fmul_rn(act[3], id)),
+                codes4(__fmul_rn(act[4], id), __fmul_rn(act[5], id), __fmul_rn(act[6], id), __fmul_rn(act[7], id)));
+          if (oct == 0 && live) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = d;
         }
-        ptx::bar_sync(1 + grp, 128);
-      }
-      if (kGU) {
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive_remote(ptx::mapa_shared(bar_max(grp), rank));
-          ptx::mbar_arrive_remote(ptx::mapa_shared(bar_max(grp), rank ^ 1u));
-        }
-        // a warp that gives up here stops at the next tile's vote: the named barriers stay matched
-        const bool ok = wait_bar<true>(bar_max(grp), parity, abort_flag, kp.status, kp.wait_ns);
-        if (ok) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int jj = 32 * grp + 16 * c + tok;
-            if (jj >= t.n_tok) continue;
-            const float m = fmaxf(ptx::ld_shared_f32(s_max + c * 64), ptx::ld_shared_f32(s_max + 128 + c * 64));
-            float d, id;
-            block_scale(m, d, id);
-            const size_t r = static_cast<size_t>(t.r0 + jj);
-            if (in)
-              *reinterpret_cast<uint2*>(p.act + r * p.N + col) = make_uint2(
-                  codes4(__fmul_rn(act[c][0], id), __fmul_rn(act[c][1], id), __fmul_rn(act[c][2], id),
-                         __fmul_rn(act[c][3], id)),
-                  codes4(__fmul_rn(act[c][4], id), __fmul_rn(act[c][5], id), __fmul_rn(act[c][6], id),
-                         __fmul_rn(act[c][7], id)));
-            if (oct == 0 && leader) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = d;
-          }
-        }
+        ptx::bar_sync(1 + h, 256);
       }
     }
   }
 
-  // ---- exit: if either CTA of the pair gave up, drain before freeing memory
+  // ---- exit: a CTA that gave up drains its MMAs and copies before it frees memory
   __syncthreads();
-  ptx::cluster_sync();
-  const bool gave_up =
-      *abort_flag != 0 ||
-      ld_cluster_u32(ptx::mapa_shared(sbase + S::MISC + 4, rank ^ 1u)) != 0;
-  if (gave_up) {
+  if (*abort_flag != 0) {
     if (mma_any) {   // the issuing threads
-      ptx::mma_commit_pair(bar_drain(warp - 1), 1);
+      ptx::mma_commit(bar_drain(warp - 1));
       gemm::spin_bounded(bar_drain(warp - 1), 0);
     }
-    if (warp == 0 && lane == 0) {
-      const uint64_t t0 = ptx::globaltimer_ns();
-      while (ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
-      }
-    }
+    // the producer's copies: the last kStages fills may still be on their way
+    if (warp == 0 && lane == 0)
+      for (uint32_t i = loads < kStages ? 0 : loads - kStages; i < loads; ++i)
+        gemm::spin_bounded(bar_full(i % kStages), (i / kStages) & 1u);
   }
   __syncthreads();
-  ptx::cluster_sync();  // the peer may still use this CTA's shared memory or TMEM until here
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc2(tmem_base, 512);
+    ptx::tmem_dealloc(tmem_base, 512);
   }
 }
 
@@ -744,46 +686,27 @@ int launch_range(const char* op, const CUtensorMap (&tt)[4], const CUtensorMap& 
                  cudaStream_t stream) {
   auto kern = fp8_gemm_kernel<kGU>;
   const int smem = Smem::ALLOC;
-  static std::atomic<int> pairs_dev[64] = {};   // resident clusters, once the kernel is configured
+  static std::atomic<int> ready_dev[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     dev = -1;
   }
   const bool cache = dev >= 0 && dev < 64;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  int max_pairs = cache ? pairs_dev[dev].load(std::memory_order_acquire) : 0;
-  if (max_pairs <= 0) {
+  if (!cache || !ready_dev[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return set_error(MOE_ERR_CUDA, "%s: cannot reserve %d bytes of shared memory: %s", op, smem,
                        cudaGetErrorString(cudaGetLastError()));
-    // a pair must sit in one GPC, so fewer than SMs / 2 pairs may fit at once
-    max_pairs = sm_count() / 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * max_pairs), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0)
-      max_pairs = clusters < max_pairs ? clusters : max_pairs;
-    else
-      cudaGetLastError();
-    if (cache) pairs_dev[dev].store(max_pairs, std::memory_order_release);
+    if (cache) ready_dev[dev].store(1, std::memory_order_release);
   }
   const GemmParams& p = kp.g;
   const int fb_cols = kGU ? 128 : 256;
-  long long pairs = (p.P + kTokBlock - 1) / kTokBlock + (p.G < p.P ? p.G : p.P);
-  pairs *= (p.N + fb_cols - 1) / fb_cols;       // an upper bound on the tiles
-  if (pairs > max_pairs) pairs = max_pairs;
-  return launch_status(launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs), 1, 1),
-                                     dim3(kThreads, 1, 1), smem, stream, attr, 1, tt[0], tt[1],
-                                     tt[2], tt[3], tw, kp),
+  long long tiles = (p.P + kTokBlock - 1) / kTokBlock + (p.G < p.P ? p.G : p.P);
+  tiles *= (p.N + fb_cols - 1) / fb_cols;       // an upper bound
+  const long long sms = sm_count();
+  if (tiles > sms) tiles = sms;
+  return launch_status(launch_kernel(kern, dim3(static_cast<unsigned>(tiles), 1, 1), dim3(kThreads, 1, 1),
+                                     smem, stream, nullptr, 0, tt[0], tt[1], tt[2], tt[3], tw, kp),
                        op);
 }
 
@@ -798,7 +721,7 @@ int launch_product(const char* op, const GemmParams& p0, bool gateup, cudaStream
   // 128-byte swizzle as a bf16 operand's box
   for (int i = 0; i < 4; ++i)
     if ((rc = gemm::make_tmap(&tt[i], p.a, p.P, p.K / 2, 16 << i, op, "a_codes")) != MOE_OK) return rc;
-  if ((rc = gemm::make_tmap(&tw, p.w, static_cast<long long>(p.G) * rows, p.K / 2, gateup ? 64 : 128,
+  if ((rc = gemm::make_tmap(&tw, p.w, static_cast<long long>(p.G) * rows, p.K / 2, 128,
                             op, "weights")) != MOE_OK)
     return rc;
   DeviceDiag diag = device_diag();
