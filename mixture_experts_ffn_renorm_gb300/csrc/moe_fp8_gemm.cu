@@ -49,7 +49,6 @@ namespace moe {
 namespace fp8 {
 namespace {
 
-using gemm::wait_bar;
 using gemm::wait_bar_spin;
 
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
@@ -58,28 +57,34 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   return v;
 }
 
-// Bounded wait (see gemm::wait_bar) for the loops that run once per scale block and
-// warp, where every instruction counts: the probe without a time hint (the one with a
-// hint is a software loop around it), and no result.  A wait that gives up raises the
-// status and the CTA's abort flag; its warp goes on with what is there, its later waits
-// end at once, and it stops at the tile's vote.
-__device__ __forceinline__ void wait_lean(uint32_t bar, uint32_t parity, uint32_t abort_flag,
-                                          unsigned int* status, unsigned long long limit_ns) {
-  if (!ptx::mbar_try_wait(bar, parity)) {
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(bar, parity) && ld_shared_u32(abort_flag) == 0) {
-      if (ptx::globaltimer_ns() - t0 > limit_ns) {
-        if (status) atomicOr(status, static_cast<unsigned int>(MOE_STATUS_TIMEOUT));
-        asm volatile("st.shared.u32 [%0], 1;" ::"r"(abort_flag) : "memory");
-      }
+// Bounded wait (see gemm::wait_bar) for the loops that run once per scale block, where
+// every instruction counts: the probe without a time hint (the one with a hint is a
+// software loop around it).  A wait that gives up raises the status and the CTA's abort
+// flag.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint32_t abort_flag,
+                                         unsigned int* status, unsigned long long limit_ns) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (ld_shared_u32(abort_flag) != 0) return false;
+    if (ptx::globaltimer_ns() - t0 > limit_ns) {
+      if (status) atomicOr(status, static_cast<unsigned int>(MOE_STATUS_TIMEOUT));
+      asm volatile("st.shared.u32 [%0], 1;" ::"r"(abort_flag) : "memory");
     }
   }
+  return true;
+}
+// the same for a whole warp, which after a wait that gives up goes on with what is there:
+// its later waits end at once, and it stops at the tile's vote
+__device__ __forceinline__ void wait_lean(uint32_t bar, uint32_t parity, uint32_t abort_flag,
+                                          unsigned int* status, unsigned long long limit_ns) {
+  wait_one(bar, parity, abort_flag, status, limit_ns);
   __syncwarp();
 }
 
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of other roles (one of its warps idle)
-constexpr int kAuxRegs = 64, kEpiRegs = 104;
+constexpr int kAuxRegs = 32, kEpiRegs = 112;
 // the split draws on the registers the block was launched with (96 a thread)
 static_assert(128 * kAuxRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 96, "register split");
 constexpr int kTokBlock = 128;              // rows per rows tile
@@ -341,15 +346,18 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           const uint32_t idesc = ptx::idesc_e4m3_f32(128, big ? 128 : (t.n_tok + 15) & ~15);
           for (int kb = 0; kb < nk; ++kb, parts += 2) {
             const uint32_t acc = parts & acc_mask;
-            ok = wait_bar(bar_tempty(acc), ((parts >> acc_shift) & 1u) ^ 1u, abort_flag, kp.status,
-                          kp.wait_ns) &&
-                 wait_bar(bar_full(stage), phase, abort_flag, kp.status, kp.wait_ns);
-            if (!ok) break;
-            ptx::tc_fence_after();
             const uint64_t dw = ptx::desc_kmajor_sw128(sbase + S::W + stage * kWBytes + me * (kWBytes / 2));
             const uint64_t dt = ptx::desc_kmajor_sw128(sbase + S::T + stage * kTBytes);
             const uint32_t d = tmem_base + acc * acc_cols;
             const uint64_t da = big ? dt : dw, db = big ? dw : dt;   // rows tiles: tokens on M
+            // the accumulator last: its release is what the round trip waits for
+            if (!wait_one(bar_full(stage), phase, sbase + S::MISC + 4, kp.status, kp.wait_ns) ||
+                !wait_one(bar_tempty(acc), ((parts >> acc_shift) & 1u) ^ 1u, sbase + S::MISC + 4,
+                          kp.status, kp.wait_ns)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
 #pragma unroll
             for (int k = 0; k < kBlk / kMmaK; ++k)   // a fresh sum per scale block
               ptx::mma_e4m3(d, da + 2ull * k, db + 2ull * k, idesc, k != 0 ? 1u : 0u);
