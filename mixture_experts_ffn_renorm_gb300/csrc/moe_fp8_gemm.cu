@@ -56,30 +56,10 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-
-// Bounded wait (see gemm::wait_bar) for the loops that run once per scale block, where
-// every instruction counts: the probe without a time hint (the one with a hint is a
-// software loop around it).  A wait that gives up raises the status and the CTA's abort
-// flag.
-__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint32_t abort_flag,
-                                         unsigned int* status, unsigned long long limit_ns) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer_ns();
-  while (!ptx::mbar_try_wait(bar, parity)) {
-    if (ld_shared_u32(abort_flag) != 0) return false;
-    if (ptx::globaltimer_ns() - t0 > limit_ns) {
-      if (status) atomicOr(status, static_cast<unsigned int>(MOE_STATUS_TIMEOUT));
-      asm volatile("st.shared.u32 [%0], 1;" ::"r"(abort_flag) : "memory");
-    }
-  }
-  return true;
-}
-// the same for a whole warp, which after a wait that gives up goes on with what is there:
-// its later waits end at once, and it stops at the tile's vote
-__device__ __forceinline__ void wait_lean(uint32_t bar, uint32_t parity, uint32_t abort_flag,
-                                          unsigned int* status, unsigned long long limit_ns) {
-  wait_one(bar, parity, abort_flag, status, limit_ns);
-  __syncwarp();
+__device__ __forceinline__ uint64_t ld_shared_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 constexpr int kEpiWarps = 16;
@@ -105,13 +85,38 @@ struct Smem {
   static constexpr int BARS = META + 2048;
   // full, empty [kStages], tfull, tempty [kMaxAcc], drain [2]
   static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + 2;
-  static constexpr int MISC = BARS + NBARS * 8;                 // tmem slot, abort flag, scan
-  static constexpr int ROWS_START = (MISC + 8 + 8 * (kThreads / 32) + 15) & ~15;
+  static constexpr int MISC = (BARS + NBARS * 8 + 15) & ~15;                 // tmem slot, then:
+  static constexpr int kAbort = 4, kSmall = 8, kStatus = 16, kLimit = 24, kScan = 32;
+  static constexpr int ROWS_START = (MISC + kScan + 8 * (kThreads / 32) + 15) & ~15;
   static constexpr int TAIL_START = ROWS_START + (kMaxGroupsLaunch + 1) * 4;
   static constexpr int GOFF = TAIL_START + (kMaxGroupsLaunch + 1) * 4;
   static constexpr int ALLOC = GOFF + (kMaxGroupsLaunch + 1) * 4 + 1024;
 };
 static_assert(Smem::ALLOC <= 227 * 1024, "shared memory");
+
+// Bounded wait (see gemm::wait_bar) for the loops that run once per scale block, where
+// every instruction and register counts: the probe without a time hint (the one with a
+// hint is a software loop around it), and the limit and the status word's address from
+// shared memory (`misc`).  A wait that gives up raises the status and the CTA's abort flag.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint32_t misc) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (ld_shared_u32(misc + Smem::kAbort) != 0) return false;
+    if (ptx::globaltimer_ns() - t0 > ld_shared_u64(misc + Smem::kLimit)) {
+      unsigned int* status = reinterpret_cast<unsigned int*>(ld_shared_u64(misc + Smem::kStatus));
+      if (status) atomicOr(status, static_cast<unsigned int>(MOE_STATUS_TIMEOUT));
+      asm volatile("st.shared.u32 [%0], 1;" ::"r"(misc + Smem::kAbort) : "memory");
+    }
+  }
+  return true;
+}
+// the same for a whole warp, which after a wait that gives up goes on with what is there:
+// its later waits end at once, and it stops at the tile's vote
+__device__ __forceinline__ void wait_lean(uint32_t bar, uint32_t parity, uint32_t misc) {
+  wait_one(bar, parity, misc);
+  __syncwarp();
+}
 
 struct KernelParams {
   GemmParams g;
@@ -119,6 +124,25 @@ struct KernelParams {
   unsigned long long wait_ns;
   unsigned int* status;
   unsigned long long* launches;
+};
+
+// What an epilogue thread is, worked out anew where it is needed: the loops over the
+// scale blocks have no registers left to carry it through.
+struct Ids {
+  int e, h, set, f, et, ht;
+  __device__ __forceinline__ Ids(int warp, int lane) {
+    asm volatile("" : "+r"(warp), "+r"(lane));
+    e = warp - 4;                      // 0..15
+    h = (e >> 2) & 1;                  // half of the columns of a part
+    set = e >> 3;                      // the part
+    f = (warp & 3) * 32 + lane;        // TMEM lane
+    et = e * 32 + lane;                // 0..511
+    ht = (set << 7) | f;               // thread among those of its half of the columns
+  }
+  // the thread's column of accumulator 0: tensor memory's lane quarter is the warp's
+  __device__ __forceinline__ uint32_t tmem(uint32_t base) const {
+    return base + (static_cast<uint32_t>(f & ~31) << 16);
+  }
 };
 
 struct Tile {
@@ -185,8 +209,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = ptx::smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::MISC + 4);
-  int2* scan_tmp = reinterpret_cast<int2*>(smem + S::MISC + 8);   // one pair per warp
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::MISC + S::kAbort);
+  int2* scan_tmp = reinterpret_cast<int2*>(smem + S::MISC + S::kScan);   // one pair per warp
   int* rows_start = reinterpret_cast<int*>(smem + S::ROWS_START);
   int* tail_start = reinterpret_cast<int*>(smem + S::TAIL_START);
   int* goff = reinterpret_cast<int*>(smem + S::GOFF);
@@ -216,6 +240,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     }
     for (int i = 0; i < 2; ++i) ptx::mbar_init(bar_drain(i), 1);
     *abort_flag = 0;
+    *reinterpret_cast<unsigned int**>(smem + S::MISC + S::kStatus) = kp.status;
+    *reinterpret_cast<unsigned long long*>(smem + S::MISC + S::kLimit) = kp.wait_ns;
     ptx::fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -279,6 +305,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     run_t += tail_blocks(rows) * n_fb;
   }
   if (threadIdx.x == 0) {
+    *reinterpret_cast<int*>(smem + S::MISC + S::kSmall) = small;
     rows_start[G] = all_b;
     tail_start[G] = all_t;
   }
@@ -289,9 +316,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   const uint32_t tmem_base = *tmem_slot;
   const int nk = blocks_of(p.K);
   const int total = sch.total();
-  const int acc_shift = small ? 3 : 2;             // log2 of the accumulators in the ring
-  const uint32_t acc_mask = (1u << acc_shift) - 1u;
-  const uint32_t acc_cols = 512u >> acc_shift;
 
   bool mma_any = false;
   uint32_t loads = 0;   // stages the producer has filled
@@ -337,6 +361,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       // the MMAs run, so there is one for each part.
       if (ptx::elect_one()) {
         const uint32_t me = warp - 1;
+        const int acc_shift = small ? 3 : 2;   // log2 of the accumulators in the ring
+        const uint32_t acc_mask = (1u << acc_shift) - 1u, acc_cols = 512u >> acc_shift;
         int stage = 0;
         uint32_t phase = 0, parts = me;    // the part's place among the accumulators taken so far
         bool ok = true;
@@ -351,9 +377,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
             const uint32_t d = tmem_base + acc * acc_cols;
             const uint64_t da = big ? dt : dw, db = big ? dw : dt;   // rows tiles: tokens on M
             // the accumulator last: its release is what the round trip waits for
-            if (!wait_one(bar_full(stage), phase, sbase + S::MISC + 4, kp.status, kp.wait_ns) ||
-                !wait_one(bar_tempty(acc), ((parts >> acc_shift) & 1u) ^ 1u, sbase + S::MISC + 4,
-                          kp.status, kp.wait_ns)) {
+            if (!wait_one(bar_full(stage), phase, sbase + S::MISC) ||
+                !wait_one(bar_tempty(acc), ((parts >> acc_shift) & 1u) ^ 1u, sbase + S::MISC)) {
               ok = false;
               break;
             }
@@ -372,49 +397,54 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   } else {
     // ------------------------------------------------------------ joins and epilogue
     ptx::setmaxnreg_inc<kEpiRegs>();
-    const int e = warp - 4;                          // 0..15
-    const int grp = e >> 2;                          // four warps that cover the 128 TMEM lanes
-    const int h = grp & 1, set = grp >> 1;           // half of the columns of part `set`
-    const int q = warp & 3;                          // TMEM lane quarter
-    const int f = q * 32 + lane;                     // TMEM lane
-    const int et = e * 32 + lane;                    // 0..511
-    const int ht = (set << 7) | f;                   // thread among those of its half of the columns
-    const uint32_t tmem_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    const int rb = blocks_of(kp.rows_per_group);
-    uint32_t parts = set;      // the part's place among the accumulators passed so far
+    // this role's own copies: what is carried over from before the register split is spilled,
+    // and reloaded in the loops
+    int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+    asm volatile("" : "+r"(warp), "+r"(lane), "+r"(sbase));
+    const uint32_t tmem_base = ld_shared_u32(sbase + S::MISC);
+    const int nk = blocks_of(p.K);
+    const Schedule sch{sbase, p.G, p.N, kFbCols};
+    auto bar_tfull = [&](int a) { return sbase + S::BARS + 8u * (2 * kStages + a); };
+    auto bar_tempty = [&](int a) { return sbase + S::BARS + 8u * (2 * kStages + kMaxAcc + a); };
+    uint32_t parts = (warp - 4) >> 3;   // the part's place among the accumulators passed so far
     uint32_t n_tails = 0;      // weights tiles so far: META's half
-    for (int tile = unit; tile < total; tile += n_units) {
+    for (int tile = blockIdx.x; tile < sch.total(); tile += gridDim.x) {
       if (tile < sch.word(S::ROWS_START, G)) {
         // ---------------------------------------------------------- rows tile
         float sum[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) sum[i] = 0.0f;
-        const float *sa, *sw0;
-        int split;
-        uint32_t to_sw1;
+        // element indexes of the scales fit 32 bits: one per 128 or 16384 codes of one byte
+        uint32_t sa, sw, to_sw1 = 0, taddr0;
+        int split = 64;                              // columns of the first weight scale block
         {
+          const Ids id(warp, lane);
           const Tile t = sch.at(tile);
-          const int j = f;                     // this thread's row of the tile
-          sa = p.sa + static_cast<size_t>(t.r0 + (j < t.n_tok ? j : 0)) * nk;
+          const int rb = blocks_of(kp.rows_per_group);
+          sa = static_cast<uint32_t>(t.r0 + (id.f < t.n_tok ? id.f : 0)) * nk;
           // the weight rows behind this thread's 64 columns: one scale block, or (up rows of
           // I not a multiple of 128) two that meet at a multiple of 16
-          const int wr = kGU ? t.n0 + 64 * h + (set == 0 ? p.N : 0) : t.n0 + 128 * set + 64 * h;
+          const int wr = kGU ? t.n0 + 64 * id.h + (id.set == 0 ? p.N : 0) : t.n0 + 128 * id.set + 64 * id.h;
           const int wb = min(wr / kBlk, rb - 1);
-          sw0 = p.sw + (static_cast<size_t>(t.g) * rb + wb) * nk;
-          split = kGU && set == 0 ? (wb + 1) * kBlk - wr : 64;           // columns of the first block
-          to_sw1 = kGU && split < 64 && wb + 1 < rb ? nk : 0;
+          sw = (static_cast<uint32_t>(t.g) * rb + wb) * nk;
+          if (kGU && id.set == 0) split = (wb + 1) * kBlk - wr;
+          if (kGU && split < 64 && wb + 1 < rb) to_sw1 = nk;
+          taddr0 = id.tmem(tmem_base) + 64 * id.h;
         }
-        float a0 = __ldg(sa), w0 = __ldg(sw0), x0 = kGU ? __ldg(sw0 + to_sw1) : 0.0f;
-        for (int kb = 0; kb < nk; ++kb) {
+        float a0 = __ldg(p.sa + sa), w0 = __ldg(p.sw + sw), x0 = kGU ? __ldg(p.sw + (sw + to_sw1)) : 0.0f;
+#pragma unroll 1
+        for (int left = nk; left > 0; --left) {
           const float s0 = __fmul_rn(a0, w0), s1 = kGU ? __fmul_rn(a0, x0) : 0.0f;
-          const int next = min(kb + 1, nk - 1);      // the next block's scales, on their way
-          a0 = __ldg(sa + next);
-          w0 = __ldg(sw0 + next);
-          if (kGU) x0 = __ldg(sw0 + to_sw1 + next);
+          if (left > 1) {                            // the next block's scales, on their way
+            a0 = __ldg(p.sa + ++sa);
+            w0 = __ldg(p.sw + ++sw);
+            if (kGU) x0 = __ldg(p.sw + (sw + to_sw1));
+          }
           const uint32_t acc = parts & 3u;
-          wait_lean(bar_tfull(acc), (parts >> 2) & 1u, sbase + S::MISC + 4, kp.status, kp.wait_ns);
+          wait_lean(bar_tfull(acc), (parts >> 2) & 1u, sbase + S::MISC);
           ptx::tc_fence_after();
-          const uint32_t taddr = tmem_lane + acc * 128 + 64 * h;
+          const uint32_t taddr = taddr0 + acc * 128;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t v[16];
@@ -431,9 +461,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           parts += 2;
         }
         // one decision for the sixteen warps
-        if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + 4) == 0)) break;
-        const Tile t = sch.at(tile);                 // anew
-        const int j = f;
+        if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + S::kAbort) == 0)) break;
+        const Ids id(warp, lane);
+        const int e = id.e, h = id.h, set = id.set, f = id.f, et = id.et;
+        const Tile t = sch.at(tile);
+        const int j = f;                             // this thread's row of the tile
         const bool live = j < t.n_tok;
         uint32_t pk[32];                             // the 64 results in bf16
         int d = -1;
@@ -511,27 +543,29 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           for (int i = 0; i < 32; ++i)
             if (col + (i & 16) < p.N) m = fmaxf(m, fabsf(act[i]));        // N % 16 == 0
           const uint32_t s_max = sbase + S::META;    // [4 groups][128 rows]
-          ptx::st_shared_f32(s_max + (grp * 128 + f) * 4, m);
+          ptx::st_shared_f32(s_max + ((2 * set + h) * 128 + f) * 4, m);
           ptx::bar_sync(6, 32 * kEpiWarps);
 #pragma unroll
           for (int i = 0; i < 4; ++i) m = fmaxf(m, ptx::ld_shared_f32(s_max + (i * 128 + f) * 4));
           if (live) {
-            float dd, id;
-            block_scale(m, dd, id);
+            float dd, inv;
+            block_scale(m, dd, inv);
             const size_t r = static_cast<size_t>(t.r0 + j);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float x[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) x[k] = act[16 * i + k];
-              if (col + 16 * i < p.N) *reinterpret_cast<uint4*>(p.act + r * p.N + col + 16 * i) = codes16(x, id);
+              if (col + 16 * i < p.N) *reinterpret_cast<uint4*>(p.act + r * p.N + col + 16 * i) = codes16(x, inv);
             }
-            if (grp == 0) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = dd;
+            if (h + set == 0) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = dd;
           }
         }
         continue;
       }
       // ------------------------------------------------------------ weights tile
+      const Ids id(warp, lane);
+      const int e = id.e, h = id.h, set = id.set, f = id.f, et = id.et, ht = id.ht;
       const Tile t = sch.at(tile);
       const int parity = n_tails++ & 1;
       int* dst_t = reinterpret_cast<int*>(smem + S::META) + parity * kTail;               // plain
@@ -550,12 +584,16 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
 #pragma unroll
       for (int i = 0; i < 32; ++i) sum[i] = 0.0f;
       if (32 * h < t.n_tok) {
+        const int acc_shift = ld_shared_u32(sbase + S::MISC + S::kSmall) ? 3 : 2;
+        const uint32_t acc_mask = (1u << acc_shift) - 1u, acc_cols = 512u >> acc_shift;
         const uint32_t n_arrive = t.n_tok > 32 ? 1 : 2;
         const int wr = kGU ? t.n0 + f + (set == 0 ? p.N : 0) : t.n0 + 128 * set + f;   // this thread's weight row
+        const int rb = blocks_of(kp.rows_per_group);
         const float* sw_p = p.sw + (static_cast<size_t>(t.g) * rb + min(wr / kBlk, rb - 1)) * nk;
         const float* sa_p = p.sa + static_cast<size_t>(t.r0 + min(32 * h + lane, t.n_tok - 1)) * nk;
         const uint32_t fac = sbase + S::FAC + e * 256;
         const bool wide = t.n_tok > 32 * h + 16;
+        const uint32_t taddr0 = id.tmem(tmem_base) + 32 * h;
         float a0 = __ldg(sa_p), w0 = __ldg(sw_p);
         for (int kb = 0; kb < nk; ++kb) {
           const float s = w0;
@@ -565,10 +603,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           a0 = __ldg(sa_p + next);
           w0 = __ldg(sw_p + next);
           const uint32_t acc = parts & acc_mask;
-          wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, sbase + S::MISC + 4, kp.status, kp.wait_ns);
+          wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, sbase + S::MISC);
           ptx::tc_fence_after();
           uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(tmem_lane + acc * acc_cols + 32 * h, v);
+          ptx::tmem_ld_32x32b_x32(taddr0 + acc * acc_cols, v);
           ptx::tmem_ld_wait();
           ptx::tc_fence_before();
           if (lane == 0) ptx::mbar_arrive_n(bar_tempty(acc), n_arrive);
@@ -589,7 +627,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       }
       // one decision for the sixteen warps (and those without rows wait for the others);
       // the barrier also publishes dst_t / w_t
-      if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + 4) == 0)) break;
+      if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + S::kAbort) == 0)) break;
       // 16 rows of the half at a time through its 8 KB of staging: [16 rows][256 weight rows] bf16,
       // 16-byte pieces XOR-swizzled by the row
       const uint32_t ost = sbase + S::EPI + h * 8192;
@@ -657,12 +695,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           if (!in) m = 0.0f;
 #pragma unroll
           for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          float d, id;
-          block_scale(m, d, id);
+          float d, inv;
+          block_scale(m, d, inv);
           if (in && live)
             *reinterpret_cast<uint2*>(p.act + r * p.N + col) = make_uint2(
-                codes4(__fmul_rn(act[0], id), __fmul_rn(act[1], id), __fmul_rn(act[2], id), __fmul_rn(act[3], id)),
-                codes4(__fmul_rn(act[4], id), __fmul_rn(act[5], id), __fmul_rn(act[6], id), __fmul_rn(act[7], id)));
+                codes4(__fmul_rn(act[0], inv), __fmul_rn(act[1], inv), __fmul_rn(act[2], inv), __fmul_rn(act[3], inv)),
+                codes4(__fmul_rn(act[4], inv), __fmul_rn(act[5], inv), __fmul_rn(act[6], inv), __fmul_rn(act[7], inv)));
           if (oct == 0 && live) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = d;
         }
         ptx::bar_sync(1 + h, 256);
