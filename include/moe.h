@@ -807,8 +807,8 @@ enum {
   MOE_KID_ROUTE_BACKWARD = 25,   /* moe_route_backward */
   MOE_KID_ROUTE_LOSSES = 26,     /* moe_route_backward: the losses' last sum */
   MOE_KID_ROUTE_DX = 27,         /* moe_route_logits_backward: grad_x */
-  MOE_KID_ROUTE_DW = 28,         /* moe_route_logits_backward: grad_w_router */
-  MOE_KID_ROUTE_DBIAS = 29,      /* moe_route_logits_backward: grad_bias */
+  MOE_KID_ROUTE_DW = 28,         /* moe_route_logits_backward: grad_w_router and grad_bias */
+  MOE_KID_ROUTE_REDUCE = 29,     /* moe_route_logits_backward: their sums over token ranges */
   MOE_KID_COUNT = 32
 };
 int moe_device_status(int* status_out, int clear);

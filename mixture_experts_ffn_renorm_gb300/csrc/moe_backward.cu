@@ -2,7 +2,8 @@
 //
 // Combine, out[t,:] = rs sum_k w[t,k] eo[t,k,:]:
 //   dw[t,k] = rs <eo[t,k,:], dout[t,:]>,   deo[t,k,:] = (rs w[t,k]) dout[t,:]
-// Router: see moe.h (moe_route_backward, moe_route_logits_backward).
+// Router weights to logits: see moe.h (moe_route_backward).  The products behind
+// the logits are in moe_route_grad.cu.
 #include "moe_common.cuh"
 
 namespace moe {
@@ -297,72 +298,6 @@ route_losses_kernel(const float* __restrict__ partial, int n, float balance, flo
   }
 }
 
-// ------------------------------------------------------------------ router: products
-// C[m,n] = sum_k A[m,k] B[k,n] on the CUDA cores, 64 x 64 tiles, f32 throughout.
-// kDx: A = dl [T,E], B = w_router [E,H], C = grad_x bf16.  Otherwise A = dl^T,
-// B = x [T,H], C = grad_w_router f32.
-template <bool kDx>
-__global__ void __launch_bounds__(256)
-route_gemm_kernel(const float* __restrict__ dl, const uint16_t* __restrict__ b, int M, int N, int Kd,
-                  int E, void* __restrict__ c, unsigned long long* launches) {
-  __shared__ float as[16][65], bs[16][65];
-  count_launch(launches, kDx ? MOE_KID_ROUTE_DX : MOE_KID_ROUTE_DW);
-  grid_dep_wait();
-  grid_dep_launch();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < Kd; k0 += 16) {
-    for (int i = tid; i < 16 * 64; i += 256) {
-      const int k = kDx ? i & 15 : i >> 6, m = kDx ? i >> 4 : i & 63;
-      const bool ok = k0 + k < Kd && m0 + m < M;
-      as[k][m] = ok ? __ldg(dl + (kDx ? static_cast<size_t>(m0 + m) * E + k0 + k
-                                      : static_cast<size_t>(k0 + k) * E + m0 + m)) : 0.0f;
-      const int n = i & 63, kk = i >> 6;
-      bs[kk][n] = k0 + kk < Kd && n0 + n < N
-          ? bf16_bits_to_f32(__ldg(b + static_cast<size_t>(k0 + kk) * N + n0 + n)) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][ty * 4 + i], bs[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m < M && n < N) {
-        if (kDx) static_cast<uint16_t*>(c)[static_cast<size_t>(m) * N + n] = f32_to_bf16_bits(acc[i][j]);
-        else static_cast<float*>(c)[static_cast<size_t>(m) * N + n] = acc[i][j];
-      }
-    }
-}
-
-// column sums of dl: one block per 32 columns, rows strided over its 8 warps
-__global__ void __launch_bounds__(256)
-route_bias_kernel(const float* __restrict__ dl, int T, int E, float* __restrict__ db,
-                  unsigned long long* launches) {
-  __shared__ float red[8][33];
-  count_launch(launches, MOE_KID_ROUTE_DBIAS);
-  grid_dep_wait();
-  grid_dep_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e = blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (e < E)
-    for (int t = warp; t < T; t += 8) s += __ldg(dl + static_cast<size_t>(t) * E + e);
-  red[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && e < E) {
-    float v = 0.0f;
-    for (int i = 0; i < 8; ++i) v += red[i][lane];
-    db[e] = v;
-  }
-}
-
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_dtype(const char* op, const char* what, int dt) {
@@ -472,56 +407,6 @@ int moe_route_backward(const float* logits, const int32_t* topk_ids, const float
                                      static_cast<const float*>(workspace), blocks,
                                      balance_coef * inv_t, z_coef * inv_t, losses, diag.launches),
                        op);
-}
-
-size_t moe_route_logits_backward_workspace_size(int, int, int) { return 0; }
-
-int moe_route_logits_backward(const float* grad_logits, const void* x_bf16, const void* w_router_bf16,
-                              int T, int H, int E, void* grad_x_bf16, float* grad_w_router,
-                              float* grad_bias, void* workspace, size_t ws_bytes, void* stream) {
-  clear_error();
-  const char* op = "moe_route_logits_backward";
-  if (T < 0 || H <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d", op, T, H);
-  if (E < 1 || E > 1024) return set_error(MOE_ERR_ARG, "%s: E=%d outside [1, 1024]", op, E);
-  if (H % 8 != 0) return set_error(MOE_ERR_ALIGN, "%s: H=%d is not a multiple of 8", op, H);
-  if (!grad_x_bf16 && !grad_w_router && !grad_bias)
-    return set_error(MOE_ERR_ARG, "%s: no output requested", op);
-  if (T > 0 && (!grad_logits || (grad_x_bf16 && !w_router_bf16) || (grad_w_router && !x_bf16)))
-    return set_error(MOE_ERR_ARG, "%s: NULL operand", op);
-  if (!aligned16(x_bf16) || !aligned16(w_router_bf16) || !aligned16(grad_x_bf16) ||
-      !aligned16(grad_w_router))
-    return set_error(MOE_ERR_ALIGN, "%s: x, w_router, grad_x and grad_w_router must be 16-byte aligned",
-                     op);
-  if (!aligned4(grad_logits) || !aligned4(grad_bias))
-    return set_error(MOE_ERR_ALIGN, "%s: grad_logits and grad_bias must be 4-byte aligned", op);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T == 0) {   // sums over no token
-    if (grad_w_router &&
-        cudaMemsetAsync(grad_w_router, 0, static_cast<size_t>(E) * H * sizeof(float), s) != cudaSuccess)
-      return check_launch(op);
-    if (grad_bias && cudaMemsetAsync(grad_bias, 0, E * sizeof(float), s) != cudaSuccess)
-      return check_launch(op);
-    return MOE_OK;
-  }
-  if ((T + 63) / 64 > 65535) return set_error(MOE_ERR_ARG, "%s: T=%d is too large", op, T);
-  unsigned long long* launches = device_diag().launches;
-  int rc = MOE_OK;
-  const unsigned nt = static_cast<unsigned>((H + 63) / 64);
-  if (grad_x_bf16)
-    rc = launch_status(launch_kernel(route_gemm_kernel<true>, dim3(nt, (T + 63) / 64), dim3(256), 0, s,
-                                     nullptr, 0, grad_logits, static_cast<const uint16_t*>(w_router_bf16),
-                                     T, H, E, E, grad_x_bf16, launches),
-                       op);
-  if (rc == MOE_OK && grad_w_router)
-    rc = launch_status(launch_kernel(route_gemm_kernel<false>, dim3(nt, (E + 63) / 64), dim3(256), 0, s,
-                                     nullptr, 0, grad_logits, static_cast<const uint16_t*>(x_bf16), E, H,
-                                     T, E, static_cast<void*>(grad_w_router), launches),
-                       op);
-  if (rc == MOE_OK && grad_bias)
-    rc = launch_status(launch_kernel(route_bias_kernel, dim3((E + 31) / 32), dim3(256), 0, s, nullptr, 0,
-                                     grad_logits, T, E, grad_bias, launches),
-                       op);
-  return rc;
 }
 
 }  // extern "C"

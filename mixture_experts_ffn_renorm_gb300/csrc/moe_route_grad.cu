@@ -1,0 +1,594 @@
+// moe_route_grad.cu -- moe_route_logits_backward: the gradients of the router's
+// logits product l = x W^T + bias, given dl [T,E] in f32:
+//   dx[t,:] = sum_e dl[t,e] W[e,:]     dW[e,:] = sum_t dl[t,e] x[t,:]     db[e] = sum_t dl[t,e]
+//
+// x and W are bf16 and dl is f32.  The tensor core multiplies bf16, so dl enters as
+// a sum of bf16 values, dl = hi + mid + lo (8 + 8 + 8 significand bits: exact), and
+// every product is exact in f32.  dW takes all three parts; dx, which is rounded to
+// bf16, takes hi + mid (error 2^-16 of each term).  x and W are read as they lie in
+// memory: their contiguous dimension is an output dimension of both products, so
+// they go to the tensor core as MN-major operands straight from TMA boxes.
+//
+// The floor is the bytes: x read and dx written once (67 MB at T = 8192, H = 2048,
+// E = 128: 9.9 us), against 4 + 6 FLOP per element and expert on the tensor core
+// (21 GFLOP: 12 us of it at most).
+//
+//   dW  CTA: 128 experts x 128 columns of H x a range of tokens, 64 tokens a step.
+//       Eight warps load dl, split it and write the three parts as MN-major operand
+//       tiles; a ninth loads x by TMA and issues the MMAs.  hi is summed in one
+//       accumulator and mid + lo in another; after 1024 tokens both are added to the
+//       CTA's f32 sums in memory, so no chain of tensor-core additions is longer than
+//       128.  The ranges' sums go to the workspace and a second kernel adds them in
+//       range order.  The CTAs of the first column block also sum dl for db.
+//   dx  CTA: 128 tokens x 256 columns of H, 64 experts a step; dl is split into two
+//       K-major operand tiles.  Two CTAs share an SM and fill each other's gaps.
+#include <atomic>
+
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace rgrad {
+namespace {
+
+constexpr int kConv = 256;              // converting (and epilogue) threads: warps 0-7
+constexpr int kThreads = kConv + 32;    // warp 8: TMA and MMA
+constexpr int kStepT = 64;              // tokens per step of dW
+constexpr int kChunk = 16;              // steps between two additions to memory
+constexpr int kBlk = 64 * 128;          // one operand block: 64 K rows (or 64 rows) of 128 bytes
+
+struct WsLimits {
+  unsigned long long wait_ns;
+  unsigned int* status;
+};
+
+// hi, mid and lo of 8 values, packed; a value that is not finite is all in hi
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
+  uint32_t h[4], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = v[2 * i], b = v[2 * i + 1];
+    h[i] = gemm::pack_bf16x2(a, b);
+    const float ha = __uint_as_float(h[i] << 16), hb = __uint_as_float(h[i] & 0xFFFF0000u);
+    const float ra = fabsf(ha) < INFINITY ? __fsub_rn(a, ha) : 0.0f;   // exact
+    const float rb = fabsf(hb) < INFINITY ? __fsub_rn(b, hb) : 0.0f;
+    m[i] = gemm::pack_bf16x2(ra, rb);
+    l[i] = gemm::pack_bf16x2(__fsub_rn(ra, __uint_as_float(m[i] << 16)),
+                             __fsub_rn(rb, __uint_as_float(m[i] & 0xFFFF0000u)));
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  mid = make_uint4(m[0], m[1], m[2], m[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// dl[t, e0 .. e0 + 7], zeros outside [0,T) x [0,E); whole vectors when the row allows it
+__device__ __forceinline__ void load_dl8(const float* __restrict__ dl, int t, int e0, int T, int E,
+                                         bool vec, float (&v)[8]) {
+  const float* p = dl + static_cast<size_t>(t) * E + e0;
+  if (t < T && vec && e0 + 8 <= E) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = t < T && e0 + i < E ? __ldg(p + i) : 0.0f;
+  }
+}
+
+// Bounded wait of any thread; false once it gives up (the status is raised and the
+// CTA's abort flag set).
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                     const WsLimits& lim) {
+  return gemm::wait_bar(bar, parity, abort_flag, lim.status, lim.wait_ns);
+}
+
+// ------------------------------------------------------------------ dW
+struct DwSmem {
+  static constexpr int A = 0;                          // 2 stages x 3 parts x 2 blocks of 64 experts
+  static constexpr int B = A + 2 * 6 * kBlk;           // 2 stages x 2 blocks of 64 columns
+  static constexpr int DB = B + 2 * 2 * kBlk;          // db: [2 token halves][128] f32
+  static constexpr int BARS = DB + 16 * 128 * 4;       // fullA, fullB, empty [2], done
+  static constexpr int MISC = BARS + 64;
+  static constexpr int ALLOC = MISC + 16 + 1024;
+};
+
+struct DwParams {
+  const float* dl;
+  int T, H, E, steps;          // steps of 64 tokens per range
+  float* out;                  // [ranges][E][H] or null (db alone)
+  float* db;                   // [ranges][E] or null
+  WsLimits lim;
+  unsigned long long* launches;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
+  using S = DwSmem;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = ptx::smem_u32(smem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto full_a = [&](int s) { return sb + S::BARS + 8u * s; };
+  auto full_b = [&](int s) { return sb + S::BARS + 16 + 8u * s; };
+  auto empty = [&](int s) { return sb + S::BARS + 32 + 8u * s; };
+  const uint32_t done = sb + S::BARS + 48;
+  count_launch(p.launches, MOE_KID_ROUTE_DW);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(full_a(s), kConv);
+      ptx::mbar_init(full_b(s), 1);
+      ptx::mbar_init(empty(s), 1);
+    }
+    ptx::mbar_init(done, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) ptx::tma_prefetch_desc(&tmX);
+  // Tensor memory is taken after the wait and before the next kernel may start: these CTAs
+  // share SMs, and none that waits for another kernel holds what that kernel needs.
+  grid_dep_wait();
+  if (warp == 8) {
+    ptx::tmem_alloc(sb + S::MISC, 256);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  grid_dep_launch();
+  const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + S::MISC);
+  const int h0 = blockIdx.x * 128, e0 = blockIdx.y * 128;
+  const size_t range = blockIdx.z;
+  const int t0 = static_cast<int>(range) * p.steps * kStepT;
+  const int steps = min(p.steps, (p.T - t0 + kStepT - 1) / kStepT);
+  const bool mul = p.out != nullptr;
+  uint32_t issued = 0;
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA and MMA
+    if (mul && ptx::elect_one()) {
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32_mn(128, 128, true, true);
+      auto load = [&](int i) {
+        ptx::mbar_arrive_expect_tx(full_b(i & 1), 2 * kBlk);
+        for (int b = 0; b < 2; ++b)
+          ptx::tma_load_2d(sb + S::B + ((i & 1) * 2 + b) * kBlk, &tmX, h0 + 64 * b, t0 + i * kStepT, full_b(i & 1));
+      };
+      bool ok = true;
+      load(0);
+      ++issued;
+      for (int i = 0; ok && i < steps; ++i) {
+        const int s = i & 1;
+        if (i + 1 < steps) {   // the next step's x, once the MMAs that read its stage are done
+          ok = i == 0 || wait(empty(s ^ 1), ((i - 1) >> 1) & 1, abort_flag, p.lim);
+          if (!ok) break;
+          load(i + 1);
+          ++issued;
+        }
+        ok = wait(full_b(s), (i >> 1) & 1, abort_flag, p.lim) && wait(full_a(s), (i >> 1) & 1, abort_flag, p.lim);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint64_t db = ptx::desc_mnmajor_sw128(sb + S::B + s * 2 * kBlk, kBlk);
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const uint64_t da = ptx::desc_mnmajor_sw128(sb + S::A + (s * 6 + part * 2) * kBlk, kBlk);
+#pragma unroll
+          for (int k = 0; k < kStepT / 16; ++k)   // a fresh sum per chunk of steps; mid and lo share one
+            ptx::mma_bf16(tmem + (part ? 128u : 0u), da + 128ull * k, db + 128ull * k, idesc,
+                          i % kChunk != 0 || k != 0 || part == 2 ? 1u : 0u);
+        }
+        ptx::mma_commit(empty(s));
+        if (i % kChunk == kChunk - 1 || i == steps - 1) {
+          ptx::mma_commit(done);
+          // the epilogue reads the accumulators before the next chunk's first MMA: it arrives on
+          // that step's full barrier only afterwards
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ conversion and epilogue
+    const int o = threadIdx.x & 15, r = threadIdx.x >> 4;      // 8 experts of the 128, token of 16
+    const int e = e0 + 8 * o;
+    const bool vec = (p.E & 3) == 0 && (reinterpret_cast<uintptr_t>(p.dl) & 15) == 0;
+    // this thread's 16 bytes of row t of a block of 64 experts, swizzled by the row
+    const uint32_t at = (o >> 3) * kBlk + (((o & 7) ^ (r & 7)) << 4);
+    float colsum[8] = {};
+    bool ok = true;   // a thread that gives up still meets the others at the chunks' ends
+    for (int i = 0; i < steps; ++i) {
+      const int s = i & 1;
+      float v[4][8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load_dl8(p.dl, t0 + i * kStepT + r + 16 * j, e, p.T, p.E, vec, v[j]);
+      if (p.db && blockIdx.x == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) colsum[k] += v[j][k];
+      }
+      if (!mul) continue;
+      if (ok && i >= 2 && !wait(empty(s), ((i - 2) >> 1) & 1, abort_flag, p.lim)) ok = false;
+      if (ok) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 x[3];
+          split8(v[j], x[0], x[1], x[2]);
+          const uint32_t dst = sb + S::A + s * 6 * kBlk + at + (r + 16 * j) * 128;
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+            ptx::st_shared_v4(dst + part * 2 * kBlk, x[part].x, x[part].y, x[part].z, x[part].w);
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(full_a(s));
+      }
+      // the end of a chunk: its sums to memory, before the next chunk's first operands are announced
+      if (i % kChunk == kChunk - 1 || i == steps - 1) {
+        if (ok && !wait(done, (i / kChunk) & 1, abort_flag, p.lim)) ok = false;
+        if (!ptx::bar_and(1, kConv, ok)) break;
+        ptx::tc_fence_after();
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (warp >> 2) * 64;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t a[32], b[32];
+          ptx::tmem_ld_32x32b_x32(ta + 32 * c, a);
+          ptx::tmem_ld_32x32b_x32(ta + 128 + 32 * c, b);
+          ptx::tmem_ld_wait();
+          const int h = h0 + (warp >> 2) * 64 + 32 * c;
+          if (e0 + row < p.E) {
+            float4* out = reinterpret_cast<float4*>(p.out + (range * p.E + e0 + row) * p.H + h);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (h + 4 * k < p.H) {               // H % 8 == 0
+                float4 y;
+                y.x = __uint_as_float(a[4 * k]) + __uint_as_float(b[4 * k]);
+                y.y = __uint_as_float(a[4 * k + 1]) + __uint_as_float(b[4 * k + 1]);
+                y.z = __uint_as_float(a[4 * k + 2]) + __uint_as_float(b[4 * k + 2]);
+                y.w = __uint_as_float(a[4 * k + 3]) + __uint_as_float(b[4 * k + 3]);
+                if (i >= kChunk) {                 // this thread wrote the chunks before
+                  const float4 z = out[k];
+                  y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+                }
+                out[k] = y;
+              }
+            }
+          }
+        }
+        ptx::tc_fence_before();
+        ptx::bar_sync(1, kConv);   // every warp has read the accumulators
+        ptx::tc_fence_after();
+      }
+    }
+    if (p.db && blockIdx.x == 0) {
+      // the 16 threads of an expert octet, in row order
+      float* red = reinterpret_cast<float*>(smem + S::DB);     // [16][128]
+#pragma unroll
+      for (int k = 0; k < 8; ++k) red[r * 128 + 8 * o + k] = colsum[k];
+      ptx::bar_sync(1, kConv);
+      if (threadIdx.x < 128 && e0 + static_cast<int>(threadIdx.x) < p.E) {
+        float sum = 0.0f;
+        for (int k = 0; k < 16; ++k) sum += red[k * 128 + threadIdx.x];
+        p.db[range * p.E + e0 + threadIdx.x] = sum;
+      }
+    }
+  }
+  // ---- exit: a CTA that gave up drains its copies and MMAs first
+  __syncthreads();
+  if (*abort_flag != 0 && issued != 0) {
+    ptx::mma_commit(done);
+    const uint64_t g0 = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - g0 < 100000ull) {
+    }
+    for (uint32_t i = issued < 2 ? 0 : issued - 2; i < issued; ++i)
+      gemm::spin_bounded(full_b(i & 1), (i >> 1) & 1);
+  }
+  __syncthreads();
+  if (warp == 8) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 256);
+  }
+}
+
+// the ranges' sums in range order: dW as vectors of four, then db
+__global__ void __launch_bounds__(256)
+route_reduce_kernel(const float* __restrict__ part_w, const float* __restrict__ part_b, int ranges,
+                    long long n4, int E, float* __restrict__ dw, float* __restrict__ db,
+                    unsigned long long* launches) {
+  count_launch(launches, MOE_KID_ROUTE_REDUCE);
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (dw && i < n4) {
+    const float4* p = reinterpret_cast<const float4*>(part_w) + i;
+    float4 s = p[0];
+    for (int r = 1; r < ranges; ++r) {
+      const float4 v = p[r * n4];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    reinterpret_cast<float4*>(dw)[i] = s;
+  }
+  if (db && i < E) {
+    float s = part_b[i];
+    for (int r = 1; r < ranges; ++r) s += part_b[static_cast<size_t>(r) * E + i];
+    db[i] = s;
+  }
+}
+
+// ------------------------------------------------------------------ dx
+struct DxSmem {
+  static constexpr int A = 0;                          // 2 parts x 128 tokens x 128 bytes (64 experts)
+  static constexpr int B = A + 2 * 2 * kBlk;           // 4 blocks of 64 columns x 64 experts
+  static constexpr int BARS = B + 4 * kBlk;            // fullA, fullB, done
+  static constexpr int MISC = BARS + 32;
+  static constexpr int ALLOC = MISC + 16 + 1024;
+};
+
+struct DxParams {
+  const float* dl;
+  int T, H, E;
+  uint16_t* dx;
+  WsLimits lim;
+  unsigned long long* launches;
+};
+
+__global__ void __launch_bounds__(kThreads, 2)
+route_dx_kernel(const __grid_constant__ CUtensorMap tmW, const DxParams p) {
+  using S = DxSmem;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = ptx::smem_u32(smem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t full_a = sb + S::BARS, full_b = sb + S::BARS + 8, done = sb + S::BARS + 16;
+  count_launch(p.launches, MOE_KID_ROUTE_DX);
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(full_a, kConv);
+    ptx::mbar_init(full_b, 1);
+    ptx::mbar_init(done, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) ptx::tma_prefetch_desc(&tmW);
+  // Tensor memory is taken after the wait and before the next kernel may start: these CTAs
+  // share SMs, and none that waits for another kernel holds what that kernel needs.
+  grid_dep_wait();
+  if (warp == 8) {
+    ptx::tmem_alloc(sb + S::MISC, 256);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  grid_dep_launch();
+  const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + S::MISC);
+  const int h0 = blockIdx.x * 256, t0 = blockIdx.y * 128;
+  const int steps = (p.E + 63) / 64;
+  uint32_t issued = 0;
+  if (warp == 8) {
+    if (ptx::elect_one()) {
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32_mn(128, 256, false, true);
+      bool ok = true;
+      for (int i = 0; ok && i < steps; ++i) {
+        // the step before has been multiplied: its operands may be overwritten
+        ok = i == 0 || wait(done, (i - 1) & 1, abort_flag, p.lim);
+        if (!ok) break;
+        ptx::mbar_arrive_expect_tx(full_b, 4 * kBlk);
+        for (int b = 0; b < 4; ++b)
+          ptx::tma_load_2d(sb + S::B + b * kBlk, &tmW, h0 + 64 * b, 64 * i, full_b);
+        ++issued;
+        ok = wait(full_b, i & 1, abort_flag, p.lim) && wait(full_a, i & 1, abort_flag, p.lim);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint64_t db = ptx::desc_mnmajor_sw128(sb + S::B, kBlk);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint64_t da = ptx::desc_kmajor_sw128(sb + S::A + part * 2 * kBlk);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ptx::mma_bf16(tmem, da + 2ull * k, db + 128ull * k, idesc, (i | part | k) != 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(done);
+      }
+    }
+  } else {
+    const int o = threadIdx.x & 7, r = threadIdx.x >> 3;       // 8 experts of 64, token of 32
+    const bool vec = (p.E & 3) == 0 && (reinterpret_cast<uintptr_t>(p.dl) & 15) == 0;
+    bool ok = true;
+    for (int i = 0; ok && i < steps; ++i) {
+      float v[4][8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load_dl8(p.dl, t0 + r + 32 * j, 64 * i + 8 * o, p.T, p.E, vec, v[j]);
+      if (i > 0 && !wait(done, (i - 1) & 1, abort_flag, p.lim)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 hi, mid, lo;
+        split8(v[j], hi, mid, lo);
+        const int row = r + 32 * j;
+        const uint32_t dst = sb + S::A + row * 128 + ((o ^ (row & 7)) << 4);
+        ptx::st_shared_v4(dst, hi.x, hi.y, hi.z, hi.w);
+        ptx::st_shared_v4(dst + 2 * kBlk, mid.x, mid.y, mid.z, mid.w);
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(full_a);
+    }
+    if (ok && !wait(done, (steps - 1) & 1, abort_flag, p.lim)) ok = false;
+    if (ptx::bar_and(1, kConv, ok)) {
+      // [128 tokens][256 columns] bf16 through the operands' memory: 512 bytes a row, 16-byte
+      // pieces XOR-swizzled by the row; then a warp stores one row at a time
+      ptx::tc_fence_after();
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (warp >> 2) * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t a[32];
+        ptx::tmem_ld_32x32b_x32(ta + 32 * c, a);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int piece = (warp >> 2) * 16 + 4 * c + k;
+          uint32_t w[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            w[m] = gemm::pack_bf16x2(__uint_as_float(a[8 * k + 2 * m]), __uint_as_float(a[8 * k + 2 * m + 1]));
+          ptx::st_shared_v4(sb + row * 512 + ((piece ^ (row & 31)) << 4), w[0], w[1], w[2], w[3]);
+        }
+      }
+      ptx::tc_fence_before();
+      ptx::bar_sync(1, kConv);
+      for (int j = warp; j < 128; j += 8) {
+        const int t = t0 + j, h = h0 + 8 * lane;
+        if (t < p.T && h < p.H)
+          *reinterpret_cast<uint4*>(p.dx + static_cast<size_t>(t) * p.H + h) =
+              ptx::ld_shared_v4(sb + j * 512 + ((lane ^ (j & 31)) << 4));
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort_flag != 0 && issued != 0) {
+    ptx::mma_commit(done);
+    const uint64_t g0 = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - g0 < 100000ull) {
+    }
+    gemm::spin_bounded(full_b, (issued - 1) & 1);
+  }
+  __syncthreads();
+  if (warp == 8) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 256);
+  }
+}
+
+static_assert(DxSmem::ALLOC * 2 <= 227 * 1024, "two dx CTAs per SM");
+static_assert(DwSmem::ALLOC <= 227 * 1024, "shared memory");
+
+// steps of 64 tokens per range: enough ranges to give every SM a CTA, but at least two
+// steps in each, since a range costs a pass over its [E,H] sums
+struct Ranges {
+  int steps, count;
+};
+Ranges ranges_of(int T, int H, int E) {
+  const int total = (T + kStepT - 1) / kStepT;
+  const int tiles = ((H + 127) / 128) * ((E + 127) / 128);
+  int want = sm_count() / tiles;
+  if (want > (total + 1) / 2) want = (total + 1) / 2;
+  if (want > 32) want = 32;
+  if (want < 1) want = 1;
+  Ranges r;
+  r.steps = (total + want - 1) / want;
+  r.count = (total + r.steps - 1) / r.steps;
+  return r;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <typename K>
+int reserve(const char* op, K kern, int smem, std::atomic<int>* ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    dev = -1;
+  }
+  const bool cache = dev >= 0 && dev < 64;
+  if (cache && ready[dev].load(std::memory_order_acquire)) return MOE_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "%s: cannot reserve %d bytes of shared memory: %s", op, smem,
+                     cudaGetErrorString(cudaGetLastError()));
+  if (cache) ready[dev].store(1, std::memory_order_release);
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace rgrad
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::rgrad;
+
+extern "C" {
+
+size_t moe_route_logits_backward_workspace_size(int T, int H, int E) {
+  if (T <= 0 || H <= 0 || E <= 0) return 0;
+  const Ranges r = ranges_of(T, H, E);
+  if (r.count == 1) return 0;
+  return static_cast<size_t>(r.count) * E * (static_cast<size_t>(H) + 1) * sizeof(float);
+}
+
+int moe_route_logits_backward(const float* grad_logits, const void* x_bf16, const void* w_router_bf16,
+                              int T, int H, int E, void* grad_x_bf16, float* grad_w_router,
+                              float* grad_bias, void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  const char* op = "moe_route_logits_backward";
+  if (T < 0 || H <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d", op, T, H);
+  if (E < 1 || E > 1024) return set_error(MOE_ERR_ARG, "%s: E=%d outside [1, 1024]", op, E);
+  if (H % 8 != 0) return set_error(MOE_ERR_ALIGN, "%s: H=%d is not a multiple of 8", op, H);
+  if (!grad_x_bf16 && !grad_w_router && !grad_bias)
+    return set_error(MOE_ERR_ARG, "%s: no output requested", op);
+  if (T > 0 && (!grad_logits || (grad_x_bf16 && !w_router_bf16) || (grad_w_router && !x_bf16)))
+    return set_error(MOE_ERR_ARG, "%s: NULL operand", op);
+  if (!aligned16(x_bf16) || !aligned16(w_router_bf16) || !aligned16(grad_x_bf16) ||
+      !aligned16(grad_w_router))
+    return set_error(MOE_ERR_ALIGN, "%s: x, w_router, grad_x and grad_w_router must be 16-byte aligned",
+                     op);
+  if (!aligned4(grad_logits) || !aligned4(grad_bias))
+    return set_error(MOE_ERR_ALIGN, "%s: grad_logits and grad_bias must be 4-byte aligned", op);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {   // sums over no token
+    if (grad_w_router &&
+        cudaMemsetAsync(grad_w_router, 0, static_cast<size_t>(E) * H * sizeof(float), s) != cudaSuccess)
+      return check_launch(op);
+    if (grad_bias && cudaMemsetAsync(grad_bias, 0, E * sizeof(float), s) != cudaSuccess)
+      return check_launch(op);
+    return MOE_OK;
+  }
+  if ((T + 127) / 128 > 65535) return set_error(MOE_ERR_ARG, "%s: T=%d is too large", op, T);
+  const bool sums = grad_w_router || grad_bias;
+  const Ranges rg = ranges_of(T, H, E);
+  if (sums && rg.count > 1) {
+    if (!workspace || ws_bytes < moe_route_logits_backward_workspace_size(T, H, E))
+      return set_error(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", op, ws_bytes,
+                       moe_route_logits_backward_workspace_size(T, H, E));
+    if (!aligned16(workspace)) return set_error(MOE_ERR_ALIGN, "%s: workspace must be 16-byte aligned", op);
+  }
+  DeviceDiag diag = device_diag();
+  const WsLimits lim{gemm::pipeline_wait_ns(), diag.status};
+  static std::atomic<int> ready_dx[64] = {}, ready_dw[64] = {};
+  int rc;
+  if (sums) {
+    if ((rc = reserve(op, route_dw_kernel, DwSmem::ALLOC, ready_dw)) != MOE_OK) return rc;
+    CUtensorMap tm{};
+    if (grad_w_router && (rc = gemm::make_tmap(&tm, x_bf16, T, H, kStepT, op, "x")) != MOE_OK) return rc;
+    float* part_w = rg.count > 1 ? static_cast<float*>(workspace) : grad_w_router;
+    float* part_b = rg.count > 1 ? static_cast<float*>(workspace) + static_cast<size_t>(rg.count) * E * H : grad_bias;
+    DwParams p{grad_logits, T, H, E, rg.steps, grad_w_router ? part_w : nullptr,
+               grad_bias ? part_b : nullptr, lim, diag.launches};
+    rc = launch_status(launch_kernel(route_dw_kernel,
+                                     dim3(grad_w_router ? (H + 127) / 128 : 1, (E + 127) / 128, rg.count),
+                                     dim3(kThreads), DwSmem::ALLOC, s, nullptr, 0, tm, p),
+                       op);
+    if (rc != MOE_OK) return rc;
+    if (rg.count > 1) {
+      const long long n4 = static_cast<long long>(E) * H / 4;
+      const long long n = grad_w_router ? (n4 > E ? n4 : E) : E;
+      rc = launch_status(launch_kernel(route_reduce_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256),
+                                       0, s, nullptr, 0, static_cast<const float*>(part_w),
+                                       static_cast<const float*>(part_b), rg.count, n4, E, grad_w_router,
+                                       grad_bias, diag.launches),
+                         op);
+      if (rc != MOE_OK) return rc;
+    }
+  }
+  if (grad_x_bf16) {
+    if ((rc = reserve(op, route_dx_kernel, DxSmem::ALLOC, ready_dx)) != MOE_OK) return rc;
+    CUtensorMap tm;
+    if ((rc = gemm::make_tmap(&tm, w_router_bf16, E, H, 64, op, "w_router")) != MOE_OK) return rc;
+    DxParams p{grad_logits, T, H, E, static_cast<uint16_t*>(grad_x_bf16), lim, diag.launches};
+    rc = launch_status(launch_kernel(route_dx_kernel, dim3((H + 255) / 256, (T + 127) / 128), dim3(kThreads),
+                                     DxSmem::ALLOC, s, nullptr, 0, tm, p),
+                       op);
+  }
+  return rc;
+}
+
+}  // extern "C"

@@ -394,6 +394,15 @@ __device__ __forceinline__ uint64_t desc_kmajor_sw128(uint32_t smem_addr) {
   return d;
 }
 
+// The same of an MN-major operand (the 16-bit values of one K row contiguous), as TMA
+// SWIZZLE_128B boxes of 64 values x rows write it: blocks of 64 values `lbo` bytes apart
+// (leading byte offset), groups of 8 K rows 1024 bytes apart (stride byte offset).  16 K
+// rows on is 2048 bytes on.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = desc_kmajor_sw128(smem_addr) & ~(static_cast<uint64_t>(0x3FFFu) << 16);
+  return d | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16: f32 accumulator (bits 4-5
 // = 1), A and B bf16 (bits 7-9 and 10-12 = 1), both K-major (bits 15, 16 = 0),
 // N >> 3 in bits 17-22, M >> 4 in bits 24-28.
@@ -402,6 +411,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// with an MN-major A (bit 15) or B (bit 16)
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_mn(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_bf16_f32(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
 // The same for kind::f8f6f4: f32 accumulator, A and B E4M3 (format 0), both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
