@@ -16,9 +16,11 @@
 //   dW  CTA: 128 experts x 128 columns of H x a range of tokens, 64 tokens a step.
 //       Eight warps load dl, split it and write the three parts as MN-major operand
 //       tiles; a ninth loads x by TMA and issues the MMAs.  hi is summed in one
-//       accumulator and mid + lo in another; after 1024 tokens both are added to the
-//       CTA's f32 sums in memory, so no chain of tensor-core additions is longer than
-//       128.  The ranges' sums go to the workspace and a second kernel adds them in
+//       accumulator and mid + lo in another; every 256 tokens both are added to f32 sums
+//       in registers while a second pair of accumulators fills, so no chain of
+//       tensor-core additions (which may truncate) is longer than 32.  (With chains of
+//       1024 tokens dW was more than 1.5 times as far from the 64-bit result as an f32
+//       product.)  The ranges' sums go to the workspace and a second kernel adds them in
 //       range order.  The CTAs of the first column block also sum dl for db.
 //   dx  CTA: 128 tokens x 256 columns of H, 64 experts a step; dl is split into two
 //       K-major operand tiles.  Two CTAs share an SM and fill each other's gaps.
@@ -33,7 +35,7 @@ namespace {
 constexpr int kConv = 256;              // converting (and epilogue) threads: warps 0-7
 constexpr int kThreads = kConv + 32;    // warp 8: TMA and MMA
 constexpr int kStepT = 64;              // tokens per step of dW
-constexpr int kChunk = 16;              // steps between two additions to memory
+constexpr int kChunk = 4;               // steps between two additions to the f32 sums
 constexpr int kBlk = 64 * 128;          // one operand block: 64 K rows (or 64 rows) of 128 bytes
 
 struct WsLimits {
@@ -87,7 +89,7 @@ struct DwSmem {
   static constexpr int A = 0;                          // 2 stages x 3 parts x 2 blocks of 64 experts
   static constexpr int B = A + 2 * 6 * kBlk;           // 2 stages x 2 blocks of 64 columns
   static constexpr int DB = B + 2 * 2 * kBlk;          // db: [2 token halves][128] f32
-  static constexpr int BARS = DB + 16 * 128 * 4;       // fullA, fullB, empty [2], done
+  static constexpr int BARS = DB + 16 * 128 * 4;       // fullA, fullB, empty, done [2]
   static constexpr int MISC = BARS + 64;
   static constexpr int ALLOC = MISC + 16 + 1024;
 };
@@ -113,7 +115,7 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
   auto full_a = [&](int s) { return sb + S::BARS + 8u * s; };
   auto full_b = [&](int s) { return sb + S::BARS + 16 + 8u * s; };
   auto empty = [&](int s) { return sb + S::BARS + 32 + 8u * s; };
-  const uint32_t done = sb + S::BARS + 48;
+  auto done = [&](int a) { return sb + S::BARS + 48 + 8u * a; };
   count_launch(p.launches, MOE_KID_ROUTE_DW);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -121,7 +123,7 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
       ptx::mbar_init(full_b(s), 1);
       ptx::mbar_init(empty(s), 1);
     }
-    ptx::mbar_init(done, 1);
+    for (int a = 0; a < 2; ++a) ptx::mbar_init(done(a), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -130,7 +132,7 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
   // share SMs, and none that waits for another kernel holds what that kernel needs.
   grid_dep_wait();
   if (warp == 8) {
-    ptx::tmem_alloc(sb + S::MISC, 256);
+    ptx::tmem_alloc(sb + S::MISC, 512);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -173,15 +175,11 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
           const uint64_t da = ptx::desc_mnmajor_sw128(sb + S::A + (s * 6 + part * 2) * kBlk, kBlk);
 #pragma unroll
           for (int k = 0; k < kStepT / 16; ++k)   // a fresh sum per chunk of steps; mid and lo share one
-            ptx::mma_bf16(tmem + (part ? 128u : 0u), da + 128ull * k, db + 128ull * k, idesc,
+            ptx::mma_bf16(tmem + ((i / kChunk) & 1) * 256u + (part ? 128u : 0u), da + 128ull * k, db + 128ull * k, idesc,
                           i % kChunk != 0 || k != 0 || part == 2 ? 1u : 0u);
         }
         ptx::mma_commit(empty(s));
-        if (i % kChunk == kChunk - 1 || i == steps - 1) {
-          ptx::mma_commit(done);
-          // the epilogue reads the accumulators before the next chunk's first MMA: it arrives on
-          // that step's full barrier only afterwards
-        }
+        if (i % kChunk == kChunk - 1 || i == steps - 1) ptx::mma_commit(done((i / kChunk) & 1));
       }
     }
   } else {
@@ -192,7 +190,29 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
     // this thread's 16 bytes of row t of a block of 64 experts, swizzled by the row
     const uint32_t at = (o >> 3) * kBlk + (((o & 7) ^ (r & 7)) << 4);
     float colsum[8] = {};
+    float sum[64];                 // expert e0 + TMEM lane, columns 64 (warp / 4) + 0 .. 63
+#pragma unroll
+    for (int k = 0; k < 64; ++k) sum[k] = 0.0f;
     bool ok = true;   // a thread that gives up still meets the others at the chunks' ends
+    // adds chunk c's accumulators to the sums; the issuer takes them again two chunks on, after
+    // this thread's arrive on that chunk's first operands
+    auto take = [&](int c) {
+      if (ok && !wait(done(c & 1), (c >> 1) & 1, abort_flag, p.lim)) ok = false;
+      ok = ptx::bar_and(1, kConv, ok);
+      if (!ok) return;
+      ptx::tc_fence_after();
+      const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (c & 1) * 256 + (warp >> 2) * 64;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a[16], b[16];
+        ptx::tmem_ld_32x32b_x16(ta + 16 * k, a);
+        ptx::tmem_ld_32x32b_x16(ta + 128 + 16 * k, b);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[16 * k + j] += __uint_as_float(a[j]) + __uint_as_float(b[j]);
+      }
+      ptx::tc_fence_before();
+    };
     for (int i = 0; i < steps; ++i) {
       const int s = i & 1;
       float v[4][8];
@@ -219,42 +239,21 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(full_a(s));
       }
-      // the end of a chunk: its sums to memory, before the next chunk's first operands are announced
-      if (i % kChunk == kChunk - 1 || i == steps - 1) {
-        if (ok && !wait(done, (i / kChunk) & 1, abort_flag, p.lim)) ok = false;
-        if (!ptx::bar_and(1, kConv, ok)) break;
-        ptx::tc_fence_after();
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (warp >> 2) * 64;
+      // the chunk before, while this one is multiplied
+      if (i % kChunk == 0 && i > 0) {
+        take(i / kChunk - 1);
+        if (!ok) break;            // all of them
+      }
+    }
+    if (mul && ok) take((steps - 1) / kChunk);
+    if (mul && ok) {
+      const int row = (warp & 3) * 32 + lane, h = h0 + (warp >> 2) * 64;
+      if (e0 + row < p.E) {
+        float4* out = reinterpret_cast<float4*>(p.out + (range * p.E + e0 + row) * p.H + h);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t a[32], b[32];
-          ptx::tmem_ld_32x32b_x32(ta + 32 * c, a);
-          ptx::tmem_ld_32x32b_x32(ta + 128 + 32 * c, b);
-          ptx::tmem_ld_wait();
-          const int h = h0 + (warp >> 2) * 64 + 32 * c;
-          if (e0 + row < p.E) {
-            float4* out = reinterpret_cast<float4*>(p.out + (range * p.E + e0 + row) * p.H + h);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (h + 4 * k < p.H) {               // H % 8 == 0
-                float4 y;
-                y.x = __uint_as_float(a[4 * k]) + __uint_as_float(b[4 * k]);
-                y.y = __uint_as_float(a[4 * k + 1]) + __uint_as_float(b[4 * k + 1]);
-                y.z = __uint_as_float(a[4 * k + 2]) + __uint_as_float(b[4 * k + 2]);
-                y.w = __uint_as_float(a[4 * k + 3]) + __uint_as_float(b[4 * k + 3]);
-                if (i >= kChunk) {                 // this thread wrote the chunks before
-                  const float4 z = out[k];
-                  y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
-                }
-                out[k] = y;
-              }
-            }
-          }
-        }
-        ptx::tc_fence_before();
-        ptx::bar_sync(1, kConv);   // every warp has read the accumulators
-        ptx::tc_fence_after();
+        for (int k = 0; k < 16; ++k)
+          if (h + 4 * k < p.H)     // H % 8 == 0
+            out[k] = make_float4(sum[4 * k], sum[4 * k + 1], sum[4 * k + 2], sum[4 * k + 3]);
       }
     }
     if (p.db && blockIdx.x == 0) {
@@ -273,7 +272,7 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
   // ---- exit: a CTA that gave up drains its copies and MMAs first
   __syncthreads();
   if (*abort_flag != 0 && issued != 0) {
-    ptx::mma_commit(done);
+    ptx::mma_commit(done(0));
     const uint64_t g0 = ptx::globaltimer_ns();
     while (ptx::globaltimer_ns() - g0 < 100000ull) {
     }
@@ -283,7 +282,7 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
   __syncthreads();
   if (warp == 8) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 256);
+    ptx::tmem_dealloc(tmem, 512);
   }
 }
 
