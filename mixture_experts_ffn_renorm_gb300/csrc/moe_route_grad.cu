@@ -213,11 +213,20 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
       }
       ptx::tc_fence_before();
     };
+    float next[4][8];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load_dl8(p.dl, t0 + i * kStepT + r + 16 * j, e, p.T, p.E, vec, next[j]);
+    };
+    fetch(0);
     for (int i = 0; i < steps; ++i) {
       const int s = i & 1;
       float v[4][8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load_dl8(p.dl, t0 + i * kStepT + r + 16 * j, e, p.T, p.E, vec, v[j]);
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[j][k] = next[j][k];
+      if (i + 1 < steps) fetch(i + 1);   // on its way while this step is split
       if (p.db && blockIdx.x == 0) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -392,10 +401,19 @@ route_dx_kernel(const __grid_constant__ CUtensorMap tmW, const DxParams p) {
     const int o = threadIdx.x & 7, r = threadIdx.x >> 3;       // 8 experts of 64, token of 32
     const bool vec = (p.E & 3) == 0 && (reinterpret_cast<uintptr_t>(p.dl) & 15) == 0;
     bool ok = true;
+    float next[4][8];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load_dl8(p.dl, t0 + r + 32 * j, 64 * i + 8 * o, p.T, p.E, vec, next[j]);
+    };
+    fetch(0);
     for (int i = 0; ok && i < steps; ++i) {
       float v[4][8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load_dl8(p.dl, t0 + r + 32 * j, 64 * i + 8 * o, p.T, p.E, vec, v[j]);
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[j][k] = next[j][k];
+      if (i + 1 < steps) fetch(i + 1);   // on its way while this step is split
       if (i > 0 && !wait(done, (i - 1) & 1, abort_flag, p.lim)) {
         ok = false;
         break;
@@ -462,8 +480,8 @@ route_dx_kernel(const __grid_constant__ CUtensorMap tmW, const DxParams p) {
 static_assert(DxSmem::ALLOC * 2 <= 227 * 1024, "two dx CTAs per SM");
 static_assert(DwSmem::ALLOC <= 227 * 1024, "shared memory");
 
-// steps of 64 tokens per range: enough ranges to give every SM a CTA, but at least two
-// steps in each, since a range costs a pass over its [E,H] sums
+// steps of 64 tokens per range: enough ranges to give every SM a CTA, but at least six
+// steps in each, since a range costs a pass over its [E,H] sums and more than one a launch
 struct Ranges {
   int steps, count;
 };
@@ -471,7 +489,7 @@ Ranges ranges_of(int T, int H, int E) {
   const int total = (T + kStepT - 1) / kStepT;
   const int tiles = ((H + 127) / 128) * ((E + 127) / 128);
   int want = sm_count() / tiles;
-  if (want > (total + 1) / 2) want = (total + 1) / 2;
+  if (want > total / 6) want = total / 6;
   if (want > 32) want = 32;
   if (want < 1) want = 1;
   Ranges r;
