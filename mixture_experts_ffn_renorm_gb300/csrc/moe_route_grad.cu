@@ -36,6 +36,7 @@ constexpr int kConv = 256;              // converting (and epilogue) threads: wa
 constexpr int kThreads = kConv + 32;    // warp 8: TMA and MMA
 constexpr int kStepT = 64;              // tokens per step of dW
 constexpr int kChunk = 4;               // steps between two additions to the f32 sums
+constexpr int kBStages = 4;             // steps of x on their way (its first touch is in DRAM)
 constexpr int kBlk = 64 * 128;          // one operand block: 64 K rows (or 64 rows) of 128 bytes
 
 struct WsLimits {
@@ -77,20 +78,29 @@ __device__ __forceinline__ void load_dl8(const float* __restrict__ dl, int t, in
   }
 }
 
-// Bounded wait of any thread; false once it gives up (the status is raised and the
-// CTA's abort flag set).
+// Bounded wait of any thread (see gemm::wait_bar; the probe without a time hint wakes
+// sooner); false once it gives up (the status is raised and the CTA's abort flag set).
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                      const WsLimits& lim) {
-  return gemm::wait_bar(bar, parity, abort_flag, lim.status, lim.wait_ns);
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (ptx::globaltimer_ns() - t0 > lim.wait_ns) {
+      if (lim.status) atomicOr(lim.status, static_cast<unsigned int>(MOE_STATUS_TIMEOUT));
+      *abort_flag = 1;
+    }
+  }
+  return true;
 }
 
 // ------------------------------------------------------------------ dW
 struct DwSmem {
   static constexpr int A = 0;                          // 2 stages x 3 parts x 2 blocks of 64 experts
-  static constexpr int B = A + 2 * 6 * kBlk;           // 2 stages x 2 blocks of 64 columns
-  static constexpr int DB = B + 2 * 2 * kBlk;          // db: [2 token halves][128] f32
-  static constexpr int BARS = DB + 16 * 128 * 4;       // fullA, fullB, empty, done [2]
-  static constexpr int MISC = BARS + 64;
+  static constexpr int B = A + 2 * 6 * kBlk;           // kBStages x 2 blocks of 64 columns
+  static constexpr int DB = B + kBStages * 2 * kBlk;   // db: [16 token rows][128] f32
+  static constexpr int BARS = DB + 16 * 128 * 4;       // fullA, empty, done [2], fullB [kBStages]
+  static constexpr int MISC = BARS + 48 + 8 * kBStages;
   static constexpr int ALLOC = MISC + 16 + 1024;
 };
 
@@ -99,6 +109,7 @@ struct DwParams {
   int T, H, E, steps;          // steps of 64 tokens per range
   float* out;                  // [ranges][E][H] or null (db alone)
   float* db;                   // [ranges][E] or null
+  int behind_dx;               // launched right behind route_dx_kernel
   WsLimits lim;
   unsigned long long* launches;
 };
@@ -113,24 +124,25 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto full_a = [&](int s) { return sb + S::BARS + 8u * s; };
-  auto full_b = [&](int s) { return sb + S::BARS + 16 + 8u * s; };
-  auto empty = [&](int s) { return sb + S::BARS + 32 + 8u * s; };
-  auto done = [&](int a) { return sb + S::BARS + 48 + 8u * a; };
+  auto empty = [&](int s) { return sb + S::BARS + 16 + 8u * s; };
+  auto done = [&](int a) { return sb + S::BARS + 32 + 8u * a; };
+  auto full_b = [&](int s) { return sb + S::BARS + 48 + 8u * s; };
   count_launch(p.launches, MOE_KID_ROUTE_DW);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(full_a(s), kConv);
-      ptx::mbar_init(full_b(s), 1);
       ptx::mbar_init(empty(s), 1);
     }
+    for (int s = 0; s < kBStages; ++s) ptx::mbar_init(full_b(s), 1);
     for (int a = 0; a < 2; ++a) ptx::mbar_init(done(a), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 8 && lane == 0) ptx::tma_prefetch_desc(&tmX);
-  // Tensor memory is taken after the wait and before the next kernel may start: these CTAs
-  // share SMs, and none that waits for another kernel holds what that kernel needs.
-  grid_dep_wait();
+  // Behind dx of the same call nothing here waits for it: dx let this kernel start once all
+  // earlier work was complete, the two share no output, and the wait comes at the end, so
+  // that what follows finds both done.
+  if (!p.behind_dx) grid_dep_wait();
   if (warp == 8) {
     ptx::tmem_alloc(sb + S::MISC, 512);
     ptx::tmem_relinquish();
@@ -151,25 +163,27 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
     if (mul && ptx::elect_one()) {
       constexpr uint32_t idesc = ptx::idesc_bf16_f32_mn(128, 128, true, true);
       auto load = [&](int i) {
-        ptx::mbar_arrive_expect_tx(full_b(i & 1), 2 * kBlk);
+        const int s = i % kBStages;
+        ptx::mbar_arrive_expect_tx(full_b(s), 2 * kBlk);
         for (int b = 0; b < 2; ++b)
-          ptx::tma_load_2d(sb + S::B + ((i & 1) * 2 + b) * kBlk, &tmX, h0 + 64 * b, t0 + i * kStepT, full_b(i & 1));
+          ptx::tma_load_2d(sb + S::B + (s * 2 + b) * kBlk, &tmX, h0 + 64 * b, t0 + i * kStepT, full_b(s));
+        ++issued;
       };
       bool ok = true;
-      load(0);
-      ++issued;
+      for (int i = 0; i < kBStages - 1 && i < steps; ++i) load(i);
       for (int i = 0; ok && i < steps; ++i) {
         const int s = i & 1;
-        if (i + 1 < steps) {   // the next step's x, once the MMAs that read its stage are done
+        // x of a later step, into the stage that the step before this one has been multiplied from
+        if (i + kBStages - 1 < steps) {
           ok = i == 0 || wait(empty(s ^ 1), ((i - 1) >> 1) & 1, abort_flag, p.lim);
           if (!ok) break;
-          load(i + 1);
-          ++issued;
+          load(i + kBStages - 1);
         }
-        ok = wait(full_b(s), (i >> 1) & 1, abort_flag, p.lim) && wait(full_a(s), (i >> 1) & 1, abort_flag, p.lim);
+        ok = wait(full_b(i % kBStages), (i / kBStages) & 1, abort_flag, p.lim) &&
+             wait(full_a(s), (i >> 1) & 1, abort_flag, p.lim);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint64_t db = ptx::desc_mnmajor_sw128(sb + S::B + s * 2 * kBlk, kBlk);
+        const uint64_t db = ptx::desc_mnmajor_sw128(sb + S::B + (i % kBStages) * 2 * kBlk, kBlk);
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
           const uint64_t da = ptx::desc_mnmajor_sw128(sb + S::A + (s * 6 + part * 2) * kBlk, kBlk);
@@ -213,31 +227,19 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
       }
       ptx::tc_fence_before();
     };
-    float next[4][8];
-    auto fetch = [&](int i) {
+    float v[4][8];   // this step's values, replaced by the next step's as they are split
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load_dl8(p.dl, t0 + i * kStepT + r + 16 * j, e, p.T, p.E, vec, next[j]);
-    };
-    fetch(0);
+    for (int j = 0; j < 4; ++j) load_dl8(p.dl, t0 + r + 16 * j, e, p.T, p.E, vec, v[j]);
     for (int i = 0; i < steps; ++i) {
       const int s = i & 1;
-      float v[4][8];
+      if (mul && ok && i >= 2 && !wait(empty(s), ((i - 2) >> 1) & 1, abort_flag, p.lim)) ok = false;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] = next[j][k];
-      if (i + 1 < steps) fetch(i + 1);   // on its way while this step is split
-      if (p.db && blockIdx.x == 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        if (p.db && blockIdx.x == 0) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) colsum[k] += v[j][k];
-      }
-      if (!mul) continue;
-      if (ok && i >= 2 && !wait(empty(s), ((i - 2) >> 1) & 1, abort_flag, p.lim)) ok = false;
-      if (ok) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        }
+        if (mul && ok) {
           uint4 x[3];
           split8(v[j], x[0], x[1], x[2]);
           const uint32_t dst = sb + S::A + s * 6 * kBlk + at + (r + 16 * j) * 128;
@@ -245,6 +247,10 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
           for (int part = 0; part < 3; ++part)
             ptx::st_shared_v4(dst + part * 2 * kBlk, x[part].x, x[part].y, x[part].z, x[part].w);
         }
+        if (i + 1 < steps) load_dl8(p.dl, t0 + (i + 1) * kStepT + r + 16 * j, e, p.T, p.E, vec, v[j]);
+      }
+      if (!mul) continue;
+      if (ok) {
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(full_a(s));
       }
@@ -285,14 +291,15 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
     const uint64_t g0 = ptx::globaltimer_ns();
     while (ptx::globaltimer_ns() - g0 < 100000ull) {
     }
-    for (uint32_t i = issued < 2 ? 0 : issued - 2; i < issued; ++i)
-      gemm::spin_bounded(full_b(i & 1), (i >> 1) & 1);
+    for (uint32_t i = issued < kBStages ? 0 : issued - kBStages; i < issued; ++i)
+      gemm::spin_bounded(full_b(i % kBStages), (i / kBStages) & 1);
   }
   __syncthreads();
   if (warp == 8) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
+  if (p.behind_dx) grid_dep_wait();
 }
 
 // the ranges' sums in range order: dW as vectors of four, then db
@@ -572,6 +579,16 @@ int moe_route_logits_backward(const float* grad_logits, const void* x_bf16, cons
   const WsLimits lim{gemm::pipeline_wait_ns(), diag.status};
   static std::atomic<int> ready_dx[64] = {}, ready_dw[64] = {};
   int rc;
+  if (grad_x_bf16) {
+    if ((rc = reserve(op, route_dx_kernel, DxSmem::ALLOC, ready_dx)) != MOE_OK) return rc;
+    CUtensorMap tm;
+    if ((rc = gemm::make_tmap(&tm, w_router_bf16, E, H, 64, op, "w_router")) != MOE_OK) return rc;
+    DxParams p{grad_logits, T, H, E, static_cast<uint16_t*>(grad_x_bf16), lim, diag.launches};
+    rc = launch_status(launch_kernel(route_dx_kernel, dim3((H + 255) / 256, (T + 127) / 128), dim3(kThreads),
+                                     DxSmem::ALLOC, s, nullptr, 0, tm, p),
+                       op);
+    if (rc != MOE_OK) return rc;
+  }
   if (sums) {
     if ((rc = reserve(op, route_dw_kernel, DwSmem::ALLOC, ready_dw)) != MOE_OK) return rc;
     CUtensorMap tm{};
@@ -579,7 +596,7 @@ int moe_route_logits_backward(const float* grad_logits, const void* x_bf16, cons
     float* part_w = rg.count > 1 ? static_cast<float*>(workspace) : grad_w_router;
     float* part_b = rg.count > 1 ? static_cast<float*>(workspace) + static_cast<size_t>(rg.count) * E * H : grad_bias;
     DwParams p{grad_logits, T, H, E, rg.steps, grad_w_router ? part_w : nullptr,
-               grad_bias ? part_b : nullptr, lim, diag.launches};
+               grad_bias ? part_b : nullptr, grad_x_bf16 && pdl_enabled() ? 1 : 0, lim, diag.launches};
     rc = launch_status(launch_kernel(route_dw_kernel,
                                      dim3(grad_w_router ? (H + 127) / 128 : 1, (E + 127) / 128, rg.count),
                                      dim3(kThreads), DwSmem::ALLOC, s, nullptr, 0, tm, p),
@@ -596,16 +613,7 @@ int moe_route_logits_backward(const float* grad_logits, const void* x_bf16, cons
       if (rc != MOE_OK) return rc;
     }
   }
-  if (grad_x_bf16) {
-    if ((rc = reserve(op, route_dx_kernel, DxSmem::ALLOC, ready_dx)) != MOE_OK) return rc;
-    CUtensorMap tm;
-    if ((rc = gemm::make_tmap(&tm, w_router_bf16, E, H, 64, op, "w_router")) != MOE_OK) return rc;
-    DxParams p{grad_logits, T, H, E, static_cast<uint16_t*>(grad_x_bf16), lim, diag.launches};
-    rc = launch_status(launch_kernel(route_dx_kernel, dim3((H + 255) / 256, (T + 127) / 128), dim3(kThreads),
-                                     DxSmem::ALLOC, s, nullptr, 0, tm, p),
-                       op);
-  }
-  return rc;
+  return MOE_OK;
 }
 
 }  // extern "C"
