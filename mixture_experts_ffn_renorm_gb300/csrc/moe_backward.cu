@@ -10,24 +10,33 @@ namespace moe {
 namespace bwd {
 namespace {
 
-// 8 consecutive values of a row as f32
+// 8 consecutive values of a row as they lie in memory, and widened
 template <bool kBf16>
-__device__ __forceinline__ void load8(const void* base, size_t i, float (&v)[8]) {
-  if (kBf16) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw8 {
+  uint4 a[kBf16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* base, size_t i) {
+    const uint4* p = reinterpret_cast<const uint4*>(
+        kBf16 ? static_cast<const void*>(static_cast<const uint16_t*>(base) + i)
+              : static_cast<const void*>(static_cast<const float*>(base) + i));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    for (int j = 0; j < (kBf16 ? 1 : 2); ++j) a[j] = __ldg(p + j);
   }
-}
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    if (kBf16) {
+      const uint32_t w[4] = {a[0].x, a[0].y, a[0].z, a[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    } else {
+      const uint4 b = a[kBf16 ? 0 : 1];
+      const uint32_t w[8] = {a[0].x, a[0].y, a[0].z, a[0].w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    }
+  }
+};
 template <bool kBf16>
 __device__ __forceinline__ void store8(void* base, size_t i, const float (&v)[8]) {
   if (kBf16) {
@@ -57,10 +66,11 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // ------------------------------------------------------------------ combine
-// A block takes one token and up to 8 of its expert rows; a thread strides over
-// the channels 8 at a time, so dout is read once and the rows' loads are all in
-// flight together.
-constexpr int kCbThreads = 128;
+// A block takes one token and up to 8 of its expert rows; a thread owns 8 channels
+// (and strides over the rest), so dout is read once and the rows' loads are all in
+// flight together.  Bound by bytes: 285 MB at 4096 tokens of 8 bf16 rows of 2048 with
+// both gradients, 42 us at the copy rate; it takes 45.8.
+constexpr int kCbThreads = 256;
 constexpr int kCbRows = 8;
 
 template <bool kEoBf16, bool kDoBf16, bool kDeoBf16>
@@ -84,23 +94,32 @@ combine_backward_kernel(const void* __restrict__ eo, const float* __restrict__ w
     f[j] = w && j < kn ? __fmul_rn(__ldg(w + t * K + k0 + j), rs) : rs;
   }
   for (int c = threadIdx.x * 8; c < H; c += kCbThreads * 8) {
+    Raw8<kDoBf16> rd;
+    rd.load(dout, t * H + c);
     float d[8];
-    load8<kDoBf16>(dout, t * H + c, d);
+    if (dw) {
+      Raw8<kEoBf16> re[kCbRows];
 #pragma unroll
-    for (int j = 0; j < kCbRows; ++j) {
-      if (j < kn) {
-        const size_t at = (t * K + k0 + j) * H + c;
-        if (dw) {
-          float e[8];
-          load8<kEoBf16>(eo, at, e);
+      for (int j = 0; j < kCbRows; ++j) re[j].load(eo, (t * K + k0 + min(j, kn - 1)) * H + c);
+      rd.widen(d);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[j] = fmaf(e[i], d[i], acc[j]);
-        }
-        if (deo) {
+      for (int j = 0; j < kCbRows; ++j) {
+        float e[8];
+        re[j].widen(e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[j] = fmaf(e[i], d[i], acc[j]);
+      }
+    } else {
+      rd.widen(d);
+    }
+    if (deo) {
+#pragma unroll
+      for (int j = 0; j < kCbRows; ++j) {
+        if (j < kn) {
           float o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = __fmul_rn(d[i], f[j]);
-          store8<kDeoBf16>(deo, at, o);
+          store8<kDeoBf16>(deo, (t * K + k0 + j) * H + c, o);
         }
       }
     }
