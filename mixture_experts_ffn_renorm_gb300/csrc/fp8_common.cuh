@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include "gemm_common.cuh"
+#include "sm100_ptx_fp8.cuh"
 
 namespace moe {
 namespace fp8 {

@@ -27,6 +27,7 @@
 #include <atomic>
 
 #include "gemm_common.cuh"
+#include "sm100_ptx_fp8.cuh"
 
 namespace moe {
 namespace rgrad {

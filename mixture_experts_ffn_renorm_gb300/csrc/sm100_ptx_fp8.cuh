@@ -1,0 +1,89 @@
+// sm100_ptx_fp8.cuh -- inline-PTX wrappers of the FP8 products and of the router's
+// gradient, beside those of sm100_ptx.cuh: E4M3 MMAs, MN-major operands, register
+// split, single-thread election.  Written from the PTX ISA's instruction descriptions.
+#pragma once
+
+#include "sm100_ptx.cuh"
+
+namespace moe {
+namespace ptx {
+
+// n arrivals at once
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+// true in one lane of a converged warp.  tcgen05 instructions behind it issue about
+// four times as fast as behind a lane test: the compiler knows that one thread runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Register split between warpgroups: every warp of a warpgroup executes the same
+// one, and the shares together stay within the launch's threads x registers.
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T on E4M3 operands (32 of K), f32 accumulator
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns (see tmem_ld_32x32b_x32)
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Shared-memory matrix descriptor of an MN-major operand (the 16-bit values of one K row
+// contiguous), as TMA SWIZZLE_128B boxes of 64 values x rows write it: blocks of 64 values
+// `lbo` bytes apart (leading byte offset), groups of 8 K rows 1024 bytes apart (stride byte
+// offset).  16 K rows on is 2048 bytes on.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = desc_kmajor_sw128(smem_addr) & ~(static_cast<uint64_t>(0x3FFFu) << 16);
+  return d | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+}
+
+// Instruction descriptors (see idesc_bf16_f32): bf16 with an MN-major A (bit 15) or B
+// (bit 16); kind::f8f6f4 with an f32 accumulator, A and B E4M3 (format 0), both K-major
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_mn(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_bf16_f32(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+}  // namespace ptx
+}  // namespace moe

@@ -13,15 +13,18 @@ from __future__ import annotations
 
 import torch
 
-from . import (BF16, QFMT_Q4_K, QFMT_Q8_0, moe_combine, moe_combine_gate,
+from . import (BF16, QFMT_Q4_K, QFMT_Q8_0, moe_combine, moe_combine_backward, moe_combine_gate,
                moe_gate_workspace_size, moe_grouped_gemm_down_bf16,
                moe_grouped_gemm_down_bf16_shared, moe_grouped_gemm_down_fp8w,
-               moe_grouped_gemm_down_q, moe_grouped_gemm_gateup_silu_bf16,
+               moe_grouped_gemm_down_q, moe_grouped_gemm_fp8, moe_grouped_gemm_gateup_silu_bf16,
                moe_grouped_gemm_gateup_silu_bf16_shared, moe_grouped_gemm_gateup_silu_bf16_staged,
-               moe_grouped_gemm_gateup_silu_fp8w, moe_gateup_staged_workspace_size,
+               moe_grouped_gemm_gateup_silu_fp8, moe_grouped_gemm_gateup_silu_fp8w,
+               moe_gateup_staged_workspace_size,
                moe_grouped_gemm_gateup_silu_q, moe_dequantize_q_bf16, moe_permute,
-               moe_permute_workspace_size, moe_quantize_act_q8, moe_route_topk,
-               moe_route_topk_workspace_size)
+               moe_permute_workspace_size, moe_quantize_act_fp8, moe_quantize_act_q8,
+               moe_route_backward, moe_route_backward_workspace_size, moe_route_logits_backward,
+               moe_route_logits_backward_workspace_size, moe_route_topk,
+               moe_route_topk_workspace_size, moe_silu_mul_backward_fp8, moe_transpose_fp8w)
 
 # keep-quant weight formats: name -> (library format id, weights per activation block)
 Q_WEIGHTS = {"q8_0": (QFMT_Q8_0, 32), "q4_k": (QFMT_Q4_K, 256)}
@@ -47,6 +50,14 @@ class MoeBlock:
     ``w13_e4m3`` / ``w13_scale`` and ``w2_e4m3`` / ``w2_scale`` (codes uint8 of
     the same shapes, f32 scales per 128 x 128 block); the shared expert stays
     bf16 and runs in launches of its own.
+    fp8_acts=True (with fp8_weights): the routed experts' activations are FP8 too.  The
+    routed token rows are quantised (a scale per row and 128 columns) into expert order,
+    and the gate/up product quantises its own activations for the down product; no
+    x_perm and no bf16 act rows exist.  H and I multiples of 16.
+    training=True (with fp8_acts, no shared expert): forward() keeps what backward()
+    needs, the expert rows are stored without their routing weight, which the combine
+    applies, and a transposed copy of the expert weights is kept.  backward() gives the
+    gradients of the router, its bias and the tokens; the expert weights are frozen.
     qweights="q8_0" | "q4_k": keep-quant routed experts, ``w13q`` [E, 2I, H/blk*bytes]
     and ``w2q`` [E, H, I/blk*bytes] GGUF blocks (uint8).  The token rows and the
     act rows are quantized to 8-bit blocks on the device, the gate/up GEMM reads
@@ -64,7 +75,7 @@ class MoeBlock:
 
     def __init__(self, H, I, E, K, weights, max_tokens, device="cuda", I_shared=0,
                  routed_scale=1.0, gather=False, fuse_shared=True, fp8_weights=False,
-                 qweights=None, q_dequant=False, staged=False):
+                 qweights=None, q_dequant=False, staged=False, fp8_acts=False, training=False):
         self.H, self.I, self.E, self.K, self.Is = H, I, E, K, I_shared
         if qweights is not None:
             if qweights not in Q_WEIGHTS:
@@ -100,6 +111,13 @@ class MoeBlock:
                        (I_shared > 0 and self.fuse_shared)):
             raise ValueError("staged rows need plain bf16 experts, gather=False and no fused "
                              "shared expert")
+        self.fp8_acts, self.training = fp8_acts, training
+        if fp8_acts and not fp8_weights:
+            raise ValueError("fp8_acts needs fp8_weights")
+        if fp8_acts and (H % 16 or I % 16):
+            raise ValueError(f"FP8 activations need H and I to be multiples of 16, not {H} and {I}")
+        if training and (not fp8_acts or I_shared > 0):
+            raise ValueError("training needs fp8_acts and no shared expert")
         self.routed_scale = float(routed_scale)
         self.device = torch.device(device)
         if self.device.type != "cuda":
@@ -137,11 +155,38 @@ class MoeBlock:
         self.expert_offsets = torch.empty((E + 1,), dtype=i32, device=dv)
         self.sorted_pair = torch.empty((P,), dtype=i32, device=dv)
         self.pair_to_row = torch.empty((P,), dtype=i32, device=dv)
-        self.x_perm = None if always else torch.empty((P, H), dtype=bf, device=dv)
+        self.x_perm = None if always or fp8_acts else torch.empty((P, H), dtype=bf, device=dv)
         # zero-filled once, then passed unchanged to every staged call
         self.ws_staged = (torch.zeros(max(16, moe_gateup_staged_workspace_size(P)),
                                       dtype=torch.uint8, device=dv) if staged else None)
-        self.act = torch.empty((P, I), dtype=bf, device=dv)
+        self.act = None if fp8_acts else torch.empty((P, I), dtype=bf, device=dv)
+        blocks = lambda n: -(-n // 128)
+        if fp8_acts:
+            # E4M3 codes and scales of the routed rows and of the activations
+            self.x_q = torch.empty((P, H), dtype=torch.uint8, device=dv)
+            self.x_s = torch.empty((P, blocks(H)), dtype=f32, device=dv)
+            self.act_q = torch.empty((P, I), dtype=torch.uint8, device=dv)
+            self.act_s = torch.empty((P, blocks(I)), dtype=f32, device=dv)
+            self.gate_up = torch.empty((P, 2 * I), dtype=bf, device=dv) if training else None
+        if training:
+            self.logits = torch.empty((T, E), dtype=f32, device=dv)
+            self.grad_topk_w = torch.empty((T, K), dtype=f32, device=dv)
+            self.grad_logits = torch.empty((T, E), dtype=f32, device=dv)
+            self.losses = torch.empty((2,), dtype=f32, device=dv)
+            self.grad_x = torch.empty((T, H), dtype=bf, device=dv)
+            self.grad_x_router = torch.empty((T, H), dtype=bf, device=dv)
+            self.grad_w_router = torch.empty((E, H), dtype=f32, device=dv)
+            self.grad_logit_bias = torch.empty((E,), dtype=f32, device=dv)
+            self.dact = torch.empty((P, I), dtype=bf, device=dv)
+            self.dgu_q = torch.empty((P, 2 * I), dtype=torch.uint8, device=dv)
+            self.dgu_s = torch.empty((P, blocks(2 * I)), dtype=f32, device=dv)
+            # the products of the gradient contract over the forward's output columns
+            self.w13_t, self.w13_ts = self._transposed(self.w13_q, self.w13_s)
+            self.w2_t, self.w2_ts = self._transposed(self.w2_q, self.w2_s)
+            self.ws_grad = torch.empty(
+                (max(256, moe_route_backward_workspace_size(T, E),
+                     moe_route_logits_backward_workspace_size(T, H, E)),),
+                dtype=torch.uint8, device=dv)
         if self.qfmt:
             # 8-bit activation blocks of the token rows and of the act rows
             self.x_q = torch.empty((T, H), dtype=torch.int8, device=dv)
@@ -184,11 +229,11 @@ class MoeBlock:
         mark("start", edge=True)
         moe_route_topk(x, self.w_router, self.logit_bias,
                        self.w_shared_gate if self.has_shared else None, None, T, H, E, K, 1, 0, 1,
-                       self.topk_ids, self.topk_w, None,
+                       self.topk_ids, self.topk_w, self.logits if self.training else None,
                        self.gate_logit if self.has_shared else None, ws, ws.numel(), stream)
         mark("route")
         fused = self.has_shared and self.fuse_shared
-        gathered = self.gather is True or (
+        gathered = self.gather is True or self.fp8_acts or (
             self.gather == "auto" and P <= 16 * E and not fused and not self.staged
             and not self.fp8 and not self.qfmt)
         moe_permute(self.topk_ids, x, T, K, E, H, self.expert_offsets, self.sorted_pair,
@@ -201,6 +246,13 @@ class MoeBlock:
             moe_grouped_gemm_gateup_silu_q(self.x_q, self.x_s, T, self.sorted_pair, K, self.w13_q,
                                            self.qfmt, self.expert_offsets, P, H, I, E, self.act,
                                            stream)
+        elif self.fp8_acts:
+            moe_quantize_act_fp8(x, T, H, K, self.pair_to_row, None, 1.0, self.x_q, self.x_s,
+                                 stream)
+            mark("quant_x")
+            moe_grouped_gemm_gateup_silu_fp8(self.x_q, self.x_s, self.w13_q, self.w13_s,
+                                             self.expert_offsets, P, H, I, E, self.gate_up,
+                                             self.act_q, self.act_s, stream)
         elif self.fp8:
             moe_grouped_gemm_gateup_silu_fp8w(self.x_perm, self.w13_q, self.w13_s,
                                               self.expert_offsets, P, H, I, E, self.act, None, 0,
@@ -229,6 +281,10 @@ class MoeBlock:
             moe_grouped_gemm_down_q(self.act_q, self.act_s, self.w2_q, self.qfmt,
                                     self.expert_offsets, self.topk_w, self.sorted_pair, P, I, H, E,
                                     self.expert_out, stream)
+        elif self.fp8_acts:
+            moe_grouped_gemm_fp8(self.act_q, self.act_s, self.w2_q, self.w2_s,
+                                 self.expert_offsets, None if self.training else self.topk_w,
+                                 self.sorted_pair, P, I, H, E, self.expert_out, stream)
         elif self.fp8:
             moe_grouped_gemm_down_fp8w(self.act, self.w2_q, self.w2_s, self.expert_offsets,
                                        self.topk_w, self.sorted_pair, P, I, H, E, self.expert_out,
@@ -256,10 +312,55 @@ class MoeBlock:
             mark("combine", edge=True)
             return out
         else:
-            moe_combine(self.expert_out, BF16, None, None, BF16, self.routed_scale, T, K, H, out,
-                        BF16, stream)
+            moe_combine(self.expert_out, BF16, self.topk_w if self.training else None, None, BF16,
+                        self.routed_scale, T, K, H, out, BF16, stream)
         mark("combine", edge=True)
         return out
+
+    def backward(self, x, dout, balance_coef=0.0, z_coef=0.0, stream=None):
+        """Gradients of the last forward(x), given the gradient dout [T, H] bf16 of its output,
+        plus the router's auxiliary losses.  Returns a dict of views of the block's buffers:
+        grad_x bf16 [T, H] (through the experts and the router), grad_w_router f32 [E, H],
+        grad_logit_bias f32 [E], grad_topk_w f32 [T, K], losses f32 [2] (balance, z).  The
+        choice of experts and the quantisers' roundings count as constant (the gradient
+        passes a rounding unchanged).  No call allocates or synchronises."""
+        if not self.training:
+            raise ValueError("backward() needs MoeBlock(training=True)")
+        T = x.shape[0]
+        assert T <= self.max_tokens and dout.shape == x.shape
+        assert x.dtype == dout.dtype == torch.bfloat16 and x.is_contiguous() and dout.is_contiguous()
+        H, I, E, K = self.H, self.I, self.E, self.K
+        P = T * K
+        ws = self.ws_grad
+        moe_combine_backward(self.expert_out, BF16, self.topk_w, dout, BF16, self.routed_scale, T,
+                             K, H, self.grad_topk_w, None, BF16, stream)
+        moe_route_backward(self.logits, self.topk_ids, self.grad_topk_w, self.expert_offsets, T, E,
+                           K, 1, 0, balance_coef, z_coef, self.grad_logits, self.losses, ws,
+                           ws.numel(), stream)
+        moe_route_logits_backward(self.grad_logits, x, self.w_router, T, H, E, self.grad_x_router,
+                                  self.grad_w_router, self.grad_logit_bias, ws, ws.numel(), stream)
+        # through the experts: the rows' gradients in expert order, back through down, SiLU-mul
+        # and gate/up; the routed rows' buffers of the forward are free again
+        moe_quantize_act_fp8(dout, T, H, K, self.pair_to_row, self.topk_w, self.routed_scale,
+                             self.x_q, self.x_s, stream)
+        moe_grouped_gemm_fp8(self.x_q, self.x_s, self.w2_t, self.w2_ts, self.expert_offsets, None,
+                             None, P, H, I, E, self.dact, stream)
+        moe_silu_mul_backward_fp8(self.gate_up, self.dact, P, I, self.dgu_q, self.dgu_s, stream)
+        moe_grouped_gemm_fp8(self.dgu_q, self.dgu_s, self.w13_t, self.w13_ts, self.expert_offsets,
+                             None, self.sorted_pair, P, 2 * I, H, E, self.expert_out, stream)
+        moe_combine(self.expert_out, BF16, None, self.grad_x_router, BF16, 1.0, T, K, H,
+                    self.grad_x, BF16, stream)
+        return {"grad_x": self.grad_x[:T], "grad_w_router": self.grad_w_router,
+                "grad_logit_bias": self.grad_logit_bias, "grad_topk_w": self.grad_topk_w[:T],
+                "losses": self.losses}
+
+    def _transposed(self, w, scale):
+        G, R, C = w.shape
+        wt = torch.empty((G, C, R), dtype=torch.uint8, device=self.device)
+        st = torch.empty((G, scale.shape[2], scale.shape[1]), dtype=torch.float32,
+                         device=self.device)
+        moe_transpose_fp8w(w, scale, G, R, C, wt, st)
+        return wt, st
 
     @staticmethod
     def _dequantized(weights, H, I, E, qfmt, device):
