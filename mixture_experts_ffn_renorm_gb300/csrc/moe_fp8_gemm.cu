@@ -64,7 +64,7 @@ __device__ __forceinline__ uint64_t ld_shared_u64(uint32_t addr) {
 
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of other roles (one of its warps idle)
-constexpr int kAuxRegs = 32, kEpiRegs = 112;
+constexpr int kAuxRegs = 48, kEpiRegs = 104;
 // the split draws on the registers the block was launched with (96 a thread)
 static_assert(128 * kAuxRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 96, "register split");
 constexpr int kTokBlock = 128;              // rows per rows tile
@@ -76,15 +76,24 @@ constexpr int kMaxAcc = 8;
 constexpr int kMaxGroupsLaunch = 512;       // groups of one launch (schedule in shared memory)
 constexpr int kMmaK = 32;                   // K per tcgen05.mma of 8-bit types
 
+// Scales of 8 blocks: the rows' as [block][128 rows], 16 bytes of padding per block (so that
+// the four rows x 8 blocks of one copy instruction meet 32 banks); then up to three weight
+// scale blocks' as [which][8].  which, plain: the two 128-row parts; gate/up: the gate rows,
+// and the up rows, which of I not a multiple of 128 lie in two scale blocks.
+constexpr int kChunk = 8, kRowStride = 128 * 4 + 16;
+constexpr int kChunkW = kChunk * kRowStride, kChunkBytes = kChunkW + 3 * kChunk * 4;
+
 struct Smem {
   static constexpr int W = 0;
   static constexpr int T = W + kStages * kWBytes;
   static constexpr int EPI = T + kStages * kTBytes;             // 16 KB of staging
-  static constexpr int FAC = EPI + 16384;                       // weights tiles: a warp's row scales [2][32]
-  static constexpr int META = FAC + kEpiWarps * 256;            // dst and weight of weights tiles, or row maxima
-  static constexpr int BARS = META + 2048;
-  // full, empty [kStages], tfull, tempty [kMaxAcc], drain [2]
-  static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + 2;
+  static constexpr int SCALE = EPI + 16384;                     // two chunks of scales
+  static constexpr int META = SCALE + 2 * kChunkBytes;          // two tiles' destinations and weights, or row maxima
+  static constexpr int INFO = META + 2048;                      // two tiles
+  static constexpr int BARS = INFO + 32;
+  // full, empty [kStages], tfull, tempty [kMaxAcc], drain [2], ifull, iempty [2],
+  // sfull, sempty [2]
+  static constexpr int NBARS = 2 * kStages + 2 * kMaxAcc + 10;
   static constexpr int MISC = (BARS + NBARS * 8 + 15) & ~15;                 // tmem slot, then:
   static constexpr int kAbort = 4, kSmall = 8, kStatus = 16, kLimit = 24, kScan = 32;
   static constexpr int ROWS_START = (MISC + kScan + 8 * (kThreads / 32) + 15) & ~15;
@@ -226,6 +235,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
   auto bar_tfull = [&](int a) { return bars + 8u * (2 * kStages + a); };
   auto bar_tempty = [&](int a) { return bars + 8u * (2 * kStages + kMaxAcc + a); };
   auto bar_drain = [&](int i) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + i); };
+  auto bar_ifull = [&](int i) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + 2 + i); };
+  auto bar_iempty = [&](int i) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + 4 + i); };
+  auto bar_sfull = [&](int i) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + 6 + i); };
+  auto bar_sempty = [&](int i) { return bars + 8u * (2 * kStages + 2 * kMaxAcc + 8 + i); };
 
   count_launch(kp.launches, p.kid);
 
@@ -238,7 +251,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       ptx::mbar_init(bar_tfull(a), 1);    // the issuer's MMA commit
       ptx::mbar_init(bar_tempty(a), 8);   // the epilogue warps of its part
     }
-    for (int i = 0; i < 2; ++i) ptx::mbar_init(bar_drain(i), 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar_drain(i), 1);
+      ptx::mbar_init(bar_ifull(i), 32);          // warp 3
+      ptx::mbar_init(bar_iempty(i), kEpiWarps);
+      ptx::mbar_init(bar_sfull(i), 32);          // warp 3's copies
+      ptx::mbar_init(bar_sempty(i), kEpiWarps);
+    }
     *abort_flag = 0;
     *reinterpret_cast<unsigned int**>(smem + S::MISC + S::kStatus) = kp.status;
     *reinterpret_cast<unsigned long long*>(smem + S::MISC + S::kLimit) = kp.wait_ns;
@@ -324,7 +343,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     ptx::setmaxnreg_dec<kAuxRegs>();
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer
-      // lanes 0 and 1 the boxes of the two parts' weight rows, lane 2 the token rows
+      // one lane per box: the two parts' 128 weight rows each (gate/up: 64 up rows, then the 64
+      // gate rows of the same features), the token rows
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -333,11 +353,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         const int tbox = t.n_tok > 64 ? 128 : (t.n_tok > 32 ? 64 : (t.n_tok > 16 ? 32 : 16));
         const uint32_t bytes = kWBytes + tbox * 128;
         const int wrow = t.g * kp.rows_per_group + t.n0;
-        const CUtensorMap* mbox =
-            lane < 2 ? &tmW : (tbox == 16 ? &tmT16 : (tbox == 32 ? &tmT32 : (tbox == 64 ? &tmT64 : &tmT128)));
-        const int ybox = lane == 2 ? t.r0 : (kGU ? (lane == 0 ? wrow + p.N : wrow) : wrow + 128 * lane);
-        const uint32_t dbox = lane == 2 ? S::T : S::W + lane * (kWBytes / 2);
-        const uint32_t dstep = lane == 2 ? kTBytes : kWBytes;
+        constexpr int kTokLane = kGU ? 4 : 2;
+        const CUtensorMap* mbox = lane < kTokLane ? &tmW
+                                  : (tbox == 16 ? &tmT16 : (tbox == 32 ? &tmT32 : (tbox == 64 ? &tmT64 : &tmT128)));
+        const int ybox = lane == kTokLane ? t.r0
+                         : (kGU ? wrow + 64 * (lane >> 1) + (lane & 1 ? 0 : p.N) : wrow + 128 * lane);
+        const uint32_t dbox = lane == kTokLane ? S::T : S::W + lane * (kWBytes / kTokLane);
+        const uint32_t dstep = lane == kTokLane ? kTBytes : kWBytes;
         for (int kb = 0; kb < nk; ++kb) {
           bool got = true;
           if (lane == 0) {
@@ -351,7 +373,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           }
           ++loads;
           // the maps see pairs of codes as 2-byte elements: 64 of them per scale block
-          if (lane < 3) ptx::tma_load_2d(sbase + dbox + stage * dstep, mbox, kb * 64, ybox, bar_full(stage));
+          if (lane <= kTokLane) ptx::tma_load_2d(sbase + dbox + stage * dstep, mbox, kb * 64, ybox, bar_full(stage));
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
       }
@@ -393,6 +415,61 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           }
         }
       }
+    } else {
+      // ---------------------------------------------------------- tiles and scales
+      // Warp 3 works ahead of the epilogue: chunks of scales, the tile, and its rows'
+      // destinations and weights, which cost a binary search and two dependent loads.
+      uint32_t n = 0, q = 0;     // tiles and chunks so far
+      bool ok = true;
+      for (int tile = unit; ok && tile < total; tile += n_units, ++n) {
+        const Tile t = sch.at(tile);
+        const int rb = blocks_of(kp.rows_per_group);
+        // this lane copies block `blk` of rows sub, sub + 4, ..., and of weight scale block `sub`
+        const int blk = lane & 7, sub = lane >> 3;
+        const int wb = kGU && sub > 0 ? (p.N + t.n0) / kBlk + sub - 1 : t.n0 / kBlk + sub;
+        const float* sa = p.sa + static_cast<size_t>(t.r0 + sub) * nk + blk;
+        const float* sw = p.sw + (static_cast<size_t>(t.g) * rb + min(wb, rb - 1)) * nk + blk;
+        auto copy = [&](int kb) {
+          ok = __all_sync(0xffffffffu, wait_one(bar_sempty(q & 1), ((q >> 1) & 1u) ^ 1u, sbase + S::MISC));
+          if (!ok) return;
+          const uint32_t at = sbase + S::SCALE + (q & 1) * kChunkBytes;
+          if (kb + blk < nk) {
+            uint32_t to = at + blk * kRowStride + sub * 4;
+            const float* from = sa + kb;
+            for (int r = sub; r < t.n_tok; r += 4, to += 16, from += 4 * nk) ptx::cp_async_4(to, from);
+            if (sub < (kGU ? 3 : 2)) ptx::cp_async_4(at + kChunkW + (sub * kChunk + blk) * 4, sw + kb);
+          }
+          ptx::cp_async_arrive_noinc(bar_sfull(q & 1));
+          ++q;
+        };
+        copy(0);
+        if (!ok) break;
+        int d[4];
+        float w[4];
+        if (!kGU) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = lane + 32 * i;
+            d[i] = j < t.n_tok ? (p.row_to_pair ? __ldg(p.row_to_pair + t.r0 + j) : t.r0 + j) : -1;
+            if (d[i] >= p.P) d[i] = -1;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = p.pair_weight && d[i] >= 0 ? __ldg(p.pair_weight + d[i]) : 1.0f;
+        }
+        if (!__all_sync(0xffffffffu, wait_one(bar_iempty(n & 1), ((n >> 1) & 1u) ^ 1u, sbase + S::MISC))) break;
+        if (!kGU) {
+          const uint32_t at = sbase + S::META + (n & 1) * 1024 + lane * 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ptx::st_shared_f32(at + 128 * i, __int_as_float(d[i]));
+            ptx::st_shared_f32(at + 512 + 128 * i, w[i]);
+          }
+        }
+        if (lane == 0) ptx::st_shared_v4(sbase + S::INFO + (n & 1) * 16, t.g, t.r0, t.n_tok, t.n0);
+        ptx::mbar_arrive(bar_ifull(n & 1));
+        for (int kb = kChunk; ok && kb < nk; kb += kChunk) copy(kb);
+      }
+      ptx::cp_async_wait_all();
     }
   } else {
     // ------------------------------------------------------------ joins and epilogue
@@ -407,177 +484,187 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     const Schedule sch{sbase, p.G, p.N, kFbCols};
     auto bar_tfull = [&](int a) { return sbase + S::BARS + 8u * (2 * kStages + a); };
     auto bar_tempty = [&](int a) { return sbase + S::BARS + 8u * (2 * kStages + kMaxAcc + a); };
+    auto bar_ifull = [&](int i) { return sbase + S::BARS + 8u * (2 * kStages + 2 * kMaxAcc + 2 + i); };
+    auto bar_iempty = [&](int i) { return sbase + S::BARS + 8u * (2 * kStages + 2 * kMaxAcc + 4 + i); };
+    auto bar_sfull = [&](int i) { return sbase + S::BARS + 8u * (2 * kStages + 2 * kMaxAcc + 6 + i); };
+    auto bar_sempty = [&](int i) { return sbase + S::BARS + 8u * (2 * kStages + 2 * kMaxAcc + 8 + i); };
+    // the n-th tile of this CTA
+    auto wait_info = [&](uint32_t n) {
+      return __all_sync(0xffffffffu, wait_one(bar_ifull(n & 1), (n >> 1) & 1u, sbase + S::MISC)) != 0;
+    };
+    auto info = [&](uint32_t n) {
+      const uint4 v = ptx::ld_shared_v4(sbase + S::INFO + (n & 1) * 16);
+      Tile t;
+      t.g = v.x;
+      t.r0 = v.y;
+      t.n_tok = v.z;
+      t.n0 = v.w;
+      return t;
+    };
     uint32_t parts = (warp - 4) >> 3;   // the part's place among the accumulators passed so far
-    uint32_t n_tails = 0;      // weights tiles so far: META's half
-    for (int tile = blockIdx.x; tile < sch.total(); tile += gridDim.x) {
-      if (tile < sch.word(S::ROWS_START, G)) {
-        // ---------------------------------------------------------- rows tile
-        float sum[64];
+    uint32_t n = 0, q = 0;              // tiles and chunks passed
+    int tile = blockIdx.x;
+    bool on = true;
+    // ------------------------------------------------------------ rows tiles
+    for (; tile < sch.word(Smem::ROWS_START, G); tile += gridDim.x, ++n) {
+      if (!wait_info(n)) {
+        ptx::bar_and(5, 32 * kEpiWarps, false);
+        on = false;
+        break;
+      }
+      float sum[64];   // gate/up: 32 features' up, then their gate
 #pragma unroll
-        for (int i = 0; i < 64; ++i) sum[i] = 0.0f;
-        // element indexes of the scales fit 32 bits: one per 128 or 16384 codes of one byte
-        uint32_t sa, sw, to_sw1 = 0, taddr0;
-        int split = 64;                              // columns of the first weight scale block
-        {
-          const Ids id(warp, lane);
-          const Tile t = sch.at(tile);
-          const int rb = blocks_of(kp.rows_per_group);
-          sa = static_cast<uint32_t>(t.r0 + (id.f < t.n_tok ? id.f : 0)) * nk;
-          // the weight rows behind this thread's 64 columns: one scale block, or (up rows of
-          // I not a multiple of 128) two that meet at a multiple of 16
-          const int wr = kGU ? t.n0 + 64 * id.h + (id.set == 0 ? p.N : 0) : t.n0 + 128 * id.set + 64 * id.h;
-          const int wb = min(wr / kBlk, rb - 1);
-          sw = (static_cast<uint32_t>(t.g) * rb + wb) * nk;
-          if (kGU && id.set == 0) split = (wb + 1) * kBlk - wr;
-          if (kGU && split < 64 && wb + 1 < rb) to_sw1 = nk;
-          taddr0 = id.tmem(tmem_base) + 64 * id.h;
-        }
-        float a0 = __ldg(p.sa + sa), w0 = __ldg(p.sw + sw), x0 = kGU ? __ldg(p.sw + (sw + to_sw1)) : 0.0f;
-#pragma unroll 1
-        for (int left = nk; left > 0; --left) {
-          const float s0 = __fmul_rn(a0, w0), s1 = kGU ? __fmul_rn(a0, x0) : 0.0f;
-          if (left > 1) {                            // the next block's scales, on their way
-            a0 = __ldg(p.sa + ++sa);
-            w0 = __ldg(p.sw + ++sw);
-            if (kGU) x0 = __ldg(p.sw + (sw + to_sw1));
-          }
-          const uint32_t acc = parts & 3u;
-          wait_lean(bar_tfull(acc), (parts >> 2) & 1u, sbase + S::MISC);
-          ptx::tc_fence_after();
-          const uint32_t taddr = taddr0 + acc * 128;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[16];
-            ptx::tmem_ld_32x32b_x16(taddr + 16 * c, v);
-            ptx::tmem_ld_wait();
-            if (c == 3) {                            // the warp has read all of it
-              ptx::tc_fence_before();
-              if (lane == 0) ptx::mbar_arrive(bar_tempty(acc));
-            }
-            const float sc = !kGU || 16 * c < split ? s0 : s1;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum[16 * c + i] = fmaf(__uint_as_float(v[i]), sc, sum[16 * c + i]);
-          }
-          parts += 2;
-        }
-        // one decision for the sixteen warps
-        if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + S::kAbort) == 0)) break;
+      for (int i = 0; i < 64; ++i) sum[i] = 0.0f;
+      uint32_t taddr0, row4, w_at, u0_at = 0, u1_at = 0;   // row4 and below: within a chunk
+      {
         const Ids id(warp, lane);
-        const int e = id.e, h = id.h, set = id.set, f = id.f, et = id.et;
-        const Tile t = sch.at(tile);
-        const int j = f;                             // this thread's row of the tile
-        const bool live = j < t.n_tok;
-        uint32_t pk[32];                             // the 64 results in bf16
-        int d = -1;
-        if (!kGU) {
-          float w = 1.0f;
-          if (live) {
-            d = p.row_to_pair ? __ldg(p.row_to_pair + t.r0 + j) : t.r0 + j;
-            if (d >= p.P) d = -1;
-            if (p.pair_weight && d >= 0) w = __ldg(p.pair_weight + d);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i)               // one f32 multiply, then the one bf16 rounding
-            pk[i] = gemm::pack_bf16x2(__fmul_rn(sum[2 * i], w), __fmul_rn(sum[2 * i + 1], w));
-        } else {
-          d = live ? t.r0 + j : -1;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) pk[i] = gemm::pack_bf16x2(sum[2 * i], sum[2 * i + 1]);
-        }
-        if (!kGU || p.out) {
-          // 16 columns of the warp's 32 rows at a time through its own 1 KB: two lanes store
-          // one row's 32 bytes
-          const uint32_t st = sbase + S::EPI + e * 1024;
-          const int cols = kGU ? 2 * p.N : p.N;
-          const int lim = kGU ? t.n0 + 64 * h : t.n0 + 128 * set + 64 * h;   // the first column within its half
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t sx = (lane >> 2) & 1;
-            ptx::st_shared_v4(st + lane * 32 + (sx << 4), pk[8 * c], pk[8 * c + 1], pk[8 * c + 2], pk[8 * c + 3]);
-            ptx::st_shared_v4(st + lane * 32 + ((sx ^ 1u) << 4), pk[8 * c + 4], pk[8 * c + 5], pk[8 * c + 6], pk[8 * c + 7]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int row = 16 * i + (lane >> 1), k = lane & 1;
-              const uint4 val = ptx::ld_shared_v4(st + row * 32 + ((k ^ ((row >> 2) & 1)) << 4));
-              const int dr = __shfl_sync(0xffffffffu, d, row);
-              const int cc = lim + 16 * c + 8 * k;
-              if (dr >= 0 && cc < p.N)
-                *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(dr) * cols + (kGU && set == 0 ? p.N : 0) + cc) = val;
-            }
-            __syncwarp();
-          }
-        }
+        taddr0 = id.tmem(tmem_base) + (kGU ? 32 : 64) * id.h;
+        row4 = id.f * 4;
+        w_at = kChunkW + (kGU ? 0 : id.set * kChunk * 4);
         if (kGU) {
-          // Set 0 holds up, set 1 gate, of the same row and 64 features: set 0 goes on with the
-          // first 32 features and set 1 with the others, 16 at a time through shared memory.
-          float act[32], m = 0.0f;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            ptx::bar_sync(6, 32 * kEpiWarps);
-            const uint32_t mine = sbase + S::EPI + et * 16, theirs = sbase + S::EPI + (et ^ 256) * 16;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t g4[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) g4[k] = set == 0 ? pk[16 + 8 * c + 4 * i + k] : pk[8 * c + 4 * i + k];
-              ptx::st_shared_v4(mine + i * 8192, g4[0], g4[1], g4[2], g4[3]);
-            }
-            ptx::bar_sync(6, 32 * kEpiWarps);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint4 o4 = ptx::ld_shared_v4(theirs + i * 8192);
-              const uint32_t o[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t own = set == 0 ? pk[8 * c + 4 * i + k] : pk[16 + 8 * c + 4 * i + k];
-                const uint32_t gw = set == 0 ? o[k] : own, uw = set == 0 ? own : o[k];
-                const int n = 16 * c + 8 * i + 2 * k;
-                act[n] = silu_mul(__uint_as_float(gw << 16), __uint_as_float(uw << 16));
-                act[n + 1] = silu_mul(__uint_as_float(gw & 0xFFFF0000u), __uint_as_float(uw & 0xFFFF0000u));
-              }
-            }
-          }
-          const int col = t.n0 + 64 * h + 32 * set;  // the first of this thread's 32 features
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col + (i & 16) < p.N) m = fmaxf(m, fabsf(act[i]));        // N % 16 == 0
-          const uint32_t s_max = sbase + S::META;    // [4 groups][128 rows]
-          ptx::st_shared_f32(s_max + ((2 * set + h) * 128 + f) * 4, m);
-          ptx::bar_sync(6, 32 * kEpiWarps);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m = fmaxf(m, ptx::ld_shared_f32(s_max + (i * 128 + f) * 4));
-          if (live) {
-            float dd, inv;
-            block_scale(m, dd, inv);
-            const size_t r = static_cast<size_t>(t.r0 + j);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float x[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = act[16 * i + k];
-              if (col + 16 * i < p.N) *reinterpret_cast<uint4*>(p.act + r * p.N + col + 16 * i) = codes16(x, inv);
-            }
-            if (h + set == 0) p.act_scale[r * blocks_of(p.N) + t.n0 / kBlk] = dd;
-          }
+          const int up = p.N + info(n).n0, ur = up + 64 * id.set + 32 * id.h;
+          u0_at = kChunkW + (1 + ur / kBlk - up / kBlk) * kChunk * 4;
+          u1_at = kChunkW + (1 + (ur + 16) / kBlk - up / kBlk) * kChunk * 4;
         }
-        continue;
       }
-      // ------------------------------------------------------------ weights tile
+      uint32_t sc = 0;                             // the chunk's address, 4 bytes on per block
+#pragma unroll 1
+      for (int kb = 0; kb < nk; ++kb) {
+        if ((kb & (kChunk - 1)) == 0) {
+          if (kb > 0) {
+            if (lane == 0) ptx::mbar_arrive(bar_sempty(q & 1));
+            ++q;
+          }
+          wait_lean(bar_sfull(q & 1), (q >> 1) & 1u, sbase + S::MISC);
+          sc = sbase + S::SCALE + (q & 1) * kChunkBytes;
+        }
+        const float a0 = ptx::ld_shared_f32(sc + (kb & (kChunk - 1)) * (kRowStride - 4) + row4);
+        const float s0 = __fmul_rn(a0, ptx::ld_shared_f32(sc + w_at));
+        const float s1 = kGU ? __fmul_rn(a0, ptx::ld_shared_f32(sc + u0_at)) : 0.0f;
+        const float s2 = kGU ? __fmul_rn(a0, ptx::ld_shared_f32(sc + u1_at)) : 0.0f;
+        sc += 4;
+        const uint32_t acc = parts & 3u;
+        wait_lean(bar_tfull(acc), (parts >> 2) & 1u, sbase + S::MISC);
+        ptx::tc_fence_after();
+        const uint32_t taddr = taddr0 + acc * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(taddr + (kGU ? 64 * (c >> 1) + 16 * (c & 1) : 16 * c), v);
+          ptx::tmem_ld_wait();
+          if (c == 3) {                            // the warp has read all of it
+            ptx::tc_fence_before();
+            if (lane == 0) ptx::mbar_arrive(bar_tempty(acc));
+          }
+          const float s = !kGU || c > 1 ? s0 : (c == 0 ? s1 : s2);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[16 * c + i] = fmaf(__uint_as_float(v[i]), s, sum[16 * c + i]);
+        }
+        parts += 2;
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_sempty(q & 1));
+      ++q;
+      // one decision for the sixteen warps
+      if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + S::kAbort) == 0)) {
+        on = false;
+        break;
+      }
       const Ids id(warp, lane);
-      const int e = id.e, h = id.h, set = id.set, f = id.f, et = id.et, ht = id.ht;
-      const Tile t = sch.at(tile);
-      const int parity = n_tails++ & 1;
-      int* dst_t = reinterpret_cast<int*>(smem + S::META) + parity * kTail;               // plain
-      float* w_t = reinterpret_cast<float*>(smem + S::META + 512) + parity * kTail;
-      if (!kGU && et < kTail) {
-        // destination rows and weights; the last readers of this half (two tiles ago) passed the
-        // previous tile's vote
-        int d = et < t.n_tok ? (p.row_to_pair ? __ldg(p.row_to_pair + t.r0 + et) : t.r0 + et) : -1;
-        if (d >= p.P) d = -1;
-        dst_t[et] = d;
-        w_t[et] = p.pair_weight && d >= 0 ? __ldg(p.pair_weight + d) : 1.0f;
+      const int h = id.h, set = id.set, f = id.f;
+      const Tile t = info(n);
+      uint32_t pk[32];                             // the 64 results in bf16
+      int d = -1;                                  // the destination row
+      if (!kGU) {
+        const uint32_t at = sbase + S::META + (n & 1) * 1024 + f * 4;
+        d = static_cast<int>(ld_shared_u32(at));
+        const float w = ptx::ld_shared_f32(at + 512);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)               // one f32 multiply, then the one bf16 rounding
+          pk[i] = gemm::pack_bf16x2(__fmul_rn(sum[2 * i], w), __fmul_rn(sum[2 * i + 1], w));
+      } else {
+        if (f < t.n_tok) d = t.r0 + f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = gemm::pack_bf16x2(sum[2 * i], sum[2 * i + 1]);
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_iempty(n & 1));
+      // Eight rows at a time through the warp's 1 KB, so that eight lanes store a row's 128 bytes:
+      // stores of single 32-byte sectors took 4500 cycles a tile, as long as five scale blocks.
+      const int col = kGU ? t.n0 + 64 * set + 32 * h : t.n0 + 128 * set + 64 * h;
+      const uint32_t st = sbase + S::EPI + ((id.e & 3) * 4 + 2 * set + h) * 1024;
+      if (!kGU || p.out) {
+        const int piece = lane & 7, row_stride = kGU ? 2 * p.N : p.N;
+        const int cc = kGU ? col + 8 * (piece & 3) : col + 8 * piece;
+        uint16_t* o = p.out + cc + (kGU && piece < 4 ? p.N : 0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if ((lane >> 3) == q) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              ptx::st_shared_v4(st + piece * 128 + ((c ^ piece) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = 4 * i + (lane >> 3);
+            const uint4 val = ptx::ld_shared_v4(st + row * 128 + ((piece ^ row) << 4));
+            const int dr = __shfl_sync(0xffffffffu, d, 8 * q + row);
+            if (dr >= 0 && cc < p.N) *reinterpret_cast<uint4*>(o + static_cast<size_t>(dr) * row_stride) = val;
+          }
+          __syncwarp();
+        }
+      }
+      if (kGU) {
+        float act[32], m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          act[2 * i] = silu_mul(__uint_as_float(pk[16 + i] << 16), __uint_as_float(pk[i] << 16));
+          act[2 * i + 1] = silu_mul(__uint_as_float(pk[16 + i] & 0xFFFF0000u), __uint_as_float(pk[i] & 0xFFFF0000u));
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (col + (i & 16) < p.N) m = fmaxf(m, fabsf(act[i]));        // N % 16 == 0
+        // the four threads of a row, in four warps of the same rows
+        const uint32_t s_max = sbase + S::META + f * 4;                 // [4][128 rows]
+        ptx::st_shared_f32(s_max + (2 * set + h) * 512, m);
+        ptx::bar_sync(6 + (warp & 3), 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, ptx::ld_shared_f32(s_max + i * 512));
+        float dd, inv;
+        block_scale(m, dd, inv);
+        if (h + set == 0 && d >= 0) p.act_scale[static_cast<size_t>(d) * blocks_of(p.N) + t.n0 / kBlk] = dd;
+        // the four warps' 4 KB hold their rows' codes; eight lanes store a row's 128 bytes
+        const uint32_t rows = sbase + S::EPI + (warp & 3) * 4096;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = act[16 * i + k];
+          const uint4 c = codes16(x, inv);
+          ptx::st_shared_v4(rows + lane * 128 + (((4 * set + 2 * h + i) ^ (lane & 7)) << 4), c.x, c.y, c.z, c.w);
+        }
+        ptx::bar_sync(6 + (warp & 3), 128);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = (2 * set + h) * 8 + 4 * i + (lane >> 3), piece = lane & 7;
+          const uint4 val = ptx::ld_shared_v4(rows + row * 128 + ((piece ^ (row & 7)) << 4));
+          const int dr = __shfl_sync(0xffffffffu, d, row), cc = t.n0 + 16 * piece;
+          if (dr >= 0 && cc < p.N) *reinterpret_cast<uint4*>(p.act + static_cast<size_t>(dr) * p.N + cc) = val;
+        }
+      }
+    }
+    // ------------------------------------------------------------ weights tiles
+    const int total = sch.total();
+    for (; on && tile < total; tile += gridDim.x, ++n) {
+      if (!wait_info(n)) {
+        ptx::bar_and(5, 32 * kEpiWarps, false);
+        break;
+      }
+      const Ids id(warp, lane);
+      const int h = id.h, set = id.set, f = id.f, ht = id.ht;
+      const Tile t = info(n);
+      const uint32_t dst_t = sbase + S::META + (n & 1) * 1024, w_t = dst_t + 512;   // plain
       // half h joins the rows 32 h .. of the tile; where the second half has none, the first
       // one's warps arrive on the accumulators' barriers for both
       float sum[32];
@@ -587,21 +674,26 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         const int acc_shift = ld_shared_u32(sbase + S::MISC + S::kSmall) ? 3 : 2;
         const uint32_t acc_mask = (1u << acc_shift) - 1u, acc_cols = 512u >> acc_shift;
         const uint32_t n_arrive = t.n_tok > 32 ? 1 : 2;
-        const int wr = kGU ? t.n0 + f + (set == 0 ? p.N : 0) : t.n0 + 128 * set + f;   // this thread's weight row
-        const int rb = blocks_of(kp.rows_per_group);
-        const float* sw_p = p.sw + (static_cast<size_t>(t.g) * rb + min(wr / kBlk, rb - 1)) * nk;
-        const float* sa_p = p.sa + static_cast<size_t>(t.r0 + min(32 * h + lane, t.n_tok - 1)) * nk;
-        const uint32_t fac = sbase + S::FAC + e * 256;
         const bool wide = t.n_tok > 32 * h + 16;
         const uint32_t taddr0 = id.tmem(tmem_base) + 32 * h;
-        float a0 = __ldg(sa_p), w0 = __ldg(sw_p);
+        uint32_t w_at = kChunkW + set * kChunk * 4;
+        if (kGU) {
+          const int up = p.N + t.n0;
+          w_at = kChunkW + (f < 64 ? 1 + (up + 64 * set + f) / kBlk - up / kBlk : 0) * kChunk * 4;
+        }
+        uint32_t sc = 0;
         for (int kb = 0; kb < nk; ++kb) {
-          const float s = w0;
-          const uint32_t fk = fac + (kb & 1) * 128;
-          ptx::st_shared_f32(fk + lane * 4, a0);
-          const int next = min(kb + 1, nk - 1);      // the next block's scales, on their way
-          a0 = __ldg(sa_p + next);
-          w0 = __ldg(sw_p + next);
+          if ((kb & (kChunk - 1)) == 0) {
+            if (kb > 0) {
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(bar_sempty(q & 1));
+              ++q;
+            }
+            wait_lean(bar_sfull(q & 1), (q >> 1) & 1u, sbase + S::MISC);
+            sc = sbase + S::SCALE + (q & 1) * kChunkBytes;
+          }
+          const uint32_t fk = sc + (kb & (kChunk - 1)) * kRowStride + 128 * h;
+          const float s = ptx::ld_shared_f32(sc + w_at + (kb & (kChunk - 1)) * 4);
           const uint32_t acc = parts & acc_mask;
           wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, sbase + S::MISC);
           ptx::tc_fence_after();
@@ -622,11 +714,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           }
           parts += 2;
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_sempty(q & 1));
+        ++q;
       } else {
         parts += 2 * nk;
+        for (int kb = 0; kb < nk; kb += kChunk, ++q) {   // every phase is seen, every chunk released
+          wait_lean(bar_sfull(q & 1), (q >> 1) & 1u, sbase + S::MISC);
+          if (lane == 0) ptx::mbar_arrive(bar_sempty(q & 1));
+        }
       }
-      // one decision for the sixteen warps (and those without rows wait for the others);
-      // the barrier also publishes dst_t / w_t
+      // one decision for the sixteen warps (and those without rows wait for the others)
       if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + S::kAbort) == 0)) break;
       // 16 rows of the half at a time through its 8 KB of staging: [16 rows][256 weight rows] bf16,
       // 16-byte pieces XOR-swizzled by the row
@@ -644,7 +742,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
 #pragma unroll
           for (int k = 0; k < 4; ++k) x[k] = sum[16 * c + 4 * i + k];
           if (!kGU && p.pair_weight) {           // one f32 multiply, then the one bf16 rounding
-            const uint4 w4 = ptx::ld_shared_v4(ptx::smem_u32(w_t) + 4 * j0 + 16 * i);
+            const uint4 w4 = ptx::ld_shared_v4(w_t + 4 * j0 + 16 * i);
             x[0] = __fmul_rn(x[0], __uint_as_float(w4.x));
             x[1] = __fmul_rn(x[1], __uint_as_float(w4.y));
             x[2] = __fmul_rn(x[2], __uint_as_float(w4.z));
@@ -666,16 +764,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
             const int jj = (ht >> 5) + 8 * i;
             const int cc = t.n0 + 8 * lane;
             if (j0 + jj < t.n_tok && cc < p.N) {
-              const int d = dst_t[j0 + jj];
+              const int d = static_cast<int>(ld_shared_u32(dst_t + 4 * (j0 + jj)));
               const uint4 val = ptx::ld_shared_v4(ost + jj * 512 + ((lane ^ jj) << 4));
               if (d >= 0) *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(d) * p.N + cc) = val;
             }
           }
         } else {
-          // sixteen threads hold a row: up pieces first, then gate
+          // sixteen threads hold a row; 8 pieces of up, 8 of gate, and the other 64 features' ones
           const uint32_t row = ost + tok * 512;
-          const uint4 u4 = ptx::ld_shared_v4(row + ((oct ^ tok) << 4));
-          const uint4 g4 = ptx::ld_shared_v4(row + (((oct + 16) ^ tok) << 4));
+          const int piece = (oct >> 3) * 16 + (oct & 7);
+          const uint4 u4 = ptx::ld_shared_v4(row + ((piece ^ tok) << 4));
+          const uint4 g4 = ptx::ld_shared_v4(row + (((piece + 8) ^ tok) << 4));
           const bool in = col < p.N;             // N % 16 == 0
           const bool live = j0 + tok < t.n_tok;
           const size_t r = static_cast<size_t>(t.r0 + j0 + tok);
@@ -705,6 +804,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         }
         ptx::bar_sync(1 + h, 256);
       }
+      if (lane == 0) ptx::mbar_arrive(bar_iempty(n & 1));
     }
   }
 
@@ -767,7 +867,7 @@ int launch_product(const char* op, const GemmParams& p0, bool gateup, cudaStream
   // 128-byte swizzle as a bf16 operand's box
   for (int i = 0; i < 4; ++i)
     if ((rc = gemm::make_tmap(&tt[i], p.a, p.P, p.K / 2, 16 << i, op, "a_codes")) != MOE_OK) return rc;
-  if ((rc = gemm::make_tmap(&tw, p.w, static_cast<long long>(p.G) * rows, p.K / 2, 128,
+  if ((rc = gemm::make_tmap(&tw, p.w, static_cast<long long>(p.G) * rows, p.K / 2, gateup ? 64 : 128,
                             op, "weights")) != MOE_OK)
     return rc;
   DeviceDiag diag = device_diag();

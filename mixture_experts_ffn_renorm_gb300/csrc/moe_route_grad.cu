@@ -100,8 +100,8 @@ struct DwSmem {
   static constexpr int A = 0;                          // 2 stages x 3 parts x 2 blocks of 64 experts
   static constexpr int B = A + 2 * 6 * kBlk;           // kBStages x 2 blocks of 64 columns
   static constexpr int DB = B + kBStages * 2 * kBlk;   // db: [16 token rows][128] f32
-  static constexpr int BARS = DB + 16 * 128 * 4;       // fullA, empty, done [2], fullB [kBStages]
-  static constexpr int MISC = BARS + 48 + 8 * kBStages;
+  static constexpr int BARS = DB + 16 * 128 * 4;       // fullA, empty, done [2], fullB [kBStages], drain
+  static constexpr int MISC = BARS + 48 + 8 * (kBStages + 1);
   static constexpr int ALLOC = MISC + 16 + 1024;
 };
 
@@ -128,6 +128,7 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
   auto empty = [&](int s) { return sb + S::BARS + 16 + 8u * s; };
   auto done = [&](int a) { return sb + S::BARS + 32 + 8u * a; };
   auto full_b = [&](int s) { return sb + S::BARS + 48 + 8u * s; };
+  const uint32_t drain = full_b(kBStages);
   count_launch(p.launches, MOE_KID_ROUTE_DW);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -136,6 +137,7 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
     }
     for (int s = 0; s < kBStages; ++s) ptx::mbar_init(full_b(s), 1);
     for (int a = 0; a < 2; ++a) ptx::mbar_init(done(a), 1);
+    ptx::mbar_init(drain, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -208,7 +210,9 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
     float sum[64];                 // expert e0 + TMEM lane, columns 64 (warp / 4) + 0 .. 63
 #pragma unroll
     for (int k = 0; k < 64; ++k) sum[k] = 0.0f;
-    bool ok = true;   // a thread that gives up still meets the others at the chunks' ends
+    // a thread that gives up (ok) still meets the others at the chunks' ends, where all of
+    // them leave together (on)
+    bool ok = true, on = true;
     // adds chunk c's accumulators to the sums; the issuer takes them again two chunks on, after
     // this thread's arrive on that chunk's first operands
     auto take = [&](int c) {
@@ -258,10 +262,13 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
       // the chunk before, while this one is multiplied
       if (i % kChunk == 0 && i > 0) {
         take(i / kChunk - 1);
-        if (!ok) break;            // all of them
+        if (!ok) {                 // in all of them
+          on = false;
+          break;
+        }
       }
     }
-    if (mul && ok) take((steps - 1) / kChunk);
+    if (mul && on) take((steps - 1) / kChunk);
     if (mul && ok) {
       const int row = (warp & 3) * 32 + lane, h = h0 + (warp >> 2) * 64;
       if (e0 + row < p.E) {
@@ -288,10 +295,8 @@ route_dw_kernel(const __grid_constant__ CUtensorMap tmX, const DwParams p) {
   // ---- exit: a CTA that gave up drains its copies and MMAs first
   __syncthreads();
   if (*abort_flag != 0 && issued != 0) {
-    ptx::mma_commit(done(0));
-    const uint64_t g0 = ptx::globaltimer_ns();
-    while (ptx::globaltimer_ns() - g0 < 100000ull) {
-    }
+    ptx::mma_commit(drain);
+    gemm::spin_bounded(drain, 0);
     for (uint32_t i = issued < kBStages ? 0 : issued - kBStages; i < issued; ++i)
       gemm::spin_bounded(full_b(i % kBStages), (i / kBStages) & 1);
   }
@@ -332,7 +337,7 @@ route_reduce_kernel(const float* __restrict__ part_w, const float* __restrict__ 
 struct DxSmem {
   static constexpr int A = 0;                          // 2 parts x 128 tokens x 128 bytes (64 experts)
   static constexpr int B = A + 2 * 2 * kBlk;           // 4 blocks of 64 columns x 64 experts
-  static constexpr int BARS = B + 4 * kBlk;            // fullA, fullB, done
+  static constexpr int BARS = B + 4 * kBlk;            // fullA, fullB, done, drain
   static constexpr int MISC = BARS + 32;
   static constexpr int ALLOC = MISC + 16 + 1024;
 };
@@ -354,12 +359,13 @@ route_dx_kernel(const __grid_constant__ CUtensorMap tmW, const DxParams p) {
   const uint32_t sb = ptx::smem_u32(smem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t full_a = sb + S::BARS, full_b = sb + S::BARS + 8, done = sb + S::BARS + 16;
+  const uint32_t full_a = sb + S::BARS, full_b = sb + S::BARS + 8, done = sb + S::BARS + 16, drain = sb + S::BARS + 24;
   count_launch(p.launches, MOE_KID_ROUTE_DX);
   if (threadIdx.x == 0) {
     ptx::mbar_init(full_a, kConv);
     ptx::mbar_init(full_b, 1);
     ptx::mbar_init(done, 1);
+    ptx::mbar_init(drain, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -472,10 +478,8 @@ route_dx_kernel(const __grid_constant__ CUtensorMap tmW, const DxParams p) {
   }
   __syncthreads();
   if (*abort_flag != 0 && issued != 0) {
-    ptx::mma_commit(done);
-    const uint64_t g0 = ptx::globaltimer_ns();
-    while (ptx::globaltimer_ns() - g0 < 100000ull) {
-    }
+    ptx::mma_commit(drain);
+    gemm::spin_bounded(drain, 0);
     gemm::spin_bounded(full_b, (issued - 1) & 1);
   }
   __syncthreads();

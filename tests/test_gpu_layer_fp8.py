@@ -126,6 +126,25 @@ def test_backward(T, H, I, E, K):
         assert torch.equal(again[k].cpu(), v), k
 
 
+@pytest.mark.parametrize("T", [3, 80])
+def test_shared_expert_beside_fp8_activations(T):
+    # the shared expert stays bf16: the block's output is the routed part plus the gated shared rows
+    cfg = W.LayerConfig("s", T=T, H=256, I=128, E=8, K=2, I_shared=64)
+    d = W.layer_inputs(cfg)
+    d["w13_e4m3"], d["w13_scale"] = W.quantize_fp8_block(d["w13"])
+    d["w2_e4m3"], d["w2_scale"] = W.quantize_fp8_block(d["w2"])
+    blk = MoeBlock(256, 128, 8, 2, d, I_shared=64, max_tokens=T, fp8_weights=True, fp8_acts=True)
+    x = to_dev(d["x"])
+    out = blk.forward(x)
+    blk.logit_bias = torch.zeros(8, device=DEV)
+    want, *_ = layer64(blk, x, blk.topk_ids[:T])
+    xd = x.double().cpu()
+    g, u = (xd @ blk.w13_shared[0].double().cpu().t()).split(64, 1)
+    y = (torch.nn.functional.silu(g) * u) @ blk.w2_shared[0].double().cpu().t()
+    gate = torch.sigmoid(xd @ blk.w_shared_gate.double().cpu().reshape(-1, 1))
+    assert rel(out.cpu(), (want + gate * y).detach()) < 0.125
+
+
 def test_block_refuses_what_it_lacks():
     cfg = W.LayerConfig("r", T=4, H=64, I=32, E=4, K=2)
     d = W.layer_inputs(cfg)
