@@ -62,9 +62,37 @@ __device__ __forceinline__ uint64_t ld_shared_u64(uint32_t addr) {
   return v;
 }
 
+// Two f32 values in one register pair: one instruction joins both, and the joins' issue slots
+// are what bounds a block next to its MMAs.  Each half is rounded like the scalar operation.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ uint64_t pair(float v) { return pair(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+  const float2 f = unpair(v);
+  return gemm::pack_bf16x2(f.x, f.y);
+}
+
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of other roles (one of its warps idle)
-constexpr int kAuxRegs = 48, kEpiRegs = 104;
+constexpr int kAuxRegs = 64, kEpiRegs = 104;
 // the split draws on the registers the block was launched with (96 a thread)
 static_assert(128 * kAuxRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 96, "register split");
 constexpr int kTokBlock = 128;              // rows per rows tile
@@ -139,8 +167,10 @@ struct KernelParams {
 // scale blocks have no registers left to carry it through.
 struct Ids {
   int e, h, set, f, et, ht;
-  __device__ __forceinline__ Ids(int warp, int lane) {
-    asm volatile("" : "+r"(warp), "+r"(lane));
+  __device__ __forceinline__ Ids() {
+    int tid;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+    const int warp = tid >> 5, lane = tid & 31;
     e = warp - 4;                      // 0..15
     h = (e >> 2) & 1;                  // half of the columns of a part
     set = e >> 3;                      // the part
@@ -476,9 +506,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     ptx::setmaxnreg_inc<kEpiRegs>();
     // this role's own copies: what is carried over from before the register split is spilled,
     // and reloaded in the loops
-    int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t sbase = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-    asm volatile("" : "+r"(warp), "+r"(lane), "+r"(sbase));
+    asm volatile("" : "+r"(sbase));
     const uint32_t tmem_base = ld_shared_u32(sbase + S::MISC);
     const int nk = blocks_of(p.K);
     const Schedule sch{sbase, p.G, p.N, kFbCols};
@@ -501,7 +530,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       t.n0 = v.w;
       return t;
     };
-    uint32_t parts = (warp - 4) >> 3;   // the part's place among the accumulators passed so far
+    uint32_t parts = Ids().set;   // the part's place among the accumulators passed so far
     uint32_t n = 0, q = 0;              // tiles and chunks passed
     int tile = blockIdx.x;
     bool on = true;
@@ -512,37 +541,32 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         on = false;
         break;
       }
-      float sum[64];   // gate/up: 32 features' up, then their gate
+      uint64_t sum[32];   // 64 columns; gate/up: 32 features' up, then their gate
 #pragma unroll
-      for (int i = 0; i < 64; ++i) sum[i] = 0.0f;
-      uint32_t taddr0, row4, w_at, u0_at = 0, u1_at = 0;   // row4 and below: within a chunk
+      for (int i = 0; i < 32; ++i) sum[i] = 0;
+      uint32_t taddr0, w_at, to_u0 = 0, to_u1 = 0;   // w_at: within a chunk; the others from there
       {
-        const Ids id(warp, lane);
+        const Ids id;
         taddr0 = id.tmem(tmem_base) + (kGU ? 32 : 64) * id.h;
-        row4 = id.f * 4;
         w_at = kChunkW + (kGU ? 0 : id.set * kChunk * 4);
         if (kGU) {
           const int up = p.N + info(n).n0, ur = up + 64 * id.set + 32 * id.h;
-          u0_at = kChunkW + (1 + ur / kBlk - up / kBlk) * kChunk * 4;
-          u1_at = kChunkW + (1 + (ur + 16) / kBlk - up / kBlk) * kChunk * 4;
+          to_u0 = (1 + ur / kBlk - up / kBlk) * kChunk * 4;
+          to_u1 = (1 + (ur + 16) / kBlk - up / kBlk) * kChunk * 4;
         }
       }
-      uint32_t sc = 0;                             // the chunk's address, 4 bytes on per block
 #pragma unroll 1
-      for (int kb = 0; kb < nk; ++kb) {
-        if ((kb & (kChunk - 1)) == 0) {
-          if (kb > 0) {
-            if (lane == 0) ptx::mbar_arrive(bar_sempty(q & 1));
-            ++q;
-          }
-          wait_lean(bar_sfull(q & 1), (q >> 1) & 1u, sbase + S::MISC);
-          sc = sbase + S::SCALE + (q & 1) * kChunkBytes;
-        }
-        const float a0 = ptx::ld_shared_f32(sc + (kb & (kChunk - 1)) * (kRowStride - 4) + row4);
-        const float s0 = __fmul_rn(a0, ptx::ld_shared_f32(sc + w_at));
-        const float s1 = kGU ? __fmul_rn(a0, ptx::ld_shared_f32(sc + u0_at)) : 0.0f;
-        const float s2 = kGU ? __fmul_rn(a0, ptx::ld_shared_f32(sc + u1_at)) : 0.0f;
-        sc += 4;
+      for (int left = nk; left > 0; left -= kChunk) {
+      wait_lean(bar_sfull(q & 1), (q >> 1) & 1u, sbase + S::MISC);
+      uint32_t row_at = sbase + S::SCALE + (q & 1) * kChunkBytes;
+      uint32_t wt_at = row_at + w_at;
+      row_at += Ids().f * 4;
+#pragma unroll 1
+      for (const uint32_t end = wt_at + 4 * min(left, kChunk); wt_at != end; wt_at += 4, row_at += kRowStride) {
+        const float a0 = ptx::ld_shared_f32(row_at);
+        const float s0 = __fmul_rn(a0, ptx::ld_shared_f32(wt_at));
+        const float s1 = kGU ? __fmul_rn(a0, ptx::ld_shared_f32(wt_at + to_u0)) : 0.0f;
+        const float s2 = kGU ? __fmul_rn(a0, ptx::ld_shared_f32(wt_at + to_u1)) : 0.0f;
         const uint32_t acc = parts & 3u;
         wait_lean(bar_tfull(acc), (parts >> 2) & 1u, sbase + S::MISC);
         ptx::tc_fence_after();
@@ -554,24 +578,25 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           ptx::tmem_ld_wait();
           if (c == 3) {                            // the warp has read all of it
             ptx::tc_fence_before();
-            if (lane == 0) ptx::mbar_arrive(bar_tempty(acc));
+            if (ptx::elect_one()) ptx::mbar_arrive(bar_tempty(acc));
           }
-          const float s = !kGU || c > 1 ? s0 : (c == 0 ? s1 : s2);
+          const uint64_t s = pair(!kGU || c > 1 ? s0 : (c == 0 ? s1 : s2));
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sum[16 * c + i] = fmaf(__uint_as_float(v[i]), s, sum[16 * c + i]);
+          for (int i = 0; i < 8; ++i) sum[8 * c + i] = fma2(pair(v[2 * i], v[2 * i + 1]), s, sum[8 * c + i]);
         }
         parts += 2;
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar_sempty(q & 1));
+      if (ptx::elect_one()) ptx::mbar_arrive(bar_sempty(q & 1));
       ++q;
+      }
       // one decision for the sixteen warps
       if (!ptx::bar_and(5, 32 * kEpiWarps, ld_shared_u32(sbase + S::MISC + S::kAbort) == 0)) {
         on = false;
         break;
       }
-      const Ids id(warp, lane);
-      const int h = id.h, set = id.set, f = id.f;
+      const Ids id;
+      const int h = id.h, set = id.set, f = id.f, lane = f & 31;
       const Tile t = info(n);
       uint32_t pk[32];                             // the 64 results in bf16
       int d = -1;                                  // the destination row
@@ -581,11 +606,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         const float w = ptx::ld_shared_f32(at + 512);
 #pragma unroll
         for (int i = 0; i < 32; ++i)               // one f32 multiply, then the one bf16 rounding
-          pk[i] = gemm::pack_bf16x2(__fmul_rn(sum[2 * i], w), __fmul_rn(sum[2 * i + 1], w));
+          pk[i] = pack_bf16(mul2(sum[i], pair(w)));
       } else {
         if (f < t.n_tok) d = t.r0 + f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) pk[i] = gemm::pack_bf16x2(sum[2 * i], sum[2 * i + 1]);
+        for (int i = 0; i < 32; ++i) pk[i] = pack_bf16(sum[i]);
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar_iempty(n & 1));
@@ -628,14 +653,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         // the four threads of a row, in four warps of the same rows
         const uint32_t s_max = sbase + S::META + f * 4;                 // [4][128 rows]
         ptx::st_shared_f32(s_max + (2 * set + h) * 512, m);
-        ptx::bar_sync(6 + (warp & 3), 128);
+        ptx::bar_sync(6 + (f >> 5), 128);
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = fmaxf(m, ptx::ld_shared_f32(s_max + i * 512));
         float dd, inv;
         block_scale(m, dd, inv);
         if (h + set == 0 && d >= 0) p.act_scale[static_cast<size_t>(d) * blocks_of(p.N) + t.n0 / kBlk] = dd;
         // the four warps' 4 KB hold their rows' codes; eight lanes store a row's 128 bytes
-        const uint32_t rows = sbase + S::EPI + (warp & 3) * 4096;
+        const uint32_t rows = sbase + S::EPI + (f >> 5) * 4096;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float x[16];
@@ -644,7 +669,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           const uint4 c = codes16(x, inv);
           ptx::st_shared_v4(rows + lane * 128 + (((4 * set + 2 * h + i) ^ (lane & 7)) << 4), c.x, c.y, c.z, c.w);
         }
-        ptx::bar_sync(6 + (warp & 3), 128);
+        ptx::bar_sync(6 + (f >> 5), 128);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int row = (2 * set + h) * 8 + 4 * i + (lane >> 3), piece = lane & 7;
@@ -661,15 +686,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         ptx::bar_and(5, 32 * kEpiWarps, false);
         break;
       }
-      const Ids id(warp, lane);
-      const int h = id.h, set = id.set, f = id.f, ht = id.ht;
+      const Ids id;
+      const int h = id.h, set = id.set, f = id.f, ht = id.ht, lane = f & 31;
       const Tile t = info(n);
       const uint32_t dst_t = sbase + S::META + (n & 1) * 1024, w_t = dst_t + 512;   // plain
       // half h joins the rows 32 h .. of the tile; where the second half has none, the first
       // one's warps arrive on the accumulators' barriers for both
-      float sum[32];
+      uint64_t sum[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) sum[i] = 0.0f;
+      for (int i = 0; i < 16; ++i) sum[i] = 0;
       if (32 * h < t.n_tok) {
         const int acc_shift = ld_shared_u32(sbase + S::MISC + S::kSmall) ? 3 : 2;
         const uint32_t acc_mask = (1u << acc_shift) - 1u, acc_cols = 512u >> acc_shift;
@@ -693,7 +718,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
             sc = sbase + S::SCALE + (q & 1) * kChunkBytes;
           }
           const uint32_t fk = sc + (kb & (kChunk - 1)) * kRowStride + 128 * h;
-          const float s = ptx::ld_shared_f32(sc + w_at + (kb & (kChunk - 1)) * 4);
+          const uint64_t s2 = pair(ptx::ld_shared_f32(sc + w_at + (kb & (kChunk - 1)) * 4));
           const uint32_t acc = parts & acc_mask;
           wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, sbase + S::MISC);
           ptx::tc_fence_after();
@@ -706,10 +731,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           for (int i = 0; i < 8; ++i) {
             if (i < 4 || wide) {
               const uint4 a4 = ptx::ld_shared_v4(fk + 16 * i);
-              sum[4 * i] = fmaf(__uint_as_float(v[4 * i]), __fmul_rn(__uint_as_float(a4.x), s), sum[4 * i]);
-              sum[4 * i + 1] = fmaf(__uint_as_float(v[4 * i + 1]), __fmul_rn(__uint_as_float(a4.y), s), sum[4 * i + 1]);
-              sum[4 * i + 2] = fmaf(__uint_as_float(v[4 * i + 2]), __fmul_rn(__uint_as_float(a4.z), s), sum[4 * i + 2]);
-              sum[4 * i + 3] = fmaf(__uint_as_float(v[4 * i + 3]), __fmul_rn(__uint_as_float(a4.w), s), sum[4 * i + 3]);
+              const uint64_t lo = mul2(pair(a4.x, a4.y), s2), hi = mul2(pair(a4.z, a4.w), s2);
+              sum[2 * i] = fma2(pair(v[4 * i], v[4 * i + 1]), lo, sum[2 * i]);
+              sum[2 * i + 1] = fma2(pair(v[4 * i + 2], v[4 * i + 3]), hi, sum[2 * i + 1]);
             }
           }
           parts += 2;
@@ -738,19 +762,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         if (j0 >= t.n_tok) continue;             // the same for the whole half
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = sum[16 * c + 4 * i + k];
+          uint64_t x[2] = {sum[8 * c + 2 * i], sum[8 * c + 2 * i + 1]};
           if (!kGU && p.pair_weight) {           // one f32 multiply, then the one bf16 rounding
             const uint4 w4 = ptx::ld_shared_v4(w_t + 4 * j0 + 16 * i);
-            x[0] = __fmul_rn(x[0], __uint_as_float(w4.x));
-            x[1] = __fmul_rn(x[1], __uint_as_float(w4.y));
-            x[2] = __fmul_rn(x[2], __uint_as_float(w4.z));
-            x[3] = __fmul_rn(x[3], __uint_as_float(w4.w));
+            x[0] = mul2(x[0], pair(w4.x, w4.y));
+            x[1] = mul2(x[1], pair(w4.z, w4.w));
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {          // gate/up: narrowed before the activation
-            const uint32_t pk = gemm::pack_bf16x2(x[2 * k], x[2 * k + 1]);
+            const uint32_t pk = pack_bf16(x[k]);
             const int jj = 4 * i + 2 * k;
             ptx::st_shared_u16((place ^ (jj << 4)) + jj * 512, static_cast<uint16_t>(pk));
             ptx::st_shared_u16((place ^ ((jj + 1) << 4)) + (jj + 1) * 512, static_cast<uint16_t>(pk >> 16));
