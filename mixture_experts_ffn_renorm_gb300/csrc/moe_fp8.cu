@@ -35,17 +35,21 @@ quant_rows_kernel(const uint16_t* __restrict__ x, int T, int H, int K,
   const int t = static_cast<int>(item / chunks);
   const int col = static_cast<int>(item % chunks) * 512 + lane * 16;
   const bool live = col < H;   // H % 16 == 0
-  float v[16];
   uint4 a = make_uint4(0, 0, 0, 0), b = a;
   if (live) {
     const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(t) * H + col);
     a = __ldg(src);
     b = __ldg(src + 1);
   }
-  widen16(a, b, v);
-  float amax = 0.0f;
+  const uint32_t raw[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint64_t v[8];
+  __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));   // fmaxf skips NaN
+  for (int i = 0; i < 8; ++i) {
+    v[i] = pair(raw[i] << 16, raw[i] & 0xFFFF0000u);
+    top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i])));   // skips NaN
+  }
+  float amax = fmaxf(__low2float(top), __high2float(top));
 #pragma unroll
   for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (!live) return;
@@ -54,9 +58,10 @@ quant_rows_kernel(const uint16_t* __restrict__ x, int T, int H, int K,
   uint4 same = make_uint4(0, 0, 0, 0);
   float same_d = 0.0f;
   if (!pair_weight) {   // one factor for all rows: one set of codes
-    float w[16], id;
+    uint64_t w[8];
+    float id;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __fmul_rn(v[i], routed_scale);
+    for (int i = 0; i < 8; ++i) w[i] = mul2(v[i], pair(routed_scale));
     block_scale(__fmul_rn(amax, fabsf(routed_scale)), same_d, id);
     same = codes16(w, id);
   }
@@ -68,9 +73,10 @@ quant_rows_kernel(const uint16_t* __restrict__ x, int T, int H, int K,
     float d = same_d;
     if (pair_weight) {
       const float f = __fmul_rn(__ldg(pair_weight + p), routed_scale);
-      float w[16], id;
+      uint64_t w[8];
+      float id;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = __fmul_rn(v[i], f);
+      for (int i = 0; i < 8; ++i) w[i] = mul2(v[i], pair(f));
       block_scale(__fmul_rn(amax, fabsf(f)), d, id);
       out = codes16(w, id);
     }

@@ -62,29 +62,6 @@ __device__ __forceinline__ uint64_t ld_shared_u64(uint32_t addr) {
   return v;
 }
 
-// Two f32 values in one register pair: one instruction joins both, and the joins' issue slots
-// are what bounds a block next to its MMAs.  Each half is rounded like the scalar operation.
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ uint64_t pair(float v) { return pair(__float_as_uint(v), __float_as_uint(v)); }
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
   const float2 f = unpair(v);
   return gemm::pack_bf16x2(f.x, f.y);
@@ -614,28 +591,32 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar_iempty(n & 1));
-      // Eight rows at a time through the warp's 1 KB, so that eight lanes store a row's 128 bytes:
-      // stores of single 32-byte sectors took 4500 cycles a tile, as long as five scale blocks.
+      // Sixteen rows and 32 columns at a time through the warp's 1 KB, so that four lanes store
+      // 64 bytes of a row.
       const int col = kGU ? t.n0 + 64 * set + 32 * h : t.n0 + 128 * set + 64 * h;
       const uint32_t st = sbase + S::EPI + ((id.e & 3) * 4 + 2 * set + h) * 1024;
       if (!kGU || p.out) {
-        const int piece = lane & 7, row_stride = kGU ? 2 * p.N : p.N;
-        const int cc = kGU ? col + 8 * (piece & 3) : col + 8 * piece;
-        uint16_t* o = p.out + cc + (kGU && piece < 4 ? p.N : 0);
+        const int row_stride = kGU ? 2 * p.N : p.N;
+        // this lane's pieces: of row `lane`, and to be stored, of row 8 i + lane / 4
+        const uint32_t mine = st + (lane & 15) * 64, swz = (lane >> 1) & 3;
+        const uint32_t from = st + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if ((lane >> 3) == q) {
+        for (int q = 0; q < 4; ++q) {              // q & 1: half of the columns (gate/up: up, gate)
+          const int cc = col + 8 * (lane & 3) + (kGU ? 0 : 32 * (q & 1));
+          if ((lane >> 4) == (q >> 1)) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              ptx::st_shared_v4(st + piece * 128 + ((c ^ piece) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+            for (int c = 0; c < 4; ++c) {
+              const int k = 16 * (q & 1) + 4 * c;
+              ptx::st_shared_v4(mine + ((c ^ swz) << 4), pk[k], pk[k + 1], pk[k + 2], pk[k + 3]);
+            }
           }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int row = 4 * i + (lane >> 3);
-            const uint4 val = ptx::ld_shared_v4(st + row * 128 + ((piece ^ row) << 4));
-            const int dr = __shfl_sync(0xffffffffu, d, 8 * q + row);
-            if (dr >= 0 && cc < p.N) *reinterpret_cast<uint4*>(o + static_cast<size_t>(dr) * row_stride) = val;
+            const uint4 val = ptx::ld_shared_v4(from + i * 512);
+            const int dr = __shfl_sync(0xffffffffu, d, 16 * (q >> 1) + 8 * i + (lane >> 2));
+            if (dr >= 0 && cc < p.N)
+              *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(dr) * row_stride + cc + (kGU && q % 2 == 0 ? p.N : 0)) = val;
           }
           __syncwarp();
         }

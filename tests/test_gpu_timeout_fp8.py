@@ -75,7 +75,7 @@ def test_expiry_is_reported_and_the_device_stays_usable(calls, size):
         before = launches()
         assert call() == m.OK                   # the launch itself is accepted
         torch.cuda.synchronize()                # and the kernel ends
-        assert launched_since(before, kid) == 1
+        assert launched_since(before, kid) >= 1
         assert m.moe_device_status(clear=True) & m.STATUS_TIMEOUT, kid
         m.moe_set_wait_limit_ns(FULL_LIMIT_NS)
         for o in outs:
