@@ -96,6 +96,11 @@ __device__ __forceinline__ uint4 codes16(const uint64_t (&v)[8], float id) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// silu(g) u; tolerance-checked: the fast exponential and division serve
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
 struct GemmParams {
   const uint8_t* a;
   const float* sa;               // [P, blocks(K)]
@@ -114,6 +119,14 @@ struct GemmParams {
 // the products on the tensor cores (moe_fp8_gemm.cu); gateup: SiLU-mul and
 // quantised activations.  Arguments already checked.
 int launch_product(const char* op, const GemmParams& p, bool gateup, cudaStream_t stream);
+
+// the same for calls of few dot products (rows times weight rows), where a warp per 4 columns
+// reads the weights (moe_fp8_few.cu).  Its time grows with the products, that of the tiles
+// with the columns of a row: 7.8 us against 11.5 (12288 products of 2048), 4.6 against 6.9
+// (16384 of 768), 9.1 against 13.9 (16384 of 4096); 7.8 against 7.8 (32768 of 768), 8.9
+// against 9.4 (32768 of 2048), 17.3 against 14.5 (24576 of 2048 with gate/up).
+constexpr int kFewRows = 16, kFewProducts = 16384;
+int launch_few(const char* op, const GemmParams& p, bool gateup, cudaStream_t stream);
 
 }  // namespace fp8
 }  // namespace moe

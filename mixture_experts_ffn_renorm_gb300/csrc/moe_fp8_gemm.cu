@@ -20,24 +20,30 @@
 //                  32 of the token rows, whose scales its warp keeps in shared memory.
 // Rows tiles need no transpose and no scale loads per product, and pad to 128 rows;
 // weights tiles pad to 16 rows, which is what ragged and decode-sized groups need.
-// Every block makes the round trip MMA -> join -> MMA, so its latency counts more
-// than the bytes that a CTA pair would save: on pairs (256 x 256 tiles, 32 instead
-// of 48 KB a stage and SM) the barriers of the trip cross the SMs, it takes about
-// 1700 cycles against 512 of MMA work, and an 8192 x 4096 x 2048 product 75 us.
+// What bounds it: a block's joins.  A part's eight warps each wait for its accumulator, read
+// 64 columns in four steps and add them up, about 740 cycles a block against 512 of MMA work
+// (with the multiply-adds left out a block takes 530; with the accumulators released before
+// they are read, as long as before).  The joins use paired multiply-adds, whose issue slots
+// were the bound before (845 cycles), and the scales come through shared memory: a warp
+// that reads its 32 rows' scales itself touches 32 cache lines a block, and from 32 blocks a
+// row on took 1600.  Tried and not kept: CTA pairs (256 x 256 tiles; the trip to the peer costs
+// what the shared weight rows save: 78.5 us against 78.7 for 9728 x 4096 x 2048), one MMA of
+// N = 256 for both parts (83.0: its one issuer waits for both parts' joins), tiles left in
+// staging and stored during the next one (81.4), 32-byte stores from registers (79.6).
 //
 //   warp 0      TMA producer: 256 weight rows and up to 128 token rows of one scale
 //               block (128 bytes a row) per stage
 //   warps 1-2   tensor memory (1); the two threads that issue MMAs, one per part
+//   warp 3      the tiles' descriptions and the scales, ahead of the epilogue
 //   warps 4-19  block joins and the epilogue; part 0 the first eight, part 1 the others
 //
-// gate/up: part 0 holds the up rows and part 1 the gate rows of the same 128
-// features.  Gate and up are narrowed to bf16, silu(gate) * up is formed in f32 and
-// a row's 128 features are quantised with one scale.
-//   rows tiles: two threads hold a row's up and gate of 64 features; each takes 32
-//     of them, through shared memory.  The row's largest magnitude is that of four
-//     threads.
-//   weights tiles: the bf16 results are transposed through shared memory, and
-//     sixteen threads form a row's 128 activations.
+// gate/up: a part holds the up rows and then the gate rows of 64 features.  Gate and up are
+// narrowed to bf16, silu(gate) * up is formed in f32 and a row's 128 features are quantised
+// with one scale.
+//   rows tiles: a thread's 64 columns are up and gate of 32 features; the row's largest
+//     magnitude is that of four threads.
+//   weights tiles: the bf16 results are transposed through shared memory, and sixteen
+//     threads form a row's 128 activations.
 //
 // The tile schedule and the bounded waits are those of moe_gemm.cu; a CTA that gives
 // up drains its MMAs and copies before it frees tensor memory.
@@ -205,11 +211,6 @@ __device__ __forceinline__ int rows_blocks(int rows) {
 }
 __device__ __forceinline__ int tail_blocks(int rows) {
   return rows > 0 && rows % kTokBlock != 0 && rows % kTokBlock <= kTail ? 1 : 0;
-}
-
-// silu(g) u; tolerance-checked: the fast exponential and division serve
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
 template <bool kGU>
@@ -862,6 +863,7 @@ int launch_range(const char* op, const CUtensorMap (&tt)[4], const CUtensorMap& 
 int launch_product(const char* op, const GemmParams& p0, bool gateup, cudaStream_t stream) {
   GemmParams p = p0;
   const int rows = gateup ? 2 * p.N : p.N;
+  if (p.P <= kFewRows && static_cast<long long>(p.P) * rows <= kFewProducts) return launch_few(op, p, gateup, stream);
   CUtensorMap tt[4], tw;
   int rc;
   // pairs of codes as 2-byte elements (K is a multiple of 16): the same bytes and the same

@@ -278,6 +278,15 @@ def test_transpose(G, Rr, C):
     assert (full_w[G:] == 0x5A).all() and (full_s[G:] == 7.0).all()
 
 
+@pytest.mark.parametrize("sizes,K,N", [([4, 0, 0, 5, 7], 4096, 1024), ([0] * 40 + [1] + [0] * 90 + [2], 1040, 392),
+                                       ([16], 528, 1000), ([17], 528, 960), ([9], 2048, 1816), ([1] * 700, 144, 128)])
+def test_few_rows_and_the_tiles_beyond(sizes, K, N):
+    # either side of the bounds on rows and products, and more groups than one launch of the tiles holds
+    test_product(sizes, K, N, "down")
+    if N % 16 == 0:
+        test_gateup(sizes, K, N // 2 // 16 * 16, True)
+
+
 def test_empty_calls_launch_nothing():
     before = launches()
     assert m.moe_quantize_act_fp8(None, 0, 64, 2, None, None, 1.0, None, None) == m.OK
