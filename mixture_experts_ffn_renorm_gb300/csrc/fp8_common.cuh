@@ -62,35 +62,12 @@ __device__ __forceinline__ uint4 codes16(const float (&v)[16], float id) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Two f32 values in one register pair: one instruction for both.  Each half is rounded like
-// the scalar operation.
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ uint64_t pair(float v) { return pair(__float_as_uint(v), __float_as_uint(v)); }
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // 16 values, as pairs, times id as E4M3 codes
 __device__ __forceinline__ uint4 codes16(const uint64_t (&v)[8], float id) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 lo = unpair(mul2(v[2 * i], pair(id))), hi = unpair(mul2(v[2 * i + 1], pair(id)));
+    const float2 lo = ptx::unpair(ptx::mul2(v[2 * i], ptx::pair(id))), hi = ptx::unpair(ptx::mul2(v[2 * i + 1], ptx::pair(id)));
     w[i] = codes4(lo.x, lo.y, hi.x, hi.y);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);

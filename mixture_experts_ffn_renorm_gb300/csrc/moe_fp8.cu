@@ -46,7 +46,7 @@ quant_rows_kernel(const uint16_t* __restrict__ x, int T, int H, int K,
   __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    v[i] = pair(raw[i] << 16, raw[i] & 0xFFFF0000u);
+    v[i] = ptx::pair(raw[i] << 16, raw[i] & 0xFFFF0000u);
     top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i])));   // skips NaN
   }
   float amax = fmaxf(__low2float(top), __high2float(top));
@@ -61,7 +61,7 @@ quant_rows_kernel(const uint16_t* __restrict__ x, int T, int H, int K,
     uint64_t w[8];
     float id;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = mul2(v[i], pair(routed_scale));
+    for (int i = 0; i < 8; ++i) w[i] = ptx::mul2(v[i], ptx::pair(routed_scale));
     block_scale(__fmul_rn(amax, fabsf(routed_scale)), same_d, id);
     same = codes16(w, id);
   }
@@ -76,7 +76,7 @@ quant_rows_kernel(const uint16_t* __restrict__ x, int T, int H, int K,
       uint64_t w[8];
       float id;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = mul2(v[i], pair(f));
+      for (int i = 0; i < 8; ++i) w[i] = ptx::mul2(v[i], ptx::pair(f));
       block_scale(__fmul_rn(amax, fabsf(f)), d, id);
       out = codes16(w, id);
     }

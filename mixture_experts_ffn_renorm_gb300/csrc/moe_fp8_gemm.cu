@@ -69,7 +69,7 @@ __device__ __forceinline__ uint64_t ld_shared_u64(uint32_t addr) {
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
-  const float2 f = unpair(v);
+  const float2 f = ptx::unpair(v);
   return gemm::pack_bf16x2(f.x, f.y);
 }
 
@@ -558,9 +558,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
             ptx::tc_fence_before();
             if (ptx::elect_one()) ptx::mbar_arrive(bar_tempty(acc));
           }
-          const uint64_t s = pair(!kGU || c > 1 ? s0 : (c == 0 ? s1 : s2));
+          const uint64_t s = ptx::pair(!kGU || c > 1 ? s0 : (c == 0 ? s1 : s2));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[8 * c + i] = fma2(pair(v[2 * i], v[2 * i + 1]), s, sum[8 * c + i]);
+          for (int i = 0; i < 8; ++i) sum[8 * c + i] = ptx::fma2(ptx::pair(v[2 * i], v[2 * i + 1]), s, sum[8 * c + i]);
         }
         parts += 2;
       }
@@ -584,7 +584,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         const float w = ptx::ld_shared_f32(at + 512);
 #pragma unroll
         for (int i = 0; i < 32; ++i)               // one f32 multiply, then the one bf16 rounding
-          pk[i] = pack_bf16(mul2(sum[i], pair(w)));
+          pk[i] = pack_bf16(ptx::mul2(sum[i], ptx::pair(w)));
       } else {
         if (f < t.n_tok) d = t.r0 + f;
 #pragma unroll
@@ -700,7 +700,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
             sc = sbase + S::SCALE + (q & 1) * kChunkBytes;
           }
           const uint32_t fk = sc + (kb & (kChunk - 1)) * kRowStride + 128 * h;
-          const uint64_t s2 = pair(ptx::ld_shared_f32(sc + w_at + (kb & (kChunk - 1)) * 4));
+          const uint64_t s2 = ptx::pair(ptx::ld_shared_f32(sc + w_at + (kb & (kChunk - 1)) * 4));
           const uint32_t acc = parts & acc_mask;
           wait_lean(bar_tfull(acc), (parts >> acc_shift) & 1u, sbase + S::MISC);
           ptx::tc_fence_after();
@@ -713,9 +713,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           for (int i = 0; i < 8; ++i) {
             if (i < 4 || wide) {
               const uint4 a4 = ptx::ld_shared_v4(fk + 16 * i);
-              const uint64_t lo = mul2(pair(a4.x, a4.y), s2), hi = mul2(pair(a4.z, a4.w), s2);
-              sum[2 * i] = fma2(pair(v[4 * i], v[4 * i + 1]), lo, sum[2 * i]);
-              sum[2 * i + 1] = fma2(pair(v[4 * i + 2], v[4 * i + 3]), hi, sum[2 * i + 1]);
+              const uint64_t lo = ptx::mul2(ptx::pair(a4.x, a4.y), s2), hi = ptx::mul2(ptx::pair(a4.z, a4.w), s2);
+              sum[2 * i] = ptx::fma2(ptx::pair(v[4 * i], v[4 * i + 1]), lo, sum[2 * i]);
+              sum[2 * i + 1] = ptx::fma2(ptx::pair(v[4 * i + 2], v[4 * i + 3]), hi, sum[2 * i + 1]);
             }
           }
           parts += 2;
@@ -747,8 +747,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
           uint64_t x[2] = {sum[8 * c + 2 * i], sum[8 * c + 2 * i + 1]};
           if (!kGU && p.pair_weight) {           // one f32 multiply, then the one bf16 rounding
             const uint4 w4 = ptx::ld_shared_v4(w_t + 4 * j0 + 16 * i);
-            x[0] = mul2(x[0], pair(w4.x, w4.y));
-            x[1] = mul2(x[1], pair(w4.z, w4.w));
+            x[0] = ptx::mul2(x[0], ptx::pair(w4.x, w4.y));
+            x[1] = ptx::mul2(x[1], ptx::pair(w4.z, w4.w));
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {          // gate/up: narrowed before the activation
