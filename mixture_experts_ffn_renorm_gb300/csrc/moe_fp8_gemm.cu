@@ -549,18 +549,40 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
         wait_lean(bar_tfull(acc), (parts >> 2) & 1u, sbase + S::MISC);
         ptx::tc_fence_after();
         const uint32_t taddr = taddr0 + acc * 128;
+        // Gate/up, whose three scales leave fewer registers, reads 8 columns at a time with the
+        // next 8 on their way; plain tiles read 16.  (9728 x 4096 x 2048: gate/up 71.1 us
+        // instead of 74.1, plain 80.2 instead of 74.2.)
+        if constexpr (kGU) {
+          uint32_t v[2][8];
+          ptx::tmem_ld_32x32b_x8(taddr, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[16];
-          ptx::tmem_ld_32x32b_x16(taddr + (kGU ? 64 * (c >> 1) + 16 * (c & 1) : 16 * c), v);
-          ptx::tmem_ld_wait();
-          if (c == 3) {                            // the warp has read all of it
-            ptx::tc_fence_before();
-            if (ptx::elect_one()) ptx::mbar_arrive(bar_tempty(acc));
+          for (int c = 0; c < 8; ++c) {
+            ptx::tmem_ld_wait();
+            if (c < 7) {
+              ptx::tmem_ld_32x32b_x8(taddr + 64 * ((c + 1) >> 2) + 8 * ((c + 1) & 3), v[(c + 1) & 1]);
+            } else {                               // the warp has read all of it
+              ptx::tc_fence_before();
+              if (ptx::elect_one()) ptx::mbar_arrive(bar_tempty(acc));
+            }
+            const uint64_t s = ptx::pair(c > 3 ? s0 : (c < 2 ? s1 : s2));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sum[4 * c + i] = ptx::fma2(ptx::pair(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s, sum[4 * c + i]);
           }
-          const uint64_t s = ptx::pair(!kGU || c > 1 ? s0 : (c == 0 ? s1 : s2));
+        } else {
+          const uint64_t s = ptx::pair(s0);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[8 * c + i] = ptx::fma2(ptx::pair(v[2 * i], v[2 * i + 1]), s, sum[8 * c + i]);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(taddr + 16 * c, v);
+            ptx::tmem_ld_wait();
+            if (c == 3) {
+              ptx::tc_fence_before();
+              if (ptx::elect_one()) ptx::mbar_arrive(bar_tempty(acc));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[8 * c + i] = ptx::fma2(ptx::pair(v[2 * i], v[2 * i + 1]), s, sum[8 * c + i]);
+          }
         }
         parts += 2;
       }
