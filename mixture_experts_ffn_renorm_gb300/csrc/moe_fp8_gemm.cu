@@ -20,16 +20,21 @@
 //                  32 of the token rows, whose scales its warp keeps in shared memory.
 // Rows tiles need no transpose and no scale loads per product, and pad to 128 rows;
 // weights tiles pad to 16 rows, which is what ragged and decode-sized groups need.
+//
 // What bounds it: a block's joins.  A part's eight warps each wait for its accumulator, read
 // 64 columns in four steps and add them up, about 740 cycles a block against 512 of MMA work
 // (with the multiply-adds left out a block takes 530; with the accumulators released before
 // they are read, as long as before).  The joins use paired multiply-adds, whose issue slots
 // were the bound before (845 cycles), and the scales come through shared memory: a warp
 // that reads its 32 rows' scales itself touches 32 cache lines a block, and from 32 blocks a
-// row on took 1600.  Tried and not kept: CTA pairs (256 x 256 tiles; the trip to the peer costs
-// what the shared weight rows save: 78.5 us against 78.7 for 9728 x 4096 x 2048), one MMA of
-// N = 256 for both parts (83.0: its one issuer waits for both parts' joins), tiles left in
-// staging and stored during the next one (81.4), 32-byte stores from registers (79.6).
+// row on took 1600.  A tile costs about 4600 cycles besides (launch and fill of an eight-tile
+// call spread over its tiles included 5700): the vote, the packing, the stores, and the first
+// block's scales and accumulator, while the MMAs run two blocks ahead and then wait.
+// Times of 9728 x 4096 x 2048, 74.2 us as built; tried and not kept, each against the step it
+// was tried on: CTA pairs (256 x 256 tiles; the trip to the peer costs what the shared weight
+// rows save: 78.5 against 78.7), one MMA of N = 256 for both parts (83.0 against 78.7: its one
+// issuer waits for both parts' joins), tiles left in staging and stored during the next one
+// (81.4 against 78.7), three operand stages and 64 KB of staging (80.8 against 74.2).
 //
 //   warp 0      TMA producer: 256 weight rows and up to 128 token rows of one scale
 //               block (128 bytes a row) per stage
@@ -312,7 +317,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
     }
   }
   if (lane == 31) scan_tmp[warp] = make_int2(incl_b, incl_t);
-  const bool small = __syncthreads_or(rows_max > 64) == 0;   // eight accumulators of 64 columns
+  const bool small = __syncthreads_or(rows_max > kTail) == 0;   // eight accumulators of kTail columns
   int run_b = incl_b - n_big, run_t = incl_t - n_tail;
   int all_b = 0, all_t = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
@@ -615,7 +620,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmT16, const __grid_constant
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar_iempty(n & 1));
       // Sixteen rows and 32 columns at a time through the warp's 1 KB, so that four lanes store
-      // 64 bytes of a row.
+      // 64 bytes of a row.  (A 16-byte shared store takes its passes whether 8 or 16 lanes are
+      // active: eight rows of 128 bytes at a time took 78.7 us where this takes 74.2, all 32 rows
+      // of 32 bytes 79.6, 32-byte stores straight from registers 79.6.)
       const int col = kGU ? t.n0 + 64 * set + 32 * h : t.n0 + 128 * set + 64 * h;
       const uint32_t st = sbase + S::EPI + ((id.e & 3) * 4 + 2 * set + h) * 1024;
       if (!kGU || p.out) {
