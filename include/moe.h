@@ -750,7 +750,9 @@ int moe_combine_backward(const void* expert_out, int eo_dtype, const float* w, c
  *   grad_logits f32 [T,E];  x bf16 [T,H];  w_router bf16 [E,H]
  *   each output may be NULL (not all three); x may be NULL without
  *   grad_w_router, w_router without grad_x
- *   workspace   >= moe_route_logits_backward_workspace_size(T, H, E) bytes, 16-byte aligned
+ *   workspace   >= moe_route_logits_backward_workspace_size(T, H, E) bytes, 16-byte aligned;
+ *               the size never falls as T grows, so one queried for the most tokens serves
+ *               every call
  *   T >= 0 (T = 0: the sums are 0), H > 0 multiple of 8, 1 <= E <= 1024
  * Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (x, w_router, grad_x and grad_w_router 16
  * bytes, the others 4), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.

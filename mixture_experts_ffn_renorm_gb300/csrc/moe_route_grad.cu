@@ -536,6 +536,7 @@ static_assert(DwSmem::ALLOC <= 227 * 1024, "shared memory");
 // steps in each, since a range costs a pass over its [E,H] sums and more than one a launch
 struct Ranges {
   int steps, count;
+  int bound;   // no smaller for more tokens, never below count: what the workspace is sized by
 };
 Ranges ranges_of(int T, int H, int E) {
   const int total = (T + kStepT - 1) / kStepT;
@@ -545,6 +546,8 @@ Ranges ranges_of(int T, int H, int E) {
   if (want > 32) want = 32;
   if (want < 1) want = 1;
   Ranges r;
+  r.bound = want;
+  // whole steps: fewer tokens can make more ranges (54 steps in nine ranges, 55 in eight)
   r.steps = (total + want - 1) / want;
   r.count = (total + r.steps - 1) / r.steps;
   return r;
@@ -580,8 +583,8 @@ extern "C" {
 size_t moe_route_logits_backward_workspace_size(int T, int H, int E) {
   if (T <= 0 || H <= 0 || E <= 0) return 0;
   const Ranges r = ranges_of(T, H, E);
-  if (r.count == 1) return 0;
-  return static_cast<size_t>(r.count) * E * (static_cast<size_t>(H) + 1) * sizeof(float);
+  if (r.bound == 1) return 0;
+  return static_cast<size_t>(r.bound) * E * (static_cast<size_t>(H) + 1) * sizeof(float);
 }
 
 int moe_route_logits_backward(const float* grad_logits, const void* x_bf16, const void* w_router_bf16,
