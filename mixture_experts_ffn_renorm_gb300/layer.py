@@ -177,6 +177,8 @@ class MoeBlock:
             self.grad_x_router = torch.empty((T, H), dtype=bf, device=dv)
             self.grad_w_router = torch.empty((E, H), dtype=f32, device=dv)
             self.grad_logit_bias = torch.empty((E,), dtype=f32, device=dv)
+            # the rows' gradients: expert_out keeps the forward's rows for another backward()
+            self.grad_rows = torch.empty((P, H), dtype=bf, device=dv)
             self.dact = torch.empty((P, I), dtype=bf, device=dv)
             self.dgu_q = torch.empty((P, 2 * I), dtype=torch.uint8, device=dv)
             self.dgu_s = torch.empty((P, blocks(2 * I)), dtype=f32, device=dv)
@@ -206,6 +208,7 @@ class MoeBlock:
         self.graph = None
         self.graph_x = None
         self._pipe = None
+        self._tokens = None      # of the last forward(): what backward() is the gradient of
 
     # one forward over x [T, H] bf16 (device); returns a view of the output buffer.
     # marks: optional list; a CUDA event is recorded after each stage and
@@ -219,6 +222,7 @@ class MoeBlock:
         H, I, E, K = self.H, self.I, self.E, self.K
         P = T * K
         ws = self.workspace
+        self._tokens = None
 
         def mark(name, edge=False):
             if marks is not None and (stages or edge):
@@ -298,6 +302,7 @@ class MoeBlock:
             moe_grouped_gemm_down_bf16(self.act, self.w2, self.expert_offsets, self.topk_w,
                                        self.sorted_pair, P, I, H, E, self.expert_out, None, 0,
                                        stream)
+        self._tokens = T
         mark("gemm_down")
         out = self.out[:T] if out is None else out
         if self.has_shared:
@@ -323,11 +328,18 @@ class MoeBlock:
         grad_x bf16 [T, H] (through the experts and the router), grad_w_router f32 [E, H],
         grad_logit_bias f32 [E], grad_topk_w f32 [T, K], losses f32 [2] (balance, z).  The
         choice of experts and the quantisers' roundings count as constant (the gradient
-        passes a rounding unchanged).  No call allocates or synchronises."""
+        passes a rounding unchanged).  x holds that forward's tokens; another number of tokens
+        than the last forward() or replay() took is a ValueError (the replay of a graph that a
+        program captured by itself does not count).  What the forward kept stays until the next
+        one: backward() may be called again, with another dout or other coefficients.  No call
+        allocates or synchronises."""
         if not self.training:
             raise ValueError("backward() needs MoeBlock(training=True)")
         T = x.shape[0]
-        assert T <= self.max_tokens and dout.shape == x.shape
+        if T != self._tokens:
+            raise ValueError("backward() needs a forward() before it" if self._tokens is None else
+                             f"backward() of {T} tokens, but the last forward() took {self._tokens}")
+        assert dout.shape == x.shape
         assert x.dtype == dout.dtype == torch.bfloat16 and x.is_contiguous() and dout.is_contiguous()
         H, I, E, K = self.H, self.I, self.E, self.K
         P = T * K
@@ -347,8 +359,8 @@ class MoeBlock:
                              None, P, H, I, E, self.dact, stream)
         moe_silu_mul_backward_fp8(self.gate_up, self.dact, P, I, self.dgu_q, self.dgu_s, stream)
         moe_grouped_gemm_fp8(self.dgu_q, self.dgu_s, self.w13_t, self.w13_ts, self.expert_offsets,
-                             None, self.sorted_pair, P, 2 * I, H, E, self.expert_out, stream)
-        moe_combine(self.expert_out, BF16, None, self.grad_x_router, BF16, 1.0, T, K, H,
+                             None, self.sorted_pair, P, 2 * I, H, E, self.grad_rows, stream)
+        moe_combine(self.grad_rows, BF16, None, self.grad_x_router, BF16, 1.0, T, K, H,
                     self.grad_x, BF16, stream)
         return {"grad_x": self.grad_x[:T], "grad_w_router": self.grad_w_router,
                 "grad_logit_bias": self.grad_logit_bias, "grad_topk_w": self.grad_topk_w[:T],
@@ -391,7 +403,8 @@ class MoeBlock:
 
     def replay(self):
         self.graph.replay()
-        return self.out[: self.graph_x.shape[0]]
+        self._tokens = self.graph_x.shape[0]
+        return self.out[: self._tokens]
 
     def run_host_batches(self, x_hosts, out_hosts):
         """End to end over pinned host batches: out_hosts[i] <- block(x_hosts[i]).
