@@ -745,8 +745,8 @@ int moe_combine_backward(const void* expert_out, int eo_dtype, const float* w, c
  *   grad_x[t,:]        = bf16( sum_e dl[t,e] * w_router[e,:] )
  *   grad_w_router[e,:] = sum_t dl[t,e] * x[t,:]       f32
  *   grad_bias[e]       = sum_t dl[t,e]                f32
- * dl enters at 24-bit (grad_w_router) or at least 16-bit (grad_x) precision, sums
- * are f32 in a fixed order: the same call gives the same bits.
+ * dl enters with all its bits, sums are f32 in a fixed order: the same call gives
+ * the same bits.
  *   grad_logits f32 [T,E];  x bf16 [T,H];  w_router bf16 [E,H]
  *   each output may be NULL (not all three); x may be NULL without
  *   grad_w_router, w_router without grad_x

@@ -4,14 +4,16 @@
 //
 // x and W are bf16 and dl is f32.  The tensor core multiplies bf16, so dl enters as
 // a sum of bf16 values, dl = hi + mid + lo (8 + 8 + 8 significand bits: exact), and
-// every product is exact in f32.  dW takes all three parts; dx, which is rounded to
-// bf16, takes hi + mid (error 2^-16 of each term).  x and W are read as they lie in
-// memory: their contiguous dimension is an output dimension of both products, so
-// they go to the tensor core as MN-major operands straight from TMA boxes.
+// every product is exact in f32.  Both products take all three parts: the rows of a
+// softmax router's dl sum to zero, so what the rows of W have in common cancels in dx, and
+// what is left can lie below the 16 bits of hi + mid (which took dx 15.5 us instead of
+// 18.8).  x and W are read as they lie in memory: their contiguous dimension is an output
+// dimension of both products, so they go to the tensor core as MN-major operands straight
+// from TMA boxes.
 //
 // The floor is the bytes: x read and dx written once (67 MB at T = 8192, H = 2048,
-// E = 128: 9.9 us), against 4 + 6 FLOP per element and expert on the tensor core
-// (21 GFLOP: 12 us of it at most).
+// E = 128: 9.9 us), against 6 + 6 FLOP per element and expert on the tensor core
+// (26 GFLOP: 14 us of it at most).
 //
 //   dW  CTA: 128 experts x 128 columns of H x a range of tokens, 64 tokens a step.
 //       Eight warps load dl, split it and write the three parts as MN-major operand
@@ -27,8 +29,8 @@
 //       parts of dl and x are written there (500), and dl's loads pass through the same
 //       memory (600: a timing copy without them takes 1250 a step).  Sixteen converting
 //       warps instead of eight took 28.4 us, so it is not the conversion's latency.
-//   dx  CTA: 128 tokens x 256 columns of H, 64 experts a step; dl is split into two
-//       K-major operand tiles.  Two CTAs share an SM and fill each other's gaps.  15.3 us
+//   dx  CTA: 128 tokens x 256 columns of H, 64 experts a step; dl is split into three
+//       K-major operand tiles.  Two CTAs share an SM and fill each other's gaps.  18.8 us
 //       alone for 34 MB written, in 1.7 rounds of CTAs that each load, split, multiply and
 //       store in turn; dW starts beside its last ones.
 #include <atomic>
@@ -52,28 +54,30 @@ struct WsLimits {
   unsigned int* status;
 };
 
-// hi, mid and lo of 8 values, packed; a value that is not finite is all in hi
+// hi, mid and lo of 8 values, packed, by cutting off: a part is the upper half of the rest's
+// word.  A value that is not finite is all in hi.
 __device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
-  uint32_t h[4], m[4], l[4];
+  uint32_t part[3][8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = v[2 * i], b = v[2 * i + 1];
-    h[i] = gemm::pack_bf16x2(a, b);
-    const float ha = __uint_as_float(h[i] << 16), hb = __uint_as_float(h[i] & 0xFFFF0000u);
-    const float ra = fabsf(ha) < INFINITY ? __fsub_rn(a, ha) : 0.0f;   // exact
-    const float rb = fabsf(hb) < INFINITY ? __fsub_rn(b, hb) : 0.0f;
-    m[i] = gemm::pack_bf16x2(ra, rb);
-    l[i] = gemm::pack_bf16x2(__fsub_rn(ra, __uint_as_float(m[i] << 16)),
-                             __fsub_rn(rb, __uint_as_float(m[i] & 0xFFFF0000u)));
+  for (int i = 0; i < 8; ++i) {
+    const bool fin = fabsf(v[i]) < INFINITY;
+    // the upper half of a NaN's word may read as an infinity
+    part[0][i] = v[i] != v[i] ? 0x7FFF0000u : __float_as_uint(v[i]) & 0xFFFF0000u;
+    const float r = fin ? __fsub_rn(v[i], __uint_as_float(part[0][i])) : 0.0f;   // exact
+    part[1][i] = __float_as_uint(r) & 0xFFFF0000u;
+    part[2][i] = __float_as_uint(__fsub_rn(r, __uint_as_float(part[1][i])));
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  mid = make_uint4(m[0], m[1], m[2], m[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  uint32_t w[3][4];
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[p][i] = __byte_perm(part[p][2 * i], part[p][2 * i + 1], 0x7632);
+  hi = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+  mid = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+  lo = make_uint4(w[2][0], w[2][1], w[2][2], w[2][3]);
 }
 
-// The same by cutting off instead of rounding, which is exact too and takes fewer
-// instructions (1100 instead of 1350 cycles a step of dW): a cut part is the upper half of
-// the word.
+// The same in paired instructions where all 8 values are finite.
 __device__ __forceinline__ void cut8(const float (&v)[8], uint4& hi, uint4& mid, uint4& lo) {
   uint32_t h[4], m[4], l[4];
   uint64_t finite = 0;                   // 0 times every rest: NaN where a value is not finite
@@ -375,8 +379,8 @@ route_reduce_kernel(const float* __restrict__ part_w, const float* __restrict__ 
 
 // ------------------------------------------------------------------ dx
 struct DxSmem {
-  static constexpr int A = 0;                          // 2 parts x 128 tokens x 128 bytes (64 experts)
-  static constexpr int B = A + 2 * 2 * kBlk;           // 4 blocks of 64 columns x 64 experts
+  static constexpr int A = 0;                          // 3 parts x 128 tokens x 128 bytes (64 experts)
+  static constexpr int B = A + 3 * 2 * kBlk;           // 4 blocks of 64 columns x 64 experts
   static constexpr int BARS = B + 4 * kBlk;            // fullA, fullB, done, drain
   static constexpr int MISC = BARS + 32;
   static constexpr int ALLOC = MISC + 16 + 1024;
@@ -442,7 +446,7 @@ route_dx_kernel(const __grid_constant__ CUtensorMap tmW, const DxParams p) {
         ptx::tc_fence_after();
         const uint64_t db = ptx::desc_mnmajor_sw128(sb + S::B, kBlk);
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
+        for (int part = 0; part < 3; ++part) {
           const uint64_t da = ptx::desc_kmajor_sw128(sb + S::A + part * 2 * kBlk);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -475,11 +479,12 @@ route_dx_kernel(const __grid_constant__ CUtensorMap tmW, const DxParams p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint4 hi, mid, lo;
-        split8(v[j], hi, mid, lo);
+        cut8(v[j], hi, mid, lo);
         const int row = r + 32 * j;
         const uint32_t dst = sb + S::A + row * 128 + ((o ^ (row & 7)) << 4);
         ptx::st_shared_v4(dst, hi.x, hi.y, hi.z, hi.w);
         ptx::st_shared_v4(dst + 2 * kBlk, mid.x, mid.y, mid.z, mid.w);
+        ptx::st_shared_v4(dst + 4 * kBlk, lo.x, lo.y, lo.z, lo.w);
       }
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(full_a);
