@@ -468,8 +468,9 @@ int moe_grouped_gemm_down_fp8w(const void* act_bf16, const uint8_t* w2_e4m3,
  * moe_transpose_fp8w -- [G, R, C] codes and their block scales as [G, C, R]
  * (exact: a block's scale moves with it); R and C multiples of 16.
  *
- * Errors of the five: MOE_ERR_ARG (sizes, NULL operands, NULL group_offsets
- * with G > 1), MOE_ERR_ALIGN (codes, x and bf16 buffers 16-byte, scales and
+ * Errors of the five: MOE_ERR_ARG (sizes; P, a row's columns, or the weight rows of
+ * 512 groups together above 2^31 - 2^12; R of the transpose above 64 * 65535; NULL
+ * operands, NULL group_offsets with G > 1), MOE_ERR_ALIGN (codes, x and bf16 buffers 16-byte, scales and
  * indices 4-byte aligned; the multiples above), MOE_ERR_CUDA.  P = 0 (T = 0) is
  * a no-op.  No workspace.  A device-side wait that runs past its limit sets
  * MOE_STATUS_TIMEOUT (moe_set_wait_limit_ns).
@@ -753,7 +754,7 @@ int moe_combine_backward(const void* expert_out, int eo_dtype, const float* w, c
  *   workspace   >= moe_route_logits_backward_workspace_size(T, H, E) bytes, 16-byte aligned;
  *               the size never falls as T grows, so one queried for the most tokens serves
  *               every call
- *   T >= 0 (T = 0: the sums are 0), H > 0 multiple of 8, 1 <= E <= 1024
+ *   0 <= T <= 128 * 65535 (T = 0: the sums are 0), H > 0 multiple of 8, 1 <= E <= 1024
  * Errors: MOE_ERR_ARG, MOE_ERR_ALIGN (x, w_router, grad_x and grad_w_router 16
  * bytes, the others 4), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.
  * ---------------------------------------------------------------------- */

@@ -78,6 +78,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
+constexpr int kMaxGroupsLaunch = 512;       // groups of one launch of the tiles (schedule in shared memory)
+
 struct GemmParams {
   const uint8_t* a;
   const float* sa;               // [P, blocks(K)]

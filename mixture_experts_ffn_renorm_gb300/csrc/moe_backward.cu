@@ -143,6 +143,8 @@ combine_backward_kernel(const void* __restrict__ eo, const float* __restrict__ w
 // ------------------------------------------------------------------ router: logits
 constexpr int kRtWarps = 8;   // tokens per block
 
+int route_blocks(int T) { return T / kRtWarps + (T % kRtWarps != 0); }
+
 struct RouteParams {
   const float* logits;
   const int32_t* ids;
@@ -362,6 +364,7 @@ int moe_combine_backward(const void* expert_out, int eo_dtype, const float* w, c
   if (T < 0 || H <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d", op, T, H);
   if (K < 1 || K > 64) return set_error(MOE_ERR_ARG, "%s: K=%d outside [1, 64]", op, K);
   if (H % 8 != 0) return set_error(MOE_ERR_ALIGN, "%s: H=%d is not a multiple of 8", op, H);
+  if (H > kMaxDim) return set_error(MOE_ERR_ARG, "%s: H=%d is too large", op, H);
   if (!dw && !d_expert_out) return set_error(MOE_ERR_ARG, "%s: no output requested", op);
   if (T == 0) return MOE_OK;
   if (!dout || (dw && !expert_out)) return set_error(MOE_ERR_ARG, "%s: NULL operand", op);
@@ -394,7 +397,7 @@ int moe_combine_backward(const void* expert_out, int eo_dtype, const float* w, c
 
 size_t moe_route_backward_workspace_size(int T, int E) {
   if (T <= 0 || E <= 0) return 0;
-  return static_cast<size_t>((T + kRtWarps - 1) / kRtWarps) * 2 * sizeof(float);
+  return static_cast<size_t>(route_blocks(T)) * 2 * sizeof(float);
 }
 
 int moe_route_backward(const float* logits, const int32_t* topk_ids, const float* grad_w,
@@ -433,7 +436,7 @@ int moe_route_backward(const float* logits, const int32_t* topk_ids, const float
   RouteParams p{logits, topk_ids, grad_w, expert_offsets, T, E, K, renormalize, scoring, balance_coef,
                 z_coef, grad_logits, sum_losses ? static_cast<float*>(workspace) : nullptr, losses,
                 diag.status, diag.launches};
-  const int blocks = (T + kRtWarps - 1) / kRtWarps;
+  const int blocks = route_blocks(T);
   auto go = [&](auto kern) {
     return launch_status(launch_kernel(kern, dim3(blocks), dim3(32 * kRtWarps), 0, s, nullptr, 0, p), op);
   };

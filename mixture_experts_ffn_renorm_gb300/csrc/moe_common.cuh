@@ -33,6 +33,9 @@ inline int launch_status(cudaError_t e, const char* what) {
   return set_error(MOE_ERR_CUDA, "%s: kernel launch failed: %s", what, cudaGetErrorString(e));
 }
 
+// The largest size that can be rounded up to any tile, or stepped past by any stride, in int.
+constexpr int kMaxDim = 0x7FFFF000;
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Programmatic dependent launch (process-wide switch, moe_set_pdl; on by default).

@@ -226,13 +226,20 @@ transpose_codes_kernel(const uint8_t* __restrict__ w, const float* __restrict__ 
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// the checks the two products share; K is the contraction length
+// the checks the two products share; K is the contraction length, N the output columns, with
+// their names in the call; a group has rows_per_col * N weight rows
 int check_product(const char* op, const void* a, const void* sa, const void* w, const void* sw,
-                  const void* group_offsets, int P, int K, int N, int G) {
+                  const void* group_offsets, int P, int K, const char* k_name, int N,
+                  const char* n_name, int rows_per_col, int G) {
   if (P < 0) return set_error(MOE_ERR_ARG, "%s: P=%d < 0", op, P);
   if (K <= 0 || N <= 0) return set_error(MOE_ERR_ARG, "%s: dimensions must be positive", op);
   if (G < 1 || G > gemm::kMaxGroups)
     return set_error(MOE_ERR_ARG, "%s: G=%d outside [1, %d]", op, G, gemm::kMaxGroups);
+  if (P > kMaxDim) return set_error(MOE_ERR_ARG, "%s: P=%d is too large", op, P);
+  if (K > kMaxDim) return set_error(MOE_ERR_ARG, "%s: %s=%d is too large", op, k_name, K);
+  if (N > kMaxDim / rows_per_col) return set_error(MOE_ERR_ARG, "%s: %s=%d is too large", op, n_name, N);
+  const long long rows = static_cast<long long>(G < kMaxGroupsLaunch ? G : kMaxGroupsLaunch) * rows_per_col * N;
+  if (rows > kMaxDim) return set_error(MOE_ERR_ARG, "%s: %lld weight rows are too large a number", op, rows);
   if (P == 0) return MOE_OK;
   if (!a || !sa || !w || !sw) return set_error(MOE_ERR_ARG, "%s: NULL operand or scales", op);
   if (!group_offsets && G > 1)
@@ -260,6 +267,7 @@ int moe_quantize_act_fp8(const void* x_bf16, int T, int H, int K, const int32_t*
   const char* op = "moe_quantize_act_fp8";
   if (T < 0 || H <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d", op, T, H);
   if (K < 1 || K > 64) return set_error(MOE_ERR_ARG, "%s: K=%d outside [1, 64]", op, K);
+  if (H > kMaxDim) return set_error(MOE_ERR_ARG, "%s: H=%d is too large", op, H);
   if (static_cast<long long>(T) * K > 0x7FFFFFFFLL)
     return set_error(MOE_ERR_ARG, "%s: T*K is too large", op);
   if (H % 16 != 0) return set_error(MOE_ERR_ALIGN, "%s: H=%d is not a multiple of 16", op, H);
@@ -287,7 +295,8 @@ int moe_grouped_gemm_fp8(const uint8_t* a_codes, const float* a_scales, const ui
                          int G, void* out_bf16, void* stream) {
   clear_error();
   const char* op = "moe_grouped_gemm_fp8";
-  int rc = check_product(op, a_codes, a_scales, w_e4m3, w_scale, group_offsets, P, K, N, G);
+  int rc = check_product(op, a_codes, a_scales, w_e4m3, w_scale, group_offsets, P, K, "K", N, "N",
+                         1, G);
   if (rc != MOE_OK) return rc;
   if (K % 16 != 0 || N % 8 != 0)
     return set_error(MOE_ERR_ALIGN, "%s: K=%d must be a multiple of 16 and N=%d of 8", op, K, N);
@@ -320,7 +329,8 @@ int moe_grouped_gemm_gateup_silu_fp8(const uint8_t* a_codes, const float* a_scal
                                      void* stream) {
   clear_error();
   const char* op = "moe_grouped_gemm_gateup_silu_fp8";
-  int rc = check_product(op, a_codes, a_scales, w13_e4m3, w13_scale, group_offsets, P, H, I, G);
+  int rc = check_product(op, a_codes, a_scales, w13_e4m3, w13_scale, group_offsets, P, H, "H", I,
+                         "I", 2, G);
   if (rc != MOE_OK) return rc;
   if (H % 16 != 0 || I % 16 != 0)
     return set_error(MOE_ERR_ALIGN, "%s: H=%d and I=%d must be multiples of 16", op, H, I);
@@ -350,7 +360,8 @@ int moe_silu_mul_backward_fp8(const void* gate_up_bf16, const void* dact_bf16, i
                               uint8_t* codes, float* scales, void* stream) {
   clear_error();
   const char* op = "moe_silu_mul_backward_fp8";
-  if (P < 0 || I <= 0 || I > 0x3FFFFFFF) return set_error(MOE_ERR_ARG, "%s: bad sizes P=%d I=%d", op, P, I);
+  if (P < 0 || I <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes P=%d I=%d", op, P, I);
+  if (I > kMaxDim / 2) return set_error(MOE_ERR_ARG, "%s: I=%d is too large", op, I);
   if (I % 16 != 0) return set_error(MOE_ERR_ALIGN, "%s: I=%d is not a multiple of 16", op, I);
   if (P == 0) return MOE_OK;
   if (!gate_up_bf16 || !dact_bf16 || !codes || !scales)
@@ -381,7 +392,8 @@ int moe_transpose_fp8w(const uint8_t* w_e4m3, const float* w_scale, int G, int R
   if (R <= 0 || C <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes R=%d C=%d", op, R, C);
   if (R % 16 != 0 || C % 16 != 0)
     return set_error(MOE_ERR_ALIGN, "%s: R=%d and C=%d must be multiples of 16", op, R, C);
-  if ((R + 63) / 64 > 65535) return set_error(MOE_ERR_ARG, "%s: R=%d is too large", op, R);
+  if (R > 64 * 65535) return set_error(MOE_ERR_ARG, "%s: R=%d is too large", op, R);   // the grid's y
+  if (C > kMaxDim) return set_error(MOE_ERR_ARG, "%s: C=%d is too large", op, C);
   if (!w_e4m3 || !w_scale || !out_e4m3 || !out_scale)
     return set_error(MOE_ERR_ARG, "%s: NULL operand", op);
   if (!aligned16(w_e4m3) || !aligned16(out_e4m3) || !aligned4(w_scale) || !aligned4(out_scale))

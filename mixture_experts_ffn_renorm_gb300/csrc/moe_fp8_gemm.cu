@@ -92,7 +92,6 @@ constexpr int kStages = 4;
 constexpr int kWBytes = 256 * 128;          // a stage's weight rows
 constexpr int kTBytes = 128 * 128;          // a stage's token rows, at most
 constexpr int kMaxAcc = 8;
-constexpr int kMaxGroupsLaunch = 512;       // groups of one launch (schedule in shared memory)
 constexpr int kMmaK = 32;                   // K per tcgen05.mma of 8-bit types
 
 // Scales of 8 blocks: the rows' as [block][128 rows], 16 bytes of padding per block (so that

@@ -544,9 +544,9 @@ struct Ranges {
   int bound;   // no smaller for more tokens, never below count: what the workspace is sized by
 };
 Ranges ranges_of(int T, int H, int E) {
-  const int total = (T + kStepT - 1) / kStepT;
-  const int tiles = ((H + 127) / 128) * ((E + 127) / 128);
-  int want = sm_count() / tiles;
+  const int total = T / kStepT + (T % kStepT != 0);
+  const long long tiles = (H / 128 + (H % 128 != 0)) * ((E - 1) / 128 + 1ll);
+  int want = static_cast<int>(sm_count() / tiles);
   if (want > total / 6) want = total / 6;
   if (want > 32) want = 32;
   if (want < 1) want = 1;
@@ -600,6 +600,8 @@ int moe_route_logits_backward(const float* grad_logits, const void* x_bf16, cons
   if (T < 0 || H <= 0) return set_error(MOE_ERR_ARG, "%s: bad sizes T=%d H=%d", op, T, H);
   if (E < 1 || E > 1024) return set_error(MOE_ERR_ARG, "%s: E=%d outside [1, 1024]", op, E);
   if (H % 8 != 0) return set_error(MOE_ERR_ALIGN, "%s: H=%d is not a multiple of 8", op, H);
+  if (T > 128 * 65535) return set_error(MOE_ERR_ARG, "%s: T=%d is too large", op, T);   // the grid's y
+  if (H > kMaxDim) return set_error(MOE_ERR_ARG, "%s: H=%d is too large", op, H);
   if (!grad_x_bf16 && !grad_w_router && !grad_bias)
     return set_error(MOE_ERR_ARG, "%s: no output requested", op);
   if (T > 0 && (!grad_logits || (grad_x_bf16 && !w_router_bf16) || (grad_w_router && !x_bf16)))
@@ -619,7 +621,6 @@ int moe_route_logits_backward(const float* grad_logits, const void* x_bf16, cons
       return check_launch(op);
     return MOE_OK;
   }
-  if ((T + 127) / 128 > 65535) return set_error(MOE_ERR_ARG, "%s: T=%d is too large", op, T);
   const bool sums = grad_w_router || grad_bias;
   const Ranges rg = ranges_of(T, H, E);
   if (sums && rg.count > 1) {
