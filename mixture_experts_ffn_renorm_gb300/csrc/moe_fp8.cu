@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256)
 transpose_codes_kernel(const uint8_t* __restrict__ w, const float* __restrict__ scale, int R, int C,
                        uint8_t* __restrict__ out, float* __restrict__ out_scale,
                        unsigned long long* launches) {
-  __shared__ uint8_t tile[64][68];
+  __shared__ __align__(4) uint8_t tile[64][68];   // stored as words
   count_launch(launches, MOE_KID_TRANSPOSE_FP8);
   grid_dep_wait();
   grid_dep_launch();
