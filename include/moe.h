@@ -413,8 +413,12 @@ int moe_grouped_gemm_down_fp8w(const void* act_bf16, const uint8_t* w2_e4m3,
  * of a row may be short).  For row r of group g, output n and blocks b of the
  * contraction:
  *   y[r,n] = sum_b (sa[r,b] * sw[g,n/128,b]) * sum_{k in b} a[r,k] * w[g,n,k]
- * The block sums run on E4M3 products accumulated in f32 and are joined in f32
- * in block order.  A NaN or an infinity in an activation row makes that row's
+ * All sums are f32 in a fixed order: the same call gives the same bits.  The order
+ * depends on the call's rows and on the rows of the group, not on the values: calls
+ * of at most 16 rows and 16384 results (gate/up: gate and up each counted) add
+ * pieces of 16 columns and join them across a warp; other calls add whole blocks
+ * on the tensor cores and join those in block order.  So a row's last bits may
+ * differ between a call of its own and a larger one.  A NaN or an infinity in an activation row makes that row's
  * results NaN.
  *
  * moe_quantize_act_fp8 -- the activation quantiser.  For pair p = t*K + j, with
@@ -812,6 +816,8 @@ enum {
   MOE_KID_ROUTE_DX = 27,         /* moe_route_logits_backward: grad_x */
   MOE_KID_ROUTE_DW = 28,         /* moe_route_logits_backward: grad_w_router and grad_bias */
   MOE_KID_ROUTE_REDUCE = 29,     /* moe_route_logits_backward: their sums over token ranges */
+  MOE_KID_GEMM_FP8_FEW = 30,     /* the launches of 20 and 21 that read the weights row by row:
+                                    calls of few rows and products */
   MOE_KID_COUNT = 32
 };
 int moe_device_status(int* status_out, int clear);

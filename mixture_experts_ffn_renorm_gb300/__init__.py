@@ -28,7 +28,7 @@ KID = {
     "quant_act": 13, "gemm_q": 14, "gemm_q_gateup": 15, "gemm_q_down": 16, "dequant_q": 17,
     "exp_sigmoid": 18, "quant_fp8": 19, "gemm_fp8": 20, "gemm_fp8_gateup": 21,
     "silu_backward": 22, "transpose_fp8": 23, "combine_backward": 24, "route_backward": 25,
-    "route_losses": 26, "route_dx": 27, "route_dw": 28, "route_reduce": 29,
+    "route_losses": 26, "route_dx": 27, "route_dw": 28, "route_reduce": 29, "gemm_fp8_few": 30,
 }
 KID_COUNT = 32
 QFMT_Q8_0, QFMT_Q4_K = 1, 2

@@ -109,6 +109,7 @@ __device__ __forceinline__ void dots(const uint8_t* __restrict__ a, const float*
 __global__ void __launch_bounds__(32 * kWarps)
 few_rows_kernel(const GemmParams p, unsigned long long* launches) {
   count_launch(launches, p.kid);
+  count_launch(launches, MOE_KID_GEMM_FP8_FEW);
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
@@ -136,6 +137,7 @@ few_rows_gateup_kernel(const GemmParams p, unsigned long long* launches) {
   __shared__ float s_max[4 * kWarps];
   cluster_arrive();              // waited for before the first store to another CTA
   count_launch(launches, p.kid);
+  count_launch(launches, MOE_KID_GEMM_FP8_FEW);
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
