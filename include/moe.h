@@ -731,8 +731,10 @@ int moe_combine_backward(const void* expert_out, int eo_dtype, const float* w, c
  *                 s / sum s (sigmoid)
  *   z-loss:       z_coef * mean_t (logsumexp_e l[t,e])^2
  * All f32.  An expert at -inf has weight and gradient 0, and a token whose every
- * logit is -inf adds nothing to either loss; other infinities and NaN give NaN in
- * their own row.
+ * logit is -inf adds nothing to either loss.  A NaN, and with softmax scores or the
+ * z-loss a +inf, gives NaN in its own row wherever the formulas have it enter (the
+ * renormalised forms without an auxiliary loss read the chosen experts' logits
+ * only); a sigmoid score of +inf is 1 with slope 0, and adds a gradient of 0.
  *   logits         f32 [T,E] (with the bias, as moe_route_topk's logits_out)
  *   topk_ids       int32 [T,K], distinct per token; an id outside [0,E) is
  *                  skipped and raises MOE_STATUS_BAD_ID
