@@ -29,10 +29,6 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
-  return __half2float(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3));
-}
-
 // 8 bf16 values of a 16-byte vector
 __device__ __forceinline__ void widen8(const uint4& a, float (&v)[8]) {
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};

@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
 }
 
 constexpr int kEpiWarps = 16;
-constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of other roles (one of its warps idle)
+constexpr int kThreads = 128 + 32 * kEpiWarps;   // a warpgroup of the other roles
 constexpr int kAuxRegs = 64, kEpiRegs = 104;
 // the split draws on the registers the block was launched with (96 a thread)
 static_assert(128 * kAuxRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 96, "register split");

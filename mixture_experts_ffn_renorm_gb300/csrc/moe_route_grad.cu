@@ -7,7 +7,7 @@
 // every product is exact in f32.  Both products take all three parts: the rows of a
 // softmax router's dl sum to zero, so what the rows of W have in common cancels in dx, and
 // what is left can lie below the 16 bits of hi + mid (which took dx 15.5 us instead of
-// 18.8).  x and W are read as they lie in memory: their contiguous dimension is an output
+// 18.7).  x and W are read as they lie in memory: their contiguous dimension is an output
 // dimension of both products, so they go to the tensor core as MN-major operands straight
 // from TMA boxes.
 //
@@ -30,7 +30,7 @@
 //       memory (600: a timing copy without them takes 1250 a step).  Sixteen converting
 //       warps instead of eight took 28.4 us, so it is not the conversion's latency.
 //   dx  CTA: 128 tokens x 256 columns of H, 64 experts a step; dl is split into three
-//       K-major operand tiles.  Two CTAs share an SM and fill each other's gaps.  18.8 us
+//       K-major operand tiles.  Two CTAs share an SM and fill each other's gaps.  18.7 us
 //       alone for 34 MB written, in 1.7 rounds of CTAs that each load, split, multiply and
 //       store in turn; dW starts beside its last ones.
 #include <atomic>

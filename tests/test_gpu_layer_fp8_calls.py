@@ -64,3 +64,14 @@ def test_backward_is_of_the_last_forward():
     got = blk.backward(x, dout)
     for k, v in want.items():
         assert torch.equal(got[k], v), k
+
+
+def test_no_tokens():
+    blk, x, (dout, _) = problem(5, 128, 64, 8, 2)
+    blk.forward(x)
+    blk.backward(x, dout, 0.1, 0.1)
+    assert blk.forward(x[:0]).shape == (0, 128)
+    got = blk.backward(x[:0], dout[:0], 0.1, 0.1)      # sums over no token, in place of the call before's
+    assert got["grad_x"].shape == (0, 128) and got["grad_topk_w"].shape == (0, 2)
+    for k in ("grad_w_router", "grad_logit_bias", "losses"):
+        assert (got[k] == 0).all(), k
