@@ -776,6 +776,149 @@ int moe_route_logits_backward(const float* grad_logits, const void* x_bf16,
 size_t moe_route_logits_backward_workspace_size(int T, int H, int E);
 
 /* ------------------------------------------------------------------------
+ * moe_layer_few_bf16 / moe_layer_few_fp8w -- a whole MoE layer for at most 16
+ * tokens in one launch: router, chosen experts, optional shared expert, weighted
+ * sum, residual.
+ *   ids, w   as moe_route_topk / moe_route_topk_ex give them for the same
+ *            arguments, bit for bit
+ *   y_e(x) = W2_e ( silu(W13_e[:I] x) * (W13_e[I:] x) ),  silu(z) = z / (1 + exp(-z))
+ *   out[t] = bf16( sum_j (w[t,j] routed_scale) y_ids[t,j](x[t])
+ *                  + gate[t] y_shared(x[t]) + residual[t] )
+ * gate = sigmoid(w_shared_gate . x[t]), 1 without w_shared_gate.  Everything
+ * between the weights and out is f32: unlike the launches of the block, nothing is
+ * narrowed before the activation, before the down product or per expert row, so
+ * the two agree within the bf16 roundings of those.  Sums are in a fixed order: the same
+ * call gives the same bits on GPUs of the same SM count.
+ *   w13, w2     bf16 [E, 2I, H] (gate rows first), [E, H, I]; fp8w: E4M3 codes with
+ *               f32 scales per 128 x 128 block as for the *_fp8w calls, each weight
+ *               f32(code) * scale, not rounded
+ *   w_shared_gate, w13_shared, w2_shared   bf16 [H] or NULL, [2 Is, H], [H, Is] (bf16 with
+ *               either kind of experts); NULL when I_shared is 0
+ *   residual    bf16 [T, H] or NULL; may be x, and out may be either
+ *   topk_ids    int32 [T, K] out or NULL;  topk_w f32 [T, K] out or NULL
+ *   workspace   >= moe_layer_few_workspace_size(...) bytes, 16-byte aligned,
+ *               zero-filled before its first use and then passed to later calls
+ *               unchanged (it holds a barrier; calls of any sizes that it is large enough for
+ *               may share it).  Calls that may run at the same time need their own.  After
+ *               MOE_STATUS_TIMEOUT it is zero-filled again.
+ *   0 <= T <= 16; 1 <= H, I <= 8192 multiples of 8 (fp8w: 16); 0 <= I_shared <= 8192, a
+ *   multiple of 8; E, K, renormalize, scoring, n_group, topk_group, group_score as
+ *   moe_route_topk_ex
+ * The launch is cooperative: its CTAs, one per SM, start together or not at all.
+ * Errors: those of moe_route_topk_ex; MOE_ERR_ARG (T or a size outside its range, NULL
+ * operands, a shared expert's weights with I_shared 0), MOE_ERR_ALIGN (x, weights and
+ * workspace 16 bytes, f32 and int arrays 4, residual and out 2; the multiples above),
+ * MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  A device-side wait that runs past its limit
+ * (moe_set_wait_limit_ns) sets MOE_STATUS_TIMEOUT.
+ * ---------------------------------------------------------------------- */
+enum { MOE_LAYER_FEW_MAX_TOKENS = 16 };
+int moe_layer_few_bf16(const void* x_bf16, const void* w_router_bf16, const float* logit_bias,
+                       const float* select_bias, const void* w13_bf16, const void* w2_bf16,
+                       const void* w_shared_gate_bf16, const void* w13_shared_bf16,
+                       const void* w2_shared_bf16, const void* residual_bf16, int T, int H, int I,
+                       int E, int K, int I_shared, int renormalize, int scoring, int n_group,
+                       int topk_group, int group_score, float routed_scale, int32_t* topk_ids,
+                       float* topk_w, void* out_bf16, void* workspace, size_t ws_bytes,
+                       void* stream);
+int moe_layer_few_fp8w(const void* x_bf16, const void* w_router_bf16, const float* logit_bias,
+                       const float* select_bias, const uint8_t* w13_e4m3, const float* w13_scale,
+                       const uint8_t* w2_e4m3, const float* w2_scale,
+                       const void* w_shared_gate_bf16, const void* w13_shared_bf16,
+                       const void* w2_shared_bf16, const void* residual_bf16, int T, int H, int I,
+                       int E, int K, int I_shared, int renormalize, int scoring, int n_group,
+                       int topk_group, int group_score, float routed_scale, int32_t* topk_ids,
+                       float* topk_w, void* out_bf16, void* workspace, size_t ws_bytes,
+                       void* stream);
+size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int K, int I_shared);
+
+/* ------------------------------------------------------------------------
+ * moe_grouped_gemm_bias_act_bf16 -- grouped product with bias, activation, row weight
+ * and residual in its epilogue: the projections of experts that are plain two-layer
+ * networks, and (G = 1) of dense layers.  For row r of group g and dst =
+ * row_to_pair ? row_to_pair[r] : r:
+ *   z[r,n]     = sum_k a[r,k] w_g(n,k) + bias[g,n]
+ *   pre_act[r] = bf16(z[r])                                  (when given)
+ *   out[dst,n] = bf16( act(z[r,n]) * pair_weight[dst] + residual[dst,n] )
+ * Sums and epilogue are f32, each output rounded once, no multiply without pair_weight.
+ *   activation  MOE_ACT_*: none; relu max(z, 0); relu2 max(z, 0)^2; gelu z Phi(z);
+ *               gelu_tanh 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); silu z / (1 + exp(-z)).
+ *               The exponentials are the fast ones (a few binary32 ulps), Phi is off by
+ *               at most 1e-7.
+ *   a           bf16 [P, K], rows in group order
+ *   w           w_layout MOE_W_ROWS: bf16 [G, N, K], a row per output column;
+ *               MOE_W_COLUMNS: bf16 [G, K, N].  With the weights of a MOE_W_ROWS product of
+ *               a [P, K] and its dz [P, N] as a, MOE_W_COLUMNS (K and N exchanged) gives the
+ *               gradient of that product's rows.
+ *   bias        f32 [G, N] or NULL
+ *   pre_act     bf16 [P, N] out, row order, or NULL (what moe_bias_act_backward reads)
+ *   pair_weight f32 [P] indexed by dst, or NULL;  row_to_pair int32 [P] or NULL; a dst
+ *               outside [0, P) is skipped, no two rows have the same one
+ *   residual    bf16 [P, N] indexed by dst, or NULL; may be out
+ *   group_offsets int32 [G+1], read on the device, clamped to [0, P]; may be NULL when G == 1
+ *   out         bf16 [P, N]; rows outside every group are not written
+ *   workspace   moe_grouped_gemm_bias_act_workspace_size(P, K, N, G) bytes, 16-byte aligned, for
+ *               the sums of calls of few rows, which cut K into ranges to use every SM.  A
+ *               size queried for the most rows serves every call.  A smaller one, or NULL,
+ *               costs speed only (fewer ranges, whose last bits differ).  Calls that may
+ *               run at the same time need their own.
+ *   P >= 0; K and N multiples of 8; 1 <= G <= 1024
+ *
+ * moe_bias_act_backward -- through that epilogue, dy[r] = dout[dst] * pair_weight[dst]:
+ *   dz[r,n]               = bf16( dy[r,n] act'(z[r,n]) )
+ *   grad_bias[g,n]        = sum over g's rows of dy[r,n] act'(z[r,n])      f32, not rounded
+ *   grad_pair_weight[dst] = sum_n dout[dst,n] act(z[r,n])                  f32
+ * (the residual's gradient is dout itself; relu's slope at 0 is 0).  Sums are f32 in
+ * a fixed order: the same call gives the same bits.
+ *   dout       bf16 [P, N] indexed by dst;  z bf16 [P, N] (pre_act), may be NULL
+ *              without activation and grad_pair_weight
+ *   dz         bf16 [P, N] out, may be z;  grad_bias f32 [G, N] out or NULL (0 for an
+ *              empty group);  grad_pair_weight f32 [P] out or NULL (needs no pair_weight)
+ *              A row with a dst outside [0, P) has dz 0; rows outside every group are not written.
+ *   workspace  >= moe_bias_act_backward_workspace_size(P, N, G) bytes, 16-byte aligned
+ *
+ * moe_grouped_gemm_wgrad_bf16 -- the weights' gradient of a MOE_W_ROWS product:
+ *   grad_w[g,n,k] = (add_to ? add_to[g,n,k] : 0) + sum over g's rows of dz[r,n] a[r,k]    f32
+ * The tensor core adds at most 512 rows in one accumulator; those sums are joined in
+ * f32 in row order.  A fixed order: the same call gives the same bits.
+ *   dz bf16 [P, N], a bf16 [P, K];  add_to, grad_w f32 [G, N, K]; add_to may be grad_w
+ *   workspace  >= moe_grouped_gemm_wgrad_workspace_size(P, N, K, G) bytes, 16-byte aligned; NULL when that is 0
+ *   Every group is written, empty ones too.
+ *
+ * Errors of the three: MOE_ERR_ARG (sizes; P, K or N above 2^31 - 2^12; activation, w_layout; NULL operands, NULL
+ * group_offsets with G > 1; no output), MOE_ERR_ALIGN (bf16 and f32 matrices and the workspace 16 bytes,
+ * other f32 and indices 4; the multiples of 8), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  P = 0
+ * is a no-op but for grad_bias and grad_w.  A device-side wait that runs past its limit
+ * sets MOE_STATUS_TIMEOUT (moe_set_wait_limit_ns).
+ * ---------------------------------------------------------------------- */
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_RELU2 = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4,
+  MOE_ACT_SILU = 5
+};
+enum { MOE_W_ROWS = 0, MOE_W_COLUMNS = 1 };
+int moe_grouped_gemm_bias_act_bf16(const void* a_bf16, const void* w_bf16, int w_layout,
+                                   const float* bias, int activation, void* pre_act_bf16,
+                                   const float* pair_weight, const int32_t* row_to_pair,
+                                   const void* residual_bf16, const int32_t* group_offsets, int P,
+                                   int K, int N, int G, void* out_bf16, void* workspace,
+                                   size_t ws_bytes, void* stream);
+size_t moe_grouped_gemm_bias_act_workspace_size(int P, int K, int N, int G);
+int moe_bias_act_backward(const void* dout_bf16, const void* z_bf16, int activation,
+                          const float* pair_weight, const int32_t* row_to_pair,
+                          const int32_t* group_offsets, int P, int N, int G, void* dz_bf16,
+                          float* grad_bias, float* grad_pair_weight, void* workspace,
+                          size_t ws_bytes, void* stream);
+size_t moe_bias_act_backward_workspace_size(int P, int N, int G);
+int moe_grouped_gemm_wgrad_bf16(const void* dz_bf16, const void* a_bf16,
+                                const int32_t* group_offsets, int P, int N, int K, int G,
+                                const float* add_to, float* grad_w, void* workspace,
+                                size_t ws_bytes, void* stream);
+size_t moe_grouped_gemm_wgrad_workspace_size(int P, int N, int K, int G);
+
+/* ------------------------------------------------------------------------
  * Introspection (not on the hot path; these synchronise the device).
  *
  * moe_device_status: reads and optionally clears the library's device status
@@ -820,7 +963,14 @@ enum {
   MOE_KID_ROUTE_REDUCE = 29,     /* moe_route_logits_backward: their sums over token ranges */
   MOE_KID_GEMM_FP8_FEW = 30,     /* the launches of 20 and 21 that read the weights row by row:
                                     calls of few rows and products */
-  MOE_KID_COUNT = 32
+  MOE_KID_LAYER_FEW = 31,         /* moe_layer_few_bf16, moe_layer_few_fp8w */
+  MOE_KID_GEMM_BIAS_ACT = 32,     /* moe_grouped_gemm_bias_act_bf16 */
+  MOE_KID_BIAS_ACT_JOIN = 33,     /* moe_grouped_gemm_bias_act_bf16: the sum over ranges of K */
+  MOE_KID_BIAS_ACT_BACKWARD = 34, /* moe_bias_act_backward */
+  MOE_KID_BIAS_ACT_REDUCE = 35,   /* moe_bias_act_backward: sums over row and column blocks */
+  MOE_KID_GEMM_WGRAD = 36,        /* moe_grouped_gemm_wgrad_bf16 */
+  MOE_KID_WGRAD_REDUCE = 37,      /* moe_grouped_gemm_wgrad_bf16: the sum over ranges of rows */
+  MOE_KID_COUNT = 40
 };
 int moe_device_status(int* status_out, int clear);
 int moe_launch_counts(unsigned long long* counts, int n);

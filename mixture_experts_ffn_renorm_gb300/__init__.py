@@ -29,8 +29,10 @@ KID = {
     "exp_sigmoid": 18, "quant_fp8": 19, "gemm_fp8": 20, "gemm_fp8_gateup": 21,
     "silu_backward": 22, "transpose_fp8": 23, "combine_backward": 24, "route_backward": 25,
     "route_losses": 26, "route_dx": 27, "route_dw": 28, "route_reduce": 29, "gemm_fp8_few": 30,
+    "layer_few": 31, "gemm_bias_act": 32, "bias_act_join": 33, "bias_act_backward": 34,
+    "bias_act_reduce": 35, "gemm_wgrad": 36, "wgrad_reduce": 37,
 }
-KID_COUNT = 32
+KID_COUNT = 40
 QFMT_Q8_0, QFMT_Q4_K = 1, 2
 
 EXPORTS = (
@@ -48,7 +50,11 @@ EXPORTS = (
     "moe_quantize_act_fp8", "moe_grouped_gemm_fp8", "moe_grouped_gemm_gateup_silu_fp8",
     "moe_silu_mul_backward_fp8", "moe_transpose_fp8w", "moe_combine_backward",
     "moe_route_backward", "moe_route_backward_workspace_size", "moe_route_logits_backward",
-    "moe_route_logits_backward_workspace_size",
+    "moe_route_logits_backward_workspace_size", "moe_layer_few_bf16", "moe_layer_few_fp8w",
+    "moe_layer_few_workspace_size", "moe_grouped_gemm_bias_act_bf16",
+    "moe_grouped_gemm_bias_act_workspace_size", "moe_bias_act_backward",
+    "moe_bias_act_backward_workspace_size", "moe_grouped_gemm_wgrad_bf16",
+    "moe_grouped_gemm_wgrad_workspace_size",
 )
 
 
@@ -116,6 +122,16 @@ _SIGS = {
     "moe_route_backward_workspace_size": ([_I, _I], _SZ),
     "moe_route_logits_backward": ([_P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P], _I),
     "moe_route_logits_backward_workspace_size": ([_I, _I, _I], _SZ),
+    "moe_layer_few_bf16": ([_P] * 10 + [_I] * 11 + [_F] + [_P] * 4 + [_SZ, _P], _I),
+    "moe_layer_few_fp8w": ([_P] * 12 + [_I] * 11 + [_F] + [_P] * 4 + [_SZ, _P], _I),
+    "moe_layer_few_workspace_size": ([_I] * 6, _SZ),
+    "moe_grouped_gemm_bias_act_bf16": ([_P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P,
+                                        _P, _SZ, _P], _I),
+    "moe_grouped_gemm_bias_act_workspace_size": ([_I] * 4, _SZ),
+    "moe_bias_act_backward": ([_P, _P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P], _I),
+    "moe_bias_act_backward_workspace_size": ([_I] * 3, _SZ),
+    "moe_grouped_gemm_wgrad_bf16": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _SZ, _P], _I),
+    "moe_grouped_gemm_wgrad_workspace_size": ([_I] * 4, _SZ),
     "moe_launch_counts": ([ctypes.POINTER(ctypes.c_ulonglong), _I], _I),
 }
 
@@ -479,6 +495,90 @@ def moe_route_logits_backward(grad_logits, x, w_router, T, H, E, grad_x, grad_w_
 
 def moe_route_logits_backward_workspace_size(T, H, E) -> int:
     return lib().moe_route_logits_backward_workspace_size(T, H, E)
+
+
+LAYER_FEW_MAX_TOKENS = 16
+
+
+def moe_layer_few_bf16(x, w_router, logit_bias, select_bias, w13, w2, w_shared_gate, w13_shared,
+                       w2_shared, residual, T, H, I, E, K, I_shared, renormalize, scoring, n_group,
+                       topk_group, group_score, routed_scale, topk_ids, topk_w, out, workspace,
+                       ws_bytes, stream=None, check=True):
+    """A whole MoE layer for at most LAYER_FEW_MAX_TOKENS tokens in one launch (see moe.h)."""
+    rc = lib().moe_layer_few_bf16(_ptr(x), _ptr(w_router), _ptr(logit_bias), _ptr(select_bias),
+                                  _ptr(w13), _ptr(w2), _ptr(w_shared_gate), _ptr(w13_shared),
+                                  _ptr(w2_shared), _ptr(residual), T, H, I, E, K, I_shared,
+                                  renormalize, scoring, n_group, topk_group, group_score,
+                                  float(routed_scale), _ptr(topk_ids), _ptr(topk_w), _ptr(out),
+                                  _ptr(workspace), ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_layer_few_fp8w(x, w_router, logit_bias, select_bias, w13_e4m3, w13_scale, w2_e4m3, w2_scale,
+                       w_shared_gate, w13_shared, w2_shared, residual, T, H, I, E, K, I_shared,
+                       renormalize, scoring, n_group, topk_group, group_score, routed_scale,
+                       topk_ids, topk_w, out, workspace, ws_bytes, stream=None, check=True):
+    """The same with block-scaled FP8 expert weights (see moe.h)."""
+    rc = lib().moe_layer_few_fp8w(_ptr(x), _ptr(w_router), _ptr(logit_bias), _ptr(select_bias),
+                                  _ptr(w13_e4m3), _ptr(w13_scale), _ptr(w2_e4m3), _ptr(w2_scale),
+                                  _ptr(w_shared_gate), _ptr(w13_shared), _ptr(w2_shared),
+                                  _ptr(residual), T, H, I, E, K, I_shared, renormalize, scoring,
+                                  n_group, topk_group, group_score, float(routed_scale),
+                                  _ptr(topk_ids), _ptr(topk_w), _ptr(out), _ptr(workspace),
+                                  ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_layer_few_workspace_size(T, H, I, E, K, I_shared) -> int:
+    return lib().moe_layer_few_workspace_size(T, H, I, E, K, I_shared)
+
+
+# activations and weight layouts of the products with an epilogue
+ACT_NONE, ACT_RELU, ACT_RELU2, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(6)
+W_ROWS, W_COLUMNS = 0, 1
+
+
+def moe_grouped_gemm_bias_act_bf16(a, w, w_layout, bias, activation, pre_act, pair_weight,
+                                   row_to_pair, residual, group_offsets, P, K, N, G, out,
+                                   workspace=None, ws_bytes=0, stream=None, check=True):
+    """Grouped product with bias, activation, row weight and residual (see moe.h)."""
+    rc = lib().moe_grouped_gemm_bias_act_bf16(
+        _ptr(a), _ptr(w), w_layout, _ptr(bias), activation, _ptr(pre_act), _ptr(pair_weight),
+        _ptr(row_to_pair), _ptr(residual), _ptr(group_offsets), P, K, N, G, _ptr(out),
+        _ptr(workspace), ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_grouped_gemm_bias_act_workspace_size(P, K, N, G) -> int:
+    return lib().moe_grouped_gemm_bias_act_workspace_size(P, K, N, G)
+
+
+def moe_bias_act_backward(dout, z, activation, pair_weight, row_to_pair, group_offsets, P, N, G, dz,
+                          grad_bias, grad_pair_weight, workspace=None, ws_bytes=0, stream=None,
+                          check=True):
+    """Gradient of that epilogue: dz, bias and row weights (see moe.h)."""
+    rc = lib().moe_bias_act_backward(_ptr(dout), _ptr(z), activation, _ptr(pair_weight),
+                                     _ptr(row_to_pair), _ptr(group_offsets), P, N, G, _ptr(dz),
+                                     _ptr(grad_bias), _ptr(grad_pair_weight), _ptr(workspace),
+                                     ws_bytes, _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_bias_act_backward_workspace_size(P, N, G) -> int:
+    return lib().moe_bias_act_backward_workspace_size(P, N, G)
+
+
+def moe_grouped_gemm_wgrad_bf16(dz, a, group_offsets, P, N, K, G, add_to, grad_w, workspace=None,
+                                ws_bytes=0, stream=None, check=True):
+    """Gradient of the grouped product's weights, f32, optionally added to a sum (see moe.h)."""
+    rc = lib().moe_grouped_gemm_wgrad_bf16(_ptr(dz), _ptr(a), _ptr(group_offsets), P, N, K, G,
+                                           _ptr(add_to), _ptr(grad_w), _ptr(workspace), ws_bytes,
+                                           _stream(stream))
+    return _check(rc) if check else rc
+
+
+def moe_grouped_gemm_wgrad_workspace_size(P, N, K, G) -> int:
+    return lib().moe_grouped_gemm_wgrad_workspace_size(P, N, K, G)
 
 
 def moe_gate_workspace_size(T) -> int:

@@ -96,6 +96,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // of 64 columns x box_rows rows and the 128-byte swizzle
 int make_tmap(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows,
               const char* op, const char* what);
+// the same for `groups` such matrices one behind the other, as a three-dimensional map: what a
+// box reads beyond a matrix's rows or columns is zero, not the next matrix
+int make_tmap3(CUtensorMap* m, const void* base, int groups, int rows, int cols, int box_rows,
+               const char* op, const char* what);
 // the same for one-byte elements (FP8 codes), unswizzled
 int make_tmap_u8(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows,
                  const char* op, const char* what);

@@ -1,0 +1,253 @@
+// moe_bias_act_grad.cu -- the gradient of the products' epilogue (moe_gemm_bias_act.cu):
+//
+//   dy[r] = dout[dst] * pair_weight[dst],  s = dy act'(z):  dz = bf16(s),
+//   grad_bias[g] = sum of s over g's rows,  grad_pair_weight[dst] = sum_n dout[dst,n] act(z[r,n])
+//
+// One pass over dout and z: what bounds it is HBM (6 bytes an element).  A CTA takes 32 rows x 1024
+// columns; a warp a row at a time, a lane 8 columns of each 256, so that its column sums stay
+// in 32 registers and its row sum is one butterfly.  A CTA's rows may meet several groups: at
+// each group's end the warps' column sums are joined through shared memory in warp order and
+// leave as one partial row.  Block c and group g meet in partial row c + g: along the rows
+// either index or both step up, so no two meetings share one, and the second kernel finds a
+// group's rows from its offsets alone.  It adds them in block order: fixed order, no atomics.
+#include "activation.cuh"
+#include "gemm_common.cuh"
+
+namespace moe {
+namespace gemm {
+namespace {
+
+constexpr int kRows = 32;            // rows of a CTA
+constexpr int kCols = 1024;          // columns of a CTA: 32 per lane
+constexpr int kWarps = 8;
+
+struct BackParams {
+  const uint16_t* dout;
+  const uint16_t* z;
+  int activation;
+  const float* pair_weight;
+  const int32_t* row_to_pair;
+  const int32_t* group_offsets;
+  int P, N, G;
+  uint16_t* dz;
+  float* part_b;                     // [blocks + G][N] column sums, or null
+  float* part_w;                     // [column blocks][P] row sums by dst, or null
+  unsigned long long* launches;
+};
+
+__device__ __forceinline__ int offset_at(const int32_t* off, int i, int P) {
+  return off ? min(max(__ldg(off + i), 0), P) : (i == 0 ? 0 : P);
+}
+
+__device__ __forceinline__ void widen(const uint4& u, float (&v)[8]) {
+  const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(q[i] << 16);
+    v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+  }
+}
+
+template <int kAct>
+__global__ void __launch_bounds__(32 * kWarps)
+bias_act_backward_kernel(const BackParams p) {
+  __shared__ float s_sum[kWarps][kCols];
+  count_launch(p.launches, MOE_KID_BIAS_ACT_BACKWARD);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int block = blockIdx.x, r_lo = block * kRows, r_hi = min(p.P, r_lo + kRows);
+  const int n0 = blockIdx.y * kCols + lane * 8;
+  // the last group that starts at or before the block's first row
+  int before = 0;
+  for (int g0 = 0; g0 < p.G; g0 += 32 * kWarps) {
+    const int g = g0 + static_cast<int>(threadIdx.x);
+    before += __syncthreads_count(g < p.G && offset_at(p.group_offsets, g, p.P) <= r_lo);
+  }
+  int g = max(before - 1, 0);
+  for (int r0 = max(r_lo, offset_at(p.group_offsets, g, p.P)); g < p.G; ++g) {
+    const int r1 = min(r_hi, offset_at(p.group_offsets, g + 1, p.P));
+    if (r1 > r0) {
+      float sum[kCols / 256][8] = {};
+      for (int r = r0 + warp; r < r1; r += kWarps) {
+        const int d = p.row_to_pair ? __ldg(p.row_to_pair + r) : r;
+        const bool in = d >= 0 && d < p.P;
+        const float w = in && p.pair_weight ? __ldg(p.pair_weight + d) : 1.0f;
+        uint4 dv[kCols / 256], zv[kCols / 256];
+#pragma unroll
+        for (int i = 0; i < kCols / 256; ++i) {
+          const int n = n0 + 256 * i;
+          const bool on = in && n < p.N;
+          dv[i] = on ? *reinterpret_cast<const uint4*>(p.dout + static_cast<size_t>(d) * p.N + n)
+                     : make_uint4(0, 0, 0, 0);
+          zv[i] = on && p.z ? *reinterpret_cast<const uint4*>(p.z + static_cast<size_t>(r) * p.N + n)
+                            : make_uint4(0, 0, 0, 0);
+        }
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kCols / 256; ++i) {
+          const int n = n0 + 256 * i;
+          if (n >= p.N) continue;
+          float dy[8], zz[8];
+          widen(dv[i], dy);
+          widen(zv[i], zz);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float y;
+            const float s = act::slope<kAct>(zz[k], y);
+            dot = fmaf(dy[k], y, dot);
+            dy[k] = in ? __fmul_rn(dy[k], w) * s : 0.0f;
+            sum[i][k] += dy[k];
+          }
+          *reinterpret_cast<uint4*>(p.dz + static_cast<size_t>(r) * p.N + n) =
+              make_uint4(pack_bf16x2(dy[0], dy[1]), pack_bf16x2(dy[2], dy[3]), pack_bf16x2(dy[4], dy[5]),
+                         pack_bf16x2(dy[6], dy[7]));
+        }
+        if (p.part_w) {
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+          if (lane == 0 && in) p.part_w[static_cast<size_t>(blockIdx.y) * p.P + d] = dot;
+        }
+      }
+      if (p.part_b) {
+#pragma unroll
+        for (int i = 0; i < kCols / 256; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; k += 4)
+            *reinterpret_cast<float4*>(&s_sum[warp][256 * i + lane * 8 + k]) =
+                make_float4(sum[i][k], sum[i][k + 1], sum[i][k + 2], sum[i][k + 3]);
+        __syncthreads();
+        const int c = threadIdx.x * 4, n = blockIdx.y * kCols + c;
+        if (n < p.N) {
+          float4 s = *reinterpret_cast<const float4*>(&s_sum[0][c]);
+#pragma unroll
+          for (int i = 1; i < kWarps; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(&s_sum[i][c]);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+          }
+          *reinterpret_cast<float4*>(p.part_b + (static_cast<size_t>(block) + g) * p.N + n) = s;
+        }
+        __syncthreads();
+      }
+      r0 = r1;
+    }
+    if (r0 >= r_hi) break;
+  }
+}
+
+// grad_bias: blockIdx.y is the group, a thread four columns; grad_pair_weight (rows of
+// blockIdx.y == G): a thread one row
+__global__ void __launch_bounds__(256)
+bias_act_reduce_kernel(const BackParams p, float* __restrict__ grad_bias, float* __restrict__ grad_w, int col_blocks) {
+  count_launch(p.launches, MOE_KID_BIAS_ACT_REDUCE);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int g = blockIdx.y;
+  if (grad_bias && g < p.G && 4 * i < p.N) {
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int r0 = offset_at(p.group_offsets, g, p.P), r1 = offset_at(p.group_offsets, g + 1, p.P);
+    if (r1 > r0) {
+      const float* q = p.part_b + static_cast<size_t>(g) * p.N + 4 * i;
+#pragma unroll 8
+      for (int b = r0 / kRows; b <= (r1 - 1) / kRows; ++b) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(b) * p.N));
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+    }
+    *reinterpret_cast<float4*>(grad_bias + static_cast<size_t>(g) * p.N + 4 * i) = s;
+  }
+  if (grad_w && g == p.G && i < p.P) {
+    // rows outside every group, and destinations that no row has, keep what they hold: this
+    // thread is a row, not a destination
+    const int lo = offset_at(p.group_offsets, 0, p.P), hi = offset_at(p.group_offsets, p.G, p.P);
+    const int d = p.row_to_pair ? __ldg(p.row_to_pair + i) : i;
+    if (i < lo || i >= hi || d < 0 || d >= p.P) return;
+    float s = __ldcg(p.part_w + d);
+    for (int b = 1; b < col_blocks; ++b) s += __ldcg(p.part_w + static_cast<size_t>(b) * p.P + d);
+    grad_w[d] = s;
+  }
+}
+
+int blocks_of(int n, int size) { return n / size + (n % size != 0); }
+size_t pad(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+size_t bias_bytes(int P, int N, int G) {
+  return pad((static_cast<size_t>(blocks_of(P, kRows)) + G) * N * 4);
+}
+
+}  // namespace
+}  // namespace gemm
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::gemm;
+
+extern "C" size_t moe_bias_act_backward_workspace_size(int P, int N, int G) {
+  if (P <= 0 || N <= 0 || G <= 0) return 0;
+  const size_t cb = blocks_of(N, kCols);
+  return bias_bytes(P, N, G) + (cb > 1 ? pad(cb * P * 4) : 0);
+}
+
+extern "C" int moe_bias_act_backward(const void* dout_bf16, const void* z_bf16, int activation,
+                                     const float* pair_weight, const int32_t* row_to_pair,
+                                     const int32_t* group_offsets, int P, int N, int G, void* dz_bf16,
+                                     float* grad_bias, float* grad_pair_weight, void* workspace,
+                                     size_t ws_bytes, void* stream) {
+  clear_error();
+  const char* op = "moe_bias_act_backward";
+  if (P < 0 || N < 1) return set_error(MOE_ERR_ARG, "%s: P=%d, N=%d", op, P, N);
+  if (P > kMaxDim || N > kMaxDim) return set_error(MOE_ERR_ARG, "%s: P=%d or N=%d is too large", op, P, N);
+  if (blocks_of(N, kCols) > 65535) return set_error(MOE_ERR_ARG, "%s: N=%d is too large", op, N);
+  if (G < 1 || G > kMaxGroups) return set_error(MOE_ERR_ARG, "%s: G=%d outside [1, %d]", op, G, kMaxGroups);
+  if (activation < MOE_ACT_NONE || activation > MOE_ACT_SILU)
+    return set_error(MOE_ERR_ARG, "%s: activation=%d is not a MOE_ACT_* value", op, activation);
+  if (N % 8) return set_error(MOE_ERR_ALIGN, "%s: N=%d must be a multiple of 8", op, N);
+  if (!group_offsets && G != 1) return set_error(MOE_ERR_ARG, "%s: group_offsets is NULL with G=%d", op, G);
+  if (P > 0 && (!dout_bf16 || !dz_bf16)) return set_error(MOE_ERR_ARG, "%s: dout or dz is NULL", op);
+  if (P > 0 && !z_bf16 && (activation != MOE_ACT_NONE || grad_pair_weight))
+    return set_error(MOE_ERR_ARG, "%s: an activation or grad_pair_weight needs z", op);
+  for (const void* q : {dout_bf16, z_bf16, const_cast<const void*>(dz_bf16), static_cast<const void*>(grad_bias),
+                        const_cast<const void*>(workspace)})
+    if (q && !aligned16(q))
+      return set_error(MOE_ERR_ALIGN, "%s: dout, z, dz, grad_bias and workspace must be 16-byte aligned", op);
+  for (const void* q : {static_cast<const void*>(pair_weight), static_cast<const void*>(row_to_pair),
+                        static_cast<const void*>(group_offsets), static_cast<const void*>(grad_pair_weight)})
+    if (reinterpret_cast<uintptr_t>(q) & 3u)
+      return set_error(MOE_ERR_ALIGN, "%s: weights and indices must be 4-byte aligned", op);
+  if (P == 0 && !grad_bias) return MOE_OK;
+  const int cb = blocks_of(N, kCols);
+  const bool rows = grad_pair_weight && cb > 1 && P > 0;   // row sums of several column blocks to join
+  const size_t need = (grad_bias && P > 0 ? bias_bytes(P, N, G) : 0) + (rows ? pad(static_cast<size_t>(cb) * P * 4) : 0);
+  if (need > 0 && (!workspace || ws_bytes < need))
+    return set_error(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes is smaller than the %zu needed", op,
+                     workspace ? ws_bytes : 0, need);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  BackParams p{};
+  p.dout = static_cast<const uint16_t*>(dout_bf16);
+  p.z = static_cast<const uint16_t*>(z_bf16);
+  p.activation = activation;
+  p.pair_weight = pair_weight;
+  p.row_to_pair = row_to_pair;
+  p.group_offsets = group_offsets;
+  p.P = P; p.N = N; p.G = G;
+  p.dz = static_cast<uint16_t*>(dz_bf16);
+  p.part_b = grad_bias ? static_cast<float*>(workspace) : nullptr;
+  float* joined = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (grad_bias ? bias_bytes(P, N, G) : 0));
+  p.part_w = rows ? joined : grad_pair_weight;
+  p.launches = device_diag().launches;
+  if (P > 0) {
+    void (*const kernels[])(BackParams) = {
+        bias_act_backward_kernel<MOE_ACT_NONE>, bias_act_backward_kernel<MOE_ACT_RELU>,
+        bias_act_backward_kernel<MOE_ACT_RELU2>, bias_act_backward_kernel<MOE_ACT_GELU>,
+        bias_act_backward_kernel<MOE_ACT_GELU_TANH>, bias_act_backward_kernel<MOE_ACT_SILU>};
+    const int rc = launch_status(launch_kernel(kernels[activation], dim3(blocks_of(P, kRows), cb), dim3(32 * kWarps), 0,
+                                               s, nullptr, 0, p),
+                                 op);
+    if (rc != MOE_OK) return rc;
+  }
+  if (!grad_bias && !rows) return MOE_OK;
+  const int x = blocks_of(grad_bias ? N / 4 : 0, 256), xr = rows ? blocks_of(P, 256) : 0;
+  return launch_status(launch_kernel(bias_act_reduce_kernel, dim3(x > xr ? x : xr, G + (rows ? 1 : 0)), dim3(256), 0, s,
+                                     nullptr, 0, p, grad_bias, rows ? grad_pair_weight : nullptr, cb),
+                       op);
+}

@@ -818,6 +818,25 @@ int make_tmap(CUtensorMap* m, const void* base, long long rows, int cols, int bo
   return MOE_OK;
 }
 
+int make_tmap3(CUtensorMap* m, const void* base, int groups, int rows, int cols, int box_rows,
+               const char* op, const char* what) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return set_error(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", op);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(groups)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2,
+                           static_cast<cuuint64_t>(cols) * 2 * static_cast<cuuint64_t>(rows)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(BK), static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(MOE_ERR_CUDA, "%s: tensor map for %s rejected (CUresult %d)", op, what,
+                     static_cast<int>(r));
+  return MOE_OK;
+}
+
 // rows x cols FP8 codes (one byte each, cols contiguous), box of 64 cols x box_rows
 // rows, unswizzled (the converter warps read it as plain rows of 64 bytes)
 int make_tmap_u8(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows,

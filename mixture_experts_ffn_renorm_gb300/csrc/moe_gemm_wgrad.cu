@@ -1,0 +1,434 @@
+// moe_gemm_wgrad.cu -- the weights' gradient of the grouped products:
+//
+//   grad_w[g] = add_to[g] + sum over g's rows r of dz[r, :]^T a[r, :]        f32 [N, K]
+//
+// A tile is 128 rows (of N) x 256 columns (of K) of one group's gradient on one SM; the
+// contraction runs over the group's rows, 64 a stage.  Both operands are read as they lie,
+// rows contiguous along N and K: MN-major operands of tcgen05.mma, in TMA boxes of 64 columns x 64
+// rows.  Where a group ends inside a stage, the rows behind it belong to the next group (or to
+// nobody: they may hold NaN), so the issuing warp overwrites them with zeros in both operands
+// up to the next 16, and the MMAs of the stage stop there.
+//
+// Two reasons keep the sums out of the tensor core's accumulators for long: its additions cut off
+// bits that f32 gradients of many rows would miss, and the next tile's products should not
+// wait for this tile's stores.  So every 512 rows the products move to the other accumulator
+// of 256 columns and the epilogue warps (a thread: one row, 128 columns) add the finished one to
+// their registers; a tile's sums leave through 4 KB of shared memory per warp as whole 128-byte
+// lines, with add_to's values read the same way.
+//
+// With a few groups of many rows there are fewer tiles than SMs: the rows are cut into ranges whose
+// sums go to the workspace, and a second kernel adds them in range order.
+#include <atomic>
+
+#include "fp8_common.cuh"
+
+namespace moe {
+namespace gemm {
+namespace {
+
+constexpr int kThreads = 320;        // producer, MMA, eight epilogue warps
+constexpr int kTileN = 128, kTileK = 256;
+constexpr int kRowsStage = 64;
+constexpr int kStages = 4;
+constexpr int kBox = 64 * kRowsStage * 2;          // 64 columns x 64 rows
+constexpr int kABytes = kTileN / 64 * kBox, kBBytes = kTileK / 64 * kBox;
+constexpr int kChunk = 8;            // stages of one accumulator: 512 rows
+constexpr int kMaxRanges = 16;
+constexpr int kRangeRows = 512;      // rows of a range, at least
+
+struct Params {
+  const int32_t* group_offsets;
+  int P, N, K, G;
+  const float* add_to;
+  float* out;                        // grad_w, or the ranges' sums
+  int ranges;
+  unsigned long long wait_ns;
+  unsigned int* status;
+  unsigned long long* launches;
+};
+
+struct Smem {
+  static constexpr int A = 0;
+  static constexpr int B = A + kStages * kABytes;
+  static constexpr int OUT = B + kStages * kBBytes;          // 8 warps x 4 KB
+  static constexpr int BARS = OUT + 8 * 4096;                // full, empty, tfull[2], tempty[2], drain
+  static constexpr int MISC = BARS + (2 * kStages + 5) * 8;
+  static constexpr int ALLOC = MISC + 16 + 1024;
+};
+static_assert(Smem::ALLOC <= 227 * 1024, "shared memory");
+
+struct Tile {
+  int g, n0, k0, range;
+  int r0, r1;                        // the rows of its sum
+};
+
+__device__ __forceinline__ Tile tile_of(const Params& p, long long i, int tn, int tk) {
+  Tile t;
+  const long long per = static_cast<long long>(tn) * tk * p.ranges;
+  t.g = static_cast<int>(i / per);
+  int local = static_cast<int>(i - t.g * per);
+  t.range = local / (tn * tk);
+  local -= t.range * tn * tk;
+  t.k0 = local / tn * kTileK;
+  t.n0 = local % tn * kTileN;
+  auto off = [&](int g) {
+    return p.group_offsets ? min(max(__ldg(p.group_offsets + g), 0), p.P) : (g == 0 ? 0 : p.P);
+  };
+  const int lo = off(t.g), hi = max(off(t.g + 1), lo);
+  if (p.ranges == 1) {
+    t.r0 = lo;
+    t.r1 = hi;
+  } else {                           // whole stages
+    const long long steps = (hi - lo) / kRowsStage + ((hi - lo) % kRowsStage != 0);
+    t.r0 = lo + static_cast<int>(steps * t.range / p.ranges) * kRowsStage;
+    const long long e = lo + steps * (t.range + 1) / p.ranges * kRowsStage;
+    t.r1 = e < hi ? static_cast<int>(e) : hi;
+  }
+  return t;
+}
+
+__device__ __forceinline__ int steps_of(const Tile& t) { return (t.r1 - t.r0 + kRowsStage - 1) / kRowsStage; }
+
+__global__ void __launch_bounds__(kThreads, 1)
+wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = ptx::smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::BARS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Smem::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Smem::MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar_full = [&](int s) { return ptx::smem_u32(bars + s); };
+  auto bar_empty = [&](int s) { return ptx::smem_u32(bars + kStages + s); };
+  auto bar_tfull = [&](int a) { return ptx::smem_u32(bars + 2 * kStages + a); };
+  auto bar_tempty = [&](int a) { return ptx::smem_u32(bars + 2 * kStages + 2 + a); };
+  const uint32_t bar_drain = ptx::smem_u32(bars + 2 * kStages + 4);
+
+  count_launch(p.launches, MOE_KID_GEMM_WGRAD);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bar_full(s), 1);
+      ptx::mbar_init(bar_empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(bar_tfull(a), 1);
+      ptx::mbar_init(bar_tempty(a), 8);
+    }
+    ptx::mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&tmA);
+    ptx::tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tn = (p.N + kTileN - 1) / kTileN, tk = (p.K + kTileK - 1) / kTileK;
+  const long long tiles = static_cast<long long>(p.G) * tn * tk * p.ranges;
+  uint32_t issued = 0;
+  bool mma_any = false;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (ptx::elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (long long i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+        const Tile t = tile_of(p, i, tn, tk);
+        for (int r = t.r0; r < t.r1; r += kRowsStage) {
+          ok = wait_bar_spin(bar_empty(stage), phase ^ 1u, abort_flag, p.status, p.wait_ns);
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(bar_full(stage), kABytes + kBBytes);
+#pragma unroll
+          for (int b = 0; b < kTileN / 64; ++b)
+            ptx::tma_load_2d(sb + Smem::A + stage * kABytes + b * kBox, &tmA, t.n0 + 64 * b, r, bar_full(stage));
+#pragma unroll
+          for (int b = 0; b < kTileK / 64; ++b)
+            ptx::tma_load_2d(sb + Smem::B + stage * kBBytes + b * kBox, &tmB, t.k0 + 64 * b, r, bar_full(stage));
+          ++issued;
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (a whole warp: it
+    // clears the rows behind a group's end)
+    constexpr uint32_t idesc = ptx::idesc_bf16_f32_mn(kTileN, kTileK, true, true);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, uses[2] = {0, 0};
+    bool ok = true;
+    for (long long i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+      const Tile t = tile_of(p, i, tn, tk);
+      const int steps = steps_of(t);
+      for (int st = 0; st < steps; ++st) {
+        const int in_chunk = st % kChunk;
+        if (in_chunk == 0) {
+          ok = wait_bar(bar_tempty(acc), ((acc ? uses[1] : uses[0]) & 1u) ^ 1u, abort_flag, p.status, p.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        ok = wait_bar(bar_full(stage), phase, abort_flag, p.status, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t a = sb + Smem::A + stage * kABytes, b = sb + Smem::B + stage * kBBytes;
+        const int rows = min(kRowsStage, t.r1 - t.r0 - st * kRowsStage), ends = (rows + 15) & ~15;
+        if (rows < ends) {
+          for (int r = rows + (lane >> 3); r < ends; r += 4) {
+#pragma unroll
+            for (int x = 0; x < kTileN / 64; ++x)
+              ptx::st_shared_v4(a + x * kBox + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int x = 0; x < kTileK / 64; ++x)
+              ptx::st_shared_v4(b + x * kBox + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ptx::tc_fence_after();
+        const bool last = in_chunk == kChunk - 1 || st == steps - 1;
+        if (ptx::elect_one()) {
+          const uint64_t da = ptx::desc_mnmajor_sw128(a, kBox), db = ptx::desc_mnmajor_sw128(b, kBox);
+#pragma unroll
+          for (int k = 0; k < kRowsStage / 16; ++k)
+            if (16 * k < rows)
+              ptx::mma_bf16(tmem + static_cast<uint32_t>(acc) * kTileK, da + 128ull * k, db + 128ull * k, idesc,
+                            in_chunk != 0 || k != 0 ? 1u : 0u);
+          ptx::mma_commit(bar_empty(stage));
+          if (last) ptx::mma_commit(bar_tfull(acc));
+        }
+        __syncwarp();
+        mma_any = true;
+        if (last) {
+          if (acc) ++uses[1]; else ++uses[0];
+          acc ^= 1;
+        }
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;      // TMEM lane quarter; 128 of the columns
+    const uint32_t ost = sb + Smem::OUT + (warp - 2) * 4096;
+    int acc = 0;
+    uint32_t uses[2] = {0, 0};
+    bool ok = true;
+    for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
+      const Tile t = tile_of(p, i, tn, tk);
+      const int steps = steps_of(t);
+      float sum[128];
+#pragma unroll
+      for (int k = 0; k < 128; ++k) sum[k] = 0.0f;
+      for (int st = 0; st < steps; st += kChunk) {
+        ok = ok && wait_bar(bar_tfull(acc), (acc ? uses[1] : uses[0]) & 1u, abort_flag, p.status, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc) * kTileK + half * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(ta + 32 * c, v);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sum[32 * c + k] += __uint_as_float(v[k]);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_tempty(acc));
+        if (acc) ++uses[1]; else ++uses[0];
+        acc ^= 1;
+      }
+      if (!ok) break;
+      // 32 rows x 32 columns at a time: 128 bytes a row, 16-byte pieces XOR-swizzled by the row;
+      // eight lanes store a row
+      const size_t base = (static_cast<size_t>(t.range) * p.G + t.g) * p.N;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          ptx::st_shared_v4(ost + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(sum[32 * c + 4 * k]),
+                            __float_as_uint(sum[32 * c + 4 * k + 1]), __float_as_uint(sum[32 * c + 4 * k + 2]),
+                            __float_as_uint(sum[32 * c + 4 * k + 3]));
+        __syncwarp();
+        const int col = t.k0 + half * 128 + 32 * c + (lane & 7) * 4;
+#pragma unroll
+        for (int k0 = 0; k0 < 8; k0 += 4) {
+          float4 add[4];
+          if (p.add_to) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int n = t.n0 + q * 32 + 4 * (k0 + k) + (lane >> 3);
+              add[k] = n < p.N && col < p.K ? *reinterpret_cast<const float4*>(p.add_to + (base + n) * p.K + col)
+                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = 4 * (k0 + k) + (lane >> 3), n = t.n0 + q * 32 + r;
+            const uint4 u = ptx::ld_shared_v4(ost + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            float4 s = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                   __uint_as_float(u.w));
+            if (p.add_to) {
+              s.x += add[k].x; s.y += add[k].y; s.z += add[k].z; s.w += add[k].w;
+            }
+            if (n < p.N && col < p.K)      // K % 8 == 0: four columns are in or out together
+              *reinterpret_cast<float4*>(p.out + (base + n) * p.K + col) = s;
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  // ---- exit: a CTA that gave up drains its copies and MMAs first
+  __syncthreads();
+  if (*abort_flag != 0) {
+    if (warp == 1 && mma_any && ptx::elect_one()) {
+      ptx::mma_commit(bar_drain);
+      spin_bounded(bar_drain, 0);
+    }
+    for (uint32_t i = issued < kStages ? 0 : issued - kStages; i < issued; ++i)
+      spin_bounded(bar_full(i % kStages), (i / kStages) & 1);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// the ranges' sums in range order, on add_to
+__global__ void __launch_bounds__(256)
+wgrad_reduce_kernel(const float* __restrict__ part, int ranges, long long n4, const float* add_to, float* out,
+                    unsigned long long* launches) {
+  count_launch(launches, MOE_KID_WGRAD_REDUCE);
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const float4* q = reinterpret_cast<const float4*>(part) + i;
+  float4 v[kMaxRanges];
+#pragma unroll
+  for (int r = 0; r < kMaxRanges; ++r)
+    if (r < ranges) v[r] = __ldcg(q + r * n4);
+  float4 s = ranges > 0 ? v[0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int r = 1; r < kMaxRanges; ++r)
+    if (r < ranges) {
+      s.x += v[r].x; s.y += v[r].y; s.z += v[r].z; s.w += v[r].w;
+    }
+  if (add_to) {
+    const float4 a = reinterpret_cast<const float4*>(add_to)[i];
+    s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+  }
+  reinterpret_cast<float4*>(out)[i] = s;
+}
+
+// Ranges of rows: as many as give every SM a tile, each of at least kRangeRows of the average
+// group's rows
+int ranges_of(int P, int N, int K, int G) {
+  const long long tiles = static_cast<long long>(G) * ((N - 1ll) / kTileN + 1) * ((K - 1ll) / kTileK + 1);
+  long long s = sm_count() / tiles;
+  const long long most = P / G / kRangeRows;
+  s = s < most ? s : most;
+  s = s < kMaxRanges ? s : kMaxRanges;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+}  // namespace
+}  // namespace gemm
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::gemm;
+
+extern "C" size_t moe_grouped_gemm_wgrad_workspace_size(int P, int N, int K, int G) {
+  if (P <= 0 || N <= 0 || K <= 0 || G <= 0) return 0;
+  const int s = ranges_of(P, N, K, G);   // grows with P
+  return s < 2 ? 0 : static_cast<size_t>(s) * G * N * K * 4;
+}
+
+extern "C" int moe_grouped_gemm_wgrad_bf16(const void* dz_bf16, const void* a_bf16, const int32_t* group_offsets,
+                                           int P, int N, int K, int G, const float* add_to, float* grad_w,
+                                           void* workspace, size_t ws_bytes, void* stream) {
+  clear_error();
+  const char* op = "moe_grouped_gemm_wgrad_bf16";
+  if (P < 0 || N < 1 || K < 1) return set_error(MOE_ERR_ARG, "%s: P=%d, N=%d, K=%d", op, P, N, K);
+  if (P > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return set_error(MOE_ERR_ARG, "%s: P=%d, N=%d or K=%d is too large", op, P, N, K);
+  if (G < 1 || G > kMaxGroups) return set_error(MOE_ERR_ARG, "%s: G=%d outside [1, %d]", op, G, kMaxGroups);
+  if (N % 8 || K % 8) return set_error(MOE_ERR_ALIGN, "%s: N=%d and K=%d must be multiples of 8", op, N, K);
+  if (((N - 1ll) / kTileN + 1) * ((K - 1ll) / kTileK + 1) * kMaxRanges > kMaxDim ||
+      static_cast<double>(G) * N * K > 0x1p38)
+    return set_error(MOE_ERR_ARG, "%s: G=%d, N=%d and K=%d are too large together", op, G, N, K);
+  if (!grad_w) return set_error(MOE_ERR_ARG, "%s: grad_w is NULL", op);
+  if (!group_offsets && G != 1) return set_error(MOE_ERR_ARG, "%s: group_offsets is NULL with G=%d", op, G);
+  if (P > 0 && (!dz_bf16 || !a_bf16)) return set_error(MOE_ERR_ARG, "%s: dz or a is NULL", op);
+  for (const void* q : {dz_bf16, a_bf16, static_cast<const void*>(add_to), static_cast<const void*>(grad_w),
+                        const_cast<const void*>(workspace)})
+    if (q && !aligned16(q))
+      return set_error(MOE_ERR_ALIGN, "%s: dz, a, add_to, grad_w and workspace must be 16-byte aligned", op);
+  if (reinterpret_cast<uintptr_t>(group_offsets) & 3u)
+    return set_error(MOE_ERR_ALIGN, "%s: group_offsets must be 4-byte aligned", op);
+  const size_t need = moe_grouped_gemm_wgrad_workspace_size(P, N, K, G);
+  if (need > 0 && (!workspace || ws_bytes < need))
+    return set_error(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes is smaller than the %zu needed", op,
+                     workspace ? ws_bytes : 0, need);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t n = static_cast<size_t>(G) * N * K;
+  DeviceDiag diag = device_diag();
+  if (P == 0) {                      // sums of nothing
+    return launch_status(launch_kernel(wgrad_reduce_kernel, dim3(static_cast<unsigned>((n / 4 + 255) / 256)), dim3(256),
+                                       0, s, nullptr, 0, static_cast<const float*>(nullptr), 0,
+                                       static_cast<long long>(n / 4), add_to, grad_w, diag.launches),
+                         op);
+  }
+  Params p{};
+  p.group_offsets = group_offsets;
+  p.P = P; p.N = N; p.K = K; p.G = G;
+  p.ranges = ranges_of(P, N, K, G);
+  p.add_to = p.ranges > 1 ? nullptr : add_to;
+  p.out = p.ranges > 1 ? static_cast<float*>(workspace) : grad_w;
+  p.status = diag.status;
+  p.launches = diag.launches;
+  p.wait_ns = pipeline_wait_ns();
+  CUtensorMap ta, tb;
+  int rc;
+  if ((rc = make_tmap(&ta, dz_bf16, P, N, kRowsStage, op, "dz")) != MOE_OK) return rc;
+  if ((rc = make_tmap(&tb, a_bf16, P, K, kRowsStage, op, "a")) != MOE_OK) return rc;
+  static std::atomic<int> configured[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    dev = -1;
+  }
+  const bool cache = dev >= 0 && dev < 64;
+  if (!cache || !configured[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::ALLOC) != cudaSuccess)
+      return set_error(MOE_ERR_CUDA, "%s: cannot reserve %d bytes of shared memory: %s", op, Smem::ALLOC,
+                       cudaGetErrorString(cudaGetLastError()));
+    if (cache) configured[dev].store(1, std::memory_order_release);
+  }
+  const long long tiles =
+      static_cast<long long>(G) * ((N - 1) / kTileN + 1) * ((K - 1) / kTileK + 1) * p.ranges;
+  const int sms = sm_count();
+  rc = launch_status(launch_kernel(wgrad_kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kThreads),
+                                   Smem::ALLOC, s, nullptr, 0, ta, tb, p),
+                     op);
+  if (rc != MOE_OK || p.ranges == 1) return rc;
+  return launch_status(launch_kernel(wgrad_reduce_kernel, dim3(static_cast<unsigned>((n / 4 + 255) / 256)), dim3(256), 0, s,
+                                     nullptr, 0, static_cast<const float*>(workspace), p.ranges,
+                                     static_cast<long long>(n / 4), add_to, grad_w, diag.launches),
+                       op);
+}

@@ -16,6 +16,7 @@
 #include <math.h>
 
 #include "moe_common.cuh"
+#include "route_device.cuh"
 
 namespace moe {
 
@@ -26,7 +27,10 @@ int launch_router_logits(const void* x, const void* w_router, const float* bias,
 namespace {
 
 constexpr int kWarpsPerBlock = 8;
-constexpr int kMaxGroups = 64;   // n_group limit of the grouped router
+using route::kMaxGroups;
+using route::kTokWarp;
+using route::rank_key;
+using route::ranks_above;
 
 // The router forms beyond ungrouped softmax (selection bias, sigmoid scores,
 // expert groups); all off: the plain router.
@@ -37,17 +41,6 @@ struct RouteEx {
   int topk_group;            // groups that stay eligible
   int group_score;           // 0: a group's best key; 1: its two best keys added
 };
-
-// Order-preserving 32-bit key of a logit for the selection: larger key = ranks
-// higher.  -0 and +0 share a key (they compare equal), every NaN gets key 0
-// (below -inf, whose key is 0x007FFFFF), and equal keys go to the lower expert
-// id -- the order "descending value, ties to the lower id, NaN last".
-__device__ __forceinline__ uint32_t rank_key(float v) {
-  if (v != v) return 0u;
-  uint32_t u = __float_as_uint(v);
-  if ((u & 0x7FFFFFFFu) == 0u) u = 0u;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
 
 // shared-expert gate logit of token t: a plain f32 dot product of x[t] and wsg
 // (one warp; the result from lane 0)
@@ -72,20 +65,14 @@ __device__ __forceinline__ void shared_gate_logit(const uint16_t* __restrict__ x
 }
 
 // Router logits of small batches (T <= kSmallRouterT) on CUDA cores: warp w
-// owns expert w % E and the kTokWarp tokens kTokWarp (w / E), ...  Lane l owns
-// the 8-element chunks l, l + 32, ... of H.  For each block of kChunks chunks
-// the lane loads the expert's weights and the tokens' inputs all at once (one
-// memory round trip), and adds each token's products into its f32 sum by fused
-// multiply-adds in index order.  The warp adds its 32 lane sums by a
-// butterfly, and lane 0 adds the bias and stores the logits.  At these sizes
+// owns expert w % E and the kTokWarp tokens kTokWarp (w / E), ... (small_logits);
+// lane 0 adds the bias and stores the logits.  At these sizes
 // the tensor-core GEMM is a latency chain (a 128-row token tile, a K split
 // whose partial sums the selection adds back); here the E x T/kTokWarp warps
 // each wait for one round trip per 2048 elements of H, the router weights come
 // from L2 after their first read, and x stays in L2.
 constexpr int kSmallRouterT = 64;
 constexpr int kLogitWarps = 8;
-constexpr int kChunks = 8;     // 16-byte chunks per lane and block: 2048 of H
-constexpr int kTokWarp = 2;    // tokens per warp
 
 __global__ void __launch_bounds__(kLogitWarps * 32)
 router_logits_small(const uint16_t* __restrict__ x, const uint16_t* __restrict__ wr,
@@ -102,50 +89,13 @@ router_logits_small(const uint16_t* __restrict__ x, const uint16_t* __restrict__
   const int nt = min(kTokWarp, T - t0);
   const uint16_t* wrow = wr + static_cast<size_t>(e) * H;
   float sum[kTokWarp];
-#pragma unroll
-  for (int u = 0; u < kTokWarp; ++u) sum[u] = 0.0f;
-  for (int hb = 0; hb < H; hb += 256 * kChunks) {
-    uint4 w4[kChunks];
-    uint4 x4[kTokWarp][kChunks];
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int h = hb + 256 * c + 8 * lane;
-      w4[c] = h < H ? __ldg(reinterpret_cast<const uint4*>(wrow + h)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int u = 0; u < kTokWarp; ++u)
-        x4[u][c] = (h < H && u < nt)
-                       ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(t0 + u) * H + h))
-                       : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int u = 0; u < kTokWarp; ++u)
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const uint32_t xw[4] = {x4[u][c].x, x4[u][c].y, x4[u][c].z, x4[u][c].w};
-        const uint32_t ww[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          sum[u] = __fmaf_rn(__uint_as_float(xw[q] << 16), __uint_as_float(ww[q] << 16), sum[u]);
-          sum[u] = __fmaf_rn(__uint_as_float(xw[q] & 0xFFFF0000u),
-                             __uint_as_float(ww[q] & 0xFFFF0000u), sum[u]);
-        }
-      }
-  }
+  route::small_logits(x, wrow, H, t0, nt, lane, sum);
   const float b = bias ? __ldg(bias + e) : 0.0f;
 #pragma unroll
   for (int u = 0; u < kTokWarp; ++u) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
     if (lane == 0 && u < nt)
       logits[static_cast<size_t>(t0 + u) * E + e] = bias ? __fadd_rn(sum[u], b) : sum[u];
   }
-}
-
-// Does key a (expert ia) rank above key b (expert ib): larger first, ties to
-// the lower index, NaN last (the order of rank_key).
-__device__ __forceinline__ bool ranks_above(float a, int ia, float b, int ib) {
-  const uint32_t ka = rank_key(a), kb = rank_key(b);
-  return ka > kb || (ka == kb && ia < ib);
 }
 
 // The warp's top-K of one token for the plain router (at most 8 entries a lane):
