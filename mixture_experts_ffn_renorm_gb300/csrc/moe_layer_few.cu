@@ -15,16 +15,23 @@
 //   down      a CTA owns H / CTAs output columns for all experts: it sums routed_scale w y
 //             over a token's experts in shared memory, so no partial sums cross CTAs
 //
-// The barrier between gate/up and down costs no bandwidth: the producer thread runs ahead of it
-// and fills the ring with the down rows, which do not depend on it.
+// The barrier between gate/up and down costs no bandwidth: the copies run ahead of it, since
+// the down rows do not depend on it.
 //
-// A chunk of the ring holds whole weight rows.  A consumer group of eight warps takes every
-// second chunk; a warp takes 8 rows x 256 columns (a lane 8 columns), keeps the tokens' 8
-// columns in registers, and sums 8 rows x up to 4 tokens over its lanes by a transposing
-// butterfly; the segments of a row are then added in order through shared memory.  All sums
-// are f32 in a fixed order, nothing between the weights and the output is narrowed, and no
-// atomics touch data.  CUDA cores suffice: a touched expert has 1.5 tokens on average at T = 16,
+// Every warp is a stream of its own: three 4 KB slots that its lanes refill as soon as they have
+// read them, so 192 KB an SM are in flight and no warp waits for another.  A slot holds up to 2 KB of two
+// rows: a feature's gate and up row, or two output columns' rows of an expert.  A lane takes 8
+// columns of each 256; bf16 weights meet bf16 tokens in the multiply-add that widens (exact
+// products, f32 sums), FP8 weights and the f32 activations are widened first.  After the last
+// piece of a row the sums of two rows x up to 16 tokens are joined over the lanes by a
+// transposing butterfly.  A down row's sums are added to its tokens' outputs in expert order by the one
+// warp that owns it, experts of even and of odd place apart (two rows share an activation's load).
+// All sums are f32 in a fixed order, nothing between the weights and the output is narrowed, and
+// no atomics touch data.  CUDA cores suffice: a touched expert has 1.5 tokens on average at T = 16,
 // and with f32 activations a tensor-core product would need them split into bf16 parts.
+//
+// Chunks shared by eight warps, with a group barrier after each, took 80 us for one token (2048 x 768,
+// 128 experts, 8 of them chosen): 13000 cycles a chunk of index arithmetic and barriers.
 #include <atomic>
 
 #include "fp8_common.cuh"
@@ -34,20 +41,18 @@ namespace moe {
 namespace few {
 namespace {
 
-constexpr int kMaxT = 16;          // tokens: one warp of a group per token in the choice
-constexpr int kMaxDim = 8192;      // H, I, I_shared: a gate and an up row fit a ring slot
+constexpr int kMaxT = 16;          // tokens: one warp per token in the choice
+constexpr int kMaxDim = 8192;      // H, I, I_shared
 constexpr int kMaxE = 1024;
 constexpr int kMaxPairs = kMaxT * 32;
-constexpr int kGroupWarps = 8;     // warps of a consumer group
-constexpr int kConsumers = 2 * 32 * kGroupWarps;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kSeg = 256;          // columns of a segment: 8 per lane
-constexpr int kMaxSlots = 16;
-constexpr int kItems = 32;         // items (8 rows x a segment) of a chunk, at most
-constexpr int kMaxRows = 64;       // rows of a chunk, at most
-constexpr int kBarAll = 1, kBarGroup = 2;   // named barriers: both groups; one group (+ its index)
-
-static_assert(kMaxDim / kSeg == kItems, "eight rows of any width are a chunk");
+constexpr int kSlots = 3;          // per warp
+constexpr int kPiece = 2048;       // bytes of a row in a slot, at most
+constexpr int kSlotBytes = 2 * kPiece;
+constexpr unsigned long long kCopyGraceNs = 100000ull;
+constexpr int kRing = kWarps * kSlots * kSlotBytes;
 
 struct Params {
   const uint16_t* x;
@@ -73,7 +78,7 @@ struct Params {
   float* gate;                     // [T]
   float* act;                      // [T K, I]
   float* act_s;                    // [T, Is]
-  int slot_bytes, n_slots, rows_max;
+  int rows_max;                    // output columns of a CTA, at most
   unsigned long long wait_ns;
   unsigned int* status;
   unsigned long long* launches;
@@ -82,8 +87,7 @@ struct Params {
 // Shared memory: the fixed part, then the output sums, then the ring (which first holds the
 // choice's scores)
 struct alignas(16) Fixed {
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
-  float red[2][2][kItems * 8 * 4]; // [group][buffer][item][row of 8][token of 4]
+  uint64_t full[kWarps][kSlots];
   float weight[kMaxPairs];         // routing weight of a pair, times routed_scale
   float gate[kMaxT];               // sigmoid of the shared expert's gate
   uint32_t mask[kMaxE];            // tokens that chose an expert
@@ -291,120 +295,139 @@ __device__ void group_experts(const Params& p, Fixed& f, int lane) {
   }
 }
 
-// One consumer group's or the producer's walk over a phase's chunks, in the same order
-struct Chunk {
-  int d;          // touched expert, or D: the shared expert
-  int n0, cnt;    // first feature (gate/up) or output column (down), and how many
+// The pieces of a warp's stream, in order: its features of gate/up, then its rows of down.  Two
+// cursors walk it, the copies' ahead of the sums'.
+struct Cursor {
+  int phase;      // 0 gate/up, 1 down, 2 end
+  int i;          // gate/up: feature among the CTA's; down: first of the two rows among the CTA's
+  int d, n;       // touched expert (D: the shared one); feature of the expert
+  int k;          // column of the piece
 };
 
-// rows of `bytes` that a chunk takes, at most: what a slot holds, in at most kItems items
-__device__ __forceinline__ int chunk_rows(const Params& p, int bytes, int cols) {
-  const int nseg = (cols + kSeg - 1) / kSeg;       // at most kMaxDim / kSeg = kItems
-  return min(min(p.slot_bytes / bytes, kMaxRows), kItems / nseg * 8);
-}
-
 template <bool kFp8>
-struct GateUpWalk {
-  int d, n, left, sh, sh_end, D, I, per, per_s;
-  __device__ GateUpWalk(const Params& p, const Fixed& f) {
+struct Stream {
+  const Params& p;
+  const Fixed& f;
+  int D, warp, lane;
+  long long f0;                    // the CTA's first feature among the routed ones in one line
+  int nr, ns, s0;                  // its routed and shared features, the first shared one
+  int col0, cols;                  // its output columns
+
+  __device__ Stream(const Params& p_, const Fixed& f_, int warp_, int lane_) : p(p_), f(f_), warp(warp_), lane(lane_) {
+    D = f.n_groups;
     // all features in one line, a shared expert's bf16 feature beside FP8 ones counted twice
     constexpr int kCost = kFp8 ? 2 : 1;
-    D = f.n_groups;
-    I = p.I;
-    const long long routed = static_cast<long long>(D) * I, all = routed + kCost * p.Is;
-    const long long f0 = all * blockIdx.x / gridDim.x, f1 = all * (blockIdx.x + 1) / gridDim.x;
-    const long long r0 = f0 < routed ? f0 : routed, r1 = f1 < routed ? f1 : routed;
-    d = static_cast<int>(r0 / I);
-    n = static_cast<int>(r0 - static_cast<long long>(d) * I);
-    left = static_cast<int>(r1 - r0);
-    sh = static_cast<int>(((f0 > routed ? f0 - routed : 0) + kCost - 1) / kCost);
-    sh_end = static_cast<int>(((f1 > routed ? f1 - routed : 0) + kCost - 1) / kCost);
-    per_s = max(1, chunk_rows(p, 2 * p.H, p.H) / 2);
-    per = kFp8 ? max(1, chunk_rows(p, p.H, p.H) / 2) : per_s;
+    const long long routed = static_cast<long long>(D) * p.I, all = routed + kCost * p.Is;
+    const long long a = all * blockIdx.x / gridDim.x, b = all * (blockIdx.x + 1) / gridDim.x;
+    f0 = a < routed ? a : routed;
+    nr = static_cast<int>((b < routed ? b : routed) - f0);
+    s0 = static_cast<int>(((a > routed ? a - routed : 0) + kCost - 1) / kCost);
+    ns = static_cast<int>(((b > routed ? b - routed : 0) + kCost - 1) / kCost) - s0;
+    col0 = static_cast<int>(static_cast<long long>(p.H) * blockIdx.x / gridDim.x);
+    cols = static_cast<int>(static_cast<long long>(p.H) * (blockIdx.x + 1) / gridDim.x) - col0;
   }
-  __device__ bool next(Chunk& c) {
-    if (left > 0) {
-      c.d = d;
-      c.n0 = n;
-      c.cnt = min(per, min(I - n, left));
-      left -= c.cnt;
-      n += c.cnt;
-      if (n == I) {
-        n = 0;
-        ++d;
+  __device__ bool quant(int d) const { return kFp8 && d < D; }
+  __device__ int inner(int d) const { return d < D ? p.I : p.Is; }
+  // columns of a row, and of a piece of it
+  __device__ int row_cols(const Cursor& c) const { return c.phase == 0 ? p.H : inner(c.d); }
+  __device__ int piece_cols(int d) const { return quant(d) ? kPiece : kPiece / 2; }
+
+  __device__ void feature(Cursor& c) const {
+    if (c.i < nr) {
+      const unsigned at = static_cast<unsigned>(f0 + c.i);      // below 512 * 8192
+      c.d = static_cast<int>(at / static_cast<unsigned>(p.I));
+      c.n = static_cast<int>(at - static_cast<unsigned>(c.d) * static_cast<unsigned>(p.I));
+    } else if (c.i < nr + ns) {
+      c.d = D;
+      c.n = s0 + c.i - nr;
+    } else {                       // down: experts of this half of the warps, two rows a warp
+      c.phase = 1;
+      c.d = warp >> 3;
+      c.i = 2 * (warp & 7);
+      if (c.i >= cols || c.d >= groups()) c.phase = 2;
+    }
+  }
+  __device__ int groups() const { return D + (p.Is > 0 ? 1 : 0); }
+  __device__ Cursor begin() const {
+    Cursor c{0, warp, 0, 0, 0};
+    feature(c);
+    return c;
+  }
+  // the next feature or pair of rows
+  __device__ void next_item(Cursor& c) const {
+    c.k = 0;
+    if (c.phase == 0) {
+      c.i += kWarps;
+      feature(c);
+    } else {
+      c.i += kWarps;               // eight warps, two rows each
+      if (c.i >= cols) {
+        c.i = 2 * (warp & 7);
+        c.d += 2;
+        if (c.d >= groups()) c.phase = 2;
       }
-      return true;
     }
-    if (sh >= sh_end) return false;
-    c.d = D;
-    c.n0 = sh;
-    c.cnt = min(per_s, sh_end - sh);
-    sh += c.cnt;
-    return true;
+  }
+  __device__ void next_piece(Cursor& c) const {
+    c.k += piece_cols(c.d);
+    if (c.k >= row_cols(c)) next_item(c);
+  }
+  // the copies of a piece: lanes 0 and 1 a row each
+  __device__ void issue(const Cursor& c, uint32_t slot, uint32_t bar) const {
+    if (c.phase == 2) return;
+    const bool q = quant(c.d);
+    const int C = row_cols(c), I = inner(c.d);
+    const uint32_t bytes = static_cast<uint32_t>(min(piece_cols(c.d), C - c.k)) * (q ? 1 : 2);
+    const int rows = c.phase == 0 || c.i + 1 < cols ? 2 : 1;
+    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes * rows);
+    if (lane < rows) {
+      const size_t row_bytes = static_cast<size_t>(C) * (q ? 1 : 2);
+      const uint8_t* w;
+      size_t row;
+      if (c.phase == 0) {
+        w = static_cast<const uint8_t*>(c.d < D ? p.w13 : p.w13s);
+        row = (c.d < D ? static_cast<size_t>(f.expert[c.d]) * 2 * I : 0) + c.n + (lane ? I : 0);
+      } else {
+        w = static_cast<const uint8_t*>(c.d < D ? p.w2 : p.w2s);
+        row = (c.d < D ? static_cast<size_t>(f.expert[c.d]) * p.H : 0) + col0 + c.i + lane;
+      }
+      bulk_load(slot + lane * kPiece, w + row * row_bytes + static_cast<size_t>(c.k) * (q ? 1 : 2), bytes, bar);
+    }
   }
 };
 
-template <bool kFp8>
-struct DownWalk {
-  int d, n, r0, r1, groups, D, per, per_s;
-  // first output column of a CTA
-  static __device__ int column(int H, unsigned cta) {
-    return static_cast<int>(static_cast<long long>(H) * cta / gridDim.x);
-  }
-  __device__ DownWalk(const Params& p, const Fixed& f) {
-    r0 = column(p.H, blockIdx.x);
-    r1 = column(p.H, blockIdx.x + 1);
-    D = f.n_groups;
-    groups = r1 > r0 ? D + (p.Is > 0 ? 1 : 0) : 0;
-    d = 0;
-    n = r0;
-    // even parts of the CTA's columns
-    auto even = [&](int cap) {
-      const int parts = (r1 - r0 + cap - 1) / cap;
-      return parts > 0 ? (r1 - r0 + parts - 1) / parts : 1;
-    };
-    per = even(chunk_rows(p, (kFp8 ? 1 : 2) * p.I, p.I));
-    per_s = p.Is > 0 ? even(chunk_rows(p, 2 * p.Is, p.Is)) : 1;
-  }
-  __device__ bool next(Chunk& c) {
-    if (d >= groups) return false;
-    c.d = d;
-    c.n0 = n;
-    c.cnt = min(d == D ? per_s : per, r1 - n);
-    n += c.cnt;
-    if (n == r1) {
-      n = r0;
-      ++d;
-    }
-    return true;
-  }
-};
+// two exact bf16 products added to an f32 sum, low halves first
+__device__ __forceinline__ float fma_bf16x2(uint32_t a, uint32_t b, float c) {
+  float d;
+  asm("{\n\t.reg .b16 al, ah, bl, bh;\n\t.reg .f32 t;\n\t"
+      "mov.b32 {al, ah}, %1;\n\tmov.b32 {bl, bh}, %2;\n\t"
+      "fma.rn.f32.bf16 t, al, bl, %3;\n\tfma.rn.f32.bf16 %0, ah, bh, t;\n\t}"
+      : "=f"(d) : "r"(a), "r"(b), "f"(c));
+  return d;
+}
 
-// 8 weights of a row at shared address a, as f32
-template <bool kFp8>
-__device__ __forceinline__ void load8(uint32_t a, float (&w)[8]) {
-  if (kFp8) {
-    uint32_t u[2];
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "r"(a) : "memory");
+__device__ __forceinline__ void widen_bf16(const uint4& u, float (&w)[8]) {
+  const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
-          static_cast<__nv_fp8x2_storage_t>(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3));
-      w[2 * i] = __low2float(h);
-      w[2 * i + 1] = __high2float(h);
-    }
-  } else {
-    const uint4 u = ptx::ld_shared_v4(a);
-    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[2 * i] = __uint_as_float(q[i] << 16);
-      w[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
-    }
+  for (int i = 0; i < 4; ++i) {
+    w[2 * i] = __uint_as_float(q[i] << 16);
+    w[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
   }
 }
 
-// Sums v[n] over the warp's lanes, n = 8 NT a power of two up to 32: lane l ends with the sum
+__device__ __forceinline__ void load_e4m3(uint32_t a, float (&w)[8]) {
+  uint32_t u[2];
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "r"(a) : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3));
+    w[2 * i] = __low2float(h);
+    w[2 * i + 1] = __high2float(h);
+  }
+}
+
+// Sums v[n] over the warp's lanes, n a power of two up to 32: lane l ends with the sum
 // of value l * n / 32.  Each step halves the values a lane keeps, so 32 take 31 exchanges.
 template <int kN>
 __device__ __forceinline__ float transpose_sum(float (&v)[kN], int lane) {
@@ -425,123 +448,136 @@ __device__ __forceinline__ float transpose_sum(float (&v)[kN], int lane) {
   return v[0];
 }
 
-// A group's work on one chunk and NT tokens (n_tok of them live): every warp sums its items of
-// 8 rows x 256 columns into red[(item * 8 + row) * 4 + token], items ordered by row batch, then
-// segment.  kDown: the tokens' rows are f32 activations, else bf16 tokens.
-template <int NT, bool kFp8, bool kDown>
-__device__ __forceinline__ void chunk_sums(const Params& p, const void* const (&src)[NT],
-                                           const float* scale0, const float* scale1, int scale_off0,
-                                           int scale_off1, int half, int rows, int cols,
-                                           uint32_t at, uint32_t full, uint32_t parity, bool first,
-                                           volatile int* abort_flag, int warp, int lane,
-                                           float* red) {
-  const int nseg = (cols + kSeg - 1) / kSeg, items = nseg * ((rows + 7) >> 3);
-  const int row_bytes = cols * (kFp8 ? 1 : 2), nblk = (cols + 127) >> 7;
-  bool waited = !first;
-  for (int it = warp; it < items || !waited; it += kGroupWarps) {
-    const bool live = it < items;
-    const int b = live ? it / nseg : 0, col = (live ? it - b * nseg : nseg) * kSeg + lane * 8;
-    const bool in = live && col < cols;
-    float x[NT][8];
+// A warp's ring
+struct Ring {
+  uint32_t slots, bars;            // shared addresses of slot 0 and its barrier
+  int s;
+  uint32_t phase;
+};
+
+// One item: a feature (kDown false: rows gate and up) or two output columns (kDown) of one
+// expert, for its NT tokens (padded by repeating the last): all pieces of the two rows.  Returns the
+// sum of row r and token t, value 2 t + r, in lane (2 t + r) * 16 / NT.
+template <int NT, bool kQ, bool kDown, bool kFp8>
+__device__ __forceinline__ float item(const Stream<kFp8>& st, Ring& ring, Cursor& c, Cursor& ahead, int n_tok,
+                                      volatile int* abort_flag) {
+  const Params& p = st.p;
+  const Fixed& f = st.f;
+  const int lane = st.lane, C = st.row_cols(c), per = kQ ? kPiece : kPiece / 2;
+  // the tokens' rows (tokens, or f32 activations)
+  const int first = f.first[c.d];
+  const uint8_t* src[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (!in) {
+  for (int t = 0; t < NT; ++t) {
+    const int at = first + min(t, n_tok - 1);
+    if (!kDown) src[t] = reinterpret_cast<const uint8_t*>(p.x + static_cast<size_t>(f.token[at]) * C);
+    else if (c.d < st.D) src[t] = reinterpret_cast<const uint8_t*>(p.act + static_cast<size_t>(f.pair[at]) * C);
+    else src[t] = reinterpret_cast<const uint8_t*>(p.act_s + static_cast<size_t>(f.token[at]) * C);
+  }
+  const float *sc0 = nullptr, *sc1 = nullptr;
+  if (kQ) {
+    const int nblk = (C + 127) >> 7, R = kDown ? p.H : 2 * p.I;
+    const float* base = (kDown ? p.s2 : p.s13) + static_cast<size_t>(f.expert[c.d]) * ((R + 127) >> 7) * nblk;
+    const int r0 = kDown ? st.col0 + c.i : c.n, r1 = kDown ? min(r0 + 1, p.H - 1) : p.I + c.n;
+    sc0 = base + static_cast<size_t>(r0 >> 7) * nblk;
+    sc1 = base + static_cast<size_t>(r1 >> 7) * nblk;
+  }
+  float acc[2 * NT];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[t][i] = 0.0f;
-      } else if (kDown) {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(src[t]) + col);
-        const float4 u = __ldcg(s), w = __ldcg(s + 1);
-        x[t][0] = u.x; x[t][1] = u.y; x[t][2] = u.z; x[t][3] = u.w;
-        x[t][4] = w.x; x[t][5] = w.y; x[t][6] = w.z; x[t][7] = w.w;
+  for (int i = 0; i < 2 * NT; ++i) acc[i] = 0.0f;
+  for (int k = 0; k < C; k += per) {
+    const int n = min(per, C - k);
+    const bool landed = __all_sync(0xffffffffu, wait(ring.bars + 8 * ring.s, ring.phase, abort_flag, p));
+    const uint32_t at = ring.slots + ring.s * kSlotBytes + lane * (kQ ? 8 : 16);
+#pragma unroll(NT <= 2 ? 4 : NT <= 4 ? 2 : 1)
+    for (int c0 = 0; c0 < n; c0 += kSeg) {
+      const int col = c0 + lane * 8;
+      if (col >= n) break;
+      const uint32_t a = at + c0 * (kQ ? 1 : 2);
+      if (!kQ && !kDown) {
+        const uint4 g = ptx::ld_shared_v4(a), u = ptx::ld_shared_v4(a + kPiece);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src[t]) + ((k + col) >> 3));
+          acc[2 * t] = fma_bf16x2(x.x, g.x, acc[2 * t]);
+          acc[2 * t + 1] = fma_bf16x2(x.x, u.x, acc[2 * t + 1]);
+          acc[2 * t] = fma_bf16x2(x.y, g.y, acc[2 * t]);
+          acc[2 * t + 1] = fma_bf16x2(x.y, u.y, acc[2 * t + 1]);
+          acc[2 * t] = fma_bf16x2(x.z, g.z, acc[2 * t]);
+          acc[2 * t + 1] = fma_bf16x2(x.z, u.z, acc[2 * t + 1]);
+          acc[2 * t] = fma_bf16x2(x.w, g.w, acc[2 * t]);
+          acc[2 * t + 1] = fma_bf16x2(x.w, u.w, acc[2 * t + 1]);
+        }
       } else {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src[t]) + col));
-        const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+        float w0[8], w1[8];
+        float d0 = 1.0f, d1 = 1.0f;
+        if (kQ) {
+          load_e4m3(a, w0);
+          load_e4m3(a + kPiece, w1);
+          d0 = __ldg(sc0 + ((k + col) >> 7));
+          d1 = __ldg(sc1 + ((k + col) >> 7));
+        } else {
+          widen_bf16(ptx::ld_shared_v4(a), w0);
+          widen_bf16(ptx::ld_shared_v4(a + kPiece), w1);
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[t][2 * i] = __uint_as_float(q[i] << 16);
-          x[t][2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+        for (int t = 0; t < NT; ++t) {
+          float x[8];
+          if (kDown) {             // written by other SMs before the grid barrier: not the read-only path
+            const float4* q = reinterpret_cast<const float4*>(src[t]) + ((k + col) >> 2);
+            const float4 lo = q[0], hi = q[1];
+            x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+            x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+          } else {
+            widen_bf16(__ldg(reinterpret_cast<const uint4*>(src[t]) + ((k + col) >> 3)), x);
+          }
+          float s0 = kQ ? 0.0f : acc[2 * t], s1 = kQ ? 0.0f : acc[2 * t + 1];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            s0 = fmaf(x[i], w0[i], s0);
+            s1 = fmaf(x[i], w1[i], s1);
+          }
+          acc[2 * t] = kQ ? fmaf(s0, d0, acc[2 * t]) : s0;
+          acc[2 * t + 1] = kQ ? fmaf(s1, d1, acc[2 * t + 1]) : s1;
         }
       }
     }
-    float sc[8];
-    if (kFp8 && in) {
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int row = min(8 * b + r, rows - 1);   // rows [half, 2 half) are up rows
-        const bool up = !kDown && row >= half;
-        const int at_row = up ? scale_off1 + row - half : scale_off0 + row;
-        sc[r] = __ldg((up ? scale1 : scale0) + static_cast<size_t>(at_row >> 7) * nblk + (col >> 7));
-      }
+    __syncwarp();                  // all lanes have read the slot
+    if (landed) st.issue(ahead, ring.slots + ring.s * kSlotBytes, ring.bars + 8 * ring.s);
+    if (ahead.phase < 2) st.next_piece(ahead);
+    if (++ring.s == kSlots) {
+      ring.s = 0;
+      ring.phase ^= 1u;
     }
-    if (!waited) {
-      wait(full, parity, abort_flag, p);
-      waited = true;
-    }
-    if (!live) break;
-    float acc[8 * NT];
-#pragma unroll
-    for (int i = 0; i < 8 * NT; ++i) acc[i] = 0.0f;
-    const uint32_t a = at + static_cast<uint32_t>(8 * b) * row_bytes + col * (kFp8 ? 1 : 2);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      if (8 * b + r >= rows) break;
-      if (!in) continue;
-      float w[8];
-      load8<kFp8>(a + r * row_bytes, w);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float s = x[t][0] * w[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) s = fmaf(x[t][i], w[i], s);
-        acc[r * NT + t] = kFp8 ? s * sc[r] : s;
-      }
-    }
-    const float s = transpose_sum<8 * NT>(acc, lane);
-    constexpr int kRep = 32 / (8 * NT);   // lanes that hold the same sum
-    const int idx = lane / kRep;
-    if (lane % kRep == 0) red[(it * 8 + idx / NT) * 4 + idx % NT] = s;
   }
-}
-
-// value of (row, token) of a chunk: its segments in order
-__device__ __forceinline__ float row_sum(const float* red, int nseg, int row, int t) {
-  const float* q = red + ((row >> 3) * nseg * 8 + (row & 7)) * 4 + t;
-  float s = q[0];
-  for (int i = 1; i < nseg; ++i) s += q[i * 32];
-  return s;
+  return transpose_sum<2 * NT>(acc, lane);
 }
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
 layer_few_kernel(const Params p) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   Fixed& f = *reinterpret_cast<Fixed*>(smem_raw);
   float* out_sum = reinterpret_cast<float*>(smem_raw + sizeof(Fixed));   // [2][T][rows_max]
   const uint32_t ring_off = (sizeof(Fixed) + 2u * p.T * p.rows_max * 4u + 127u) & ~127u;
-  uint8_t* ring = smem_raw + ring_off;
+  uint8_t* slots = smem_raw + ring_off;
   volatile int* abort_flag = &f.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = p.T, H = p.H, E = p.E, K = p.K;
 
   count_launch(p.launches, MOE_KID_LAYER_FEW);
-  if (tid == 0) {
-    for (int s = 0; s < p.n_slots; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&f.full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&f.empty[s]), kGroupWarps);
-    }
-    f.abort_flag = 0;
-    ptx::fence_mbar_init();
-  }
+  if (lane < kSlots) ptx::mbar_init(ptx::smem_u32(&f.full[warp][lane]), 1);
+  if (tid == 0) f.abort_flag = 0;
+  ptx::fence_mbar_init();
   for (int e = tid; e < E; e += kThreads) f.mask[e] = 0u;
   for (int i = tid; i < 2 * T * p.rows_max; i += kThreads) out_sum[i] = 0.0f;
   grid_dep_wait();
   grid_dep_launch();
 
   // ---- logits, and the shared expert's gate logits as one more row
-  if (warp < 2 * kGroupWarps) {
+  {
     const int rows = E + (p.w_gate ? 1 : 0), halves = (T + route::kTokWarp - 1) / route::kTokWarp;
-    for (int task = blockIdx.x + gridDim.x * warp; task < rows * halves;
-         task += gridDim.x * 2 * kGroupWarps) {
+    for (int task = blockIdx.x + gridDim.x * warp; task < rows * halves; task += gridDim.x * kWarps) {
       const int e = task % rows, t0 = task / rows * route::kTokWarp;
       float sum[route::kTokWarp];
       route::small_logits(p.x, e < E ? p.w_router + static_cast<size_t>(e) * H : p.w_gate, H, t0,
@@ -563,11 +599,10 @@ layer_few_kernel(const Params p) {
 
   // ---- choice of experts
   if (warp < T) {
-    float* v = reinterpret_cast<float*>(ring) + static_cast<size_t>(warp) * 2 * E;
+    float* v = reinterpret_cast<float*>(slots) + static_cast<size_t>(warp) * 2 * E;
     choose(p, f, warp, lane, v, v + E);
   }
-  if (warp == 2 * kGroupWarps && lane < T)
-    f.gate[lane] = p.w_gate ? sigmoid_f32(__ldcg(p.gate + lane)) : 1.0f;
+  if (tid < T) f.gate[tid] = p.w_gate ? sigmoid_f32(__ldcg(p.gate + tid)) : 1.0f;
   __syncthreads();
   if (warp == 0) group_experts(p, f, lane);
   __syncthreads();
@@ -584,159 +619,69 @@ layer_few_kernel(const Params p) {
   ptx::fence_proxy_async_smem();   // the scores in the ring, before copies overwrite them
   __syncthreads();
 
-  const int D = f.n_groups;
-  const int col0 = DownWalk<kFp8>::column(H, blockIdx.x);   // this CTA's output columns
-  if (warp == 2 * kGroupWarps) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t issued = 0, phase = 1;
-      // one chunk of `cnt` rows at src (and at src2), of `bytes` each
-      auto put = [&](const uint8_t* src, const uint8_t* src2, uint32_t bytes) {
-        if (!wait(ptx::smem_u32(&f.empty[s]), phase, abort_flag, p)) return false;
-        const uint32_t bar = ptx::smem_u32(&f.full[s]);
-        const uint32_t dst = ptx::smem_u32(ring) + static_cast<uint32_t>(s) * p.slot_bytes;
-        ptx::mbar_arrive_expect_tx(bar, src2 ? 2 * bytes : bytes);
-        bulk_load(dst, src, bytes, bar);
-        if (src2) bulk_load(dst + bytes, src2, bytes, bar);
-        ++issued;
-        if (++s == p.n_slots) {
-          s = 0;
-          phase ^= 1u;
-        }
-        return true;
-      };
-      Chunk c;
-      bool ok = true;
-      for (GateUpWalk<kFp8> walk(p, f); ok && walk.next(c);) {
-        const bool q = kFp8 && c.d < D;          // E4M3 rows
-        const int I = c.d < D ? p.I : p.Is;
-        const size_t row = static_cast<size_t>(H) * (q ? 1 : 2);
-        const uint8_t* w = c.d < D ? static_cast<const uint8_t*>(p.w13) +
-                                         static_cast<size_t>(f.expert[c.d]) * 2 * I * row
-                                   : reinterpret_cast<const uint8_t*>(p.w13s);
-        ok = put(w + c.n0 * row, w + (static_cast<size_t>(I) + c.n0) * row,
-                 static_cast<uint32_t>(c.cnt * row));
-      }
-      for (DownWalk<kFp8> walk(p, f); ok && walk.next(c);) {
-        const bool q = kFp8 && c.d < D;
-        const size_t row = static_cast<size_t>(c.d < D ? p.I : p.Is) * (q ? 1 : 2);
-        const uint8_t* w = c.d < D ? static_cast<const uint8_t*>(p.w2) +
-                                         static_cast<size_t>(f.expert[c.d]) * H * row
-                                   : reinterpret_cast<const uint8_t*>(p.w2s);
-        ok = put(w + c.n0 * row, nullptr, static_cast<uint32_t>(c.cnt * row));
-      }
-      // a CTA that gave up lets its copies land before it ends
-      const uint32_t n = p.n_slots;
-      for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i)
-        gemm::spin_bounded(ptx::smem_u32(&f.full[i % n]), (i / n) & 1u);
-    }
-    return;
+  // ---- the experts
+  const Stream<kFp8> st(p, f, warp, lane);
+  const int D = st.D;
+  Ring ring{ptx::smem_u32(slots) + warp * kSlots * kSlotBytes, ptx::smem_u32(&f.full[warp][0]), 0, 0u};
+  Cursor c = st.begin(), ahead = c;
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    st.issue(ahead, ring.slots + s * kSlotBytes, ring.bars + 8 * s);
+    if (ahead.phase < 2) st.next_piece(ahead);
   }
-
-  // ------------------------------------------------------------ consumers
-  const int group = warp / kGroupWarps, gwarp = warp - group * kGroupWarps;
-  const int gtid = tid - group * 32 * kGroupWarps;
-  int index = 0;                   // of the chunk, over both phases
-  int s = 0;
-  uint32_t phase = 0;
-  int buffer = 0;
-  auto advance = [&]() {
-    ++index;
-    if (++s == p.n_slots) {
-      s = 0;
-      phase ^= 1u;
-    }
-  };
-  // sums of one chunk for up to 4 of its expert's tokens; returns the buffer they are in
-  auto sums = [&](auto down, auto fp8, const Chunk& c, int i0, int nt, bool first) {
-    constexpr bool kDown = decltype(down)::value, kQ = decltype(fp8)::value;
-    const bool shared = c.d == D;
-    const int I = shared ? p.Is : p.I, cols = kDown ? I : H, rows = kDown ? c.cnt : 2 * c.cnt;
-    const uint32_t at = ptx::smem_u32(ring) + static_cast<uint32_t>(s) * p.slot_bytes;
-    const uint32_t full = ptx::smem_u32(&f.full[s]);
-    float* red = f.red[group][buffer];
-    const float *sc0 = nullptr, *sc1 = nullptr;
-    int so0 = 0, so1 = 0;
-    if (kQ) {
-      const int nblk = (cols + 127) >> 7, R = kDown ? H : 2 * I;
-      sc0 = (kDown ? p.s2 : p.s13) + static_cast<size_t>(f.expert[c.d]) * ((R + 127) >> 7) * nblk;
-      sc1 = sc0;
-      so0 = c.n0;
-      so1 = I + c.n0;
-    }
-    const int first_pair = f.first[c.d] + i0;
-    auto src_of = [&](int i) -> const void* {
-      const int at_pair = first_pair + min(i, nt - 1);
-      if (!kDown) return p.x + static_cast<size_t>(f.token[at_pair]) * H;
-      if (shared) return p.act_s + static_cast<size_t>(f.token[at_pair]) * I;
-      return p.act + static_cast<size_t>(f.pair[at_pair]) * I;
-    };
-    if (nt == 1) {
-      const void* const src[1] = {src_of(0)};
-      chunk_sums<1, kQ, kDown>(p, src, sc0, sc1, so0, so1, c.cnt, rows, cols, at, full, phase, first,
-                               abort_flag, gwarp, lane, red);
-    } else if (nt == 2) {
-      const void* const src[2] = {src_of(0), src_of(1)};
-      chunk_sums<2, kQ, kDown>(p, src, sc0, sc1, so0, so1, c.cnt, rows, cols, at, full, phase, first,
-                               abort_flag, gwarp, lane, red);
-    } else {
-      const void* const src[4] = {src_of(0), src_of(1), src_of(2), src_of(3)};
-      chunk_sums<4, kQ, kDown>(p, src, sc0, sc1, so0, so1, c.cnt, rows, cols, at, full, phase, first,
-                               abort_flag, gwarp, lane, red);
-    }
-  };
-  auto chunk = [&](auto down, const Chunk& c) {
+  // an item for tokens [0, n_tok) of its expert; lane (2 t + r) * 16 / NT gets row r, token t
+  auto run = [&](auto down, auto nt, int n_tok) {
     constexpr bool kDown = decltype(down)::value;
-    const bool shared = c.d == D;
-    const int I = shared ? p.Is : p.I, nseg = ((kDown ? I : H) + kSeg - 1) / kSeg;
-    const int n_tok = f.first[c.d + 1] - f.first[c.d];
-    for (int i0 = 0; i0 < n_tok; i0 += 4) {
-      const int nt = min(4, n_tok - i0);
-      if (kFp8 && !shared) sums(down, std::true_type{}, c, i0, nt, i0 == 0);
-      else sums(down, std::false_type{}, c, i0, nt, i0 == 0);
-      if (i0 + 4 >= n_tok) {       // this warp's last read of the slot
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&f.empty[s]));
+    constexpr int NT = decltype(nt)::value;
+    const float v = kFp8 && c.d < D ? item<NT, kFp8, kDown>(st, ring, c, ahead, n_tok, abort_flag)
+                                    : item<NT, false, kDown>(st, ring, c, ahead, n_tok, abort_flag);
+    constexpr int kRep = 16 / NT;            // lanes that hold the same sum
+    const int t = lane / (2 * kRep), r = lane / kRep & 1, pair = f.first[c.d] + t;
+    if (kDown) {
+      if (lane % kRep == 0 && t < n_tok && c.i + r < st.cols) {
+        const int tok = f.token[pair];
+        const float w = c.d < D ? f.weight[f.pair[pair]] : f.gate[tok];
+        float* o = out_sum + ((warp >> 3) * T + tok) * p.rows_max + c.i + r;
+        *o = fmaf(w, v, *o);
       }
-      ptx::bar_sync(kBarGroup + group, 32 * kGroupWarps);
-      const float* red = f.red[group][buffer];
-      buffer ^= 1;                 // the other half is free: its readers have passed this barrier
-      for (int i = gtid; i < c.cnt * nt; i += 32 * kGroupWarps) {
-        const int t = i / c.cnt, r = i - t * c.cnt, pair = f.first[c.d] + i0 + t;
-        if (kDown) {
-          const float y = row_sum(red, nseg, r, t);
-          const int tok = f.token[pair];
-          const float w = shared ? f.gate[tok] : f.weight[f.pair[pair]];
-          float* o = out_sum + (group * T + tok) * p.rows_max + c.n0 + r - col0;
-          *o = fmaf(w, y, *o);
-        } else {
-          const float g = row_sum(red, nseg, r, t), u = row_sum(red, nseg, c.cnt + r, t);
-          const float a = g / (1.0f + __expf(-g)) * u;
-          if (shared) p.act_s[static_cast<size_t>(f.token[pair]) * I + c.n0 + r] = a;
-          else p.act[static_cast<size_t>(f.pair[pair]) * I + c.n0 + r] = a;
-        }
+    } else {
+      const float up = __shfl_down_sync(0xffffffffu, v, kRep);
+      if (lane % (2 * kRep) == 0 && t < n_tok) {
+        const float a = v / (1.0f + __expf(-v)) * up;
+        if (c.d < D) p.act[static_cast<size_t>(f.pair[pair]) * p.I + c.n] = a;
+        else p.act_s[static_cast<size_t>(f.token[pair]) * p.Is + c.n] = a;
       }
     }
   };
-  Chunk c;
-  for (GateUpWalk<kFp8> walk(p, f); walk.next(c); advance())
-    if ((index & 1) == group) chunk(std::false_type{}, c);
-  ptx::bar_sync(kBarAll, kConsumers);
+  auto each = [&](auto down) {
+    const int n_tok = f.first[c.d + 1] - f.first[c.d];
+    if (n_tok == 1) run(down, std::integral_constant<int, 1>{}, n_tok);
+    else if (n_tok == 2) run(down, std::integral_constant<int, 2>{}, n_tok);
+    else if (n_tok <= 4) run(down, std::integral_constant<int, 4>{}, n_tok);
+    else if (n_tok <= 8) run(down, std::integral_constant<int, 8>{}, n_tok);
+    else run(down, std::integral_constant<int, 16>{}, n_tok);
+    st.next_item(c);
+  };
+  while (c.phase == 0) each(std::false_type{});
+  __syncthreads();
   if (tid == 0) grid_barrier(abort_flag, p);
-  ptx::bar_sync(kBarAll, kConsumers);
-  for (DownWalk<kFp8> walk(p, f); walk.next(c); advance())
-    if ((index & 1) == group) chunk(std::true_type{}, c);
-  ptx::bar_sync(kBarAll, kConsumers);
+  __syncthreads();
+  while (c.phase == 1) each(std::true_type{});
+  __syncthreads();
 
-  // ---- both groups' sums, the residual, one rounding
-  const int rows = DownWalk<kFp8>::column(H, blockIdx.x + 1) - col0;
-  for (int i = tid; i < T * rows; i += kConsumers) {
-    const int t = i / rows, r = i - t * rows;
+  // ---- both halves' sums, the residual, one rounding
+  for (int i = tid; i < T * st.cols; i += kThreads) {
+    const int t = i / st.cols, r = i - t * st.cols;
     float v = out_sum[t * p.rows_max + r] + out_sum[(T + t) * p.rows_max + r];
-    const size_t at = static_cast<size_t>(t) * H + col0 + r;
+    const size_t at = static_cast<size_t>(t) * H + st.col0 + r;
     if (p.residual) v += bf16_bits_to_f32(p.residual[at]);
     p.out[at] = f32_to_bf16_bits(v);
+  }
+  // a CTA that gave up lets its copies land before it ends
+  if (*abort_flag) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
+    }
   }
 }
 
@@ -825,25 +770,11 @@ int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   p.act_s = reinterpret_cast<float*>(ws + l.act_s);
   const int ctas = sm_count();
   p.rows_max = (p.H + ctas - 1) / ctas;
-  // a slot holds a feature's gate and up row and a down row
-  int slot = 16384;
-  auto grow = [&](int bytes) { slot = bytes > slot ? bytes : slot; };
-  grow(2 * p.H * (kFp8 ? 1 : 2));
-  grow(p.I * (kFp8 ? 1 : 2));
-  if (p.Is > 0) {
-    grow(4 * p.H);
-    grow(2 * p.Is);
-  }
-  p.slot_bytes = (slot + 127) & ~127;
   const int fixed = (static_cast<int>(sizeof(Fixed)) + 2 * p.T * p.rows_max * 4 + 127) & ~127;
   constexpr int kSmem = 227 * 1024;
-  p.n_slots = (kSmem - fixed) / p.slot_bytes;
-  if (p.n_slots > kMaxSlots) p.n_slots = kMaxSlots;
-  int ring = p.n_slots * p.slot_bytes;
-  if (ring < 2 * p.T * p.E * 4) ring = 2 * p.T * p.E * 4;   // the scores of the choice
-  const int smem = fixed + ring;
-  if (p.n_slots < 2 || smem > kSmem)
-    return set_error(MOE_ERR_CUDA, "%s: %d SMs leave no room for the ring", op, ctas);
+  const int scores = 2 * p.T * p.E * 4;      // of the choice, in the ring
+  const int smem = fixed + (scores > kRing ? scores : kRing);
+  if (smem > kSmem) return set_error(MOE_ERR_CUDA, "%s: %d SMs leave no room for the ring", op, ctas);
   auto kern = layer_few_kernel<kFp8>;
   static std::atomic<int> configured[64] = {};
   int dev = 0;
