@@ -18,20 +18,24 @@
 // The barrier between gate/up and down costs no bandwidth: the copies run ahead of it, since
 // the down rows do not depend on it.
 //
-// Every warp is a stream of its own: three 4 KB slots that its lanes refill as soon as they have
-// read them, so 192 KB an SM are in flight and no warp waits for another.  A slot holds up to 2 KB of two
-// rows: a feature's gate and up row, or two output columns' rows of an expert.  A lane takes 8
-// columns of each 256; bf16 weights meet bf16 tokens in the multiply-add that widens (exact
-// products, f32 sums), FP8 weights and the f32 activations are widened first.  After the last
-// piece of a row the sums of two rows x up to 16 tokens are joined over the lanes by a
-// transposing butterfly.  A down row's sums are added to its tokens' outputs in expert order by the one
-// warp that owns it, experts of even and of odd place apart (two rows share an activation's load).
+// Every warp is a stream of its own: two slots of 8 KB that its lanes refill as soon as they have
+// read them (16 rows of 512 bytes, or 8 of 1 KB: in a loop of copies alone these two shapes reach 7.0
+// TB/s with 8 to 12 warps an SM; rows of 256 bytes reach 5.2), and no warp waits for another.
+// The products are mma.sync: a few tokens leave tcgen05's 128 rows empty, and what counts is
+// instructions per byte of weights.  Weight rows are the M side, tokens the N side; a lane reads 16 bytes of a row
+// and the same 16 bytes' columns of a token, which permutes the columns of a step alike on both sides.
+//   gate/up   4 gate rows and the 4 up rows of the same features, bf16 tokens: exact products,
+//             f32 sums; silu(gate) up times routing weight in f32
+//   down      16 output columns.  The f32 activations are kept as three bf16 parts that add up
+//             to them (8 bits each, rounded to nearest, 24 in all), so their products stay exact too;
+//             a token's sums over its experts never leave the registers.
+// FP8 weights are widened to bf16, exactly, and a block's sums take its scale in f32.
 // All sums are f32 in a fixed order, nothing between the weights and the output is narrowed, and
-// no atomics touch data.  CUDA cores suffice: a touched expert has 1.5 tokens on average at T = 16,
-// and with f32 activations a tensor-core product would need them split into bf16 parts.
+// no atomics touch data.
 //
 // Chunks shared by eight warps, with a group barrier after each, took 80 us for one token (2048 x 768,
-// 128 experts, 8 of them chosen): 13000 cycles a chunk of index arithmetic and barriers.
+// 128 experts, 8 of them chosen): 13000 cycles a chunk of index arithmetic and barriers.  Single
+// warps with multiply-adds took 37 us, and 319 for 16 tokens, where an expert of many tokens held all SMs up.
 #include <atomic>
 
 #include "fp8_common.cuh"
@@ -45,12 +49,15 @@ constexpr int kMaxT = 16;          // tokens: one warp per token in the choice
 constexpr int kMaxDim = 8192;      // H, I, I_shared
 constexpr int kMaxE = 1024;
 constexpr int kMaxPairs = kMaxT * 32;
-constexpr int kWarps = 16;
+constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSeg = 256;          // columns of a segment: 8 per lane
-constexpr int kSlots = 3;          // per warp
-constexpr int kPiece = 2048;       // bytes of a row in a slot, at most
-constexpr int kSlotBytes = 2 * kPiece;
+constexpr int kSlots = 2;          // per warp
+// gate/up: 4 features' gate and up rows, 1 KB of each; down: 16 rows, 512 bytes of each.  Rows lie
+// 64 bytes off a multiple of 128 apart, so two rows x 64 bytes, a quarter-warp's read, meet all banks once.
+constexpr int kFeat = 4;
+constexpr int kGuPiece = 1024, kGuPitch = kGuPiece + 64;
+constexpr int kDnPiece = 512, kDnPitch = kDnPiece + 64;
+constexpr int kSlotBytes = 16 * kDnPitch;
 constexpr unsigned long long kCopyGraceNs = 100000ull;
 constexpr int kRing = kWarps * kSlots * kSlotBytes;
 
@@ -73,31 +80,33 @@ struct Params {
   int32_t* ids;                    // outputs, or null
   float* w;
   uint16_t* out;
-  unsigned int* barrier;           // [0] arrivals, [1] generation
+  unsigned long long* barrier;     // arrivals of all launches
   float* logits;                   // [T, E]
   float* gate;                     // [T]
-  float* act;                      // [T K, I]
-  float* act_s;                    // [T, Is]
-  int rows_max;                    // output columns of a CTA, at most
+  uint16_t* act;                   // [3][T K, I], then [3][T, Is]: parts of the weighted activations
   unsigned long long wait_ns;
   unsigned int* status;
   unsigned long long* launches;
 };
 
-// Shared memory: the fixed part, then the output sums, then the ring (which first holds the
-// choice's scores)
+// Shared memory: the fixed part, then the ring, which first holds the choice's scratch and last
+// the warps' sums
 struct alignas(16) Fixed {
   uint64_t full[kWarps][kSlots];
   float weight[kMaxPairs];         // routing weight of a pair, times routed_scale
   float gate[kMaxT];               // sigmoid of the shared expert's gate
-  uint32_t mask[kMaxE];            // tokens that chose an expert
   uint16_t pair[kMaxPairs + kMaxT];    // pairs by expert; then the shared expert's tokens
   uint16_t token[kMaxPairs + kMaxT];   // their tokens
   int16_t expert[kMaxPairs + 1];   // touched experts, ascending
   int16_t first[kMaxPairs + 3];    // their first pair
-  int16_t slot[kMaxT][32];         // chosen experts of a token, by rank
+  uint16_t tokens[kMaxPairs + 1];  // their tokens, a bit each
   int n_groups;                    // touched experts, without the shared one
   int abort_flag;
+};
+struct Scratch {
+  uint32_t mask[kMaxE];            // tokens that chose an expert, then its first pair above
+  int16_t slot[kMaxT][32];         // chosen experts of a token, by rank
+  float scores[1];                 // [T][2 E]
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -125,33 +134,30 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
   }
 }
 
-// One thread's part of the grid barrier: the last CTA to arrive resets the count and starts the
-// next generation.  Every CTA arrives exactly once per barrier, also one that has given up.
-__device__ __forceinline__ void grid_barrier(volatile int* abort_flag, const Params& p) {
-  const uint32_t gen = *reinterpret_cast<volatile uint32_t*>(p.barrier + 1);
-  __threadfence();
-  if (atomicAdd(p.barrier, 1u) == gridDim.x - 1) {
-    atomicSub(p.barrier, gridDim.x);   // not a store: a CTA that gave up may arrive again at any time
-    __threadfence();
-    ptx::st_release_gpu_u32(p.barrier + 1, gen + 1u);
-    return;
-  }
+// The grid barrier counts arrivals and is never reset: `target` is the count that this CTA's arrival
+// belongs to, a multiple of the CTAs.  One thread's part: its release covers the CTA's writes, which
+// it has seen through the block barrier before it, its acquire those of all others.
+__device__ __forceinline__ void grid_barrier(unsigned long long target, volatile int* abort_flag, const Params& p) {
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");
+  asm volatile("red.relaxed.gpu.global.add.u64 [%0], 1;" ::"l"(p.barrier) : "memory");
   const uint64_t t0 = ptx::globaltimer_ns();
-  while (ptx::ld_acquire_gpu_u32(p.barrier + 1) == gen) {
-    if (*abort_flag) return;
+  while (true) {
+    unsigned long long n;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(n) : "l"(p.barrier) : "memory");
+    if (n >= target) return;
     if (ptx::globaltimer_ns() - t0 > p.wait_ns) {
       if (p.status) atomicOr(p.status, static_cast<unsigned int>(MOE_STATUS_TIMEOUT));
       *abort_flag = 1;
       return;
     }
   }
-  __threadfence();
 }
 
 // The pairs of a token: one warp picks the K experts in the router's order and forms their
-// weights with the router's arithmetic.  v and key: E values of shared memory each.
-__device__ void choose(const Params& p, Fixed& f, int t, int lane, float* v, float* key) {
+// weights with the router's arithmetic.
+__device__ void choose(const Params& p, Fixed& f, Scratch& x, int t, int lane) {
   const int E = p.E, K = p.K;
+  float *v = x.scores + static_cast<size_t>(t) * 2 * E, *key = v + E;
   for (int e = lane; e < E; e += 32) {
     const float l = __ldcg(p.logits + static_cast<size_t>(t) * E + e);
     const float s = p.scoring ? sigmoid_f32(l) : l;
@@ -255,9 +261,9 @@ __device__ void choose(const Params& p, Fixed& f, int t, int lane, float* v, flo
   }
   if (lane < K) {
     const float w = p.scoring && !p.renormalize ? num : __fdiv_rn(num, den);
-    f.slot[t][lane] = static_cast<int16_t>(id);
+    x.slot[t][lane] = static_cast<int16_t>(id);
     f.weight[t * K + lane] = __fmul_rn(w, p.routed_scale);
-    atomicOr(&f.mask[id], 1u << t);
+    atomicOr(&x.mask[id], 1u << t);
     if (blockIdx.x == 0) {
       if (p.ids) p.ids[t * K + lane] = id;
       if (p.w) p.w[t * K + lane] = w;
@@ -267,11 +273,11 @@ __device__ void choose(const Params& p, Fixed& f, int t, int lane, float* v, flo
 
 // Touched experts in ascending order with their pairs (tokens ascending), then the shared
 // expert's tokens.  One warp scans the experts; then a thread per pair places it.
-__device__ void group_experts(const Params& p, Fixed& f, int lane) {
+__device__ void group_experts(const Params& p, Fixed& f, Scratch& x, int lane) {
   const int per = (p.E + 31) / 32, lo = min(p.E, lane * per), hi = min(p.E, lo + per);
   int n = 0;                       // touched experts, and their pairs in the upper half
   for (int e = lo; e < hi; ++e)
-    if (f.mask[e]) n += 1 + (__popc(f.mask[e]) << 16);
+    if (x.mask[e]) n += 1 + (__popc(x.mask[e]) << 16);
   int incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -280,11 +286,12 @@ __device__ void group_experts(const Params& p, Fixed& f, int lane) {
   }
   int run = incl - n;
   for (int e = lo; e < hi; ++e) {
-    const uint32_t m = f.mask[e];
+    const uint32_t m = x.mask[e];
     if (!m) continue;
     f.expert[run & 0xFFFF] = static_cast<int16_t>(e);
     f.first[run & 0xFFFF] = static_cast<int16_t>(run >> 16);
-    f.mask[e] = m | (static_cast<uint32_t>(run >> 16) << 16);   // tokens below, first pair above
+    f.tokens[run & 0xFFFF] = static_cast<uint16_t>(m);
+    x.mask[e] = m | (static_cast<uint32_t>(run >> 16) << 16);
     run += 1 + (__popc(m) << 16);
   }
   if (lane == 31) {
@@ -292,15 +299,16 @@ __device__ void group_experts(const Params& p, Fixed& f, int lane) {
     f.n_groups = D;
     f.first[D] = static_cast<int16_t>(P);
     f.first[D + 1] = static_cast<int16_t>(P + p.T);
+    f.tokens[D] = static_cast<uint16_t>((1u << p.T) - 1u);   // the shared expert's
   }
 }
 
-// The pieces of a warp's stream, in order: its features of gate/up, then its rows of down.  Two
-// cursors walk it, the copies' ahead of the sums'.
+// The pieces of a warp's stream, in order: its blocks of features of gate/up, piece by piece, then
+// its (expert, piece) units of down.  Two cursors walk it, the copies' ahead of the sums'.
 struct Cursor {
   int phase;      // 0 gate/up, 1 down, 2 end
-  int i;          // gate/up: feature among the CTA's; down: first of the two rows among the CTA's
-  int d, n;       // touched expert (D: the shared one); feature of the expert
+  int i;          // gate/up: block among the CTA's; down: unit among the row block's
+  int d, n, cnt;  // touched expert (D: the shared one); gate/up: its features [n, n + cnt)
   int k;          // column of the piece
 };
 
@@ -309,143 +317,151 @@ struct Stream {
   const Params& p;
   const Fixed& f;
   int D, warp, lane;
-  long long f0;                    // the CTA's first feature among the routed ones in one line
-  int nr, ns, s0;                  // its routed and shared features, the first shared one
-  int col0, cols;                  // its output columns
+  // gate/up: the CTA's features, all touched experts' in one line: [.., n0 blocks of the first expert,
+  // whole experts, ..], `routed` blocks in all, then the shared expert's from s0
+  int d0, i0, n0, end_d, end_n, routed, s0, s_end, blocks;
+  // down: output columns [col0, col0 + cols) of the CTA, [row0, row0 + rows) of this warp's row block
+  int col0, cols, row_blocks, row0, rows, unit0, unit_step, pieces, units;
 
   __device__ Stream(const Params& p_, const Fixed& f_, int warp_, int lane_) : p(p_), f(f_), warp(warp_), lane(lane_) {
     D = f.n_groups;
-    // all features in one line, a shared expert's bf16 feature beside FP8 ones counted twice
-    constexpr int kCost = kFp8 ? 2 : 1;
-    const long long routed = static_cast<long long>(D) * p.I, all = routed + kCost * p.Is;
-    const long long a = all * blockIdx.x / gridDim.x, b = all * (blockIdx.x + 1) / gridDim.x;
-    f0 = a < routed ? a : routed;
-    nr = static_cast<int>((b < routed ? b : routed) - f0);
-    s0 = static_cast<int>(((a > routed ? a - routed : 0) + kCost - 1) / kCost);
-    ns = static_cast<int>(((b > routed ? b - routed : 0) + kCost - 1) / kCost) - s0;
+    // a shared expert's bf16 feature beside FP8 ones counts twice
+    constexpr unsigned kCost = kFp8 ? 2 : 1;
+    const unsigned I = p.I, line = static_cast<unsigned>(D) * I;           // at most 512 * 8192
+    const unsigned long long all = line + kCost * p.Is;
+    const unsigned a = static_cast<unsigned>(all * blockIdx.x / gridDim.x);
+    const unsigned b = static_cast<unsigned>(all * (blockIdx.x + 1) / gridDim.x);
+    const unsigned ra = min(a, line), rb = min(b, line);
+    d0 = static_cast<int>(ra / I);
+    i0 = static_cast<int>(ra - d0 * I);
+    end_d = static_cast<int>(rb / I);
+    end_n = static_cast<int>(rb - end_d * I);
+    const int per = static_cast<int>(I) / kFeat;                           // I % 8 == 0
+    if (end_d == d0) {
+      n0 = routed = (end_n - i0 + kFeat - 1) / kFeat;
+    } else {
+      n0 = (static_cast<int>(I) - i0 + kFeat - 1) / kFeat;
+      routed = n0 + (end_d - d0 - 1) * per + (end_n + kFeat - 1) / kFeat;
+    }
+    s0 = static_cast<int>((a - ra + kCost - 1) / kCost);
+    s_end = static_cast<int>((b - rb + kCost - 1) / kCost);
+    blocks = routed + (s_end - s0 + kFeat - 1) / kFeat;
     col0 = static_cast<int>(static_cast<long long>(p.H) * blockIdx.x / gridDim.x);
     cols = static_cast<int>(static_cast<long long>(p.H) * (blockIdx.x + 1) / gridDim.x) - col0;
+    // even blocks of at most 16 rows; the warps take blocks in turn, and share a block's units
+    row_blocks = (cols + 15) >> 4;
+    const int rb_i = row_blocks ? warp % row_blocks : 0;
+    row0 = row_blocks ? cols * rb_i / row_blocks : 0;
+    rows = row_blocks ? cols * (rb_i + 1) / row_blocks - row0 : 0;
+    unit0 = row_blocks ? warp / row_blocks : 0;
+    unit_step = row_blocks ? (kWarps - 1 - rb_i) / row_blocks + 1 : 1;
+    const int pc = kDnPiece / (kFp8 ? 1 : 2);
+    pieces = (p.I + pc - 1) / pc;
+    units = rows > 0 ? D * pieces + (p.Is + kDnPiece / 2 - 1) / (kDnPiece / 2) : 0;
   }
   __device__ bool quant(int d) const { return kFp8 && d < D; }
   __device__ int inner(int d) const { return d < D ? p.I : p.Is; }
-  // columns of a row, and of a piece of it
-  __device__ int row_cols(const Cursor& c) const { return c.phase == 0 ? p.H : inner(c.d); }
-  __device__ int piece_cols(int d) const { return quant(d) ? kPiece : kPiece / 2; }
+  __device__ int gu_cols(int d) const { return quant(d) ? kGuPiece : kGuPiece / 2; }
+  __device__ int dn_cols(int d) const { return quant(d) ? kDnPiece : kDnPiece / 2; }
 
-  __device__ void feature(Cursor& c) const {
-    if (c.i < nr) {
-      const unsigned at = static_cast<unsigned>(f0 + c.i);      // below 512 * 8192
-      c.d = static_cast<int>(at / static_cast<unsigned>(p.I));
-      c.n = static_cast<int>(at - static_cast<unsigned>(c.d) * static_cast<unsigned>(p.I));
-    } else if (c.i < nr + ns) {
-      c.d = D;
-      c.n = s0 + c.i - nr;
-    } else {                       // down: experts of this half of the warps, two rows a warp
+  __device__ void locate(Cursor& c) const {
+    if (c.phase == 0) {
+      if (c.i < n0) {
+        c.d = d0;
+        c.n = i0 + kFeat * c.i;
+        c.cnt = min(kFeat, (end_d == d0 ? end_n : p.I) - c.n);
+        return;
+      }
+      if (c.i < routed) {
+        const unsigned per = static_cast<unsigned>(p.I) / kFeat, j = static_cast<unsigned>(c.i - n0);
+        c.d = d0 + 1 + static_cast<int>(j / per);
+        c.n = kFeat * static_cast<int>(j % per);
+        c.cnt = min(kFeat, (c.d == end_d ? end_n : p.I) - c.n);
+        return;
+      }
+      if (c.i < blocks) {
+        c.d = D;
+        c.n = s0 + kFeat * (c.i - routed);
+        c.cnt = min(kFeat, s_end - c.n);
+        return;
+      }
       c.phase = 1;
-      c.d = warp >> 3;
-      c.i = 2 * (warp & 7);
-      if (c.i >= cols || c.d >= groups()) c.phase = 2;
+      c.i = unit0;
+    }
+    if (c.i >= units) {
+      c.phase = 2;
+    } else if (c.i < D * pieces) {
+      c.d = c.i / pieces;
+      c.k = (c.i - c.d * pieces) * dn_cols(0);
+    } else {
+      c.d = D;
+      c.k = (c.i - D * pieces) * (kDnPiece / 2);
     }
   }
-  __device__ int groups() const { return D + (p.Is > 0 ? 1 : 0); }
   __device__ Cursor begin() const {
-    Cursor c{0, warp, 0, 0, 0};
-    feature(c);
+    Cursor c{0, warp, 0, 0, 0, 0};
+    locate(c);
     return c;
   }
-  // the next feature or pair of rows
-  __device__ void next_item(Cursor& c) const {
-    c.k = 0;
+  __device__ void next(Cursor& c) const {
     if (c.phase == 0) {
+      c.k += gu_cols(c.d);
+      if (c.k < p.H) return;
+      c.k = 0;
       c.i += kWarps;
-      feature(c);
     } else {
-      c.i += kWarps;               // eight warps, two rows each
-      if (c.i >= cols) {
-        c.i = 2 * (warp & 7);
-        c.d += 2;
-        if (c.d >= groups()) c.phase = 2;
-      }
+      c.i += unit_step;
     }
+    locate(c);
   }
-  __device__ void next_piece(Cursor& c) const {
-    c.k += piece_cols(c.d);
-    if (c.k >= row_cols(c)) next_item(c);
-  }
-  // the copies of a piece: lanes 0 and 1 a row each
+  // the copies of a piece, a row per lane
   __device__ void issue(const Cursor& c, uint32_t slot, uint32_t bar) const {
     if (c.phase == 2) return;
     const bool q = quant(c.d);
-    const int C = row_cols(c), I = inner(c.d);
-    const uint32_t bytes = static_cast<uint32_t>(min(piece_cols(c.d), C - c.k)) * (q ? 1 : 2);
-    const int rows = c.phase == 0 || c.i + 1 < cols ? 2 : 1;
-    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, bytes * rows);
-    if (lane < rows) {
-      const size_t row_bytes = static_cast<size_t>(C) * (q ? 1 : 2);
-      const uint8_t* w;
-      size_t row;
-      if (c.phase == 0) {
-        w = static_cast<const uint8_t*>(c.d < D ? p.w13 : p.w13s);
-        row = (c.d < D ? static_cast<size_t>(f.expert[c.d]) * 2 * I : 0) + c.n + (lane ? I : 0);
-      } else {
-        w = static_cast<const uint8_t*>(c.d < D ? p.w2 : p.w2s);
-        row = (c.d < D ? static_cast<size_t>(f.expert[c.d]) * p.H : 0) + col0 + c.i + lane;
-      }
-      bulk_load(slot + lane * kPiece, w + row * row_bytes + static_cast<size_t>(c.k) * (q ? 1 : 2), bytes, bar);
+    const int I = inner(c.d), esz = q ? 1 : 2;
+    const uint8_t* w;
+    size_t row;
+    int C, n, dst;
+    bool mine;
+    if (c.phase == 0) {
+      w = static_cast<const uint8_t*>(c.d < D ? p.w13 : p.w13s);
+      row = (c.d < D ? static_cast<size_t>(f.expert[c.d]) * 2 * I : 0) + (lane < kFeat ? 0 : I) + c.n + lane % kFeat;
+      C = p.H;
+      n = min(gu_cols(c.d), C - c.k);
+      dst = lane * kGuPitch;
+      mine = lane < 2 * kFeat && lane % kFeat < c.cnt;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * esz * 2 * c.cnt));
+    } else {
+      w = static_cast<const uint8_t*>(c.d < D ? p.w2 : p.w2s);
+      row = (c.d < D ? static_cast<size_t>(f.expert[c.d]) * p.H : 0) + col0 + row0 + lane;
+      C = I;
+      n = min(dn_cols(c.d), C - c.k);
+      dst = lane * kDnPitch;
+      mine = lane < rows;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * esz * rows));
     }
+    if (mine)
+      bulk_load(slot + dst, w + (row * C + c.k) * esz, static_cast<uint32_t>(n * esz), bar);
   }
 };
 
-// two exact bf16 products added to an f32 sum, low halves first
-__device__ __forceinline__ float fma_bf16x2(uint32_t a, uint32_t b, float c) {
-  float d;
-  asm("{\n\t.reg .b16 al, ah, bl, bh;\n\t.reg .f32 t;\n\t"
-      "mov.b32 {al, ah}, %1;\n\tmov.b32 {bl, bh}, %2;\n\t"
-      "fma.rn.f32.bf16 t, al, bl, %3;\n\tfma.rn.f32.bf16 %0, ah, bh, t;\n\t}"
-      : "=f"(d) : "r"(a), "r"(b), "f"(c));
-  return d;
+// c += A B for 16 rows x 8 tokens x 16 columns, bf16 and f32.  Lane (g, q) = (lane / 4, lane % 4) holds
+// A's rows g and g + 8, B's token g, and of c rows g (0, 1) and g + 8 (2, 3), tokens 2 q and 2 q + 1.
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void widen_bf16(const uint4& u, float (&w)[8]) {
-  const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[2 * i] = __uint_as_float(q[i] << 16);
-    w[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
-  }
-}
-
-__device__ __forceinline__ void load_e4m3(uint32_t a, float (&w)[8]) {
-  uint32_t u[2];
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "r"(a) : "memory");
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3));
-    w[2 * i] = __low2float(h);
-    w[2 * i + 1] = __high2float(h);
-  }
-}
-
-// Sums v[n] over the warp's lanes, n a power of two up to 32: lane l ends with the sum
-// of value l * n / 32.  Each step halves the values a lane keeps, so 32 take 31 exchanges.
-template <int kN>
-__device__ __forceinline__ float transpose_sum(float (&v)[kN], int lane) {
-#pragma unroll
-  for (int o = 16, n = kN; o >= 1; o >>= 1) {
-    if (n > 1) {
-      n >>= 1;
-#pragma unroll
-      for (int i = 0; i < kN / 2; ++i) {
-        if (i >= n) break;
-        const float keep = lane & o ? v[i + n] : v[i], give = lane & o ? v[i] : v[i + n];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-      }
-    } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-    }
-  }
-  return v[0];
+// four E4M3 codes as bf16, exactly
+__device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  const __half2 a = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3));
+  const __half2 b = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3));
+  lo = gemm::pack_bf16x2(__low2float(a), __high2float(a));
+  hi = gemm::pack_bf16x2(__low2float(b), __high2float(b));
 }
 
 // A warp's ring
@@ -455,102 +471,231 @@ struct Ring {
   uint32_t phase;
 };
 
-// One item: a feature (kDown false: rows gate and up) or two output columns (kDown) of one
-// expert, for its NT tokens (padded by repeating the last): all pieces of the two rows.  Returns the
-// sum of row r and token t, value 2 t + r, in lane (2 t + r) * 16 / NT.
-template <int NT, bool kQ, bool kDown, bool kFp8>
-__device__ __forceinline__ float item(const Stream<kFp8>& st, Ring& ring, Cursor& c, Cursor& ahead, int n_tok,
-                                      volatile int* abort_flag) {
+// waits for the current slot; then, once it has been read, refills it and steps on
+template <bool kFp8>
+__device__ __forceinline__ bool take(const Stream<kFp8>& st, const Ring& r, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, wait(r.bars + 8 * r.s, r.phase, abort_flag, st.p));
+}
+template <bool kFp8>
+__device__ __forceinline__ void give(const Stream<kFp8>& st, Ring& r, Cursor& ahead, bool landed) {
+  __syncwarp();                    // all lanes have read the slot
+  if (landed) st.issue(ahead, r.slots + r.s * kSlotBytes, r.bars + 8 * r.s);
+  if (ahead.phase < 2) st.next(ahead);
+  if (++r.s == kSlots) {
+    r.s = 0;
+    r.phase ^= 1u;
+  }
+}
+
+// One block of gate/up: the sums of 4 features' gate and up rows (MMA rows 0-3 and 4-7) over the
+// whole width, for the expert's tokens in NB eights
+template <int NB, bool kQ, bool kFp8>
+__device__ __forceinline__ void gate_up(const Stream<kFp8>& st, Ring& ring, const Cursor& c, Cursor& ahead, int n_tok,
+                                        volatile int* abort_flag, float (&out)[NB][4]) {
   const Params& p = st.p;
   const Fixed& f = st.f;
-  const int lane = st.lane, C = st.row_cols(c), per = kQ ? kPiece : kPiece / 2;
-  // the tokens' rows (tokens, or f32 activations)
+  const int lane = st.lane, g = lane >> 2, q = lane & 3, H = p.H, per = kQ ? kGuPiece : kGuPiece / 2;
   const int first = f.first[c.d];
-  const uint8_t* src[NT];
+  const uint4* x[NB];
+  bool has[NB];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int at = first + min(t, n_tok - 1);
-    if (!kDown) src[t] = reinterpret_cast<const uint8_t*>(p.x + static_cast<size_t>(f.token[at]) * C);
-    else if (c.d < st.D) src[t] = reinterpret_cast<const uint8_t*>(p.act + static_cast<size_t>(f.pair[at]) * C);
-    else src[t] = reinterpret_cast<const uint8_t*>(p.act_s + static_cast<size_t>(f.token[at]) * C);
+  for (int b = 0; b < NB; ++b) {
+    has[b] = 8 * b + g < n_tok;
+    x[b] = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(has[b] ? f.token[first + 8 * b + g] : 0) * H);
   }
-  const float *sc0 = nullptr, *sc1 = nullptr;
+  const float* sc0 = nullptr;      // scales of this lane's row: feature g & 3, gate or up
   if (kQ) {
-    const int nblk = (C + 127) >> 7, R = kDown ? p.H : 2 * p.I;
-    const float* base = (kDown ? p.s2 : p.s13) + static_cast<size_t>(f.expert[c.d]) * ((R + 127) >> 7) * nblk;
-    const int r0 = kDown ? st.col0 + c.i : c.n, r1 = kDown ? min(r0 + 1, p.H - 1) : p.I + c.n;
-    sc0 = base + static_cast<size_t>(r0 >> 7) * nblk;
-    sc1 = base + static_cast<size_t>(r1 >> 7) * nblk;
+    const int nblk = (H + 127) >> 7, row = (g < kFeat ? 0 : p.I) + min(c.n + (g & 3), p.I - 1);
+    sc0 = p.s13 + (static_cast<size_t>(f.expert[c.d]) * ((2 * p.I + 127) >> 7) + (row >> 7)) * nblk;
   }
-  float acc[2 * NT];
+  float acc[NB][2][4];
 #pragma unroll
-  for (int i = 0; i < 2 * NT; ++i) acc[i] = 0.0f;
-  for (int k = 0; k < C; k += per) {
-    const int n = min(per, C - k);
-    const bool landed = __all_sync(0xffffffffu, wait(ring.bars + 8 * ring.s, ring.phase, abort_flag, p));
-    const uint32_t at = ring.slots + ring.s * kSlotBytes + lane * (kQ ? 8 : 16);
-#pragma unroll(NT <= 2 ? 4 : NT <= 4 ? 2 : 1)
-    for (int c0 = 0; c0 < n; c0 += kSeg) {
-      const int col = c0 + lane * 8;
-      if (col >= n) break;
-      const uint32_t a = at + c0 * (kQ ? 1 : 2);
-      if (!kQ && !kDown) {
-        const uint4 g = ptx::ld_shared_v4(a), u = ptx::ld_shared_v4(a + kPiece);
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src[t]) + ((k + col) >> 3));
-          acc[2 * t] = fma_bf16x2(x.x, g.x, acc[2 * t]);
-          acc[2 * t + 1] = fma_bf16x2(x.x, u.x, acc[2 * t + 1]);
-          acc[2 * t] = fma_bf16x2(x.y, g.y, acc[2 * t]);
-          acc[2 * t + 1] = fma_bf16x2(x.y, u.y, acc[2 * t + 1]);
-          acc[2 * t] = fma_bf16x2(x.z, g.z, acc[2 * t]);
-          acc[2 * t + 1] = fma_bf16x2(x.z, u.z, acc[2 * t + 1]);
-          acc[2 * t] = fma_bf16x2(x.w, g.w, acc[2 * t]);
-          acc[2 * t + 1] = fma_bf16x2(x.w, u.w, acc[2 * t + 1]);
-        }
-      } else {
-        float w0[8], w1[8];
-        float d0 = 1.0f, d1 = 1.0f;
+    for (int j = 0; j < 4; ++j) acc[b][0][j] = acc[b][1][j] = out[b][j] = 0.0f;
+  constexpr int kStep = kQ ? 64 : 32;            // columns of a step: 16 bytes of a row per lane
+  for (int k = 0; k < H; k += per) {
+    const int n = min(per, H - k);
+    const uint32_t at = ring.slots + ring.s * kSlotBytes + g * kGuPitch + q * 16;
+    bool landed = false;
+    // 4 steps at a time: their tokens' loads first, for the first ones ahead of the wait
+    for (int k0 = 0; k0 < n; k0 += 4 * kStep) {
+      uint4 b[NB][4][kQ ? 2 : 1];
+      float sc[2];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int h = 0; h < (kQ ? 2 : 1); ++h) {
+            const int col = k0 + s * kStep + (kQ ? 16 : 8) * q + 8 * h;
+            b[i][s][h] = has[i] && col < n ? __ldg(x[i] + ((k + col) >> 3)) : make_uint4(0, 0, 0, 0);
+          }
+      if (kQ) {                                  // 4 steps are two scale blocks
+        sc[0] = __ldg(sc0 + ((k + k0) >> 7));
+        sc[1] = k0 + 128 < n ? __ldg(sc0 + ((k + k0 + 128) >> 7)) : 0.0f;
+      }
+      if (k0 == 0) landed = take(st, ring, abort_flag);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (k0 + s * kStep >= n) break;
+        const bool in = k0 + s * kStep + (kQ ? 16 : 8) * q < n;   // behind the row's end: stale bytes
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (in) w = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2));
         if (kQ) {
-          load_e4m3(a, w0);
-          load_e4m3(a + kPiece, w1);
-          d0 = __ldg(sc0 + ((k + col) >> 7));
-          d1 = __ldg(sc1 + ((k + col) >> 7));
+          const uint32_t code[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t lo, hi;
+            widen4(code[j], lo, hi);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              const uint4& u = b[i][s][kQ ? j >> 1 : 0];
+              mma(acc[i][j & 1], lo, 0u, hi, 0u, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
+            }
+          }
+          if ((s & 1) || k0 + (s + 1) * kStep >= n) {             // the end of a scale block
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                out[i][j] = fmaf(acc[i][0][j] + acc[i][1][j], sc[s >> 1], out[i][j]);
+                acc[i][0][j] = acc[i][1][j] = 0.0f;
+              }
+          }
         } else {
-          widen_bf16(ptx::ld_shared_v4(a), w0);
-          widen_bf16(ptx::ld_shared_v4(a + kPiece), w1);
-        }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float x[8];
-          if (kDown) {             // written by other SMs before the grid barrier: not the read-only path
-            const float4* q = reinterpret_cast<const float4*>(src[t]) + ((k + col) >> 2);
-            const float4 lo = q[0], hi = q[1];
-            x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-            x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
-          } else {
-            widen_bf16(__ldg(reinterpret_cast<const uint4*>(src[t]) + ((k + col) >> 3)), x);
+          for (int i = 0; i < NB; ++i) {
+            mma(acc[i][0], w.x, 0u, w.y, 0u, b[i][s][0].x, b[i][s][0].y);
+            mma(acc[i][1], w.z, 0u, w.w, 0u, b[i][s][0].z, b[i][s][0].w);
           }
-          float s0 = kQ ? 0.0f : acc[2 * t], s1 = kQ ? 0.0f : acc[2 * t + 1];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s0 = fmaf(x[i], w0[i], s0);
-            s1 = fmaf(x[i], w1[i], s1);
-          }
-          acc[2 * t] = kQ ? fmaf(s0, d0, acc[2 * t]) : s0;
-          acc[2 * t + 1] = kQ ? fmaf(s1, d1, acc[2 * t + 1]) : s1;
         }
       }
     }
-    __syncwarp();                  // all lanes have read the slot
-    if (landed) st.issue(ahead, ring.slots + ring.s * kSlotBytes, ring.bars + 8 * ring.s);
-    if (ahead.phase < 2) st.next_piece(ahead);
-    if (++ring.s == kSlots) {
-      ring.s = 0;
-      ring.phase ^= 1u;
+    give(st, ring, ahead, landed);
+  }
+  if (!kQ) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) out[b][j] = acc[b][0][j] + acc[b][1][j];
+  }
+}
+
+// One unit of down: 16 output columns x a piece of one expert's activations, added to the tokens'
+// sums.  Tokens that did not choose the expert take nothing from it, not even a product with zero.
+template <bool kQ, bool kFp8>
+__device__ __forceinline__ void down(const Stream<kFp8>& st, Ring& ring, const Cursor& c, Cursor& ahead,
+                                     volatile int* abort_flag, float (&total)[2][4]) {
+  const Params& p = st.p;
+  const Fixed& f = st.f;
+  const int lane = st.lane, g = lane >> 2, q = lane & 3, I = st.inner(c.d), per = kQ ? kDnPiece : kDnPiece / 2;
+  const int n = min(per, I - c.k);
+  const uint32_t tokens = f.tokens[c.d];
+  const size_t parts = c.d < st.D ? static_cast<size_t>(p.T) * p.K * I : static_cast<size_t>(p.T) * I;
+  const uint16_t* base = p.act + (c.d < st.D ? 0 : 3 * static_cast<size_t>(p.T) * p.K * p.I);
+  const uint32_t at = ring.slots + ring.s * kSlotBytes + g * kDnPitch + q * 16;
+  constexpr int kStep = kQ ? 64 : 32, kHalf = kQ ? 2 : 1, kBatch = kQ ? 2 : 4;   // steps of a batch of loads
+  const float *sc0 = nullptr, *sc1 = nullptr;
+  if (kQ) {
+    const int nblk = (I + 127) >> 7, r = st.col0 + st.row0 + g;
+    const float* s2 = p.s2 + static_cast<size_t>(f.expert[c.d]) * ((p.H + 127) >> 7) * nblk;
+    sc0 = s2 + static_cast<size_t>(min(r, p.H - 1) >> 7) * nblk;
+    sc1 = s2 + static_cast<size_t>(min(r + 8, p.H - 1) >> 7) * nblk;
+  }
+  bool waited = false, landed = false;
+#pragma unroll
+  for (int nb = 0; nb < 2; ++nb) {
+    const uint32_t here = tokens >> (8 * nb) & 0xFFu;
+    if (!here) continue;
+    const int t = 8 * nb + g;
+    const bool has = tokens >> t & 1u;
+    const uint4* a = nullptr;
+    if (has) {
+      const int pair = f.first[c.d] + __popc(tokens & ((1u << t) - 1u));
+      a = reinterpret_cast<const uint4*>(base + static_cast<size_t>(c.d < st.D ? f.pair[pair] : t) * I + c.k);
+    }
+    float acc[4][4], sum[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sum[j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i][j] = 0.0f;
+    }
+    for (int k0 = 0; k0 < n; k0 += kBatch * kStep) {
+      uint4 b[kBatch][3][kHalf];
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s)
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h) {      // written by other SMs before the grid barrier
+            const int col = k0 + s * kStep + 8 * kHalf * q + 8 * h;
+            b[s][part][h] = has && col < n ? a[(part * parts + col) >> 3] : make_uint4(0, 0, 0, 0);
+          }
+      float d0 = 1.0f, d1 = 1.0f;
+      if (kQ) {                                  // a batch is one scale block
+        d0 = __ldg(sc0 + ((c.k + k0) >> 7));
+        d1 = __ldg(sc1 + ((c.k + k0) >> 7));
+      }
+      if (!waited) {
+        landed = take(st, ring, abort_flag);
+        waited = true;
+      }
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        if (k0 + s * kStep >= n) break;
+        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+        if (k0 + s * kStep + 8 * kHalf * q < n) {
+          w0 = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2));
+          w1 = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2) + 8 * kDnPitch);
+        }
+        if (kQ) {
+          const uint32_t c0[4] = {w0.x, w0.y, w0.z, w0.w}, c1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a0, a2, a1, a3;
+            widen4(c0[j], a0, a2);
+            widen4(c1[j], a1, a3);
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+              const uint4& u = b[s][part][kQ ? j >> 1 : 0];
+              mma(acc[(part ? 2 : 0) + (j & 1)], a0, a1, a2, a3, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            const uint4& u = b[s][part][0];
+            mma(acc[part ? 2 : 0], w0.x, w1.x, w0.y, w1.y, u.x, u.y);
+            mma(acc[part ? 3 : 1], w0.z, w1.z, w0.w, w1.w, u.z, u.w);
+          }
+        }
+      }
+      if (kQ) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[j] = fmaf(acc[0][j] + acc[1][j] + (acc[2][j] + acc[3][j]), j < 2 ? d0 : d1, sum[j]);
+          acc[0][j] = acc[1][j] = acc[2][j] = acc[3][j] = 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v = kQ ? sum[j] : acc[0][j] + acc[1][j] + (acc[2][j] + acc[3][j]);
+      if (tokens >> (8 * nb + 2 * q + (j & 1)) & 1u) total[nb][j] += v;
     }
   }
-  return transpose_sum<2 * NT>(acc, lane);
+  give(st, ring, ahead, landed);
+}
+
+// v as three bf16 parts that add up to it (an infinity or NaN as its first part alone)
+__device__ __forceinline__ void cut3(float v, uint16_t (&part)[3]) {
+  part[0] = f32_to_bf16_bits(v);
+  const float r = v - bf16_bits_to_f32(part[0]);
+  const bool fine = fabsf(r) < __int_as_float(0x7f800000);   // false for NaN
+  part[1] = fine ? f32_to_bf16_bits(r) : 0;
+  part[2] = fine ? f32_to_bf16_bits(r - bf16_bits_to_f32(part[1])) : 0;
 }
 
 template <bool kFp8>
@@ -558,9 +703,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 layer_few_kernel(const Params p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Fixed& f = *reinterpret_cast<Fixed*>(smem_raw);
-  float* out_sum = reinterpret_cast<float*>(smem_raw + sizeof(Fixed));   // [2][T][rows_max]
-  const uint32_t ring_off = (sizeof(Fixed) + 2u * p.T * p.rows_max * 4u + 127u) & ~127u;
-  uint8_t* slots = smem_raw + ring_off;
+  constexpr uint32_t kRingAt = (sizeof(Fixed) + 127u) & ~127u;
+  uint8_t* slots = smem_raw + kRingAt;
+  Scratch& x = *reinterpret_cast<Scratch*>(slots);
   volatile int* abort_flag = &f.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = p.T, H = p.H, E = p.E, K = p.K;
@@ -569,10 +714,12 @@ layer_few_kernel(const Params p) {
   if (lane < kSlots) ptx::mbar_init(ptx::smem_u32(&f.full[warp][lane]), 1);
   if (tid == 0) f.abort_flag = 0;
   ptx::fence_mbar_init();
-  for (int e = tid; e < E; e += kThreads) f.mask[e] = 0u;
-  for (int i = tid; i < 2 * T * p.rows_max; i += kThreads) out_sum[i] = 0.0f;
+  for (int e = tid; e < E; e += kThreads) x.mask[e] = 0u;
   grid_dep_wait();
   grid_dep_launch();
+  // the arrivals of earlier launches are a multiple of the CTAs, and before this CTA's own nobody passes
+  unsigned long long arrivals = 0;
+  if (tid == 0) arrivals = (*reinterpret_cast<volatile unsigned long long*>(p.barrier) / gridDim.x + 1) * gridDim.x;
 
   // ---- logits, and the shared expert's gate logits as one more row
   {
@@ -594,85 +741,97 @@ layer_few_kernel(const Params p) {
     }
   }
   __syncthreads();
-  if (tid == 0) grid_barrier(abort_flag, p);
+  if (tid == 0) grid_barrier(arrivals, abort_flag, p);
   __syncthreads();
 
   // ---- choice of experts
-  if (warp < T) {
-    float* v = reinterpret_cast<float*>(slots) + static_cast<size_t>(warp) * 2 * E;
-    choose(p, f, warp, lane, v, v + E);
-  }
+  for (int t = warp; t < T; t += kWarps) choose(p, f, x, t, lane);
   if (tid < T) f.gate[tid] = p.w_gate ? sigmoid_f32(__ldcg(p.gate + tid)) : 1.0f;
   __syncthreads();
-  if (warp == 0) group_experts(p, f, lane);
+  if (warp == 0) group_experts(p, f, x, lane);
   __syncthreads();
   for (int i = tid; i < T * K + T; i += kThreads) {
     const int t = i < T * K ? i / K : i - T * K;
     int at = i;
     if (i < T * K) {
-      const uint32_t m = f.mask[f.slot[t][i - t * K]];
+      const uint32_t m = x.mask[x.slot[t][i - t * K]];
       at = static_cast<int>(m >> 16) + __popc(m & ((1u << t) - 1u));
     }
     f.pair[at] = static_cast<uint16_t>(i);
     f.token[at] = static_cast<uint16_t>(t);
   }
-  ptx::fence_proxy_async_smem();   // the scores in the ring, before copies overwrite them
+  ptx::fence_proxy_async_smem();   // the scratch in the ring, before copies overwrite it
   __syncthreads();
 
   // ---- the experts
   const Stream<kFp8> st(p, f, warp, lane);
-  const int D = st.D;
+  const int D = st.D, g = lane >> 2, q = lane & 3;
   Ring ring{ptx::smem_u32(slots) + warp * kSlots * kSlotBytes, ptx::smem_u32(&f.full[warp][0]), 0, 0u};
   Cursor c = st.begin(), ahead = c;
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) {
     st.issue(ahead, ring.slots + s * kSlotBytes, ring.bars + 8 * s);
-    if (ahead.phase < 2) st.next_piece(ahead);
+    if (ahead.phase < 2) st.next(ahead);
   }
-  // an item for tokens [0, n_tok) of its expert; lane (2 t + r) * 16 / NT gets row r, token t
-  auto run = [&](auto down, auto nt, int n_tok) {
-    constexpr bool kDown = decltype(down)::value;
-    constexpr int NT = decltype(nt)::value;
-    const float v = kFp8 && c.d < D ? item<NT, kFp8, kDown>(st, ring, c, ahead, n_tok, abort_flag)
-                                    : item<NT, false, kDown>(st, ring, c, ahead, n_tok, abort_flag);
-    constexpr int kRep = 16 / NT;            // lanes that hold the same sum
-    const int t = lane / (2 * kRep), r = lane / kRep & 1, pair = f.first[c.d] + t;
-    if (kDown) {
-      if (lane % kRep == 0 && t < n_tok && c.i + r < st.cols) {
-        const int tok = f.token[pair];
-        const float w = c.d < D ? f.weight[f.pair[pair]] : f.gate[tok];
-        float* o = out_sum + ((warp >> 3) * T + tok) * p.rows_max + c.i + r;
-        *o = fmaf(w, v, *o);
-      }
-    } else {
-      const float up = __shfl_down_sync(0xffffffffu, v, kRep);
-      if (lane % (2 * kRep) == 0 && t < n_tok) {
-        const float a = v / (1.0f + __expf(-v)) * up;
-        if (c.d < D) p.act[static_cast<size_t>(f.pair[pair]) * p.I + c.n] = a;
-        else p.act_s[static_cast<size_t>(f.token[pair]) * p.Is + c.n] = a;
-      }
-    }
+  // gate and up of feature c.n + g and token i of the expert, weighted and cut for the down product
+  auto emit = [&](float gate, float up, int n_tok, int i) {
+    if (g >= c.cnt || i >= n_tok) return;        // c.cnt <= 4: rows 0-3
+    const int pair = f.first[c.d] + i, tok = f.token[pair];
+    const bool shared = c.d == D;
+    const int row = shared ? tok : f.pair[pair], I = shared ? p.Is : p.I, rows = shared ? T : T * K;
+    const float a = gate / (1.0f + __expf(-gate)) * up * (shared ? f.gate[tok] : f.weight[row]);
+    uint16_t part[3];
+    cut3(a, part);
+    uint16_t* to = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) + static_cast<size_t>(row) * I + c.n + g;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) to[j * static_cast<size_t>(rows) * I] = part[j];
   };
-  auto each = [&](auto down) {
+  auto block = [&](auto nb, int n_tok) {
+    constexpr int NB = decltype(nb)::value;
+    float v[NB][4];
+    if (kFp8 && c.d < D) gate_up<NB, kFp8>(st, ring, c, ahead, n_tok, abort_flag, v);
+    else gate_up<NB, false>(st, ring, c, ahead, n_tok, abort_flag, v);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float up = __shfl_down_sync(0xffffffffu, v[b][j], 4 * kFeat);
+        emit(v[b][j], up, n_tok, 8 * b + 2 * q + j);
+      }
+  };
+  while (c.phase == 0) {
     const int n_tok = f.first[c.d + 1] - f.first[c.d];
-    if (n_tok == 1) run(down, std::integral_constant<int, 1>{}, n_tok);
-    else if (n_tok == 2) run(down, std::integral_constant<int, 2>{}, n_tok);
-    else if (n_tok <= 4) run(down, std::integral_constant<int, 4>{}, n_tok);
-    else if (n_tok <= 8) run(down, std::integral_constant<int, 8>{}, n_tok);
-    else run(down, std::integral_constant<int, 16>{}, n_tok);
-    st.next_item(c);
-  };
-  while (c.phase == 0) each(std::false_type{});
+    if (n_tok <= 8) block(std::integral_constant<int, 1>{}, n_tok);
+    else block(std::integral_constant<int, 2>{}, n_tok);
+    c.i += kWarps;
+    st.locate(c);
+  }
   __syncthreads();
-  if (tid == 0) grid_barrier(abort_flag, p);
+  if (tid == 0) grid_barrier(arrivals + gridDim.x, abort_flag, p);
   __syncthreads();
-  while (c.phase == 1) each(std::true_type{});
+  float total[2][4] = {};
+  while (c.phase == 1) {
+    if (kFp8 && c.d < D) down<kFp8>(st, ring, c, ahead, abort_flag, total);
+    else down<false>(st, ring, c, ahead, abort_flag, total);
+    st.next(c);
+  }
   __syncthreads();
 
-  // ---- both halves' sums, the residual, one rounding
+  // ---- the warps' sums in warp order, the residual, one rounding
+  float* sums = reinterpret_cast<float*>(slots);                 // [warp][row of 16][token of 16]
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[(warp * 16 + g + 8 * (j >> 1)) * 16 + 8 * b + 2 * q + (j & 1)] = total[b][j];
+  __syncthreads();
   for (int i = tid; i < T * st.cols; i += kThreads) {
     const int t = i / st.cols, r = i - t * st.cols;
-    float v = out_sum[t * p.rows_max + r] + out_sum[(T + t) * p.rows_max + r];
+    // the row block of column r: the last one that starts at or before it
+    int rb = r * st.row_blocks / st.cols;
+    if (rb + 1 < st.row_blocks && st.cols * (rb + 1) / st.row_blocks <= r) ++rb;
+    const int row = r - st.cols * rb / st.row_blocks;
+    float v = 0.0f;
+    for (int w = rb; w < kWarps; w += st.row_blocks) v += sums[(w * 16 + row) * 16 + t];
     const size_t at = static_cast<size_t>(t) * H + st.col0 + r;
     if (p.residual) v += bf16_bits_to_f32(p.residual[at]);
     p.out[at] = f32_to_bf16_bits(v);
@@ -689,15 +848,14 @@ layer_few_kernel(const Params p) {
 size_t pad(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 struct Layout {
-  size_t logits, gate, act, act_s, bytes;
+  size_t logits, gate, act, bytes;
 };
 Layout layout_of(int T, int I, int E, int K, int Is) {
   Layout l;
-  l.logits = 256;                  // the barrier's words before it
+  l.logits = 256;                  // the barrier's count before it
   l.gate = l.logits + pad(static_cast<size_t>(T) * E * 4);
   l.act = l.gate + pad(static_cast<size_t>(T) * 4);
-  l.act_s = l.act + pad(static_cast<size_t>(T) * K * I * 4);
-  l.bytes = l.act_s + pad(static_cast<size_t>(T) * Is * 4);
+  l.bytes = l.act + pad(6 * static_cast<size_t>(T) * (static_cast<size_t>(K) * I + Is));
   return l;
 }
 
@@ -763,18 +921,16 @@ template <bool kFp8>
 int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   const Layout l = layout_of(p.T, p.I, p.E, p.K, p.Is);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.barrier = reinterpret_cast<unsigned int*>(ws);
+  p.barrier = reinterpret_cast<unsigned long long*>(ws);
   p.logits = reinterpret_cast<float*>(ws + l.logits);
   p.gate = reinterpret_cast<float*>(ws + l.gate);
-  p.act = reinterpret_cast<float*>(ws + l.act);
-  p.act_s = reinterpret_cast<float*>(ws + l.act_s);
+  p.act = reinterpret_cast<uint16_t*>(ws + l.act);
   const int ctas = sm_count();
-  p.rows_max = (p.H + ctas - 1) / ctas;
-  const int fixed = (static_cast<int>(sizeof(Fixed)) + 2 * p.T * p.rows_max * 4 + 127) & ~127;
-  constexpr int kSmem = 227 * 1024;
-  const int scores = 2 * p.T * p.E * 4;      // of the choice, in the ring
-  const int smem = fixed + (scores > kRing ? scores : kRing);
-  if (smem > kSmem) return set_error(MOE_ERR_CUDA, "%s: %d SMs leave no room for the ring", op, ctas);
+  if (p.H > 16ll * kWarps * ctas)      // row blocks of the down product: a warp has one
+    return set_error(MOE_ERR_CUDA, "%s: H=%d on %d SMs", op, p.H, ctas);
+  constexpr int kFixed = (static_cast<int>(sizeof(Fixed)) + 127) & ~127, kSmem = kFixed + kRing;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(sizeof(Scratch) + 2 * kMaxT * kMaxE * 4 <= kRing && kWarps * 1024 <= kRing, "what the ring holds besides");
   auto kern = layer_few_kernel<kFp8>;
   static std::atomic<int> configured[64] = {};
   int dev = 0;
@@ -797,7 +953,7 @@ int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
-  return launch_status(launch_kernel(kern, dim3(ctas), dim3(kThreads), smem, stream, attr, 1, p), op);
+  return launch_status(launch_kernel(kern, dim3(ctas), dim3(kThreads), kSmem, stream, attr, 1, p), op);
 }
 
 }  // namespace
