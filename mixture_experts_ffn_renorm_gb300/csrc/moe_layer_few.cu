@@ -51,7 +51,7 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxPairs = kMaxT * 32;
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSlots = 2;          // per warp
+constexpr int kSlots = 2;          // per warp (the loop's two cursors)
 // gate/up: 4 features' gate and up rows, 1 KB of each; down: 16 rows, 512 bytes of each.  Rows lie
 // 64 bytes off a multiple of 128 apart, so two rows x 64 bytes, a quarter-warp's read, meet all banks once.
 constexpr int kFeat = 4;
@@ -153,28 +153,65 @@ __device__ __forceinline__ void grid_barrier(unsigned long long target, volatile
   }
 }
 
+// one copy of the router's exponential: what runs once per call costs its instructions' way
+// from memory (the kernel of one token spent a third of its time waiting for code)
+__device__ __noinline__ float exp_once(float v) { return exp_f32(v); }
+__device__ __forceinline__ float sigmoid_once(float v) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, exp_once(-v))); }
+
+// The K best of a token's E keys in the router's order (descending, ties to the lower id, NaN last)
+// among those whose bit of `taken` is clear: the j-th id in lane j.  A lane holds entries lane +
+// 32 i, its best one found again only after it was taken.
+template <int kPer>
+__device__ __forceinline__ int pick(const float* key, int E, int K, int lane, uint32_t taken) {
+  uint32_t k[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    k[i] = lane + 32 * i < E ? route::rank_key(key[lane + 32 * i]) : 0u;
+    if (lane + 32 * i >= E) taken |= 1u << i;
+  }
+  int id = 0;
+#pragma unroll 1
+  for (int j = 0; j < K; ++j) {
+    uint32_t bk = 0u, bid = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (!((taken >> i) & 1u) && (bid == 0xFFFFFFFFu || k[i] > bk)) {
+        bk = k[i];
+        bid = static_cast<uint32_t>(lane + 32 * i);
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+    const uint32_t win = __reduce_min_sync(0xffffffffu, bk == top ? bid : 0xFFFFFFFFu);
+    if ((win & 31u) == static_cast<uint32_t>(lane)) taken |= 1u << (win >> 5);
+    if (lane == j) id = static_cast<int>(win);
+  }
+  return id;
+}
+
 // The pairs of a token: one warp picks the K experts in the router's order and forms their
 // weights with the router's arithmetic.
-__device__ void choose(const Params& p, Fixed& f, Scratch& x, int t, int lane) {
+__device__ __forceinline__ void choose(const Params& p, Fixed& f, Scratch& x, int t, int lane) {
   const int E = p.E, K = p.K;
   float *v = x.scores + static_cast<size_t>(t) * 2 * E, *key = v + E;
+#pragma unroll 1
   for (int e = lane; e < E; e += 32) {
     const float l = __ldcg(p.logits + static_cast<size_t>(t) * E + e);
-    const float s = p.scoring ? sigmoid_f32(l) : l;
+    const float s = p.scoring ? sigmoid_once(l) : l;
     v[e] = s;
     key[e] = p.select_bias ? __fadd_rn(s, __ldg(p.select_bias + e)) : s;
   }
   __syncwarp();
-  uint32_t taken = 0;              // bit i: entry lane + 32 i is not eligible any more
+  uint32_t taken = 0;              // bit i: entry lane + 32 i is not eligible
   if (p.n_group > 1) {
+    // lane g scores groups g and g + 32 by their best key or two; the topk_group best stay open
     const int gs = E / p.n_group;
-    uint32_t gkey[2], gtaken = 0, open[2] = {0u, 0u};
-#pragma unroll
+    uint32_t gkey[2] = {0u, 0u}, open[2] = {0u, 0u}, gtaken = 0;
+#pragma unroll 1
     for (int q = 0; q < 2; ++q) {
       const int g = lane + 32 * q;
-      gkey[q] = 0u;
+      uint32_t k = 0u;
       if (g < p.n_group) {
         int b0 = -1, b1 = -1;
+#pragma unroll 1
         for (int e = g * gs; e < g * gs + gs; ++e) {
           if (b0 < 0 || route::ranks_above(key[e], e, key[b0], b0)) {
             b1 = b0;
@@ -183,81 +220,51 @@ __device__ void choose(const Params& p, Fixed& f, Scratch& x, int t, int lane) {
             b1 = e;
           }
         }
-        gkey[q] = route::rank_key(p.group_score ? __fadd_rn(key[b0], key[b1]) : key[b0]);
+        k = route::rank_key(p.group_score ? __fadd_rn(key[b0], key[b1]) : key[b0]);
       }
+      if (q) gkey[1] = k;
+      else gkey[0] = k;
     }
+#pragma unroll 1
     for (int j = 0; j < p.topk_group; ++j) {
       uint32_t bk = 0u, bid = 0xFFFFFFFFu;
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        if (lane + 32 * q < p.n_group && !((gtaken >> q) & 1u) &&
-            (bid == 0xFFFFFFFFu || gkey[q] > bk)) {
+        if (lane + 32 * q < p.n_group && !((gtaken >> q) & 1u) && (bid == 0xFFFFFFFFu || gkey[q] > bk)) {
           bk = gkey[q];
           bid = static_cast<uint32_t>(lane + 32 * q);
         }
       const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-      const uint32_t win =
-          __reduce_min_sync(0xffffffffu, bid != 0xFFFFFFFFu && bk == top ? bid : 0xFFFFFFFFu);
-      if (static_cast<int>(win & 31u) == lane) gtaken |= 1u << (win >> 5);
+      const uint32_t win = __reduce_min_sync(0xffffffffu, bk == top ? bid : 0xFFFFFFFFu);
+      if ((win & 31u) == static_cast<uint32_t>(lane)) gtaken |= 1u << (win >> 5);
       if (win >> 5) open[1] |= 1u << (win & 31u);
       else open[0] |= 1u << win;
     }
+#pragma unroll 1
     for (int i = 0; lane + 32 * i < E; ++i) {
       const int g = (lane + 32 * i) / gs;
-      const uint32_t bits = g >> 5 ? open[1] : open[0];
-      if (!((bits >> (g & 31)) & 1u)) taken |= 1u << i;
+      if (!((g >> 5 ? open[1] : open[0]) >> (g & 31) & 1u)) taken |= 1u << i;
     }
   }
-  // a lane's best entry is looked for again only after it was taken
-  uint32_t bk = 0u, bid = 0xFFFFFFFFu;
-  auto rescan = [&]() {
-    bk = 0u;
-    bid = 0xFFFFFFFFu;
-    for (int i = 0; lane + 32 * i < E; ++i) {
-      if ((taken >> i) & 1u) continue;
-      const uint32_t k = route::rank_key(key[lane + 32 * i]);
-      if (bid == 0xFFFFFFFFu || k > bk) {
-        bk = k;
-        bid = static_cast<uint32_t>(lane + 32 * i);
-      }
-    }
-  };
-  rescan();
-  float sel = 0.0f;
-  int id = 0;
-  for (int j = 0; j < K; ++j) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-    const uint32_t win =
-        __reduce_min_sync(0xffffffffu, bid != 0xFFFFFFFFu && bk == top ? bid : 0xFFFFFFFFu);
-    if (lane == j) {
-      id = static_cast<int>(win);
-      sel = v[win];
-    }
-    if (static_cast<int>(win & 31u) == lane) {
-      taken |= 1u << (win >> 5);
-      rescan();
-    }
-  }
-  float num = sel, den = 1.0f;
-  if (p.scoring) {
-    if (p.renormalize) {
-      den = 0.0f;
-      for (int j = 0; j < K; ++j) den = __fadd_rn(den, __shfl_sync(0xffffffffu, sel, j));
-    }
-  } else {
-    const float m = __shfl_sync(0xffffffffu, sel, 0);
+  const int id = E <= 256 ? pick<8>(key, E, K, lane, taken) : pick<32>(key, E, K, lane, taken);
+  const float sel = v[id];
+  float num = sel, den = 0.0f;
+  const float m = __shfl_sync(0xffffffffu, sel, 0);
+  if (!p.scoring) {
     const float d = __fsub_rn(sel, m);
-    num = (lane == 0 && d == 0.0f) ? 1.0f : exp_f32(d);
-    den = 0.0f;
-    if (p.renormalize) {
-      for (int j = 0; j < K; ++j) den = __fadd_rn(den, __shfl_sync(0xffffffffu, num, j));
-    } else {
-      // the sum over all experts, in id order
-      for (int e = lane; e < E; e += 32) key[e] = exp_f32(__fsub_rn(v[e], m));
-      __syncwarp();
-#pragma unroll 8
-      for (int e = 0; e < E; ++e) den = __fadd_rn(den, key[e]);
-    }
+    num = (lane == 0 && d == 0.0f) ? 1.0f : exp_once(d);
+  }
+  if (p.renormalize) {
+#pragma unroll 1
+    for (int j = 0; j < K; ++j) den = __fadd_rn(den, __shfl_sync(0xffffffffu, num, j));
+  } else if (!p.scoring) {
+    // the sum over all experts, in id order
+    __syncwarp();
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) key[e] = exp_once(__fsub_rn(v[e], m));
+    __syncwarp();
+#pragma unroll 4
+    for (int e = 0; e < E; ++e) den = __fadd_rn(den, key[e]);
   }
   if (lane < K) {
     const float w = p.scoring && !p.renormalize ? num : __fdiv_rn(num, den);
@@ -273,9 +280,10 @@ __device__ void choose(const Params& p, Fixed& f, Scratch& x, int t, int lane) {
 
 // Touched experts in ascending order with their pairs (tokens ascending), then the shared
 // expert's tokens.  One warp scans the experts; then a thread per pair places it.
-__device__ void group_experts(const Params& p, Fixed& f, Scratch& x, int lane) {
+__device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch& x, int lane) {
   const int per = (p.E + 31) / 32, lo = min(p.E, lane * per), hi = min(p.E, lo + per);
   int n = 0;                       // touched experts, and their pairs in the upper half
+#pragma unroll 1
   for (int e = lo; e < hi; ++e)
     if (x.mask[e]) n += 1 + (__popc(x.mask[e]) << 16);
   int incl = n;
@@ -285,6 +293,7 @@ __device__ void group_experts(const Params& p, Fixed& f, Scratch& x, int lane) {
     if (lane >= o) incl += u;
   }
   int run = incl - n;
+#pragma unroll 1
   for (int e = lo; e < hi; ++e) {
     const uint32_t m = x.mask[e];
     if (!m) continue;
@@ -328,9 +337,9 @@ struct Stream {
     // a shared expert's bf16 feature beside FP8 ones counts twice
     constexpr unsigned kCost = kFp8 ? 2 : 1;
     const unsigned I = p.I, line = static_cast<unsigned>(D) * I;           // at most 512 * 8192
-    const unsigned long long all = line + kCost * p.Is;
-    const unsigned a = static_cast<unsigned>(all * blockIdx.x / gridDim.x);
-    const unsigned b = static_cast<unsigned>(all * (blockIdx.x + 1) / gridDim.x);
+    const unsigned all = line + kCost * p.Is, cta = blockIdx.x;
+    const unsigned a = all / gridDim.x * cta + min(cta, all % gridDim.x);
+    const unsigned b = a + all / gridDim.x + (cta < all % gridDim.x ? 1u : 0u);
     const unsigned ra = min(a, line), rb = min(b, line);
     d0 = static_cast<int>(ra / I);
     i0 = static_cast<int>(ra - d0 * I);
@@ -346,8 +355,9 @@ struct Stream {
     s0 = static_cast<int>((a - ra + kCost - 1) / kCost);
     s_end = static_cast<int>((b - rb + kCost - 1) / kCost);
     blocks = routed + (s_end - s0 + kFeat - 1) / kFeat;
-    col0 = static_cast<int>(static_cast<long long>(p.H) * blockIdx.x / gridDim.x);
-    cols = static_cast<int>(static_cast<long long>(p.H) * (blockIdx.x + 1) / gridDim.x) - col0;
+    const unsigned H = p.H;
+    col0 = static_cast<int>(H / gridDim.x * cta + min(cta, H % gridDim.x));
+    cols = static_cast<int>(H / gridDim.x + (cta < H % gridDim.x ? 1u : 0u));
     // even blocks of at most 16 rows; the warps take blocks in turn, and share a block's units
     row_blocks = (cols + 15) >> 4;
     const int rb_i = row_blocks ? warp % row_blocks : 0;
@@ -464,229 +474,130 @@ __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
   hi = gemm::pack_bf16x2(__low2float(b), __high2float(b));
 }
 
-// A warp's ring
-struct Ring {
-  uint32_t slots, bars;            // shared addresses of slot 0 and its barrier
-  int s;
-  uint32_t phase;
-};
-
-// waits for the current slot; then, once it has been read, refills it and steps on
-template <bool kFp8>
-__device__ __forceinline__ bool take(const Stream<kFp8>& st, const Ring& r, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, wait(r.bars + 8 * r.s, r.phase, abort_flag, st.p));
-}
-template <bool kFp8>
-__device__ __forceinline__ void give(const Stream<kFp8>& st, Ring& r, Cursor& ahead, bool landed) {
-  __syncwarp();                    // all lanes have read the slot
-  if (landed) st.issue(ahead, r.slots + r.s * kSlotBytes, r.bars + 8 * r.s);
-  if (ahead.phase < 2) st.next(ahead);
-  if (++r.s == kSlots) {
-    r.s = 0;
-    r.phase ^= 1u;
-  }
-}
-
-// One block of gate/up: the sums of 4 features' gate and up rows (MMA rows 0-3 and 4-7) over the
-// whole width, for the expert's tokens in NB eights
-template <int NB, bool kQ, bool kFp8>
-__device__ __forceinline__ void gate_up(const Stream<kFp8>& st, Ring& ring, const Cursor& c, Cursor& ahead, int n_tok,
-                                        volatile int* abort_flag, float (&out)[NB][4]) {
-  const Params& p = st.p;
-  const Fixed& f = st.f;
-  const int lane = st.lane, g = lane >> 2, q = lane & 3, H = p.H, per = kQ ? kGuPiece : kGuPiece / 2;
-  const int first = f.first[c.d];
-  const uint4* x[NB];
-  bool has[NB];
+// One piece of a block of gate/up: products of 4 features' gate and up rows (MMA rows 0-3 and 4-7,
+// this lane's row and 16-byte column at `at`) with eight of the expert's tokens, added to c.
+// x: this lane's token from the piece's first column, or null; sc: this lane's row's scales from there.
+template <bool kQ>
+__device__ __forceinline__ void gate_up(uint32_t at, int n, int q, const uint4* x, const float* sc, float (&c)[4]) {
+  constexpr int kStep = kQ ? 64 : 32, kBatch = kQ ? 2 : 4;       // columns of a step: 16 bytes of a row per lane
+  float acc[2][4] = {};
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += kBatch * kStep) {
+    uint4 b[kBatch][kQ ? 2 : 1];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    has[b] = 8 * b + g < n_tok;
-    x[b] = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(has[b] ? f.token[first + 8 * b + g] : 0) * H);
-  }
-  const float* sc0 = nullptr;      // scales of this lane's row: feature g & 3, gate or up
-  if (kQ) {
-    const int nblk = (H + 127) >> 7, row = (g < kFeat ? 0 : p.I) + min(c.n + (g & 3), p.I - 1);
-    sc0 = p.s13 + (static_cast<size_t>(f.expert[c.d]) * ((2 * p.I + 127) >> 7) + (row >> 7)) * nblk;
-  }
-  float acc[NB][2][4];
+    for (int s = 0; s < kBatch; ++s)
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[b][0][j] = acc[b][1][j] = out[b][j] = 0.0f;
-  constexpr int kStep = kQ ? 64 : 32;            // columns of a step: 16 bytes of a row per lane
-  for (int k = 0; k < H; k += per) {
-    const int n = min(per, H - k);
-    const uint32_t at = ring.slots + ring.s * kSlotBytes + g * kGuPitch + q * 16;
-    bool landed = false;
-    // 4 steps at a time: their tokens' loads first, for the first ones ahead of the wait
-    for (int k0 = 0; k0 < n; k0 += 4 * kStep) {
-      uint4 b[NB][4][kQ ? 2 : 1];
-      float sc[2];
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int h = 0; h < (kQ ? 2 : 1); ++h) {
-            const int col = k0 + s * kStep + (kQ ? 16 : 8) * q + 8 * h;
-            b[i][s][h] = has[i] && col < n ? __ldg(x[i] + ((k + col) >> 3)) : make_uint4(0, 0, 0, 0);
-          }
-      if (kQ) {                                  // 4 steps are two scale blocks
-        sc[0] = __ldg(sc0 + ((k + k0) >> 7));
-        sc[1] = k0 + 128 < n ? __ldg(sc0 + ((k + k0 + 128) >> 7)) : 0.0f;
+      for (int h = 0; h < (kQ ? 2 : 1); ++h) {
+        const int col = k0 + s * kStep + (kQ ? 16 : 8) * q + 8 * h;
+        b[s][h] = x && col < n ? __ldg(x + (col >> 3)) : make_uint4(0, 0, 0, 0);
       }
-      if (k0 == 0) landed = take(st, ring, abort_flag);
+    const float d = kQ ? __ldg(sc + (k0 >> 7)) : 1.0f;           // FP8: a batch is a scale block
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (k0 + s * kStep >= n) break;
-        const bool in = k0 + s * kStep + (kQ ? 16 : 8) * q < n;   // behind the row's end: stale bytes
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (in) w = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2));
-        if (kQ) {
-          const uint32_t code[4] = {w.x, w.y, w.z, w.w};
+    for (int s = 0; s < kBatch; ++s) {
+      uint4 w = make_uint4(0, 0, 0, 0);                          // behind the row's end lie stale bytes
+      if (k0 + s * kStep + (kQ ? 16 : 8) * q < n) w = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2));
+      if (kQ) {
+        const uint32_t code[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t lo, hi;
-            widen4(code[j], lo, hi);
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-              const uint4& u = b[i][s][kQ ? j >> 1 : 0];
-              mma(acc[i][j & 1], lo, 0u, hi, 0u, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
-            }
-          }
-          if ((s & 1) || k0 + (s + 1) * kStep >= n) {             // the end of a scale block
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                out[i][j] = fmaf(acc[i][0][j] + acc[i][1][j], sc[s >> 1], out[i][j]);
-                acc[i][0][j] = acc[i][1][j] = 0.0f;
-              }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            mma(acc[i][0], w.x, 0u, w.y, 0u, b[i][s][0].x, b[i][s][0].y);
-            mma(acc[i][1], w.z, 0u, w.w, 0u, b[i][s][0].z, b[i][s][0].w);
-          }
+        for (int j = 0; j < 4; ++j) {
+          uint32_t lo, hi;
+          widen4(code[j], lo, hi);
+          const uint4& u = b[s][kQ ? j >> 1 : 0];
+          mma(acc[j & 1], lo, 0u, hi, 0u, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
         }
+      } else {
+        mma(acc[0], w.x, 0u, w.y, 0u, b[s][0].x, b[s][0].y);
+        mma(acc[1], w.z, 0u, w.w, 0u, b[s][0].z, b[s][0].w);
       }
     }
-    give(st, ring, ahead, landed);
+    if (kQ) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        c[j] = fmaf(acc[0][j] + acc[1][j], d, c[j]);
+        acc[0][j] = acc[1][j] = 0.0f;
+      }
+    }
   }
   if (!kQ) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) out[b][j] = acc[b][0][j] + acc[b][1][j];
+    for (int j = 0; j < 2; ++j) c[j] += acc[0][j] + acc[1][j];
   }
 }
 
-// One unit of down: 16 output columns x a piece of one expert's activations, added to the tokens'
-// sums.  Tokens that did not choose the expert take nothing from it, not even a product with zero.
-template <bool kQ, bool kFp8>
-__device__ __forceinline__ void down(const Stream<kFp8>& st, Ring& ring, const Cursor& c, Cursor& ahead,
-                                     volatile int* abort_flag, float (&total)[2][4]) {
-  const Params& p = st.p;
-  const Fixed& f = st.f;
-  const int lane = st.lane, g = lane >> 2, q = lane & 3, I = st.inner(c.d), per = kQ ? kDnPiece : kDnPiece / 2;
-  const int n = min(per, I - c.k);
-  const uint32_t tokens = f.tokens[c.d];
-  const size_t parts = c.d < st.D ? static_cast<size_t>(p.T) * p.K * I : static_cast<size_t>(p.T) * I;
-  const uint16_t* base = p.act + (c.d < st.D ? 0 : 3 * static_cast<size_t>(p.T) * p.K * p.I);
-  const uint32_t at = ring.slots + ring.s * kSlotBytes + g * kDnPitch + q * 16;
-  constexpr int kStep = kQ ? 64 : 32, kHalf = kQ ? 2 : 1, kBatch = kQ ? 2 : 4;   // steps of a batch of loads
-  const float *sc0 = nullptr, *sc1 = nullptr;
-  if (kQ) {
-    const int nblk = (I + 127) >> 7, r = st.col0 + st.row0 + g;
-    const float* s2 = p.s2 + static_cast<size_t>(f.expert[c.d]) * ((p.H + 127) >> 7) * nblk;
-    sc0 = s2 + static_cast<size_t>(min(r, p.H - 1) >> 7) * nblk;
-    sc1 = s2 + static_cast<size_t>(min(r + 8, p.H - 1) >> 7) * nblk;
-  }
-  bool waited = false, landed = false;
+// One unit of down: products of 16 output columns' rows (at, 8 rows on) with the three parts of eight
+// tokens' activations, `parts` 16-byte vectors apart.  a: this lane's token, or null.
+template <bool kQ>
+__device__ __forceinline__ void down(uint32_t at, int n, int q, const uint4* a, size_t parts, const float* sc0,
+                                     const float* sc1, float (&c)[4]) {
+  constexpr int kStep = kQ ? 64 : 32, kHalf = kQ ? 2 : 1, kBatch = kQ ? 2 : 4;
+  float acc[4][4] = {};
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += kBatch * kStep) {
+    uint4 b[kBatch][3][kHalf];
 #pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
-    const uint32_t here = tokens >> (8 * nb) & 0xFFu;
-    if (!here) continue;
-    const int t = 8 * nb + g;
-    const bool has = tokens >> t & 1u;
-    const uint4* a = nullptr;
-    if (has) {
-      const int pair = f.first[c.d] + __popc(tokens & ((1u << t) - 1u));
-      a = reinterpret_cast<const uint4*>(base + static_cast<size_t>(c.d < st.D ? f.pair[pair] : t) * I + c.k);
-    }
-    float acc[4][4], sum[4];
+    for (int s = 0; s < kBatch; ++s)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      sum[j] = 0.0f;
+      for (int part = 0; part < 3; ++part)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i][j] = 0.0f;
-    }
-    for (int k0 = 0; k0 < n; k0 += kBatch * kStep) {
-      uint4 b[kBatch][3][kHalf];
-#pragma unroll
-      for (int s = 0; s < kBatch; ++s)
-#pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int h = 0; h < kHalf; ++h) {      // written by other SMs before the grid barrier
-            const int col = k0 + s * kStep + 8 * kHalf * q + 8 * h;
-            b[s][part][h] = has && col < n ? a[(part * parts + col) >> 3] : make_uint4(0, 0, 0, 0);
-          }
-      float d0 = 1.0f, d1 = 1.0f;
-      if (kQ) {                                  // a batch is one scale block
-        d0 = __ldg(sc0 + ((c.k + k0) >> 7));
-        d1 = __ldg(sc1 + ((c.k + k0) >> 7));
-      }
-      if (!waited) {
-        landed = take(st, ring, abort_flag);
-        waited = true;
-      }
-#pragma unroll
-      for (int s = 0; s < kBatch; ++s) {
-        if (k0 + s * kStep >= n) break;
-        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-        if (k0 + s * kStep + 8 * kHalf * q < n) {
-          w0 = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2));
-          w1 = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2) + 8 * kDnPitch);
+        for (int h = 0; h < kHalf; ++h) {      // written by other SMs before the grid barrier
+          const int col = k0 + s * kStep + 8 * kHalf * q + 8 * h;
+          b[s][part][h] = a && col < n ? a[part * parts + (col >> 3)] : make_uint4(0, 0, 0, 0);
         }
-        if (kQ) {
-          const uint32_t c0[4] = {w0.x, w0.y, w0.z, w0.w}, c1[4] = {w1.x, w1.y, w1.z, w1.w};
+    float d0 = 1.0f, d1 = 1.0f;
+    if (kQ) {                                  // a batch is one scale block
+      d0 = __ldg(sc0 + (k0 >> 7));
+      d1 = __ldg(sc1 + (k0 >> 7));
+    }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t a0, a2, a1, a3;
-            widen4(c0[j], a0, a2);
-            widen4(c1[j], a1, a3);
-#pragma unroll
-            for (int part = 0; part < 3; ++part) {
-              const uint4& u = b[s][part][kQ ? j >> 1 : 0];
-              mma(acc[(part ? 2 : 0) + (j & 1)], a0, a1, a2, a3, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint4& u = b[s][part][0];
-            mma(acc[part ? 2 : 0], w0.x, w1.x, w0.y, w1.y, u.x, u.y);
-            mma(acc[part ? 3 : 1], w0.z, w1.z, w0.w, w1.w, u.z, u.w);
-          }
-        }
+    for (int s = 0; s < kBatch; ++s) {
+      uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+      if (k0 + s * kStep + 8 * kHalf * q < n) {
+        w0 = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2));
+        w1 = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2) + 8 * kDnPitch);
       }
       if (kQ) {
+        const uint32_t c0[4] = {w0.x, w0.y, w0.z, w0.w}, c1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sum[j] = fmaf(acc[0][j] + acc[1][j] + (acc[2][j] + acc[3][j]), j < 2 ? d0 : d1, sum[j]);
-          acc[0][j] = acc[1][j] = acc[2][j] = acc[3][j] = 0.0f;
+          uint32_t a0, a1, a2, a3;
+          widen4(c0[j], a0, a2);
+          widen4(c1[j], a1, a3);
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            const uint4& u = b[s][part][kQ ? j >> 1 : 0];
+            mma(acc[(part ? 2 : 0) + (j & 1)], a0, a1, a2, a3, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const uint4& u = b[s][part][0];
+          mma(acc[part ? 2 : 0], w0.x, w1.x, w0.y, w1.y, u.x, u.y);
+          mma(acc[part ? 3 : 1], w0.z, w1.z, w0.w, w1.w, u.z, u.w);
         }
       }
     }
+    if (kQ) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float v = kQ ? sum[j] : acc[0][j] + acc[1][j] + (acc[2][j] + acc[3][j]);
-      if (tokens >> (8 * nb + 2 * q + (j & 1)) & 1u) total[nb][j] += v;
+      for (int j = 0; j < 4; ++j) {
+        c[j] = fmaf(acc[0][j] + acc[1][j] + (acc[2][j] + acc[3][j]), j < 2 ? d0 : d1, c[j]);
+        acc[0][j] = acc[1][j] = acc[2][j] = acc[3][j] = 0.0f;
+      }
     }
   }
-  give(st, ring, ahead, landed);
+  if (!kQ) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] += acc[0][j] + acc[1][j] + (acc[2][j] + acc[3][j]);
+  }
+}
+
+__device__ __forceinline__ void swap4(float (&a)[4], float (&b)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float t = a[j];
+    a[j] = b[j];
+    b[j] = t;
+  }
 }
 
 // v as three bf16 parts that add up to it (an infinity or NaN as its first part alone)
@@ -724,6 +635,7 @@ layer_few_kernel(const Params p) {
   // ---- logits, and the shared expert's gate logits as one more row
   {
     const int rows = E + (p.w_gate ? 1 : 0), halves = (T + route::kTokWarp - 1) / route::kTokWarp;
+#pragma unroll 1
     for (int task = blockIdx.x + gridDim.x * warp; task < rows * halves; task += gridDim.x * kWarps) {
       const int e = task % rows, t0 = task / rows * route::kTokWarp;
       float sum[route::kTokWarp];
@@ -745,11 +657,13 @@ layer_few_kernel(const Params p) {
   __syncthreads();
 
   // ---- choice of experts
+#pragma unroll 1
   for (int t = warp; t < T; t += kWarps) choose(p, f, x, t, lane);
-  if (tid < T) f.gate[tid] = p.w_gate ? sigmoid_f32(__ldcg(p.gate + tid)) : 1.0f;
+  if (tid < T) f.gate[tid] = p.w_gate ? sigmoid_once(__ldcg(p.gate + tid)) : 1.0f;
   __syncthreads();
   if (warp == 0) group_experts(p, f, x, lane);
   __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < T * K + T; i += kThreads) {
     const int t = i < T * K ? i / K : i - T * K;
     int at = i;
@@ -763,67 +677,129 @@ layer_few_kernel(const Params p) {
   ptx::fence_proxy_async_smem();   // the scratch in the ring, before copies overwrite it
   __syncthreads();
 
-  // ---- the experts
+  // ---- the experts.  One loop over the pieces of both phases, so that their code is there once:
+  // wait for the slot, multiply, refill the slot
   const Stream<kFp8> st(p, f, warp, lane);
   const int D = st.D, g = lane >> 2, q = lane & 3;
-  Ring ring{ptx::smem_u32(slots) + warp * kSlots * kSlotBytes, ptx::smem_u32(&f.full[warp][0]), 0, 0u};
-  Cursor c = st.begin(), ahead = c;
-#pragma unroll
+  const uint32_t ring = ptx::smem_u32(slots) + warp * kSlots * kSlotBytes, bars = ptx::smem_u32(&f.full[warp][0]);
+  Cursor c[kSlots], ahead = st.begin();          // of the pieces in the slots, the oldest first
+#pragma unroll 1
   for (int s = 0; s < kSlots; ++s) {
-    st.issue(ahead, ring.slots + s * kSlotBytes, ring.bars + 8 * s);
+    st.issue(ahead, ring + s * kSlotBytes, bars + 8 * s);
+    c[0] = c[1];
+    c[1] = ahead;
     if (ahead.phase < 2) st.next(ahead);
   }
-  // gate and up of feature c.n + g and token i of the expert, weighted and cut for the down product
-  auto emit = [&](float gate, float up, int n_tok, int i) {
-    if (g >= c.cnt || i >= n_tok) return;        // c.cnt <= 4: rows 0-3
-    const int pair = f.first[c.d] + i, tok = f.token[pair];
-    const bool shared = c.d == D;
-    const int row = shared ? tok : f.pair[pair], I = shared ? p.Is : p.I, rows = shared ? T : T * K;
-    const float a = gate / (1.0f + __expf(-gate)) * up * (shared ? f.gate[tok] : f.weight[row]);
-    uint16_t part[3];
-    cut3(a, part);
-    uint16_t* to = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) + static_cast<size_t>(row) * I + c.n + g;
+  int s = 0;
+  uint32_t parity = 0;
+  float cur[4] = {}, other[4] = {};              // sums of tokens 0-7 and 8-15 (gate/up: of the expert's)
+#pragma unroll 1
+  for (int phase = 0; phase < 2; ++phase) {
+#pragma unroll 1
+    while (c[0].phase == phase) {
+      const int d = c[0].d, k = c[0].k, first = f.first[d], I = st.inner(d);
+      const bool quant = st.quant(d), shared = d == D;
+      const uint32_t at = ring + s * kSlotBytes + q * 16;
+      const bool landed = __all_sync(0xffffffffu, wait(bars + 8 * s, parity, abort_flag, p));
+      if (phase == 0) {
+        const int n = min(st.gu_cols(d), H - k), n_tok = f.first[d + 1] - first;
+        const float* sc = nullptr;
+        if (kFp8 && quant) {                     // scales of this lane's row: feature g & 3, gate or up
+          const int nblk = (H + 127) >> 7, row = (g < kFeat ? 0 : I) + min(c[0].n + (g & 3), I - 1);
+          sc = p.s13 + (static_cast<size_t>(f.expert[d]) * ((2 * I + 127) >> 7) + (row >> 7)) * nblk + (k >> 7);
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < n_tok; i0 += 8) {
+          const uint4* xt = i0 + g < n_tok ? reinterpret_cast<const uint4*>(
+                                                 p.x + static_cast<size_t>(f.token[first + i0 + g]) * H + k)
+                                           : nullptr;
+          if (kFp8 && quant) gate_up<kFp8>(at + g * kGuPitch, n, q, xt, sc, cur);
+          else gate_up<false>(at + g * kGuPitch, n, q, xt, sc, cur);
+          if (n_tok > 8) swap4(cur, other);
+        }
+        if (k + n == H) {
+          // the features' last piece: silu(gate) up, weighted, in parts for the down product
+#pragma unroll 1
+          for (int i0 = 0; i0 < n_tok; i0 += 8) {
 #pragma unroll
-    for (int j = 0; j < 3; ++j) to[j * static_cast<size_t>(rows) * I] = part[j];
-  };
-  auto block = [&](auto nb, int n_tok) {
-    constexpr int NB = decltype(nb)::value;
-    float v[NB][4];
-    if (kFp8 && c.d < D) gate_up<NB, kFp8>(st, ring, c, ahead, n_tok, abort_flag, v);
-    else gate_up<NB, false>(st, ring, c, ahead, n_tok, abort_flag, v);
+            for (int j = 0; j < 2; ++j) {
+              const float gate = cur[j], up = __shfl_down_sync(0xffffffffu, gate, 4 * kFeat);
+              const int i = i0 + 2 * q + j;
+              if (g < c[0].cnt && i < n_tok) {   // cnt <= 4: rows 0-3
+                const int pair = f.pair[first + i], tok = f.token[first + i], row = shared ? tok : pair;
+                const float a = gate / (1.0f + __expf(-gate)) * up * (shared ? f.gate[tok] : f.weight[pair]);
+                uint16_t part[3];
+                cut3(a, part);
+                const size_t step = static_cast<size_t>(shared ? T : T * K) * I;
+                uint16_t* to = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) +
+                               static_cast<size_t>(row) * I + c[0].n + g;
+                to[0] = part[0];
+                to[step] = part[1];
+                to[2 * step] = part[2];
+              }
+            }
+            if (n_tok > 8) swap4(cur, other);
+          }
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+          for (int j = 0; j < 4; ++j) cur[j] = other[j] = 0.0f;
+        }
+      } else {
+        // tokens that did not choose the expert take nothing from it, not even a product with zero
+        const int n = min(st.dn_cols(d), I - k);
+        const uint32_t tokens = f.tokens[d];
+        const size_t step = (static_cast<size_t>(shared ? T : T * K) * I) >> 3;
+        const uint16_t* act = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) + k;
+        const float *sc0 = nullptr, *sc1 = nullptr;
+        if (kFp8 && quant) {
+          const int nblk = (I + 127) >> 7, r = st.col0 + st.row0 + g;
+          const float* s2 = p.s2 + static_cast<size_t>(f.expert[d]) * ((H + 127) >> 7) * nblk + (k >> 7);
+          sc0 = s2 + static_cast<size_t>(min(r, H - 1) >> 7) * nblk;
+          sc1 = s2 + static_cast<size_t>(min(r + 8, H - 1) >> 7) * nblk;
+        }
+#pragma unroll 1
+        for (int t0 = 0; t0 < 16; t0 += 8) {
+          if (tokens >> t0 & 0xFFu) {
+            const int t = t0 + g;
+            const uint4* a = nullptr;
+            if (tokens >> t & 1u) {
+              const int row = shared ? t : f.pair[first + __popc(tokens & ((1u << t) - 1u))];
+              a = reinterpret_cast<const uint4*>(act + static_cast<size_t>(row) * I);
+            }
+            float v[4] = {};
+            if (kFp8 && quant) down<kFp8>(at + g * kDnPitch, n, q, a, step, sc0, sc1, v);
+            else down<false>(at + g * kDnPitch, n, q, a, step, sc0, sc1, v);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float up = __shfl_down_sync(0xffffffffu, v[b][j], 4 * kFeat);
-        emit(v[b][j], up, n_tok, 8 * b + 2 * q + j);
+            for (int j = 0; j < 4; ++j)
+              if (tokens >> (t0 + 2 * q + (j & 1)) & 1u) cur[j] += v[j];
+          }
+          swap4(cur, other);
+        }
       }
-  };
-  while (c.phase == 0) {
-    const int n_tok = f.first[c.d + 1] - f.first[c.d];
-    if (n_tok <= 8) block(std::integral_constant<int, 1>{}, n_tok);
-    else block(std::integral_constant<int, 2>{}, n_tok);
-    c.i += kWarps;
-    st.locate(c);
+      __syncwarp();                              // all lanes have read the slot
+      if (landed) st.issue(ahead, ring + s * kSlotBytes, bars + 8 * s);
+      c[0] = c[1];
+      c[1] = ahead;
+      if (ahead.phase < 2) st.next(ahead);
+      s ^= 1;
+      parity ^= s ? 0u : 1u;
+    }
+    __syncthreads();
+    if (phase == 0) {
+      if (tid == 0) grid_barrier(arrivals + gridDim.x, abort_flag, p);
+      __syncthreads();
+    }
   }
-  __syncthreads();
-  if (tid == 0) grid_barrier(arrivals + gridDim.x, abort_flag, p);
-  __syncthreads();
-  float total[2][4] = {};
-  while (c.phase == 1) {
-    if (kFp8 && c.d < D) down<kFp8>(st, ring, c, ahead, abort_flag, total);
-    else down<false>(st, ring, c, ahead, abort_flag, total);
-    st.next(c);
-  }
-  __syncthreads();
 
   // ---- the warps' sums in warp order, the residual, one rounding
   float* sums = reinterpret_cast<float*>(slots);                 // [warp][row of 16][token of 16]
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sums[(warp * 16 + g + 8 * (j >> 1)) * 16 + 8 * b + 2 * q + (j & 1)] = total[b][j];
+  for (int j = 0; j < 4; ++j) {
+    float* to = sums + (warp * 16 + g + 8 * (j >> 1)) * 16 + 2 * q + (j & 1);
+    to[0] = cur[j];
+    to[8] = other[j];
+  }
   __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < T * st.cols; i += kThreads) {
     const int t = i / st.cols, r = i - t * st.cols;
     // the row block of column r: the last one that starts at or before it
@@ -831,6 +807,7 @@ layer_few_kernel(const Params p) {
     if (rb + 1 < st.row_blocks && st.cols * (rb + 1) / st.row_blocks <= r) ++rb;
     const int row = r - st.cols * rb / st.row_blocks;
     float v = 0.0f;
+#pragma unroll 1
     for (int w = rb; w < kWarps; w += st.row_blocks) v += sums[(w * 16 + row) * 16 + t];
     const size_t at = static_cast<size_t>(t) * H + st.col0 + r;
     if (p.residual) v += bf16_bits_to_f32(p.residual[at]);
