@@ -18,12 +18,14 @@
 // The barrier between gate/up and down costs no bandwidth: the copies run ahead of it, since
 // the down rows do not depend on it.
 //
-// Every warp is a stream of its own: two slots of 8 KB that its lanes refill as soon as they have
-// read them (16 rows of 512 bytes, or 8 of 1 KB: in a loop of copies alone these two shapes reach 7.0
-// TB/s with 8 to 12 warps an SM; rows of 256 bytes reach 5.2), and no warp waits for another.
+// Every warp is a stream of its own: two slots of 8 KB that it refills as soon as it has read them, and
+// no warp waits for another.  A slot is one or two TMA boxes, swizzled over 128 bytes, whose third
+// dimension steps along the rows: one instruction a box.  (Copies of single rows reach the same 7.0 TB/s
+// in a loop of copies alone, but each costs its warp about 200 cycles to issue, 1700 a slot.)
 // The products are mma.sync: a few tokens leave tcgen05's 128 rows empty, and what counts is
 // instructions per byte of weights.  Weight rows are the M side, tokens the N side; a lane reads 16 bytes of a row
-// and the same 16 bytes' columns of a token, which permutes the columns of a step alike on both sides.
+// and the same columns of a token, which permutes the columns of a step alike on both sides.  Columns of
+// the N side without a token repeat another's, and their sums are dropped.
 //   gate/up   4 gate rows and the 4 up rows of the same features, bf16 tokens: exact products,
 //             f32 sums; silu(gate) up times routing weight in f32
 //   down      16 output columns.  The f32 activations are kept as three bf16 parts that add up
@@ -52,12 +54,12 @@ constexpr int kMaxPairs = kMaxT * 32;
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSlots = 2;          // per warp (the loop's two cursors)
-// gate/up: 4 features' gate and up rows, 1 KB of each; down: 16 rows, 512 bytes of each.  Rows lie
-// 64 bytes off a multiple of 128 apart, so two rows x 64 bytes, a quarter-warp's read, meet all banks once.
+// A slot, in blocks of 128 bytes of a row: gate/up 8 blocks x 4 features' gate rows, then the same of their
+// up rows; down 4 blocks x 16 rows
 constexpr int kFeat = 4;
-constexpr int kGuPiece = 1024, kGuPitch = kGuPiece + 64;
-constexpr int kDnPiece = 512, kDnPitch = kDnPiece + 64;
-constexpr int kSlotBytes = 16 * kDnPitch;
+constexpr int kGuBlocks = 8, kDnBlocks = 4;
+constexpr int kSlotBytes = 8192;
+static_assert(2 * kFeat * kGuBlocks * 128 == kSlotBytes && 16 * kDnBlocks * 128 == kSlotBytes, "slot");
 constexpr unsigned long long kCopyGraceNs = 100000ull;
 constexpr int kRing = kWarps * kSlots * kSlotBytes;
 
@@ -109,11 +111,10 @@ struct Scratch {
   float scores[1];                 // [T][2 E]
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, int row, int block, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(row), "r"(block), "r"(bar)
       : "memory");
 }
 
@@ -325,6 +326,7 @@ template <bool kFp8>
 struct Stream {
   const Params& p;
   const Fixed& f;
+  const CUtensorMap *m13, *m2, *m13s, *m2s;
   int D, warp, lane;
   // gate/up: the CTA's features, all touched experts' in one line: [.., n0 blocks of the first expert,
   // whole experts, ..], `routed` blocks in all, then the shared expert's from s0
@@ -332,7 +334,9 @@ struct Stream {
   // down: output columns [col0, col0 + cols) of the CTA, [row0, row0 + rows) of this warp's row block
   int col0, cols, row_blocks, row0, rows, unit0, unit_step, pieces, units;
 
-  __device__ Stream(const Params& p_, const Fixed& f_, int warp_, int lane_) : p(p_), f(f_), warp(warp_), lane(lane_) {
+  __device__ Stream(const Params& p_, const Fixed& f_, const CUtensorMap* m13_, const CUtensorMap* m2_,
+                    const CUtensorMap* m13s_, const CUtensorMap* m2s_, int warp_, int lane_)
+      : p(p_), f(f_), m13(m13_), m2(m2_), m13s(m13s_), m2s(m2s_), warp(warp_), lane(lane_) {
     D = f.n_groups;
     // a shared expert's bf16 feature beside FP8 ones counts twice
     constexpr unsigned kCost = kFp8 ? 2 : 1;
@@ -365,14 +369,14 @@ struct Stream {
     rows = row_blocks ? cols * (rb_i + 1) / row_blocks - row0 : 0;
     unit0 = row_blocks ? warp / row_blocks : 0;
     unit_step = row_blocks ? (kWarps - 1 - rb_i) / row_blocks + 1 : 1;
-    const int pc = kDnPiece / (kFp8 ? 1 : 2);
-    pieces = (p.I + pc - 1) / pc;
-    units = rows > 0 ? D * pieces + (p.Is + kDnPiece / 2 - 1) / (kDnPiece / 2) : 0;
+    pieces = (p.I + dn_cols(0) - 1) / dn_cols(0);
+    units = rows > 0 ? D * pieces + (p.Is + dn_cols(D) - 1) / dn_cols(D) : 0;
   }
   __device__ bool quant(int d) const { return kFp8 && d < D; }
   __device__ int inner(int d) const { return d < D ? p.I : p.Is; }
-  __device__ int gu_cols(int d) const { return quant(d) ? kGuPiece : kGuPiece / 2; }
-  __device__ int dn_cols(int d) const { return quant(d) ? kDnPiece : kDnPiece / 2; }
+  __device__ int block_cols(int d) const { return quant(d) ? 128 : 64; }       // of 128 bytes
+  __device__ int gu_cols(int d) const { return kGuBlocks * block_cols(d); }    // of a piece
+  __device__ int dn_cols(int d) const { return kDnBlocks * block_cols(d); }
 
   __device__ void locate(Cursor& c) const {
     if (c.phase == 0) {
@@ -405,7 +409,7 @@ struct Stream {
       c.k = (c.i - c.d * pieces) * dn_cols(0);
     } else {
       c.d = D;
-      c.k = (c.i - D * pieces) * (kDnPiece / 2);
+      c.k = (c.i - D * pieces) * dn_cols(D);
     }
   }
   __device__ Cursor begin() const {
@@ -424,34 +428,24 @@ struct Stream {
     }
     locate(c);
   }
-  // the copies of a piece, a row per lane
+  // the copies of a piece (one lane).  Only whole blocks of a row are copied: what is left of it is read
+  // from where it lies.  Rows behind the expert's are read and not used.
   __device__ void issue(const Cursor& c, uint32_t slot, uint32_t bar) const {
     if (c.phase == 2) return;
-    const bool q = quant(c.d);
-    const int I = inner(c.d), esz = q ? 1 : 2;
-    const uint8_t* w;
-    size_t row;
-    int C, n, dst;
-    bool mine;
-    if (c.phase == 0) {
-      w = static_cast<const uint8_t*>(c.d < D ? p.w13 : p.w13s);
-      row = (c.d < D ? static_cast<size_t>(f.expert[c.d]) * 2 * I : 0) + (lane < kFeat ? 0 : I) + c.n + lane % kFeat;
-      C = p.H;
-      n = min(gu_cols(c.d), C - c.k);
-      dst = lane * kGuPitch;
-      mine = lane < 2 * kFeat && lane % kFeat < c.cnt;
-      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * esz * 2 * c.cnt));
-    } else {
-      w = static_cast<const uint8_t*>(c.d < D ? p.w2 : p.w2s);
-      row = (c.d < D ? static_cast<size_t>(f.expert[c.d]) * p.H : 0) + col0 + row0 + lane;
-      C = I;
-      n = min(dn_cols(c.d), C - c.k);
-      dst = lane * kDnPitch;
-      mine = lane < rows;
-      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * esz * rows));
+    const int cols = block_cols(c.d), block = c.k / cols, I = inner(c.d);
+    if (c.k + cols > (c.phase == 0 ? p.H : I)) {
+      ptx::mbar_arrive(bar);
+      return;
     }
-    if (mine)
-      bulk_load(slot + dst, w + (row * C + c.k) * esz, static_cast<uint32_t>(n * esz), bar);
+    ptx::mbar_arrive_expect_tx(bar, kSlotBytes);
+    if (c.phase == 0) {
+      const CUtensorMap* m = c.d < D ? m13 : m13s;
+      const int row = (c.d < D ? f.expert[c.d] * 2 * I : 0) + c.n;
+      box_load(slot, m, row, block, bar);
+      box_load(slot + kSlotBytes / 2, m, row + I, block, bar);
+    } else {
+      box_load(slot, c.d < D ? m2 : m2s, (c.d < D ? f.expert[c.d] * p.H : 0) + col0 + row0, block, bar);
+    }
   }
 };
 
@@ -459,7 +453,7 @@ struct Stream {
 // A's rows g and g + 8, B's token g, and of c rows g (0, 1) and g + 8 (2, 3), tokens 2 q and 2 q + 1.
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -474,121 +468,150 @@ __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
   hi = gemm::pack_bf16x2(__low2float(b), __high2float(b));
 }
 
-// One piece of a block of gate/up: products of 4 features' gate and up rows (MMA rows 0-3 and 4-7,
-// this lane's row and 16-byte column at `at`) with eight of the expert's tokens, added to c.
-// x: this lane's token from the piece's first column, or null; sc: this lane's row's scales from there.
+// two steps' weights of a lane, 16 bytes each, as MMA operands: bf16 for 2 x 16 columns, or codes for 4 x 16
 template <bool kQ>
-__device__ __forceinline__ void gate_up(uint32_t at, int n, int q, const uint4* x, const float* sc, float (&c)[4]) {
-  constexpr int kStep = kQ ? 64 : 32, kBatch = kQ ? 2 : 4;       // columns of a step: 16 bytes of a row per lane
-  float acc[2][4] = {};
-#pragma unroll 1
-  for (int k0 = 0; k0 < n; k0 += kBatch * kStep) {
-    uint4 b[kBatch][kQ ? 2 : 1];
-#pragma unroll
-    for (int s = 0; s < kBatch; ++s)
-#pragma unroll
-      for (int h = 0; h < (kQ ? 2 : 1); ++h) {
-        const int col = k0 + s * kStep + (kQ ? 16 : 8) * q + 8 * h;
-        b[s][h] = x && col < n ? __ldg(x + (col >> 3)) : make_uint4(0, 0, 0, 0);
-      }
-    const float d = kQ ? __ldg(sc + (k0 >> 7)) : 1.0f;           // FP8: a batch is a scale block
-#pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      uint4 w = make_uint4(0, 0, 0, 0);                          // behind the row's end lie stale bytes
-      if (k0 + s * kStep + (kQ ? 16 : 8) * q < n) w = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2));
-      if (kQ) {
-        const uint32_t code[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t lo, hi;
-          widen4(code[j], lo, hi);
-          const uint4& u = b[s][kQ ? j >> 1 : 0];
-          mma(acc[j & 1], lo, 0u, hi, 0u, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
-        }
-      } else {
-        mma(acc[0], w.x, 0u, w.y, 0u, b[s][0].x, b[s][0].y);
-        mma(acc[1], w.z, 0u, w.w, 0u, b[s][0].z, b[s][0].w);
-      }
-    }
+struct Row {
+  uint32_t v[kQ ? 4 : 2][2];       // [MMA][first and second 8 columns]
+  __device__ __forceinline__ explicit Row(const uint4& w) {
     if (kQ) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        c[j] = fmaf(acc[0][j] + acc[1][j], d, c[j]);
-        acc[0][j] = acc[1][j] = 0.0f;
-      }
+      widen4(w.x, v[0][0], v[0][1]);
+      widen4(w.y, v[1][0], v[1][1]);
+      widen4(w.z, v[kQ ? 2 : 0][0], v[kQ ? 2 : 0][1]);
+      widen4(w.w, v[kQ ? 3 : 0][0], v[kQ ? 3 : 0][1]);
+    } else {
+      v[0][0] = w.x;
+      v[0][1] = w.y;
+      v[1][0] = w.z;
+      v[1][1] = w.w;
     }
   }
-  if (!kQ) {
+};
+
+// c[0] += the first MMA's products, c[1] the second's (two sums, two chains)
+template <bool kQ>
+__device__ __forceinline__ void products(float (&c)[2][4], const Row<kQ>& lo, const Row<kQ>* hi, const uint4 (&u)[kQ ? 2 : 1]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) c[j] += acc[0][j] + acc[1][j];
+  for (int j = 0; j < (kQ ? 4 : 2); ++j) {
+    const uint4& b = u[kQ ? j >> 1 : 0];
+    mma(c[j & 1], lo.v[j][0], hi ? hi->v[j][0] : 0u, lo.v[j][1], hi ? hi->v[j][1] : 0u, j & 1 ? b.z : b.x,
+        j & 1 ? b.w : b.y);
   }
 }
 
-// One unit of down: products of 16 output columns' rows (at, 8 rows on) with the three parts of eight
-// tokens' activations, `parts` 16-byte vectors apart.  a: this lane's token, or null.
+// One piece of a block of gate/up: products of 4 features' gate and up rows (MMA rows 0-3 and 4-7)
+// with eight of the expert's tokens, added to c.  at: this lane's row in the slot; x: its token's
+// values of the piece, 16 bytes a vector; w: its weight row of the piece in memory, for what no block
+// holds; sc: its row's scales.  In a block of 128 bytes a lane takes vectors 2 q and 2 q + 1.
 template <bool kQ>
-__device__ __forceinline__ void down(uint32_t at, int n, int q, const uint4* a, size_t parts, const float* sc0,
-                                     const float* sc1, float (&c)[4]) {
-  constexpr int kStep = kQ ? 64 : 32, kHalf = kQ ? 2 : 1, kBatch = kQ ? 2 : 4;
-  float acc[4][4] = {};
-#pragma unroll 1
-  for (int k0 = 0; k0 < n; k0 += kBatch * kStep) {
-    uint4 b[kBatch][3][kHalf];
+__device__ __forceinline__ void gate_up(const uint8_t* at, int n, int g, int q, const uint4* x, const uint8_t* w,
+                                        const float* sc, float (&c)[4]) {
+  constexpr int kCols = kQ ? 128 : 64, kVec = kQ ? 2 : 1;       // of a block; token vectors to a weight vector
+  const int r = g & 3, full = n / kCols;
+  float acc[2][4] = {};
+  auto join = [&](float d) {
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s)
+    for (int j = 0; j < 2; ++j) {
+      c[j] = kQ ? fmaf(acc[0][j] + acc[1][j], d, c[j]) : c[j] + (acc[0][j] + acc[1][j]);
+      acc[0][j] = acc[1][j] = 0.0f;
+    }
+  };
+#pragma unroll(kQ ? 2 : 4)
+  for (int i = 0; i < full; ++i) {
+    uint4 u[2][kVec];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) u[h][v] = __ldg(x + i * (kCols / 8) + (2 * q + h) * kVec + v);
+    const float d = kQ ? __ldg(sc + i) : 1.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const Row<kQ> row(*reinterpret_cast<const uint4*>(at + i * (kFeat * 128) +
+                                                        (((2 * q + h) ^ r ^ ((i & 1) << 2)) << 4)));
+      products<kQ>(acc, row, nullptr, u[h]);
+    }
+    if (kQ) join(d);               // a block is a scale block
+  }
+  if (full * kCols < n) {          // the row's end: vectors behind it are zeros on both sides
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const int col = full * kCols + (2 * q + h) * 8 * kVec;
+      uint4 u[kVec], v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) u[k] = v;
+      if (col < n) {
+        v = __ldg(reinterpret_cast<const uint4*>(w + col * (kQ ? 1 : 2)));
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) u[k] = __ldg(x + (col >> 3) + k);
+      }
+      products<kQ>(acc, Row<kQ>(v), nullptr, u);
+    }
+    if (kQ) join(__ldg(sc + full));
+  }
+  if (!kQ) join(1.0f);
+}
+
+// One unit of down: products of 16 output columns' rows (this lane's rows g and g + 8) with the three
+// parts of eight tokens' activations, `parts` vectors apart, added to c.
+template <bool kQ>
+__device__ __forceinline__ void down(const uint8_t* at, int n, int g, int q, const uint4* a, size_t parts,
+                                     const uint8_t* w0, const uint8_t* w1, const float* sc0, const float* sc1,
+                                     float (&c)[4]) {
+  constexpr int kCols = kQ ? 128 : 64, kVec = kQ ? 2 : 1;
+  const int full = n / kCols;
+  float hi[2][4] = {}, lo[2][4] = {};      // sums of the first parts, and of the smaller ones
+  auto join = [&](float d0, float d1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v = hi[0][j] + hi[1][j] + (lo[0][j] + lo[1][j]);
+      c[j] = kQ ? fmaf(v, j < 2 ? d0 : d1, c[j]) : c[j] + v;
+      hi[0][j] = hi[1][j] = lo[0][j] = lo[1][j] = 0.0f;
+    }
+  };
+#pragma unroll(kQ ? 1 : 2)
+  for (int i = 0; i < full; ++i) {
+    uint4 u[2][3][kVec];                   // written by other SMs before the grid barrier
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int part = 0; part < 3; ++part)
 #pragma unroll
-        for (int h = 0; h < kHalf; ++h) {      // written by other SMs before the grid barrier
-          const int col = k0 + s * kStep + 8 * kHalf * q + 8 * h;
-          b[s][part][h] = a && col < n ? a[part * parts + (col >> 3)] : make_uint4(0, 0, 0, 0);
-        }
-    float d0 = 1.0f, d1 = 1.0f;
-    if (kQ) {                                  // a batch is one scale block
-      d0 = __ldg(sc0 + (k0 >> 7));
-      d1 = __ldg(sc1 + (k0 >> 7));
+        for (int v = 0; v < kVec; ++v) u[h][part][v] = a[part * parts + i * (kCols / 8) + (2 * q + h) * kVec + v];
+    const float d0 = kQ ? __ldg(sc0 + i) : 1.0f, d1 = kQ ? __ldg(sc1 + i) : 1.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* from = at + i * 2048 + (((2 * q + h) ^ g) << 4);
+      const Row<kQ> r0(*reinterpret_cast<const uint4*>(from)), r1(*reinterpret_cast<const uint4*>(from + 1024));
+      products<kQ>(hi, r0, &r1, u[h][0]);
+      products<kQ>(lo, r0, &r1, u[h][1]);
+      products<kQ>(lo, r0, &r1, u[h][2]);
     }
-#pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-      if (k0 + s * kStep + 8 * kHalf * q < n) {
-        w0 = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2));
-        w1 = ptx::ld_shared_v4(at + (k0 + s * kStep) * (kQ ? 1 : 2) + 8 * kDnPitch);
-      }
-      if (kQ) {
-        const uint32_t c0[4] = {w0.x, w0.y, w0.z, w0.w}, c1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t a0, a1, a2, a3;
-          widen4(c0[j], a0, a2);
-          widen4(c1[j], a1, a3);
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint4& u = b[s][part][kQ ? j >> 1 : 0];
-            mma(acc[(part ? 2 : 0) + (j & 1)], a0, a1, a2, a3, j & 1 ? u.z : u.x, j & 1 ? u.w : u.y);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          const uint4& u = b[s][part][0];
-          mma(acc[part ? 2 : 0], w0.x, w1.x, w0.y, w1.y, u.x, u.y);
-          mma(acc[part ? 3 : 1], w0.z, w1.z, w0.w, w1.w, u.z, u.w);
-        }
-      }
-    }
-    if (kQ) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[j] = fmaf(acc[0][j] + acc[1][j] + (acc[2][j] + acc[3][j]), j < 2 ? d0 : d1, c[j]);
-        acc[0][j] = acc[1][j] = acc[2][j] = acc[3][j] = 0.0f;
-      }
-    }
+    if (kQ) join(d0, d1);
   }
-  if (!kQ) {
+  if (full * kCols < n) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const int col = full * kCols + (2 * q + h) * 8 * kVec;
+      uint4 u[3][kVec], v0 = make_uint4(0, 0, 0, 0), v1 = v0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] += acc[0][j] + acc[1][j] + (acc[2][j] + acc[3][j]);
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) u[part][k] = v0;
+      if (col < n) {
+        v0 = __ldg(reinterpret_cast<const uint4*>(w0 + col * (kQ ? 1 : 2)));
+        v1 = __ldg(reinterpret_cast<const uint4*>(w1 + col * (kQ ? 1 : 2)));
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) u[part][k] = a[part * parts + (col >> 3) + k];
+      }
+      const Row<kQ> r0(v0), r1(v1);
+      products<kQ>(hi, r0, &r1, u[0]);
+      products<kQ>(lo, r0, &r1, u[1]);
+      products<kQ>(lo, r0, &r1, u[2]);
+    }
+    if (kQ) join(__ldg(sc0 + full), __ldg(sc1 + full));
   }
+  if (!kQ) join(1.0f, 1.0f);
 }
 
 __device__ __forceinline__ void swap4(float (&a)[4], float (&b)[4]) {
@@ -611,11 +634,12 @@ __device__ __forceinline__ void cut3(float v, uint16_t (&part)[3]) {
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
-layer_few_kernel(const Params p) {
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  Fixed& f = *reinterpret_cast<Fixed*>(smem_raw);
-  constexpr uint32_t kRingAt = (sizeof(Fixed) + 127u) & ~127u;
-  uint8_t* slots = smem_raw + kRingAt;
+layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant__ CUtensorMap m2,
+                 const __grid_constant__ CUtensorMap m13s, const __grid_constant__ CUtensorMap m2s, const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // the ring at a multiple of 1024 bytes, the swizzle's period, the fixed part behind it
+  uint8_t* slots = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
+  Fixed& f = *reinterpret_cast<Fixed*>(slots + kRing);
   Scratch& x = *reinterpret_cast<Scratch*>(slots);
   volatile int* abort_flag = &f.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -623,7 +647,11 @@ layer_few_kernel(const Params p) {
 
   count_launch(p.launches, MOE_KID_LAYER_FEW);
   if (lane < kSlots) ptx::mbar_init(ptx::smem_u32(&f.full[warp][lane]), 1);
-  if (tid == 0) f.abort_flag = 0;
+  if (tid == 0) {
+    f.abort_flag = 0;
+    ptx::tma_prefetch_desc(&m13);
+    ptx::tma_prefetch_desc(&m2);
+  }
   ptx::fence_mbar_init();
   for (int e = tid; e < E; e += kThreads) x.mask[e] = 0u;
   grid_dep_wait();
@@ -679,13 +707,13 @@ layer_few_kernel(const Params p) {
 
   // ---- the experts.  One loop over the pieces of both phases, so that their code is there once:
   // wait for the slot, multiply, refill the slot
-  const Stream<kFp8> st(p, f, warp, lane);
+  const Stream<kFp8> st(p, f, &m13, &m2, &m13s, &m2s, warp, lane);
   const int D = st.D, g = lane >> 2, q = lane & 3;
   const uint32_t ring = ptx::smem_u32(slots) + warp * kSlots * kSlotBytes, bars = ptx::smem_u32(&f.full[warp][0]);
   Cursor c[kSlots], ahead = st.begin();          // of the pieces in the slots, the oldest first
 #pragma unroll 1
   for (int s = 0; s < kSlots; ++s) {
-    st.issue(ahead, ring + s * kSlotBytes, bars + 8 * s);
+    if (lane == 0) st.issue(ahead, ring + s * kSlotBytes, bars + 8 * s);
     c[0] = c[1];
     c[1] = ahead;
     if (ahead.phase < 2) st.next(ahead);
@@ -699,22 +727,27 @@ layer_few_kernel(const Params p) {
     while (c[0].phase == phase) {
       const int d = c[0].d, k = c[0].k, first = f.first[d], I = st.inner(d);
       const bool quant = st.quant(d), shared = d == D;
-      const uint32_t at = ring + s * kSlotBytes + q * 16;
+      const uint8_t* at = slots + (warp * kSlots + s) * kSlotBytes;
       const bool landed = __all_sync(0xffffffffu, wait(bars + 8 * s, parity, abort_flag, p));
       if (phase == 0) {
         const int n = min(st.gu_cols(d), H - k), n_tok = f.first[d + 1] - first;
+        // this lane's row: feature g & 3, gate or up
+        const int row = (g < kFeat ? 0 : I) + min(c[0].n + (g & 3), I - 1);
+        const size_t in = (shared ? 0 : static_cast<size_t>(f.expert[d]) * 2 * I) + row;
+        const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w13s) : p.w13) +
+                           (in * H + k) * (quant ? 1 : 2);
         const float* sc = nullptr;
-        if (kFp8 && quant) {                     // scales of this lane's row: feature g & 3, gate or up
-          const int nblk = (H + 127) >> 7, row = (g < kFeat ? 0 : I) + min(c[0].n + (g & 3), I - 1);
+        if (kFp8 && quant) {
+          const int nblk = (H + 127) >> 7;
           sc = p.s13 + (static_cast<size_t>(f.expert[d]) * ((2 * I + 127) >> 7) + (row >> 7)) * nblk + (k >> 7);
         }
+        const uint8_t* mine = at + (g >> 2) * (kSlotBytes / 2) + (g & 3) * 128;
 #pragma unroll 1
         for (int i0 = 0; i0 < n_tok; i0 += 8) {
-          const uint4* xt = i0 + g < n_tok ? reinterpret_cast<const uint4*>(
-                                                 p.x + static_cast<size_t>(f.token[first + i0 + g]) * H + k)
-                                           : nullptr;
-          if (kFp8 && quant) gate_up<kFp8>(at + g * kGuPitch, n, q, xt, sc, cur);
-          else gate_up<false>(at + g * kGuPitch, n, q, xt, sc, cur);
+          const uint4* xt = reinterpret_cast<const uint4*>(
+              p.x + static_cast<size_t>(f.token[first + min(i0 + g, n_tok - 1)]) * H + k);
+          if (kFp8 && quant) gate_up<kFp8>(mine, n, g, q, xt, w, sc, cur);
+          else gate_up<false>(mine, n, g, q, xt, w, sc, cur);
           if (n_tok > 8) swap4(cur, other);
         }
         if (k + n == H) {
@@ -749,25 +782,29 @@ layer_few_kernel(const Params p) {
         const uint32_t tokens = f.tokens[d];
         const size_t step = (static_cast<size_t>(shared ? T : T * K) * I) >> 3;
         const uint16_t* act = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) + k;
+        // this lane's rows
+        const int r0 = min(st.col0 + st.row0 + g, H - 1), r1 = min(r0 + 8, H - 1);
+        const size_t in = shared ? 0 : static_cast<size_t>(f.expert[d]) * H;
+        const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w2s) : p.w2);
+        const uint8_t *w0 = w + ((in + r0) * I + k) * (quant ? 1 : 2), *w1 = w + ((in + r1) * I + k) * (quant ? 1 : 2);
         const float *sc0 = nullptr, *sc1 = nullptr;
         if (kFp8 && quant) {
-          const int nblk = (I + 127) >> 7, r = st.col0 + st.row0 + g;
+          const int nblk = (I + 127) >> 7;
           const float* s2 = p.s2 + static_cast<size_t>(f.expert[d]) * ((H + 127) >> 7) * nblk + (k >> 7);
-          sc0 = s2 + static_cast<size_t>(min(r, H - 1) >> 7) * nblk;
-          sc1 = s2 + static_cast<size_t>(min(r + 8, H - 1) >> 7) * nblk;
+          sc0 = s2 + static_cast<size_t>(r0 >> 7) * nblk;
+          sc1 = s2 + static_cast<size_t>(r1 >> 7) * nblk;
         }
 #pragma unroll 1
         for (int t0 = 0; t0 < 16; t0 += 8) {
           if (tokens >> t0 & 0xFFu) {
             const int t = t0 + g;
-            const uint4* a = nullptr;
-            if (tokens >> t & 1u) {
-              const int row = shared ? t : f.pair[first + __popc(tokens & ((1u << t) - 1u))];
-              a = reinterpret_cast<const uint4*>(act + static_cast<size_t>(row) * I);
-            }
+            // a token without the expert repeats the expert's first
+            const int i = tokens >> t & 1u ? __popc(tokens & ((1u << t) - 1u)) : 0;
+            const uint4* a =
+                reinterpret_cast<const uint4*>(act + static_cast<size_t>(shared ? f.token[first + i] : f.pair[first + i]) * I);
             float v[4] = {};
-            if (kFp8 && quant) down<kFp8>(at + g * kDnPitch, n, q, a, step, sc0, sc1, v);
-            else down<false>(at + g * kDnPitch, n, q, a, step, sc0, sc1, v);
+            if (kFp8 && quant) down<kFp8>(at + g * 128, n, g, q, a, step, w0, w1, sc0, sc1, v);
+            else down<false>(at + g * 128, n, g, q, a, step, w0, w1, sc0, sc1, v);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (tokens >> (t0 + 2 * q + (j & 1)) & 1u) cur[j] += v[j];
@@ -776,7 +813,7 @@ layer_few_kernel(const Params p) {
         }
       }
       __syncwarp();                              // all lanes have read the slot
-      if (landed) st.issue(ahead, ring + s * kSlotBytes, bars + 8 * s);
+      if (landed && lane == 0) st.issue(ahead, ring + s * kSlotBytes, bars + 8 * s);
       c[0] = c[1];
       c[1] = ahead;
       if (ahead.phase < 2) st.next(ahead);
@@ -894,6 +931,14 @@ int check(const char* op, const Params& p, bool fp8, const void* workspace, size
   return MOE_OK;
 }
 
+// rows of `cols` bf16 values or codes as [128 bytes][rows][blocks along a row]
+int make_map(CUtensorMap* m, const void* base, bool codes, int rows, int cols, int box_rows, int box_blocks,
+             const char* op, const char* what) {
+  const int n = codes ? 128 : 64;
+  if (cols < n) return MOE_OK;
+  return gemm::make_tmap_blocks(m, base, codes, rows, cols, n, box_rows, box_blocks, op, what);
+}
+
 template <bool kFp8>
 int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   const Layout l = layout_of(p.T, p.I, p.E, p.K, p.Is);
@@ -905,7 +950,7 @@ int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   const int ctas = sm_count();
   if (p.H > 16ll * kWarps * ctas)      // row blocks of the down product: a warp has one
     return set_error(MOE_ERR_CUDA, "%s: H=%d on %d SMs", op, p.H, ctas);
-  constexpr int kFixed = (static_cast<int>(sizeof(Fixed)) + 127) & ~127, kSmem = kFixed + kRing;
+  constexpr int kSmem = kRing + static_cast<int>(sizeof(Fixed)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(sizeof(Scratch) + 2 * kMaxT * kMaxE * 4 <= kRing && kWarps * 1024 <= kRing, "what the ring holds besides");
   auto kern = layer_few_kernel<kFp8>;
@@ -926,11 +971,23 @@ int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   p.status = diag.status;
   p.launches = diag.launches;
   p.wait_ns = gemm::pipeline_wait_ns();
+  // a map without a whole block of 128 bytes is never used
+  CUtensorMap m13{}, m2{}, m13s{}, m2s{};
+  int rc;
+  const int E2I = p.E * 2 * p.I, EH = p.E * p.H;
+  if ((rc = make_map(&m13, p.w13, kFp8, E2I, p.H, kFeat, kGuBlocks, op, "w13")) != MOE_OK) return rc;
+  if ((rc = make_map(&m2, p.w2, kFp8, EH, p.I, 16, kDnBlocks, op, "w2")) != MOE_OK) return rc;
+  if (p.Is > 0) {
+    if ((rc = make_map(&m13s, p.w13s, false, 2 * p.Is, p.H, kFeat, kGuBlocks, op, "w13_shared")) != MOE_OK) return rc;
+    if ((rc = make_map(&m2s, p.w2s, false, p.H, p.Is, 16, kDnBlocks, op, "w2_shared")) != MOE_OK) return rc;
+  }
   // cooperative: the CTAs wait for one another, so all of them start together or none does
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
-  return launch_status(launch_kernel(kern, dim3(ctas), dim3(kThreads), kSmem, stream, attr, 1, p), op);
+  return launch_status(launch_kernel(kern, dim3(ctas), dim3(kThreads), kSmem, stream, attr, 1, m13, m2, m13s, m2s,
+                                     p),
+                       op);
 }
 
 }  // namespace
