@@ -26,11 +26,11 @@
 // instructions per byte of weights.  Weight rows are the M side, tokens the N side; a lane reads 16 bytes of a row
 // and the same columns of a token, which permutes the columns of a step alike on both sides.  Columns of
 // the N side without a token repeat another's, and their sums are dropped.
-//   gate/up   4 gate rows and the 4 up rows of the same features, bf16 tokens: exact products,
-//             f32 sums; silu(gate) up times routing weight in f32
+//   gate/up   4 gate rows and the 4 up rows of the same features at two places of the contraction, against
+//             four tokens at the same two: exact products, f32 sums; silu(gate) up times routing weight in f32
 //   down      16 output columns.  The f32 activations are kept as three bf16 parts that add up
-//             to them (8 bits each, rounded to nearest, 24 in all), so their products stay exact too;
-//             a token's sums over its experts never leave the registers.
+//             to them (8 bits each, rounded to nearest, 24 in all), so their products stay exact too; two
+//             tokens' parts are six columns.  A token's sums over its experts never leave the registers.
 // FP8 weights are widened to bf16, exactly, and a block's sums take its scale in f32.
 // All sums are f32 in a fixed order, nothing between the weights and the output is narrowed, and
 // no atomics touch data.
@@ -487,140 +487,132 @@ struct Row {
   }
 };
 
-// c[0] += the first MMA's products, c[1] the second's (two sums, two chains)
+// c[0] += the first MMAs' products, c[1] the second's (two sums, two chains): rows 0-7 lo, 8-15 hi
 template <bool kQ>
-__device__ __forceinline__ void products(float (&c)[2][4], const Row<kQ>& lo, const Row<kQ>* hi, const uint4 (&u)[kQ ? 2 : 1]) {
+__device__ __forceinline__ void products(float (&c)[2][4], const Row<kQ>& lo, const Row<kQ>& hi, const uint4 (&u)[kQ ? 2 : 1]) {
 #pragma unroll
   for (int j = 0; j < (kQ ? 4 : 2); ++j) {
     const uint4& b = u[kQ ? j >> 1 : 0];
-    mma(c[j & 1], lo.v[j][0], hi ? hi->v[j][0] : 0u, lo.v[j][1], hi ? hi->v[j][1] : 0u, j & 1 ? b.z : b.x,
-        j & 1 ? b.w : b.y);
+    mma(c[j & 1], lo.v[j][0], hi.v[j][0], lo.v[j][1], hi.v[j][1], j & 1 ? b.z : b.x, j & 1 ? b.w : b.y);
   }
 }
-
-// One piece of a block of gate/up: products of 4 features' gate and up rows (MMA rows 0-3 and 4-7)
-// with eight of the expert's tokens, added to c.  at: this lane's row in the slot; x: its token's
-// values of the piece, 16 bytes a vector; w: its weight row of the piece in memory, for what no block
-// holds; sc: its row's scales.  In a block of 128 bytes a lane takes vectors 2 q and 2 q + 1.
+// c += the two sums, with FP8 times the scales of rows 0-7 and 8-15; and clears them
 template <bool kQ>
-__device__ __forceinline__ void gate_up(const uint8_t* at, int n, int g, int q, const uint4* x, const uint8_t* w,
-                                        const float* sc, float (&c)[4]) {
-  constexpr int kCols = kQ ? 128 : 64, kVec = kQ ? 2 : 1;       // of a block; token vectors to a weight vector
-  const int r = g & 3, full = n / kCols;
-  float acc[2][4] = {};
-  auto join = [&](float d) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      c[j] = kQ ? fmaf(acc[0][j] + acc[1][j], d, c[j]) : c[j] + (acc[0][j] + acc[1][j]);
-      acc[0][j] = acc[1][j] = 0.0f;
-    }
-  };
-#pragma unroll(kQ ? 2 : 4)
-  for (int i = 0; i < full; ++i) {
-    uint4 u[2][kVec];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int v = 0; v < kVec; ++v) u[h][v] = __ldg(x + i * (kCols / 8) + (2 * q + h) * kVec + v);
-    const float d = kQ ? __ldg(sc + i) : 1.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const Row<kQ> row(*reinterpret_cast<const uint4*>(at + i * (kFeat * 128) +
-                                                        (((2 * q + h) ^ r ^ ((i & 1) << 2)) << 4)));
-      products<kQ>(acc, row, nullptr, u[h]);
-    }
-    if (kQ) join(d);               // a block is a scale block
-  }
-  if (full * kCols < n) {          // the row's end: vectors behind it are zeros on both sides
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const int col = full * kCols + (2 * q + h) * 8 * kVec;
-      uint4 u[kVec], v = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) u[k] = v;
-      if (col < n) {
-        v = __ldg(reinterpret_cast<const uint4*>(w + col * (kQ ? 1 : 2)));
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) u[k] = __ldg(x + (col >> 3) + k);
-      }
-      products<kQ>(acc, Row<kQ>(v), nullptr, u);
-    }
-    if (kQ) join(__ldg(sc + full));
-  }
-  if (!kQ) join(1.0f);
-}
-
-// One unit of down: products of 16 output columns' rows (this lane's rows g and g + 8) with the three
-// parts of eight tokens' activations, `parts` vectors apart, added to c.
-template <bool kQ>
-__device__ __forceinline__ void down(const uint8_t* at, int n, int g, int q, const uint4* a, size_t parts,
-                                     const uint8_t* w0, const uint8_t* w1, const float* sc0, const float* sc1,
-                                     float (&c)[4]) {
-  constexpr int kCols = kQ ? 128 : 64, kVec = kQ ? 2 : 1;
-  const int full = n / kCols;
-  float hi[2][4] = {}, lo[2][4] = {};      // sums of the first parts, and of the smaller ones
-  auto join = [&](float d0, float d1) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float v = hi[0][j] + hi[1][j] + (lo[0][j] + lo[1][j]);
-      c[j] = kQ ? fmaf(v, j < 2 ? d0 : d1, c[j]) : c[j] + v;
-      hi[0][j] = hi[1][j] = lo[0][j] = lo[1][j] = 0.0f;
-    }
-  };
-#pragma unroll(kQ ? 1 : 2)
-  for (int i = 0; i < full; ++i) {
-    uint4 u[2][3][kVec];                   // written by other SMs before the grid barrier
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int part = 0; part < 3; ++part)
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) u[h][part][v] = a[part * parts + i * (kCols / 8) + (2 * q + h) * kVec + v];
-    const float d0 = kQ ? __ldg(sc0 + i) : 1.0f, d1 = kQ ? __ldg(sc1 + i) : 1.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* from = at + i * 2048 + (((2 * q + h) ^ g) << 4);
-      const Row<kQ> r0(*reinterpret_cast<const uint4*>(from)), r1(*reinterpret_cast<const uint4*>(from + 1024));
-      products<kQ>(hi, r0, &r1, u[h][0]);
-      products<kQ>(lo, r0, &r1, u[h][1]);
-      products<kQ>(lo, r0, &r1, u[h][2]);
-    }
-    if (kQ) join(d0, d1);
-  }
-  if (full * kCols < n) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      const int col = full * kCols + (2 * q + h) * 8 * kVec;
-      uint4 u[3][kVec], v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-#pragma unroll
-      for (int part = 0; part < 3; ++part)
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) u[part][k] = v0;
-      if (col < n) {
-        v0 = __ldg(reinterpret_cast<const uint4*>(w0 + col * (kQ ? 1 : 2)));
-        v1 = __ldg(reinterpret_cast<const uint4*>(w1 + col * (kQ ? 1 : 2)));
-#pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int k = 0; k < kVec; ++k) u[part][k] = a[part * parts + (col >> 3) + k];
-      }
-      const Row<kQ> r0(v0), r1(v1);
-      products<kQ>(hi, r0, &r1, u[0]);
-      products<kQ>(lo, r0, &r1, u[1]);
-      products<kQ>(lo, r0, &r1, u[2]);
-    }
-    if (kQ) join(__ldg(sc0 + full), __ldg(sc1 + full));
-  }
-  if (!kQ) join(1.0f, 1.0f);
-}
-
-__device__ __forceinline__ void swap4(float (&a)[4], float (&b)[4]) {
+__device__ __forceinline__ void join(float (&sum)[2][4], float lo, float hi, float (&c)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float t = a[j];
-    a[j] = b[j];
-    b[j] = t;
+    const float v = sum[0][j] + sum[1][j];
+    c[j] = kQ ? fmaf(v, j < 2 ? lo : hi, c[j]) : c[j] + v;
+    sum[0][j] = sum[1][j] = 0.0f;
   }
+}
+
+// A lane's token values of a piece: in each of four blocks of 128 bytes of weights vectors 2 q and 2 q + 1.
+// x: the token's values of the piece's first of the four blocks, 16 bytes a vector; `full` of them are
+// whole (the others' products are with zeros).  All loads are in flight together: they are the latency of a
+// piece (680 cycles from L2; in turn with the multiplications four times that).
+template <bool kQ>
+struct Tokens {
+  static constexpr int kVec = kQ ? 2 : 1;        // token vectors to a weight vector
+  uint4 u[4][2][kVec];
+  template <bool kFinal>                         // not written while the kernel runs
+  __device__ __forceinline__ void load(const uint4* x, int q, int full) {
+    x += 2 * q * kVec;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          const uint4* from = x + (i * 8 + h) * kVec + v;
+          u[i][h][v] = i < full ? (kFinal ? __ldg(from) : *from) : make_uint4(0, 0, 0, 0);
+        }
+  }
+};
+
+// One piece of a block of gate/up for four of the expert's tokens, added to c.  The 8 rows (4 features'
+// gate rows, then their up rows) fill both halves of the MMA's rows, its first with the blocks 0-3 of 128
+// bytes of the piece, its second with 4-7; the MMA's columns 0-3 are the tokens at the first blocks'
+// columns, 4-7 the same tokens at the second's.  What counts of c is rows 0-7 of columns 0-3 and rows
+// 8-15 of columns 4-7.  at: this lane's row in the slot; sc: its row's scales.
+template <bool kQ>
+__device__ __forceinline__ void gate_up(const uint8_t* at, int r, int q, const Tokens<kQ>& x, const float* sc, int full,
+                                        float (&c)[4]) {
+  float sum[2][4] = {};
+  float d[8];
+  if (kQ) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = __ldg(sc + min(i, full - 1));
+  }
+  at += ((2 * q) ^ r) << 4;                      // vector 2 q; 2 q + 1 is 16 bytes to either side
+  const int odd = (r & 1) ? -16 : 16, turned = ((2 * q) ^ r) & 4 ? -64 : 64;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // the swizzle turns vectors 0-3 and 4-7 round in every second block
+      const uint8_t* v = at + (i & 1 ? turned : 0) + (h ? odd : 0) + i * (kFeat * 128);
+      products<kQ>(sum, Row<kQ>(*reinterpret_cast<const uint4*>(v)),
+                   Row<kQ>(*reinterpret_cast<const uint4*>(v + 4 * kFeat * 128)), x.u[i][h]);
+    }
+    if (kQ) join<kQ>(sum, d[i], d[i + 4], c);    // a block is a scale block
+  }
+  if (!kQ) join<kQ>(sum, 1.0f, 1.0f, c);
+}
+
+// One unit of down for two of the expert's tokens, added to c: 16 output columns' rows (this lane's rows
+// g and g + 8); the MMA's columns 2 j and 2 j + 1 are the two tokens' part j.
+template <bool kQ>
+__device__ __forceinline__ void down(const uint8_t* at, int g, int q, const Tokens<kQ>& x, const float* sc0,
+                                     const float* sc1, int full, float (&c)[4]) {
+  float sum[2][4] = {};
+  float d[2][4];
+  if (kQ) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      d[0][i] = __ldg(sc0 + min(i, full - 1));
+      d[1][i] = __ldg(sc1 + min(i, full - 1));
+    }
+  }
+  at += ((2 * q) ^ g) << 4;
+  const int odd = (g & 1) ? -16 : 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* v = at + (h ? odd : 0) + i * 2048;
+      products<kQ>(sum, Row<kQ>(*reinterpret_cast<const uint4*>(v)), Row<kQ>(*reinterpret_cast<const uint4*>(v + 1024)),
+                   x.u[i][h]);
+    }
+    if (kQ) join<kQ>(sum, d[0][i], d[1][i], c);
+  }
+  if (!kQ) join<kQ>(sum, 1.0f, 1.0f, c);
+}
+
+// The end of a row that fills no block, read from where it lies: MMA rows 0-7 from w0, 8-15 from w1 (or
+// zeros), scales there; x: the lane's token from the same column on.  n columns.
+template <bool kQ, bool kFinal>
+__device__ __noinline__ void row_end(const uint8_t* w0, const uint8_t* w1, const uint4* x, int n, int q, float d0, float d1,
+                                     float* c) {
+  constexpr int kVec = kQ ? 2 : 1;
+  float sum[2][4] = {}, add[4] = {};
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const int col = (2 * q + h) * 8 * kVec;
+    uint4 u[kVec], v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) u[k] = v0;
+    if (col < n) {                               // vectors behind the end are zeros on both sides
+      v0 = __ldg(reinterpret_cast<const uint4*>(w0 + col * (kQ ? 1 : 2)));
+      if (w1) v1 = __ldg(reinterpret_cast<const uint4*>(w1 + col * (kQ ? 1 : 2)));
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) u[k] = kFinal ? __ldg(x + (col >> 3) + k) : x[(col >> 3) + k];
+    }
+    products<kQ>(sum, Row<kQ>(v0), Row<kQ>(v1), u);
+  }
+  join<kQ>(sum, d0, d1, add);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] += add[j];
 }
 
 // v as three bf16 parts that add up to it (an infinity or NaN as its first part alone)
@@ -720,96 +712,165 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
   }
   int s = 0;
   uint32_t parity = 0;
-  float cur[4] = {}, other[4] = {};              // sums of tokens 0-7 and 8-15 (gate/up: of the expert's)
+  // gate/up: sums of the expert's tokens, four by four; down: of tokens 0-7 and 8-15
+  float sum[4][4] = {};
+  auto turn = [&]() {                            // the next four's sums first
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float t = sum[0][j];
+      sum[0][j] = sum[1][j];
+      sum[1][j] = sum[2][j];
+      sum[2][j] = sum[3][j];
+      sum[3][j] = t;
+    }
+  };
 #pragma unroll 1
   for (int phase = 0; phase < 2; ++phase) {
 #pragma unroll 1
     while (c[0].phase == phase) {
-      const int d = c[0].d, k = c[0].k, first = f.first[d], I = st.inner(d);
+      const int d = c[0].d, k = c[0].k, first = f.first[d], n_tok = f.first[d + 1] - first, I = st.inner(d);
       const bool quant = st.quant(d), shared = d == D;
+      const int expert = shared ? 0 : f.expert[d];
       const uint8_t* at = slots + (warp * kSlots + s) * kSlotBytes;
-      const bool landed = __all_sync(0xffffffffu, wait(bars + 8 * s, parity, abort_flag, p));
+      bool landed = false, waited = false;
+      auto take = [&]() {
+        if (!waited) landed = __all_sync(0xffffffffu, wait(bars + 8 * s, parity, abort_flag, p));
+        waited = true;
+      };
+      const int cols = st.block_cols(d);
       if (phase == 0) {
-        const int n = min(st.gu_cols(d), H - k), n_tok = f.first[d + 1] - first;
+        const int n = min(kGuBlocks * cols, H - k), full = n / cols;
         // this lane's row: feature g & 3, gate or up
         const int row = (g < kFeat ? 0 : I) + min(c[0].n + (g & 3), I - 1);
-        const size_t in = (shared ? 0 : static_cast<size_t>(f.expert[d]) * 2 * I) + row;
-        const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w13s) : p.w13) +
-                           (in * H + k) * (quant ? 1 : 2);
         const float* sc = nullptr;
-        if (kFp8 && quant) {
-          const int nblk = (H + 127) >> 7;
-          sc = p.s13 + (static_cast<size_t>(f.expert[d]) * ((2 * I + 127) >> 7) + (row >> 7)) * nblk + (k >> 7);
-        }
+        if (kFp8 && quant)
+          sc = p.s13 + (expert * ((2 * I + 127) >> 7) + (row >> 7)) * static_cast<size_t>((H + 127) >> 7) + (k >> 7);
         const uint8_t* mine = at + (g >> 2) * (kSlotBytes / 2) + (g & 3) * 128;
+        const int fours = n_tok > 4 ? 4 : 1;     // of tokens, in the sums' four places
 #pragma unroll 1
-        for (int i0 = 0; i0 < n_tok; i0 += 8) {
-          const uint4* xt = reinterpret_cast<const uint4*>(
-              p.x + static_cast<size_t>(f.token[first + min(i0 + g, n_tok - 1)]) * H + k);
-          if (kFp8 && quant) gate_up<kFp8>(mine, n, g, q, xt, w, sc, cur);
-          else gate_up<false>(mine, n, g, q, xt, w, sc, cur);
-          if (n_tok > 8) swap4(cur, other);
+        for (int i0 = 0; i0 < 4 * fours; i0 += 4) {
+          if (i0 < n_tok) {
+            const uint16_t* x = p.x + static_cast<size_t>(f.token[first + min(i0 + (g & 3), n_tok - 1)]) * H + k;
+            const uint4* xf = reinterpret_cast<const uint4*>(x + (g >> 2) * 4 * cols);
+            if (kFp8 && quant) {
+              Tokens<kFp8> u;
+              u.template load<true>(xf, q, full - (g >> 2) * 4);
+              take();
+              if (full > 0) gate_up<kFp8>(mine, g & 3, q, u, sc, full, sum[0]);
+            } else {
+              Tokens<false> u;
+              u.template load<true>(xf, q, full - (g >> 2) * 4);
+              take();
+              if (full > 0) gate_up<false>(mine, g & 3, q, u, sc, full, sum[0]);
+            }
+            if (full * cols < n) {
+              const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w13s) : p.w13);
+              w += ((static_cast<size_t>(expert) * 2 * I + row) * H + k + full * cols) * (quant ? 1 : 2);
+              const uint4* xe = reinterpret_cast<const uint4*>(x + full * cols);
+              float add[4] = {};
+              if (kFp8 && quant) row_end<kFp8, true>(w, nullptr, xe, n - full * cols, q, __ldg(sc + full), 0.0f, add);
+              else row_end<false, true>(w, nullptr, xe, n - full * cols, q, 1.0f, 1.0f, add);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sum[0][j] += add[j];
+            }
+          }
+          if (fours > 1) turn();
         }
         if (k + n == H) {
           // the features' last piece: silu(gate) up, weighted, in parts for the down product
 #pragma unroll 1
-          for (int i0 = 0; i0 < n_tok; i0 += 8) {
+          for (int i0 = 0; i0 < 4 * fours; i0 += 4) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float gate = cur[j], up = __shfl_down_sync(0xffffffffu, gate, 4 * kFeat);
+              // both halves of the columns; then lanes q < 2 hold tokens 2 q + j of rows g
+              const float v = sum[0][j] + __shfl_xor_sync(0xffffffffu, sum[0][2 + j], 2);
+              const float up = __shfl_down_sync(0xffffffffu, v, 4 * kFeat);
               const int i = i0 + 2 * q + j;
-              if (g < c[0].cnt && i < n_tok) {   // cnt <= 4: rows 0-3
-                const int pair = f.pair[first + i], tok = f.token[first + i], row = shared ? tok : pair;
-                const float a = gate / (1.0f + __expf(-gate)) * up * (shared ? f.gate[tok] : f.weight[pair]);
+              if (q < 2 && g < c[0].cnt && i < n_tok) {          // cnt <= 4: gate rows
+                const int pair = f.pair[first + i], tok = f.token[first + i], to_row = shared ? tok : pair;
+                const float a = v / (1.0f + __expf(-v)) * up * (shared ? f.gate[tok] : f.weight[pair]);
                 uint16_t part[3];
                 cut3(a, part);
                 const size_t step = static_cast<size_t>(shared ? T : T * K) * I;
                 uint16_t* to = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) +
-                               static_cast<size_t>(row) * I + c[0].n + g;
+                               static_cast<size_t>(to_row) * I + c[0].n + g;
                 to[0] = part[0];
                 to[step] = part[1];
                 to[2 * step] = part[2];
               }
             }
-            if (n_tok > 8) swap4(cur, other);
+            if (fours > 1) turn();
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) cur[j] = other[j] = 0.0f;
+          for (int j = 0; j < 4; ++j) sum[0][j] = sum[1][j] = sum[2][j] = sum[3][j] = 0.0f;
         }
       } else {
-        // tokens that did not choose the expert take nothing from it, not even a product with zero
-        const int n = min(st.dn_cols(d), I - k);
-        const uint32_t tokens = f.tokens[d];
-        const size_t step = (static_cast<size_t>(shared ? T : T * K) * I) >> 3;
-        const uint16_t* act = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) + k;
+        const int n = min(kDnBlocks * cols, I - k), full = n / cols;
         // this lane's rows
         const int r0 = min(st.col0 + st.row0 + g, H - 1), r1 = min(r0 + 8, H - 1);
-        const size_t in = shared ? 0 : static_cast<size_t>(f.expert[d]) * H;
-        const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w2s) : p.w2);
-        const uint8_t *w0 = w + ((in + r0) * I + k) * (quant ? 1 : 2), *w1 = w + ((in + r1) * I + k) * (quant ? 1 : 2);
         const float *sc0 = nullptr, *sc1 = nullptr;
         if (kFp8 && quant) {
-          const int nblk = (I + 127) >> 7;
-          const float* s2 = p.s2 + static_cast<size_t>(f.expert[d]) * ((H + 127) >> 7) * nblk + (k >> 7);
-          sc0 = s2 + static_cast<size_t>(r0 >> 7) * nblk;
-          sc1 = s2 + static_cast<size_t>(r1 >> 7) * nblk;
+          const size_t nblk = (I + 127) >> 7;
+          const float* s2 = p.s2 + expert * ((H + 127) >> 7) * nblk + (k >> 7);
+          sc0 = s2 + (r0 >> 7) * nblk;
+          sc1 = s2 + (r1 >> 7) * nblk;
         }
+        const uint16_t* act = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) +
+                              min(g >> 1, 2) * (static_cast<size_t>(shared ? T : T * K) * I) + k;
 #pragma unroll 1
-        for (int t0 = 0; t0 < 16; t0 += 8) {
-          if (tokens >> t0 & 0xFFu) {
-            const int t = t0 + g;
-            // a token without the expert repeats the expert's first
-            const int i = tokens >> t & 1u ? __popc(tokens & ((1u << t) - 1u)) : 0;
-            const uint4* a =
-                reinterpret_cast<const uint4*>(act + static_cast<size_t>(shared ? f.token[first + i] : f.pair[first + i]) * I);
-            float v[4] = {};
-            if (kFp8 && quant) down<kFp8>(at + g * 128, n, g, q, a, step, w0, w1, sc0, sc1, v);
-            else down<false>(at + g * 128, n, g, q, a, step, w0, w1, sc0, sc1, v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (tokens >> (t0 + 2 * q + (j & 1)) & 1u) cur[j] += v[j];
+        for (int i0 = 0; i0 < n_tok; i0 += 2) {
+          const int i = first + min(i0 + (g & 1), n_tok - 1);
+          const uint16_t* a = act + static_cast<size_t>(shared ? f.token[i] : f.pair[i]) * I;
+          float v[4] = {};
+          if (kFp8 && quant) {
+            Tokens<kFp8> u;
+            u.template load<false>(reinterpret_cast<const uint4*>(a), q, full);
+            take();
+            if (full > 0) down<kFp8>(at + g * 128, g, q, u, sc0, sc1, full, v);
+          } else {
+            Tokens<false> u;
+            u.template load<false>(reinterpret_cast<const uint4*>(a), q, full);
+            take();
+            if (full > 0) down<false>(at + g * 128, g, q, u, sc0, sc1, full, v);
           }
-          swap4(cur, other);
+          if (full * cols < n) {
+            const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w2s) : p.w2);
+            const int esz = quant ? 1 : 2, at_col = k + full * cols;
+            const uint8_t* w0 = w + ((static_cast<size_t>(expert) * H + r0) * I + at_col) * esz;
+            const uint8_t* w1 = w + ((static_cast<size_t>(expert) * H + r1) * I + at_col) * esz;
+            const uint4* ae = reinterpret_cast<const uint4*>(a + full * cols);
+            float add[4] = {};
+            if (kFp8 && quant)
+              row_end<kFp8, false>(w0, w1, ae, n - full * cols, q, __ldg(sc0 + full), __ldg(sc1 + full), add);
+            else
+              row_end<false, false>(w0, w1, ae, n - full * cols, q, 1.0f, 1.0f, add);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += add[j];
+          }
+          // the three parts, in lanes q = 0, 1, 2; then to the sums of the lane that keeps the token
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (q == 3) v[j] = 0.0f;
+            v[j] += __shfl_xor_sync(0xffffffffu, v[j], 1);
+            v[j] += __shfl_xor_sync(0xffffffffu, v[j], 2);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (i0 + e >= n_tok) break;
+            const int t = f.token[first + i0 + e];
+            if ((t >> 1 & 3) == q) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if (t == 2 * q + j) {
+                  sum[0][j] += v[e];
+                  sum[0][2 + j] += v[2 + e];
+                } else if (t == 8 + 2 * q + j) {
+                  sum[1][j] += v[e];
+                  sum[1][2 + j] += v[2 + e];
+                }
+              }
+            }
+          }
         }
       }
       __syncwarp();                              // all lanes have read the slot
@@ -832,8 +893,8 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float* to = sums + (warp * 16 + g + 8 * (j >> 1)) * 16 + 2 * q + (j & 1);
-    to[0] = cur[j];
-    to[8] = other[j];
+    to[0] = sum[0][j];
+    to[8] = sum[1][j];
   }
   __syncthreads();
 #pragma unroll 1
