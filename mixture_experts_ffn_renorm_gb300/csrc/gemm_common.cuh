@@ -100,11 +100,11 @@ int make_tmap(CUtensorMap* m, const void* base, long long rows, int cols, int bo
 // box reads beyond a matrix's rows or columns is zero, not the next matrix
 int make_tmap3(CUtensorMap* m, const void* base, int groups, int rows, int cols, int box_rows,
                const char* op, const char* what);
-// rows x cols bf16 values or FP8 codes as [block of columns][row][blocks along a row], 128-byte
-// swizzle: a box is box_rows x box_blocks blocks of 128 bytes.  Whole blocks only: what is left of a
+// [experts][halves][rows][cols] bf16 values or FP8 codes with the columns in blocks of 128 bytes, 128-byte
+// swizzle: a box is box_blocks blocks x every half x box_rows rows.  Whole blocks only: what is left of a
 // row lies outside the map.
-int make_tmap_blocks(CUtensorMap* m, const void* base, bool codes, int rows, int cols, int block,
-                     int box_rows, int box_blocks, const char* op, const char* what);
+int make_tmap_blocks(CUtensorMap* m, const void* base, bool codes, int experts, int halves, int rows,
+                     int cols, int box_rows, int box_blocks, const char* op, const char* what);
 // the same for one-byte elements (FP8 codes), unswizzled
 int make_tmap_u8(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows,
                  const char* op, const char* what);

@@ -837,18 +837,17 @@ int make_tmap3(CUtensorMap* m, const void* base, int groups, int rows, int cols,
   return MOE_OK;
 }
 
-int make_tmap_blocks(CUtensorMap* m, const void* base, bool codes, int rows, int cols, int block,
-                     int box_rows, int box_blocks, const char* op, const char* what) {
+int make_tmap_blocks(CUtensorMap* m, const void* base, bool codes, int experts, int halves, int rows,
+                     int cols, int box_rows, int box_blocks, const char* op, const char* what) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return set_error(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", op);
-  const int esz = codes ? 1 : 2;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(block), static_cast<cuuint64_t>(rows),
-                        static_cast<cuuint64_t>(cols / block)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * esz, static_cast<cuuint64_t>(block) * esz};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(block), static_cast<cuuint32_t>(box_rows),
-                       static_cast<cuuint32_t>(box_blocks)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  const cuuint64_t esz = codes ? 1 : 2, n = 128 / esz, C = cols, R = rows, S = halves;
+  cuuint64_t dims[5] = {n, R, S, C / n, static_cast<cuuint64_t>(experts)};
+  cuuint64_t strides[4] = {C * esz, R * C * esz, 128, S * R * C * esz};
+  cuuint32_t box[5] = {static_cast<cuuint32_t>(n), static_cast<cuuint32_t>(box_rows),
+                       static_cast<cuuint32_t>(halves), static_cast<cuuint32_t>(box_blocks), 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

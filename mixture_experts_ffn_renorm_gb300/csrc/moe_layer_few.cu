@@ -19,9 +19,9 @@
 // the down rows do not depend on it.
 //
 // Every warp is a stream of its own: two slots of 8 KB that it refills as soon as it has read them, and
-// no warp waits for another.  A slot is one or two TMA boxes, swizzled over 128 bytes, whose third
-// dimension steps along the rows: one instruction a box.  (Copies of single rows reach the same 7.0 TB/s
-// in a loop of copies alone, but each costs its warp about 200 cycles to issue, 1700 a slot.)
+// no warp waits for another.  A slot is one TMA box, swizzled over 128 bytes, one of whose dimensions
+// steps along the rows: one instruction.  (Copies of single rows reach the same 7.0 TB/s in a loop of
+// copies alone, but each costs its warp about 200 cycles to issue, 1700 a slot.)
 // The products are mma.sync: a few tokens leave tcgen05's 128 rows empty, and what counts is
 // instructions per byte of weights.  Weight rows are the M side, tokens the N side; a lane reads 16 bytes of a row
 // and the same columns of a token, which permutes the columns of a step alike on both sides.  Columns of
@@ -54,8 +54,8 @@ constexpr int kMaxPairs = kMaxT * 32;
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSlots = 2;          // per warp (the loop's two cursors)
-// A slot, in blocks of 128 bytes of a row: gate/up 8 blocks x 4 features' gate rows, then the same of their
-// up rows; down 4 blocks x 16 rows
+// A slot, in blocks of 128 bytes of a row: gate/up 8 blocks x 4 features' gate rows and their up rows;
+// down 4 blocks x 16 rows
 constexpr int kFeat = 4;
 constexpr int kGuBlocks = 8, kDnBlocks = 4;
 constexpr int kSlotBytes = 8192;
@@ -111,10 +111,12 @@ struct Scratch {
   float scores[1];                 // [T][2 E]
 };
 
-__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, int row, int block, uint32_t bar) {
+// a box of an [expert][row half][row][column] matrix, seen as blocks of 128 bytes of a row
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, int row, int block, int expert, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-          "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(row), "r"(block), "r"(bar)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(row), "r"(block), "r"(expert), "r"(bar)
       : "memory");
 }
 
@@ -333,6 +335,7 @@ struct Stream {
   int d0, i0, n0, end_d, end_n, routed, s0, s_end, blocks;
   // down: output columns [col0, col0 + cols) of the CTA, [row0, row0 + rows) of this warp's row block
   int col0, cols, row_blocks, row0, rows, unit0, unit_step, pieces, units;
+  unsigned per_inv, pieces_inv;    // of I / 4 and of pieces
 
   __device__ Stream(const Params& p_, const Fixed& f_, const CUtensorMap* m13_, const CUtensorMap* m2_,
                     const CUtensorMap* m13s_, const CUtensorMap* m2s_, int warp_, int lane_)
@@ -350,6 +353,7 @@ struct Stream {
     end_d = static_cast<int>(rb / I);
     end_n = static_cast<int>(rb - end_d * I);
     const int per = static_cast<int>(I) / kFeat;                           // I % 8 == 0
+    per_inv = 0xFFFFFFFFu / per + 1u;
     if (end_d == d0) {
       n0 = routed = (end_n - i0 + kFeat - 1) / kFeat;
     } else {
@@ -370,14 +374,19 @@ struct Stream {
     unit0 = row_blocks ? warp / row_blocks : 0;
     unit_step = row_blocks ? (kWarps - 1 - rb_i) / row_blocks + 1 : 1;
     pieces = (p.I + dn_cols(0) - 1) / dn_cols(0);
+    pieces_inv = 0xFFFFFFFFu / pieces + 1u;
     units = rows > 0 ? D * pieces + (p.Is + dn_cols(D) - 1) / dn_cols(D) : 0;
   }
   __device__ bool quant(int d) const { return kFp8 && d < D; }
   __device__ int inner(int d) const { return d < D ? p.I : p.Is; }
-  __device__ int block_cols(int d) const { return quant(d) ? 128 : 64; }       // of 128 bytes
-  __device__ int gu_cols(int d) const { return kGuBlocks * block_cols(d); }    // of a piece
-  __device__ int dn_cols(int d) const { return kDnBlocks * block_cols(d); }
+  __device__ int shift(int d) const { return quant(d) ? 7 : 6; }               // columns of a block of 128 bytes
+  __device__ int gu_cols(int d) const { return kGuBlocks << shift(d); }        // of a piece
+  __device__ int dn_cols(int d) const { return kDnBlocks << shift(d); }
 
+  // j / n for inv = ceil(2^32 / n) modulo 2^32: exact while j n < 2^32 (here below 2^31); 0 stands for n = 1
+  static __device__ int divided(int j, unsigned inv) {
+    return inv ? static_cast<int>(__umulhi(static_cast<unsigned>(j), inv)) : j;
+  }
   __device__ void locate(Cursor& c) const {
     if (c.phase == 0) {
       if (c.i < n0) {
@@ -387,9 +396,9 @@ struct Stream {
         return;
       }
       if (c.i < routed) {
-        const unsigned per = static_cast<unsigned>(p.I) / kFeat, j = static_cast<unsigned>(c.i - n0);
-        c.d = d0 + 1 + static_cast<int>(j / per);
-        c.n = kFeat * static_cast<int>(j % per);
+        const int j = c.i - n0, of = divided(j, per_inv);
+        c.d = d0 + 1 + of;
+        c.n = kFeat * j - of * p.I;
         c.cnt = min(kFeat, (c.d == end_d ? end_n : p.I) - c.n);
         return;
       }
@@ -405,7 +414,7 @@ struct Stream {
     if (c.i >= units) {
       c.phase = 2;
     } else if (c.i < D * pieces) {
-      c.d = c.i / pieces;
+      c.d = divided(c.i, pieces_inv);
       c.k = (c.i - c.d * pieces) * dn_cols(0);
     } else {
       c.d = D;
@@ -428,24 +437,19 @@ struct Stream {
     }
     locate(c);
   }
-  // the copies of a piece (one lane).  Only whole blocks of a row are copied: what is left of it is read
-  // from where it lies.  Rows behind the expert's are read and not used.
+  // the copy of a piece (one lane).  Only whole blocks of a row are copied: what is left of it is read
+  // from where it lies.  Rows behind the expert's are zeros, those of the next CTA are not used.
   __device__ void issue(const Cursor& c, uint32_t slot, uint32_t bar) const {
     if (c.phase == 2) return;
-    const int cols = block_cols(c.d), block = c.k / cols, I = inner(c.d);
-    if (c.k + cols > (c.phase == 0 ? p.H : I)) {
+    const int sh = shift(c.d), block = c.k >> sh;
+    if (c.k + (1 << sh) > (c.phase == 0 ? p.H : inner(c.d))) {
       ptx::mbar_arrive(bar);
       return;
     }
     ptx::mbar_arrive_expect_tx(bar, kSlotBytes);
-    if (c.phase == 0) {
-      const CUtensorMap* m = c.d < D ? m13 : m13s;
-      const int row = (c.d < D ? f.expert[c.d] * 2 * I : 0) + c.n;
-      box_load(slot, m, row, block, bar);
-      box_load(slot + kSlotBytes / 2, m, row + I, block, bar);
-    } else {
-      box_load(slot, c.d < D ? m2 : m2s, (c.d < D ? f.expert[c.d] * p.H : 0) + col0 + row0, block, bar);
-    }
+    const int expert = c.d < D ? f.expert[c.d] : 0;
+    if (c.phase == 0) box_load(slot, c.d < D ? m13 : m13s, c.n, block, expert, bar);
+    else box_load(slot, c.d < D ? m2 : m2s, col0 + row0, block, expert, bar);
   }
 };
 
@@ -534,26 +538,20 @@ struct Tokens {
 // gate rows, then their up rows) fill both halves of the MMA's rows, its first with the blocks 0-3 of 128
 // bytes of the piece, its second with 4-7; the MMA's columns 0-3 are the tokens at the first blocks'
 // columns, 4-7 the same tokens at the second's.  What counts of c is rows 0-7 of columns 0-3 and rows
-// 8-15 of columns 4-7.  at: this lane's row in the slot; sc: its row's scales.
+// 8-15 of columns 4-7.  at: row g of the slot; d: this lane's row's scales, block by block.
 template <bool kQ>
-__device__ __forceinline__ void gate_up(const uint8_t* at, int r, int q, const Tokens<kQ>& x, const float* sc, int full,
+__device__ __forceinline__ void gate_up(const uint8_t* at, int g, int q, const Tokens<kQ>& x, const float (&d)[8],
                                         float (&c)[4]) {
   float sum[2][4] = {};
-  float d[8];
-  if (kQ) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = __ldg(sc + min(i, full - 1));
-  }
-  at += ((2 * q) ^ r) << 4;                      // vector 2 q; 2 q + 1 is 16 bytes to either side
-  const int odd = (r & 1) ? -16 : 16, turned = ((2 * q) ^ r) & 4 ? -64 : 64;
+  at += ((2 * q) ^ g) << 4;                      // vector 2 q; 2 q + 1 is 16 bytes to either side
+  const int odd = (g & 1) ? -16 : 16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // the swizzle turns vectors 0-3 and 4-7 round in every second block
-      const uint8_t* v = at + (i & 1 ? turned : 0) + (h ? odd : 0) + i * (kFeat * 128);
-      products<kQ>(sum, Row<kQ>(*reinterpret_cast<const uint4*>(v)),
-                   Row<kQ>(*reinterpret_cast<const uint4*>(v + 4 * kFeat * 128)), x.u[i][h]);
+      const uint8_t* v = at + (h ? odd : 0) + i * 1024;
+      products<kQ>(sum, Row<kQ>(*reinterpret_cast<const uint4*>(v)), Row<kQ>(*reinterpret_cast<const uint4*>(v + 4096)),
+                   x.u[i][h]);
     }
     if (kQ) join<kQ>(sum, d[i], d[i + 4], c);    // a block is a scale block
   }
@@ -561,19 +559,11 @@ __device__ __forceinline__ void gate_up(const uint8_t* at, int r, int q, const T
 }
 
 // One unit of down for two of the expert's tokens, added to c: 16 output columns' rows (this lane's rows
-// g and g + 8); the MMA's columns 2 j and 2 j + 1 are the two tokens' part j.
+// g and g + 8, their scales d[0-3] and d[4-7]); the MMA's columns 2 j and 2 j + 1 are the two tokens' part j.
 template <bool kQ>
-__device__ __forceinline__ void down(const uint8_t* at, int g, int q, const Tokens<kQ>& x, const float* sc0,
-                                     const float* sc1, int full, float (&c)[4]) {
+__device__ __forceinline__ void down(const uint8_t* at, int g, int q, const Tokens<kQ>& x, const float (&d)[8],
+                                     float (&c)[4]) {
   float sum[2][4] = {};
-  float d[2][4];
-  if (kQ) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      d[0][i] = __ldg(sc0 + min(i, full - 1));
-      d[1][i] = __ldg(sc1 + min(i, full - 1));
-    }
-  }
   at += ((2 * q) ^ g) << 4;
   const int odd = (g & 1) ? -16 : 16;
 #pragma unroll
@@ -584,7 +574,7 @@ __device__ __forceinline__ void down(const uint8_t* at, int g, int q, const Toke
       products<kQ>(sum, Row<kQ>(*reinterpret_cast<const uint4*>(v)), Row<kQ>(*reinterpret_cast<const uint4*>(v + 1024)),
                    x.u[i][h]);
     }
-    if (kQ) join<kQ>(sum, d[0][i], d[1][i], c);
+    if (kQ) join<kQ>(sum, d[i], d[i + 4], c);
   }
   if (!kQ) join<kQ>(sum, 1.0f, 1.0f, c);
 }
@@ -648,6 +638,11 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
   for (int e = tid; e < E; e += kThreads) x.mask[e] = 0u;
   grid_dep_wait();
   grid_dep_launch();
+  // the exponential's table, for the choice: a load whose value nobody waits for
+  if (warp == kWarps - 1) {
+    float unused;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(kExpTabDev + 4 * lane));
+  }
   // the arrivals of earlier launches are a multiple of the CTAs, and before this CTA's own nobody passes
   unsigned long long arrivals = 0;
   if (tid == 0) arrivals = (*reinterpret_cast<volatile unsigned long long*>(p.barrier) / gridDim.x + 1) * gridDim.x;
@@ -737,36 +732,41 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
         if (!waited) landed = __all_sync(0xffffffffu, wait(bars + 8 * s, parity, abort_flag, p));
         waited = true;
       };
-      const int cols = st.block_cols(d);
+      const int sh = st.shift(d), cols = 1 << sh;
       if (phase == 0) {
-        const int n = min(kGuBlocks * cols, H - k), full = n / cols;
+        const int n = min(kGuBlocks * cols, H - k), full = n >> sh;
         // this lane's row: feature g & 3, gate or up
         const int row = (g < kFeat ? 0 : I) + min(c[0].n + (g & 3), I - 1);
         const float* sc = nullptr;
         if (kFp8 && quant)
           sc = p.s13 + (expert * ((2 * I + 127) >> 7) + (row >> 7)) * static_cast<size_t>((H + 127) >> 7) + (k >> 7);
-        const uint8_t* mine = at + (g >> 2) * (kSlotBytes / 2) + (g & 3) * 128;
+        const uint8_t* mine = at + g * 128;
         const int fours = n_tok > 4 ? 4 : 1;     // of tokens, in the sums' four places
+        float scale[8];
+        if (kFp8 && quant) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) scale[i] = full > 0 ? __ldg(sc + min(i, full - 1)) : 0.0f;
+        }
+        auto token = [&](int i0) {
+          return p.x + static_cast<size_t>(f.token[first + min(i0 + (g & 3), n_tok - 1)]) * H + k;
+        };
+        auto load = [&](int i0, auto& u) {
+          u.template load<true>(reinterpret_cast<const uint4*>(token(i0) + (g >> 2) * 4 * cols), q, full - (g >> 2) * 4);
+        };
+        auto multiply = [&](int i0, auto u) {
+          load(i0, u);
+          take();
+          if (full > 0) gate_up(mine, g, q, u, scale, sum[0]);
+        };
 #pragma unroll 1
         for (int i0 = 0; i0 < 4 * fours; i0 += 4) {
           if (i0 < n_tok) {
-            const uint16_t* x = p.x + static_cast<size_t>(f.token[first + min(i0 + (g & 3), n_tok - 1)]) * H + k;
-            const uint4* xf = reinterpret_cast<const uint4*>(x + (g >> 2) * 4 * cols);
-            if (kFp8 && quant) {
-              Tokens<kFp8> u;
-              u.template load<true>(xf, q, full - (g >> 2) * 4);
-              take();
-              if (full > 0) gate_up<kFp8>(mine, g & 3, q, u, sc, full, sum[0]);
-            } else {
-              Tokens<false> u;
-              u.template load<true>(xf, q, full - (g >> 2) * 4);
-              take();
-              if (full > 0) gate_up<false>(mine, g & 3, q, u, sc, full, sum[0]);
-            }
+            if (kFp8 && quant) multiply(i0, Tokens<kFp8>());
+            else multiply(i0, Tokens<false>());
             if (full * cols < n) {
               const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w13s) : p.w13);
               w += ((static_cast<size_t>(expert) * 2 * I + row) * H + k + full * cols) * (quant ? 1 : 2);
-              const uint4* xe = reinterpret_cast<const uint4*>(x + full * cols);
+              const uint4* xe = reinterpret_cast<const uint4*>(token(i0) + full * cols);
               float add[4] = {};
               if (kFp8 && quant) row_end<kFp8, true>(w, nullptr, xe, n - full * cols, q, __ldg(sc + full), 0.0f, add);
               else row_end<false, true>(w, nullptr, xe, n - full * cols, q, 1.0f, 1.0f, add);
@@ -805,7 +805,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
           for (int j = 0; j < 4; ++j) sum[0][j] = sum[1][j] = sum[2][j] = sum[3][j] = 0.0f;
         }
       } else {
-        const int n = min(kDnBlocks * cols, I - k), full = n / cols;
+        const int n = min(kDnBlocks * cols, I - k), full = n >> sh;
         // this lane's rows
         const int r0 = min(st.col0 + st.row0 + g, H - 1), r1 = min(r0 + 8, H - 1);
         const float *sc0 = nullptr, *sc1 = nullptr;
@@ -817,28 +817,35 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
         }
         const uint16_t* act = p.act + (shared ? 3 * static_cast<size_t>(T) * K * p.I : 0) +
                               min(g >> 1, 2) * (static_cast<size_t>(shared ? T : T * K) * I) + k;
+        float scale[8];
+        if (kFp8 && quant) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            scale[i] = full > 0 ? __ldg(sc0 + min(i, full - 1)) : 0.0f;
+            scale[i + 4] = full > 0 ? __ldg(sc1 + min(i, full - 1)) : 0.0f;
+          }
+        }
+        auto token = [&](int i0) {
+          const int i = first + min(i0 + (g & 1), n_tok - 1);
+          return act + static_cast<size_t>(shared ? f.token[i] : f.pair[i]) * I;
+        };
+        auto load = [&](int i0, auto& u) { u.template load<false>(reinterpret_cast<const uint4*>(token(i0)), q, full); };
+        auto multiply = [&](int i0, auto u, float (&v)[4]) {
+          load(i0, u);
+          take();
+          if (full > 0) down(at + g * 128, g, q, u, scale, v);
+        };
 #pragma unroll 1
         for (int i0 = 0; i0 < n_tok; i0 += 2) {
-          const int i = first + min(i0 + (g & 1), n_tok - 1);
-          const uint16_t* a = act + static_cast<size_t>(shared ? f.token[i] : f.pair[i]) * I;
           float v[4] = {};
-          if (kFp8 && quant) {
-            Tokens<kFp8> u;
-            u.template load<false>(reinterpret_cast<const uint4*>(a), q, full);
-            take();
-            if (full > 0) down<kFp8>(at + g * 128, g, q, u, sc0, sc1, full, v);
-          } else {
-            Tokens<false> u;
-            u.template load<false>(reinterpret_cast<const uint4*>(a), q, full);
-            take();
-            if (full > 0) down<false>(at + g * 128, g, q, u, sc0, sc1, full, v);
-          }
+          if (kFp8 && quant) multiply(i0, Tokens<kFp8>(), v);
+          else multiply(i0, Tokens<false>(), v);
           if (full * cols < n) {
             const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w2s) : p.w2);
             const int esz = quant ? 1 : 2, at_col = k + full * cols;
             const uint8_t* w0 = w + ((static_cast<size_t>(expert) * H + r0) * I + at_col) * esz;
             const uint8_t* w1 = w + ((static_cast<size_t>(expert) * H + r1) * I + at_col) * esz;
-            const uint4* ae = reinterpret_cast<const uint4*>(a + full * cols);
+            const uint4* ae = reinterpret_cast<const uint4*>(token(i0) + full * cols);
             float add[4] = {};
             if (kFp8 && quant)
               row_end<kFp8, false>(w0, w1, ae, n - full * cols, q, __ldg(sc0 + full), __ldg(sc1 + full), add);
@@ -992,12 +999,11 @@ int check(const char* op, const Params& p, bool fp8, const void* workspace, size
   return MOE_OK;
 }
 
-// rows of `cols` bf16 values or codes as [128 bytes][rows][blocks along a row]
-int make_map(CUtensorMap* m, const void* base, bool codes, int rows, int cols, int box_rows, int box_blocks,
-             const char* op, const char* what) {
-  const int n = codes ? 128 : 64;
-  if (cols < n) return MOE_OK;
-  return gemm::make_tmap_blocks(m, base, codes, rows, cols, n, box_rows, box_blocks, op, what);
+// [experts][halves][rows][cols] bf16 values or codes, a box of box_rows rows of every half
+int make_map(CUtensorMap* m, const void* base, bool codes, int experts, int halves, int rows, int cols, int box_rows,
+             int box_blocks, const char* op, const char* what) {
+  if (cols < (codes ? 128 : 64)) return MOE_OK;
+  return gemm::make_tmap_blocks(m, base, codes, experts, halves, rows, cols, box_rows, box_blocks, op, what);
 }
 
 template <bool kFp8>
@@ -1035,12 +1041,11 @@ int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   // a map without a whole block of 128 bytes is never used
   CUtensorMap m13{}, m2{}, m13s{}, m2s{};
   int rc;
-  const int E2I = p.E * 2 * p.I, EH = p.E * p.H;
-  if ((rc = make_map(&m13, p.w13, kFp8, E2I, p.H, kFeat, kGuBlocks, op, "w13")) != MOE_OK) return rc;
-  if ((rc = make_map(&m2, p.w2, kFp8, EH, p.I, 16, kDnBlocks, op, "w2")) != MOE_OK) return rc;
+  if ((rc = make_map(&m13, p.w13, kFp8, p.E, 2, p.I, p.H, kFeat, kGuBlocks, op, "w13")) != MOE_OK) return rc;
+  if ((rc = make_map(&m2, p.w2, kFp8, p.E, 1, p.H, p.I, 16, kDnBlocks, op, "w2")) != MOE_OK) return rc;
   if (p.Is > 0) {
-    if ((rc = make_map(&m13s, p.w13s, false, 2 * p.Is, p.H, kFeat, kGuBlocks, op, "w13_shared")) != MOE_OK) return rc;
-    if ((rc = make_map(&m2s, p.w2s, false, p.H, p.Is, 16, kDnBlocks, op, "w2_shared")) != MOE_OK) return rc;
+    if ((rc = make_map(&m13s, p.w13s, false, 1, 2, p.Is, p.H, kFeat, kGuBlocks, op, "w13_shared")) != MOE_OK) return rc;
+    if ((rc = make_map(&m2s, p.w2s, false, 1, 1, p.H, p.Is, 16, kDnBlocks, op, "w2_shared")) != MOE_OK) return rc;
   }
   // cooperative: the CTAs wait for one another, so all of them start together or none does
   cudaLaunchAttribute attr[1];
