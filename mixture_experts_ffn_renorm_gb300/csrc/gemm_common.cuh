@@ -100,6 +100,8 @@ int make_tmap(CUtensorMap* m, const void* base, long long rows, int cols, int bo
 // box reads beyond a matrix's rows or columns is zero, not the next matrix
 int make_tmap3(CUtensorMap* m, const void* base, int groups, int rows, int cols, int box_rows,
                const char* op, const char* what);
+// `groups` f32 matrices rows x cols one behind the other, to be stored in boxes of 32 x 32
+int make_tmap_f32_out(CUtensorMap* m, void* base, int groups, int rows, int cols, const char* op);
 // [experts][halves][rows][cols] bf16 values or FP8 codes with the columns in blocks of 128 bytes, 128-byte
 // swizzle: a box is box_blocks blocks x every half x box_rows rows.  Whole blocks only: what is left of a
 // row lies outside the map.

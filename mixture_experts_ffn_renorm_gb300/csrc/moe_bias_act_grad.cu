@@ -3,9 +3,10 @@
 //   dy[r] = dout[dst] * pair_weight[dst],  s = dy act'(z):  dz = bf16(s),
 //   grad_bias[g] = sum of s over g's rows,  grad_pair_weight[dst] = sum_n dout[dst,n] act(z[r,n])
 //
-// One pass over dout and z: what bounds it is HBM (6 bytes an element).  A CTA takes 32 rows x 1024
-// columns; a warp a row at a time, a lane 8 columns of each 256, so that its column sums stay
-// in 32 registers and its row sum is one butterfly.  A CTA's rows may meet several groups: at
+// One pass over dout and z: what bounds it is HBM (6 bytes an element).  A CTA takes 64 rows x 256
+// columns; a warp every eighth row, four of them at a time with all loads in flight, a lane 8
+// columns, so that its column sums are 8 registers and its row sums one butterfly each (1024 columns and
+// one row at a time: 32 registers, two CTAs an SM, 2.8 TB/s).  A CTA's rows may meet several groups: at
 // each group's end the warps' column sums are joined through shared memory in warp order and
 // leave as one partial row.  Block c and group g meet in partial row c + g: along the rows
 // either index or both step up, so no two meetings share one, and the second kernel finds a
@@ -17,9 +18,10 @@ namespace moe {
 namespace gemm {
 namespace {
 
-constexpr int kRows = 32;            // rows of a CTA
-constexpr int kCols = 1024;          // columns of a CTA: 32 per lane
+constexpr int kRows = 64;            // rows of a CTA
+constexpr int kCols = 256;           // columns of a CTA: 8 per lane
 constexpr int kWarps = 8;
+constexpr int kFlight = 4;           // rows of a warp whose loads are in flight together
 
 struct BackParams {
   const uint16_t* dout;
@@ -57,7 +59,8 @@ bias_act_backward_kernel(const BackParams p) {
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int block = blockIdx.x, r_lo = block * kRows, r_hi = min(p.P, r_lo + kRows);
-  const int n0 = blockIdx.y * kCols + lane * 8;
+  const int n = blockIdx.y * kCols + lane * 8;
+  const bool live = n < p.N;
   // the last group that starts at or before the block's first row
   int before = 0;
   for (int g0 = 0; g0 < p.G; g0 += 32 * kWarps) {
@@ -68,64 +71,64 @@ bias_act_backward_kernel(const BackParams p) {
   for (int r0 = max(r_lo, offset_at(p.group_offsets, g, p.P)); g < p.G; ++g) {
     const int r1 = min(r_hi, offset_at(p.group_offsets, g + 1, p.P));
     if (r1 > r0) {
-      float sum[kCols / 256][8] = {};
-      for (int r = r0 + warp; r < r1; r += kWarps) {
-        const int d = p.row_to_pair ? __ldg(p.row_to_pair + r) : r;
-        const bool in = d >= 0 && d < p.P;
-        const float w = in && p.pair_weight ? __ldg(p.pair_weight + d) : 1.0f;
-        uint4 dv[kCols / 256], zv[kCols / 256];
+      float sum[8] = {};
+      // destination and weight of this warp's rows: lane i row r0 + warp + 8 i
+      int my_d = -1;
+      float my_w = 1.0f;
+      const int my_r = r0 + warp + kWarps * lane;
+      if (my_r < r1) {
+        my_d = p.row_to_pair ? __ldg(p.row_to_pair + my_r) : my_r;
+        if (my_d < 0 || my_d >= p.P) my_d = -1;
+        else if (p.pair_weight) my_w = __ldg(p.pair_weight + my_d);
+      }
+      for (int i0 = 0; r0 + warp + kWarps * i0 < r1; i0 += kFlight) {
+        uint4 dv[kFlight], zv[kFlight];
 #pragma unroll
-        for (int i = 0; i < kCols / 256; ++i) {
-          const int n = n0 + 256 * i;
-          const bool on = in && n < p.N;
-          dv[i] = on ? *reinterpret_cast<const uint4*>(p.dout + static_cast<size_t>(d) * p.N + n)
-                     : make_uint4(0, 0, 0, 0);
-          zv[i] = on && p.z ? *reinterpret_cast<const uint4*>(p.z + static_cast<size_t>(r) * p.N + n)
-                            : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < kFlight; ++k) {
+          const int r = r0 + warp + kWarps * (i0 + k), d = __shfl_sync(0xffffffffu, my_d, i0 + k);
+          dv[k] = live && d >= 0 ? *reinterpret_cast<const uint4*>(p.dout + static_cast<size_t>(d) * p.N + n)
+                                 : make_uint4(0, 0, 0, 0);
+          zv[k] = live && d >= 0 && p.z ? *reinterpret_cast<const uint4*>(p.z + static_cast<size_t>(r) * p.N + n)
+                                        : make_uint4(0, 0, 0, 0);
         }
-        float dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kCols / 256; ++i) {
-          const int n = n0 + 256 * i;
-          if (n >= p.N) continue;
-          float dy[8], zz[8];
-          widen(dv[i], dy);
-          widen(zv[i], zz);
+        for (int k = 0; k < kFlight; ++k) {
+          const int r = r0 + warp + kWarps * (i0 + k);
+          if (r >= r1) break;
+          const int d = __shfl_sync(0xffffffffu, my_d, i0 + k);
+          const float w = __shfl_sync(0xffffffffu, my_w, i0 + k);
+          float dy[8], zz[8], dot = 0.0f;
+          widen(dv[k], dy);
+          widen(zv[k], zz);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int j = 0; j < 8; ++j) {
             float y;
-            const float s = act::slope<kAct>(zz[k], y);
-            dot = fmaf(dy[k], y, dot);
-            dy[k] = in ? __fmul_rn(dy[k], w) * s : 0.0f;
-            sum[i][k] += dy[k];
+            const float s = act::slope<kAct>(zz[j], y);
+            dot = fmaf(dy[j], y, dot);
+            dy[j] = d >= 0 ? __fmul_rn(dy[j], w) * s : 0.0f;
+            sum[j] += dy[j];
           }
-          *reinterpret_cast<uint4*>(p.dz + static_cast<size_t>(r) * p.N + n) =
-              make_uint4(pack_bf16x2(dy[0], dy[1]), pack_bf16x2(dy[2], dy[3]), pack_bf16x2(dy[4], dy[5]),
-                         pack_bf16x2(dy[6], dy[7]));
-        }
-        if (p.part_w) {
+          if (live)
+            *reinterpret_cast<uint4*>(p.dz + static_cast<size_t>(r) * p.N + n) =
+                make_uint4(pack_bf16x2(dy[0], dy[1]), pack_bf16x2(dy[2], dy[3]), pack_bf16x2(dy[4], dy[5]),
+                           pack_bf16x2(dy[6], dy[7]));
+          if (p.part_w) {
 #pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-          if (lane == 0 && in) p.part_w[static_cast<size_t>(blockIdx.y) * p.P + d] = dot;
+            for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (lane == 0 && d >= 0) p.part_w[static_cast<size_t>(blockIdx.y) * p.P + d] = dot;
+          }
         }
       }
       if (p.part_b) {
-#pragma unroll
-        for (int i = 0; i < kCols / 256; ++i)
-#pragma unroll
-          for (int k = 0; k < 8; k += 4)
-            *reinterpret_cast<float4*>(&s_sum[warp][256 * i + lane * 8 + k]) =
-                make_float4(sum[i][k], sum[i][k + 1], sum[i][k + 2], sum[i][k + 3]);
+        *reinterpret_cast<float4*>(&s_sum[warp][lane * 8]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        *reinterpret_cast<float4*>(&s_sum[warp][lane * 8 + 4]) = make_float4(sum[4], sum[5], sum[6], sum[7]);
         __syncthreads();
-        const int c = threadIdx.x * 4, n = blockIdx.y * kCols + c;
-        if (n < p.N) {
-          float4 s = *reinterpret_cast<const float4*>(&s_sum[0][c]);
+        const int at = blockIdx.y * kCols + static_cast<int>(threadIdx.x);
+        if (at < p.N) {
+          float s = s_sum[0][threadIdx.x];
 #pragma unroll
-          for (int i = 1; i < kWarps; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(&s_sum[i][c]);
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-          }
-          *reinterpret_cast<float4*>(p.part_b + (static_cast<size_t>(block) + g) * p.N + n) = s;
+          for (int i = 1; i < kWarps; ++i) s += s_sum[i][threadIdx.x];
+          p.part_b[(static_cast<size_t>(block) + g) * p.N + at] = s;
         }
         __syncthreads();
       }

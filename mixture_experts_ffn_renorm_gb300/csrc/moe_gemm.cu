@@ -857,6 +857,21 @@ int make_tmap_blocks(CUtensorMap* m, const void* base, bool codes, int experts, 
   return MOE_OK;
 }
 
+int make_tmap_f32_out(CUtensorMap* m, void* base, int groups, int rows, int cols, const char* op) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return set_error(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", op);
+  const cuuint64_t C = cols, R = rows;
+  cuuint64_t dims[3] = {C, R, static_cast<cuuint64_t>(groups)}, strides[2] = {C * 4, R * C * 4};
+  cuuint32_t box[3] = {32, 32, 1}, estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(MOE_ERR_CUDA, "%s: tensor map for the sums rejected (CUresult %d)", op,
+                     static_cast<int>(r));
+  return MOE_OK;
+}
+
 // rows x cols FP8 codes (one byte each, cols contiguous), box of 64 cols x box_rows
 // rows, unswizzled (the converter warps read it as plain rows of 64 bytes)
 int make_tmap_u8(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows,

@@ -13,8 +13,10 @@
 // bits that f32 gradients of many rows would miss, and the next tile's products should not
 // wait for this tile's stores.  So every 512 rows the products move to the other accumulator
 // of 256 columns and the epilogue warps (a thread: one row, 128 columns) add the finished one to
-// their registers; a tile's sums leave through 4 KB of shared memory per warp as whole 128-byte
-// lines, with add_to's values read the same way.
+// their registers.  Tiles of at most 512 rows skip the registers.  32 rows x 32 columns at a time leave
+// through 4 KB of shared memory per warp and a TMA store, which also cuts off what lies outside the
+// group's matrix.  (With loads from there and stores of 16 bytes a lane a tile took its warps 1400
+// instructions and 14600 cycles, six times its products.)
 //
 // With a few groups of many rows there are fewer tiles than SMs: the rows are cut into ranges whose
 // sums go to the workspace, and a second kernel adds them in range order.
@@ -50,7 +52,7 @@ struct Params {
 struct Smem {
   static constexpr int A = 0;
   static constexpr int B = A + kStages * kABytes;
-  static constexpr int OUT = B + kStages * kBBytes;          // 8 warps x 4 KB
+  static constexpr int OUT = B + kStages * kBBytes;          // 8 warps x 4 KB, a TMA store's source
   static constexpr int BARS = OUT + 8 * 4096;                // full, empty, tfull[2], tempty[2], drain
   static constexpr int MISC = BARS + (2 * kStages + 5) * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
@@ -89,8 +91,20 @@ __device__ __forceinline__ Tile tile_of(const Params& p, long long i, int tn, in
 
 __device__ __forceinline__ int steps_of(const Tile& t) { return (t.r1 - t.r0 + kRowsStage - 1) / kRowsStage; }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// this thread's stores have read their shared memory; have been written
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 __global__ void __launch_bounds__(kThreads, 1)
-wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+             const __grid_constant__ CUtensorMap tmO, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -122,6 +136,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
   if (warp == 0 && lane == 0) {
     ptx::tma_prefetch_desc(&tmA);
     ptx::tma_prefetch_desc(&tmB);
+    ptx::tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
@@ -224,72 +239,96 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     int acc = 0;
     uint32_t uses[2] = {0, 0};
     bool ok = true;
+    // waits for the accumulator's next sums; frees it
+    auto take = [&]() {
+      ok = ok && wait_bar(bar_tfull(acc), (acc ? uses[1] : uses[0]) & 1u, abort_flag, p.status, p.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      ptx::tc_fence_after();
+      return tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc) * kTileK + half * 128;
+    };
+    auto free = [&]() {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_tempty(acc));
+      if (acc) ++uses[1]; else ++uses[0];
+      acc ^= 1;
+    };
     for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
       const Tile t = tile_of(p, i, tn, tk);
       const int steps = steps_of(t);
-      float sum[128];
+      const int n = t.n0 + q * 32 + lane, z = t.range * p.G + t.g;
+      // columns [32 c, + 32) of this thread's row: add_to's, 128 bytes a row through the stage, a store
+      auto leave = [&](int c, float (&v)[32]) {
+        const int col = t.k0 + half * 128 + 32 * c;
+        if (p.add_to && n < p.N) {
+          const float* add = p.add_to + (static_cast<size_t>(t.g) * p.N + n) * p.K + col;
+          float4 a[8];
 #pragma unroll
-      for (int k = 0; k < 128; ++k) sum[k] = 0.0f;
-      for (int st = 0; st < steps; st += kChunk) {
-        ok = ok && wait_bar(bar_tfull(acc), (acc ? uses[1] : uses[0]) & 1u, abort_flag, p.status, p.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc) * kTileK + half * 128;
+          for (int k = 0; k < 8; ++k)              // K % 8 == 0: four columns are in or out together
+            a[k] = col + 4 * k < p.K ? *reinterpret_cast<const float4*>(add + 4 * k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(ta + 32 * c, v);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) sum[32 * c + k] += __uint_as_float(v[k]);
+          for (int k = 0; k < 8; ++k) {
+            v[4 * k] += a[k].x; v[4 * k + 1] += a[k].y; v[4 * k + 2] += a[k].z; v[4 * k + 3] += a[k].w;
+          }
         }
-        ptx::tc_fence_before();
+        if (lane == 0) tma_store_wait_read();      // the stage's last store
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar_tempty(acc));
-        if (acc) ++uses[1]; else ++uses[0];
-        acc ^= 1;
-      }
-      if (!ok) break;
-      // 32 rows x 32 columns at a time: 128 bytes a row, 16-byte pieces XOR-swizzled by the row;
-      // eight lanes store a row
-      const size_t base = (static_cast<size_t>(t.range) * p.G + t.g) * p.N;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          ptx::st_shared_v4(ost + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(sum[32 * c + 4 * k]),
-                            __float_as_uint(sum[32 * c + 4 * k + 1]), __float_as_uint(sum[32 * c + 4 * k + 2]),
-                            __float_as_uint(sum[32 * c + 4 * k + 3]));
+          ptx::st_shared_v4(ost + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(v[4 * k]),
+                            __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+        ptx::fence_proxy_async_smem();
         __syncwarp();
-        const int col = t.k0 + half * 128 + 32 * c + (lane & 7) * 4;
-#pragma unroll
-        for (int k0 = 0; k0 < 8; k0 += 4) {
-          float4 add[4];
-          if (p.add_to) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int n = t.n0 + q * 32 + 4 * (k0 + k) + (lane >> 3);
-              add[k] = n < p.N && col < p.K ? *reinterpret_cast<const float4*>(p.add_to + (base + n) * p.K + col)
-                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = 4 * (k0 + k) + (lane >> 3), n = t.n0 + q * 32 + r;
-            const uint4 u = ptx::ld_shared_v4(ost + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-            float4 s = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                   __uint_as_float(u.w));
-            if (p.add_to) {
-              s.x += add[k].x; s.y += add[k].y; s.z += add[k].z; s.w += add[k].w;
-            }
-            if (n < p.N && col < p.K)      // K % 8 == 0: four columns are in or out together
-              *reinterpret_cast<float4*>(p.out + (base + n) * p.K + col) = s;
-          }
+        if (lane == 0 && col < p.K && t.n0 + q * 32 < p.N) tma_store_3d(&tmO, ost, col, t.n0 + q * 32, z);
+      };
+      if (steps <= kChunk) {
+        uint32_t ta = 0;
+        if (steps > 0) {
+          ta = take();
+          if (!ok) break;
         }
-        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          if (steps > 0) {
+            uint32_t u[32];
+            ptx::tmem_ld_32x32b_x32(ta + 32 * c, u);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(u[k]);
+            if (c == 3) free();
+          } else {                                 // an empty group
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+          }
+          leave(c, v);
+        }
+        continue;
       }
+      float sum[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sum[c][k] = 0.0f;
+#pragma unroll 1
+      for (int st = 0; st < steps; st += kChunk) {
+        const uint32_t ta = take();
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t u[32];
+          ptx::tmem_ld_32x32b_x32(ta + 32 * c, u);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sum[c][k] += __uint_as_float(u[k]);
+        }
+        free();
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) leave(c, sum[c]);
     }
+    if (lane == 0) tma_store_wait();
   }
   // ---- exit: a CTA that gave up drains its copies and MMAs first
   __syncthreads();
@@ -407,6 +446,8 @@ extern "C" int moe_grouped_gemm_wgrad_bf16(const void* dz_bf16, const void* a_bf
   int rc;
   if ((rc = make_tmap(&ta, dz_bf16, P, N, kRowsStage, op, "dz")) != MOE_OK) return rc;
   if ((rc = make_tmap(&tb, a_bf16, P, K, kRowsStage, op, "a")) != MOE_OK) return rc;
+  CUtensorMap to;                    // 32 x 32 boxes of the groups' matrices, a range behind the other
+  if ((rc = make_tmap_f32_out(&to, p.out, G * p.ranges, N, K, op)) != MOE_OK) return rc;
   static std::atomic<int> configured[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -424,7 +465,7 @@ extern "C" int moe_grouped_gemm_wgrad_bf16(const void* dz_bf16, const void* a_bf
       static_cast<long long>(G) * ((N - 1) / kTileN + 1) * ((K - 1) / kTileK + 1) * p.ranges;
   const int sms = sm_count();
   rc = launch_status(launch_kernel(wgrad_kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kThreads),
-                                   Smem::ALLOC, s, nullptr, 0, ta, tb, p),
+                                   Smem::ALLOC, s, nullptr, 0, ta, tb, to, p),
                      op);
   if (rc != MOE_OK || p.ranges == 1) return rc;
   return launch_status(launch_kernel(wgrad_reduce_kernel, dim3(static_cast<unsigned>((n / 4 + 255) / 256)), dim3(256), 0, s,

@@ -279,8 +279,9 @@ def test_backward_of_many_small_groups_and_rows_of_none():
 def test_backward_without_outputs_or_z():
     c = Back(100, 264, 2, offsets([60, 40]), kind=0)
     c.run(z=False, dpw=False)
-    c.run(db=False, dpw=False, ws=None)
-    c.run(db=False, ws=None)                     # one column block: no workspace
+    c.run(db=False, dpw=False, ws=None)          # no sums: no workspace
+    c.run(db=False)
+    Back(100, 136, 2, offsets([60, 40])).run(db=False)
     Back(100, 2056, 2, offsets([60, 40]), kind=5).run(db=False)
     Back(100, 2056, 2, offsets([60, 40]), kind=5).run(dpw=False)
     c = Back(100, 264, 2, offsets([60, 40]), kind=4)
