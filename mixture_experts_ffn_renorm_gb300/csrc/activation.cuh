@@ -3,6 +3,7 @@
 #pragma once
 
 #include "moe_common.cuh"
+#include "sm100_ptx_fp8.cuh"
 
 namespace moe {
 namespace act {
@@ -46,36 +47,79 @@ __device__ __forceinline__ float apply(float z) {
   return z;
 }
 
-// d act / d z, and act(z)
+// act(z) and d act / d z of two values at once, in pairs of f32 (one instruction for both of a pair's
+// additions, multiplications and multiply-adds): the epilogue's gradient reads 6 bytes an element, and
+// with single values its instructions, not HBM, bound it.
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t each(float (*f)(float), uint64_t v) {
+  const float2 u = ptx::unpair(v);
+  return ptx::pair(__float_as_uint(f(u.x)), __float_as_uint(f(u.y)));
+}
+__device__ __forceinline__ float exp2_fast(float v) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+  return y;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// 1 / (1 + 2^v): the logistic function of -v / log2(e)
+__device__ __forceinline__ uint64_t logistic2(uint64_t v) {
+  return each(rcp_fast, add2(each(exp2_fast, v), ptx::pair(1.0f)));
+}
+
 template <int kAct>
-__device__ __forceinline__ float slope(float z, float& y) {
-  if (kAct == MOE_ACT_RELU) {
-    y = z < 0.0f ? 0.0f : z;
-    return z > 0.0f ? 1.0f : 0.0f;
+__device__ __forceinline__ void slope2(uint64_t z, uint64_t& y, uint64_t& s) {
+  using ptx::fma2;
+  using ptx::mul2;
+  using ptx::pair;
+  if (kAct == MOE_ACT_RELU || kAct == MOE_ACT_RELU2) {
+    const float2 u = ptx::unpair(z);
+    const float a = u.x < 0.0f ? 0.0f : u.x, b = u.y < 0.0f ? 0.0f : u.y;       // keeps NaN
+    const uint64_t r = pair(__float_as_uint(a), __float_as_uint(b));
+    if (kAct == MOE_ACT_RELU) {
+      y = r;
+      s = pair(__float_as_uint(u.x > 0.0f ? 1.0f : 0.0f), __float_as_uint(u.y > 0.0f ? 1.0f : 0.0f));
+    } else {
+      y = mul2(r, r);
+      s = add2(r, r);
+    }
+  } else if (kAct == MOE_ACT_GELU) {
+    // see normal_cdf; Phi(z) = 1/2 + sign(z) (1/2 - Phi(-|z|))
+    const uint64_t sign = z & 0x8000000080000000ull, x = z ^ sign;
+    const uint64_t t = each(rcp_fast, fma2(x, pair(0.3275911f * 0.70710678f), pair(1.0f)));
+    const uint64_t e = each(exp2_fast, mul2(mul2(z, z), pair(-0.5f * kLog2e)));
+    uint64_t q = fma2(t, pair(0.5f * 1.061405429f), pair(0.5f * -1.453152027f));
+    q = fma2(t, q, pair(0.5f * 1.421413741f));
+    q = fma2(t, q, pair(0.5f * -0.284496736f));
+    q = fma2(t, q, pair(0.5f * 0.254829592f));
+    const uint64_t tail = mul2(mul2(q, t), e);
+    const uint64_t phi = add2(fma2(tail, pair(-1.0f), pair(0.5f)) ^ sign, pair(0.5f));
+    y = mul2(z, phi);
+    s = fma2(mul2(z, pair(0.39894228f)), e, phi);            // Phi(z) + z phi(z)
+  } else if (kAct == MOE_ACT_GELU_TANH) {
+    const uint64_t zz = mul2(z, z);
+    const uint64_t p = logistic2(mul2(mul2(z, pair(-2.0f * kTanhScale * kLog2e)), fma2(zz, pair(kTanhCube), pair(1.0f))));
+    y = mul2(z, p);
+    // p + 2 c z p (1 - p) (1 + 3 b z^2)
+    const uint64_t d = mul2(y, fma2(p, pair(-1.0f), pair(1.0f)));
+    s = fma2(mul2(d, pair(2.0f * kTanhScale)), fma2(zz, pair(3.0f * kTanhCube), pair(1.0f)), p);
+  } else if (kAct == MOE_ACT_SILU) {
+    const uint64_t p = logistic2(mul2(z, pair(-kLog2e)));
+    y = mul2(z, p);
+    s = fma2(y, fma2(p, pair(-1.0f), pair(1.0f)), p);        // p + z p (1 - p)
+  } else {
+    y = z;
+    s = pair(1.0f);
   }
-  if (kAct == MOE_ACT_RELU2) {
-    const float r = z < 0.0f ? 0.0f : z;
-    y = r * r;
-    return 2.0f * r;
-  }
-  if (kAct == MOE_ACT_GELU) {
-    float e;
-    const float c = normal_cdf(z, e);
-    y = z * c;
-    return fmaf(z * 0.39894228f, e, c);            // Phi(z) + z phi(z)
-  }
-  if (kAct == MOE_ACT_GELU_TANH) {
-    const float s = logistic(2.0f * kTanhScale * z * fmaf(kTanhCube * z, z, 1.0f));
-    y = z * s;
-    return fmaf(2.0f * kTanhScale * z * s * (1.0f - s), fmaf(3.0f * kTanhCube * z, z, 1.0f), s);
-  }
-  if (kAct == MOE_ACT_SILU) {
-    const float s = logistic(z);
-    y = z * s;
-    return s * fmaf(z, 1.0f - s, 1.0f);
-  }
-  y = z;
-  return 1.0f;
 }
 
 // f(std::integral_constant<int, activation>) for a run-time activation

@@ -33,7 +33,7 @@ struct BackParams {
   int P, N, G;
   uint16_t* dz;
   float* part_b;                     // [blocks + G][N] column sums, or null
-  float* part_w;                     // [column blocks][P] row sums by dst, or null
+  float* part_w;                     // [column blocks][P] row sums by row (one block: by dst), or null
   unsigned long long* launches;
 };
 
@@ -41,13 +41,11 @@ __device__ __forceinline__ int offset_at(const int32_t* off, int i, int P) {
   return off ? min(max(__ldg(off + i), 0), P) : (i == 0 ? 0 : P);
 }
 
-__device__ __forceinline__ void widen(const uint4& u, float (&v)[8]) {
+// 8 bf16 values as four pairs of f32
+__device__ __forceinline__ void widen(const uint4& u, uint64_t (&v)[4]) {
   const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(q[i] << 16);
-    v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) v[i] = ptx::pair(q[i] << 16, q[i] & 0xFFFF0000u);
 }
 
 template <int kAct>
@@ -71,7 +69,7 @@ bias_act_backward_kernel(const BackParams p) {
   for (int r0 = max(r_lo, offset_at(p.group_offsets, g, p.P)); g < p.G; ++g) {
     const int r1 = min(r_hi, offset_at(p.group_offsets, g + 1, p.P));
     if (r1 > r0) {
-      float sum[8] = {};
+      uint64_t sum[4] = {};
       // destination and weight of this warp's rows: lane i row r0 + warp + 8 i
       int my_d = -1;
       float my_w = 1.0f;
@@ -97,31 +95,38 @@ bias_act_backward_kernel(const BackParams p) {
           if (r >= r1) break;
           const int d = __shfl_sync(0xffffffffu, my_d, i0 + k);
           const float w = __shfl_sync(0xffffffffu, my_w, i0 + k);
-          float dy[8], zz[8], dot = 0.0f;
+          uint64_t dy[4], zz[4], dots = 0;
+          uint32_t out[4];
           widen(dv[k], dy);
           widen(zv[k], zz);
+          const uint64_t w2 = ptx::pair(w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float y;
-            const float s = act::slope<kAct>(zz[j], y);
-            dot = fmaf(dy[j], y, dot);
-            dy[j] = d >= 0 ? __fmul_rn(dy[j], w) * s : 0.0f;
-            sum[j] += dy[j];
+          for (int j = 0; j < 4; ++j) {
+            uint64_t y, s;
+            act::slope2<kAct>(zz[j], y, s);
+            dots = ptx::fma2(dy[j], y, dots);
+            const uint64_t v = d >= 0 ? ptx::mul2(ptx::mul2(dy[j], w2), s) : 0ull;
+            sum[j] = act::add2(sum[j], v);
+            const float2 u = ptx::unpair(v);
+            out[j] = pack_bf16x2(u.x, u.y);
           }
           if (live)
             *reinterpret_cast<uint4*>(p.dz + static_cast<size_t>(r) * p.N + n) =
-                make_uint4(pack_bf16x2(dy[0], dy[1]), pack_bf16x2(dy[2], dy[3]), pack_bf16x2(dy[4], dy[5]),
-                           pack_bf16x2(dy[6], dy[7]));
+                make_uint4(out[0], out[1], out[2], out[3]);
           if (p.part_w) {
+            const float2 u = ptx::unpair(dots);
+            float dot = u.x + u.y;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (lane == 0 && d >= 0) p.part_w[static_cast<size_t>(blockIdx.y) * p.P + d] = dot;
+            // several column blocks: by row, for the sum; one: the gradient itself, by destination
+            if (lane == 0 && d >= 0)
+              p.part_w[gridDim.y > 1 ? static_cast<size_t>(blockIdx.y) * p.P + r : static_cast<size_t>(d)] = dot;
           }
         }
       }
       if (p.part_b) {
-        *reinterpret_cast<float4*>(&s_sum[warp][lane * 8]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-        *reinterpret_cast<float4*>(&s_sum[warp][lane * 8 + 4]) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint64_t*>(&s_sum[warp][lane * 8 + 2 * j]) = sum[j];
         __syncthreads();
         const int at = blockIdx.y * kCols + static_cast<int>(threadIdx.x);
         if (at < p.N) {
@@ -138,38 +143,55 @@ bias_act_backward_kernel(const BackParams p) {
   }
 }
 
-// grad_bias: blockIdx.y is the group, a thread four columns; grad_pair_weight (rows of
-// blockIdx.y == G): a thread one row
+// grad_bias: kSlices threads share a group's blocks of four columns, their sums joined in order; a CTA
+// of the first G * bias_ctas takes one group and 64 x 4 columns.  grad_pair_weight: the CTAs behind
+// them, a thread a row.
+constexpr int kSlices = 4;
+
 __global__ void __launch_bounds__(256)
-bias_act_reduce_kernel(const BackParams p, float* __restrict__ grad_bias, float* __restrict__ grad_w, int col_blocks) {
+bias_act_reduce_kernel(const BackParams p, float* __restrict__ grad_bias, float* __restrict__ grad_w, int bias_ctas,
+                       int col_blocks) {
+  __shared__ float4 s_part[kSlices][64];
   count_launch(p.launches, MOE_KID_BIAS_ACT_REDUCE);
   grid_dep_wait();
   grid_dep_launch();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  const int g = blockIdx.y;
-  if (grad_bias && g < p.G && 4 * i < p.N) {
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int id = blockIdx.x;
+  if (id < p.G * bias_ctas) {
+    const int g = id / bias_ctas, x = threadIdx.x & 63, slice = threadIdx.x >> 6;
+    const int c = 4 * ((id - g * bias_ctas) * 64 + x);
     const int r0 = offset_at(p.group_offsets, g, p.P), r1 = offset_at(p.group_offsets, g + 1, p.P);
-    if (r1 > r0) {
-      const float* q = p.part_b + static_cast<size_t>(g) * p.N + 4 * i;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (r1 > r0 && c < p.N) {
+      const float* q = p.part_b + static_cast<size_t>(g) * p.N + c;
+      const int b0 = r0 / kRows, n = (r1 - 1) / kRows - b0 + 1;
 #pragma unroll 8
-      for (int b = r0 / kRows; b <= (r1 - 1) / kRows; ++b) {
+      for (int b = b0 + n * slice / kSlices; b < b0 + n * (slice + 1) / kSlices; ++b) {
         const float4 v = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(b) * p.N));
         s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
       }
     }
-    *reinterpret_cast<float4*>(grad_bias + static_cast<size_t>(g) * p.N + 4 * i) = s;
+    s_part[slice][x] = s;
+    __syncthreads();
+    if (slice == 0 && c < p.N) {
+#pragma unroll
+      for (int i = 1; i < kSlices; ++i) {
+        const float4 v = s_part[i][x];
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+      *reinterpret_cast<float4*>(grad_bias + static_cast<size_t>(g) * p.N + c) = s;
+    }
+    return;
   }
-  if (grad_w && g == p.G && i < p.P) {
-    // rows outside every group, and destinations that no row has, keep what they hold: this
-    // thread is a row, not a destination
-    const int lo = offset_at(p.group_offsets, 0, p.P), hi = offset_at(p.group_offsets, p.G, p.P);
-    const int d = p.row_to_pair ? __ldg(p.row_to_pair + i) : i;
-    if (i < lo || i >= hi || d < 0 || d >= p.P) return;
-    float s = __ldcg(p.part_w + d);
-    for (int b = 1; b < col_blocks; ++b) s += __ldcg(p.part_w + static_cast<size_t>(b) * p.P + d);
-    grad_w[d] = s;
-  }
+  const long long i = static_cast<long long>(id - p.G * bias_ctas) * 256 + threadIdx.x;
+  // rows outside every group, and destinations that no row has, keep what they hold
+  const int lo = offset_at(p.group_offsets, 0, p.P), hi = offset_at(p.group_offsets, p.G, p.P);
+  if (!grad_w || i < lo || i >= hi) return;
+  const int d = p.row_to_pair ? __ldg(p.row_to_pair + i) : static_cast<int>(i);
+  if (d < 0 || d >= p.P) return;
+  float s = __ldcg(p.part_w + i);
+#pragma unroll 4
+  for (int b = 1; b < col_blocks; ++b) s += __ldcg(p.part_w + static_cast<size_t>(b) * p.P + i);
+  grad_w[d] = s;
 }
 
 int blocks_of(int n, int size) { return n / size + (n % size != 0); }
@@ -249,8 +271,8 @@ extern "C" int moe_bias_act_backward(const void* dout_bf16, const void* z_bf16, 
     if (rc != MOE_OK) return rc;
   }
   if (!grad_bias && !rows) return MOE_OK;
-  const int x = blocks_of(grad_bias ? N / 4 : 0, 256), xr = rows ? blocks_of(P, 256) : 0;
-  return launch_status(launch_kernel(bias_act_reduce_kernel, dim3(x > xr ? x : xr, G + (rows ? 1 : 0)), dim3(256), 0, s,
-                                     nullptr, 0, p, grad_bias, rows ? grad_pair_weight : nullptr, cb),
+  const int bias_ctas = grad_bias ? blocks_of(N, 256) : 0, row_ctas = rows ? blocks_of(P, 256) : 0;
+  return launch_status(launch_kernel(bias_act_reduce_kernel, dim3(G * bias_ctas + row_ctas), dim3(256), 0, s, nullptr, 0, p,
+                                     grad_bias, rows ? grad_pair_weight : nullptr, bias_ctas, cb),
                        op);
 }
