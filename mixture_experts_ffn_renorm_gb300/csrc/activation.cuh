@@ -8,48 +8,12 @@
 namespace moe {
 namespace act {
 
-// Phi(z), the normal distribution function, and e = exp(-z^2 / 2).  erfc from Abramowitz &
-// Stegun, Handbook of Mathematical Functions, 7.1.26: erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2),
-// t = 1 / (1 + p x), x >= 0, off by at most 1.5e-7, which is below bf16's half step of any
-// value that counts beside its row; two special-function operations instead of a library erf.
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-  const float x = fabsf(z) * 0.70710678f;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-  e = __expf(-x * x);
-  float q = fmaf(t, 1.061405429f, -1.453152027f);
-  q = fmaf(t, q, 1.421413741f);
-  q = fmaf(t, q, -0.284496736f);
-  q = fmaf(t, q, 0.254829592f);
-  const float tail = 0.5f * q * t * e;           // Phi(-|z|)
-  return z < 0.0f ? tail : 1.0f - tail;          // NaN stays NaN through tail
-}
-
-// 1 / (1 + exp(-v)); the quotient of an overflowed exponential is 0
-__device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
-
 constexpr float kTanhScale = 0.79788456f;   // sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
 
-template <int kAct>
-__device__ __forceinline__ float apply(float z) {
-  if (kAct == MOE_ACT_RELU) return z < 0.0f ? 0.0f : z;   // keeps NaN
-  if (kAct == MOE_ACT_RELU2) {
-    const float r = z < 0.0f ? 0.0f : z;
-    return r * r;
-  }
-  if (kAct == MOE_ACT_GELU) {
-    float e;
-    return z * normal_cdf(z, e);
-  }
-  if (kAct == MOE_ACT_GELU_TANH)   // 0.5 (1 + tanh u) = logistic(2 u)
-    return z * logistic(2.0f * kTanhScale * z * fmaf(kTanhCube * z, z, 1.0f));
-  if (kAct == MOE_ACT_SILU) return z * logistic(z);
-  return z;
-}
-
 // act(z) and d act / d z of two values at once, in pairs of f32 (one instruction for both of a pair's
-// additions, multiplications and multiply-adds): the epilogue's gradient reads 6 bytes an element, and
-// with single values its instructions, not HBM, bound it.
+// additions, multiplications and multiply-adds): with single values their instructions bounded the
+// products' epilogue and its gradient, not the tensor core or HBM.
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -93,7 +57,10 @@ __device__ __forceinline__ void slope2(uint64_t z, uint64_t& y, uint64_t& s) {
       s = add2(r, r);
     }
   } else if (kAct == MOE_ACT_GELU) {
-    // see normal_cdf; Phi(z) = 1/2 + sign(z) (1/2 - Phi(-|z|))
+    // Phi(-|z|) = erfc(|z| / sqrt 2) / 2, with erfc from Abramowitz & Stegun, Handbook of Mathematical
+    // Functions, 7.1.26: erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0, off by
+    // at most 1.5e-7, which is below bf16's half step of any value that counts beside its row.  Then
+    // Phi(z) = 1/2 + sign(z) (1/2 - Phi(-|z|))
     const uint64_t sign = z & 0x8000000080000000ull, x = z ^ sign;
     const uint64_t t = each(rcp_fast, fma2(x, pair(0.3275911f * 0.70710678f), pair(1.0f)));
     const uint64_t e = each(exp2_fast, mul2(mul2(z, z), pair(-0.5f * kLog2e)));
@@ -120,6 +87,14 @@ __device__ __forceinline__ void slope2(uint64_t z, uint64_t& y, uint64_t& s) {
     y = z;
     s = pair(1.0f);
   }
+}
+
+// act of a pair (what of slope2 its result does not need is not computed)
+template <int kAct>
+__device__ __forceinline__ uint64_t apply2(uint64_t z) {
+  uint64_t y, s;
+  slope2<kAct>(z, y, s);
+  return y;
 }
 
 // f(std::integral_constant<int, activation>) for a run-time activation

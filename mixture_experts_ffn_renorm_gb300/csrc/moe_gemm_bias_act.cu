@@ -14,10 +14,11 @@
 //               barrier
 //   warp 1      tensor memory; in the even CTA the thread that issues the pair's MMAs
 //   warps 2-9   epilogue in both CTAs: two groups of four warps take the tile's 32-row chunks in
-//               turn.  A thread holds one output column of 32 rows, so the bias is one register;
-//               activation and weight are applied there, in f32; rows leave as 16-byte pieces
-//               through a transpose in shared memory, into which the residual's rows come
-//               first: a thread adds and rounds once, in place, at its own slots.
+//               turn.  A thread holds pairs of consecutive rows of four output columns (16 x 256-bit reads of
+//               tensor memory), so that bias, activation and weight run on pairs of f32, and matrix stores
+//               transpose the rounded pairs on their way to shared memory, from where rows leave as
+//               16-byte pieces; the residual's rows come the same way back.  (A column of 32 rows a thread,
+//               stored as 32 single values, took 26000 cycles a tile with GELU and z, twice its products.)
 //
 // Weights [G, N, K] are K-major operands.  Weights [G, K, N] (the rows' gradient of a layer's
 // own weights) are MN-major ones, boxes of 64 columns x 64 K rows in the same stage: no
@@ -110,11 +111,6 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr)
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
   return v;
-}
-__device__ __forceinline__ float ld_shared_bf16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return bf16_bits_to_f32(v);
 }
 
 // kColumns: weights [G, K, N]
@@ -296,24 +292,28 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
     const int et = static_cast<int>(threadIdx.x) - 64 - 128 * eg;   // 0..127 in the group
     const int ea = static_cast<int>(threadIdx.x) - 64;              // 0..255 over both
     const int q = warp & 3;                                         // TMEM lane quarter
-    const int f = q * 32 + lane;                                    // column of the CTA's 128
+    // this thread's columns of the CTA's 128: f + 8 i, and its rows of eight: 2 (lane % 4) + 0, 1
+    const int f = q * 32 + (lane >> 2), r2 = 2 * (lane & 3);
     const int bar_g = 1 + eg;
     const uint32_t tempty = ptx::mapa_shared(bar_tempty(0), 0);     // + 8 * acc
-    // [32 rows][128 columns] bf16, 16-byte pieces XOR-swizzled by the row; this thread's slot in
-    // row j for each j modulo 16
+    // [32 rows][128 columns] bf16, 16-byte pieces XOR-swizzled by the row; for the matrix stores this
+    // lane addresses row lane % 8 of each eight, the eight columns q * 32 + 8 (lane / 8)
     const uint32_t ost = sb + Smem::EPI + eg * 8192;
-    uint32_t slot[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) slot[j] = ost + (((f >> 3) ^ j) << 4) + (f & 7) * 2;
+    const int mrow = lane & 7, mpiece = q * 4 + (lane >> 3);
     uint32_t uses[2] = {0, 0};
     int acc = 0;
     for (int u = unit; u < work; u += n_units) {
       const Tile t = tile_of(S == 1 ? u : u / S, start, goff, G, n_fb);
       const int sp = S == 1 ? 0 : u % S;
-      const int col0 = t.n0 + static_cast<int>(rank) * 128, col = col0 + f;
+      const int col0 = t.n0 + static_cast<int>(rank) * 128;
       int* dst_t = s_dst + acc * kRowBlock;
       float* w_t = s_w + acc * kRowBlock;
-      const float b = p.bias && !p.part && col < p.N ? __ldg(p.bias + static_cast<size_t>(t.g) * p.N + col) : 0.0f;
+      float b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[i] = p.bias && !p.part && col0 + f + 8 * i < p.N
+                   ? __ldg(p.bias + static_cast<size_t>(t.g) * p.N + col0 + f + 8 * i)
+                   : 0.0f;
       int d = -1;
       float w = 1.0f;
       if (ea < t.rows) {
@@ -351,8 +351,10 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
                          : make_uint4(0, 0, 0, 0);
           }
         }
-        uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(j0), v);
+        // [column half][row eight j, column + 8 e, row k]: v[h][4 j + 2 e + k]
+        uint32_t v[2][16];
+        ptx::tmem_ld_16x256b_x4(taddr + static_cast<uint32_t>(j0), v[0]);
+        ptx::tmem_ld_16x256b_x4(taddr + (16u << 16) + static_cast<uint32_t>(j0), v[1]);
         ptx::tmem_ld_wait();
         if (j0 + 64 >= t.rows) {     // this warp's last read of the accumulator
           ptx::tc_fence_before();
@@ -360,32 +362,45 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
           if (lane == 0) ptx::mbar_arrive_remote_relaxed(tempty + 8u * acc);
         }
         if (p.part) {
-          if (col < p.N) {
-            float* to = p.part + (static_cast<size_t>(sp) * p.N + col) * p.part_rows + t.r0 + j0;
-            const bool vec = (reinterpret_cast<uintptr_t>(to) & 15) == 0;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              if (vec && j0 + i + 4 <= t.rows) {
-                *reinterpret_cast<uint4*>(to + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int i = 0; i < 4; ++i) {
+            const int col = col0 + f + 8 * i;
+            if (col >= p.N) continue;
+            float* to = p.part + (static_cast<size_t>(sp) * p.N + col) * p.part_rows + t.r0 + j0 + r2;
+            const bool vec = (reinterpret_cast<uintptr_t>(to) & 7) == 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t lo = v[i >> 1][4 * j + 2 * (i & 1)], hi = v[i >> 1][4 * j + 2 * (i & 1) + 1];
+              const int r = j0 + 8 * j + r2;
+              if (vec && r + 1 < t.rows) {
+                *reinterpret_cast<uint2*>(to + 8 * j) = make_uint2(lo, hi);
               } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (j0 + i + k < t.rows) to[i + k] = __uint_as_float(v[i + k]);
+                if (r < t.rows) to[8 * j] = __uint_as_float(lo);
+                if (r + 1 < t.rows) to[8 * j + 1] = __uint_as_float(hi);
               }
             }
           }
           continue;
         }
-        float y[32];
+        uint64_t y[4][4];            // [column f + 8 i][rows 8 j + r2, + 1]
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(v[i]) + b;
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            y[i][j] = act::add2(ptx::pair(v[i >> 1][4 * j + 2 * (i & 1)], v[i >> 1][4 * j + 2 * (i & 1) + 1]),
+                                ptx::pair(b[i]));
         // this group's 32 x 128 values to rows of a [P, N] matrix
         auto store = [&](uint16_t* to, bool scattered) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t pk = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-            ptx::st_shared_u16(slot[(2 * i) & 15] + 2 * i * 256, static_cast<uint16_t>(pk & 0xFFFFu));
-            ptx::st_shared_u16(slot[(2 * i + 1) & 15] + (2 * i + 1) * 256, static_cast<uint16_t>(pk >> 16));
+          for (int j = 0; j < 4; ++j) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 u = ptx::unpair(y[i][j]);
+              pk[i] = pack_bf16x2(u.x, u.y);
+            }
+            const int row = 8 * j + mrow;
+            ptx::stmatrix_x4_trans(ost + row * 256 + ((mpiece ^ (row & 15)) << 4), pk[0], pk[1], pk[2], pk[3]);
           }
           ptx::bar_sync(bar_g, 128);
 #pragma unroll
@@ -403,11 +418,17 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
         if (p.z) store(p.z, false);
         act::dispatch(p.activation, [&](auto a) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = act::apply<decltype(a)::value>(y[i]);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[i][j] = act::apply2<decltype(a)::value>(y[i][j]);
         });
         if (p.pair_weight) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = __fmul_rn(y[i], w_t[j0 + i]);
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t w2 = *reinterpret_cast<const uint64_t*>(w_t + j0 + 8 * j + r2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i][j] = ptx::mul2(y[i][j], w2);
+          }
         }
         if (p.residual) {
 #pragma unroll
@@ -417,7 +438,14 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
           }
           ptx::bar_sync(bar_g, 128);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = __fadd_rn(y[i], ld_shared_bf16(slot[i & 15] + i * 256));
+          for (int j = 0; j < 4; ++j) {
+            const int row = 8 * j + mrow;
+            uint32_t u[4];
+            ptx::ldmatrix_x4_trans(ost + row * 256 + ((mpiece ^ (row & 15)) << 4), u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i][j] = act::add2(y[i][j], ptx::pair(u[i] << 16, u[i] & 0xFFFF0000u));
+          }
+          __syncwarp();              // this warp's columns are read by it alone before it writes them
         }
         store(p.out, true);
       }
@@ -506,7 +534,12 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   if (d < 0 || d >= p.P) return;
   act::dispatch(p.activation, [&](auto a) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = act::apply<decltype(a)::value>(y[i]);
+    for (int i = 0; i < 4; i += 2) {
+      const float2 u = ptx::unpair(act::apply2<decltype(a)::value>(
+          ptx::pair(__float_as_uint(y[i]), __float_as_uint(y[i + 1]))));
+      y[i] = u.x;
+      y[i + 1] = u.y;
+    }
   });
   const size_t at = static_cast<size_t>(d) * p.N + n;
   if (p.pair_weight) {

@@ -105,6 +105,33 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
+// 16 lanes x 32 consecutive 32-bit columns, as four accumulator fragments of 16 x 8: thread (r, q) =
+// (lane / 4, lane % 4) gets of fragment j lanes r (0, 1) and r + 8 (2, 3), columns 8 j + 2 q and + 1
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed on their way: thread (r, q) holds elements (r, 2 q) and
+// (r, 2 q + 1) of each, which go to (come from) rows 2 q and 2 q + 1 in memory, place r.  Lane 8 i + k gives the
+// address of matrix i's row k in memory, 16 bytes.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // Shared-memory matrix descriptor of an MN-major operand (the 16-bit values of one K row
 // contiguous), as TMA SWIZZLE_128B boxes of 64 values x rows write it: blocks of 64 values
 // `lbo` bytes apart (leading byte offset), groups of 8 K rows 1024 bytes apart (stride byte
