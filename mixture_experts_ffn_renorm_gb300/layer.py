@@ -13,14 +13,19 @@ from __future__ import annotations
 
 import torch
 
-from . import (BF16, QFMT_Q4_K, QFMT_Q8_0, moe_combine, moe_combine_backward, moe_combine_gate,
+from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_RELU2, ACT_SILU, BF16,
+               LAYER_FEW_MAX_TOKENS, QFMT_Q4_K, QFMT_Q8_0, W_COLUMNS, W_ROWS,
+               moe_bias_act_backward, moe_bias_act_backward_workspace_size, moe_combine, moe_combine_backward, moe_combine_gate,
                moe_gate_workspace_size, moe_grouped_gemm_down_bf16,
                moe_grouped_gemm_down_bf16_shared, moe_grouped_gemm_down_fp8w,
+               moe_grouped_gemm_bias_act_bf16, moe_grouped_gemm_bias_act_workspace_size,
                moe_grouped_gemm_down_q, moe_grouped_gemm_fp8, moe_grouped_gemm_gateup_silu_bf16,
                moe_grouped_gemm_gateup_silu_bf16_shared, moe_grouped_gemm_gateup_silu_bf16_staged,
                moe_grouped_gemm_gateup_silu_fp8, moe_grouped_gemm_gateup_silu_fp8w,
                moe_gateup_staged_workspace_size,
-               moe_grouped_gemm_gateup_silu_q, moe_dequantize_q_bf16, moe_permute,
+               moe_grouped_gemm_gateup_silu_q, moe_grouped_gemm_wgrad_bf16,
+               moe_grouped_gemm_wgrad_workspace_size, moe_dequantize_q_bf16, moe_layer_few_bf16,
+               moe_layer_few_fp8w, moe_layer_few_workspace_size, moe_permute,
                moe_permute_workspace_size, moe_quantize_act_fp8, moe_quantize_act_q8,
                moe_route_backward, moe_route_backward_workspace_size, moe_route_logits_backward,
                moe_route_logits_backward_workspace_size, moe_route_topk,
@@ -68,6 +73,10 @@ class MoeBlock:
     on average (decode-sized; plain bf16 experts, no fused shared expert), where
     the 32-row tiles gather as fast as they read x_perm and the permute's row
     copy is saved, and materialises x_perm otherwise.
+    few=True (bf16 or FP8 weights without fp8_acts): calls of at most 16 tokens run the
+    whole layer in one launch (moe_layer_few_*), where nothing is narrowed to bf16 between
+    the weights and the output; the choice of experts is the same, the output agrees within
+    the roundings of the separate launches.  Larger calls run as without it.
     q_dequant=True (with qweights): the GGUF blocks are expanded to bf16 once, on the
     device, when the block is built, and the layer runs the bf16 tensor-core path --
     the faster choice when the experts see many rows each (prefill-sized batches).
@@ -75,7 +84,8 @@ class MoeBlock:
 
     def __init__(self, H, I, E, K, weights, max_tokens, device="cuda", I_shared=0,
                  routed_scale=1.0, gather=False, fuse_shared=True, fp8_weights=False,
-                 qweights=None, q_dequant=False, staged=False, fp8_acts=False, training=False):
+                 qweights=None, q_dequant=False, staged=False, fp8_acts=False, training=False,
+                 few=False):
         self.H, self.I, self.E, self.K, self.Is = H, I, E, K, I_shared
         if qweights is not None:
             if qweights not in Q_WEIGHTS:
@@ -118,6 +128,9 @@ class MoeBlock:
             raise ValueError(f"FP8 activations need H and I to be multiples of 16, not {H} and {I}")
         if training and (not fp8_acts or I_shared > 0):
             raise ValueError("training needs fp8_acts and no shared expert")
+        if few and (self.qfmt or fp8_acts):
+            raise ValueError("few needs bf16 experts or FP8 weights without fp8_acts")
+        self.few = few
         self.routed_scale = float(routed_scale)
         self.device = torch.device(device)
         if self.device.type != "cuda":
@@ -205,6 +218,10 @@ class MoeBlock:
         self.ws_gate = moe_gate_workspace_size(T)
         self.workspace = torch.empty((max(self.ws_route, self.ws_perm, self.ws_gate, 256),),
                                      dtype=torch.uint8, device=dv)
+        if few:
+            # zero-filled once (it holds a barrier), then passed unchanged to every call
+            n = moe_layer_few_workspace_size(min(T, LAYER_FEW_MAX_TOKENS), H, I, E, K, I_shared)
+            self.ws_few = torch.zeros((max(16, n),), dtype=torch.uint8, device=dv)
         self.graph = None
         self.graph_x = None
         self._pipe = None
@@ -231,6 +248,12 @@ class MoeBlock:
                 marks.append((name, ev))
 
         mark("start", edge=True)
+        if self.few and T <= LAYER_FEW_MAX_TOKENS:
+            out = self.out[:T] if out is None else out
+            self._forward_few(x, T, out, stream)
+            self._tokens = T
+            mark("layer", edge=True)
+            return out
         moe_route_topk(x, self.w_router, self.logit_bias,
                        self.w_shared_gate if self.has_shared else None, None, T, H, E, K, 1, 0, 1,
                        self.topk_ids, self.topk_w, self.logits if self.training else None,
@@ -321,6 +344,18 @@ class MoeBlock:
                         self.routed_scale, T, K, H, out, BF16, stream)
         mark("combine", edge=True)
         return out
+
+    def _forward_few(self, x, T, out, stream):
+        shared = ((self.w_shared_gate, self.w13_shared, self.w2_shared) if self.has_shared
+                  else (None, None, None))
+        rest = (*shared, None, T, self.H, self.I, self.E, self.K, self.Is, 1, 0, 1, 1, 0,
+                self.routed_scale, self.topk_ids, self.topk_w, out, self.ws_few,
+                self.ws_few.numel(), stream)
+        if self.fp8:
+            moe_layer_few_fp8w(x, self.w_router, self.logit_bias, None, self.w13_q, self.w13_s,
+                               self.w2_q, self.w2_s, *rest)
+        else:
+            moe_layer_few_bf16(x, self.w_router, self.logit_bias, None, self.w13, self.w2, *rest)
 
     def backward(self, x, dout, balance_coef=0.0, z_coef=0.0, stream=None):
         """Gradients of the last forward(x), given the gradient dout [T, H] bf16 of its output,
@@ -461,3 +496,132 @@ class MoeBlock:
         cs.wait_stream(up)
         cs.wait_stream(down)
         return out_hosts
+
+
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "relu2": ACT_RELU2, "gelu": ACT_GELU,
+               "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+
+
+class MoeMlpBlock:
+    """One MoE block whose experts are plain two-layer networks with biases,
+    y = W2 act(W1 x + b1) + b2, with resident weights and, for training, all gradients.
+
+        route -> permute -> product (bias, activation) -> product (bias, weight, scatter) -> combine
+
+    weights: dict with ``w_router`` [E, H], ``w1`` [E, I, H], ``w2`` [E, H, I] (bf16) and
+    optional ``b1`` [E, I], ``b2`` [E, H], ``logit_bias`` [E] (f32).  activation: a key of
+    ACTIVATIONS.  H and I multiples of 8.  training=True: forward() keeps what backward() needs.
+    No call allocates or synchronises; a forward and its backward can be captured into a graph.
+    """
+
+    def __init__(self, H, I, E, K, weights, max_tokens, activation="gelu", device="cuda",
+                 routed_scale=1.0, training=False):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, not {activation!r}")
+        if H % 8 or I % 8:
+            raise ValueError(f"H and I must be multiples of 8, not {H} and {I}")
+        self.H, self.I, self.E, self.K, self.max_tokens = H, I, E, K, max_tokens
+        self.act, self.training = ACTIVATIONS[activation], training
+        self.routed_scale = float(routed_scale)
+        self.device = dv = torch.device(device)
+        if dv.type != "cuda":
+            raise ValueError(f"MoeMlpBlock needs a CUDA device, not {dv}; there is no CPU path")
+        self.w_router, self.w1, self.w2 = (_dev_bf16(weights[k], dv) for k in ("w_router", "w1", "w2"))
+        f32 = torch.float32
+        opt = lambda k: (None if weights.get(k) is None else
+                         torch.as_tensor(weights[k], dtype=f32).to(dv).contiguous())
+        self.b1, self.b2, self.logit_bias = opt("b1"), opt("b2"), opt("logit_bias")
+        T, P = max_tokens, max_tokens * K
+        new = lambda *shape, dt=torch.bfloat16: torch.empty(shape, dtype=dt, device=dv)
+        i32 = torch.int32
+        self.topk_ids, self.topk_w = new(T, K, dt=i32), new(T, K, dt=f32)
+        self.expert_offsets, self.sorted_pair, self.pair_to_row = new(E + 1, dt=i32), new(P, dt=i32), new(P, dt=i32)
+        self.x_perm, self.hidden, self.rows, self.out = new(P, H), new(P, I), new(P, H), new(T, H)
+        self.logits = self.z1 = self.z2 = None
+        size = max(moe_route_topk_workspace_size(T, E, K), moe_permute_workspace_size(T, K, E),
+                   moe_grouped_gemm_bias_act_workspace_size(P, H, I, E),
+                   moe_grouped_gemm_bias_act_workspace_size(P, I, H, E))
+        if training:
+            self.logits, self.z1, self.z2 = new(T, E, dt=f32), new(P, I), new(P, H)
+            self.drows, self.dz2, self.dhidden, self.dz1 = new(P, H), new(P, H), new(P, I), new(P, I)
+            self.grad_topk_w, self.grad_logits = new(T, K, dt=f32), new(T, E, dt=f32)
+            self.losses, self.grad_x, self.grad_x_router = new(2, dt=f32), new(T, H), new(T, H)
+            self.grad_w_router, self.grad_logit_bias = new(E, H, dt=f32), new(E, dt=f32)
+            self.grad_w1, self.grad_b1 = new(E, I, H, dt=f32), new(E, I, dt=f32)
+            self.grad_w2, self.grad_b2 = new(E, H, I, dt=f32), new(E, H, dt=f32)
+            size = max(size, moe_bias_act_backward_workspace_size(P, I, E),
+                       moe_bias_act_backward_workspace_size(P, H, E),
+                       moe_grouped_gemm_wgrad_workspace_size(P, I, H, E),
+                       moe_grouped_gemm_wgrad_workspace_size(P, H, I, E),
+                       moe_route_backward_workspace_size(T, E),
+                       moe_route_logits_backward_workspace_size(T, H, E))
+        self.workspace = new(max(256, size), dt=torch.uint8)
+        self._tokens = None
+
+    def forward(self, x, residual=None, stream=None, out=None):
+        """x bf16 [T, H], contiguous -> bf16 [T, H]: the routed sum, plus residual [T, H] if given,
+        rounded once."""
+        T = x.shape[0]
+        assert T <= self.max_tokens and x.dtype == torch.bfloat16 and x.is_contiguous()
+        assert residual is None or (residual.shape == x.shape and residual.dtype == x.dtype and
+                                    residual.is_contiguous())
+        H, I, E, K, ws = self.H, self.I, self.E, self.K, self.workspace
+        P = T * K
+        self._tokens = None
+        moe_route_topk(x, self.w_router, self.logit_bias, None, None, T, H, E, K, 1, 0, 1,
+                       self.topk_ids, self.topk_w, self.logits, None, ws, ws.numel(), stream)
+        moe_permute(self.topk_ids, x, T, K, E, H, self.expert_offsets, self.sorted_pair,
+                    self.pair_to_row, self.x_perm, ws, ws.numel(), stream)
+        moe_grouped_gemm_bias_act_bf16(self.x_perm, self.w1, W_ROWS, self.b1, self.act, self.z1,
+                                       None, None, None, self.expert_offsets, P, H, I, E,
+                                       self.hidden, ws, ws.numel(), stream)
+        moe_grouped_gemm_bias_act_bf16(self.hidden, self.w2, W_ROWS, self.b2, ACT_NONE, self.z2,
+                                       self.topk_w, self.sorted_pair, None, self.expert_offsets, P,
+                                       I, H, E, self.rows, ws, ws.numel(), stream)
+        out = self.out[:T] if out is None else out
+        moe_combine(self.rows, BF16, None, residual, BF16, self.routed_scale, T, K, H, out, BF16,
+                    stream)
+        self._tokens = T
+        return out
+
+    def backward(self, x, dout, balance_coef=0.0, z_coef=0.0, stream=None):
+        """Gradients of the last forward(x), given the gradient dout [T, H] bf16 of its output, plus
+        the router's auxiliary losses: a dict of views of the block's buffers -- grad_x bf16 [T, H]
+        (through experts and router; a residual's is dout itself), f32 grad_w1, grad_b1, grad_w2,
+        grad_b2, grad_w_router, grad_logit_bias, grad_topk_w and losses [2].  The choice of experts
+        counts as constant.  May be called again after one forward, with another dout."""
+        if not self.training:
+            raise ValueError("backward() needs MoeMlpBlock(training=True)")
+        T = x.shape[0]
+        if T != self._tokens:
+            raise ValueError("backward() needs a forward() before it" if self._tokens is None else
+                             f"backward() of {T} tokens, but the last forward() took {self._tokens}")
+        assert dout.shape == x.shape
+        assert x.dtype == dout.dtype == torch.bfloat16 and x.is_contiguous() and dout.is_contiguous()
+        H, I, E, K, ws = self.H, self.I, self.E, self.K, self.workspace
+        P, off, pair = T * K, self.expert_offsets, self.sorted_pair
+        wsa = (ws, ws.numel(), stream)
+        # the rows' gradients in pair order, then through the second product's weight and bias
+        moe_combine_backward(None, BF16, None, dout, BF16, self.routed_scale, T, K, H, None,
+                             self.drows, BF16, stream)
+        moe_bias_act_backward(self.drows, self.z2, ACT_NONE, self.topk_w, pair, off, P, H, E,
+                              self.dz2, self.grad_b2, self.grad_topk_w, *wsa)
+        moe_grouped_gemm_wgrad_bf16(self.dz2, self.hidden, off, P, H, I, E, None, self.grad_w2, *wsa)
+        moe_grouped_gemm_bias_act_bf16(self.dz2, self.w2, W_COLUMNS, None, ACT_NONE, None, None,
+                                       None, None, off, P, H, I, E, self.dhidden, *wsa)
+        moe_bias_act_backward(self.dhidden, self.z1, self.act, None, None, off, P, I, E, self.dz1,
+                              self.grad_b1, None, *wsa)
+        moe_grouped_gemm_wgrad_bf16(self.dz1, self.x_perm, off, P, I, H, E, None, self.grad_w1, *wsa)
+        # the tokens': rows in pair order, summed on the router's part
+        moe_grouped_gemm_bias_act_bf16(self.dz1, self.w1, W_COLUMNS, None, ACT_NONE, None, None,
+                                       pair, None, off, P, I, H, E, self.drows, *wsa)
+        moe_route_backward(self.logits, self.topk_ids, self.grad_topk_w, off, T, E, K, 1, 0,
+                           balance_coef, z_coef, self.grad_logits, self.losses, *wsa)
+        moe_route_logits_backward(self.grad_logits, x, self.w_router, T, H, E, self.grad_x_router,
+                                  self.grad_w_router, self.grad_logit_bias, *wsa)
+        moe_combine(self.drows, BF16, None, self.grad_x_router, BF16, 1.0, T, K, H, self.grad_x,
+                    BF16, stream)
+        return {"grad_x": self.grad_x[:T], "grad_w_router": self.grad_w_router,
+                "grad_logit_bias": self.grad_logit_bias, "grad_topk_w": self.grad_topk_w[:T],
+                "grad_w1": self.grad_w1, "grad_b1": self.grad_b1, "grad_w2": self.grad_w2,
+                "grad_b2": self.grad_b2, "losses": self.losses}
