@@ -9,6 +9,7 @@ import torch
 
 import mixture_experts_ffn_renorm_gb300 as m
 
+from .gpu_util import DEV
 from .test_gpu_bias_act import Product, Wgrad, offsets
 from .test_gpu_layer_few import Case
 
@@ -31,6 +32,7 @@ def runs_out(call, outs, reset=lambda: None):
     torch.cuda.synchronize()
     assert m.moe_device_status() == 0
     want = [o.clone() for o in outs]
+    torch.zeros(1 << 29, dtype=torch.uint8, device=DEV)     # the inputs leave L2
     m.moe_set_wait_limit_ns(1000)
     call()
     assert m.moe_device_status(clear=True) & m.STATUS_TIMEOUT
@@ -53,12 +55,13 @@ def test_layer(T, fp8):
 
 
 @pytest.mark.parametrize("columns", [False, True])
-@pytest.mark.parametrize("P", [2, 4000])
-def test_product(P, columns):
-    c = Product(P, 4096, 4096, 1, None, columns, residual=True)
+def test_product(columns):
+    c = Product(4000, 4096, 4096, 1, None, columns, residual=True)
     runs_out(c.call, (c.out,))
 
 
 def test_weight_gradient():
-    for c in (Wgrad(4096, 2048, 2048, 4, offsets([1024] * 4)), Wgrad(8192, 256, 256)):
-        runs_out(c.call, (c.dw,))
+    # a tile per SM and group, 60 MB of rows: its first sums are 9 us of HBM away
+    G = 152
+    c = Wgrad(512 * G, 128, 256, G, offsets([512] * G))
+    runs_out(c.call, (c.dw,))
