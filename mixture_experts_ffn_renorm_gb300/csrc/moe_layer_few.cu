@@ -102,6 +102,7 @@ struct alignas(16) Fixed {
   int16_t expert[kMaxPairs + 1];   // touched experts, ascending
   int16_t first[kMaxPairs + 3];    // their first pair
   uint16_t tokens[kMaxPairs + 1];  // their tokens, a bit each
+  int16_t cost[kMaxPairs + 2];     // costs of the touched experts before them
   int n_groups;                    // touched experts, without the shared one
   int abort_flag;
 };
@@ -281,30 +282,46 @@ __device__ __forceinline__ void choose(const Params& p, Fixed& f, Scratch& x, in
   }
 }
 
+// What a feature of an expert costs an SM, in halves: its rows' way from memory hides one pass over
+// four tokens, and every further pass takes about half as long.  (Cut by features alone, one
+// expert of five tokens among 83 of one or two held all SMs up for 40 of 190 us.)
+__device__ __forceinline__ int cost_of(int tokens) { return 2 + ((tokens - 1) >> 2); }
+
 // Touched experts in ascending order with their pairs (tokens ascending), then the shared
 // expert's tokens.  One warp scans the experts; then a thread per pair places it.
 __device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch& x, int lane) {
   const int per = (p.E + 31) / 32, lo = min(p.E, lane * per), hi = min(p.E, lo + per);
-  int n = 0;                       // touched experts, and their pairs in the upper half
+  int n = 0, cost = 0;             // touched experts, and their pairs in the upper half; their costs
 #pragma unroll 1
   for (int e = lo; e < hi; ++e)
-    if (x.mask[e]) n += 1 + (__popc(x.mask[e]) << 16);
-  int incl = n;
+    if (x.mask[e]) {
+      const int tokens = __popc(x.mask[e]);
+      n += 1 + (tokens << 16);
+      cost += cost_of(tokens);
+    }
+  int incl = n, costs = cost;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
+    const int u = __shfl_up_sync(0xffffffffu, incl, o), w = __shfl_up_sync(0xffffffffu, costs, o);
+    if (lane >= o) {
+      incl += u;
+      costs += w;
+    }
   }
   int run = incl - n;
+  costs -= cost;
 #pragma unroll 1
   for (int e = lo; e < hi; ++e) {
     const uint32_t m = x.mask[e];
     if (!m) continue;
+    const int tokens = __popc(m);
     f.expert[run & 0xFFFF] = static_cast<int16_t>(e);
     f.first[run & 0xFFFF] = static_cast<int16_t>(run >> 16);
     f.tokens[run & 0xFFFF] = static_cast<uint16_t>(m);
+    f.cost[run & 0xFFFF] = static_cast<int16_t>(costs);
     x.mask[e] = m | (static_cast<uint32_t>(run >> 16) << 16);
-    run += 1 + (__popc(m) << 16);
+    run += 1 + (tokens << 16);
+    costs += cost_of(tokens);
   }
   if (lane == 31) {
     const int D = run & 0xFFFF, P = run >> 16;
@@ -312,6 +329,7 @@ __device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch
     f.first[D] = static_cast<int16_t>(P);
     f.first[D + 1] = static_cast<int16_t>(P + p.T);
     f.tokens[D] = static_cast<uint16_t>((1u << p.T) - 1u);   // the shared expert's
+    f.cost[D] = static_cast<int16_t>(costs);
   }
 }
 
@@ -341,17 +359,30 @@ struct Stream {
                     const CUtensorMap* m13s_, const CUtensorMap* m2s_, int warp_, int lane_)
       : p(p_), f(f_), m13(m13_), m2(m2_), m13s(m13s_), m2s(m2s_), warp(warp_), lane(lane_) {
     D = f.n_groups;
-    // a shared expert's bf16 feature beside FP8 ones counts twice
-    constexpr unsigned kCost = kFp8 ? 2 : 1;
-    const unsigned I = p.I, line = static_cast<unsigned>(D) * I;           // at most 512 * 8192
-    const unsigned all = line + kCost * p.Is, cta = blockIdx.x;
+    // The features in one line, each as long as it costs (a shared expert's bf16 feature beside FP8
+    // ones twice as long), cut evenly: at most 5 * 512 * 8192 + 10 * 8192 long.  A feature is the
+    // CTA's in whose part it begins.
+    const unsigned I = p.I, shared_cost = (kFp8 ? 2u : 1u) * cost_of(p.T);
+    const unsigned line = static_cast<unsigned>(f.cost[D]) * I, all = line + shared_cost * p.Is, cta = blockIdx.x;
     const unsigned a = all / gridDim.x * cta + min(cta, all % gridDim.x);
     const unsigned b = a + all / gridDim.x + (cta < all % gridDim.x ? 1u : 0u);
-    const unsigned ra = min(a, line), rb = min(b, line);
-    d0 = static_cast<int>(ra / I);
-    i0 = static_cast<int>(ra - d0 * I);
-    end_d = static_cast<int>(rb / I);
-    end_n = static_cast<int>(rb - end_d * I);
+    auto place = [&](unsigned at, int& d, int& i) {          // the first feature that begins at or behind `at`
+      at = min(at, line);
+      int lo = 0, hi = D;                                    // cost[lo] I <= at; hi: beyond or D
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<unsigned>(f.cost[mid]) * I <= at) lo = mid; else hi = mid;
+      }
+      const unsigned each = static_cast<unsigned>(f.cost[lo + 1] - f.cost[lo]);
+      i = static_cast<int>((at - static_cast<unsigned>(f.cost[lo]) * I + each - 1) / each);
+      d = lo;
+      if (i >= static_cast<int>(I)) {
+        i = 0;
+        ++d;
+      }
+    };
+    place(a, d0, i0);
+    place(b, end_d, end_n);
     const int per = static_cast<int>(I) / kFeat;                           // I % 8 == 0
     per_inv = 0xFFFFFFFFu / per + 1u;
     if (end_d == d0) {
@@ -360,8 +391,8 @@ struct Stream {
       n0 = (static_cast<int>(I) - i0 + kFeat - 1) / kFeat;
       routed = n0 + (end_d - d0 - 1) * per + (end_n + kFeat - 1) / kFeat;
     }
-    s0 = static_cast<int>((a - ra + kCost - 1) / kCost);
-    s_end = static_cast<int>((b - rb + kCost - 1) / kCost);
+    s0 = a > line ? static_cast<int>((a - line + shared_cost - 1) / shared_cost) : 0;
+    s_end = b > line ? static_cast<int>((b - line + shared_cost - 1) / shared_cost) : 0;
     blocks = routed + (s_end - s0 + kFeat - 1) / kFeat;
     const unsigned H = p.H;
     col0 = static_cast<int>(H / gridDim.x * cta + min(cta, H % gridDim.x));
@@ -638,10 +669,15 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
   for (int e = tid; e < E; e += kThreads) x.mask[e] = 0u;
   grid_dep_wait();
   grid_dep_launch();
-  // the exponential's table, for the choice: a load whose value nobody waits for
-  if (warp == kWarps - 1) {
+  // the exponential's table, for the choice, and the tokens: loads whose values nobody waits for, so
+  // that later ones find a line a lane in L1 (24 KB of it, what the ring leaves)
+  {
     float unused;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(kExpTabDev + 4 * lane));
+    if (warp == kWarps - 1) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(kExpTabDev + 4 * lane));
+    const int lines = min(T * H / 64, 192);
+#pragma unroll 1
+    for (int i = tid; i < lines; i += kThreads)
+      asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(p.x + static_cast<size_t>(i) * 64));
   }
   // the arrivals of earlier launches are a multiple of the CTAs, and before this CTA's own nobody passes
   unsigned long long arrivals = 0;
