@@ -164,31 +164,68 @@ __device__ __forceinline__ float sigmoid_once(float v) { return __fdiv_rn(1.0f, 
 
 // The K best of a token's E keys in the router's order (descending, ties to the lower id, NaN last)
 // among those whose bit of `taken` is clear: the j-th id in lane j.  A lane holds entries lane +
-// 32 i, its best one found again only after it was taken.
+// 32 i, sorted once; a pick compares the lanes' heads, and the winning lane's next entry moves up.
 template <int kPer>
 __device__ __forceinline__ int pick(const float* key, int E, int K, int lane, uint32_t taken) {
-  uint32_t k[kPer];
+  uint32_t k[kPer], id[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    k[i] = lane + 32 * i < E ? route::rank_key(key[lane + 32 * i]) : 0u;
-    if (lane + 32 * i >= E) taken |= 1u << i;
+    const int e = lane + 32 * i;
+    const bool out = e >= E || (taken >> i & 1u);            // below every expert, and never reached
+    k[i] = out ? 0u : route::rank_key(key[e]);
+    id[i] = out ? 0xFFFFFFFFu : static_cast<uint32_t>(e);
   }
-  int id = 0;
+#pragma unroll
+  for (int r = 0; r < kPer; ++r)                             // odd-even transposition
+#pragma unroll
+    for (int i = r & 1; i + 1 < kPer; i += 2) {
+      const bool turn = k[i + 1] > k[i] || (k[i + 1] == k[i] && id[i + 1] < id[i]);
+      const uint32_t k0 = k[i], i0 = id[i];
+      k[i] = turn ? k[i + 1] : k0;
+      id[i] = turn ? id[i + 1] : i0;
+      k[i + 1] = turn ? k0 : k[i + 1];
+      id[i + 1] = turn ? i0 : id[i + 1];
+    }
+  int mine = 0;
+#pragma unroll 1
+  for (int j = 0; j < K; ++j) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, k[0]);
+    const uint32_t win = __reduce_min_sync(0xffffffffu, k[0] == top ? id[0] : 0xFFFFFFFFu);
+    if (lane == j) mine = static_cast<int>(win);
+    if ((win & 31u) == static_cast<uint32_t>(lane)) {
+#pragma unroll
+      for (int i = 0; i + 1 < kPer; ++i) {
+        k[i] = k[i + 1];
+        id[i] = id[i + 1];
+      }
+      k[kPer - 1] = 0u;
+      id[kPer - 1] = 0xFFFFFFFFu;
+    }
+  }
+  return mine;
+}
+
+// The same for many experts: a lane looks through its entries again for every pick
+__device__ __forceinline__ int pick_many(const float* key, int E, int K, int lane, uint32_t taken) {
+  int mine = 0;
 #pragma unroll 1
   for (int j = 0; j < K; ++j) {
     uint32_t bk = 0u, bid = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (!((taken >> i) & 1u) && (bid == 0xFFFFFFFFu || k[i] > bk)) {
-        bk = k[i];
-        bid = static_cast<uint32_t>(lane + 32 * i);
+#pragma unroll 4
+    for (int i = 0; i < (E + 31) / 32; ++i) {
+      const int e = lane + 32 * i;
+      const uint32_t k = e < E ? route::rank_key(key[e]) : 0u;
+      if (e < E && !(taken >> i & 1u) && (bid == 0xFFFFFFFFu || k > bk)) {
+        bk = k;
+        bid = static_cast<uint32_t>(e);
       }
+    }
     const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
     const uint32_t win = __reduce_min_sync(0xffffffffu, bk == top ? bid : 0xFFFFFFFFu);
     if ((win & 31u) == static_cast<uint32_t>(lane)) taken |= 1u << (win >> 5);
-    if (lane == j) id = static_cast<int>(win);
+    if (lane == j) mine = static_cast<int>(win);
   }
-  return id;
+  return mine;
 }
 
 // The pairs of a token: one warp picks the K experts in the router's order and forms their
@@ -197,11 +234,19 @@ __device__ __forceinline__ void choose(const Params& p, Fixed& f, Scratch& x, in
   const int E = p.E, K = p.K;
   float *v = x.scores + static_cast<size_t>(t) * 2 * E, *key = v + E;
 #pragma unroll 1
-  for (int e = lane; e < E; e += 32) {
-    const float l = __ldcg(p.logits + static_cast<size_t>(t) * E + e);
-    const float s = p.scoring ? sigmoid_once(l) : l;
-    v[e] = s;
-    key[e] = p.select_bias ? __fadd_rn(s, __ldg(p.select_bias + e)) : s;
+  for (int e0 = lane; e0 < E; e0 += 256) {
+    float l[8];                    // in flight together
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      l[i] = e0 + 32 * i < E ? __ldcg(p.logits + static_cast<size_t>(t) * E + e0 + 32 * i) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = e0 + 32 * i;
+      if (e >= E) break;
+      const float s = p.scoring ? sigmoid_once(l[i]) : l[i];
+      v[e] = s;
+      key[e] = p.select_bias ? __fadd_rn(s, __ldg(p.select_bias + e)) : s;
+    }
   }
   __syncwarp();
   uint32_t taken = 0;              // bit i: entry lane + 32 i is not eligible
@@ -250,7 +295,9 @@ __device__ __forceinline__ void choose(const Params& p, Fixed& f, Scratch& x, in
       if (!((g >> 5 ? open[1] : open[0]) >> (g & 31) & 1u)) taken |= 1u << i;
     }
   }
-  const int id = E <= 256 ? pick<8>(key, E, K, lane, taken) : pick<32>(key, E, K, lane, taken);
+  const int id = E <= 128   ? pick<4>(key, E, K, lane, taken)
+                 : E <= 256 ? pick<8>(key, E, K, lane, taken)
+                            : pick_many(key, E, K, lane, taken);
   const float sel = v[id];
   float num = sel, den = 0.0f;
   const float m = __shfl_sync(0xffffffffu, sel, 0);
@@ -669,16 +716,6 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
   for (int e = tid; e < E; e += kThreads) x.mask[e] = 0u;
   grid_dep_wait();
   grid_dep_launch();
-  // the exponential's table, for the choice, and the tokens: loads whose values nobody waits for, so
-  // that later ones find a line a lane in L1 (24 KB of it, what the ring leaves)
-  {
-    float unused;
-    if (warp == kWarps - 1) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(kExpTabDev + 4 * lane));
-    const int lines = min(T * H / 64, 192);
-#pragma unroll 1
-    for (int i = tid; i < lines; i += kThreads)
-      asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(p.x + static_cast<size_t>(i) * 64));
-  }
   // the arrivals of earlier launches are a multiple of the CTAs, and before this CTA's own nobody passes
   unsigned long long arrivals = 0;
   if (tid == 0) arrivals = (*reinterpret_cast<volatile unsigned long long*>(p.barrier) / gridDim.x + 1) * gridDim.x;
@@ -710,6 +747,14 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
   // ---- choice of experts
 #pragma unroll 1
   for (int t = warp; t < T; t += kWarps) choose(p, f, x, t, lane);
+  // Meanwhile the other warps bring the tokens to L1, where the barrier's acquire has left nothing, if
+  // they fit into the 24 KB that the ring leaves: loads of their 32-byte sectors whose values nobody waits for
+  if (warp >= T && T * H <= 12 * 1024) {
+    float unused;
+#pragma unroll 1
+    for (int i = (warp - T) * 32 + lane; i < T * H / 16; i += (kWarps - T) * 32)
+      asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(unused) : "l"(p.x + static_cast<size_t>(i) * 16));
+  }
   if (tid < T) f.gate[tid] = p.w_gate ? sigmoid_once(__ldcg(p.gate + tid)) : 1.0f;
   __syncthreads();
   if (warp == 0) group_experts(p, f, x, lane);
