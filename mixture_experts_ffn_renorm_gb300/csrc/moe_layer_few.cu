@@ -121,8 +121,8 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, int
       : "memory");
 }
 
-// Bounded wait; false, at once, when this CTA has given up.  Callers go on either way: every
-// loop is finite, so a CTA that gave up runs to its end without waiting again.
+// Bounded wait; false when it ran out or this CTA has given up.  Callers go on either way: every
+// loop is finite, so a warp that gave up runs to its end without waiting again.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                      const Params& p) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -788,6 +788,9 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
   }
   int s = 0;
   uint32_t parity = 0;
+  // A warp whose wait ran out neither waits nor copies again: the slot's barrier is a phase behind from
+  // there on, where a wait would return at once and a copy would arm the same phase twice.
+  bool gave_up = false;
   // gate/up: sums of the expert's tokens, four by four; down: of tokens 0-7 and 8-15
   float sum[4][4] = {};
   auto turn = [&]() {                            // the next four's sums first
@@ -810,8 +813,10 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
       const uint8_t* at = slots + (warp * kSlots + s) * kSlotBytes;
       bool landed = false, waited = false;
       auto take = [&]() {
-        if (!waited) landed = __all_sync(0xffffffffu, wait(bars + 8 * s, parity, abort_flag, p));
+        if (waited) return;
         waited = true;
+        landed = !gave_up && __all_sync(0xffffffffu, wait(bars + 8 * s, parity, abort_flag, p));
+        gave_up = !landed;
       };
       const int sh = st.shift(d), cols = 1 << sh;
       if (phase == 0) {
