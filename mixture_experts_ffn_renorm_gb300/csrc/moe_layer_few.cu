@@ -10,10 +10,9 @@
 //   logits    a warp per (expert, two tokens), as in the router's small batches; grid barrier
 //   choice    every CTA selects the experts of all tokens (the router's order and bits) and
 //             groups the T K pairs by expert
-//   gate/up   the features of the touched experts, in one line, cut evenly over the CTAs:
-//             act[p, n] = silu(gate) up in f32 to the workspace; grid barrier
-//   down      a CTA owns H / CTAs output columns for all experts: it sums routed_scale w y
-//             over a token's experts in shared memory, so no partial sums cross CTAs
+//   gate/up   the features of the touched experts in one line, each as long as its expert's tokens make it,
+//             cut evenly over the CTAs: w[p] act[p, n] to the workspace; grid barrier
+//   down      a CTA owns H / CTAs output columns for all experts, so no partial sums cross CTAs
 //
 // The barrier between gate/up and down costs no bandwidth: the copies run ahead of it, since
 // the down rows do not depend on it.
@@ -35,9 +34,15 @@
 // All sums are f32 in a fixed order, nothing between the weights and the output is narrowed, and
 // no atomics touch data.
 //
-// Chunks shared by eight warps, with a group barrier after each, took 80 us for one token (2048 x 768,
-// 128 experts, 8 of them chosen): 13000 cycles a chunk of index arithmetic and barriers.  Single
-// warps with multiply-adds took 37 us, and 319 for 16 tokens, where an expert of many tokens held all SMs up.
+// What it measured (2048 x 768, 128 experts, 8 of them chosen; bf16): one token 27.4 us, of which 3.2 until
+// the logits have crossed the grid, 3 the choice, 15 gate/up (7.4 of them the weights' way), 1 the second barrier, 3.5 down;
+// 16 tokens 151 us at 5.2 TB/s.  Steps on the way, us for one token and for 16:
+//   chunks shared by eight warps, a group barrier after each      80  681   13000 cycles a chunk of index arithmetic
+//   a ring per warp, single rows and multiply-adds                37  319   an expert of many tokens held all SMs up
+//   mma.sync, three parts, one loop for both phases               33  186   (140 KB of code had to come from L2)
+//   TMA boxes, a piece's token loads in flight together           28  187   (680 cycles each, in turn, before)
+//   features dealt by their experts' tokens                       28  158
+//   sorted heads in the choice, tokens to L1 beside it            27  151
 #include <atomic>
 
 #include "fp8_common.cuh"
@@ -60,7 +65,6 @@ constexpr int kFeat = 4;
 constexpr int kGuBlocks = 8, kDnBlocks = 4;
 constexpr int kSlotBytes = 8192;
 static_assert(2 * kFeat * kGuBlocks * 128 == kSlotBytes && 16 * kDnBlocks * 128 == kSlotBytes, "slot");
-constexpr unsigned long long kCopyGraceNs = 100000ull;
 constexpr int kRing = kWarps * kSlots * kSlotBytes;
 
 struct Params {
@@ -251,28 +255,34 @@ __device__ __forceinline__ void choose(const Params& p, Fixed& f, Scratch& x, in
   __syncwarp();
   uint32_t taken = 0;              // bit i: entry lane + 32 i is not eligible
   if (p.n_group > 1) {
-    // lane g scores groups g and g + 32 by their best key or two; the topk_group best stay open
+    // A group is scored by its best key or two: `sub` lanes look through its experts, each keeping two,
+    // and join them.  A key and its value are one 64-bit number, so that the larger is the better.
+    // Lane g then has the keys of groups g and g + 32; the topk_group best stay open.
     const int gs = E / p.n_group;
+    const int sub = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : 8;
     uint32_t gkey[2] = {0u, 0u}, open[2] = {0u, 0u}, gtaken = 0;
 #pragma unroll 1
-    for (int q = 0; q < 2; ++q) {
-      const int g = lane + 32 * q;
-      uint32_t k = 0u;
-      if (g < p.n_group) {
-        int b0 = -1, b1 = -1;
-#pragma unroll 1
-        for (int e = g * gs; e < g * gs + gs; ++e) {
-          if (b0 < 0 || route::ranks_above(key[e], e, key[b0], b0)) {
-            b1 = b0;
-            b0 = e;
-          } else if (b1 < 0 || route::ranks_above(key[e], e, key[b1], b1)) {
-            b1 = e;
-          }
+    for (int q = 0; q < (p.n_group > 32 ? 2 : 1); ++q) {
+      const int g = 32 * q + lane / sub;
+      unsigned long long b0 = 0, b1 = 0;
+      if (g < p.n_group)
+#pragma unroll 2
+        for (int e = g * gs + lane % sub; e < g * gs + gs; e += sub) {
+          const unsigned long long k =
+              (route::rank_key(key[e]) + 1ull) << 32 | __float_as_uint(key[e]);
+          b1 = max(b1, min(b0, k));
+          b0 = max(b0, k);
         }
-        k = route::rank_key(p.group_score ? __fadd_rn(key[b0], key[b1]) : key[b0]);
+#pragma unroll 1
+      for (int o = 1; o < sub; o <<= 1) {
+        const unsigned long long c0 = __shfl_xor_sync(0xffffffffu, b0, o), c1 = __shfl_xor_sync(0xffffffffu, b1, o);
+        b1 = max(min(b0, c0), max(b1, c1));
+        b0 = max(b0, c0);
       }
-      if (q) gkey[1] = k;
-      else gkey[0] = k;
+      const float best = __uint_as_float(static_cast<uint32_t>(b0)), next = __uint_as_float(static_cast<uint32_t>(b1));
+      const uint32_t k = route::rank_key(p.group_score ? __fadd_rn(best, next) : best);
+      if (q) gkey[1] = __shfl_sync(0xffffffffu, k, lane * sub & 31);
+      else gkey[0] = __shfl_sync(0xffffffffu, k, lane * sub & 31);
     }
 #pragma unroll 1
     for (int j = 0; j < p.topk_group; ++j) {
@@ -518,7 +528,6 @@ struct Stream {
   // the copy of a piece (one lane).  Only whole blocks of a row are copied: what is left of it is read
   // from where it lies.  Rows behind the expert's are zeros, those of the next CTA are not used.
   __device__ void issue(const Cursor& c, uint32_t slot, uint32_t bar) const {
-    if (c.phase == 2) return;
     const int sh = shift(c.d), block = c.k >> sh;
     if (c.k + (1 << sh) > (c.phase == 0 ? p.H : inner(c.d))) {
       ptx::mbar_arrive(bar);
@@ -779,18 +788,24 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
   const int D = st.D, g = lane >> 2, q = lane & 3;
   const uint32_t ring = ptx::smem_u32(slots) + warp * kSlots * kSlotBytes, bars = ptx::smem_u32(&f.full[warp][0]);
   Cursor c[kSlots], ahead = st.begin();          // of the pieces in the slots, the oldest first
-#pragma unroll 1
-  for (int s = 0; s < kSlots; ++s) {
-    if (lane == 0) st.issue(ahead, ring + s * kSlotBytes, bars + 8 * s);
-    c[0] = c[1];
-    c[1] = ahead;
-    if (ahead.phase < 2) st.next(ahead);
-  }
   int s = 0;
   uint32_t parity = 0;
   // A warp whose wait ran out neither waits nor copies again: the slot's barrier is a phase behind from
   // there on, where a wait would return at once and a copy would arm the same phase twice.
   bool gave_up = false;
+  uint32_t armed = 0;              // bit s: parity of slot s's last copy; bit s + 2: it has had one
+  auto arm = [&](int slot) {
+    if (ahead.phase == 2) return;
+    if (lane == 0) st.issue(ahead, ring + slot * kSlotBytes, bars + 8 * slot);
+    armed = (armed >> (slot + 2) & 1u ? armed ^ 1u << slot : armed) | 4u << slot;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kSlots; ++i) {
+    arm(i);
+    c[0] = c[1];
+    c[1] = ahead;
+    if (ahead.phase < 2) st.next(ahead);
+  }
   // gate/up: sums of the expert's tokens, four by four; down: of tokens 0-7 and 8-15
   float sum[4][4] = {};
   auto turn = [&]() {                            // the next four's sums first
@@ -967,7 +982,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
         }
       }
       __syncwarp();                              // all lanes have read the slot
-      if (landed && lane == 0) st.issue(ahead, ring + s * kSlotBytes, bars + 8 * s);
+      if (landed) arm(s);
       c[0] = c[1];
       c[1] = ahead;
       if (ahead.phase < 2) st.next(ahead);
@@ -1004,12 +1019,10 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
     if (p.residual) v += bf16_bits_to_f32(p.residual[at]);
     p.out[at] = f32_to_bf16_bits(v);
   }
-  // a CTA that gave up lets its copies land before it ends
-  if (*abort_flag) {
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
-    }
-  }
+  // a warp that gave up lets its copies land before it ends
+  if (gave_up)
+    for (int i = 0; i < kSlots; ++i)
+      if (armed >> (i + 2) & 1u) gemm::spin_bounded(bars + 8 * i, armed >> i & 1u);
 }
 
 // ------------------------------------------------------------------ host side
