@@ -12,8 +12,8 @@ constexpr float kTanhScale = 0.79788456f;   // sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
 
 // act(z) and d act / d z of two values at once, in pairs of f32 (one instruction for both of a pair's
-// additions, multiplications and multiply-adds): with single values their instructions bounded the
-// products' epilogue and its gradient, not the tensor core or HBM.
+// additions, multiplications and multiply-adds): their instructions bound the epilogue's gradient
+// (70.7 us with single values, 51.2 with pairs and four rows in flight; 32768 x 768, GELU).
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));

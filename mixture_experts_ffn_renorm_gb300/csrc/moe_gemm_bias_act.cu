@@ -17,14 +17,21 @@
 //               turn.  A thread holds pairs of consecutive rows of four output columns (16 x 256-bit reads of
 //               tensor memory), so that bias, activation and weight run on pairs of f32, and matrix stores
 //               transpose the rounded pairs on their way to shared memory, from where rows leave as
-//               16-byte pieces; the residual's rows come the same way back.  (A column of 32 rows a thread,
-//               stored as 32 single values, took 26000 cycles a tile with GELU and z, twice its products.)
+//               16-byte pieces; the residual's rows come the same way back.  It runs under the next
+//               tile's products.
+//
+// 65536 rows of 2048 x 768 in 128 groups, GELU and z take 191 us: 1.08 PFLOP/s and 4.6 TB/s, where HBM alone
+// takes 129 and the products 109.  32768 rows against [K, N] weights take 106 (HBM 87).  What is left lies in the tiles' shares: each
+// pair takes every n-th tile whatever its rows (the busiest has 17 % more than the mean), and 32 KB go
+// from L2 to every SM per 64 of K.  (All column blocks of a row block in turn on one pair: 220 us, as
+// the weights come from HBM again.)
 //
 // Weights [G, N, K] are K-major operands.  Weights [G, K, N] (the rows' gradient of a layer's
 // own weights) are MN-major ones, boxes of 64 columns x 64 K rows in the same stage: no
 // transposed copy is kept.  Both are seen through three-dimensional maps, so a group's ragged
 // end reads zeros and never its neighbour.
 //
+// Calls of at most 16 rows and weights [G, N, K] have a kernel of their own, below.
 // Calls whose tiles cannot fill the pairs (few rows) cut K into ranges: each leaves f32 sums in
 // the workspace and a second kernel adds them in range order and applies the epilogue.
 #include <atomic>
@@ -557,6 +564,136 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
+// ------------------------------------------------------------------ calls of at most 16 rows
+constexpr int kFewRows = 16;         // P
+constexpr int kFewWarps = 8;
+constexpr int kFewCols = 8;          // output columns of a warp
+constexpr int kFewFlight = 4;        // blocks of 64 K that a warp loads together
+
+// 16 bytes, or zeros
+__device__ __forceinline__ uint4 load_or_zero(const uint4* from, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(from), "r"(there ? 1 : 0));
+  return v;
+}
+
+// Weights [G, N, K].  A warp holds 8 output columns of one group and takes K in turn with the other `slices` - 1
+// of them, 64 at a time: a lane has 2 x 16 bytes of one of the columns, and the products of 16 rows x 8 columns
+// are mma.sync's; a CTA joins the slices' sums in order.  What bounds it is the weights' way from memory: no tensor
+// memory to allocate, no second launch, and a warp's loads of four blocks leave at once.  (A lane's 16
+// bytes lie elsewhere in the contraction than the MMA has them, alike on both sides.)
+// One row of 4096 x 1024 takes 4.3 us from HBM in a row of calls, the CTA pairs' two launches 9.2; 8192 x 8192 24 against 29;
+// 1024 x 4096 3.7 against 9.1.  Eight blocks in flight are slower (4096 x 4096: 11.1 against 7.9), as one CTA fits an SM then.
+// kTwo: more than eight rows.
+template <bool kTwo>
+__global__ void __launch_bounds__(32 * kFewWarps, 2)
+few_rows_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, const Params p, const int slices) {
+  __shared__ float s_sum[kFewWarps][kFewRows][kFewCols];
+  count_launch(p.launches, MOE_KID_GEMM_BIAS_ACT);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  // the blockIdx.y-th group that has rows
+  int group = 0, r0 = 0, rows = p.P;
+  if (p.group_offsets) {
+    int left = static_cast<int>(blockIdx.y);
+    rows = 0;
+    for (int i0 = 0; i0 < p.G; i0 += 32) {
+      const int i = i0 + lane;
+      const int lo = min(max(i < p.G ? __ldg(p.group_offsets + i) : 0, 0), p.P);
+      const int hi = min(max(i < p.G ? __ldg(p.group_offsets + i + 1) : 0, 0), p.P);
+      uint32_t has = __ballot_sync(0xffffffffu, hi > lo);
+      const int n = __popc(has);
+      if (left >= n) {
+        left -= n;
+        continue;
+      }
+      for (; left > 0; --left) has &= has - 1u;
+      const int at = __ffs(has) - 1;
+      group = i0 + at;
+      r0 = __shfl_sync(0xffffffffu, lo, at);
+      rows = __shfl_sync(0xffffffffu, hi - lo, at);
+      break;
+    }
+    if (rows == 0) return;
+  }
+  const int per = kFewWarps / slices;            // blocks of columns of a CTA
+  const int slice = warp / per, n0 = (blockIdx.x * per + warp % per) * kFewCols, K = p.K, vecs = n0 < p.N ? K >> 3 : 0;
+  const uint4* wv = reinterpret_cast<const uint4*>(w + (static_cast<size_t>(group) * p.N + n0 + g) * K);
+  const uint4* a0 = reinterpret_cast<const uint4*>(a + static_cast<size_t>(r0 + min(g, rows - 1)) * K);
+  const uint4* a1 = reinterpret_cast<const uint4*>(a + static_cast<size_t>(r0 + min(g + 8, rows - 1)) * K);
+  const bool has0 = g < rows, has1 = kTwo && g + 8 < rows;
+  float c[2][4] = {};                // two sums, two chains: rows g (0, 1) and g + 8 (2, 3), columns 2 q, 2 q + 1
+#pragma unroll 1
+  for (int b0 = slice; b0 * 8 < vecs; b0 += slices * kFewFlight) {
+    uint4 b[kFewFlight][2], u[kFewFlight][2], v[kTwo ? kFewFlight : 1][2];
+#pragma unroll
+    for (int i = 0; i < kFewFlight; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = (b0 + i * slices) * 8 + 2 * q + h;
+        b[i][h] = load_or_zero(wv + at, at < vecs);
+        u[i][h] = load_or_zero(a0 + at, has0 && at < vecs);
+        if (kTwo) v[i][h] = load_or_zero(a1 + at, has1 && at < vecs);
+      }
+    // keeps the products behind all of the loads: ptxas else sinks each load to its use, in turn
+    asm volatile("fence.acq_rel.cta;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kFewFlight; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x = u[i][h], y = kTwo ? v[kTwo ? i : 0][h] : make_uint4(0, 0, 0, 0), w4 = b[i][h];
+        ptx::mma_m16n8k16(c[0], x.x, y.x, x.y, y.y, w4.x, w4.y);
+        ptx::mma_m16n8k16(c[1], x.z, y.z, x.w, y.w, w4.z, w4.w);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s_sum[warp][g + 8 * (j >> 1)][2 * q + (j & 1)] = c[0][j] + c[1][j];
+  __syncthreads();
+  // two columns a thread
+#pragma unroll 1
+  for (int i = threadIdx.x; i < per * kFewCols / 2 * rows; i += 32 * kFewWarps) {
+    const int j = i / (per * kFewCols / 2), c2 = i - j * (per * kFewCols / 2), block = c2 / (kFewCols / 2);
+    const int n = blockIdx.x * per * kFewCols + 2 * c2, r = r0 + j;
+    if (n >= p.N) continue;
+    float2 z = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kFewWarps; ++k) {
+      if (k >= slices) break;
+      const float2 v = *reinterpret_cast<const float2*>(&s_sum[k * per + block][j][2 * c2 - block * kFewCols]);
+      z.x += v.x;
+      z.y += v.y;
+    }
+    if (p.bias) {
+      z.x += __ldg(p.bias + static_cast<size_t>(group) * p.N + n);
+      z.y += __ldg(p.bias + static_cast<size_t>(group) * p.N + n + 1);
+    }
+    if (p.z) *reinterpret_cast<uint32_t*>(p.z + static_cast<size_t>(r) * p.N + n) = pack_bf16x2(z.x, z.y);
+    const int d = p.row_to_pair ? __ldg(p.row_to_pair + r) : r;
+    if (d < 0 || d >= p.P) continue;
+    float2 y = z;
+    act::dispatch(p.activation, [&](auto k) {
+      y = ptx::unpair(act::apply2<decltype(k)::value>(ptx::pair(__float_as_uint(z.x), __float_as_uint(z.y))));
+    });
+    const size_t to = static_cast<size_t>(d) * p.N + n;
+    if (p.pair_weight) {
+      const float f = __ldg(p.pair_weight + d);
+      y.x = __fmul_rn(y.x, f);
+      y.y = __fmul_rn(y.y, f);
+    }
+    if (p.residual) {
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(p.residual + to);
+      y.x = __fadd_rn(y.x, __uint_as_float(u << 16));
+      y.y = __fadd_rn(y.y, __uint_as_float(u & 0xFFFF0000u));
+    }
+    *reinterpret_cast<uint32_t*>(p.out + to) = pack_bf16x2(y.x, y.y);
+  }
+}
+
 // ------------------------------------------------------------------ host side
 long long row_blocks(int P, int G) {
   return G == 1 ? (static_cast<long long>(P) + kRowBlock - 1) / kRowBlock : P / kRowBlock + (G < P ? G : P);
@@ -570,6 +707,17 @@ int ranges_of(long long blocks, int K, int N) {
   s = s < most ? s : most;
   s = s < kMaxRanges ? s : kMaxRanges;
   return s < 1 ? 1 : static_cast<int>(s);
+}
+// Slices of K in the kernel of few rows: the most with which all CTAs (two per SM) run at once.  4096 x 4096, one row:
+// 7.9 us with 4 slices and 256 CTAs, 9.1 with 8 and 512, 10.7 with 2 and 128.  Where a single slice
+// leaves more CTAs than that, more than eight rows take the pairs' kernel (0): 16 rows of 1024 x 32768 19 us
+// against 15.5, while eight rows take 14.7.
+int few_slices(int P, int N, int G) {
+  for (int s = kFewWarps; s; s >>= 1) {
+    const long long cols = kFewCols * kFewWarps / s;
+    if ((N + cols - 1) / cols * (G < P ? G : P) <= 2 * sm_count()) return s;
+  }
+  return P > 8 ? 0 : 1;
 }
 size_t part_bytes(int ranges, long long rows, int N) {
   return ranges < 2 ? 0 : static_cast<size_t>(ranges) * N * ((rows + 3) & ~3ll) * 4;
@@ -691,6 +839,19 @@ extern "C" int moe_grouped_gemm_bias_act_bf16(const void* a_bf16, const void* w_
   p.row_to_pair = row_to_pair;
   p.residual = static_cast<const uint16_t*>(residual_bf16);
   p.out = static_cast<uint16_t*>(out_bf16);
+  if (w_layout == MOE_W_ROWS && P <= kFewRows) {
+    const int slices = few_slices(P, N, G), cols = kFewCols * kFewWarps / (slices ? slices : 1);
+    if (slices) {
+      const DeviceDiag diag = device_diag();
+      p.launches = diag.launches;
+      return launch_status(launch_kernel(P > 8 ? few_rows_kernel<true> : few_rows_kernel<false>,
+                                         dim3((N + cols - 1) / cols, G < P ? G : P), dim3(32 * kFewWarps), 0,
+                                         static_cast<cudaStream_t>(stream), nullptr, 0,
+                                         static_cast<const uint16_t*>(a_bf16), static_cast<const uint16_t*>(w_bf16), p,
+                                         slices),
+                           op);
+    }
+  }
   p.part_rows = (P + 3) & ~3;
   p.ranges = ranges_of(row_blocks(P, G), K, N);
   const size_t one = part_bytes(2, P, N) / 2, fit = workspace ? ws_bytes / one : 0;

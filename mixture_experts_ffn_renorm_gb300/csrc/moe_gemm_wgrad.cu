@@ -18,6 +18,10 @@
 // group's matrix.  (With loads from there and stores of 16 bytes a lane a tile took its warps 1400
 // instructions and 14600 cycles, six times its products.)
 //
+// 32768 rows of 768 x 2048 in 128 groups take 177 us, 5.6 TB/s: 805 MB of gradients leave, 185 MB of rows come in.
+// 777 rows of 400 x 1040 in 13 groups with add_to take 25 us (6.7 at HBM's rate): one tile an SM, whose load,
+// products and stores come in turn.
+//
 // With a few groups of many rows there are fewer tiles than SMs: the rows are cut into ranges whose
 // sums go to the workspace, and a second kernel adds them in range order.
 #include <atomic>

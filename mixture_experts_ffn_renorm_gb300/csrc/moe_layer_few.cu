@@ -540,17 +540,6 @@ struct Stream {
   }
 };
 
-// c += A B for 16 rows x 8 tokens x 16 columns, bf16 and f32.  Lane (g, q) = (lane / 4, lane % 4) holds
-// A's rows g and g + 8, B's token g, and of c rows g (0, 1) and g + 8 (2, 3), tokens 2 q and 2 q + 1.
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // four E4M3 codes as bf16, exactly
 __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
   const __half2 a = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3));
@@ -584,7 +573,8 @@ __device__ __forceinline__ void products(float (&c)[2][4], const Row<kQ>& lo, co
 #pragma unroll
   for (int j = 0; j < (kQ ? 4 : 2); ++j) {
     const uint4& b = u[kQ ? j >> 1 : 0];
-    mma(c[j & 1], lo.v[j][0], hi.v[j][0], lo.v[j][1], hi.v[j][1], j & 1 ? b.z : b.x, j & 1 ? b.w : b.y);
+    // rows of weights x columns of tokens
+    ptx::mma_m16n8k16(c[j & 1], lo.v[j][0], hi.v[j][0], lo.v[j][1], hi.v[j][1], j & 1 ? b.z : b.x, j & 1 ? b.w : b.y);
   }
 }
 // c += the two sums, with FP8 times the scales of rows 0-7 and 8-15; and clears them

@@ -132,6 +132,18 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&v)[4
                : "memory");
 }
 
+// c += A B for 16 rows x 8 columns x 16 of K, bf16 and f32.  Lane (g, q) = (lane / 4, lane % 4) holds of
+// A's rows g (a0, a2) and g + 8 (a1, a3) and of B's column g the places 2 q, 2 q + 1 of the first
+// (a0, a1, b0) and second eight, and of c the columns 2 q, 2 q + 1 of rows g (0, 1) and g + 8 (2, 3).
+__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // Shared-memory matrix descriptor of an MN-major operand (the 16-bit values of one K row
 // contiguous), as TMA SWIZZLE_128B boxes of 64 values x rows write it: blocks of 64 values
 // `lbo` bytes apart (leading byte offset), groups of 8 K rows 1024 bytes apart (stride byte

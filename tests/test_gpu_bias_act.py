@@ -134,7 +134,7 @@ def test_a_groups_end_reads_zeros_and_not_its_neighbour(columns):
 def test_infinities_and_nan_through_the_activations():
     v = torch.tensor([float("inf"), float("-inf"), float("nan"), 0.0, -0.0, 30.0, -30.0, 1e-30], device=DEV)
     for kind in range(6):
-        for P in (1, 600):           # the join and the tile's own epilogue
+        for P in (1, 20, 600):       # the few rows' epilogue, the join's and the tile's own
             c = Product(P, 2048, 8, kind=kind)
             c.a.zero_()
             c.bias[0] = v
@@ -148,17 +148,48 @@ def test_infinities_and_nan_through_the_activations():
 
 
 def test_few_rows_split_k_and_no_workspace_only_costs_speed():
-    c = Product(2, 4096, 1024, residual=True)
+    c = Product(20, 4096, 1024, residual=True)
     before = launches()
     c.run()
     assert launched_since(before, "bias_act_join") == 1
-    for size in (None, c.ws[: 2 * 1024 * 4 * 4], c.ws[: 1024]):
+    for size in (None, c.ws[: 2 * 1024 * 20 * 4], c.ws[: 1024]):
         before = launches()
         c.out.fill_(0)
         c.call(ws=size)
         torch.cuda.synchronize()
         c.check(c.out)
         assert launched_since(before, "bias_act_join") == (1 if size is not None and size.numel() > 30000 else 0)
+
+
+@pytest.mark.parametrize("P,K,N,sizes", [
+    (1, 8, 8, None), (7, 64, 72, None), (8, 1032, 1000, None), (9, 72, 40, None), (16, 520, 2048, None),
+    (8, 72, 40000, None), (16, 136, 19456, None), (16, 136, 19464, None),       # one slice; eight rows' and more rows' limit
+    (16, 264, 392, [1] * 16), (16, 264, 392, [0, 9, 0, 0, 7]), (13, 200, 136, [0] * 40 + [1, 0, 8] + [0] * 70 + [2]),
+    (16, 72, 1288, [1] * 16 + [0] * 1008), (5, 72, 136, [0, 0, 0]),
+])
+def test_few_rows(P, K, N, sizes):
+    # one launch, without a workspace; rows of no group stay as they were
+    c = Product(P, K, N, len(sizes) if sizes else 1, offsets(sizes) if sizes else None, kind=R.GELU, pre=True, scatter=True,
+                weight=True, residual=True)
+    before = launches()
+    c.ws = None
+    c.run()
+    if P <= 8 or N < 19464:
+        assert launched_since(before, "gemm_bias_act") == 1 and launched_since(before, "bias_act_join") == 0
+
+
+def test_few_rows_read_no_other_group_and_spread_no_nan():
+    c = Product(12, 200, 136, 3, offsets([3, 4, 5]), bias=False, kind=R.SILU, pre=True)
+    c.w[0] = float("nan")
+    c.w[2] = float("inf")
+    c.a[:3] = float("nan")
+    c.a[5, 7] = float("nan")
+    c.call()
+    torch.cuda.synchronize()
+    z, dz, y, dy = R.product(c.a, c.w, False, None, R.SILU, c.off, 3)
+    ok = torch.tensor([3, 4, 6], device=DEV)
+    assert (c.out[ok].double() - y[ok]).abs().le(dy[ok] + R.UBF * (y[ok].abs() + dy[ok])).all()
+    assert c.out[:3].isnan().all() and c.out[5].isnan().all() and not c.out[7:].isfinite().any()
 
 
 def test_a_workspace_of_the_most_rows_serves_fewer():
@@ -169,7 +200,7 @@ def test_a_workspace_of_the_most_rows_serves_fewer():
 
 
 def test_out_may_be_residual():
-    for P in (2, 500):
+    for P in (2, 20, 500):
         c = Product(P, 2048, 264, scatter=True, residual=True, kind=R.SILU)
         want = c.call().clone()
         res = c.res.clone()
@@ -179,7 +210,7 @@ def test_out_may_be_residual():
 
 
 def test_same_bits_each_time_in_graphs_and_on_other_streams():
-    for P in (4, 900):
+    for P in (4, 20, 900):
         c = Product(P, 2048, 776, kind=R.GELU, residual=True)
         want = c.call().clone()
         torch.cuda.synchronize()
