@@ -14,13 +14,14 @@
 // wait for this tile's stores.  So every 512 rows the products move to the other accumulator
 // of 256 columns and the epilogue warps (a thread: one row, 128 columns) add the finished one to
 // their registers.  Tiles of at most 512 rows skip the registers.  32 rows x 32 columns at a time leave
-// through 4 KB of shared memory per warp and a TMA store, which also cuts off what lies outside the
+// through 4 KB of shared memory and a TMA store, which also cuts off what lies outside the
 // group's matrix.  (With loads from there and stores of 16 bytes a lane a tile took its warps 1400
 // instructions and 14600 cycles, six times its products.)
 //
 // 32768 rows of 768 x 2048 in 128 groups take 177 us, 5.6 TB/s: 805 MB of gradients leave, 185 MB of rows come in.
-// 777 rows of 400 x 1040 in 13 groups with add_to take 25 us (6.7 at HBM's rate): one tile an SM, whose load,
-// products and stores come in turn.
+// With add_to 280 us, 6.4 TB/s: its boxes of 32 x 32 come by TMA, four under way to each warp, into the room of two of
+// the four stages, and leave from there (loads of a lane's own row, each a latency of HBM and 32 lines: 410 us).
+// 777 rows of 400 x 1040 in 13 groups with add_to take 16.8 us (6.7 at HBM's rate), two tiles an SM at most.
 //
 // With a few groups of many rows there are fewer tiles than SMs: the rows are cut into ranges whose
 // sums go to the workspace, and a second kernel adds them in range order.
@@ -35,7 +36,6 @@ namespace {
 constexpr int kThreads = 320;        // producer, MMA, eight epilogue warps
 constexpr int kTileN = 128, kTileK = 256;
 constexpr int kRowsStage = 64;
-constexpr int kStages = 4;
 constexpr int kBox = 64 * kRowsStage * 2;          // 64 columns x 64 rows
 constexpr int kABytes = kTileN / 64 * kBox, kBBytes = kTileK / 64 * kBox;
 constexpr int kChunk = 8;            // stages of one accumulator: 512 rows
@@ -53,15 +53,19 @@ struct Params {
   unsigned long long* launches;
 };
 
+// kAdd: with add_to.  Its tile is on the way in while the tile's products are added up, so it takes half of the
+// stages' room: four boxes of 32 x 32 a warp, where without it there is one, for the stores.
+template <bool kAdd>
 struct Smem {
+  static constexpr int kStages = kAdd ? 2 : 4, kBoxes = kAdd ? 4 : 1;
   static constexpr int A = 0;
   static constexpr int B = A + kStages * kABytes;
-  static constexpr int OUT = B + kStages * kBBytes;          // 8 warps x 4 KB, a TMA store's source
-  static constexpr int BARS = OUT + 8 * 4096;                // full, empty, tfull[2], tempty[2], drain
-  static constexpr int MISC = BARS + (2 * kStages + 5) * 8;
+  static constexpr int OUT = B + kStages * kBBytes;          // 8 warps x kBoxes x 4 KB, TMA stores' sources
+  static constexpr int BARS = OUT + 8 * kBoxes * 4096;       // full, empty, tfull[2], tempty[2], drain, add[8][4]
+  static constexpr int MISC = BARS + (2 * kStages + 5 + (kAdd ? 32 : 0)) * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
 };
-static_assert(Smem::ALLOC <= 227 * 1024, "shared memory");
+static_assert(Smem<false>::ALLOC <= 227 * 1024 && Smem<true>::ALLOC <= 227 * 1024, "shared memory");
 
 struct Tile {
   int g, n0, k0, range;
@@ -100,15 +104,28 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src,
                    reinterpret_cast<uint64_t>(m)),
                "r"(src), "r"(x), "r"(y), "r"(z)
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// this thread's stores have read their shared memory; have been written
-__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// this thread's stores but for the last kLater groups have read their shared memory; all have been written
+template <int kLater>
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLater) : "memory");
+}
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+template <bool kAdd>
 __global__ void __launch_bounds__(kThreads, 1)
 wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-             const __grid_constant__ CUtensorMap tmO, const Params p) {
+             const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmAdd, const Params p) {
+  using Smem = Smem<kAdd>;
+  constexpr int kStages = Smem::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -122,6 +139,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
   auto bar_tfull = [&](int a) { return ptx::smem_u32(bars + 2 * kStages + a); };
   auto bar_tempty = [&](int a) { return ptx::smem_u32(bars + 2 * kStages + 2 + a); };
   const uint32_t bar_drain = ptx::smem_u32(bars + 2 * kStages + 4);
+  auto bar_add = [&](int w, int c) { return ptx::smem_u32(bars + 2 * kStages + 5 + 4 * w + c); };
 
   count_launch(p.launches, MOE_KID_GEMM_WGRAD);
   if (threadIdx.x == 0) {
@@ -134,6 +152,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
       ptx::mbar_init(bar_tempty(a), 8);
     }
     ptx::mbar_init(bar_drain, 1);
+    if (kAdd)
+      for (int i = 0; i < 32; ++i) ptx::mbar_init(bar_add(0, i), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -239,7 +259,19 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 2) >> 2;      // TMEM lane quarter; 128 of the columns
-    const uint32_t ost = sb + Smem::OUT + (warp - 2) * 4096;
+    const uint32_t stage = sb + Smem::OUT + (warp - 2) * Smem::kBoxes * 4096;
+    // add_to's boxes arrive in this order, four of them under way: [tile][c]
+    uint32_t arrived = 0, asked = 0;
+    auto ask = [&](long long i, int c) {           // one lane
+      const Tile t = tile_of(p, i, tn, tk);
+      ptx::mbar_arrive_expect_tx(bar_add(warp - 2, c), 4096);
+      tma_load_3d(stage + c * 4096, &tmAdd, t.k0 + half * 128 + 32 * c, t.n0 + q * 32, t.g, bar_add(warp - 2, c));
+    };
+    if (kAdd && blockIdx.x < tiles) {
+      if (lane == 0)
+        for (int c = 0; c < 4; ++c) ask(blockIdx.x, c);
+      asked = 4;
+    }
     int acc = 0;
     uint32_t uses[2] = {0, 0};
     bool ok = true;
@@ -260,30 +292,50 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
       const Tile t = tile_of(p, i, tn, tk);
       const int steps = steps_of(t);
-      const int n = t.n0 + q * 32 + lane, z = t.range * p.G + t.g;
-      // columns [32 c, + 32) of this thread's row: add_to's, 128 bytes a row through the stage, a store
+      const int z = t.range * p.G + t.g;
+      // columns [32 c, + 32) of this thread's row: 128 bytes a row through a box, a store
       auto leave = [&](int c, float (&v)[32]) {
-        const int col = t.k0 + half * 128 + 32 * c;
-        if (p.add_to && n < p.N) {
-          const float* add = p.add_to + (static_cast<size_t>(t.g) * p.N + n) * p.K + col;
-          float4 a[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)              // K % 8 == 0: four columns are in or out together
-            a[k] = col + 4 * k < p.K ? *reinterpret_cast<const float4*>(add + 4 * k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            v[4 * k] += a[k].x; v[4 * k + 1] += a[k].y; v[4 * k + 2] += a[k].z; v[4 * k + 3] += a[k].w;
-          }
+        const int col = t.k0 + half * 128 + 32 * c, row0 = t.n0 + q * 32;
+        const uint32_t mine = stage + (kAdd ? c * 4096 : 0) + lane * 128;
+        if (kAdd) {
+          ok = wait_bar(bar_add(warp - 2, c), (arrived >> 2) & 1u, abort_flag, p.status, p.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return;
+          ++arrived;
+        } else {
+          if (lane == 0) tma_store_wait_read<0>();   // the box's last store
+          __syncwarp();
         }
-        if (lane == 0) tma_store_wait_read();      // the stage's last store
-        __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          ptx::st_shared_v4(ost + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(v[4 * k]),
-                            __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t at = mine + ((k ^ (lane & 7)) << 4);
+          if (kAdd) {
+            const uint4 a = ptx::ld_shared_v4(at);
+            v[4 * k] += __uint_as_float(a.x);
+            v[4 * k + 1] += __uint_as_float(a.y);
+            v[4 * k + 2] += __uint_as_float(a.z);
+            v[4 * k + 3] += __uint_as_float(a.w);
+          }
+          ptx::st_shared_v4(at, __float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                            __float_as_uint(v[4 * k + 3]));
+        }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && col < p.K && t.n0 + q * 32 < p.N) tma_store_3d(&tmO, ost, col, t.n0 + q * 32, z);
+        // a group for every box, also without a store: the last but one has been read when its box is asked for anew
+        if (lane == 0) {
+          if (col < p.K && row0 < p.N) tma_store_3d(&tmO, stage + (kAdd ? c * 4096 : 0), col, row0, z);
+          tma_store_commit();
+        }
+        if (kAdd && arrived > 1) {
+          const long long next = c == 0 ? i : i + gridDim.x;
+          if (next < tiles) {
+            if (lane == 0) {
+              tma_store_wait_read<1>();
+              ask(next, (c + 3) & 3);
+            }
+            ++asked;
+          }
+        }
       };
       if (steps <= kChunk) {
         uint32_t ta = 0;
@@ -306,7 +358,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
             for (int k = 0; k < 32; ++k) v[k] = 0.0f;
           }
           leave(c, v);
+          if (!ok) break;
         }
+        if (!ok) break;
         continue;
       }
       float sum[4][32];
@@ -330,9 +384,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
       }
       if (!ok) break;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) leave(c, sum[c]);
+      for (int c = 0; c < 4; ++c)
+        if (ok) leave(c, sum[c]);
+      if (!ok) break;
     }
     if (lane == 0) tma_store_wait();
+    // a warp that gave up lets its copies land
+    for (; kAdd && arrived < asked; ++arrived) spin_bounded(bar_add(warp - 2, arrived & 3), (arrived >> 2) & 1u);
   }
   // ---- exit: a CTA that gave up drains its copies and MMAs first
   __syncthreads();
@@ -387,6 +445,31 @@ int ranges_of(int P, int N, int K, int G) {
   s = s < most ? s : most;
   s = s < kMaxRanges ? s : kMaxRanges;
   return s < 1 ? 1 : static_cast<int>(s);
+}
+
+template <bool kAdd>
+int launch(const char* op, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const CUtensorMap& tadd,
+           const Params& p, cudaStream_t stream) {
+  constexpr int kBytes = Smem<kAdd>::ALLOC;
+  static std::atomic<int> configured[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    dev = -1;
+  }
+  const bool cache = dev >= 0 && dev < 64;
+  if (!cache || !configured[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(wgrad_kernel<kAdd>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+      return set_error(MOE_ERR_CUDA, "%s: cannot reserve %d bytes of shared memory: %s", op, kBytes,
+                       cudaGetErrorString(cudaGetLastError()));
+    if (cache) configured[dev].store(1, std::memory_order_release);
+  }
+  const long long tiles =
+      static_cast<long long>(p.G) * ((p.N - 1) / kTileN + 1) * ((p.K - 1) / kTileK + 1) * p.ranges;
+  const int sms = sm_count();
+  return launch_status(launch_kernel(wgrad_kernel<kAdd>, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)),
+                                     dim3(kThreads), kBytes, stream, nullptr, 0, ta, tb, to, tadd, p),
+                       op);
 }
 
 }  // namespace
@@ -450,27 +533,11 @@ extern "C" int moe_grouped_gemm_wgrad_bf16(const void* dz_bf16, const void* a_bf
   int rc;
   if ((rc = make_tmap(&ta, dz_bf16, P, N, kRowsStage, op, "dz")) != MOE_OK) return rc;
   if ((rc = make_tmap(&tb, a_bf16, P, K, kRowsStage, op, "a")) != MOE_OK) return rc;
-  CUtensorMap to;                    // 32 x 32 boxes of the groups' matrices, a range behind the other
+  CUtensorMap to, tadd;              // 32 x 32 boxes of the groups' matrices, a range behind the other
   if ((rc = make_tmap_f32_out(&to, p.out, G * p.ranges, N, K, op)) != MOE_OK) return rc;
-  static std::atomic<int> configured[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    dev = -1;
-  }
-  const bool cache = dev >= 0 && dev < 64;
-  if (!cache || !configured[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::ALLOC) != cudaSuccess)
-      return set_error(MOE_ERR_CUDA, "%s: cannot reserve %d bytes of shared memory: %s", op, Smem::ALLOC,
-                       cudaGetErrorString(cudaGetLastError()));
-    if (cache) configured[dev].store(1, std::memory_order_release);
-  }
-  const long long tiles =
-      static_cast<long long>(G) * ((N - 1) / kTileN + 1) * ((K - 1) / kTileK + 1) * p.ranges;
-  const int sms = sm_count();
-  rc = launch_status(launch_kernel(wgrad_kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kThreads),
-                                   Smem::ALLOC, s, nullptr, 0, ta, tb, to, p),
-                     op);
+  tadd = to;
+  if (p.add_to && (rc = make_tmap_f32_out(&tadd, const_cast<float*>(p.add_to), G, N, K, op)) != MOE_OK) return rc;
+  rc = p.add_to ? launch<true>(op, ta, tb, to, tadd, p, s) : launch<false>(op, ta, tb, to, tadd, p, s);
   if (rc != MOE_OK || p.ranges == 1) return rc;
   return launch_status(launch_kernel(wgrad_reduce_kernel, dim3(static_cast<unsigned>((n / 4 + 255) / 256)), dim3(256), 0, s,
                                      nullptr, 0, static_cast<const float*>(workspace), p.ranges,

@@ -406,3 +406,18 @@ def test_wgrad_ranges_add_in_place_and_same_bits():
         torch.cuda.synchronize()
         assert torch.equal(acc, want) and torch.equal(c.dw, want)
     assert m.moe_device_status() == 0
+
+
+def test_wgrad_adds_in_place_over_many_tiles():
+    # 320 tiles, several an SM; N and K end inside a box; groups without rows and of more than one accumulator
+    sizes = [0, 1100, 3, 0, 17, 64, 0, 513] * 5
+    c = Wgrad(sum(sizes), 136, 776, len(sizes), offsets(sizes), add=True)
+    c.run()
+    want = c.dw.clone()
+    for _ in range(3):
+        held = c.add.clone()
+        c.call(out=held, add=held)
+        torch.cuda.synchronize()
+        assert torch.equal(held, want)
+    c = Wgrad(100, 2560, 2560, 3, offsets([50, 0, 50]), add=True)
+    c.run()

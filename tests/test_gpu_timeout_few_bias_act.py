@@ -60,8 +60,9 @@ def test_product(columns):
     runs_out(c.call, (c.out,))
 
 
-def test_weight_gradient():
+@pytest.mark.parametrize("add", [False, True])
+def test_weight_gradient(add):
     # a tile per SM and group, 60 MB of rows: its first sums are 9 us of HBM away
     G = 152
-    c = Wgrad(512 * G, 128, 256, G, offsets([512] * G))
+    c = Wgrad(512 * G, 128, 256, G, offsets([512] * G), add=add)
     runs_out(c.call, (c.dw,))
