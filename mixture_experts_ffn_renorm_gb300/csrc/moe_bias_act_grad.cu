@@ -3,10 +3,13 @@
 //   dy[r] = dout[dst] * pair_weight[dst],  s = dy act'(z):  dz = bf16(s),
 //   grad_bias[g] = sum of s over g's rows,  grad_pair_weight[dst] = sum_n dout[dst,n] act(z[r,n])
 //
-// One pass over dout and z: what bounds it is HBM (6 bytes an element).  A CTA takes 64 rows x 256
+// One pass over dout and z: what bounds it is HBM (6 bytes an element).  A CTA takes up to 64 rows x 256
 // columns; a warp every eighth row, three of them at a time with all loads in flight, a lane 8
 // columns, so that its column sums are 8 registers and its row sums one butterfly each: four CTAs an SM.
-// 32768 x 768 with GELU, bias and row weights takes 45.5 us, 3.3 TB/s: Phi's instructions and HBM in turn.  A CTA's rows may meet several groups: at
+// 32768 x 768 with bias and row weights takes 42.2 us with GELU (3.6 TB/s), 37 with ReLU: Phi's instructions and HBM in
+// turn, then the second kernel; the pass alone takes 35, with ReLU 30 (HBM 22).  (A CTA for all columns of its rows, whose row sums need no second
+// kernel: 48 us, one wave of CTAs in step.  Rows brought to L2 before the groups are looked up: no gain.)
+// A CTA's rows may meet several groups: at
 // each group's end the warps' column sums are joined through shared memory in warp order and
 // leave as one partial row.  Block c and group g meet in partial row c + g: along the rows
 // either index or both step up, so no two meetings share one, and the second kernel finds a
@@ -18,7 +21,7 @@ namespace moe {
 namespace gemm {
 namespace {
 
-constexpr int kRows = 64;            // rows of a CTA
+constexpr int kRows = 64;            // rows of a CTA, or 32 or 16 (rows_of)
 constexpr int kCols = 256;           // columns of a CTA: 8 per lane
 constexpr int kWarps = 8;
 constexpr int kFlight = 3;           // rows of a warp whose loads are in flight together (2: 47.0 us, 4: 47.6)
@@ -30,7 +33,7 @@ struct BackParams {
   const float* pair_weight;
   const int32_t* row_to_pair;
   const int32_t* group_offsets;
-  int P, N, G;
+  int P, N, G, rows;
   uint16_t* dz;
   float* part_b;                     // [blocks + G][N] column sums, or null
   float* part_w;                     // [column blocks][P] row sums by row (one block: by dst), or null
@@ -56,42 +59,45 @@ bias_act_backward_kernel(const BackParams p) {
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int block = blockIdx.x, r_lo = block * kRows, r_hi = min(p.P, r_lo + kRows);
-  const int n = blockIdx.y * kCols + lane * 8;
-  const bool live = n < p.N;
+  const int block = blockIdx.x, r_lo = block * p.rows, r_hi = min(p.P, r_lo + p.rows);
+  // this warp's rows r_lo + warp + 8 i: destination and weight, lane i
+  int my_d = -1;
+  float my_w = 1.0f;
+  const int my_r = r_lo + warp + kWarps * lane;
+  if (my_r < r_hi) {
+    my_d = p.row_to_pair ? __ldg(p.row_to_pair + my_r) : my_r;
+    if (my_d < 0 || my_d >= p.P) my_d = -1;
+    else if (p.pair_weight) my_w = __ldg(p.pair_weight + my_d);
+  }
+  float row_sum = 0.0f;
+  bool seen = false;                 // its row is some group's
   // the last group that starts at or before the block's first row
   int before = 0;
   for (int g0 = 0; g0 < p.G; g0 += 32 * kWarps) {
     const int g = g0 + static_cast<int>(threadIdx.x);
     before += __syncthreads_count(g < p.G && offset_at(p.group_offsets, g, p.P) <= r_lo);
   }
+  const int n = blockIdx.y * kCols + lane * 8;
+  const bool live = n < p.N;
   int g = max(before - 1, 0);
   for (int r0 = max(r_lo, offset_at(p.group_offsets, g, p.P)); g < p.G; ++g) {
     const int r1 = min(r_hi, offset_at(p.group_offsets, g + 1, p.P));
     if (r1 > r0) {
       uint64_t sum[4] = {};
-      // destination and weight of this warp's rows: lane i row r0 + warp + 8 i
-      int my_d = -1;
-      float my_w = 1.0f;
-      const int my_r = r0 + warp + kWarps * lane;
-      if (my_r < r1) {
-        my_d = p.row_to_pair ? __ldg(p.row_to_pair + my_r) : my_r;
-        if (my_d < 0 || my_d >= p.P) my_d = -1;
-        else if (p.pair_weight) my_w = __ldg(p.pair_weight + my_d);
-      }
-      for (int i0 = 0; r0 + warp + kWarps * i0 < r1; i0 += kFlight) {
+      for (int i0 = (r0 - r_lo - warp + kWarps - 1) / kWarps; r_lo + warp + kWarps * i0 < r1; i0 += kFlight) {
         uint4 dv[kFlight], zv[kFlight];
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
-          const int r = r0 + warp + kWarps * (i0 + k), d = __shfl_sync(0xffffffffu, my_d, i0 + k);
-          dv[k] = live && d >= 0 ? *reinterpret_cast<const uint4*>(p.dout + static_cast<size_t>(d) * p.N + n)
-                                 : make_uint4(0, 0, 0, 0);
-          zv[k] = live && d >= 0 && p.z ? *reinterpret_cast<const uint4*>(p.z + static_cast<size_t>(r) * p.N + n)
-                                        : make_uint4(0, 0, 0, 0);
+          const int r = r_lo + warp + kWarps * (i0 + k), d = __shfl_sync(0xffffffffu, my_d, i0 + k);
+          const bool there = live && r < r1 && d >= 0;
+          dv[k] = there ? *reinterpret_cast<const uint4*>(p.dout + static_cast<size_t>(d) * p.N + n)
+                        : make_uint4(0, 0, 0, 0);
+          zv[k] = there && p.z ? *reinterpret_cast<const uint4*>(p.z + static_cast<size_t>(r) * p.N + n)
+                               : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
-          const int r = r0 + warp + kWarps * (i0 + k);
+          const int r = r_lo + warp + kWarps * (i0 + k);
           if (r >= r1) break;
           const int d = __shfl_sync(0xffffffffu, my_d, i0 + k);
           const float w = __shfl_sync(0xffffffffu, my_w, i0 + k);
@@ -118,9 +124,10 @@ bias_act_backward_kernel(const BackParams p) {
             float dot = u.x + u.y;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            // several column blocks: by row, for the sum; one: the gradient itself, by destination
-            if (lane == 0 && d >= 0)
-              p.part_w[gridDim.y > 1 ? static_cast<size_t>(blockIdx.y) * p.P + r : static_cast<size_t>(d)] = dot;
+            if (lane == i0 + k) {
+              row_sum += dot;
+              seen = true;
+            }
           }
         }
       }
@@ -141,6 +148,9 @@ bias_act_backward_kernel(const BackParams p) {
     }
     if (r0 >= r_hi) break;
   }
+  // several column blocks: by row, for the sum; one: the gradient itself, by destination
+  if (p.part_w && seen && my_d >= 0)
+    p.part_w[gridDim.y > 1 ? static_cast<size_t>(blockIdx.y) * p.P + my_r : static_cast<size_t>(my_d)] = row_sum;
 }
 
 // grad_bias: kSlices threads share a group's blocks of four columns, their sums joined in order; a CTA
@@ -153,17 +163,20 @@ bias_act_reduce_kernel(const BackParams p, float* __restrict__ grad_bias, float*
                        int col_blocks) {
   __shared__ float4 s_part[kSlices][64];
   count_launch(p.launches, MOE_KID_BIAS_ACT_REDUCE);
+  const int id = blockIdx.x;
+  const bool bias = id < p.G * bias_ctas;
+  const int g = bias ? id / bias_ctas : 0;
+  // the offsets are older than the kernel before, which started after what it waited for
+  const int r0 = offset_at(p.group_offsets, g, p.P), r1 = offset_at(p.group_offsets, bias ? g + 1 : p.G, p.P);
   grid_dep_wait();
   grid_dep_launch();
-  const int id = blockIdx.x;
-  if (id < p.G * bias_ctas) {
-    const int g = id / bias_ctas, x = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  if (bias) {
+    const int x = threadIdx.x & 63, slice = threadIdx.x >> 6;
     const int c = 4 * ((id - g * bias_ctas) * 64 + x);
-    const int r0 = offset_at(p.group_offsets, g, p.P), r1 = offset_at(p.group_offsets, g + 1, p.P);
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (r1 > r0 && c < p.N) {
       const float* q = p.part_b + static_cast<size_t>(g) * p.N + c;
-      const int b0 = r0 / kRows, n = (r1 - 1) / kRows - b0 + 1;
+      const int b0 = r0 / p.rows, n = (r1 - 1) / p.rows - b0 + 1;
 #pragma unroll 8
       for (int b = b0 + n * slice / kSlices; b < b0 + n * (slice + 1) / kSlices; ++b) {
         const float4 v = __ldcg(reinterpret_cast<const float4*>(q + static_cast<size_t>(b) * p.N));
@@ -184,8 +197,7 @@ bias_act_reduce_kernel(const BackParams p, float* __restrict__ grad_bias, float*
   }
   const long long i = static_cast<long long>(id - p.G * bias_ctas) * 256 + threadIdx.x;
   // rows outside every group, and destinations that no row has, keep what they hold
-  const int lo = offset_at(p.group_offsets, 0, p.P), hi = offset_at(p.group_offsets, p.G, p.P);
-  if (!grad_w || i < lo || i >= hi) return;
+  if (!grad_w || i < r0 || i >= r1) return;
   const int d = p.row_to_pair ? __ldg(p.row_to_pair + i) : static_cast<int>(i);
   if (d < 0 || d >= p.P) return;
   float s = __ldcg(p.part_w + i);
@@ -196,8 +208,18 @@ bias_act_reduce_kernel(const BackParams p, float* __restrict__ grad_bias, float*
 
 int blocks_of(int n, int size) { return n / size + (n % size != 0); }
 size_t pad(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+// Rows of a CTA: as many as leave two CTAs an SM.  777 x 1040 in 13 groups: 6.5 us with 16 rows, 9.9 with 64; 32768 x 768:
+// 42.2 with 64, 49 with 32, whose partial sums are twice as many.
+int rows_of(int P, int N) {
+  for (int r = kRows; r > 16; r >>= 1)
+    if (static_cast<long long>(blocks_of(P, r)) * blocks_of(N, kCols) >= 2ll * sm_count()) return r;
+  return 16;
+}
+// Partial sums of any number of rows up to P: with 16 or 32 rows a CTA there are at most 2 (2 SMs - 1) / column blocks
 size_t bias_bytes(int P, int N, int G) {
-  return pad((static_cast<size_t>(blocks_of(P, kRows)) + G) * N * 4);
+  const int most = blocks_of(P, rows_of(P, N)), few = 2 * ((2 * sm_count() - 1) / blocks_of(N, kCols));
+  const int fewer = few < blocks_of(P, 16) ? few : blocks_of(P, 16);
+  return pad((static_cast<size_t>(most > fewer ? most : fewer) + G) * N * 4);
 }
 
 }  // namespace
@@ -255,6 +277,7 @@ extern "C" int moe_bias_act_backward(const void* dout_bf16, const void* z_bf16, 
   p.row_to_pair = row_to_pair;
   p.group_offsets = group_offsets;
   p.P = P; p.N = N; p.G = G;
+  p.rows = rows_of(P, N);
   p.dz = static_cast<uint16_t*>(dz_bf16);
   p.part_b = grad_bias ? static_cast<float*>(workspace) : nullptr;
   float* joined = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (grad_bias ? bias_bytes(P, N, G) : 0));
@@ -265,7 +288,7 @@ extern "C" int moe_bias_act_backward(const void* dout_bf16, const void* z_bf16, 
         bias_act_backward_kernel<MOE_ACT_NONE>, bias_act_backward_kernel<MOE_ACT_RELU>,
         bias_act_backward_kernel<MOE_ACT_RELU2>, bias_act_backward_kernel<MOE_ACT_GELU>,
         bias_act_backward_kernel<MOE_ACT_GELU_TANH>, bias_act_backward_kernel<MOE_ACT_SILU>};
-    const int rc = launch_status(launch_kernel(kernels[activation], dim3(blocks_of(P, kRows), cb), dim3(32 * kWarps), 0,
+    const int rc = launch_status(launch_kernel(kernels[activation], dim3(blocks_of(P, p.rows), cb), dim3(32 * kWarps), 0,
                                                s, nullptr, 0, p),
                                  op);
     if (rc != MOE_OK) return rc;

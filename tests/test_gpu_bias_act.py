@@ -307,6 +307,22 @@ def test_backward_of_many_small_groups_and_rows_of_none():
     c.run()
 
 
+@pytest.mark.parametrize("P", [900, 2500, 5001])     # 16, 32 and 64 rows to a block
+def test_backward_of_every_block_height(P):
+    sizes = [P // 3, 0, 1, 15, 16, 17, 63, 64, 65]
+    sizes += [5, P - sum(sizes) - 9]
+    c = Back(P, 1032, len(sizes), offsets(sizes), kind=R.GELU, scatter=True, weight=True)
+    c.dst[P - 3], c.dst[P // 2] = -7, P          # of a group's row, and of one in no group
+    c.run()
+
+
+def test_backward_workspace_of_the_most_rows_serves_fewer():
+    for N, G in ((8, 1), (768, 3), (4096, 7), (40000, 1)):
+        most = m.moe_bias_act_backward_workspace_size(40000, N, G)
+        sizes = [m.moe_bias_act_backward_workspace_size(P, N, G) for P in range(1, 40001, 13)]
+        assert max(sizes) <= most and sizes == sorted(sizes)
+
+
 def test_backward_without_outputs_or_z():
     c = Back(100, 264, 2, offsets([60, 40]), kind=0)
     c.run(z=False, dpw=False)
