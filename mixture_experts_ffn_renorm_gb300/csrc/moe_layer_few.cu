@@ -10,8 +10,8 @@
 //   logits    a warp per (expert, two tokens), as in the router's small batches; grid barrier
 //   choice    every CTA selects the experts of all tokens (the router's order and bits) and
 //             groups the T K pairs by expert
-//   gate/up   the features of the touched experts in one line, each as long as its expert's tokens make it,
-//             cut evenly over the CTAs: w[p] act[p, n] to the workspace; grid barrier
+//   gate/up   blocks of four features of the touched experts, each taken by the first warp of the grid that is
+//             free: w[p] act[p, n] to the workspace; grid barrier
 //   down      a CTA owns H / CTAs output columns for all experts, so no partial sums cross CTAs
 //
 // The barrier between gate/up and down costs no bandwidth: the copies run ahead of it, since
@@ -34,15 +34,16 @@
 // All sums are f32 in a fixed order, nothing between the weights and the output is narrowed, and
 // no atomics touch data.
 //
-// What it measured (2048 x 768, 128 experts, 8 of them chosen; bf16): one token 27.4 us, of which 3.2 until
+// What it measured (2048 x 768, 128 experts, 8 of them chosen; bf16): one token 27.0 us, of which 3.2 until
 // the logits have crossed the grid, 3 the choice, 15 gate/up (7.4 of them the weights' way), 1 the second barrier, 3.5 down;
-// 16 tokens 151 us at 5.2 TB/s.  Steps on the way, us for one token and for 16:
+// 16 tokens 130 us at 6.0 TB/s.  Steps on the way, us for one token and for 16:
 //   chunks shared by eight warps, a group barrier after each      80  681   13000 cycles a chunk of index arithmetic
 //   a ring per warp, single rows and multiply-adds                37  319   an expert of many tokens held all SMs up
 //   mma.sync, three parts, one loop for both phases               33  186   (140 KB of code had to come from L2)
 //   TMA boxes, a piece's token loads in flight together           28  187   (680 cycles each, in turn, before)
 //   features dealt by their experts' tokens                       28  158
 //   sorted heads in the choice, tokens to L1 beside it            27  151
+//   blocks taken in turn, not dealt                               27  130   (SMs differed by a third)
 #include <atomic>
 
 #include "fp8_common.cuh"
@@ -87,6 +88,7 @@ struct Params {
   float* w;
   uint16_t* out;
   unsigned long long* barrier;     // arrivals of all launches
+  unsigned int* turns;             // blocks of gate/up that were asked for; 0 between launches
   float* logits;                   // [T, E]
   float* gate;                     // [T]
   uint16_t* act;                   // [3][T K, I], then [3][T, Is]: parts of the weighted activations
@@ -106,7 +108,6 @@ struct alignas(16) Fixed {
   int16_t expert[kMaxPairs + 1];   // touched experts, ascending
   int16_t first[kMaxPairs + 3];    // their first pair
   uint16_t tokens[kMaxPairs + 1];  // their tokens, a bit each
-  int16_t cost[kMaxPairs + 2];     // costs of the touched experts before them
   int n_groups;                    // touched experts, without the shared one
   int abort_flag;
 };
@@ -339,34 +340,21 @@ __device__ __forceinline__ void choose(const Params& p, Fixed& f, Scratch& x, in
   }
 }
 
-// What a feature of an expert costs an SM, in halves: its rows' way from memory hides one pass over
-// four tokens, and every further pass takes about half as long.  (Cut by features alone, one
-// expert of five tokens among 83 of one or two held all SMs up for 40 of 190 us.)
-__device__ __forceinline__ int cost_of(int tokens) { return 2 + ((tokens - 1) >> 2); }
-
 // Touched experts in ascending order with their pairs (tokens ascending), then the shared
 // expert's tokens.  One warp scans the experts; then a thread per pair places it.
 __device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch& x, int lane) {
   const int per = (p.E + 31) / 32, lo = min(p.E, lane * per), hi = min(p.E, lo + per);
-  int n = 0, cost = 0;             // touched experts, and their pairs in the upper half; their costs
+  int n = 0;                       // touched experts, and their pairs in the upper half
 #pragma unroll 1
   for (int e = lo; e < hi; ++e)
-    if (x.mask[e]) {
-      const int tokens = __popc(x.mask[e]);
-      n += 1 + (tokens << 16);
-      cost += cost_of(tokens);
-    }
-  int incl = n, costs = cost;
+    if (x.mask[e]) n += 1 + (__popc(x.mask[e]) << 16);
+  int incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, incl, o), w = __shfl_up_sync(0xffffffffu, costs, o);
-    if (lane >= o) {
-      incl += u;
-      costs += w;
-    }
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
   }
   int run = incl - n;
-  costs -= cost;
 #pragma unroll 1
   for (int e = lo; e < hi; ++e) {
     const uint32_t m = x.mask[e];
@@ -375,10 +363,8 @@ __device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch
     f.expert[run & 0xFFFF] = static_cast<int16_t>(e);
     f.first[run & 0xFFFF] = static_cast<int16_t>(run >> 16);
     f.tokens[run & 0xFFFF] = static_cast<uint16_t>(m);
-    f.cost[run & 0xFFFF] = static_cast<int16_t>(costs);
     x.mask[e] = m | (static_cast<uint32_t>(run >> 16) << 16);
     run += 1 + (tokens << 16);
-    costs += cost_of(tokens);
   }
   if (lane == 31) {
     const int D = run & 0xFFFF, P = run >> 16;
@@ -386,7 +372,6 @@ __device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch
     f.first[D] = static_cast<int16_t>(P);
     f.first[D + 1] = static_cast<int16_t>(P + p.T);
     f.tokens[D] = static_cast<uint16_t>((1u << p.T) - 1u);   // the shared expert's
-    f.cost[D] = static_cast<int16_t>(costs);
   }
 }
 
@@ -394,8 +379,8 @@ __device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch
 // its (expert, piece) units of down.  Two cursors walk it, the copies' ahead of the sums'.
 struct Cursor {
   int phase;      // 0 gate/up, 1 down, 2 end
-  int i;          // gate/up: block among the CTA's; down: unit among the row block's
-  int d, n, cnt;  // touched expert (D: the shared one); gate/up: its features [n, n + cnt)
+  int i;          // gate/up: block of all touched experts'; down: unit among the row block's
+  int d, n;       // touched expert (D: the shared one); gate/up: its features [n, n + 4)
   int k;          // column of the piece
 };
 
@@ -405,9 +390,9 @@ struct Stream {
   const Fixed& f;
   const CUtensorMap *m13, *m2, *m13s, *m2s;
   int D, warp, lane;
-  // gate/up: the CTA's features, all touched experts' in one line: [.., n0 blocks of the first expert,
-  // whole experts, ..], `routed` blocks in all, then the shared expert's from s0
-  int d0, i0, n0, end_d, end_n, routed, s0, s_end, blocks;
+  // gate/up: blocks of features, the shared expert's first; the warp's next one is known by its turn
+  int shared_blocks, blocks;
+  unsigned turn;
   // down: output columns [col0, col0 + cols) of the CTA, [row0, row0 + rows) of this warp's row block
   int col0, cols, row_blocks, row0, rows, unit0, unit_step, pieces, units;
   unsigned per_inv, pieces_inv;    // of I / 4 and of pieces
@@ -416,41 +401,16 @@ struct Stream {
                     const CUtensorMap* m13s_, const CUtensorMap* m2s_, int warp_, int lane_)
       : p(p_), f(f_), m13(m13_), m2(m2_), m13s(m13s_), m2s(m2s_), warp(warp_), lane(lane_) {
     D = f.n_groups;
-    // The features in one line, each as long as it costs (a shared expert's bf16 feature beside FP8
-    // ones twice as long), cut evenly: at most 5 * 512 * 8192 + 10 * 8192 long.  A feature is the
-    // CTA's in whose part it begins.
-    const unsigned I = p.I, shared_cost = (kFp8 ? 2u : 1u) * cost_of(p.T);
-    const unsigned line = static_cast<unsigned>(f.cost[D]) * I, all = line + shared_cost * p.Is, cta = blockIdx.x;
-    const unsigned a = all / gridDim.x * cta + min(cta, all % gridDim.x);
-    const unsigned b = a + all / gridDim.x + (cta < all % gridDim.x ? 1u : 0u);
-    auto place = [&](unsigned at, int& d, int& i) {          // the first feature that begins at or behind `at`
-      at = min(at, line);
-      int lo = 0, hi = D;                                    // cost[lo] I <= at; hi: beyond or D
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (static_cast<unsigned>(f.cost[mid]) * I <= at) lo = mid; else hi = mid;
-      }
-      const unsigned each = static_cast<unsigned>(f.cost[lo + 1] - f.cost[lo]);
-      i = static_cast<int>((at - static_cast<unsigned>(f.cost[lo]) * I + each - 1) / each);
-      d = lo;
-      if (i >= static_cast<int>(I)) {
-        i = 0;
-        ++d;
-      }
-    };
-    place(a, d0, i0);
-    place(b, end_d, end_n);
-    const int per = static_cast<int>(I) / kFeat;                           // I % 8 == 0
+    // The blocks in one line.  A warp's first is its place in the grid, the SMs' first warps before their second
+    // ones; every further one is the next that nobody has.  The count of those is back at 0 when
+    // the launch ends.
+    const unsigned cta = blockIdx.x;
+    const int per = p.I / kFeat;                             // I % 8 == 0
     per_inv = 0xFFFFFFFFu / per + 1u;
-    if (end_d == d0) {
-      n0 = routed = (end_n - i0 + kFeat - 1) / kFeat;
-    } else {
-      n0 = (static_cast<int>(I) - i0 + kFeat - 1) / kFeat;
-      routed = n0 + (end_d - d0 - 1) * per + (end_n + kFeat - 1) / kFeat;
-    }
-    s0 = a > line ? static_cast<int>((a - line + shared_cost - 1) / shared_cost) : 0;
-    s_end = b > line ? static_cast<int>((b - line + shared_cost - 1) / shared_cost) : 0;
-    blocks = routed + (s_end - s0 + kFeat - 1) / kFeat;
+    shared_blocks = p.Is / kFeat;
+    blocks = shared_blocks + D * per;
+    turn = blocks;
+    take_turn();
     const unsigned H = p.H;
     col0 = static_cast<int>(H / gridDim.x * cta + min(cta, H % gridDim.x));
     cols = static_cast<int>(H / gridDim.x + (cta < H % gridDim.x ? 1u : 0u));
@@ -477,23 +437,10 @@ struct Stream {
   }
   __device__ void locate(Cursor& c) const {
     if (c.phase == 0) {
-      if (c.i < n0) {
-        c.d = d0;
-        c.n = i0 + kFeat * c.i;
-        c.cnt = min(kFeat, (end_d == d0 ? end_n : p.I) - c.n);
-        return;
-      }
-      if (c.i < routed) {
-        const int j = c.i - n0, of = divided(j, per_inv);
-        c.d = d0 + 1 + of;
-        c.n = kFeat * j - of * p.I;
-        c.cnt = min(kFeat, (c.d == end_d ? end_n : p.I) - c.n);
-        return;
-      }
       if (c.i < blocks) {
-        c.d = D;
-        c.n = s0 + kFeat * (c.i - routed);
-        c.cnt = min(kFeat, s_end - c.n);
+        const int j = c.i - shared_blocks, of = divided(max(j, 0), per_inv);
+        c.d = j < 0 ? D : of;
+        c.n = kFeat * (j < 0 ? c.i : j - of * (p.I / kFeat));
         return;
       }
       c.phase = 1;
@@ -509,17 +456,23 @@ struct Stream {
       c.k = (c.i - D * pieces) * dn_cols(D);
     }
   }
+  // asks for the block after the next (one lane), while the next is worked on: an answer takes as long as a load
+  __device__ void take_turn() {
+    const int warps = static_cast<int>(gridDim.x) * kWarps;
+    if (blocks > warps && lane == 0) turn = warps + atomicAdd(p.turns, 1u);
+  }
   __device__ Cursor begin() const {
-    Cursor c{0, warp, 0, 0, 0, 0};
+    Cursor c{0, static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * warp, 0, 0, 0};
     locate(c);
     return c;
   }
-  __device__ void next(Cursor& c) const {
+  __device__ void next(Cursor& c) {
     if (c.phase == 0) {
       c.k += gu_cols(c.d);
       if (c.k < p.H) return;
       c.k = 0;
-      c.i += kWarps;
+      c.i = static_cast<int>(__shfl_sync(0xffffffffu, turn, 0));
+      if (c.i < blocks) take_turn();
     } else {
       c.i += unit_step;
     }
@@ -774,7 +727,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
 
   // ---- the experts.  One loop over the pieces of both phases, so that their code is there once:
   // wait for the slot, multiply, refill the slot
-  const Stream<kFp8> st(p, f, &m13, &m2, &m13s, &m2s, warp, lane);
+  Stream<kFp8> st(p, f, &m13, &m2, &m13s, &m2s, warp, lane);
   const int D = st.D, g = lane >> 2, q = lane & 3;
   const uint32_t ring = ptx::smem_u32(slots) + warp * kSlots * kSlotBytes, bars = ptx::smem_u32(&f.full[warp][0]);
   Cursor c[kSlots], ahead = st.begin();          // of the pieces in the slots, the oldest first
@@ -827,7 +780,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
       if (phase == 0) {
         const int n = min(kGuBlocks * cols, H - k), full = n >> sh;
         // this lane's row: feature g & 3, gate or up
-        const int row = (g < kFeat ? 0 : I) + min(c[0].n + (g & 3), I - 1);
+        const int row = (g < kFeat ? 0 : I) + c[0].n + (g & 3);
         const float* sc = nullptr;
         if (kFp8 && quant)
           sc = p.s13 + (expert * ((2 * I + 127) >> 7) + (row >> 7)) * static_cast<size_t>((H + 127) >> 7) + (k >> 7);
@@ -877,7 +830,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
               const float v = sum[0][j] + __shfl_xor_sync(0xffffffffu, sum[0][2 + j], 2);
               const float up = __shfl_down_sync(0xffffffffu, v, 4 * kFeat);
               const int i = i0 + 2 * q + j;
-              if (q < 2 && g < c[0].cnt && i < n_tok) {          // cnt <= 4: gate rows
+              if (q < 2 && g < kFeat && i < n_tok) {              // gate rows
                 const int pair = f.pair[first + i], tok = f.token[first + i], to_row = shared ? tok : pair;
                 const float a = v / (1.0f + __expf(-v)) * up * (shared ? f.gate[tok] : f.weight[pair]);
                 uint16_t part[3];
@@ -981,7 +934,10 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
     }
     __syncthreads();
     if (phase == 0) {
-      if (tid == 0) grid_barrier(arrivals + gridDim.x, abort_flag, p);
+      if (tid == 0) {
+        grid_barrier(arrivals + gridDim.x, abort_flag, p);
+        if (blockIdx.x == 0) *p.turns = 0u;      // nobody asks any more
+      }
       __syncthreads();
     }
   }
@@ -1100,6 +1056,7 @@ int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   const Layout l = layout_of(p.T, p.I, p.E, p.K, p.Is);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.barrier = reinterpret_cast<unsigned long long*>(ws);
+  p.turns = reinterpret_cast<unsigned int*>(ws + 64);
   p.logits = reinterpret_cast<float*>(ws + l.logits);
   p.gate = reinterpret_cast<float*>(ws + l.gate);
   p.act = reinterpret_cast<uint16_t*>(ws + l.act);
