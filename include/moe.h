@@ -18,6 +18,11 @@
  *                                      their data gradient (weights frozen)
  *   moe_combine_backward, moe_route_backward, moe_route_logits_backward
  *                                      gradients of the combine and of the router
+ *   moe_layer_few_bf16, moe_layer_few_fp8w
+ *                                      a whole layer for at most 16 tokens in one launch
+ *   moe_grouped_gemm_bias_act_bf16     product with bias, activation, weight and residual
+ *   moe_bias_act_backward, moe_grouped_gemm_wgrad_bf16
+ *                                      gradients of its epilogue and of its weights
  *
  * Sources (vllm.cpp pages):
  *   [I3094]  issue #3094 "Row: BACKEND-ROCM-BF16-MOE": names the two grouped

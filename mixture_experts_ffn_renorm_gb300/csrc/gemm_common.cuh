@@ -107,7 +107,10 @@ int make_tmap_f32_out(CUtensorMap* m, void* base, int groups, int rows, int cols
 // row lies outside the map.
 int make_tmap_blocks(CUtensorMap* m, const void* base, bool codes, int experts, int halves, int rows,
                      int cols, int box_rows, int box_blocks, const char* op, const char* what);
-// the same for one-byte elements (FP8 codes), unswizzled
+// the same matrix, a box is one block from any column on (zeros behind the row's end)
+int make_tmap_block(CUtensorMap* m, const void* base, bool codes, int experts, int halves, int rows, int cols,
+                    int box_rows, const char* op, const char* what);
+// rows x cols of one-byte elements (FP8 codes), unswizzled
 int make_tmap_u8(CUtensorMap* m, const void* base, long long rows, int cols, int box_rows,
                  const char* op, const char* what);
 int num_sms();

@@ -857,6 +857,25 @@ int make_tmap_blocks(CUtensorMap* m, const void* base, bool codes, int experts, 
   return MOE_OK;
 }
 
+int make_tmap_block(CUtensorMap* m, const void* base, bool codes, int experts, int halves, int rows, int cols,
+                    int box_rows, const char* op, const char* what) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return set_error(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", op);
+  const cuuint64_t esz = codes ? 1 : 2, n = 128 / esz, C = cols, R = rows, S = halves;
+  cuuint64_t dims[4] = {C, R, S, static_cast<cuuint64_t>(experts)};
+  cuuint64_t strides[3] = {C * esz, R * C * esz, S * R * C * esz};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(n), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(halves), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(MOE_ERR_CUDA, "%s: tensor map for %s rejected (CUresult %d)", op, what,
+                     static_cast<int>(r));
+  return MOE_OK;
+}
+
 int make_tmap_f32_out(CUtensorMap* m, void* base, int groups, int rows, int cols, const char* op) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return set_error(MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", op);

@@ -97,6 +97,14 @@ struct Params {
   unsigned long long* launches;
 };
 
+// A weight matrix: boxes of a slot's whole blocks, and single blocks
+struct Matrix {
+  CUtensorMap slot, block;
+};
+struct Maps {
+  Matrix w13, w2, w13s, w2s;
+};
+
 // Shared memory: the fixed part, then the ring, which first holds the choice's scratch and last
 // the warps' sums
 struct alignas(16) Fixed {
@@ -123,6 +131,15 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* m, int
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4, %5}], "
       "[%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(0), "r"(row), "r"(block), "r"(expert), "r"(bar)
+      : "memory");
+}
+
+// a block of 128 bytes of the rows from any column on, what lies behind their end as zeros
+__device__ __forceinline__ void block_load(uint32_t dst, const CUtensorMap* m, int row, int col, int expert, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(col), "r"(row), "r"(0), "r"(expert), "r"(bar)
       : "memory");
 }
 
@@ -388,7 +405,7 @@ template <bool kFp8>
 struct Stream {
   const Params& p;
   const Fixed& f;
-  const CUtensorMap *m13, *m2, *m13s, *m2s;
+  const Maps& maps;
   int D, warp, lane;
   // gate/up: blocks of features, the shared expert's first; the warp's next one is known by its turn
   int shared_blocks, blocks;
@@ -397,9 +414,8 @@ struct Stream {
   int col0, cols, row_blocks, row0, rows, unit0, unit_step, pieces, units;
   unsigned per_inv, pieces_inv;    // of I / 4 and of pieces
 
-  __device__ Stream(const Params& p_, const Fixed& f_, const CUtensorMap* m13_, const CUtensorMap* m2_,
-                    const CUtensorMap* m13s_, const CUtensorMap* m2s_, int warp_, int lane_)
-      : p(p_), f(f_), m13(m13_), m2(m2_), m13s(m13s_), m2s(m2s_), warp(warp_), lane(lane_) {
+  __device__ Stream(const Params& p_, const Fixed& f_, const Maps& maps_, int warp_, int lane_)
+      : p(p_), f(f_), maps(maps_), warp(warp_), lane(lane_) {
     D = f.n_groups;
     // The blocks in one line.  A warp's first is its place in the grid, the SMs' first warps before their second
     // ones; every further one is the next that nobody has.  The count of those is back at 0 when
@@ -478,18 +494,20 @@ struct Stream {
     }
     locate(c);
   }
-  // the copy of a piece (one lane).  Only whole blocks of a row are copied: what is left of it is read
-  // from where it lies.  Rows behind the expert's are zeros, those of the next CTA are not used.
+  // The copy of a piece (one lane): one box, or where the row ends inside a block (whose rest in memory is
+  // the next row's) blocks one by one.  What lies behind the row, and rows behind the expert's, are zeros;
+  // rows of the next CTA are not used.
   __device__ void issue(const Cursor& c, uint32_t slot, uint32_t bar) const {
-    const int sh = shift(c.d), block = c.k >> sh;
-    if (c.k + (1 << sh) > (c.phase == 0 ? p.H : inner(c.d))) {
-      ptx::mbar_arrive(bar);
-      return;
-    }
+    const int sh = shift(c.d), left = (c.phase == 0 ? p.H : inner(c.d)) - c.k, n = c.phase == 0 ? kGuBlocks : kDnBlocks;
+    const int expert = c.d < D ? f.expert[c.d] : 0, row = c.phase == 0 ? c.n : col0 + row0;
+    const Matrix& m = c.phase == 0 ? (c.d < D ? maps.w13 : maps.w13s) : (c.d < D ? maps.w2 : maps.w2s);
     ptx::mbar_arrive_expect_tx(bar, kSlotBytes);
-    const int expert = c.d < D ? f.expert[c.d] : 0;
-    if (c.phase == 0) box_load(slot, c.d < D ? m13 : m13s, c.n, block, expert, bar);
-    else box_load(slot, c.d < D ? m2 : m2s, col0 + row0, block, expert, bar);
+    if (left >= n << sh || !(left & ((1 << sh) - 1))) {
+      box_load(slot, &m.slot, row, c.k >> sh, expert, bar);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) block_load(slot + i * (kSlotBytes / n), &m.block, row, c.k + (i << sh), expert, bar);
+    }
   }
 };
 
@@ -542,24 +560,25 @@ __device__ __forceinline__ void join(float (&sum)[2][4], float lo, float hi, flo
 }
 
 // A lane's token values of a piece: in each of four blocks of 128 bytes of weights vectors 2 q and 2 q + 1.
-// x: the token's values of the piece's first of the four blocks, 16 bytes a vector; `full` of them are
-// whole (the others' products are with zeros).  All loads are in flight together: they are the latency of a
+// x: the token's values of the piece's first of the four blocks, 16 bytes a vector; `vecs` of them are left of the
+// token (the others' products are with zeros).  All loads are in flight together: they are the latency of a
 // piece (680 cycles from L2; in turn with the multiplications four times that).
 template <bool kQ>
 struct Tokens {
   static constexpr int kVec = kQ ? 2 : 1;        // token vectors to a weight vector
   uint4 u[4][2][kVec];
   template <bool kFinal>                         // not written while the kernel runs
-  __device__ __forceinline__ void load(const uint4* x, int q, int full) {
+  __device__ __forceinline__ void load(const uint4* x, int q, int vecs) {
     x += 2 * q * kVec;
+    vecs -= 2 * q * kVec;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
-          const uint4* from = x + (i * 8 + h) * kVec + v;
-          u[i][h][v] = i < full ? (kFinal ? __ldg(from) : *from) : make_uint4(0, 0, 0, 0);
+          const int at = (i * 8 + h) * kVec + v;
+          u[i][h][v] = at < vecs ? (kFinal ? __ldg(x + at) : x[at]) : make_uint4(0, 0, 0, 0);
         }
   }
 };
@@ -609,32 +628,6 @@ __device__ __forceinline__ void down(const uint8_t* at, int g, int q, const Toke
   if (!kQ) join<kQ>(sum, 1.0f, 1.0f, c);
 }
 
-// The end of a row that fills no block, read from where it lies: MMA rows 0-7 from w0, 8-15 from w1 (or
-// zeros), scales there; x: the lane's token from the same column on.  n columns.
-template <bool kQ, bool kFinal>
-__device__ __noinline__ void row_end(const uint8_t* w0, const uint8_t* w1, const uint4* x, int n, int q, float d0, float d1,
-                                     float* c) {
-  constexpr int kVec = kQ ? 2 : 1;
-  float sum[2][4] = {}, add[4] = {};
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const int col = (2 * q + h) * 8 * kVec;
-    uint4 u[kVec], v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) u[k] = v0;
-    if (col < n) {                               // vectors behind the end are zeros on both sides
-      v0 = __ldg(reinterpret_cast<const uint4*>(w0 + col * (kQ ? 1 : 2)));
-      if (w1) v1 = __ldg(reinterpret_cast<const uint4*>(w1 + col * (kQ ? 1 : 2)));
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) u[k] = kFinal ? __ldg(x + (col >> 3) + k) : x[(col >> 3) + k];
-    }
-    products<kQ>(sum, Row<kQ>(v0), Row<kQ>(v1), u);
-  }
-  join<kQ>(sum, d0, d1, add);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] += add[j];
-}
-
 // v as three bf16 parts that add up to it (an infinity or NaN as its first part alone)
 __device__ __forceinline__ void cut3(float v, uint16_t (&part)[3]) {
   part[0] = f32_to_bf16_bits(v);
@@ -646,8 +639,7 @@ __device__ __forceinline__ void cut3(float v, uint16_t (&part)[3]) {
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
-layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant__ CUtensorMap m2,
-                 const __grid_constant__ CUtensorMap m13s, const __grid_constant__ CUtensorMap m2s, const Params p) {
+layer_few_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the ring at a multiple of 1024 bytes, the swizzle's period, the fixed part behind it
   uint8_t* slots = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
@@ -661,8 +653,8 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
   if (lane < kSlots) ptx::mbar_init(ptx::smem_u32(&f.full[warp][lane]), 1);
   if (tid == 0) {
     f.abort_flag = 0;
-    ptx::tma_prefetch_desc(&m13);
-    ptx::tma_prefetch_desc(&m2);
+    ptx::tma_prefetch_desc(&maps.w13.slot);
+    ptx::tma_prefetch_desc(&maps.w2.slot);
   }
   ptx::fence_mbar_init();
   for (int e = tid; e < E; e += kThreads) x.mask[e] = 0u;
@@ -727,7 +719,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
 
   // ---- the experts.  One loop over the pieces of both phases, so that their code is there once:
   // wait for the slot, multiply, refill the slot
-  Stream<kFp8> st(p, f, &m13, &m2, &m13s, &m2s, warp, lane);
+  Stream<kFp8> st(p, f, maps, warp, lane);
   const int D = st.D, g = lane >> 2, q = lane & 3;
   const uint32_t ring = ptx::smem_u32(slots) + warp * kSlots * kSlotBytes, bars = ptx::smem_u32(&f.full[warp][0]);
   Cursor c[kSlots], ahead = st.begin();          // of the pieces in the slots, the oldest first
@@ -778,7 +770,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
       };
       const int sh = st.shift(d), cols = 1 << sh;
       if (phase == 0) {
-        const int n = min(kGuBlocks * cols, H - k), full = n >> sh;
+        const int n = min(kGuBlocks * cols, H - k), last = (n - 1) >> sh;    // columns, last block
         // this lane's row: feature g & 3, gate or up
         const int row = (g < kFeat ? 0 : I) + c[0].n + (g & 3);
         const float* sc = nullptr;
@@ -789,34 +781,25 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
         float scale[8];
         if (kFp8 && quant) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) scale[i] = full > 0 ? __ldg(sc + min(i, full - 1)) : 0.0f;
+          for (int i = 0; i < 8; ++i) scale[i] = __ldg(sc + min(i, last));
         }
         auto token = [&](int i0) {
           return p.x + static_cast<size_t>(f.token[first + min(i0 + (g & 3), n_tok - 1)]) * H + k;
         };
         auto load = [&](int i0, auto& u) {
-          u.template load<true>(reinterpret_cast<const uint4*>(token(i0) + (g >> 2) * 4 * cols), q, full - (g >> 2) * 4);
+          const int from = (g >> 2) * 4 * cols;
+          u.template load<true>(reinterpret_cast<const uint4*>(token(i0) + from), q, (n - from) >> 3);
         };
         auto multiply = [&](int i0, auto u) {
           load(i0, u);
           take();
-          if (full > 0) gate_up(mine, g, q, u, scale, sum[0]);
+          gate_up(mine, g, q, u, scale, sum[0]);
         };
 #pragma unroll 1
         for (int i0 = 0; i0 < 4 * fours; i0 += 4) {
           if (i0 < n_tok) {
             if (kFp8 && quant) multiply(i0, Tokens<kFp8>());
             else multiply(i0, Tokens<false>());
-            if (full * cols < n) {
-              const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w13s) : p.w13);
-              w += ((static_cast<size_t>(expert) * 2 * I + row) * H + k + full * cols) * (quant ? 1 : 2);
-              const uint4* xe = reinterpret_cast<const uint4*>(token(i0) + full * cols);
-              float add[4] = {};
-              if (kFp8 && quant) row_end<kFp8, true>(w, nullptr, xe, n - full * cols, q, __ldg(sc + full), 0.0f, add);
-              else row_end<false, true>(w, nullptr, xe, n - full * cols, q, 1.0f, 1.0f, add);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) sum[0][j] += add[j];
-            }
           }
           if (fours > 1) turn();
         }
@@ -849,7 +832,7 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
           for (int j = 0; j < 4; ++j) sum[0][j] = sum[1][j] = sum[2][j] = sum[3][j] = 0.0f;
         }
       } else {
-        const int n = min(kDnBlocks * cols, I - k), full = n >> sh;
+        const int n = min(kDnBlocks * cols, I - k), last = (n - 1) >> sh;
         // this lane's rows
         const int r0 = min(st.col0 + st.row0 + g, H - 1), r1 = min(r0 + 8, H - 1);
         const float *sc0 = nullptr, *sc1 = nullptr;
@@ -865,39 +848,25 @@ layer_few_kernel(const __grid_constant__ CUtensorMap m13, const __grid_constant_
         if (kFp8 && quant) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            scale[i] = full > 0 ? __ldg(sc0 + min(i, full - 1)) : 0.0f;
-            scale[i + 4] = full > 0 ? __ldg(sc1 + min(i, full - 1)) : 0.0f;
+            scale[i] = __ldg(sc0 + min(i, last));
+            scale[i + 4] = __ldg(sc1 + min(i, last));
           }
         }
         auto token = [&](int i0) {
           const int i = first + min(i0 + (g & 1), n_tok - 1);
           return act + static_cast<size_t>(shared ? f.token[i] : f.pair[i]) * I;
         };
-        auto load = [&](int i0, auto& u) { u.template load<false>(reinterpret_cast<const uint4*>(token(i0)), q, full); };
+        auto load = [&](int i0, auto& u) { u.template load<false>(reinterpret_cast<const uint4*>(token(i0)), q, n >> 3); };
         auto multiply = [&](int i0, auto u, float (&v)[4]) {
           load(i0, u);
           take();
-          if (full > 0) down(at + g * 128, g, q, u, scale, v);
+          down(at + g * 128, g, q, u, scale, v);
         };
 #pragma unroll 1
         for (int i0 = 0; i0 < n_tok; i0 += 2) {
           float v[4] = {};
           if (kFp8 && quant) multiply(i0, Tokens<kFp8>(), v);
           else multiply(i0, Tokens<false>(), v);
-          if (full * cols < n) {
-            const uint8_t* w = static_cast<const uint8_t*>(shared ? static_cast<const void*>(p.w2s) : p.w2);
-            const int esz = quant ? 1 : 2, at_col = k + full * cols;
-            const uint8_t* w0 = w + ((static_cast<size_t>(expert) * H + r0) * I + at_col) * esz;
-            const uint8_t* w1 = w + ((static_cast<size_t>(expert) * H + r1) * I + at_col) * esz;
-            const uint4* ae = reinterpret_cast<const uint4*>(token(i0) + full * cols);
-            float add[4] = {};
-            if (kFp8 && quant)
-              row_end<kFp8, false>(w0, w1, ae, n - full * cols, q, __ldg(sc0 + full), __ldg(sc1 + full), add);
-            else
-              row_end<false, false>(w0, w1, ae, n - full * cols, q, 1.0f, 1.0f, add);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] += add[j];
-          }
           // the three parts, in lanes q = 0, 1, 2; then to the sums of the lane that keeps the token
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -1044,11 +1013,13 @@ int check(const char* op, const Params& p, bool fp8, const void* workspace, size
   return MOE_OK;
 }
 
-// [experts][halves][rows][cols] bf16 values or codes, a box of box_rows rows of every half
-int make_map(CUtensorMap* m, const void* base, bool codes, int experts, int halves, int rows, int cols, int box_rows,
-             int box_blocks, const char* op, const char* what) {
-  if (cols < (codes ? 128 : 64)) return MOE_OK;
-  return gemm::make_tmap_blocks(m, base, codes, experts, halves, rows, cols, box_rows, box_blocks, op, what);
+// [experts][halves][rows][cols] bf16 values or codes, boxes of box_rows rows of every half; rows without a whole
+// block of 128 bytes have no boxes of several
+int make_maps(Matrix* m, const void* base, bool codes, int experts, int halves, int rows, int cols, int box_rows,
+              int box_blocks, const char* op, const char* what) {
+  const int rc = gemm::make_tmap_block(&m->block, base, codes, experts, halves, rows, cols, box_rows, op, what);
+  if (rc != MOE_OK || cols < (codes ? 128 : 64)) return rc;
+  return gemm::make_tmap_blocks(&m->slot, base, codes, experts, halves, rows, cols, box_rows, box_blocks, op, what);
 }
 
 template <bool kFp8>
@@ -1084,22 +1055,20 @@ int launch(const char* op, Params p, void* workspace, cudaStream_t stream) {
   p.status = diag.status;
   p.launches = diag.launches;
   p.wait_ns = gemm::pipeline_wait_ns();
-  // a map without a whole block of 128 bytes is never used
-  CUtensorMap m13{}, m2{}, m13s{}, m2s{};
+  Maps maps{};
   int rc;
-  if ((rc = make_map(&m13, p.w13, kFp8, p.E, 2, p.I, p.H, kFeat, kGuBlocks, op, "w13")) != MOE_OK) return rc;
-  if ((rc = make_map(&m2, p.w2, kFp8, p.E, 1, p.H, p.I, 16, kDnBlocks, op, "w2")) != MOE_OK) return rc;
+  if ((rc = make_maps(&maps.w13, p.w13, kFp8, p.E, 2, p.I, p.H, kFeat, kGuBlocks, op, "w13")) != MOE_OK) return rc;
+  if ((rc = make_maps(&maps.w2, p.w2, kFp8, p.E, 1, p.H, p.I, 16, kDnBlocks, op, "w2")) != MOE_OK) return rc;
   if (p.Is > 0) {
-    if ((rc = make_map(&m13s, p.w13s, false, 1, 2, p.Is, p.H, kFeat, kGuBlocks, op, "w13_shared")) != MOE_OK) return rc;
-    if ((rc = make_map(&m2s, p.w2s, false, 1, 1, p.H, p.Is, 16, kDnBlocks, op, "w2_shared")) != MOE_OK) return rc;
+    if ((rc = make_maps(&maps.w13s, p.w13s, false, 1, 2, p.Is, p.H, kFeat, kGuBlocks, op, "w13_shared")) != MOE_OK)
+      return rc;
+    if ((rc = make_maps(&maps.w2s, p.w2s, false, 1, 1, p.H, p.Is, 16, kDnBlocks, op, "w2_shared")) != MOE_OK) return rc;
   }
   // cooperative: the CTAs wait for one another, so all of them start together or none does
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
-  return launch_status(launch_kernel(kern, dim3(ctas), dim3(kThreads), kSmem, stream, attr, 1, m13, m2, m13s, m2s,
-                                     p),
-                       op);
+  return launch_status(launch_kernel(kern, dim3(ctas), dim3(kThreads), kSmem, stream, attr, 1, maps, p), op);
 }
 
 }  // namespace
