@@ -562,7 +562,9 @@ class MoeMlpBlock:
         """x bf16 [T, H], contiguous -> bf16 [T, H]: the routed sum, plus residual [T, H] if given,
         rounded once."""
         T = x.shape[0]
-        assert T <= self.max_tokens and x.dtype == torch.bfloat16 and x.is_contiguous()
+        if not 1 <= T <= self.max_tokens:
+            raise ValueError(f"forward() of {T} tokens, outside [1, {self.max_tokens}]")
+        assert x.dtype == torch.bfloat16 and x.is_contiguous()
         assert residual is None or (residual.shape == x.shape and residual.dtype == x.dtype and
                                     residual.is_contiguous())
         H, I, E, K, ws = self.H, self.I, self.E, self.K, self.workspace
