@@ -20,7 +20,8 @@
 //
 // 32768 rows of 768 x 2048 in 128 groups take 177 us, 5.6 TB/s: 805 MB of gradients leave, 185 MB of rows come in.
 // With add_to 280 us, 6.4 TB/s: its boxes of 32 x 32 come by TMA, four under way to each warp, into the room of two of
-// the four stages, and leave from there (loads of a lane's own row, each a latency of HBM and 32 lines: 410 us).
+// the four stages (or one, where groups have many rows), and leave from there.  (Loads of a lane's own row, each a
+// latency of HBM and 32 lines: 410 us.  Tiles of 128 columns even the SMs' shares of few tiles out, to no gain.)
 // 777 rows of 400 x 1040 in 13 groups with add_to take 16.8 us (6.7 at HBM's rate), two tiles an SM at most.
 //
 // With a few groups of many rows there are fewer tiles than SMs: the rows are cut into ranges whose
@@ -53,19 +54,19 @@ struct Params {
   unsigned long long* launches;
 };
 
-// kAdd: with add_to.  Its tile is on the way in while the tile's products are added up, so it takes half of the
-// stages' room: four boxes of 32 x 32 a warp, where without it there is one, for the stores.
-template <bool kAdd>
+// kAddBoxes: boxes of add_to, 32 x 32, that are under way to a warp; 0 without add_to.  Four take half of the stages' room:
+// the tile's boxes arrive while its products are added up.  One has the room of the stores' box.
+template <int kAddBoxes>
 struct Smem {
-  static constexpr int kStages = kAdd ? 2 : 4, kBoxes = kAdd ? 4 : 1;
+  static constexpr int kStages = kAddBoxes == 4 ? 2 : 4, kBoxes = kAddBoxes == 4 ? 4 : 1;
   static constexpr int A = 0;
   static constexpr int B = A + kStages * kABytes;
   static constexpr int OUT = B + kStages * kBBytes;          // 8 warps x kBoxes x 4 KB, TMA stores' sources
-  static constexpr int BARS = OUT + 8 * kBoxes * 4096;       // full, empty, tfull[2], tempty[2], drain, add[8][4]
-  static constexpr int MISC = BARS + (2 * kStages + 5 + (kAdd ? 32 : 0)) * 8;
+  static constexpr int BARS = OUT + 8 * kBoxes * 4096;       // full, empty, tfull[2], tempty[2], drain, add[8][boxes]
+  static constexpr int MISC = BARS + (2 * kStages + 5 + 8 * kAddBoxes) * 8;
   static constexpr int ALLOC = MISC + 16 + 1024;
 };
-static_assert(Smem<false>::ALLOC <= 227 * 1024 && Smem<true>::ALLOC <= 227 * 1024, "shared memory");
+static_assert(Smem<0>::ALLOC <= 227 * 1024 && Smem<1>::ALLOC <= 227 * 1024 && Smem<4>::ALLOC <= 227 * 1024, "shared memory");
 
 struct Tile {
   int g, n0, k0, range;
@@ -120,11 +121,12 @@ __device__ __forceinline__ void tma_store_wait_read() {
 }
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-template <bool kAdd>
+template <int kAddBoxes>
 __global__ void __launch_bounds__(kThreads, 1)
 wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmAdd, const Params p) {
-  using Smem = Smem<kAdd>;
+  using Smem = Smem<kAddBoxes>;
+  constexpr bool kAdd = kAddBoxes > 0;
   constexpr int kStages = Smem::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -139,7 +141,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
   auto bar_tfull = [&](int a) { return ptx::smem_u32(bars + 2 * kStages + a); };
   auto bar_tempty = [&](int a) { return ptx::smem_u32(bars + 2 * kStages + 2 + a); };
   const uint32_t bar_drain = ptx::smem_u32(bars + 2 * kStages + 4);
-  auto bar_add = [&](int w, int c) { return ptx::smem_u32(bars + 2 * kStages + 5 + 4 * w + c); };
+  auto bar_add = [&](int w, int c) { return ptx::smem_u32(bars + 2 * kStages + 5 + kAddBoxes * w + c); };
 
   count_launch(p.launches, MOE_KID_GEMM_WGRAD);
   if (threadIdx.x == 0) {
@@ -153,7 +155,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     }
     ptx::mbar_init(bar_drain, 1);
     if (kAdd)
-      for (int i = 0; i < 32; ++i) ptx::mbar_init(bar_add(0, i), 1);
+      for (int i = 0; i < 8 * kAddBoxes; ++i) ptx::mbar_init(bar_add(0, i), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -260,18 +262,20 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 2) >> 2;      // TMEM lane quarter; 128 of the columns
     const uint32_t stage = sb + Smem::OUT + (warp - 2) * Smem::kBoxes * 4096;
-    // add_to's boxes arrive in this order, four of them under way: [tile][c]
+    // add_to's boxes in their order, [tile][c]; box i lies in place i % kBoxes
+    constexpr uint32_t kPlaces = Smem::kBoxes;
     uint32_t arrived = 0, asked = 0;
-    auto ask = [&](long long i, int c) {           // one lane
-      const Tile t = tile_of(p, i, tn, tk);
-      ptx::mbar_arrive_expect_tx(bar_add(warp - 2, c), 4096);
-      tma_load_3d(stage + c * 4096, &tmAdd, t.k0 + half * 128 + 32 * c, t.n0 + q * 32, t.g, bar_add(warp - 2, c));
+    auto ask = [&](long long i, int c) {
+      if (i >= tiles) return;
+      if (lane == 0) {
+        const Tile t = tile_of(p, i, tn, tk);
+        const uint32_t at = asked % kPlaces, bar = bar_add(warp - 2, at);
+        ptx::mbar_arrive_expect_tx(bar, 4096);
+        tma_load_3d(stage + at * 4096, &tmAdd, t.k0 + half * 128 + 32 * c, t.n0 + q * 32, t.g, bar);
+      }
+      ++asked;
     };
-    if (kAdd && blockIdx.x < tiles) {
-      if (lane == 0)
-        for (int c = 0; c < 4; ++c) ask(blockIdx.x, c);
-      asked = 4;
-    }
+    for (int c = 0; c < kAddBoxes; ++c) ask(blockIdx.x, c);
     int acc = 0;
     uint32_t uses[2] = {0, 0};
     bool ok = true;
@@ -296,9 +300,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
       // columns [32 c, + 32) of this thread's row: 128 bytes a row through a box, a store
       auto leave = [&](int c, float (&v)[32]) {
         const int col = t.k0 + half * 128 + 32 * c, row0 = t.n0 + q * 32;
-        const uint32_t mine = stage + (kAdd ? c * 4096 : 0) + lane * 128;
+        const uint32_t box = stage + (kAdd ? arrived % kPlaces * 4096 : 0), mine = box + lane * 128;
         if (kAdd) {
-          ok = wait_bar(bar_add(warp - 2, c), (arrived >> 2) & 1u, abort_flag, p.status, p.wait_ns);
+          ok = wait_bar(bar_add(warp - 2, arrived % kPlaces), (arrived / kPlaces) & 1u, abort_flag, p.status, p.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) return;
           ++arrived;
@@ -321,20 +325,17 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        // a group for every box, also without a store: the last but one has been read when its box is asked for anew
+        // a group for every box, also without a store: they count them
         if (lane == 0) {
-          if (col < p.K && row0 < p.N) tma_store_3d(&tmO, stage + (kAdd ? c * 4096 : 0), col, row0, z);
+          if (col < p.K && row0 < p.N) tma_store_3d(&tmO, box, col, row0, z);
           tma_store_commit();
         }
-        if (kAdd && arrived > 1) {
-          const long long next = c == 0 ? i : i + gridDim.x;
-          if (next < tiles) {
-            if (lane == 0) {
-              tma_store_wait_read<1>();
-              ask(next, (c + 3) & 3);
-            }
-            ++asked;
-          }
+        if (kAddBoxes == 1) {        // the next box, in the same place
+          if (lane == 0) tma_store_wait_read<0>();
+          ask(i + (c == 3 ? gridDim.x : 0), (c + 1) & 3);
+        } else if (kAdd && arrived > 1) {        // three boxes on, in the place of the box before this one
+          if (lane == 0) tma_store_wait_read<1>();
+          ask(i + (c > 0 ? gridDim.x : 0), (c + 3) & 3);
         }
       };
       if (steps <= kChunk) {
@@ -390,7 +391,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CU
     }
     if (lane == 0) tma_store_wait();
     // a warp that gave up lets its copies land
-    for (; kAdd && arrived < asked; ++arrived) spin_bounded(bar_add(warp - 2, arrived & 3), (arrived >> 2) & 1u);
+    for (; arrived < asked; ++arrived) spin_bounded(bar_add(warp - 2, arrived % kPlaces), (arrived / kPlaces) & 1u);
   }
   // ---- exit: a CTA that gave up drains its copies and MMAs first
   __syncthreads();
@@ -447,10 +448,10 @@ int ranges_of(int P, int N, int K, int G) {
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
-template <bool kAdd>
+template <int kAddBoxes>
 int launch(const char* op, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const CUtensorMap& tadd,
            const Params& p, cudaStream_t stream) {
-  constexpr int kBytes = Smem<kAdd>::ALLOC;
+  constexpr int kBytes = Smem<kAddBoxes>::ALLOC;
   static std::atomic<int> configured[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -459,7 +460,7 @@ int launch(const char* op, const CUtensorMap& ta, const CUtensorMap& tb, const C
   }
   const bool cache = dev >= 0 && dev < 64;
   if (!cache || !configured[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(wgrad_kernel<kAdd>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(wgrad_kernel<kAddBoxes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
       return set_error(MOE_ERR_CUDA, "%s: cannot reserve %d bytes of shared memory: %s", op, kBytes,
                        cudaGetErrorString(cudaGetLastError()));
     if (cache) configured[dev].store(1, std::memory_order_release);
@@ -467,7 +468,7 @@ int launch(const char* op, const CUtensorMap& ta, const CUtensorMap& tb, const C
   const long long tiles =
       static_cast<long long>(p.G) * ((p.N - 1) / kTileN + 1) * ((p.K - 1) / kTileK + 1) * p.ranges;
   const int sms = sm_count();
-  return launch_status(launch_kernel(wgrad_kernel<kAdd>, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)),
+  return launch_status(launch_kernel(wgrad_kernel<kAddBoxes>, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)),
                                      dim3(kThreads), kBytes, stream, nullptr, 0, ta, tb, to, tadd, p),
                        op);
 }
@@ -537,7 +538,11 @@ extern "C" int moe_grouped_gemm_wgrad_bf16(const void* dz_bf16, const void* a_bf
   if ((rc = make_tmap_f32_out(&to, p.out, G * p.ranges, N, K, op)) != MOE_OK) return rc;
   tadd = to;
   if (p.add_to && (rc = make_tmap_f32_out(&tadd, const_cast<float*>(p.add_to), G, N, K, op)) != MOE_OK) return rc;
-  rc = p.add_to ? launch<true>(op, ta, tb, to, tadd, p, s) : launch<false>(op, ta, tb, to, tadd, p, s);
+  // With many rows a group the products take longer than add_to's way and want all four stages: 512 rows a group, four boxes
+  // 187 us, one 196; 585 rows 48.0 and 44.5; 8192 rows of 4096 x 4096 343 and 224 (216 without add_to).
+  rc = !p.add_to      ? launch<0>(op, ta, tb, to, tadd, p, s)
+       : P / G <= 512 ? launch<4>(op, ta, tb, to, tadd, p, s)
+                      : launch<1>(op, ta, tb, to, tadd, p, s);
   if (rc != MOE_OK || p.ranges == 1) return rc;
   return launch_status(launch_kernel(wgrad_reduce_kernel, dim3(static_cast<unsigned>((n / 4 + 255) / 256)), dim3(256), 0, s,
                                      nullptr, 0, static_cast<const float*>(workspace), p.ranges,

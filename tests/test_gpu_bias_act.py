@@ -437,3 +437,16 @@ def test_wgrad_adds_in_place_over_many_tiles():
         assert torch.equal(held, want)
     c = Wgrad(100, 2560, 2560, 3, offsets([50, 0, 50]), add=True)
     c.run()
+
+
+def test_wgrad_adds_to_groups_of_many_rows():
+    # more than 512 rows a group on average: 180 tiles, some of them empty
+    sizes = [1500, 0, 700, 17, 1600]
+    c = Wgrad(sum(sizes), 1040, 776, 5, offsets(sizes), add=True)
+    c.run()
+    want = c.dw.clone()
+    for _ in range(3):
+        held = c.add.clone()
+        c.call(out=held, add=held)
+        torch.cuda.synchronize()
+        assert torch.equal(held, want)

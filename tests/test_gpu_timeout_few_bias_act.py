@@ -60,9 +60,9 @@ def test_product(columns):
     runs_out(c.call, (c.out,))
 
 
-@pytest.mark.parametrize("add", [False, True])
-def test_weight_gradient(add):
+@pytest.mark.parametrize("add,rows", [(False, 512), (True, 512), (True, 576)])
+def test_weight_gradient(add, rows):
     # a tile per SM and group, 60 MB of rows: its first sums are 9 us of HBM away
     G = 152
-    c = Wgrad(512 * G, 128, 256, G, offsets([512] * G), add=add)
+    c = Wgrad(rows * G, 128, 256, G, offsets([rows] * G), add=add)
     runs_out(c.call, (c.dw,))
