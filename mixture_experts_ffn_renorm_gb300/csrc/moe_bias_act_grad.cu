@@ -3,17 +3,20 @@
 //   dy[r] = dout[dst] * pair_weight[dst],  s = dy act'(z):  dz = bf16(s),
 //   grad_bias[g] = sum of s over g's rows,  grad_pair_weight[dst] = sum_n dout[dst,n] act(z[r,n])
 //
-// One pass over dout and z: what bounds it is HBM (6 bytes an element).  A CTA takes up to 64 rows x 256
-// columns; a warp every eighth row, three of them at a time with all loads in flight, a lane 8
-// columns, so that its column sums are 8 registers and its row sums one butterfly each: four CTAs an SM.
-// 32768 x 768 with bias and row weights takes 42.2 us with GELU (3.6 TB/s), 37 with ReLU: Phi's instructions and HBM in
-// turn, then the second kernel; the pass alone takes 35, with ReLU 30 (HBM 22).  (A CTA for all columns of its rows, whose row sums need no second
-// kernel: 48 us, one wave of CTAs in step.  Rows brought to L2 before the groups are looked up: no gain.)
+// One pass over dout and z: what bounds it is HBM (6 bytes an element), with GELU the instructions.  A CTA takes 256
+// columns of a range of rows, three CTAs an SM, one wave of them; a warp every eighth row, a lane 8 columns, so that its column sums are
+// 8 registers and its row sums one butterfly each.  A warp's next eight rows are always under way to its own
+// shared memory (cp.async, no barrier): 192 KB an SM.
+// 32768 x 768 with bias and row weights takes 41.7 us with GELU (3.6 TB/s), 33 with SiLU, 31.5 with ReLU; the pass alone
+// 33, 27 and 27 (HBM 22), then the second kernel.  (Blocks of 64 rows, three rows of a warp in registers, 2.5 waves: 42.6, 37.8 and
+// 37.  A CTA for all columns of 64 rows: 48.  All 64 rows of a block asked for at once: 43.6 and 39.)
 // A CTA's rows may meet several groups: at
 // each group's end the warps' column sums are joined through shared memory in warp order and
 // leave as one partial row.  Block c and group g meet in partial row c + g: along the rows
 // either index or both step up, so no two meetings share one, and the second kernel finds a
 // group's rows from its offsets alone.  It adds them in block order: fixed order, no atomics.
+#include <atomic>
+
 #include "activation.cuh"
 #include "gemm_common.cuh"
 
@@ -21,10 +24,12 @@ namespace moe {
 namespace gemm {
 namespace {
 
-constexpr int kRows = 64;            // rows of a CTA, or 32 or 16 (rows_of)
 constexpr int kCols = 256;           // columns of a CTA: 8 per lane
 constexpr int kWarps = 8;
-constexpr int kFlight = 3;           // rows of a warp whose loads are in flight together (2: 47.0 us, 4: 47.6)
+constexpr int kCtas = 3;             // per SM
+constexpr int kLeast = 16;           // rows of a CTA, at least
+constexpr int kAhead = 8;            // rows of a warp whose copies are under way
+constexpr int kBytes = kWarps * kAhead * kCols * 2 * 2;        // dout's and z's
 
 struct BackParams {
   const uint16_t* dout;
@@ -51,84 +56,112 @@ __device__ __forceinline__ void widen(const uint4& u, uint64_t (&v)[4]) {
   for (int i = 0; i < 4; ++i) v[i] = ptx::pair(q[i] << 16, q[i] & 0xFFFF0000u);
 }
 
+// 16 bytes to shared memory on their own, or zeros
+__device__ __forceinline__ void copy16(uint4* to, const uint16_t* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(to)), "l"(from), "r"(there ? 16 : 0)
+               : "memory");
+}
 template <int kAct>
-__global__ void __launch_bounds__(32 * kWarps, 4)
+__global__ void __launch_bounds__(32 * kWarps, kCtas)
 bias_act_backward_kernel(const BackParams p) {
+  extern __shared__ uint4 s_rows[];  // [warp][own row modulo kAhead][dout, z][lane]
   __shared__ float s_sum[kWarps][kCols];
   count_launch(p.launches, MOE_KID_BIAS_ACT_BACKWARD);
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int block = blockIdx.x, r_lo = block * p.rows, r_hi = min(p.P, r_lo + p.rows);
-  // this warp's rows r_lo + warp + 8 i: destination and weight, lane i
-  int my_d = -1;
-  float my_w = 1.0f;
-  const int my_r = r_lo + warp + kWarps * lane;
-  if (my_r < r_hi) {
-    my_d = p.row_to_pair ? __ldg(p.row_to_pair + my_r) : my_r;
-    if (my_d < 0 || my_d >= p.P) my_d = -1;
-    else if (p.pair_weight) my_w = __ldg(p.pair_weight + my_d);
-  }
-  float row_sum = 0.0f;
-  bool seen = false;                 // its row is some group's
+  const int block = blockIdx.x, r_lo = block * p.rows, r_hi = r_lo + min(p.rows, p.P - r_lo);
+  const int n = blockIdx.y * kCols + lane * 8;
+  const bool live = n < p.N;
+  // This warp's rows r_lo + warp + 8 i, i < own.  Destinations and weights of the 32 around row i, lane i % 32, and of
+  // the 32 after them.
+  const int own = (r_hi - r_lo - warp + kWarps - 1) / kWarps;
+  int d_now = -1, d_next = -1;
+  float w_now = 1.0f, w_next = 1.0f;
+  auto look_up = [&](int i, int& d, float& w) {
+    d = -1;
+    w = 1.0f;
+    if (i >= own) return;
+    const int r = r_lo + warp + kWarps * i;
+    d = p.row_to_pair ? __ldg(p.row_to_pair + r) : r;
+    if (d < 0 || d >= p.P) d = -1;
+    else if (p.pair_weight) w = __ldg(p.pair_weight + d);
+  };
+  look_up(lane, d_now, w_now);
+  look_up(32 + lane, d_next, w_next);
+  // The copies of row j, for i = the row that is worked on; a group for every row, also behind the last.  A row without a
+  // destination comes as zeros, of z too.
+  uint4* mine = s_rows + warp * (2 * kAhead * 32) + lane;
+  const size_t first = static_cast<size_t>(r_lo + warp) * p.N + (live ? n : 0), stride = static_cast<size_t>(kWarps) * p.N;
+  const uint16_t *z = p.z ? p.z + first : nullptr, *dout = p.dout + (live ? n : 0);
+  uint16_t* dz = p.dz + first;
+  auto bring = [&](int j, int i) {
+    const int d = __shfl_sync(0xffffffffu, (j >> 5) == (i >> 5) ? d_now : d_next, j & 31);
+    if (j < own) {
+      const bool there = live && d >= 0;
+      uint4* to = mine + (j % kAhead) * 64;
+      if (z) copy16(to + 32, z, there);
+      copy16(to, dout + (there ? static_cast<size_t>(d) * p.N : 0), there);
+    }
+    if (z) z += stride;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int j = 0; j < kAhead; ++j) bring(j, 0);
+  int i = 0;                         // the next row
+  auto step = [&]() {
+    bring(i + kAhead, i);
+    dz += stride;
+    if ((++i & 31) == 0) {
+      d_now = d_next;
+      w_now = w_next;
+      look_up(i + 32 + lane, d_next, w_next);
+    }
+  };
   // the last group that starts at or before the block's first row
   int before = 0;
   for (int g0 = 0; g0 < p.G; g0 += 32 * kWarps) {
     const int g = g0 + static_cast<int>(threadIdx.x);
     before += __syncthreads_count(g < p.G && offset_at(p.group_offsets, g, p.P) <= r_lo);
   }
-  const int n = blockIdx.y * kCols + lane * 8;
-  const bool live = n < p.N;
   int g = max(before - 1, 0);
   for (int r0 = max(r_lo, offset_at(p.group_offsets, g, p.P)); g < p.G; ++g) {
     const int r1 = min(r_hi, offset_at(p.group_offsets, g + 1, p.P));
     if (r1 > r0) {
       uint64_t sum[4] = {};
-      for (int i0 = (r0 - r_lo - warp + kWarps - 1) / kWarps; r_lo + warp + kWarps * i0 < r1; i0 += kFlight) {
-        uint4 dv[kFlight], zv[kFlight];
+#pragma unroll 1
+      while (i < own && r_lo + warp + kWarps * i < r0) step();       // rows of no group
+#pragma unroll 1
+      for (; i < own && r_lo + warp + kWarps * i < r1; step()) {
+        const float w = __shfl_sync(0xffffffffu, w_now, i & 31);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        uint64_t dy[4], zz[4] = {}, dots = 0;
+        uint32_t out[4];
+        const uint4* from = mine + (i % kAhead) * 64;
+        widen(from[0], dy);
+        if (p.z) widen(from[32], zz);
+        const uint64_t w2 = ptx::pair(w);
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-          const int r = r_lo + warp + kWarps * (i0 + k), d = __shfl_sync(0xffffffffu, my_d, i0 + k);
-          const bool there = live && r < r1 && d >= 0;
-          dv[k] = there ? *reinterpret_cast<const uint4*>(p.dout + static_cast<size_t>(d) * p.N + n)
-                        : make_uint4(0, 0, 0, 0);
-          zv[k] = there && p.z ? *reinterpret_cast<const uint4*>(p.z + static_cast<size_t>(r) * p.N + n)
-                               : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          uint64_t y, s;
+          act::slope2<kAct>(zz[j], y, s);
+          dots = ptx::fma2(dy[j], y, dots);
+          const uint64_t v = ptx::mul2(ptx::mul2(dy[j], w2), s);
+          sum[j] = act::add2(sum[j], v);
+          const float2 u = ptx::unpair(v);
+          out[j] = pack_bf16x2(u.x, u.y);
         }
+        if (live)
+          *reinterpret_cast<uint4*>(dz) = make_uint4(out[0], out[1], out[2], out[3]);
+        if (p.part_w) {
+          const float2 u = ptx::unpair(dots);
+          float dot = u.x + u.y;
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-          const int r = r_lo + warp + kWarps * (i0 + k);
-          if (r >= r1) break;
-          const int d = __shfl_sync(0xffffffffu, my_d, i0 + k);
-          const float w = __shfl_sync(0xffffffffu, my_w, i0 + k);
-          uint64_t dy[4], zz[4], dots = 0;
-          uint32_t out[4];
-          widen(dv[k], dy);
-          widen(zv[k], zz);
-          const uint64_t w2 = ptx::pair(w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint64_t y, s;
-            act::slope2<kAct>(zz[j], y, s);
-            dots = ptx::fma2(dy[j], y, dots);
-            const uint64_t v = d >= 0 ? ptx::mul2(ptx::mul2(dy[j], w2), s) : 0ull;
-            sum[j] = act::add2(sum[j], v);
-            const float2 u = ptx::unpair(v);
-            out[j] = pack_bf16x2(u.x, u.y);
-          }
-          if (live)
-            *reinterpret_cast<uint4*>(p.dz + static_cast<size_t>(r) * p.N + n) =
-                make_uint4(out[0], out[1], out[2], out[3]);
-          if (p.part_w) {
-            const float2 u = ptx::unpair(dots);
-            float dot = u.x + u.y;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (lane == i0 + k) {
-              row_sum += dot;
-              seen = true;
-            }
-          }
+          for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+          // several column blocks: by row, for the sum; one: the gradient itself, by destination
+          if (lane == (i & 31) && d_now >= 0)
+            p.part_w[gridDim.y > 1 ? static_cast<size_t>(blockIdx.y) * p.P + r_lo + warp + kWarps * i
+                                   : static_cast<size_t>(d_now)] = dot;
         }
       }
       if (p.part_b) {
@@ -139,7 +172,7 @@ bias_act_backward_kernel(const BackParams p) {
         if (at < p.N) {
           float s = s_sum[0][threadIdx.x];
 #pragma unroll
-          for (int i = 1; i < kWarps; ++i) s += s_sum[i][threadIdx.x];
+          for (int k = 1; k < kWarps; ++k) s += s_sum[k][threadIdx.x];
           p.part_b[(static_cast<size_t>(block) + g) * p.N + at] = s;
         }
         __syncthreads();
@@ -148,9 +181,7 @@ bias_act_backward_kernel(const BackParams p) {
     }
     if (r0 >= r_hi) break;
   }
-  // several column blocks: by row, for the sum; one: the gradient itself, by destination
-  if (p.part_w && seen && my_d >= 0)
-    p.part_w[gridDim.y > 1 ? static_cast<size_t>(blockIdx.y) * p.P + my_r : static_cast<size_t>(my_d)] = row_sum;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // grad_bias: kSlices threads share a group's blocks of four columns, their sums joined in order; a CTA
@@ -208,18 +239,13 @@ bias_act_reduce_kernel(const BackParams p, float* __restrict__ grad_bias, float*
 
 int blocks_of(int n, int size) { return n / size + (n % size != 0); }
 size_t pad(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
-// Rows of a CTA: as many as leave two CTAs an SM.  777 x 1040 in 13 groups: 6.5 us with 16 rows, 9.9 with 64; 32768 x 768:
-// 42.2 with 64, 49 with 32, whose partial sums are twice as many.
-int rows_of(int P, int N) {
-  for (int r = kRows; r > 16; r >>= 1)
-    if (static_cast<long long>(blocks_of(P, r)) * blocks_of(N, kCols) >= 2ll * sm_count()) return r;
-  return 16;
+// Row ranges of a call: one wave of CTAs
+int ranges_of(int P, int N) {
+  const int all = kCtas * sm_count() / blocks_of(N, kCols), most = blocks_of(P, kLeast);
+  return all < 1 ? 1 : all < most ? all : most;
 }
-// Partial sums of any number of rows up to P: with 16 or 32 rows a CTA there are at most 2 (2 SMs - 1) / column blocks
 size_t bias_bytes(int P, int N, int G) {
-  const int most = blocks_of(P, rows_of(P, N)), few = 2 * ((2 * sm_count() - 1) / blocks_of(N, kCols));
-  const int fewer = few < blocks_of(P, 16) ? few : blocks_of(P, 16);
-  return pad((static_cast<size_t>(most > fewer ? most : fewer) + G) * N * 4);
+  return pad((static_cast<size_t>(ranges_of(P, N)) + G) * N * 4);
 }
 
 }  // namespace
@@ -277,7 +303,7 @@ extern "C" int moe_bias_act_backward(const void* dout_bf16, const void* z_bf16, 
   p.row_to_pair = row_to_pair;
   p.group_offsets = group_offsets;
   p.P = P; p.N = N; p.G = G;
-  p.rows = rows_of(P, N);
+  p.rows = P > 0 ? blocks_of(P, ranges_of(P, N)) : 1;
   p.dz = static_cast<uint16_t*>(dz_bf16);
   p.part_b = grad_bias ? static_cast<float*>(workspace) : nullptr;
   float* joined = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (grad_bias ? bias_bytes(P, N, G) : 0));
@@ -288,7 +314,20 @@ extern "C" int moe_bias_act_backward(const void* dout_bf16, const void* z_bf16, 
         bias_act_backward_kernel<MOE_ACT_NONE>, bias_act_backward_kernel<MOE_ACT_RELU>,
         bias_act_backward_kernel<MOE_ACT_RELU2>, bias_act_backward_kernel<MOE_ACT_GELU>,
         bias_act_backward_kernel<MOE_ACT_GELU_TANH>, bias_act_backward_kernel<MOE_ACT_SILU>};
-    const int rc = launch_status(launch_kernel(kernels[activation], dim3(blocks_of(P, p.rows), cb), dim3(32 * kWarps), 0,
+    static std::atomic<int> configured[6][64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+      cudaGetLastError();
+      dev = -1;
+    }
+    const bool cache = dev >= 0 && dev < 64;
+    if (!cache || !configured[activation][dev].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(kernels[activation], cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+        return set_error(MOE_ERR_CUDA, "%s: cannot reserve %d bytes of shared memory: %s", op, kBytes,
+                         cudaGetErrorString(cudaGetLastError()));
+      if (cache) configured[activation][dev].store(1, std::memory_order_release);
+    }
+    const int rc = launch_status(launch_kernel(kernels[activation], dim3(blocks_of(P, p.rows), cb), dim3(32 * kWarps), kBytes,
                                                s, nullptr, 0, p),
                                  op);
     if (rc != MOE_OK) return rc;

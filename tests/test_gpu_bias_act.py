@@ -307,7 +307,7 @@ def test_backward_of_many_small_groups_and_rows_of_none():
     c.run()
 
 
-@pytest.mark.parametrize("P", [900, 2500, 5001])     # 16, 32 and 64 rows to a block
+@pytest.mark.parametrize("P", [900, 2500, 5001])     # few and many rows to a CTA, the last with fewer
 def test_backward_of_every_block_height(P):
     sizes = [P // 3, 0, 1, 15, 16, 17, 63, 64, 65]
     sizes += [5, P - sum(sizes) - 9]
