@@ -890,7 +890,8 @@ size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int K, int I_sha
  *   workspace  >= moe_grouped_gemm_wgrad_workspace_size(P, N, K, G) bytes, 16-byte aligned; NULL when that is 0
  *   Every group is written, empty ones too.
  *
- * Errors of the three: MOE_ERR_ARG (sizes; P, K or N above 2^31 - 2^12; activation, w_layout; NULL operands, NULL
+ * Errors of the three: MOE_ERR_ARG (sizes; P, K or N above 2^31 - 2^12, or N above 2^24 - 2^8 in
+ * moe_bias_act_backward; activation, w_layout; NULL operands, NULL
  * group_offsets with G > 1; no output), MOE_ERR_ALIGN (bf16 and f32 matrices and the workspace 16 bytes,
  * other f32 and indices 4; the multiples of 8), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  P = 0
  * is a no-op but for grad_bias and grad_w.  A device-side wait that runs past its limit
