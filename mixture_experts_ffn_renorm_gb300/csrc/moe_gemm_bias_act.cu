@@ -32,7 +32,7 @@
 // end reads zeros and never its neighbour.
 //
 // Calls of at most 16 rows and weights [G, N, K] have a kernel of their own, below.
-// Calls whose tiles cannot fill the pairs (few rows) cut K into ranges: each leaves f32 sums in
+// Calls whose tiles cannot fill the pairs (few rows) take tiles of fewer rows, or cut K into ranges: each leaves f32 sums in
 // the workspace and a second kernel adds them in range order and applies the epilogue.
 #include <atomic>
 
@@ -56,6 +56,7 @@ constexpr unsigned long long kCopyGraceNs = 100000ull;   // see the exit
 struct Params {
   const int32_t* group_offsets;
   int P, K, N, G;
+  int row_block;                     // rows of a tile: kRowBlock, or 128 or 64
   const float* bias;
   int activation;
   uint16_t* z;
@@ -90,7 +91,7 @@ struct Tile {
   int g, r0, rows, n0;
 };
 
-__device__ __forceinline__ Tile tile_of(int tile, const int* start, const int* goff, int G, int n_fb) {
+__device__ __forceinline__ Tile tile_of(int tile, const int* start, const int* goff, int G, int n_fb, int block) {
   int lo = 0, hi = G;                // start[lo] <= tile < start[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -99,8 +100,8 @@ __device__ __forceinline__ Tile tile_of(int tile, const int* start, const int* g
   const int local = tile - start[lo], m = local / n_fb;
   Tile t;
   t.g = lo;
-  t.r0 = goff[lo] + m * kRowBlock;
-  t.rows = min(goff[lo + 1] - t.r0, kRowBlock);
+  t.r0 = goff[lo] + m * block;
+  t.rows = min(goff[lo + 1] - t.r0, block);
   t.n0 = (local - m * n_fb) * kColBlock;
   return t;
 }
@@ -183,7 +184,7 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
     goff[g] = p.group_offsets ? min(max(__ldg(p.group_offsets + g), 0), p.P) : (g == 0 ? 0 : p.P);
   __syncthreads();
   const int n_fb = (p.N + kColBlock - 1) / kColBlock;
-  auto tiles_in = [&](int g) { return (max(goff[g + 1] - goff[g], 0) + kRowBlock - 1) / kRowBlock * n_fb; };
+  auto tiles_in = [&](int g) { return (max(goff[g + 1] - goff[g], 0) + p.row_block - 1) / p.row_block * n_fb; };
   const int per = (G + kThreads - 1) / kThreads;
   const int g_lo = min(G, static_cast<int>(threadIdx.x) * per), g_hi = min(G, g_lo + per);
   int local = 0;
@@ -221,7 +222,7 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
     uint32_t phase = 0;
     bool ok = true;
     for (int u = unit; ok && u < work; u += n_units) {
-      const Tile t = tile_of(S == 1 ? u : u / S, start, goff, G, n_fb);
+      const Tile t = tile_of(S == 1 ? u : u / S, start, goff, G, n_fb, p.row_block);
       const int sp = S == 1 ? 0 : u % S;
       const int k0 = nk * sp / S, k1 = nk * (sp + 1) / S;
       const int half = ((t.rows + 15) & ~15) >> 1;       // rows that this CTA holds
@@ -260,7 +261,7 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
       uint32_t phase = 0, uses[2] = {0, 0};
       bool ok = true;
       for (int u = unit; ok && u < work; u += n_units) {
-        const Tile t = tile_of(S == 1 ? u : u / S, start, goff, G, n_fb);
+        const Tile t = tile_of(S == 1 ? u : u / S, start, goff, G, n_fb, p.row_block);
         const int sp = S == 1 ? 0 : u % S;
         const int k0 = nk * sp / S, k1 = nk * (sp + 1) / S;
         const uint32_t idesc = ptx::idesc_bf16_f32_mn(256, (t.rows + 15) & ~15, kColumns, false);
@@ -310,7 +311,7 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
     uint32_t uses[2] = {0, 0};
     int acc = 0;
     for (int u = unit; u < work; u += n_units) {
-      const Tile t = tile_of(S == 1 ? u : u / S, start, goff, G, n_fb);
+      const Tile t = tile_of(S == 1 ? u : u / S, start, goff, G, n_fb, p.row_block);
       const int sp = S == 1 ? 0 : u % S;
       const int col0 = t.n0 + static_cast<int>(rank) * 128;
       int* dst_t = s_dst + acc * kRowBlock;
@@ -695,13 +696,15 @@ few_rows_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, 
 }
 
 // ------------------------------------------------------------------ host side
-long long row_blocks(int P, int G) {
-  return G == 1 ? (static_cast<long long>(P) + kRowBlock - 1) / kRowBlock : P / kRowBlock + (G < P ? G : P);
+constexpr int kLeastBlock = 64;      // rows of a tile where they are few
+long long row_blocks(int P, int G, int block) {
+  return G == 1 ? (static_cast<long long>(P) + block - 1) / block : P / block + (G < P ? G : P);
 }
+long long col_blocks(int N) { return (N + kColBlock - 1ll) / kColBlock; }
 // Ranges of K for `blocks` row blocks: as many as fill the pairs, each of at least kRangeSteps
 // steps.  One row of 4096 x 1024 takes 4 tiles of 64 steps: 16 ranges, 64 pairs at work.
 int ranges_of(long long blocks, int K, int N) {
-  const long long tiles = blocks * ((N + kColBlock - 1ll) / kColBlock);
+  const long long tiles = blocks * col_blocks(N);
   long long s = sm_count() / 2 / tiles;
   const long long most = (K + BK - 1ll) / BK / kRangeSteps;
   s = s < most ? s : most;
@@ -721,6 +724,29 @@ int few_slices(int P, int N, int G) {
 }
 size_t part_bytes(int ranges, long long rows, int N) {
   return ranges < 2 ? 0 : static_cast<size_t>(ranges) * N * ((rows + 3) & ~3ll) * 4;
+}
+
+// Rows of a tile and ranges of K.  Where every tile has a pair of its own, fewer rows make the epilogue shorter (it takes
+// chunks of 64 rows in turn) and save ranges, whose sums go to memory and back; but more tiles leave fewer ranges, and a
+// pair more K steps.  The estimate is in ns: 350 a K step (a stage's way, with six under way), 600 a chunk, 2500 for a second
+// launch, and for a range's sums 1.5 ps each (4 where groups begin at odd rows).  What it chooses: 2000 rows of 1024 x 512 in 8
+// groups 128 rows and one range, 12.3 us (256 rows and two ranges: 27.6); 777 rows of 1040 x 1000 in 13 groups
+// 128 rows, 12.1 (256: 13.3); 1024 rows of 4096 x 512 128 rows and four ranges, 18.0 (256 and nine 17.0, 64 and two 22.5).
+void plan(Params& p) {
+  double best = 0.0;
+  for (int block = kRowBlock; block >= kLeastBlock; block /= 2) {
+    const long long blocks = row_blocks(p.P, p.G, block), tiles = blocks * col_blocks(p.N);
+    if (block < kRowBlock && tiles > sm_count() / 2) break;
+    const int s = ranges_of(blocks, p.K, p.N), steps = ((p.K + BK - 1) / BK + s - 1) / s;
+    const double rows = block < p.P ? block : p.P;
+    const double t = 350.0 * steps + 600.0 * ((static_cast<int>(rows) + 63) / 64) +
+                     (s > 1 ? 2500.0 + (p.G > 1 ? 4e-3 : 1.5e-3) * s * p.P * p.N : 0.0);
+    if (block == kRowBlock || t < best) {
+      best = t;
+      p.row_block = block;
+      p.ranges = s;
+    }
+  }
 }
 
 template <bool kColumns>
@@ -762,7 +788,7 @@ int launch(const char* op, const CUtensorMap (&tt)[4], const CUtensorMap& tw, Pa
       cudaGetLastError();
     if (cache) resident[dev].store(pairs, std::memory_order_relaxed);
   }
-  const long long work = row_blocks(p.P, p.G) * ((p.N + kColBlock - 1ll) / kColBlock) * p.ranges;
+  const long long work = row_blocks(p.P, p.G, p.row_block) * col_blocks(p.N) * p.ranges;
   if (work < pairs) pairs = work < 1 ? 1 : static_cast<int>(work);
   DeviceDiag diag = device_diag();
   p.status = diag.status;
@@ -787,15 +813,16 @@ using namespace moe::gemm;
 
 extern "C" size_t moe_grouped_gemm_bias_act_workspace_size(int P, int K, int N, int G) {
   if (P <= 0 || K <= 0 || N <= 0 || G <= 0) return 0;
-  // the most that any number of rows up to P takes: a workspace for the largest call serves all
+  // the most that any number of rows up to P takes, whatever the tiles: a workspace for the largest call serves all
   size_t most = 0;
-  for (long long b = 1; b <= row_blocks(P, G); ++b) {
-    const int s = ranges_of(b, K, N);
-    if (s < 2) break;
-    const long long rows = b * kRowBlock < P ? b * kRowBlock : P;
-    const size_t n = part_bytes(s, rows, N);
-    most = n > most ? n : most;
-  }
+  for (int block = kLeastBlock; block <= kRowBlock; block *= 2)
+    for (long long b = 1; b <= row_blocks(P, G, block); ++b) {
+      const int s = ranges_of(b, K, N);
+      if (s < 2) break;
+      const long long rows = b * block < P ? b * block : P;
+      const size_t n = part_bytes(s, rows, N);
+      most = n > most ? n : most;
+    }
   return most;
 }
 
@@ -816,7 +843,7 @@ extern "C" int moe_grouped_gemm_bias_act_bf16(const void* a_bf16, const void* w_
   if (activation < MOE_ACT_NONE || activation > MOE_ACT_SILU)
     return set_error(MOE_ERR_ARG, "%s: activation=%d is not a MOE_ACT_* value", op, activation);
   if (K % 8 || N % 8) return set_error(MOE_ERR_ALIGN, "%s: K=%d and N=%d must be multiples of 8", op, K, N);
-  if (row_blocks(P, G) * ((N + kColBlock - 1ll) / kColBlock) > kMaxDim)
+  if (row_blocks(P, G, kRowBlock) * col_blocks(N) > kMaxDim)
     return set_error(MOE_ERR_ARG, "%s: P=%d and N=%d are too large together", op, P, N);
   if (P == 0) return MOE_OK;
   if (!a_bf16 || !w_bf16 || !out_bf16) return set_error(MOE_ERR_ARG, "%s: a, w or out is NULL", op);
@@ -853,7 +880,7 @@ extern "C" int moe_grouped_gemm_bias_act_bf16(const void* a_bf16, const void* w_
     }
   }
   p.part_rows = (P + 3) & ~3;
-  p.ranges = ranges_of(row_blocks(P, G), K, N);
+  plan(p);
   const size_t one = part_bytes(2, P, N) / 2, fit = workspace ? ws_bytes / one : 0;
   if (static_cast<size_t>(p.ranges) > fit) p.ranges = static_cast<int>(fit);
   if (p.ranges < 2) p.ranges = 1;

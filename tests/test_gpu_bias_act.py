@@ -199,6 +199,21 @@ def test_a_workspace_of_the_most_rows_serves_fewer():
             assert m.moe_grouped_gemm_bias_act_workspace_size(P, K, N, G) <= most
 
 
+@pytest.mark.parametrize("columns", [False, True])
+@pytest.mark.parametrize("P,K,N,sizes", [
+    (2000, 1024, 512, [300, 0, 700, 1, 499, 63, 64, 373]), (1024, 4096, 512, None), (130, 520, 264, None),
+    (65, 72, 4096, None), (300, 264, 1000, [129, 127, 44]),
+])
+def test_tiles_of_fewer_rows(P, K, N, sizes, columns):
+    # 64 and 128 rows a tile, with and without ranges of K
+    c = Product(P, K, N, len(sizes) if sizes else 1, offsets(sizes) if sizes else None, columns, kind=R.SILU, pre=True,
+                scatter=True, weight=True, residual=True)
+    c.run()
+    c.call(ws=None)
+    torch.cuda.synchronize()
+    c.check(c.out)
+
+
 def test_out_may_be_residual():
     for P in (2, 20, 500):
         c = Product(P, 2048, 264, scatter=True, residual=True, kind=R.SILU)
