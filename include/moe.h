@@ -864,7 +864,7 @@ size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int K, int I_sha
  *   workspace   moe_grouped_gemm_bias_act_workspace_size(P, K, N, G) bytes, 16-byte aligned, for
  *               the sums of calls of few rows, which cut K into ranges to use every SM.  A
  *               size queried for the most rows serves every call.  A smaller one, or NULL,
- *               costs speed only (fewer ranges, whose last bits differ); calls of at most 8 rows
+ *               costs speed only (fewer ranges, whose last bits differ); small calls
  *               with MOE_W_ROWS use none.  Calls that may
  *               run at the same time need their own.
  *   P >= 0; K and N multiples of 8; 1 <= G <= 1024

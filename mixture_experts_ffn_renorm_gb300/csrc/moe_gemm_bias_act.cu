@@ -31,7 +31,7 @@
 // transposed copy is kept.  Both are seen through three-dimensional maps, so a group's ragged
 // end reads zeros and never its neighbour.
 //
-// Calls of at most 16 rows and weights [G, N, K] have a kernel of their own, below.
+// Calls of few rows and weights [G, N, K] have a kernel of their own, below.
 // Calls whose tiles cannot fill the pairs (few rows) take tiles of fewer rows, or cut K into ranges: each leaves f32 sums in
 // the workspace and a second kernel adds them in range order and applies the epilogue.
 #include <atomic>
@@ -565,8 +565,8 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
-// ------------------------------------------------------------------ calls of at most 16 rows
-constexpr int kFewRows = 16;         // P
+// ------------------------------------------------------------------ calls of few rows
+constexpr int kFewRows = 16;         // rows of a CTA
 constexpr int kFewWarps = 8;
 constexpr int kFewCols = 8;          // output columns of a warp
 constexpr int kFewFlight = 4;        // blocks of 64 K that a warp loads together
@@ -582,7 +582,7 @@ __device__ __forceinline__ uint4 load_or_zero(const uint4* from, bool there) {
   return v;
 }
 
-// Weights [G, N, K].  A warp holds 8 output columns of one group and takes K in turn with the other `slices` - 1
+// Weights [G, N, K].  A warp holds 8 output columns for at most 16 rows of one group and takes K in turn with the other `slices` - 1
 // of them, 64 at a time: a lane has 2 x 16 bytes of one of the columns, and the products of 16 rows x 8 columns
 // are mma.sync's; a CTA joins the slices' sums in order.  What bounds it is the weights' way from memory: no tensor
 // memory to allocate, no second launch, and a warp's loads of four blocks leave at once.  (A lane's 16
@@ -598,8 +598,8 @@ few_rows_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, 
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  // the blockIdx.y-th group that has rows
-  int group = 0, r0 = 0, rows = p.P;
+  // the blockIdx.y-th block of at most 16 rows of a group
+  int group = 0, r0 = static_cast<int>(blockIdx.y) * kFewRows, rows = min(p.P - r0, kFewRows);
   if (p.group_offsets) {
     int left = static_cast<int>(blockIdx.y);
     rows = 0;
@@ -607,17 +607,23 @@ few_rows_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, 
       const int i = i0 + lane;
       const int lo = min(max(i < p.G ? __ldg(p.group_offsets + i) : 0, 0), p.P);
       const int hi = min(max(i < p.G ? __ldg(p.group_offsets + i + 1) : 0, 0), p.P);
-      uint32_t has = __ballot_sync(0xffffffffu, hi > lo);
-      const int n = __popc(has);
-      if (left >= n) {
-        left -= n;
+      const int own = hi > lo ? (hi - lo + kFewRows - 1) / kFewRows : 0;
+      int upto = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const uint32_t behind = __ballot_sync(0xffffffffu, upto > left);
+      if (behind == 0) {
+        left -= __shfl_sync(0xffffffffu, upto, 31);
         continue;
       }
-      for (; left > 0; --left) has &= has - 1u;
-      const int at = __ffs(has) - 1;
+      const int at = __ffs(behind) - 1;
+      left -= __shfl_sync(0xffffffffu, upto - own, at);
       group = i0 + at;
-      r0 = __shfl_sync(0xffffffffu, lo, at);
-      rows = __shfl_sync(0xffffffffu, hi - lo, at);
+      r0 = __shfl_sync(0xffffffffu, lo, at) + left * kFewRows;
+      rows = min(__shfl_sync(0xffffffffu, hi, at) - r0, kFewRows);
       break;
     }
     if (rows == 0) return;
@@ -711,14 +717,24 @@ int ranges_of(long long blocks, int K, int N) {
   s = s < kMaxRanges ? s : kMaxRanges;
   return s < 1 ? 1 : static_cast<int>(s);
 }
-// Slices of K in the kernel of few rows: the most with which all CTAs (two per SM) run at once.  4096 x 4096, one row:
-// 7.9 us with 4 slices and 256 CTAs, 9.1 with 8 and 512, 10.7 with 2 and 128.  Where a single slice
-// leaves more CTAs than that, more than eight rows take the pairs' kernel (0): 16 rows of 1024 x 32768 19 us
-// against 15.5, while eight rows take 14.7.
-int few_slices(int P, int N, int G) {
+// blocks of 16 rows of a group, at most
+int few_blocks(int P, int G) {
+  if (G == 1) return P / kFewRows + (P % kFewRows != 0);
+  const int blocks = P / kFewRows + (G < P ? G : P);
+  return blocks < P ? blocks : P;
+}
+// Slices of K in the kernel of few rows, or 0: the pairs' kernel.  The most slices with which all CTAs (two per SM) run at once:
+// one row of 4096 x 4096 takes 7.9 us with 4 slices and 256 CTAs, 9.1 with 8 and 512, 10.7 with 2 and 128.
+// Every block of 16 rows reads the weights anew, so with several of them a warp may have four batches of K, each a
+// latency: 128 rows of 512 x 512 2.9 us (pairs 8.0), 64 rows of 2048 x 768 6.1 (8.5), in 8 groups 8.9 (12.4), 48 rows of
+// 4096 x 1024, four batches, 9.4 (9.8); with eight batches 32 rows of 4096 x 4096 take 16.1 (13.0).  One block takes any
+// K, and where a single slice leaves more CTAs than two per SM at most eight rows: 16 rows of 1024 x 32768 19 us against
+// 15.5, eight 14.7.
+int few_slices(int P, int K, int N, int G) {
   for (int s = kFewWarps; s; s >>= 1) {
     const long long cols = kFewCols * kFewWarps / s;
-    if ((N + cols - 1) / cols * (G < P ? G : P) <= 2 * sm_count()) return s;
+    if ((N + cols - 1) / cols * few_blocks(P, G) <= 2 * sm_count())
+      return P <= kFewRows || K <= 4 * kFewFlight * 64 * s ? s : 0;
   }
   return P > 8 ? 0 : 1;
 }
@@ -866,13 +882,13 @@ extern "C" int moe_grouped_gemm_bias_act_bf16(const void* a_bf16, const void* w_
   p.row_to_pair = row_to_pair;
   p.residual = static_cast<const uint16_t*>(residual_bf16);
   p.out = static_cast<uint16_t*>(out_bf16);
-  if (w_layout == MOE_W_ROWS && P <= kFewRows) {
-    const int slices = few_slices(P, N, G), cols = kFewCols * kFewWarps / (slices ? slices : 1);
+  if (w_layout == MOE_W_ROWS) {
+    const int slices = few_slices(P, K, N, G), cols = kFewCols * kFewWarps / (slices ? slices : 1);
     if (slices) {
       const DeviceDiag diag = device_diag();
       p.launches = diag.launches;
       return launch_status(launch_kernel(P > 8 ? few_rows_kernel<true> : few_rows_kernel<false>,
-                                         dim3((N + cols - 1) / cols, G < P ? G : P), dim3(32 * kFewWarps), 0,
+                                         dim3((N + cols - 1) / cols, few_blocks(P, G)), dim3(32 * kFewWarps), 0,
                                          static_cast<cudaStream_t>(stream), nullptr, 0,
                                          static_cast<const uint16_t*>(a_bf16), static_cast<const uint16_t*>(w_bf16), p,
                                          slices),

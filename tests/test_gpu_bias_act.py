@@ -134,8 +134,8 @@ def test_a_groups_end_reads_zeros_and_not_its_neighbour(columns):
 def test_infinities_and_nan_through_the_activations():
     v = torch.tensor([float("inf"), float("-inf"), float("nan"), 0.0, -0.0, 30.0, -30.0, 1e-30], device=DEV)
     for kind in range(6):
-        for P in (1, 20, 600):       # the few rows' epilogue, the join's and the tile's own
-            c = Product(P, 2048, 8, kind=kind)
+        for P, columns in ((1, False), (20, True), (600, True)):     # the few rows' epilogue, the join's and the tile's own
+            c = Product(P, 2048 if P < 600 else 256, 8, columns=columns, kind=kind)
             c.a.zero_()
             c.bias[0] = v
             c.call()
@@ -148,11 +148,11 @@ def test_infinities_and_nan_through_the_activations():
 
 
 def test_few_rows_split_k_and_no_workspace_only_costs_speed():
-    c = Product(20, 4096, 1024, residual=True)
+    c = Product(200, 4096, 1024, residual=True)
     before = launches()
     c.run()
     assert launched_since(before, "bias_act_join") == 1
-    for size in (None, c.ws[: 2 * 1024 * 20 * 4], c.ws[: 1024]):
+    for size in (None, c.ws[: 2 * 1024 * 200 * 4], c.ws[: 1024]):
         before = launches()
         c.out.fill_(0)
         c.call(ws=size)
@@ -166,6 +166,8 @@ def test_few_rows_split_k_and_no_workspace_only_costs_speed():
     (8, 72, 40000, None), (16, 136, 19456, None), (16, 136, 19464, None),       # one slice; eight rows' and more rows' limit
     (16, 264, 392, [1] * 16), (16, 264, 392, [0, 9, 0, 0, 7]), (13, 200, 136, [0] * 40 + [1, 0, 8] + [0] * 70 + [2]),
     (16, 72, 1288, [1] * 16 + [0] * 1008), (5, 72, 136, [0, 0, 0]),
+    (17, 520, 264, None), (129, 136, 520, None), (100, 264, 136, [0, 33, 1, 0, 16, 17, 31]),     # several blocks of 16 rows
+    (300, 72, 72, [1, 0] * 40 + [100, 0, 90, 60]), (64, 2048, 768, None),
 ])
 def test_few_rows(P, K, N, sizes):
     # one launch, without a workspace; rows of no group stay as they were
@@ -174,7 +176,7 @@ def test_few_rows(P, K, N, sizes):
     before = launches()
     c.ws = None
     c.run()
-    if P <= 8 or N < 19464:
+    if (P, N) != (16, 19464):
         assert launched_since(before, "gemm_bias_act") == 1 and launched_since(before, "bias_act_join") == 0
 
 
@@ -215,8 +217,8 @@ def test_tiles_of_fewer_rows(P, K, N, sizes, columns):
 
 
 def test_out_may_be_residual():
-    for P in (2, 20, 500):
-        c = Product(P, 2048, 264, scatter=True, residual=True, kind=R.SILU)
+    for P, columns in ((2, False), (20, True), (500, False)):
+        c = Product(P, 2048, 264, columns=columns, scatter=True, residual=True, kind=R.SILU)
         want = c.call().clone()
         res = c.res.clone()
         c.call(out=res, residual=res)
@@ -225,8 +227,8 @@ def test_out_may_be_residual():
 
 
 def test_same_bits_each_time_in_graphs_and_on_other_streams():
-    for P in (4, 20, 900):
-        c = Product(P, 2048, 776, kind=R.GELU, residual=True)
+    for P, columns in ((4, False), (20, True), (900, False)):
+        c = Product(P, 2048, 776, columns=columns, kind=R.GELU, residual=True)
         want = c.call().clone()
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()

@@ -29,7 +29,7 @@ def test_graphs_that_share_a_workspace():
     ws = torch.zeros(max(c.ws.numel() for c in cases), dtype=torch.uint8, device=DEV)
     for c in cases:
         c.ws = ws
-    products = [Product(20, 4096, 520, residual=True, seed=1), Product(100, 2048, 264, seed=2)]
+    products = [Product(20, 4096, 520, columns=True, residual=True, seed=1), Product(100, 2048, 264, columns=True, seed=2)]
     shared = ws_of(max(p.ws.numel() for p in products))
     for p in products:
         p.ws = shared
@@ -48,7 +48,8 @@ def test_graphs_that_share_a_workspace():
 
 
 def test_programmatic_launch_off_gives_the_same_bits():
-    layer, few, pair = Case(7, 1032, 400, 60, 6, Is=64), Product(3, 520, 264), Product(40, 2048, 264, residual=True)
+    layer, few, pair = (Case(7, 1032, 400, 60, 6, Is=64), Product(3, 520, 264),
+                        Product(40, 2048, 264, columns=True, residual=True))
     back = Back(900, 520, 3, offsets([100, 0, 800]), scatter=True, weight=True)
     grad = Wgrad(300, 136, 264, 2, offsets([170, 130]), add=True)
     one = Wgrad(3000, 136, 264, 1)                   # ranges of rows
