@@ -21,10 +21,11 @@
 //               tile's products.
 //
 // 65536 rows of 2048 x 768 in 128 groups, GELU and z take 191 us: 1.08 PFLOP/s and 4.6 TB/s, where HBM alone
-// takes 129 and the products 109.  32768 rows against [K, N] weights take 106 (HBM 87).  What is left lies in the tiles' shares: each
-// pair takes every n-th tile whatever its rows (the busiest has 17 % more than the mean), and 32 KB go
-// from L2 to every SM per 64 of K.  (All column blocks of a row block in turn on one pair: 220 us, as
-// the weights come from HBM again.)
+// takes 129 and the products 109.  32768 rows against [K, N] weights take 106 (HBM 87).  Dense, 16384 x 4096 x 4096
+// reaches 1837 TFLOP/s: what is left is the way of many groups' weights and rows from HBM through L2 at once (16 groups
+// instead of 128: 139 us).  (All column blocks of a row block in turn on one pair: 220 us, as the weights come from HBM
+// again.  Tiles dealt by their costs: 190, though the busiest pair has 8 % more than the mean, as those that share rows and
+// weights then run apart.  Stages brought to L2 ahead: 260; prefetches take the copies' own throughput.)
 //
 // Weights [G, N, K] are K-major operands.  Weights [G, K, N] (the rows' gradient of a layer's
 // own weights) are MN-major ones, boxes of 64 columns x 64 K rows in the same stage: no
