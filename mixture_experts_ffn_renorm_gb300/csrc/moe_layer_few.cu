@@ -88,7 +88,7 @@ struct Params {
   float* w;
   uint16_t* out;
   unsigned long long* barrier;     // arrivals of all launches
-  unsigned int* turns;             // blocks of gate/up that were asked for; 0 between launches
+  unsigned int* turns;             // blocks of gate/up that were asked for
   float* logits;                   // [T, E]
   float* gate;                     // [T]
   uint16_t* act;                   // [3][T K, I], then [3][T, Is]: parts of the weighted activations
@@ -418,8 +418,7 @@ struct Stream {
       : p(p_), f(f_), maps(maps_), warp(warp_), lane(lane_) {
     D = f.n_groups;
     // The blocks in one line.  A warp's first is its place in the grid, the SMs' first warps before their second
-    // ones; every further one is the next that nobody has.  The count of those is back at 0 when
-    // the launch ends.
+    // ones; every further one is the next that nobody has.
     const unsigned cta = blockIdx.x;
     const int per = p.I / kFeat;                             // I % 8 == 0
     per_inv = 0xFFFFFFFFu / per + 1u;
@@ -685,7 +684,10 @@ layer_few_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
   }
   __syncthreads();
-  if (tid == 0) grid_barrier(arrivals, abort_flag, p);
+  if (tid == 0) {
+    if (blockIdx.x == 0) *p.turns = 0u;          // nobody asks before the barrier
+    grid_barrier(arrivals, abort_flag, p);
+  }
   __syncthreads();
 
   // ---- choice of experts
@@ -903,10 +905,7 @@ layer_few_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
     __syncthreads();
     if (phase == 0) {
-      if (tid == 0) {
-        grid_barrier(arrivals + gridDim.x, abort_flag, p);
-        if (blockIdx.x == 0) *p.turns = 0u;      // nobody asks any more
-      }
+      if (tid == 0) grid_barrier(arrivals + gridDim.x, abort_flag, p);
       __syncthreads();
     }
   }
