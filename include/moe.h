@@ -848,7 +848,7 @@ size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int K, int I_sha
  *   activation  MOE_ACT_*: none; relu max(z, 0); relu2 max(z, 0)^2; gelu z Phi(z);
  *               gelu_tanh 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); silu z / (1 + exp(-z)).
  *               The exponentials are the fast ones (a few binary32 ulps), Phi is off by
- *               at most 1e-7.
+ *               at most 3e-7, and below z = -4 by at most 2^-14 of itself (down to z = -13).
  *   a           bf16 [P, K], rows in group order
  *   w           w_layout MOE_W_ROWS: bf16 [G, N, K], a row per output column;
  *               MOE_W_COLUMNS: bf16 [G, K, N].  With the weights of a MOE_W_ROWS product of

@@ -57,19 +57,23 @@ __device__ __forceinline__ void slope2(uint64_t z, uint64_t& y, uint64_t& s) {
       s = add2(r, r);
     }
   } else if (kAct == MOE_ACT_GELU) {
-    // Phi(-|z|) = erfc(|z| / sqrt 2) / 2, with erfc from Abramowitz & Stegun, Handbook of Mathematical
-    // Functions, 7.1.26: erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0, off by
-    // at most 1.5e-7, which is below bf16's half step of any value that counts beside its row.  Then
-    // Phi(z) = 1/2 + sign(z) (1/2 - Phi(-|z|))
-    const uint64_t sign = z & 0x8000000080000000ull, x = z ^ sign;
-    const uint64_t t = each(rcp_fast, fma2(x, pair(0.3275911f * 0.70710678f), pair(1.0f)));
+    // Phi(-|z|) = (c1 t + .. + c6 t^6) exp(-z^2 / 2), t = 1 / (1 + p |z|): the form of Abramowitz & Stegun,
+    // Handbook of Mathematical Functions, 7.1.26, with coefficients fitted here (least squares, reweighted towards
+    // the largest error) so that the series is off by at most 0.7e-7 and by 2^-14 of Phi(-|z|), as far as exp's
+    // range goes: theirs holds the first bound only and has no digit left at z = -5.25.  A negative z takes the tail
+    // as it is (1/2 - (1/2 - tail) would cut it off), a positive one what is left of 1.  With the roundings
+    // Phi is off by at most 3e-7, and below z = -4 by 2^-14 of itself.
+    const uint64_t x = z & 0x7FFFFFFF7FFFFFFFull;
+    const uint64_t t = each(rcp_fast, fma2(x, pair(0.292f), pair(1.0f)));
     const uint64_t e = each(exp2_fast, mul2(mul2(z, z), pair(-0.5f * kLog2e)));
-    uint64_t q = fma2(t, pair(0.5f * 1.061405429f), pair(0.5f * -1.453152027f));
-    q = fma2(t, q, pair(0.5f * 1.421413741f));
-    q = fma2(t, q, pair(0.5f * -0.284496736f));
-    q = fma2(t, q, pair(0.5f * 0.254829592f));
+    uint64_t q = fma2(t, pair(-0.086436026f), pair(0.2696572f));
+    q = fma2(t, q, pair(-0.0747589f));
+    q = fma2(t, q, pair(0.16993603f));
+    q = fma2(t, q, pair(0.10418754f));
+    q = fma2(t, q, pair(0.11741414f));
     const uint64_t tail = mul2(mul2(q, t), e);
-    const uint64_t phi = add2(fma2(tail, pair(-1.0f), pair(0.5f)) ^ sign, pair(0.5f));
+    const float2 u = ptx::unpair(z), lo = ptx::unpair(tail), hi = ptx::unpair(fma2(tail, pair(-1.0f), pair(1.0f)));
+    const uint64_t phi = pair(__float_as_uint(u.x < 0.0f ? lo.x : hi.x), __float_as_uint(u.y < 0.0f ? lo.y : hi.y));
     y = mul2(z, phi);
     s = fma2(mul2(z, pair(0.39894228f)), e, phi);            // Phi(z) + z phi(z)
   } else if (kAct == MOE_ACT_GELU_TANH) {
