@@ -80,9 +80,9 @@ __device__ __forceinline__ void slope2(uint64_t z, uint64_t& y, uint64_t& s) {
     const uint64_t zz = mul2(z, z);
     const uint64_t p = logistic2(mul2(mul2(z, pair(-2.0f * kTanhScale * kLog2e)), fma2(zz, pair(kTanhCube), pair(1.0f))));
     y = mul2(z, p);
-    // p + 2 c z p (1 - p) (1 + 3 b z^2)
+    // p + 2 c z p (1 - p) (1 + 3 b z^2), z^2 last: beyond 2^64 it is infinite, where p (1 - p) is 0
     const uint64_t d = mul2(y, fma2(p, pair(-1.0f), pair(1.0f)));
-    s = fma2(mul2(d, pair(2.0f * kTanhScale)), fma2(zz, pair(3.0f * kTanhCube), pair(1.0f)), p);
+    s = fma2(fma2(mul2(mul2(d, z), z), pair(3.0f * kTanhCube), d), pair(2.0f * kTanhScale), p);
   } else if (kAct == MOE_ACT_SILU) {
     const uint64_t p = logistic2(mul2(z, pair(-kLog2e)));
     y = mul2(z, p);
