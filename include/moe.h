@@ -816,7 +816,7 @@ size_t moe_route_logits_backward_workspace_size(int T, int H, int E);
  * MOE_ERR_WORKSPACE, MOE_ERR_CUDA.  A device-side wait that runs past its limit
  * (moe_set_wait_limit_ns) sets MOE_STATUS_TIMEOUT.
  * ---------------------------------------------------------------------- */
-enum { MOE_LAYER_FEW_MAX_TOKENS = 16 };
+enum { MOE_LAYER_FEW_MAX_TOKENS = 16, MOE_LAYER_FEW_MAX_DIM = 8192 /* H, I, I_shared */ };
 int moe_layer_few_bf16(const void* x_bf16, const void* w_router_bf16, const float* logit_bias,
                        const float* select_bias, const void* w13_bf16, const void* w2_bf16,
                        const void* w_shared_gate_bf16, const void* w13_shared_bf16,

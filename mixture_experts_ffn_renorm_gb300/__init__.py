@@ -498,6 +498,7 @@ def moe_route_logits_backward_workspace_size(T, H, E) -> int:
 
 
 LAYER_FEW_MAX_TOKENS = 16
+LAYER_FEW_MAX_DIM = 8192     # of H, I and I_shared
 
 
 def moe_layer_few_bf16(x, w_router, logit_bias, select_bias, w13, w2, w_shared_gate, w13_shared,

@@ -53,8 +53,8 @@ namespace moe {
 namespace few {
 namespace {
 
-constexpr int kMaxT = 16;          // tokens: one warp per token in the choice
-constexpr int kMaxDim = 8192;      // H, I, I_shared
+constexpr int kMaxT = MOE_LAYER_FEW_MAX_TOKENS;    // one warp per token in the choice
+constexpr int kMaxDim = MOE_LAYER_FEW_MAX_DIM;     // H, I, I_shared
 constexpr int kMaxE = 1024;
 constexpr int kMaxPairs = kMaxT * 32;
 constexpr int kWarps = 12;

@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from . import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_RELU2, ACT_SILU, BF16,
-               LAYER_FEW_MAX_TOKENS, QFMT_Q4_K, QFMT_Q8_0, W_COLUMNS, W_ROWS,
+               LAYER_FEW_MAX_DIM, LAYER_FEW_MAX_TOKENS, QFMT_Q4_K, QFMT_Q8_0, W_COLUMNS, W_ROWS,
                moe_bias_act_backward, moe_bias_act_backward_workspace_size, moe_combine, moe_combine_backward, moe_combine_gate,
                moe_gate_workspace_size, moe_grouped_gemm_down_bf16,
                moe_grouped_gemm_down_bf16_shared, moe_grouped_gemm_down_fp8w,
@@ -76,7 +76,8 @@ class MoeBlock:
     few=True (bf16 or FP8 weights without fp8_acts): calls of at most 16 tokens run the
     whole layer in one launch (moe_layer_few_*), where nothing is narrowed to bf16 between
     the weights and the output; the choice of experts is the same, the output agrees within
-    the roundings of the separate launches.  Larger calls run as without it.
+    the roundings of the separate launches.  Larger calls run as without it, and so does a block
+    with H, I or I_shared above LAYER_FEW_MAX_DIM.
     q_dequant=True (with qweights): the GGUF blocks are expanded to bf16 once, on the
     device, when the block is built, and the layer runs the bf16 tensor-core path --
     the faster choice when the experts see many rows each (prefill-sized batches).
@@ -130,7 +131,9 @@ class MoeBlock:
             raise ValueError("training needs fp8_acts and no shared expert")
         if few and (self.qfmt or fp8_acts):
             raise ValueError("few needs bf16 experts or FP8 weights without fp8_acts")
-        self.few = few
+        # the largest call that the one launch takes
+        self.few_tokens = (LAYER_FEW_MAX_TOKENS
+                           if few and max(H, I, I_shared) <= LAYER_FEW_MAX_DIM else 0)
         self.routed_scale = float(routed_scale)
         self.device = torch.device(device)
         if self.device.type != "cuda":
@@ -218,9 +221,9 @@ class MoeBlock:
         self.ws_gate = moe_gate_workspace_size(T)
         self.workspace = torch.empty((max(self.ws_route, self.ws_perm, self.ws_gate, 256),),
                                      dtype=torch.uint8, device=dv)
-        if few:
+        if self.few_tokens:
             # zero-filled once (it holds a barrier), then passed unchanged to every call
-            n = moe_layer_few_workspace_size(min(T, LAYER_FEW_MAX_TOKENS), H, I, E, K, I_shared)
+            n = moe_layer_few_workspace_size(min(T, self.few_tokens), H, I, E, K, I_shared)
             self.ws_few = torch.zeros((max(16, n),), dtype=torch.uint8, device=dv)
         self.graph = None
         self.graph_x = None
@@ -248,7 +251,7 @@ class MoeBlock:
                 marks.append((name, ev))
 
         mark("start", edge=True)
-        if self.few and T <= LAYER_FEW_MAX_TOKENS:
+        if self.few_tokens and T <= self.few_tokens:
             out = self.out[:T] if out is None else out
             self._forward_few(x, T, out, stream)
             self._tokens = T
