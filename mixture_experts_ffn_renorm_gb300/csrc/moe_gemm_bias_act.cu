@@ -39,6 +39,7 @@
 
 #include "activation.cuh"
 #include "fp8_common.cuh"
+#include "pair_drain.cuh"
 
 namespace moe {
 namespace gemm {
@@ -52,7 +53,6 @@ constexpr int kWBytes = 128 * BK * 2;
 constexpr int kTBytes = 128 * BK * 2;
 constexpr int kMaxRanges = 16;       // of K
 constexpr int kRangeSteps = 4;       // K steps of a range, at least
-constexpr unsigned long long kCopyGraceNs = 100000ull;   // see the exit
 
 struct Params {
   const int32_t* group_offsets;
@@ -79,14 +79,14 @@ struct Smem {
   static constexpr int DST = EPI + 2 * 8192;                   // int [2][256]
   static constexpr int WEIGHT = DST + 2 * kRowBlock * 4;       // float [2][256]
   static constexpr int BARS = WEIGHT + 2 * kRowBlock * 4;      // full, empty, tfull[2], tempty[2], drain
-  static constexpr int MISC = BARS + (2 * kStages + 5) * 8;    // tmem slot, abort flag, scan
+  static constexpr int MISC = BARS + (2 * kStages + 5) * 8;    // tmem slot, abort flag, scan, uses issued
   static constexpr int TILES = MISC + 64;
   static constexpr int GOFF = TILES + (kMaxGroups + 1) * 4;
   static constexpr int BYTES = GOFF + (kMaxGroups + 1) * 4;
   static constexpr int ALLOC = BYTES + 1024;
 };
 static_assert(Smem::ALLOC <= 227 * 1024, "shared memory");
-static_assert(kThreads / 32 * 4 + 8 <= 64, "scan slots");
+static_assert(kThreads / 32 * 4 + 8 <= 48, "scan slots");
 
 struct Tile {
   int g, r0, rows, n0;
@@ -106,6 +106,11 @@ __device__ __forceinline__ Tile tile_of(int tile, const int* start, const int* g
   t.n0 = (local - m * n_fb) * kColBlock;
   return t;
 }
+
+// rows of a tile that each CTA of the pair holds, the box they come in, and a CTA's bytes of a stage
+__device__ __forceinline__ int half_of(const Tile& t) { return ((t.rows + 15) & ~15) >> 1; }
+__device__ __forceinline__ int box_of(int half) { return half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128; }
+__device__ __forceinline__ uint32_t bytes_of(int box) { return kWBytes + box * BK * 2; }
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
                                                  uint32_t bar) {
@@ -136,6 +141,7 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Smem::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Smem::MISC + 4);
   int* scan = reinterpret_cast<int*>(smem + Smem::MISC + 8);
+  uint32_t* s_issued = reinterpret_cast<uint32_t*>(smem + Smem::MISC + 48);
   int* start = reinterpret_cast<int*>(smem + Smem::TILES);
   int* goff = reinterpret_cast<int*>(smem + Smem::GOFF);
   int* s_dst = reinterpret_cast<int*>(smem + Smem::DST);
@@ -220,18 +226,17 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int u = unit; ok && u < work; u += n_units) {
       const Tile t = tile_of(S == 1 ? u : u / S, start, goff, G, n_fb, p.row_block);
       const int sp = S == 1 ? 0 : u % S;
       const int k0 = nk * sp / S, k1 = nk * (sp + 1) / S;
-      const int half = ((t.rows + 15) & ~15) >> 1;       // rows that this CTA holds
-      const int box = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128;
+      const int half = half_of(t), box = box_of(half);
       const CUtensorMap* mt = box == 16 ? &tm16 : box == 32 ? &tm32 : box == 64 ? &tm64 : &tm128;
       const int row = t.r0 + static_cast<int>(rank) * half;
       const int col = t.n0 + static_cast<int>(rank) * 128;
-      const uint32_t bytes = kWBytes + box * BK * 2;
+      const uint32_t bytes = bytes_of(box);
       for (int kb = k0; kb < k1; ++kb) {
         bool got = true;
         if (lane == 0) {
@@ -252,9 +257,11 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
         } else if (lane == 1) {
           tma_load_3d_pair(dw, &tmW, kb * BK, col, t.g, bar);
         }
+        ++issued;
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
+    if (lane == 0) *s_issued = issued;
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (leader && ptx::elect_one()) {
@@ -463,8 +470,8 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
     }
   }
 
-  // ---- exit: if either CTA of the pair gave up, drain before freeing memory.  Copies are counted
-  // on the even CTA's barriers, so both CTAs give theirs a grace period to land.
+  // ---- exit: if either CTA of the pair gave up, the MMAs and both CTAs' copies are waited for before
+  // memory is freed
   __syncthreads();
   ptx::cluster_sync();
   const bool gave_up =
@@ -476,10 +483,21 @@ bias_act_kernel(const __grid_constant__ CUtensorMap tm16, const __grid_constant_
       ptx::mma_commit_pair(bar_drain, 1);
       spin_bounded(bar_drain, 0);
     }
-    if (warp == 0 && lane == 0) {
-      const uint64_t t0 = ptx::globaltimer_ns();
-      while (ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
-      }
+    if (leader && warp == 0 && lane == 0) {
+      // uses come in order: u, the work item of the last use asked for, ends before use `end`
+      int u = unit - n_units;
+      uint32_t end = 0;
+      drain_pair_copies<kStages>(
+          *s_issued, ld_shared_cluster_u32(ptx::mapa_shared(ptx::smem_u32(s_issued), 1)), bar_full,
+          [&](uint32_t i) {
+            while (i >= end) {
+              u += n_units;
+              const int sp = S == 1 ? 0 : u % S;
+              end += nk * (sp + 1) / S - nk * sp / S;
+            }
+            return bytes_of(box_of(half_of(tile_of(S == 1 ? u : u / S, start, goff, G, n_fb, p.row_block))));
+          },
+          [](uint32_t) { return 0u; });
     }
   }
   __syncthreads();
