@@ -58,10 +58,10 @@
 // moe_gemm.cu: groups in order, each group's token blocks of 256, each block's
 // feature blocks; pair u takes tiles u, u + pairs, ...  Waits are bounded like
 // moe_gemm.cu's; a CTA that gives up tells its peer, the MMAs are drained, and
-// both CTAs let their in-flight copies land before they free tensor memory.
+// the pair waits for its in-flight copies (pair_drain.cuh) before it frees tensor memory.
 #include <atomic>
 
-#include "gemm_common.cuh"
+#include "pair_drain.cuh"
 
 namespace moe {
 namespace gemm {
@@ -95,10 +95,6 @@ constexpr int kSideBytes = 16 * BK * 2;   // one CTA's token rows of a short til
 constexpr int kPStages = 6;
 constexpr int kWBytes = 128 * BK * 2; // one CTA's weight rows per stage: 16 KB
 constexpr int kTBytes = 128 * BK * 2; // one CTA's token rows per stage, at most: 16 KB
-// after a CTA gives up: how long it lets its TMA copies land before the pair
-// frees its shared and tensor memory (copies are counted on the even CTA's
-// barriers, so the odd CTA cannot wait for its own copies directly)
-constexpr unsigned long long kCopyGraceNs = 100000ull;
 
 enum PairEpi { PEPI_GATEUP = 0, PEPI_DOWN = 1 };
 
@@ -137,7 +133,8 @@ struct PSmem {
   // full[kPStages], empty[kPStages], tfull[2], tempty[2], drain, gathered[kPStages]
   static constexpr int BARS = SIDE + kPStages * kSideBytes;
   static constexpr int NBARS = 3 * kPStages + 5;
-  // tmem slot, abort flag, scan (one int per warp), staged rows: ready tiles, epoch
+  // tmem slot, abort flag, scan (one int per warp), staged rows: ready tiles, epoch;
+  // uses of the ring that the producer, the two gatherer warps and the relay came through
   static constexpr int MISC = BARS + NBARS * 8;
   static constexpr int TILE_START = MISC + 128;
   static constexpr int GOFF = TILE_START + (kMaxPairGroups + 1) * 4;
@@ -189,6 +186,15 @@ __device__ __forceinline__ PTile pair_tile(int tile, const int* tile_start, cons
   t.n0 = (local - m * n_fb) * fb_cols;
   t.nblk = 1;
   return t;
+}
+
+// one CTA's bytes of a stage of the tile
+template <bool kShorts, bool kGather>
+__device__ __forceinline__ uint32_t pair_stage_bytes(const PTile& t) {
+  const bool sh = kShorts && t.n_tok <= kShortTok;
+  const int half = ((t.n_tok + 15) & ~15) >> 1;
+  const int tbox = sh ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
+  return (sh ? t.nblk : 1) * kWBytes + (kGather ? 0 : tbox * (BK * 2));
 }
 
 // staged rows: bounded wait of the producer until the watcher has published
@@ -267,6 +273,7 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
   // producer), and this launch's flag value
   const uint32_t s_ready = ptx::smem_u32(smem + PSmem::MISC + 64);
   volatile uint32_t* s_epoch = reinterpret_cast<volatile uint32_t*>(smem + PSmem::MISC + 68);
+  uint32_t* s_uses = reinterpret_cast<uint32_t*>(smem + PSmem::MISC + 72);   // producer, gatherers, relay
   int* tile_start = reinterpret_cast<int*>(smem + PSmem::TILE_START);
   int* goff = reinterpret_cast<int*>(smem + PSmem::GOFF);
   int* s_dst = reinterpret_cast<int*>(smem + PSmem::META_DST);
@@ -373,7 +380,7 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
     // the gatherers copy them; a short tile's second feature block in two more)
     // are issued by lanes 0-4 as a single warp instruction.
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, issued = 0;
     uint32_t n_tile = 0;
     bool ok = true;
     for (int tile = unit; ok && tile < total; tile += n_units, ++n_tile) {
@@ -392,7 +399,7 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
       const int tbox = sh ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
       const CUtensorMap* mt =
           sh ? &tmT16 : (tbox == 32 ? &tmT32 : (tbox == 64 ? &tmT64 : &tmT128));
-      const uint32_t bytes = (sh ? t.nblk : 1) * kWBytes + (kGather ? 0 : tbox * (BK * 2));
+      const uint32_t bytes = pair_stage_bytes<kShorts, kGather>(t);
       const int trow = t.r0 + static_cast<int>(rank) * half;
       // this CTA's 128 weight rows: gate/up, the 64 up rows of its features
       // then their 64 gate rows; down, 128 consecutive output rows
@@ -425,10 +432,12 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
         if (issues)
           ptx::tma_load_2d_pair(sbase + dbox + stage * dstep, mbox, kb * BK, ybox,
                                 ptx::mapa_shared(bar_full(stage), 0));
+        ++issued;
         if (++stage == kPStages) { stage = 0; phase ^= 1u; }
       }
     }
     (void)n_tile;
+    if (lane == 0) s_uses[0] = issued;
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (lane == 0 && leader) {
@@ -493,7 +502,7 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
       // scope on every stage measured 2.6 times slower for the whole GEMM.
       const uint32_t full_leader = ptx::mapa_shared(bar_full(0), 0);  // + 8 * stage
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, relayed = 0;
       bool ok = true;
       for (int tile = unit; ok && tile < total; tile += n_units) {
         for (int kb = 0; kb < nk; ++kb) {
@@ -503,9 +512,11 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
           }
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive_remote_relaxed(full_leader + 8u * stage);
+          ++relayed;
           if (++stage == kPStages) { stage = 0; phase ^= 1u; }
         }
       }
+      s_uses[3] = relayed;
     }
   } else if (kStaged && warp >= kPairThreads / 32 && warp < kPairThreads / 32 + 2) {
     // ------------------------------------------------------------ stagers
@@ -597,7 +608,7 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
     const int rsub = lane >> 3;
     const uint16_t* a = p.a;
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, gathered = 0;
     bool ok = true;
     for (int tile = unit; ok && tile < total; tile += n_units) {
       const PTile t = pair_tile(tile, tile_start, goff, G, n_fb, kFbCols, kShorts);
@@ -634,9 +645,11 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
           }
         }
         ptx::cp_async_mbar_arrive_noinc(leader ? bar_full(stage) : bar_gath(stage));
+        ++gathered;
         if (++stage == kPStages) { stage = 0; phase ^= 1u; }
       }
     }
+    if (lane == 0) s_uses[1 + gw] = gathered;
     ptx::cp_async_wait_all();   // nothing of this thread lands after the CTA's exit
   } else if (warp < kPairThreads / 32) {
     // ------------------------------------------------------------ epilogue
@@ -829,7 +842,8 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
     }
   }
 
-  // ---- exit: if either CTA of the pair gave up, drain before freeing memory
+  // ---- exit: if either CTA of the pair gave up, the MMAs and both CTAs' copies are waited for
+  // before memory is freed
   __syncthreads();
   ptx::cluster_sync();
   const bool gave_up =
@@ -841,10 +855,17 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap tmT16,
       ptx::mma_commit_pair(bar_drain, 1);
       spin_bounded(bar_drain, 0);
     }
-    if (warp == 0 && lane == 0) {
-      const uint64_t t0 = ptx::globaltimer_ns();
-      while (ptx::globaltimer_ns() - t0 < kCopyGraceNs) {
-      }
+    if (leader && warp == 0 && lane == 0) {
+      const uint32_t peer = ptx::mapa_shared(ptx::smem_u32(s_uses), 1);
+      drain_pair_copies<kPStages>(
+          s_uses[0], ld_shared_cluster_u32(peer), bar_full,
+          [&](uint32_t i) {
+            const int tile = unit + static_cast<int>(i / nk) * n_units;
+            return pair_stage_bytes<kShorts, kGather>(pair_tile(tile, tile_start, goff, G, n_fb, kFbCols, kShorts));
+          },
+          [&](uint32_t i) {
+            return kGather ? gather_debt(i, s_uses[1], s_uses[2], ld_shared_cluster_u32(peer + 12u)) : 0u;
+          });
     }
   }
   __syncthreads();

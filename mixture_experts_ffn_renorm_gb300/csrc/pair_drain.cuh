@@ -32,6 +32,12 @@ __host__ __device__ __forceinline__ StageDebt stage_debt(uint32_t i, uint32_t ev
   return d;
 }
 
+// Rows that are gathered: besides the arming arrival a use's barrier counts one of each thread of the even CTA's two
+// gatherer warps and one of the odd CTA's relay.  Those that use i lacks, of roles that came through so many uses:
+__host__ __device__ __forceinline__ uint32_t gather_debt(uint32_t i, uint32_t warp0, uint32_t warp1, uint32_t relay) {
+  return (i >= warp0 ? 32u : 0u) + (i >= warp1 ? 32u : 0u) + (i >= relay ? 1u : 0u);
+}
+
 // One thread of the even CTA, after both CTAs' roles have ended.  bar(s): stage s's barrier; bytes(i): one CTA's
 // bytes of use i; arrivals(i): arrivals besides the arming one that use i's barrier still lacks.
 template <int kStages, typename Bar, typename Bytes, typename Arrivals>

@@ -66,3 +66,41 @@ def test_product(columns, sizes):
 def test_product_in_ranges_of_k():
     c = Product(500, 8192, 1024, columns=True, residual=True)       # and their join
     run_out(c.call, (c.out,))
+
+
+class Experts:
+    """gate/up and down of the block's experts, [group][rows] of x taken as they lie."""
+
+    def __init__(self, sizes, H, I):
+        g = torch.Generator(device=DEV).manual_seed(len(sizes))
+        n = lambda *s, std=1.0: (torch.randn(s, generator=g, device=DEV) * std).to(torch.bfloat16)
+        self.G, self.P, self.H, self.I = len(sizes), sum(sizes), H, I
+        self.off = offsets(sizes)
+        self.x, self.w13, self.w2 = n(self.P, H), n(self.G, 2 * I, H, std=H ** -0.5), n(self.G, H, I, std=I ** -0.5)
+        self.act, self.rows, self.out = n(self.P, I), n(self.P, H), n(self.P, H)
+        self.ident = torch.arange(self.P, dtype=torch.int32, device=DEV)
+        self.ws = torch.zeros(m.moe_gateup_staged_workspace_size(self.P), dtype=torch.uint8, device=DEV)
+
+    def gateup(self, gather=None):
+        m.moe_grouped_gemm_gateup_silu_bf16(self.x, self.P, gather, 1, self.w13, self.off, self.P, self.H, self.I, self.G, self.act)
+
+    def gathered(self):
+        self.gateup(self.ident)
+
+    def staged(self):
+        m.moe_grouped_gemm_gateup_silu_bf16_staged(self.x, self.P, self.ident, 1, self.rows, self.w13, self.off, self.P,
+                                                   self.H, self.I, self.G, self.act, self.ws, self.ws.numel())
+
+    def down(self):
+        m.moe_grouped_gemm_down_bf16(self.act, self.w2, self.off, None, None, self.P, self.I, self.H, self.G, self.out)
+
+
+@pytest.mark.parametrize("call", ["gateup", "gathered", "staged", "down"])
+@pytest.mark.parametrize("sizes", [[1024] * 8, [900, 0, 7, 1400, 33, 257, 30, 64, 2000, 129]], ids=["even", "ragged"])
+def test_experts(sizes, call):
+    prev = m.moe_set_gemm_pairing(m.GEMM_PAIR)
+    try:
+        e = Experts(sizes, 2048, 2048)
+        run_out(getattr(e, call), (e.out,) if call == "down" else (e.act,))
+    finally:
+        m.moe_set_gemm_pairing(prev)

@@ -29,12 +29,15 @@ def debt():
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
     subprocess.check_call([cc, "-gencode", "arch=compute_103a,code=sm_103a", "-O1", "-std=c++17", "-shared", "-Xcompiler",
                            "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CSRC, SRC, "-o", LIB])
-    fn = ctypes.CDLL(LIB).stage_debt_host
+    lib = ctypes.CDLL(LIB)
+    fn, gathers = lib.stage_debt_host, lib.gather_debt_host
+    gathers.restype = ctypes.c_uint
 
     def run(i, even, odd, size):
         out = (ctypes.c_uint * 3)()
         fn(i, even, odd, size, out)
         return out[0], out[1], out[2]
+    run.gathers = gathers
     return run
 
 
@@ -95,3 +98,35 @@ def test_every_phase_ends_with_its_last_copy(debt, base):
                     under_way -= 1
                     bar.complete(size)
                 assert bar.ended and bar.tx == 0 and bar.pending == 0
+
+
+def test_gathered_rows_arrivals_are_made_up(debt):
+    # even, odd: copies; the even CTA's two gatherer warps and the odd one's relay stopped anywhere in the ring
+    rnd = random.Random(7)
+    for even, odd, warp0, warp1, relay in (tuple(rnd.randint(9, 9 + STAGES) for _ in range(5)) for _ in range(4000)):
+        n = max(even, odd)
+        for i in range(n - STAGES, n):
+            if i < 9:
+                assert debt.gathers(i, warp0, warp1, relay) == 0
+                continue
+            bar, size, under_way = Barrier(1 + 64 + 1), 16384, []
+            if i < even:
+                bar.arrive(2 * size)
+            for there, k in ((i < warp0, 32), (i < warp1, 32), (i < relay, 1)):
+                # a gatherer's arrival comes when its own copies have landed
+                under_way += [bar.arrive] * k if there else []
+            under_way += [lambda: bar.complete(size)] * ((i < even) + (i < odd))
+            rnd.shuffle(under_way)
+            for _ in range(rnd.randint(0, len(under_way))):
+                under_way.pop()()
+            _, expect, complete = debt(i, even, odd, size)
+            if complete:
+                bar.complete(complete)
+            if expect:
+                bar.arrive(expect)
+            for _ in range(debt.gathers(i, warp0, warp1, relay)):
+                bar.arrive()
+            while under_way:
+                assert not bar.ended
+                under_way.pop()()
+            assert bar.ended and bar.tx == 0 and bar.pending == 0
