@@ -45,6 +45,12 @@ def _dev_bf16(a, device):
     return t.to(device).contiguous()
 
 
+def _rows(what, t, H):
+    """Refuses what is not contiguous bf16 rows of H: the kernels read and write by these sizes alone."""
+    if t.dim() != 2 or t.shape[1] != H or t.dtype != torch.bfloat16 or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous bf16 rows of {H}, not {list(t.shape)} of {t.dtype}")
+
+
 class MoeBlock:
     """One MoE expert block with resident weights.
 
@@ -240,6 +246,11 @@ class MoeBlock:
         T = x.shape[0]
         assert T <= self.max_tokens and x.dtype == torch.bfloat16 and x.is_contiguous()
         H, I, E, K = self.H, self.I, self.E, self.K
+        _rows("x", x, H)
+        if out is not None:
+            _rows("out", out, H)
+            if out.shape[0] < T:
+                raise ValueError(f"out has {out.shape[0]} rows for {T} tokens")
         P = T * K
         ws = self.workspace
         self._tokens = None
@@ -380,6 +391,7 @@ class MoeBlock:
         assert dout.shape == x.shape
         assert x.dtype == dout.dtype == torch.bfloat16 and x.is_contiguous() and dout.is_contiguous()
         H, I, E, K = self.H, self.I, self.E, self.K
+        _rows("x", x, H)
         P = T * K
         ws = self.ws_grad
         moe_combine_backward(self.expert_out, BF16, self.topk_w, dout, BF16, self.routed_scale, T,
@@ -523,6 +535,15 @@ class MoeMlpBlock:
             raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, not {activation!r}")
         if H % 8 or I % 8:
             raise ValueError(f"H and I must be multiples of 8, not {H} and {I}")
+        for key, shape, optional in (("w_router", (E, H), False), ("w1", (E, I, H), False), ("w2", (E, H, I), False),
+                                     ("b1", (E, I), True), ("b2", (E, H), True), ("logit_bias", (E,), True)):
+            a = weights.get(key)
+            if a is None and optional:
+                continue
+            if a is None or tuple(a.shape) != shape:
+                raise ValueError(f"{key} must be {list(shape)}, not {None if a is None else list(a.shape)}")
+            if not optional and isinstance(a, torch.Tensor) and a.dtype != torch.bfloat16:
+                raise ValueError(f"{key} must be bf16, not {a.dtype}")
         self.H, self.I, self.E, self.K, self.max_tokens = H, I, E, K, max_tokens
         self.act, self.training = ACTIVATIONS[activation], training
         self.routed_scale = float(routed_scale)
@@ -567,10 +588,12 @@ class MoeMlpBlock:
         T = x.shape[0]
         if not 1 <= T <= self.max_tokens:
             raise ValueError(f"forward() of {T} tokens, outside [1, {self.max_tokens}]")
-        assert x.dtype == torch.bfloat16 and x.is_contiguous()
-        assert residual is None or (residual.shape == x.shape and residual.dtype == x.dtype and
-                                    residual.is_contiguous())
         H, I, E, K, ws = self.H, self.I, self.E, self.K, self.workspace
+        for what, t in (("x", x), ("residual", residual), ("out", out)):
+            if t is not None:
+                _rows(what, t, H)
+                if t.shape[0] != T:
+                    raise ValueError(f"{what} has {t.shape[0]} rows for {T} tokens")
         P = T * K
         self._tokens = None
         moe_route_topk(x, self.w_router, self.logit_bias, None, None, T, H, E, K, 1, 0, 1,
@@ -601,9 +624,11 @@ class MoeMlpBlock:
         if T != self._tokens:
             raise ValueError("backward() needs a forward() before it" if self._tokens is None else
                              f"backward() of {T} tokens, but the last forward() took {self._tokens}")
-        assert dout.shape == x.shape
-        assert x.dtype == dout.dtype == torch.bfloat16 and x.is_contiguous() and dout.is_contiguous()
         H, I, E, K, ws = self.H, self.I, self.E, self.K, self.workspace
+        _rows("x", x, H)
+        _rows("dout", dout, H)
+        if dout.shape[0] != T:
+            raise ValueError(f"dout has {dout.shape[0]} rows for {T} tokens")
         P, off, pair = T * K, self.expert_offsets, self.sorted_pair
         wsa = (ws, ws.numel(), stream)
         # the rows' gradients in pair order, then through the second product's weight and bias
