@@ -977,6 +977,7 @@ enum {
   MOE_KID_BIAS_ACT_REDUCE = 35,   /* moe_bias_act_backward: sums over row and column blocks */
   MOE_KID_GEMM_WGRAD = 36,        /* moe_grouped_gemm_wgrad_bf16 */
   MOE_KID_WGRAD_REDUCE = 37,      /* moe_grouped_gemm_wgrad_bf16: the sum over ranges of rows */
+  MOE_KID_BIAS_ACT_FEW = 38,      /* the launches of 32 by the kernel of few rows */
   MOE_KID_COUNT = 40
 };
 int moe_device_status(int* status_out, int clear);

@@ -30,7 +30,7 @@ KID = {
     "silu_backward": 22, "transpose_fp8": 23, "combine_backward": 24, "route_backward": 25,
     "route_losses": 26, "route_dx": 27, "route_dw": 28, "route_reduce": 29, "gemm_fp8_few": 30,
     "layer_few": 31, "gemm_bias_act": 32, "bias_act_join": 33, "bias_act_backward": 34,
-    "bias_act_reduce": 35, "gemm_wgrad": 36, "wgrad_reduce": 37,
+    "bias_act_reduce": 35, "gemm_wgrad": 36, "wgrad_reduce": 37, "bias_act_few": 38,
 }
 KID_COUNT = 40
 QFMT_Q8_0, QFMT_Q4_K = 1, 2

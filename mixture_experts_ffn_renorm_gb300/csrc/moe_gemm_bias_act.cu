@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
 few_rows_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, const Params p, const int slices) {
   __shared__ float s_sum[kFewWarps][kFewRows][kFewCols];
   count_launch(p.launches, MOE_KID_GEMM_BIAS_ACT);
+  count_launch(p.launches, MOE_KID_BIAS_ACT_FEW);
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
