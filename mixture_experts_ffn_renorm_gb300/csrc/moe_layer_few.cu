@@ -115,7 +115,6 @@ struct alignas(16) Fixed {
   uint16_t token[kMaxPairs + kMaxT];   // their tokens
   int16_t expert[kMaxPairs + 1];   // touched experts, ascending
   int16_t first[kMaxPairs + 3];    // their first pair
-  uint16_t tokens[kMaxPairs + 1];  // their tokens, a bit each
   int n_groups;                    // touched experts, without the shared one
   int abort_flag;
 };
@@ -379,7 +378,6 @@ __device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch
     const int tokens = __popc(m);
     f.expert[run & 0xFFFF] = static_cast<int16_t>(e);
     f.first[run & 0xFFFF] = static_cast<int16_t>(run >> 16);
-    f.tokens[run & 0xFFFF] = static_cast<uint16_t>(m);
     x.mask[e] = m | (static_cast<uint32_t>(run >> 16) << 16);
     run += 1 + (tokens << 16);
   }
@@ -388,7 +386,6 @@ __device__ __forceinline__ void group_experts(const Params& p, Fixed& f, Scratch
     f.n_groups = D;
     f.first[D] = static_cast<int16_t>(P);
     f.first[D + 1] = static_cast<int16_t>(P + p.T);
-    f.tokens[D] = static_cast<uint16_t>((1u << p.T) - 1u);   // the shared expert's
   }
 }
 
