@@ -791,7 +791,9 @@ size_t moe_route_logits_backward_workspace_size(int T, int H, int E);
  *                  + gate[t] y_shared(x[t]) + residual[t] )
  * gate = sigmoid(w_shared_gate . x[t]), 1 without w_shared_gate.  Everything
  * between the weights and out is f32: unlike the launches of the block, nothing is
- * narrowed before the activation, before the down product or per expert row, so
+ * narrowed before the activation, before the down product or per expert row (an activation
+ * enters the down product as three bf16 parts that add up to it; one above bf16's largest value is
+ * infinite, and an infinite weight of w2 gives NaN where a part is 0 or of the other sign), so
  * the two agree within the bf16 roundings of those.  Sums are in a fixed order: the same
  * call gives the same bits on GPUs of the same SM count.
  *   w13, w2     bf16 [E, 2I, H] (gate rows first), [E, H, I]; fp8w: E4M3 codes with
