@@ -525,8 +525,9 @@ enum { MOE_GEMM_AUTO = 0, MOE_GEMM_SINGLE = 1, MOE_GEMM_PAIR = 2 };
 int moe_set_gemm_pairing(int mode);
 
 /* moe_set_wait_limit_ns -- limit, in nanoseconds of device time, of every
- * pipeline wait inside the bf16 and FP8-weight grouped GEMM kernels (a role
- * waiting for a stage to land or to be freed, or for an accumulator).
+ * wait inside the grouped products (keep-quant ones apart), their gradients and the
+ * router's, and the few-token layer (a role waiting for a stage to land or to be freed, or for an
+ * accumulator; the layer's grid barriers).
  * Default and maximum 10^9 (one second), minimum 1000.  A wait that runs past
  * it raises MOE_STATUS_TIMEOUT in the status word and stops its CTA: the
  * other roles stop at their next wait, the copies and MMAs already in flight

@@ -7,8 +7,10 @@
 // columns of a range of rows, three CTAs an SM, one wave of them; a warp every eighth row, a lane 8 columns, so that its column sums are
 // 8 registers and its row sums one butterfly each.  A warp's next eight rows are always under way to its own
 // shared memory (cp.async, no barrier): 192 KB an SM.
-// 32768 x 768 with bias and row weights takes 41.7 us with GELU (3.6 TB/s), 33 with SiLU, 31.5 with ReLU; the pass alone
-// 33, 27 and 27 (HBM 22), then the second kernel.  (Blocks of 64 rows, three rows of a warp in registers, 2.5 waves: 42.6, 37.8 and
+// 32768 x 768 with bias and row weights takes 43.2 us with GELU (3.5 TB/s), 38 with GELU by tanh, 34 with SiLU, 33 with
+// ReLU or none (HBM 22).  A warp spends 286 instructions on a row's 256 columns with GELU, 195 with SiLU and 179 with ReLU,
+// which has next to no arithmetic: copies, widening, packing, the row's sum and addresses are most of them.  The second
+// kernel takes 6 us by itself.  (Blocks of 64 rows, three rows of a warp in registers, 2.5 waves: 42.6, 37.8 and
 // 37.  A CTA for all columns of 64 rows: 48.  All 64 rows of a block asked for at once: 43.6 and 39.)
 // A CTA's rows may meet several groups: at
 // each group's end the warps' column sums are joined through shared memory in warp order and

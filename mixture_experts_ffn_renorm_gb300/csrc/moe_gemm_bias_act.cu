@@ -20,10 +20,10 @@
 //               16-byte pieces; the residual's rows come the same way back.  It runs under the next
 //               tile's products.
 //
-// 65536 rows of 2048 x 768 in 128 groups, GELU and z take 191 us: 1.08 PFLOP/s and 4.6 TB/s, where HBM alone
-// takes 129 and the products 109.  32768 rows against [K, N] weights take 106 (HBM 87).  Dense, 16384 x 4096 x 4096
-// reaches 1837 TFLOP/s: what is left is the way of many groups' weights and rows from HBM through L2 at once (16 groups
-// instead of 128: 139 us).  (All column blocks of a row block in turn on one pair: 220 us, as the weights come from HBM
+// 65536 rows of 2048 x 768 in 128 groups, GELU and z take 182 us in a row of the same calls, 197 to 201 among others (1.03
+// PFLOP/s and 4.4 TB/s), where HBM alone takes 129 and the products 109.  32768 rows against [K, N] weights take 107 to
+// 110 (HBM 87).  Dense, 16384 x 4096 x 4096 reaches 1837 TFLOP/s.  What is left: the way of many groups' weights and rows
+// from HBM through L2 at once (16 groups instead of 128: 149 us in a row), and the epilogue (165 without GELU and z).  (All column blocks of a row block in turn on one pair: 220 us, as the weights come from HBM
 // again.  Tiles dealt by their costs: 190, though the busiest pair has 8 % more than the mean, as those that share rows and
 // weights then run apart.  Stages brought to L2 ahead: 260; prefetches take the copies' own throughput.)
 //
@@ -608,7 +608,7 @@ __device__ __forceinline__ uint4 load_or_zero(const uint4* from, bool there) {
 // bytes lie elsewhere in the contraction than the MMA has them, alike on both sides.)
 // One row of 4096 x 1024 takes 4.3 us from HBM in a row of calls, the CTA pairs' two launches 9.2; 8192 x 8192 24 against 29;
 // 1024 x 4096 3.7 against 9.1.  Eight blocks in flight are slower (4096 x 4096: 11.1 against 7.9), as one CTA fits an SM then.
-// kTwo: more than eight rows.
+// kTwo: more than eight rows (its 128 registers, two CTAs an SM, spill six: 16 bytes stored, 24 loaded a thread).
 template <bool kTwo>
 __global__ void __launch_bounds__(32 * kFewWarps, 2)
 few_rows_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, const Params p, const int slices) {

@@ -18,14 +18,17 @@
 // group's matrix.  (With loads from there and stores of 16 bytes a lane a tile took its warps 1400
 // instructions and 14600 cycles, six times its products.)
 //
-// 32768 rows of 768 x 2048 in 128 groups take 177 us, 5.6 TB/s: 805 MB of gradients leave, 185 MB of rows come in.
-// With add_to 280 us, 6.4 TB/s: its boxes of 32 x 32 come by TMA, four under way to each warp, into the room of two of
+// 32768 rows of 768 x 2048 in 128 uneven groups take 178 to 185 us, 5.5 TB/s: 805 MB of gradients leave, 185 MB of rows come
+// in.  With add_to 305 to 320 us, 5.7 TB/s: its boxes of 32 x 32 come by TMA, four under way to each warp, into the room of two of
 // the four stages (or one, where groups have many rows), and leave from there.  (Loads of a lane's own row, each a
 // latency of HBM and 32 lines: 410 us.  Tiles of 128 columns even the SMs' shares of few tiles out, to no gain.)
-// 777 rows of 400 x 1040 in 13 groups with add_to take 16.8 us (6.7 at HBM's rate), two tiles an SM at most.
+// 777 rows of 400 x 1040 in 13 groups with add_to take 15.5 to 16.8 us (6.7 at HBM's rate), two tiles an SM at most.
 //
 // With a few groups of many rows there are fewer tiles than SMs: the rows are cut into ranges whose
 // sums go to the workspace, and a second kernel adds them in range order.
+//
+// The sums of 128 columns and their addresses do not quite fit 168 registers, the most that three of the ten warps on
+// one scheduler can have: 64 to 104 bytes a thread are spilled.
 #include <atomic>
 
 #include "fp8_common.cuh"
