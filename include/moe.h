@@ -807,8 +807,8 @@ size_t moe_route_logits_backward_workspace_size(int T, int H, int E);
  *   workspace   >= moe_layer_few_workspace_size(...) bytes, 16-byte aligned,
  *               zero-filled before its first use and then passed to later calls
  *               unchanged (it holds a barrier; calls of any sizes that it is large enough for
- *               may share it).  Calls that may run at the same time need their own.  After
- *               MOE_STATUS_TIMEOUT it is zero-filled again.
+ *               may share it).  Calls that may run at the same time need their own.  One that
+ *               ended with MOE_STATUS_TIMEOUT leaves it in order: every CTA arrives at both barriers.
  *   0 <= T <= 16; 1 <= H, I <= 8192 multiples of 8 (fp8w: 16); 0 <= I_shared <= 8192, a
  *   multiple of 8; E, K, renormalize, scoring, n_group, topk_group, group_score as
  *   moe_route_topk_ex
